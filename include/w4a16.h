@@ -308,6 +308,115 @@ int w4a16_expand_groups(const w4a16_bf16* src, w4a16_bf16* dst, int N, int K, in
 int w4a16_embed(const uint32_t* Wq, const w4a16_bf16* scales, const w4a16_bf16* biases, const int32_t* ids,
                 w4a16_bf16* out, int T, int N, int K, void* stream);
 
+/* ---- Paged key/value cache in 8 bits -------------------------------------------
+ *
+ * What a decoder layer needs between its q/k/v and o projections: the block
+ * tables and slots of a step (w4a16_kv_plan), the write of the step's keys
+ * and values (w4a16_kv_append) and the attention that reads them
+ * (w4a16_kv_attention).
+ *
+ * The cache of one layer is `blocks` blocks of `block` tokens.  A token lives
+ * in slot = (block id) * block + offset.  Keys and values are e4m3 codes (8
+ * bits: 4 exponent, 3 significand, no infinities; 0x7F and 0xFF are NaN) with
+ * one scale per (block, head):
+ *   K[i][h][o][d] = k[i][h][o][d] * k_scale[i][h]      and V likewise.
+ * A (block, head) is `block * dim` consecutive bytes.  Scales are powers of
+ * two in 2^-64 .. 2^120.  Token positions count from 0 in each request; the
+ * token at position p of request b lives in block table[b][p / block], offset
+ * p % block. */
+typedef struct {
+  uint8_t* k;     /* [blocks][heads][block][dim] e4m3 codes, 16-byte aligned */
+  uint8_t* v;     /* [blocks][heads][block][dim] */
+  float* k_scale; /* [blocks][heads] */
+  float* v_scale; /* [blocks][heads] */
+  int blocks;     /* blocks * block and blocks * heads * block below 2^31 */
+  int heads;      /* key/value heads, 1..65535 */
+  int block;      /* tokens per block: 16, 32, 64 or 128 */
+  int dim;        /* head size: 64, 128 or 256 */
+} w4a16_kv_cache;
+
+/* Block tables, slots and positions of one step, from request lengths that
+ * live on the device.  cached[b] tokens of request b are in its blocks
+ * already, fresh[b] new ones join (both int32 [B]); every new token is one
+ * row of the step's activations, request after request.
+ *   cu[b]   = sum of fresh[0..b-1]  (int32 [B + 1])
+ *   lens[b] = cached[b] + fresh[b]  (int32 [B])
+ * The requests' new blocks are taken from free_blocks (int32 [n_free], block
+ * ids) in request order, beginning at entry *head (a device int32; NULL is
+ * 0), and written to their entries of table (int32 [B][max_blocks]; entries
+ * of earlier blocks are read, later ones left alone); *head_out = *head +
+ * blocks taken (head_out must not be head).  For token t < cu[B] of request
+ * b: positions[t] = cached[b] + t - cu[b], slots[t] its slot (int32 [T]); for
+ * cu[B] <= t < T (a padded batch) both are -1.
+ * Out-of-range inputs raise W4A16_DEVICE_KV_RANGE and never lead outside the
+ * arrays: negative lengths count as 0, tokens past T are dropped from the
+ * step (cu is cut at T), and a token whose block is missing (the free list
+ * has run out, the request is longer than max_blocks * block, or its table
+ * entry is negative) gets slot -1.  A missing block's entry is -1.
+ * All arrays 4-byte aligned.  B, T >= 0, below 2^30. */
+int w4a16_kv_plan(const int32_t* cached, const int32_t* fresh, int32_t* table, const int32_t* free_blocks,
+                  const int32_t* head, int32_t* cu, int32_t* lens, int32_t* slots, int32_t* positions,
+                  int32_t* head_out, int B, int T, int block, int max_blocks, int n_free, void* stream);
+
+/* Write T tokens' keys and values into their slots (as w4a16_kv_plan gives
+ * them; slot -1 skips a token).  k and v are bf16, token t's row of
+ * heads * dim values at k + t * k_stride (elements; a multiple of 8, so that
+ * the columns of a fused q/k/v product can be passed as they are); k and v
+ * 16-byte aligned.  For each touched (block, head), with its new rows at
+ * offsets o .. o + n - 1:
+ *   need  = the smallest power of two (at least 2^-64) with
+ *           max |finite new value| <= 448 * need
+ *   scale = need if o == 0, else max(need, the block's scale)
+ *   new code = e4m3(x / scale), round to nearest even; NaN and infinities
+ *              become the NaN code
+ *   rows before o are re-coded at the new scale if it grew: e4m3(code * old /
+ *   new), exact but for codes that become subnormal; rows after the new ones
+ *   are left alone.
+ * The tokens of one block must be consecutive in the call, in slot order (as
+ * they are in a plan), and no slot may occur twice.  A slot outside the cache
+ * is skipped and raises W4A16_DEVICE_KV_RANGE.  T >= 0; T == 0 is a no-op. */
+int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, int64_t v_stride,
+                    const int32_t* slots, const w4a16_kv_cache* cache, int T, void* stream);
+
+/* Causal attention of a step's T query rows over the cache, after the step's
+ * keys and values were appended.  q is bf16, token t's q_heads * dim values at
+ * q + t * q_stride (elements, a multiple of 8; 16-byte aligned); query head j
+ * reads key/value head j / (q_heads / heads).  cu, lens and table are a
+ * plan's.  Token t of request b stands at position p = lens[b] - (cu[b+1] -
+ * cu[b]) + t - cu[b] and sees tokens s in max(0, p - window + 1) .. p
+ * (window 0: all of 0 .. p):
+ *   out[t][j] = bf16( sum_s exp(z_s) V_s / sum_s exp(z_s) ),  z_s = scale * q . K_s
+ * with fp32 scores, maxima, sums and accumulators; the weights exp(z) enter
+ * the product with V rounded to 8 significant bits, as bf16 would, and q
+ * enters exactly.  Tokens that a row does not see have no effect on it,
+ * whatever their bytes (NaN codes included); nor have tokens whose table
+ * entry is not a block of the cache (those raise W4A16_DEVICE_KV_RANGE).  A
+ * row that sees nothing, and a row t >= cu[B], is written as zeros.
+ * out is bf16 [T][q_heads][dim], 16-byte aligned.
+ *
+ * max_new and max_len bound the step: requests have at most max_new new
+ * tokens and lens[b] <= max_len (max_len <= max_blocks * block).  They only
+ * size the launch and the workspace.  All rows of a request that exceeds one
+ * of them (or is shorter than its new tokens) are written as zeros, and
+ * W4A16_DEVICE_KV_RANGE is raised.
+ *
+ * Batch invariance.  The tokens are taken in tiles at fixed positions and
+ * joined in a fixed order, whatever the batch: out[t] depends, bit for bit,
+ * only on its query row, its position and the tokens it sees; so row m of a
+ * verify step equals the one-token step at that position over the same cache.
+ *
+ * workspace: w4a16_kv_attention_workspace_bytes(...) bytes of device memory,
+ * 256-byte aligned, no initial contents needed; calls that share one must
+ * not overlap on the GPU. */
+#define W4A16_KV_MAX_GROUP 32 /* query heads per key/value head */
+
+size_t w4a16_kv_attention_workspace_bytes(int B, int T, int q_heads, int heads, int dim, int max_new, int max_len,
+                                          int window);
+int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cache* cache, const int32_t* table,
+                       const int32_t* cu, const int32_t* lens, w4a16_bf16* out, int B, int T, int q_heads,
+                       int max_blocks, int max_new, int max_len, int window, float scale, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* Debug: q[N][K] (one byte per code) from Wq[N][K/8].  Bit-exact
  * ([W2D2 "Packed Storage Layout"]). */
 int w4a16_unpack(const uint32_t* Wq, uint8_t* q, int N, int K, void* stream);
@@ -341,6 +450,7 @@ int w4a16_get_plan(int N, int K, int kernel, w4a16_plan* out);
 /* Sticky device-side error flags, raised by kernels instead of trapping. */
 #define W4A16_DEVICE_BAD_ID 1   /* mm_id: an expert id outside 0..E-1 */
 #define W4A16_DEVICE_TIMEOUT 2  /* a bounded wait on an asynchronous copy gave up */
+#define W4A16_DEVICE_KV_RANGE 4 /* kv_*: a length, slot, block id or bound out of range */
 
 /* Synchronises `stream`, reads and clears the device flags of the current
  * device.  Returns W4A16_OK when no flag was set, W4A16_ERR_DEVICE when one

@@ -13,6 +13,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "kv.cuh"
 #include "launch.h"
 #include "stq1.cuh"
 #include "stq1.h"
@@ -547,6 +548,118 @@ int stq1_get_rows(const uint8_t* packed, const int32_t* ids, float* out, int T, 
   if (int rc = flag_pointer(&flags)) return rc;
   cudaError_t e = launch_stq1_get_rows(packed, ids, out, T, N, K, flags, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "stq1_get_rows launch");
+}
+
+// ---- paged key/value cache in 8 bits ----------------------------------------------
+
+namespace {
+
+bool kv_block_ok(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
+
+int check_kv_cache(const w4a16_kv_cache* c) {
+  if (!c) return fail(W4A16_ERR_NULL, "null cache");
+  if (!kv_block_ok(c->block)) return fail(W4A16_ERR_SHAPE, "block = %d must be 16, 32, 64 or 128", c->block);
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256)
+    return fail(W4A16_ERR_SHAPE, "dim = %d must be 64, 128 or 256", c->dim);
+  if (c->heads < 1 || c->heads > 65535) return fail(W4A16_ERR_SHAPE, "heads = %d must be in 1..65535", c->heads);
+  if (c->blocks < 1 || (int64_t)c->blocks * c->heads * c->block > INT32_MAX)
+    return fail(W4A16_ERR_SHAPE, "blocks = %d: blocks * heads * block must be in 1..2^31 - 1", c->blocks);
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(W4A16_ERR_NULL, "null cache pointer");
+  if (misaligned(c->k, 16) || misaligned(c->v, 16) || misaligned(c->k_scale, 4) || misaligned(c->v_scale, 4))
+    return fail(W4A16_ERR_ALIGN, "cache codes must be 16-byte and scales 4-byte aligned");
+  return W4A16_OK;
+}
+
+}  // namespace
+
+int w4a16_kv_plan(const int32_t* cached, const int32_t* fresh, int32_t* table, const int32_t* free_blocks,
+                  const int32_t* head, int32_t* cu, int32_t* lens, int32_t* slots, int32_t* positions,
+                  int32_t* head_out, int B, int T, int block, int max_blocks, int n_free, void* stream) {
+  if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
+  if (B < 0 || B >= kMaxDim || T < 0 || T >= kMaxDim)
+    return fail(W4A16_ERR_SHAPE, "B = %d and T = %d must be in 0..2^30 - 1", B, T);
+  if (!kv_block_ok(block)) return fail(W4A16_ERR_SHAPE, "block = %d must be 16, 32, 64 or 128", block);
+  if (max_blocks < 1 || n_free < 0)
+    return fail(W4A16_ERR_SHAPE, "max_blocks = %d must be at least 1 and n_free = %d not negative", max_blocks, n_free);
+  if (!cu || !head_out || (B > 0 && (!cached || !fresh || !table || !lens)) || (T > 0 && (!slots || !positions)) ||
+      (n_free > 0 && !free_blocks))
+    return fail(W4A16_ERR_NULL, "null array");
+  if (head == head_out) return fail(W4A16_ERR_SHAPE, "head_out must not be head");
+  const void* all[] = {cached, fresh, table, free_blocks, head, cu, lens, slots, positions, head_out};
+  for (const void* q : all)
+    if (misaligned(q, 4)) return fail(W4A16_ERR_ALIGN, "arrays must be 4-byte aligned");
+  if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
+  KvPlanArgs a{cached, fresh, table, free_blocks, head, cu, lens, slots, positions, head_out,
+               B, T, block, max_blocks, n_free, nullptr};
+  if (int rc = flag_pointer(&a.flags)) return rc;
+  cudaError_t e = launch_kv_plan(a, env().pdl, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_kv_plan launch");
+}
+
+int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, int64_t v_stride,
+                    const int32_t* slots, const w4a16_kv_cache* cache, int T, void* stream) {
+  if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
+  if (int rc = check_kv_cache(cache)) return rc;
+  if (T < 0 || T >= kMaxDim) return fail(W4A16_ERR_SHAPE, "T = %d must be in 0..2^30 - 1", T);
+  if (T == 0) return W4A16_OK;
+  if (!k || !v || !slots) return fail(W4A16_ERR_NULL, "null tensor pointer");
+  const int64_t row = (int64_t)cache->heads * cache->dim;
+  if (T > 1 && (k_stride < row || v_stride < row))
+    return fail(W4A16_ERR_SHAPE, "token strides must be at least heads * dim = %lld elements", (long long)row);
+  if (misaligned(k, 16) || misaligned(v, 16) || k_stride % 8 || v_stride % 8 || misaligned(slots, 4))
+    return fail(W4A16_ERR_ALIGN, "k and v rows must be 16-byte and slots 4-byte aligned");
+  if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
+  KvAppendArgs a{k, v, k_stride, v_stride, slots, *cache, T, nullptr};
+  if (int rc = flag_pointer(&a.flags)) return rc;
+  cudaError_t e = launch_kv_append(a, env().pdl, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_kv_append launch");
+}
+
+size_t w4a16_kv_attention_workspace_bytes(int B, int T, int q_heads, int heads, int dim, int max_new, int max_len,
+                                          int window) {
+  if (B < 1 || T < 1 || heads < 1 || q_heads < heads || q_heads % heads || max_new < 1 || max_len < 1 || window < 0 ||
+      (dim != 64 && dim != 128 && dim != 256))
+    return 0;
+  return kv_attention_workspace(B, T, q_heads, heads, dim, max_new, max_len, window);
+}
+
+int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cache* cache, const int32_t* table,
+                       const int32_t* cu, const int32_t* lens, w4a16_bf16* out, int B, int T, int q_heads,
+                       int max_blocks, int max_new, int max_len, int window, float scale, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
+  if (int rc = check_kv_cache(cache)) return rc;
+  if (B < 0 || B >= kMaxDim || T < 0 || T >= kMaxDim)
+    return fail(W4A16_ERR_SHAPE, "B = %d and T = %d must be in 0..2^30 - 1", B, T);
+  if (T > 0 && B == 0) return fail(W4A16_ERR_SHAPE, "T = %d tokens of no request", T);
+  if (q_heads < cache->heads || q_heads % cache->heads || q_heads / cache->heads > W4A16_KV_MAX_GROUP)
+    return fail(W4A16_ERR_SHAPE, "q_heads = %d must be 1..%d times the cache's %d heads", q_heads, W4A16_KV_MAX_GROUP,
+                cache->heads);
+  if (max_blocks < 1 || max_new < 1 || max_len < 1 || window < 0 ||
+      (int64_t)max_len > (int64_t)max_blocks * cache->block)
+    return fail(W4A16_ERR_SHAPE,
+                "max_blocks = %d and max_new = %d must be positive, window = %d not negative, max_len = %d in "
+                "1..max_blocks * block", max_blocks, max_new, window, max_len);
+  if (!(scale > 0.f) || scale > 3.0e38f) return fail(W4A16_ERR_SHAPE, "scale must be a positive number");
+  if (T == 0) return W4A16_OK;
+  if (!q || !table || !cu || !lens || !out) return fail(W4A16_ERR_NULL, "null tensor pointer");
+  if (T > 1 && q_stride < (int64_t)q_heads * cache->dim)
+    return fail(W4A16_ERR_SHAPE, "q_stride must be at least q_heads * dim = %lld elements",
+                (long long)q_heads * cache->dim);
+  if (misaligned(q, 16) || q_stride % 8 || misaligned(out, 16) || misaligned(table, 4) || misaligned(cu, 4) ||
+      misaligned(lens, 4))
+    return fail(W4A16_ERR_ALIGN, "q rows and out must be 16-byte, table, cu and lens 4-byte aligned");
+  const size_t need = kv_attention_workspace(B, T, q_heads, cache->heads, cache->dim, max_new, max_len, window);
+  if (need > 0 && !workspace) return fail(W4A16_ERR_NULL, "w4a16_kv_attention needs a workspace of %zu bytes", need);
+  if (misaligned(workspace, 256)) return fail(W4A16_ERR_ALIGN, "the workspace must be 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(W4A16_ERR_SHAPE, "a workspace of %zu bytes is too small (%zu)", workspace_bytes, need);
+  if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
+  KvAttentionArgs a{q, q_stride, *cache, table, cu, lens, out, B, T, q_heads, max_blocks, max_new, max_len, window,
+                    scale, workspace, nullptr};
+  if (int rc = flag_pointer(&a.flags)) return rc;
+  cudaError_t e = launch_kv_attention(a, env().pdl, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_kv_attention launch");
 }
 
 const char* w4a16_last_error(void) { return g_last_error.c_str(); }

@@ -1,0 +1,416 @@
+// kv.cu -- the paged key/value cache in 8 bits: block tables and slots from
+// request lengths (w4a16_kv_plan) and the quantising write (w4a16_kv_append).
+// The formulas are those of include/w4a16.h "Paged key/value cache".
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kv.cuh"
+#include "ptx.cuh"
+
+namespace w4a16 {
+namespace {
+
+using namespace ptx;
+
+cudaError_t launch(const void* fn, dim3 grid, int threads, void** args, int pdl, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl > 0 ? 1 : 0;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// ---- plan ----------------------------------------------------------------------------------
+//
+// Two exclusive prefix sums over the requests (new tokens, blocks to take),
+// then every token and every taken block finds its request by bisection in
+// the sums.  A call is a few kilobytes: the floor is the launch and three
+// dependent loads (lengths, table or free list, store).  Every CTA computes
+// the sums itself (requests in chunks of kPlanThreads, the running totals
+// carried in registers), so nothing is handed between CTAs and one launch
+// does it all.
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanTokens = 2048;  // tokens per CTA
+
+struct PlanParams {
+  KvPlanArgs a;
+  int shift;  // log2(block)
+};
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
+  __shared__ int s_cu[kPlanThreads + 1], s_first[kPlanThreads + 1], s_cached[kPlanThreads];
+  __shared__ int s_warp[2][32];
+  const KvPlanArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_thr = blockDim.x;
+  const int t0 = blockIdx.x * kPlanTokens, t1 = min(t0 + kPlanTokens, a.T);
+  pdl_launch_dependents();
+  pdl_wait();
+  const int head = a.head ? max(*a.head, 0) : 0;
+  int tok = 0;  // tokens and blocks of the requests before this chunk; both stay within T
+  int taken = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < a.B; b0 += n_thr) {
+    const int b = b0 + tid, n = min(n_thr, a.B - b0);
+    int cached = 0, fresh = 0;
+    if (b < a.B) {
+      cached = a.cached[b];
+      fresh = a.fresh[b];
+      if (cached < 0 || fresh < 0 || fresh > a.T || cached > INT32_MAX - a.T) {
+        bad = true;
+        cached = min(max(cached, 0), INT32_MAX - a.T);
+        fresh = min(max(fresh, 0), a.T);
+      }
+    }
+    // inclusive sum over the chunk, saturated at T after every step (T < 2^30: no overflow)
+    int c = fresh;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, c, d);
+      if (lane >= d) c = min(c + o, a.T);
+    }
+    if (lane == 31) s_warp[0][warp] = c;
+    __syncthreads();
+    if (warp == 0) {
+      int w = lane < (n_thr >> 5) ? s_warp[0][lane] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, w, d);
+        if (lane >= d) w = min(w + o, a.T);
+      }
+      s_warp[0][lane] = w;
+    }
+    __syncthreads();
+    const int incl = min((warp ? min(c + s_warp[0][warp - 1], a.T) : c) + tok, a.T);
+    if (tid == 0) s_cu[0] = tok;
+    s_cu[tid + 1] = incl;
+    __syncthreads();
+    const int mine = incl - s_cu[tid];  // tokens this request gets (fewer only past T)
+    bad |= mine < fresh;
+    const int len = cached + mine;
+    const int have = min((int)(((int64_t)cached + a.block - 1) >> p.shift), a.max_blocks);
+    const int want = (int)(((int64_t)len + a.block - 1) >> p.shift), need = min(want, a.max_blocks);
+    bad |= need < want;
+    const int take = b < a.B ? need - have : 0;  // at most the request's new tokens
+    int f = take;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, f, d);
+      if (lane >= d) f += o;
+    }
+    if (lane == 31) s_warp[1][warp] = f;
+    __syncthreads();
+    if (warp == 0) {
+      int w = lane < (n_thr >> 5) ? s_warp[1][lane] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, w, d);
+        if (lane >= d) w += o;
+      }
+      s_warp[1][lane] = w;
+    }
+    __syncthreads();
+    const int fincl = f + (warp ? s_warp[1][warp - 1] : 0) + taken;
+    if (tid == 0) s_first[0] = taken;
+    s_first[tid + 1] = fincl;
+    s_cached[tid] = cached;
+    if (blockIdx.x == 0 && b < a.B) {
+      a.cu[b] = s_cu[tid];
+      a.lens[b] = len;
+    }
+    __syncthreads();
+    // request of item x: the last i with sums[i] <= x (x is below the chunk's total)
+    auto find = [&](const int* sums, int x) {
+      int lo = 0, hi = n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sums[mid] <= x) lo = mid;
+        else hi = mid;
+      }
+      return lo;
+    };
+    auto free_block = [&](int i) {  // entry `head + i` of the free list, -1 past its end
+      const int64_t at = (int64_t)head + i;
+      if (at >= a.n_free) {
+        bad = true;
+        return -1;
+      }
+      return a.free_blocks[at];
+    };
+    for (int t = max(t0, tok) + tid; t < min(t1, s_cu[n]); t += n_thr) {
+      const int i = find(s_cu, t);
+      const int pos = s_cached[i] + t - s_cu[i], j = pos >> p.shift;
+      int entry = -1;
+      if (j < a.max_blocks) {
+        const int held = (int)(((uint32_t)s_cached[i] + (uint32_t)a.block - 1) >> p.shift);
+        entry = j < held ? a.table[(int64_t)(b0 + i) * a.max_blocks + j] : free_block(s_first[i] + j - held);
+      }
+      const int64_t slot = ((int64_t)entry << p.shift) + (pos & (a.block - 1));
+      const bool ok = entry >= 0 && slot <= INT32_MAX;
+      bad |= !ok;
+      a.slots[t] = ok ? (int)slot : -1;
+      a.positions[t] = pos;
+    }
+    for (int e = taken + blockIdx.x * n_thr + tid; e < s_first[n]; e += gridDim.x * n_thr) {
+      const int i = find(s_first, e);
+      const int held = (int)(((uint32_t)s_cached[i] + (uint32_t)a.block - 1) >> p.shift);
+      a.table[(int64_t)(b0 + i) * a.max_blocks + held + e - s_first[i]] = free_block(e);
+    }
+    tok = s_cu[n];
+    taken = s_first[n];
+    __syncthreads();
+  }
+  for (int t = max(t0, tok) + tid; t < t1; t += n_thr) {  // past the last token (a padded batch)
+    a.slots[t] = -1;
+    a.positions[t] = -1;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.cu[a.B] = tok;
+    *a.head_out = (int)min((int64_t)head + taken, (int64_t)max(head, a.n_free));
+  }
+  if (bad) atomicOr(a.flags, W4A16_DEVICE_KV_RANGE);
+}
+
+// ---- append --------------------------------------------------------------------------------
+//
+// A run is a maximal stretch of consecutive tokens of the call with
+// consecutive slots of one block; one (run, head, K or V) sets the scale of
+// one (block, head), so it belongs to one warp (up to kShortRun tokens, no
+// requantisation: decode and verify) or, after a barrier, to the whole CTA.
+// Bytes: 2 in and 1 out per element; nothing is read twice: a run's rows
+// stay in registers between the maximum and the codes.
+
+constexpr int kAppendThreads = 256, kAppendWarps = 8;  // a CTA looks at eight tokens
+constexpr int kShortRun = 4;
+constexpr int kMinExp = -64;
+
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
+__device__ __forceinline__ int exp_of(float s) { return (int)((__float_as_uint(s) >> 23) & 255) - 127; }
+
+// The smallest e >= kMinExp with a <= 448 * 2^e, for a finite bf16 magnitude
+// given by its bits: 448 = 1.75 * 2^8, so e is the exponent less 8, one more
+// when the significand is above 1.75 (subnormals are below 2^(kMinExp)).
+__device__ __forceinline__ int scale_exp(uint32_t bits) {
+  const int e = (int)(bits >> 7) - 127 - 8 + ((bits & 127) > 96 ? 1 : 0);
+  return max(e, kMinExp);
+}
+
+// The largest finite magnitude (bf16 bits) of eight values, and whether any is not finite.
+__device__ __forceinline__ uint32_t peak8(const uint4& v, bool& odd) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = word_of(v, i) & 0x7FFF7FFFu;
+    const uint32_t lo = w & 0xFFFF, hi = w >> 16;
+    const bool blo = lo >= 0x7F80, bhi = hi >= 0x7F80;
+    odd |= blo | bhi;
+    m = max(m, max(blo ? 0u : lo, bhi ? 0u : hi));
+  }
+  return m;
+}
+
+// Eight bf16 values times `inv` as e4m3 codes, round to nearest even (one
+// rounding: the product with a power of two is exact).  NaN and infinities
+// become the NaN code (the conversion alone would clamp infinities to 448).
+__device__ __forceinline__ uint2 codes8(const uint4& v, float inv, bool odd) {
+  float f[8];
+  widen8(v, f);
+  uint16_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x = f[2 * i], y = f[2 * i + 1];
+    if (odd) {
+      if (isinf(x)) x = __uint_as_float(0x7FC00000u);
+      if (isinf(y)) y = __uint_as_float(0x7FC00000u);
+    }
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x, inv), __fmul_rn(y, inv)), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+}
+
+// Four e4m3 codes at a larger scale: times `ratio` (a power of two below 1).
+__device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    out |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f.x, ratio), __fmul_rn(f.y, ratio)), __NV_SATFINITE,
+                                              __NV_E4M3)
+           << (16 * i);
+  }
+  return out;
+}
+
+struct AppendParams {
+  KvAppendArgs a;
+  int shift;   // log2(block)
+  int lpr;     // log2(16-byte chunks of a row): dim = 8 << lpr
+  int slots;   // blocks * block
+};
+
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams p) {
+  __shared__ int s_job[kAppendWarps][2];  // (first slot, tokens) of a run left to the CTA; tokens 0: none
+  __shared__ uint32_t s_peak[kAppendWarps];
+  const KvAppendArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.y, val = blockIdx.z;
+  const int heads = a.cache.heads, dim = a.cache.dim, block = a.cache.block, lpr = p.lpr;
+  const uint16_t* src = (val ? a.v : a.k) + (int64_t)h * dim;
+  const int64_t stride = val ? a.v_stride : a.k_stride;
+  uint8_t* codes = val ? a.cache.v : a.cache.k;
+  float* scales = val ? a.cache.v_scale : a.cache.k_scale;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int t = blockIdx.x * kAppendWarps + warp;
+  int slot = -1, n = 0;
+  if (t < a.T) {
+    // lane 0 the slot before, lane 1 this token's, lanes 2.. the next ones
+    const int tt = t - 1 + lane;
+    const int s = tt >= 0 && tt < a.T ? a.slots[tt] : -1;
+    const int prev = __shfl_sync(0xffffffffu, s, 0);
+    slot = __shfl_sync(0xffffffffu, s, 1);
+    const bool valid = slot >= 0 && slot < p.slots;
+    if (slot < -1 || slot >= p.slots) {
+      if (h == 0 && val == 0 && lane == 0) atomicOr(a.flags, W4A16_DEVICE_KV_RANGE);
+    }
+    const bool joins = prev >= 0 && prev + 1 == slot && (prev >> p.shift) == (slot >> p.shift);
+    if (valid && !joins) {
+      const int room = block - (slot & (block - 1));
+      // tokens of the run: consecutive slots up to the block's end
+      const unsigned same = __ballot_sync(0xffffffffu, lane == 0 || s == slot + lane - 1);
+      n = min(same == 0xffffffffu ? 31 : __ffs(~same) - 2, room);
+      while (n >= 31 && n < room) {  // longer than this warp's look ahead
+        const int more = t + n + lane;
+        const unsigned go = __ballot_sync(0xffffffffu, more < a.T && a.slots[min(more, a.T - 1)] == slot + n + lane);
+        const int k = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
+        n = min(n + k, room);
+        if (k < 32) break;
+      }
+    }
+  }
+  const int blk = slot >> p.shift, off = slot & (block - 1);
+  bool job = n > kShortRun;
+  if (n > 0 && !job) {
+    // a warp's run: dim / 8 lanes a row, 32 * 8 / dim rows a pass
+    const int rpp = 32 >> lpr, sub = lane >> lpr, c = lane & ((1 << lpr) - 1);
+    uint4 v[kShortRun];
+    uint32_t peak = 0;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < kShortRun; ++i) {
+      const int r = i * rpp + sub;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r < n) v[i] = ld_nc_v4(src + (t + r) * stride + 8 * c);
+    }
+    const int64_t at = (int64_t)blk * heads + h;
+    const float old = off ? scales[at] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kShortRun; ++i) peak = max(peak, peak8(v[i], odd));
+    peak = __reduce_max_sync(0xffffffffu, peak);
+    int e = scale_exp(peak);
+    if (off) {
+      const int eo = exp_of(old);
+      job = e > eo;  // earlier codes move to a larger scale: the whole CTA's work
+      e = max(e, eo);
+    }
+    if (!job) {
+      const float inv = exp2i(-e);
+#pragma unroll
+      for (int i = 0; i < kShortRun; ++i) {
+        const int r = i * rpp + sub;
+        if (r < n)
+          *reinterpret_cast<uint2*>(codes + ((at << p.shift) + off + r) * dim + 8 * c) = codes8(v[i], inv, odd);
+      }
+      if (off == 0 && lane == 0) scales[at] = exp2i(e);
+    }
+  }
+  if (lane == 0) {
+    s_job[warp][0] = slot;
+    s_job[warp][1] = job ? n : 0;
+  }
+  __syncthreads();
+
+  // long runs and requantisations, the CTA on one after another
+  for (int w = 0; w < kAppendWarps; ++w) {
+    const int jn = s_job[w][1];
+    if (jn == 0) continue;
+    const int js = s_job[w][0], jt = blockIdx.x * kAppendWarps + w;
+    const int jo = js & (block - 1);
+    const int64_t at = (int64_t)(js >> p.shift) * heads + h;
+    constexpr int kPer = 128 * 32 / kAppendThreads;  // chunks a thread holds of the largest run (128 tokens of 256)
+    uint4 v[kPer];
+    uint32_t peak = 0;
+    bool odd = false;
+    const int chunks = jn << lpr;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int x = i * kAppendThreads + tid;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (x < chunks) v[i] = ld_nc_v4(src + (jt + (x >> lpr)) * stride + 8 * (x & ((1 << lpr) - 1)));
+    }
+    const float old = jo ? scales[at] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) peak = max(peak, peak8(v[i], odd));
+    peak = __reduce_max_sync(0xffffffffu, peak);
+    if (lane == 0) s_peak[warp] = peak;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAppendWarps; ++i) peak = max(peak, s_peak[i]);
+    int e = scale_exp(peak);
+    uint8_t* base = codes + (at << p.shift) * dim;
+    if (jo) {
+      const int eo = exp_of(old);
+      if (e > eo) {
+        const float ratio = exp2i(max(eo - e, -126));
+        uint4* q = reinterpret_cast<uint4*>(base);
+        for (int x = tid; x < jo << (lpr - 1); x += kAppendThreads) {
+          uint4 w4 = q[x];
+          w4.x = recode4(w4.x, ratio);
+          w4.y = recode4(w4.y, ratio);
+          w4.z = recode4(w4.z, ratio);
+          w4.w = recode4(w4.w, ratio);
+          q[x] = w4;
+        }
+      }
+      e = max(e, eo);
+    }
+    const float inv = exp2i(-e);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int x = i * kAppendThreads + tid;
+      if (x < chunks) *reinterpret_cast<uint2*>(base + jo * dim + 8 * (int64_t)x) = codes8(v[i], inv, odd);
+    }
+    __syncthreads();  // every thread has read the old scale (and s_peak)
+    if (tid == 0) scales[at] = exp2i(e);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const KvPlanArgs& a, int pdl, cudaStream_t s) {
+  PlanParams p{a, __builtin_ctz((unsigned)a.block)};
+  // a thread per request and per token up to the CTA's size, at least four warps
+  int threads = a.B > a.T ? a.B : a.T;
+  threads = threads < 128 ? 128 : threads > kPlanThreads ? kPlanThreads : (threads + 31) / 32 * 32;
+  const int grid = a.T > 0 ? (a.T + kPlanTokens - 1) / kPlanTokens : 1;
+  void* args[] = {&p};
+  return launch((const void*)kv_plan_kernel, dim3((unsigned)grid), threads, args, pdl, s);
+}
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, int pdl, cudaStream_t s) {
+  AppendParams p{a, __builtin_ctz((unsigned)a.cache.block), __builtin_ctz((unsigned)a.cache.dim) - 3,
+                 a.cache.blocks * a.cache.block};
+  void* args[] = {&p};
+  return launch((const void*)kv_append_kernel,
+                dim3((unsigned)((a.T + kAppendWarps - 1) / kAppendWarps), (unsigned)a.cache.heads, 2), kAppendThreads, args,
+                pdl, s);
+}
+
+}  // namespace w4a16

@@ -8,11 +8,14 @@ Names follow the C ABI in ``include/w4a16.h``: ``mm``, ``mm_group``,
 ``mm_id``, ``unpack``, ``dequant``, ``get_plan``, ``device_status``; and in
 ``include/stq1.h`` for the STQ1_0 ternary format: ``stq1_mm``,
 ``stq1_mm_id``, ``stq1_get_rows``, ``stq1_get_plan`` over an ``STQ1Matrix``
-(repacked on the device by ``stq1_pack``).
+(repacked on the device by ``stq1_pack``).  Between a layer's q/k/v and o
+projections: ``kv_plan``, ``kv_append`` and ``kv_attention`` over a ``KVCache``
+(paged keys and values in 8 bits).
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import threading
 from dataclasses import dataclass
 
@@ -25,11 +28,12 @@ GROUP = 64
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_EXPERTS, ERR_CUDA, ERR_KERNEL, ERR_DEVICE = 0, -1, -2, -3, -4, -5, -6, -7
 KERNELS = {"auto": 0, "simt": 1, "tc": 2, "vanilla": 3, "tc_stream": 4, "tc_tile": 5, "tc_prefill": 6}
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
-DEVICE_BAD_ID = 1
+DEVICE_BAD_ID, DEVICE_TIMEOUT, DEVICE_KV_RANGE = 1, 2, 4
 
 EXPORTS = ("w4a16_mm", "w4a16_mm_ws", "w4a16_mm_g", "w4a16_workspace_bytes", "w4a16_mm_kernel", "w4a16_mm_noalloc", "w4a16_mm_group", "w4a16_mm_argmax", "w4a16_embed", "w4a16_expand_groups",
            "w4a16_mm_id", "w4a16_mm_id_kernel", "w4a16_unpack", "w4a16_dequant", "w4a16_get_plan", "w4a16_device_status", "w4a16_last_error",
            "w4a16_debug_reload_env", "w4a16_version",
+           "w4a16_kv_plan", "w4a16_kv_append", "w4a16_kv_attention", "w4a16_kv_attention_workspace_bytes",
            "stq1_packed_bytes", "stq1_pack", "stq1_mm", "stq1_mm_id", "stq1_get_rows", "stq1_get_plan")
 MAX_GROUP = 8
 STQ1_BLOCK_WEIGHTS, STQ1_BLOCK_BYTES = 256, 42
@@ -68,6 +72,13 @@ class Item(ctypes.Structure):
                 ("biases", ctypes.c_void_p), ("y", ctypes.c_void_p), ("N", ctypes.c_int)]
 
 
+class KvCacheStruct(ctypes.Structure):
+    """w4a16_kv_cache (device pointers)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("blocks", ctypes.c_int), ("heads", ctypes.c_int),
+                ("block", ctypes.c_int), ("dim", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 
@@ -101,6 +112,12 @@ def lib() -> ctypes.CDLL:
             L.w4a16_dequant.argtypes = [P, P, P, P, i, i, P]
             L.w4a16_get_plan.argtypes = [i, i, i, ctypes.POINTER(Plan)]
             L.w4a16_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_int)]
+            ll, f = ctypes.c_int64, ctypes.c_float
+            L.w4a16_kv_plan.argtypes = [P] * 10 + [i] * 5 + [P]
+            L.w4a16_kv_append.argtypes = [P, ll, P, ll, P, P, i, P]
+            L.w4a16_kv_attention.argtypes = [P, ll, P, P, P, P, P] + [i] * 7 + [f, P, z, P]
+            L.w4a16_kv_attention_workspace_bytes.argtypes = [i] * 8
+            L.w4a16_kv_attention_workspace_bytes.restype = z
             L.stq1_packed_bytes.argtypes = [i, i]
             L.stq1_packed_bytes.restype = ctypes.c_size_t
             L.stq1_pack.argtypes = [P, P, i, i, P]
@@ -110,7 +127,8 @@ def lib() -> ctypes.CDLL:
             L.stq1_get_plan.argtypes = [i, i, ctypes.POINTER(Stq1Plan)]
             for f in ("w4a16_mm", "w4a16_mm_ws", "w4a16_mm_g", "w4a16_mm_kernel", "w4a16_mm_noalloc", "w4a16_mm_group", "w4a16_mm_argmax",
                       "w4a16_embed", "w4a16_expand_groups", "w4a16_mm_id", "w4a16_mm_id_kernel", "w4a16_unpack", "w4a16_dequant",
-                      "w4a16_get_plan", "w4a16_device_status", "stq1_pack", "stq1_mm", "stq1_mm_id", "stq1_get_rows",
+                      "w4a16_get_plan", "w4a16_device_status", "w4a16_kv_plan", "w4a16_kv_append", "w4a16_kv_attention",
+                      "stq1_pack", "stq1_mm", "stq1_mm_id", "stq1_get_rows",
                       "stq1_get_plan"):
                 getattr(L, f).restype = ctypes.c_int
             L.w4a16_last_error.restype = ctypes.c_char_p
@@ -544,6 +562,167 @@ def stq1_get_plan(N: int, K: int) -> dict:
     p = Stq1Plan()
     _raise(lib().stq1_get_plan(N, K, ctypes.byref(p)))
     return {f: getattr(p, f) for f, _ in p._fields_}
+
+
+# ---- paged key/value cache in 8 bits (include/w4a16.h "Paged key/value cache") --------------
+
+KV_BLOCKS, KV_DIMS, KV_MAX_GROUP = (16, 32, 64, 128), (64, 128, 256), 32
+
+
+@dataclass
+class KVCache:
+    """Keys and values of one layer: e4m3 codes ``k``, ``v`` (torch.float8_e4m3fn
+    [blocks, heads, block, dim]) with one power-of-two scale per (block, head)
+    ``k_scale``, ``v_scale`` (float32 [blocks, heads]).  ``kv_append`` fills
+    blocks; their first contents do not matter (``empty`` leaves them unset)."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def __post_init__(self):
+        for name in ("k", "v"):
+            t = _dev_tensor(getattr(self, name), torch.float8_e4m3fn, name)
+            if t.dim() != 4 or t.shape != self.k.shape:
+                raise ValueError(f"{name} must be [blocks, heads, block, dim] (got {tuple(t.shape)})")
+        self.blocks, self.heads, self.block, self.dim = self.k.shape
+        if self.block not in KV_BLOCKS or self.dim not in KV_DIMS:
+            raise ValueError(f"block {self.block} must be one of {KV_BLOCKS}, dim {self.dim} one of {KV_DIMS}")
+        for name in ("k_scale", "v_scale"):
+            t = _dev_tensor(getattr(self, name), torch.float32, name)
+            if t.shape != (self.blocks, self.heads):
+                raise ValueError(f"{name} must be [blocks, heads] (got {tuple(t.shape)})")
+        if any(t.device != self.k.device for t in (self.v, self.k_scale, self.v_scale)):
+            raise ValueError("the cache's tensors must be on one device")
+        self._c = KvCacheStruct(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                                self.blocks, self.heads, self.block, self.dim)
+        self._ptr = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, blocks: int, heads: int, block: int, dim: int, device="cuda") -> "KVCache":
+        k, v = (torch.empty(blocks, heads, block, dim, dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
+        ks, vs = (torch.empty(blocks, heads, dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale))
+
+
+@dataclass
+class KVPlan:
+    """One step's rows (int32, on the device): ``cu`` [B + 1] first row of each
+    request, ``lens`` [B] lengths after the step, ``slots`` and ``positions``
+    [T], ``head`` [1] free-list entries taken so far."""
+
+    cu: torch.Tensor
+    lens: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    head: torch.Tensor
+
+    @classmethod
+    def empty(cls, B: int, T: int, device="cuda") -> "KVPlan":
+        return cls(*torch.empty(2 * B + 2 * T + 2, dtype=torch.int32, device=device).split((B + 1, B, T, T, 1)))
+
+
+def _i32(t: torch.Tensor, name: str, n: int | None = None) -> int:
+    """The address of a contiguous int32 CUDA tensor of n elements (None: any)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32 and t.is_contiguous()):
+        _dev_tensor(t, torch.int32, name)
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements (got {t.numel()})")
+    return t.data_ptr()
+
+
+def _kv_rows(t: torch.Tensor, name: str, heads: int, dim: int) -> int:
+    """The token stride of a bf16 CUDA tensor [T, heads, dim] whose rows are dense
+    (the tokens may be further apart: columns of a fused projection)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}] (got {tuple(t.shape)})")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != dim and heads > 1):
+        raise ValueError(f"{name}: each token's heads * dim values must be contiguous")
+    return s0 if t.shape[0] > 1 else heads * dim
+
+
+def kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: torch.Tensor, T: int, block: int,
+            head: torch.Tensor | None = None, out: KVPlan | None = None, stream=None) -> KVPlan:
+    """Block tables, slots and positions of a step through ``w4a16_kv_plan``.
+
+    cached, new: int32 [B] tokens of each request in the cache and joining it;
+    table: int32 [B, max_blocks], its entries for the new blocks written in
+    place; free: int32 block ids to take from, beginning at entry ``head``
+    (int32 [1] on the device; None is 0; the plan's ``head`` is the next one).
+    T rows: the sum of ``new``, or more (the rest get slot -1)."""
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_blocks]")
+    B, max_blocks = table.shape
+    if out is None:
+        out = KVPlan.empty(B, T, table.device)
+    rc = lib().w4a16_kv_plan(
+        _i32(cached, "cached", B), _i32(new, "new", B), _i32(table, "table"), _i32(free, "free"),
+        None if head is None else _i32(head, "head", 1), _i32(out.cu, "cu", B + 1), _i32(out.lens, "lens", B),
+        _i32(out.slots, "slots", T), _i32(out.positions, "positions", T), _i32(out.head, "head_out", 1),
+        B, T, block, max_blocks, free.numel(), _stream_ptr(stream))
+    _raise(rc)
+    return out
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Tensor, stream=None) -> None:
+    """Write keys and values k, v (bf16 [T, heads, dim]; tokens may be strided)
+    into ``slots`` (int32 [T], a plan's) of ``cache`` through ``w4a16_kv_append``."""
+    ks, vs = _kv_rows(k, "k", cache.heads, cache.dim), _kv_rows(v, "v", cache.heads, cache.dim)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of tokens")
+    _raise(lib().w4a16_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _i32(slots, "slots", T), cache._ptr, T,
+                                 _stream_ptr(stream)))
+
+
+def kv_attention_workspace_bytes(B: int, T: int, q_heads: int, cache: KVCache, max_new: int, max_len: int,
+                                 window: int = 0) -> int:
+    return int(lib().w4a16_kv_attention_workspace_bytes(B, T, q_heads, cache.heads, cache.dim, max_new, max_len, window))
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
+                 max_new: int, max_len: int, scale: float | None = None, window: int = 0,
+                 out: torch.Tensor | None = None, stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of q (bf16 [T, q_heads, dim]; tokens may be strided) over
+    ``cache`` through ``w4a16_kv_attention``: bf16 [T, q_heads, dim].
+
+    table, cu, lens: a plan's; max_new, max_len: the caller's bounds on the
+    requests' new tokens and lengths; scale: 1 / sqrt(dim) by default; window:
+    tokens that a row sees, itself included (0: all).  The workspace is
+    allocated here unless one (uint8) is given."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, dim]")
+    T, hq, dim = q.shape
+    qs = _kv_rows(q, "q", hq, cache.dim)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_blocks]")
+    B, max_blocks = table.shape
+    if out is None:
+        out = torch.empty(T, hq, dim, dtype=torch.bfloat16, device=q.device)
+    else:
+        _dev_tensor(out, torch.bfloat16, "out")
+        if out.shape != q.shape:
+            raise ValueError(f"out must be {tuple(q.shape)}")
+    L = lib()
+    n = L.w4a16_kv_attention_workspace_bytes(B, T, hq, cache.heads, dim, max_new, max_len, window)
+    if workspace is None and n:
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        if stream is not None and stream != torch.cuda.current_stream():
+            workspace.record_stream(stream)
+    wp, wn = _ws_args(workspace)
+    rc = L.w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, _i32(table, "table"), _i32(cu, "cu", B + 1),
+                              _i32(lens, "lens", B), out.data_ptr(), B, T, hq, max_blocks, max_new, max_len, window,
+                              1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, _stream_ptr(stream))
+    _raise(rc)
+    return out
 
 
 def version() -> str:
