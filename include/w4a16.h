@@ -407,7 +407,10 @@ int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, 
  *
  * workspace: w4a16_kv_attention_workspace_bytes(...) bytes of device memory,
  * 256-byte aligned, no initial contents needed; calls that share one must
- * not overlap on the GPU. */
+ * not overlap on the GPU.  0 bytes: the arguments are invalid, or the step
+ * is too large for one call (row tiles x heads x 128-token tiles, or groups of
+ * 1024 tokens x T x q_heads, of max_len tokens, above 2^31); the call then
+ * returns W4A16_ERR_SHAPE. */
 #define W4A16_KV_MAX_GROUP 32 /* query heads per key/value head */
 
 size_t w4a16_kv_attention_workspace_bytes(int B, int T, int q_heads, int heads, int dim, int max_new, int max_len,

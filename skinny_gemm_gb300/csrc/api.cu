@@ -650,7 +650,10 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
       misaligned(lens, 4))
     return fail(W4A16_ERR_ALIGN, "q rows and out must be 16-byte, table, cu and lens 4-byte aligned");
   const size_t need = kv_attention_workspace(B, T, q_heads, cache->heads, cache->dim, max_new, max_len, window);
-  if (need > 0 && !workspace) return fail(W4A16_ERR_NULL, "w4a16_kv_attention needs a workspace of %zu bytes", need);
+  if (need == 0)
+    return fail(W4A16_ERR_SHAPE, "T = %d rows over max_len = %d tokens: too many for one call (2^31 tiles or group rows)",
+                T, max_len);
+  if (!workspace) return fail(W4A16_ERR_NULL, "w4a16_kv_attention needs a workspace of %zu bytes", need);
   if (misaligned(workspace, 256)) return fail(W4A16_ERR_ALIGN, "the workspace must be 256-byte aligned");
   if (workspace_bytes < need)
     return fail(W4A16_ERR_SHAPE, "a workspace of %zu bytes is too small (%zu)", workspace_bytes, need);

@@ -55,9 +55,11 @@ using namespace ptx;
 
 constexpr int kTile = 128;      // tokens per tile (the M of the MMAs)
 constexpr int kGroupTiles = 8;  // tiles per group
-constexpr int kChains = 8;      // interleaved chains over a row's groups
-constexpr int kThreads = 192;
+constexpr int kGroupTokens = kTile * kGroupTiles;
+constexpr int kChains = 32;     // interleaved chains over a row's groups
+constexpr int kRows = 8;        // query rows of a softmax warp group
 constexpr int kDescs = 4;       // tile descriptors in flight
+constexpr int kRing = 3;        // maxima and sums: a warp may write tile t + 1 while another still folds t - 1
 constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -78,19 +80,28 @@ struct Desc {
 };
 static_assert(sizeof(Desc) == 128, "two 64-byte halves");
 
+// RP rows of a row tile (query tokens x heads of a group), eight to a softmax
+// warp group, so that threads hold the same registers whatever RP.
+// CTAs per SM and K/V slots (128 tokens each): as many bytes in flight as the
+// shared memory holds, in as many CTAs as its queries, weights and registers
+// leave room for; more CTAs hide more of the chain S -> weights -> O.
 template <int D, int RP>
 struct Geo {
+  static constexpr int kGroups = RP / kRows;                   // softmax warp groups
+  static constexpr int kThreads = 128 * kGroups + 64;
   static constexpr int kPanels = D <= 128 ? 1 : D / 128;       // 128-byte column panels of K and V
-  static constexpr int kPanelBytes = D <= 128 ? kTile * D : kTile * 128;
+  static constexpr int kRowB = D <= 128 ? D : 128;             // bytes of a panel's row
+  static constexpr int kPanelBytes = kTile * kRowB;
   static constexpr int kSlot = kTile * D;
   static constexpr int kQ = kPanels * 2 * RP * 128;
   static constexpr int kP = kTile * 2 * RP;
-  // two CTAs an SM where three K/V tiles, the queries and two weight tiles fit in half of it
-  static constexpr int kCtas = D == 256 && RP > 8 ? 1 : 2;
-  static constexpr int kSlots = D == 256 ? (RP == 8 ? 3 : RP == 16 ? 6 : 5) : D == 128 ? (RP > 16 ? 5 : 6) : 8;
-  static constexpr int kBars = 2 * kSlots + 2 * kDescs + 2 * 2 + 2 + 2 + 1 + 1;
-  static constexpr int kRows = RP * 4 * (2 * 4 * 2 + 2 * 4 + 3);  // maxima, sums (two tiles x four warps), factors, limits
-  static constexpr int kSmem = kSlots * kSlot + kQ + 2 * kP + kDescs * (int)sizeof(Desc) + kRows + 8 * kBars + 16 + 1024;
+  static constexpr int kCtas = RP == 8 ? (D == 256 ? 2 : D == 128 ? 3 : 4) : RP == 16 ? (D == 256 ? 1 : 2) : 1;
+  static constexpr int kSlots = RP == 8 ? (D == 256 ? 3 : D == 128 ? 4 : 5)
+                                : RP == 16 ? (D == 256 ? 6 : D == 128 ? 5 : 8) : D == 256 ? 5 : D == 128 ? 10 : 12;
+  static constexpr int kBars = 2 * kSlots + 2 * kDescs + 6 + 4 + kGroups + 1;
+  // maxima and sums (kRing tiles x four warps), fold factors per warp, row factors and limits
+  static constexpr int kRowData = RP * 4 * (2 * 4 * kRing + 2 * 4 + 3);
+  static constexpr int kSmem = kSlots * kSlot + kQ + 2 * kP + kDescs * (int)sizeof(Desc) + kRowData + 8 * kBars + 16 + 1024;
   static constexpr uint32_t kTmem = RP == 8 ? 64 : RP == 16 ? 128 : 256;  // S twice, O once
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
@@ -110,11 +121,11 @@ struct Params {
   int gmax;        // group slots per row
   int grid;
   // workspace
-  int64_t* starts;  // [B + 1] tiles before each request
-  float* g_acc;     // [gmax][T][q_heads][D]
-  float2* g_ml;     // [gmax][T][q_heads]
-  float* t_acc;     // [grid][2 * kGroupTiles][RP][D]
-  float2* t_ml;     // [grid][2 * kGroupTiles][RP]
+  int* starts;   // [B + 1] tiles before each request
+  float* g_acc;  // [gmax][T][q_heads][D]
+  float2* g_ml;  // [gmax][T][q_heads]
+  float* t_acc;  // [grid][2 * kGroupTiles][RP][D]
+  float2* t_ml;  // [grid][2 * kGroupTiles][RP]
   int* flags;
 };
 
@@ -144,7 +155,9 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) {
   return r;
 }
 
-__device__ __forceinline__ int row_tiles(const Params& p, const Req& r) { return (r.fresh + p.TQ - 1) / p.TQ; }
+__device__ __forceinline__ int row_tiles(const Params& p, const Req& r) {
+  return r.fresh <= p.TQ ? (r.fresh > 0) : (r.fresh + p.TQ - 1) / p.TQ;
+}
 __device__ __forceinline__ int first_tile(const Params& p, const Req& r, int rt) {
   return p.window > 0 ? max(0, r.base + rt * p.TQ - p.window + 1) / kTile : 0;
 }
@@ -155,7 +168,7 @@ __device__ __forceinline__ int last_tile(const Params& p, const Req& r, int rt) 
 // sum over 0 <= i < n of floor((b + i a) / m), all >= 0: whole parts are
 // taken out, then the lattice points under the line are counted along the
 // other axis, as in Euclid's algorithm.
-__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+__device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t s = 0;
   while (n > 0) {
     s += n * (n - 1) / 2 * (a / m) + n * (b / m);
@@ -173,7 +186,7 @@ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) 
 }
 
 // Tiles of the row tiles before rt (of one key head).
-__device__ inline int64_t tiles_before(const Params& p, const Req& r, int rt) {
+__device__ inline int tiles_before(const Params& p, const Req& r, int rt) {
   const int n = row_tiles(p, r);
   if (rt <= 0) return 0;
   if (rt == 1) return last_tile(p, r, 0) - first_tile(p, r, 0) + 1;
@@ -184,23 +197,43 @@ __device__ inline int64_t tiles_before(const Params& p, const Req& r, int rt) {
     const int i0 = x >= 0 ? 0 : min(rt, (-x + p.TQ - 1) / p.TQ);
     s -= floor_sum(rt - i0, kTile, p.TQ, max(0, x + i0 * p.TQ));
   }
-  return s;
+  return (int)s;
 }
+
+// The cut of `total` tiles into grid ranges that differ by at most one tile.
+struct Cut {
+  int per, rem;
+  __device__ __forceinline__ Cut(int total, int grid) : per(total / grid), rem(total - per * grid) {}
+  __device__ __forceinline__ int begin(int c) const { return c * per + min(c, rem); }
+  __device__ __forceinline__ int owner(int x) const {
+    const int big = rem * (per + 1);
+    return x < big ? x / (per + 1) : rem + (x - big) / max(per, 1);
+  }
+};
 
 // ---- shared pieces -----------------------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
+__device__ __forceinline__ float ex2(float x) {  // 2^x; results below 2^-126 are 0
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// a, b as hi + lo / 16 (each two codes)
+// a, b as hi + lo / 16 (each two e4m3 codes, a in the low byte), in fp32: exact for bf16 values in range
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = e4m3x2(a, b);
-  const float2 h = from_e4m3x2(hi);
-  lo = e4m3x2(__fmul_rn(__fsub_rn(a, h.x), 16.f), __fmul_rn(__fsub_rn(b, h.y), 16.f));
+  hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+  lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(__fsub_rn(a, h.x), 16.f), __fmul_rn(__fsub_rn(b, h.y), 16.f)),
+                                __NV_SATFINITE, __NV_E4M3);
+}
+
+// The same for weights, two at a time in fp16: rounding to 11 bits first
+// (2^-11) on top of the two terms' 2^-9 stays below bf16's 2^-8.
+__device__ __forceinline__ void split2h(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 x = __floats2half2_rn(a, b);
+  hi = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)x, __NV_SATFINITE, __NV_E4M3);
+  const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3));
+  lo = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)__hmul2(__hsub2(x, h), __float2half2_rn(16.f)), __NV_SATFINITE, __NV_E4M3);
 }
 
 // One step of a fold: the running (m, l) takes in (mt, lt); al and be are
@@ -208,8 +241,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 // side (m = -inf) leaves the other as it is, bit for bit.
 __device__ __forceinline__ void fold_ml(float& m, float& l, float mt, float lt, float& al, float& be) {
   const float top = fmaxf(m, mt), ref = top == -INFINITY ? 0.f : top;
-  al = exp2f(m - ref);
-  be = exp2f(mt - ref);
+  al = ex2(m - ref);
+  be = ex2(mt - ref);
   l = __fmaf_rn(l, al, __fmul_rn(lt, be));
   m = top;
 }
@@ -220,46 +253,24 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// Barrier of the four softmax warps; returns whether any thread came with `fail`.
-__device__ __forceinline__ bool softmax_sync(bool fail) {
-  uint32_t any;
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
-      : "=r"(any)
-      : "r"((uint32_t)fail)
-      : "memory");
-  return any != 0;
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
-  static_assert(N % 8 == 0, "columns");
-#pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    float t[8];
-    tmem_ld8(addr + i, t);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[i + k] = t[k];
-  }
-}
-
 // ---- the kernel -----------------------------------------------------------------------------------
 
 template <int D, int RP>
-__global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
+__global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     kv_attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using X = Geo<D, RP>;
-  constexpr int NS = X::kSlots, NP = X::kPanels;
+  constexpr int NS = X::kSlots, NP = X::kPanels, NG = X::kGroups, R = kRows;
+  constexpr int W_LOAD = 4 * NG, W_MMA = 4 * NG + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_mem = base + NS * X::kSlot;
   uint8_t* p_mem = q_mem + X::kQ;
   Desc* descs = reinterpret_cast<Desc*>(p_mem + 2 * X::kP);
-  float* s_max = reinterpret_cast<float*>(descs + kDescs);  // [2][4][RP]
-  float* s_sum = s_max + 2 * 4 * RP;                        // [2][4][RP]
-  float2* s_ab = reinterpret_cast<float2*>(s_sum + 2 * 4 * RP);  // [4][RP]
-  float* s_qf = reinterpret_cast<float*>(s_ab + 4 * RP);    // [RP] score factor of a row
-  int2* s_lim = reinterpret_cast<int2*>(s_qf + RP);         // [RP] first and last token a row sees
+  float* s_max = reinterpret_cast<float*>(descs + kDescs);           // [kRing][4 warps][RP]
+  float* s_sum = s_max + kRing * 4 * RP;                             // [kRing][4 warps][RP]
+  float2* s_ab = reinterpret_cast<float2*>(s_sum + kRing * 4 * RP);  // [4 warps][RP]
+  float* s_qf = reinterpret_cast<float*>(s_ab + 4 * RP);             // [RP] score factor of a row
+  int2* s_lim = reinterpret_cast<int2*>(s_qf + RP);                  // [RP] first and last token a row sees
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(s_lim + RP);
   const uint32_t slots = smem_u32(base), q_s = smem_u32(q_mem), p_s = smem_u32(p_mem), bars = smem_u32(bar_mem);
   auto full = [&](int i) { return bars + 8u * i; };                   // slot: copies landed
@@ -270,9 +281,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
   auto s_free = [&](int i) { return bars + 8u * (2 * NS + 2 * kDescs + 2 + i); };
   auto p_full = [&](int i) { return bars + 8u * (2 * NS + 2 * kDescs + 4 + i); };
   const uint32_t o_full = bars + 8u * (2 * NS + 2 * kDescs + 6), o_free = o_full + 8, q_full = o_full + 16;
-  const uint32_t drained = o_full + 24;
+  const uint32_t drained = o_full + 24, all_sync = o_full + 32;  // all_sync: every softmax warp
+  auto grp_sync = [&](int g) { return o_full + 40 + 8u * g; };   // the four warps of a group
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_mem + X::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile int* s_nan = reinterpret_cast<volatile int*>(s_tmem + 2);  // [2] 1 + the last (even, odd) tile with NaN codes in partly seen tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -282,21 +295,24 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
     }
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(d_full(i), 33);
-      mbar_init(d_free(i), 5);
+      mbar_init(d_free(i), 4 * NG + 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
-      mbar_init(s_free(i), 4);
-      mbar_init(p_full(i), 4);
+      mbar_init(s_free(i), 4 * NG);
+      mbar_init(p_full(i), 4 * NG);
     }
     mbar_init(o_full, 1);
-    mbar_init(o_free, 4);
-    mbar_init(q_full, 4);
+    mbar_init(o_free, 4 * NG);
+    mbar_init(q_full, 4 * NG);
     mbar_init(drained, 1);
+    mbar_init(all_sync, 4 * NG);
+    for (int i = 0; i < NG; ++i) mbar_init(grp_sync(i), 4);
     *s_abort = 0;
+    s_nan[0] = s_nan[1] = 0;
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == W_MMA) {
     tmem_alloc(smem_u32(s_tmem), X::kTmem);
     tmem_relinquish();
   }
@@ -310,26 +326,25 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
     *s_abort = 1;
   };
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {  // all lanes; the same answer for all
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_parked(bar, parity)) && !*s_abort;
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity));
   };
   pdl_launch_dependents();
   pdl_wait();
   int loads = 0;  // producer: slots requested
 
-  if (warp == 4) {
+  if (warp == W_LOAD) {
     // ---- work list and copies ----
     const int nb = kTile >> p.shift, block = 1 << p.shift;  // blocks per tile
     bool bad = false;
-    int64_t total = 0;
+    int total = 0;
     Req mine{0, 0, 0};
-    int64_t mine_end = 0;  // inclusive prefix of this lane's request
+    int mine_end = 0;  // inclusive prefix of this lane's request
     auto scan = [&](int b0) {  // loads 32 requests; their inclusive prefix of tiles after `total`
       mine = load_req(p, b0 + lane, &bad);
-      int64_t n = mine.fresh > 0 ? tiles_before(p, mine, row_tiles(p, mine)) * p.heads : 0;
+      int n = mine.fresh > 0 ? tiles_before(p, mine, row_tiles(p, mine)) * p.heads : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, n, d);
+        const int o = __shfl_up_sync(0xffffffffu, n, d);
         if (lane >= d) n += o;
       }
       mine_end = total + n;
@@ -342,24 +357,22 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
     }
     if (blockIdx.x == 0 && lane == 0) p.starts[0] = 0;
     if (bad && blockIdx.x == 0) atomicOr(p.flags, W4A16_DEVICE_KV_RANGE);
-    const int64_t all = total;
-    const int64_t beg = all * blockIdx.x / p.grid, end = all * (blockIdx.x + 1) / p.grid;
+    const Cut cut(total, p.grid);
+    const int beg = cut.begin(blockIdx.x), end = cut.begin(blockIdx.x + 1);
     // the request of `beg`
+    total = 0;
+    b0 = 0;
     if (p.B > 32) {
-      total = 0;
-      for (b0 = 0; b0 < p.B; b0 += 32) {
+      for (; b0 < p.B; b0 += 32) {
         scan(b0);
-        const int64_t e = __shfl_sync(0xffffffffu, mine_end, 31);
+        const int e = __shfl_sync(0xffffffffu, mine_end, 31);
         if (e > beg) break;
         total = e;
       }
-    } else {
-      b0 = 0;
-      total = 0;
     }
     int b = 0, rt = 0, h = 0, tile = 0, t_first = 0, t_last = -1;
-    int64_t x = beg;   // position on the line
-    int64_t seg0 = 0;  // position of the segment's first tile
+    int x = beg;   // position on the line
+    int seg0 = 0;  // position of the segment's first tile
     Req r{0, 0, 0};
     auto take = [&](int bl) {  // request b0 + bl becomes the current one
       b = b0 + bl;
@@ -374,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
     if (beg < end) {
       const unsigned past = __ballot_sync(0xffffffffu, mine_end > beg);
       const int bl = __ffs(past) - 1;
-      const int64_t start = bl > 0 ? __shfl_sync(0xffffffffu, mine_end, bl > 0 ? bl - 1 : 0) : total;
+      const int before = __shfl_sync(0xffffffffu, mine_end, max(bl - 1, 0));
       take(bl);
-      int64_t off = beg - start;
+      int off = beg - (bl > 0 ? before : total);
       int lo = 0, hi = row_tiles(p, r);
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -387,30 +400,27 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
       if (rt > 0) off -= tiles_before(p, r, rt) * p.heads;
       enter();
       const int n = t_last - t_first + 1;
-      h = (int)(off / n);
-      tile = t_first + (int)(off % n);
+      h = off / n;
+      tile = t_first + off - h * n;
       seg0 = beg - (tile - t_first);
     }
-    // block id of lane l for a tile: -2 not needed, -1 (or any bad id) not in the cache
-    auto load_id = [&](int bb, const Req& rr, int row_tile, int tl) {
-      const int lo = p.window > 0 ? max(0, rr.base + row_tile * p.TQ - p.window + 1) : 0;
-      const int hi = rr.base + min((row_tile + 1) * p.TQ, rr.fresh) - 1;
-      const int j = tl * nb + lane;
+    // block id of this lane for a tile: -2 not needed, -1 (or any bad id) not in the cache
+    auto load_id = [&]() {
+      const int lo = p.window > 0 ? max(0, r.base + rt * p.TQ - p.window + 1) : 0;
+      const int hi = r.base + min((rt + 1) * p.TQ, r.fresh) - 1;
+      const int j = tile * nb + lane;
       if (lane >= nb || (j + 1) * block <= lo || j * block > hi) return -2;
-      return j < p.max_blocks ? p.table[(int64_t)bb * p.max_blocks + j] : -1;
+      return j < p.max_blocks ? p.table[(int64_t)b * p.max_blocks + j] : -1;
     };
-    int id = beg < end ? load_id(b, r, rt, tile) : -2;
+    int id = beg < end ? load_id() : -2;
     bool fresh_seg = true, ok = true;
     int t = 0;
     for (; x < end && ok; ++x, ++t) {
       // this tile's descriptor
-      const int ds = t % kDescs;
-      const int ch = h, crt = rt, ctile = tile;
-      const Req cr = r;
-      const int64_t g_lo = max(seg0, x - (ctile % kGroupTiles)), g_hi = min(seg0 + t_last - t_first, x - ctile % kGroupTiles + kGroupTiles - 1);
-      const bool whole = g_lo >= beg && g_hi < end;
+      const int ds = t % kDescs, ch = h;
+      const int g_lo = max(seg0, x - tile % kGroupTiles), g_hi = min(seg0 + t_last - t_first, x - tile % kGroupTiles + kGroupTiles - 1);
       int fl = fresh_seg ? kNewSeg : 0;
-      if (whole) fl |= (x == g_lo ? kGroupBegin : 0) | (x == g_hi ? kGroupEnd : 0);
+      if (g_lo >= beg && g_hi < end) fl |= (x == g_lo ? kGroupBegin : 0) | (x == g_hi ? kGroupEnd : 0);
       else fl |= kPart | (g_lo >= beg ? kTail : 0);
       const bool valid = id >= 0 && id < p.blocks;
       const unsigned need = __ballot_sync(0xffffffffu, id != -2), have = __ballot_sync(0xffffffffu, valid);
@@ -418,14 +428,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
       if (t >= kDescs && !(ok = wait_warp(d_free(ds), ((t / kDescs) - 1) & 1))) break;
       Desc& de = descs[ds];
       if (lane == 0) {
-        de.flags = fl;
-        de.h = ch;
-        de.j0 = crt * p.TQ;
-        de.tile = ctile;
-        de.base = cr.base;
-        de.fresh = cr.fresh;
-        de.c0 = cr.c0;
-        de.gi = ctile / kGroupTiles - first_tile(p, cr, 0) / kGroupTiles;
+        *reinterpret_cast<int4*>(&de.flags) = make_int4(fl, ch, rt * p.TQ, tile);
+        *reinterpret_cast<int4*>(&de.base) =
+            make_int4(r.base, r.fresh, r.c0, tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles);
         if (need != have) atomicOr(p.flags, W4A16_DEVICE_KV_RANGE);
       }
       if (lane < nb) {
@@ -442,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
       if (lane == 0) mbar_arrive(d_full(ds));
       // the next tile, its block ids requested before this one's slots are waited for
       const bool same = tile < t_last;
+      int next_id = -2;
       if (x + 1 < end) {
         if (same) {
           ++tile;
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
             if (++rt == row_tiles(p, r)) {
               rt = 0;
               int bl = b - b0;
-              for (;;) {  // the next request with new tokens (there is one: x + 1 < all)
+              for (;;) {  // the next request with new tokens (there is one: the line goes on)
                 const unsigned later = __ballot_sync(0xffffffffu, mine.fresh > 0 && lane > bl);
                 if (later) {
                   take(__ffs(later) - 1);
@@ -468,12 +474,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
           enter();
           tile = t_first;
         }
+        next_id = load_id();
       }
-      const int next_id = x + 1 < end ? load_id(b, r, rt, tile) : -2;
       // lane (block, panel): one copy each of K, then of V
       const int nv = __popc(have);
       const int src = lane / NP, panel = lane % NP;
-      const int nth = src < nv ? __fns(have, 0, src + 1) : 0;
+      const int nth = src < nv ? (have == (1u << nv) - 1 ? src : __fns(have, 0, src + 1)) : 0;
       const int my_id = __shfl_sync(0xffffffffu, id, nth & 31);
       const int row = (my_id * p.heads + ch) << p.shift;
 #pragma unroll
@@ -483,452 +489,431 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
         if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(nv * block * D));
         __syncwarp();
         if (lane < nv * NP)
-          tma_load_2d(slots + slot * X::kSlot + panel * X::kPanelBytes + nth * block * (D <= 128 ? D : 128),
-                      kv ? &maps.v : &maps.k, panel * 128, row, full(slot));
+          tma_load_2d(slots + slot * X::kSlot + panel * X::kPanelBytes + nth * block * X::kRowB, kv ? &maps.v : &maps.k,
+                      panel * 128, row, full(slot));
         ++loads;
       }
       id = next_id;
       fresh_seg = !same;
     }
-    if (!ok) {
-      if (lane == 0) give_up();
-    } else {  // the end mark
+    if (ok) {  // the end mark
       const int ds = t % kDescs;
-      if (t < kDescs || wait_warp(d_free(ds), ((t / kDescs) - 1) & 1)) {
+      ok = t < kDescs || wait_warp(d_free(ds), ((t / kDescs) - 1) & 1);
+      if (ok) {
         if (lane == 0) descs[ds].flags = kEnd;
         __syncwarp();
         cp_async_arrive(d_full(ds));
         if (lane == 0) mbar_arrive(d_full(ds));
-      } else if (lane == 0) {
-        give_up();
       }
     }
-  } else if (warp == 5) {
+    if (!ok && lane == 0) give_up();
+  } else if (warp == W_MMA) {
     // ---- MMA issue: S of tile t, then O of tile t - 1 ----
     if (lane == 0) {
       constexpr uint32_t id_s = umma_idesc_e4m3(128, 2 * RP, false, false);
       constexpr uint32_t id_o = umma_idesc_e4m3(128, 2 * RP, true, true);
       bool ok = true;
-      int seg = 0;
-      auto issue_o = [&](int t) {  // O = V^T P^T of tile t
-        const int slot = (2 * t + 1) % NS;
-        ok = mbar_wait_parked(p_full(t & 1), (t >> 1) & 1) && mbar_wait_parked(full(slot), ((2 * t + 1) / NS) & 1) &&
-             (t == 0 || mbar_wait_parked(o_free, (t - 1) & 1)) && !*s_abort;
-        if (!ok) return;
-        tc_fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < NP; ++c)
-#pragma unroll
-          for (int k = 0; k < kTile / 32; ++k) {
-            const uint32_t va = slots + slot * X::kSlot + c * X::kPanelBytes + k * 32 * (D < 128 ? D : 128);
-            // heads of 64: the MMA's rows 64 .. 127 repeat whatever lies 512 bytes on, and nobody reads them
-            const uint64_t ad = D < 128 ? umma_desc(va, 512, 512, 4) : umma_desc(va, 1024, 1024, 2);
-            const uint64_t bd = umma_desc(p_s + (t & 1) * X::kP + k * 512, 128, 2048, 0);
-            umma_f8(o_col + c * 2 * RP, ad, bd, id_o, k > 0);
-          }
-        umma_commit(o_full);
-        umma_commit(empty(slot));
-      };
-      int t = 0;
-      for (;; ++t) {
+      int seg = 0, t = 0;
+      bool more = true;
+      for (; ok && more; ++t) {
         const int ds = t % kDescs;
-        ok = mbar_wait_parked(d_full(ds), (t / kDescs) & 1) && !*s_abort;
+        ok = mbar_wait_parked(d_full(ds), (t / kDescs) & 1);
         if (!ok) break;
         const int fl = descs[ds].flags;
         mbar_arrive(d_free(ds));
-        if (fl & kEnd) break;
-        if (t > 0 && (fl & kNewSeg)) issue_o(t - 1);  // the queries of a new segment come after the old one's last O
-        if (!ok) break;
-        const int slot = (2 * t) % NS;
-        if (fl & kNewSeg) ok = mbar_wait_parked(q_full, seg++ & 1);
-        ok = ok && mbar_wait_parked(full(slot), ((2 * t) / NS) & 1) &&
-             (t < 2 || mbar_wait_parked(s_free(t & 1), ((t >> 1) - 1) & 1)) && !*s_abort;
-        if (!ok) break;
-        tc_fence_after_sync();
+        more = !(fl & kEnd);
+        if (more) {
+          const int slot = (2 * t) % NS;
+          if (fl & kNewSeg) ok = mbar_wait_parked(q_full, seg++ & 1);
+          ok = ok && mbar_wait_parked(full(slot), ((2 * t) / NS) & 1) &&
+               (t < 2 || mbar_wait_parked(s_free(t & 1), ((t >> 1) - 1) & 1));
+          if (!ok) break;
+          tc_fence_after_sync();
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const uint32_t ka = slots + slot * X::kSlot + (k / 4) * X::kPanelBytes + (k % 4) * 32;
-          const uint64_t ad = D < 128 ? umma_desc(ka, 16, 512, 4) : umma_desc(ka, 16, 1024, 2);
-          const uint64_t bd = umma_desc(q_s + (k / 4) * 2 * RP * 128 + (k % 4) * 32, 16, 1024, 2);
-          umma_f8(s_col + (t & 1) * 2 * RP, ad, bd, id_s, k > 0);
-        }
-        umma_commit(s_full(t & 1));
-        umma_commit(empty(slot));
-        if (t > 0 && !(fl & kNewSeg)) issue_o(t - 1);
-        if (!ok) break;
-      }
-      if (ok && t > 0) issue_o(t - 1);
-      if (!ok) give_up();
-    }
-  } else {
-    // ---- softmax and fold: thread = token of the tile, then = output column ----
-    const uint32_t lane_col = (uint32_t)(32 * warp) << 16;
-    float acc[NP][RP];
-#pragma unroll
-    for (int c = 0; c < NP; ++c)
-#pragma unroll
-      for (int i = 0; i < RP; ++i) acc[c][i] = 0.f;
-    float m_run = -INFINITY, l_run = 0.f;  // lane r of every warp: row r
-    bool fail = false;
-    // the tile whose O is not folded yet
-    struct {
-      int flags, h, j0, tile, fresh, c0, gi;
-    } prev = {kEnd, 0, 0, 0, 0, 0, 0};
-    uint32_t poison[NP];  // rows (bits) of that tile that see a NaN in this thread's column
-#pragma unroll
-    for (int c = 0; c < NP; ++c) poison[c] = 0;
-
-    // O of tile t: into the accumulators, or out to the workspace
-    auto fold = [&](int t) {
-      if (!wait_warp(o_full, t & 1)) fail = true;
-      if (softmax_sync(fail)) {  // (also: every warp's sums of the tile are written)
-        fail = true;
-        return;
-      }
-      tc_fence_after_sync();
-      const int par = t & 1;
-      float mt = -INFINITY, lt = 0.f;
-      if (lane < RP) {
-        const float* sm = s_max + par * 4 * RP + lane;
-        const float* sl = s_sum + par * 4 * RP + lane;
-        mt = fmaxf(fmaxf(sm[0], sm[RP]), fmaxf(sm[2 * RP], sm[3 * RP]));
-        lt = __fadd_rn(__fadd_rn(sl[0], sl[RP]), __fadd_rn(sl[2 * RP], sl[3 * RP]));
-      }
-      const bool part = prev.flags & kPart;
-      if (prev.flags & kGroupBegin) {
-        m_run = -INFINITY;
-        l_run = 0.f;
-#pragma unroll
-        for (int c = 0; c < NP; ++c)
-#pragma unroll
-          for (int i = 0; i < RP; ++i) acc[c][i] = 0.f;
-      }
-      if (!part) {
-        float al, be;
-        fold_ml(m_run, l_run, mt, lt, al, be);
-        if (lane < RP) s_ab[warp * RP + lane] = make_float2(al, be);
-        __syncwarp();
-      }
-      const int rows = min(p.TQ, prev.fresh - prev.j0) * p.G;
-      const int part_slot = blockIdx.x * 2 * kGroupTiles + (prev.flags & kTail ? kGroupTiles : 0) + prev.tile % kGroupTiles;
-#pragma unroll
-      for (int c = 0; c < NP; ++c) {
-#pragma unroll
-        for (int i0 = 0; i0 < RP; i0 += 8) {
-          float hi[8], lo[8];
-          tmem_ld8(o_col + c * 2 * RP + i0 + lane_col, hi);
-          tmem_ld8(o_col + c * 2 * RP + RP + i0 + lane_col, lo);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            // weights were 256 p = hi + lo / 16
-            float o = __fmul_rn(__fmaf_rn(lo[i], 0.0625f, hi[i]), 0.00390625f);
-            if ((poison[c] >> (i0 + i)) & 1) o = __uint_as_float(0x7FC00000u);
-            if (part) {
-              const int d = c * 128 + 32 * warp + lane;
-              if (i0 + i < rows && (D >= 128 || d < D))
-                p.t_acc[((int64_t)part_slot * RP + i0 + i) * D + d] = o;
-            } else {
-              const float2 ab = s_ab[warp * RP + i0 + i];
-              acc[c][i0 + i] = __fmaf_rn(acc[c][i0 + i], ab.x, __fmul_rn(o, ab.y));
-            }
+          for (int k = 0; k < D / 32; ++k) {
+            const uint32_t ka = slots + slot * X::kSlot + (k / 4) * X::kPanelBytes + (k % 4) * 32;
+            const uint64_t ad = D < 128 ? umma_desc(ka, 16, 512, 4) : umma_desc(ka, 16, 1024, 2);
+            const uint64_t bd = umma_desc(q_s + (k / 4) * 2 * RP * 128 + (k % 4) * 32, 16, 1024, 2);
+            umma_f8(s_col + (t & 1) * 2 * RP, ad, bd, id_s, k > 0);
           }
+          umma_commit(s_full(t & 1));
+          umma_commit(empty(slot));
         }
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
-      if (part) {
-        if (warp == 0 && lane < rows) p.t_ml[(int64_t)part_slot * RP + lane] = make_float2(mt, lt);
-      } else if (prev.flags & kGroupEnd) {
-        const int64_t row0 = ((int64_t)prev.gi * p.T + prev.c0 + prev.j0) * p.q_heads + prev.h * p.G;
-        int j = 0, g = 0;
-#pragma unroll
-        for (int i = 0; i < RP; ++i) {
-          if (i < rows) {
-            const int64_t row = row0 + (int64_t)j * p.q_heads + g;
-#pragma unroll
-            for (int c = 0; c < NP; ++c) {
-              const int d = c * 128 + 32 * warp + lane;
-              if (D >= 128 || d < D) p.g_acc[row * D + d] = acc[c][i];
-            }
-          }
-          if (++g == p.G) {
-            g = 0;
-            ++j;
-          }
-        }
-        if (warp == 0 && lane < rows)
-          p.g_ml[row0 + (int64_t)(lane / p.G) * p.q_heads + lane % p.G] = make_float2(m_run, l_run);
-      }
-    };
-
-    int t = 0;
-    for (;; ++t) {
-      const int ds = t % kDescs, par = t & 1;
-      if (!wait_warp(d_full(ds), (t / kDescs) & 1)) fail = true;
-      if (softmax_sync(fail)) {
-        fail = true;
-        break;
-      }
-      const Desc& de = descs[ds];
-      const int fl = de.flags;
-      if (fl & kEnd) break;
-      const int base_tok = de.base, j0 = de.j0, fresh = de.fresh, c0 = de.c0, h = de.h, tile = de.tile, gi = de.gi;
-      const int toks = min(p.TQ, fresh - j0);
-      if (fl & kNewSeg) {
-        if (t > 0) {
-          fold(t - 1);
-          if (fail) break;
-        }
-        // query rows as e4m3 terms: 128 / RP threads a row
-        constexpr int TPR = 128 / RP, CPT = (D / 8 + TPR - 1) / TPR;
-        const int r = tid / TPR, c = tid % TPR;
-        const int j = r / p.G, g = r - j * p.G;
-        const bool live = j < toks;
-        uint4 v[CPT];
-        uint32_t peak = 0;
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-          v[i] = make_uint4(0, 0, 0, 0);
-          const int ch = c + i * TPR;
-          if (live && ch < D / 8)
-            v[i] = ld_nc_v4(p.q + (int64_t)(c0 + j0 + j) * p.q_stride + (int64_t)(h * p.G + g) * D + 8 * ch);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t u = word_of(v[i], w) & 0x7FFF7FFFu;
-            peak = max(peak, max(u & 0xFFFF, u >> 16));
-          }
-        }
-#pragma unroll
-        for (int d = TPR / 2; d; d >>= 1) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, d));
-        // largest element into (224, 448]: 448 = 1.75 * 2^8
-        const int e = min(max((int)(peak >> 7) - 127 - 8 + ((peak & 127) > 96 ? 1 : 0), -120), 120);
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-          const int ch = c + i * TPR;
-          if (ch < D / 8) {
-            float f[8];
-            widen8(v[i], f);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) split2(__fmul_rn(f[2 * w], inv), __fmul_rn(f[2 * w + 1], inv), hi[w], lo[w]);
-            // K-major, 128-byte swizzle: row n of panel ch / 16
-            auto at = [&](int n) {
-              return q_mem + (ch / 16) * 2 * RP * 128 + n * 128 + ((((ch % 16) >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8;
-            };
-            *reinterpret_cast<uint2*>(at(r)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(at(RP + r)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-          }
-        }
-        if (c == 0) {
-          const float unit = __uint_as_float((uint32_t)(127 + e) << 23);
-          // a row with a NaN or an infinity is NaN as a whole
-          s_qf[r] = peak >= 0x7F80 ? __uint_as_float(0x7FC00000u) : __fmul_rn(unit, p.qk_scale);
-          const int pos = base_tok + j0 + j;
-          s_lim[r] = live ? make_int2(p.window > 0 ? pos - p.window + 1 : 0, pos) : make_int2(0, -1);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-        if (softmax_sync(false)) {
-          fail = true;
-          break;
-        }
-      }
-      // token of this thread
-      const int tok = tile * kTile + tid;
-      const int blk = tid >> p.shift;
-      const float ks = de.ks[blk], vs = de.vs[blk];
-      const int pos0 = base_tok + j0, pos1 = pos0 + toks - 1;  // positions of the first and last row
-      const bool masked = tile * kTile + kTile - 1 > pos0 || (p.window > 0 && tile * kTile < pos1 - p.window + 1);
-      const bool fix = masked || (fl & kBadBlock);
-      const bool dead = ks == 0.f || tok > pos1 || (p.window > 0 && tok < pos0 - p.window + 1);
-      const float lv = dead ? 0.f : log2f(vs), iv = dead ? 0.f : __frcp_rn(vs);
-      if (!wait_warp(s_full(par), (t >> 1) & 1)) fail = true;
-      tc_fence_after_sync();
-      float s[RP];
-      {
-        float lo[RP];
-        tmem_ld<RP>(s_col + par * 2 * RP + lane_col, s);
-        tmem_ld<RP>(s_col + par * 2 * RP + RP + lane_col, lo);
-        tmem_wait_ld();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free(par));
-#pragma unroll
-        for (int i = 0; i < RP; ++i)
-          s[i] = __fmaf_rn(__fmul_rn(__fmaf_rn(lo[i], 0.0625f, s[i]), s_qf[i]), ks, lv);
-      }
-      if (fix) {
-#pragma unroll
-        for (int i = 0; i < RP; ++i) {
-          const int2 lim = s_lim[i];
-          if (dead || tok < lim.x || tok > lim.y) s[i] = -INFINITY;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < RP; ++i) {
-        const float m = warp_max(s[i]);
-        if (lane == i) s_max[(par * 4 + warp) * RP + i] = m;
-      }
-      // V rows that no row sees (stale shared memory, unset blocks) become
-      // zeros; NaN codes that only some rows see are taken out of V and put
-      // into those rows' results
-      bool nan_code = false;
-      uint8_t* v_row = base + ((2 * t + 1) % NS) * X::kSlot;
-      const bool partly = masked && !dead && (tok > pos0 || (p.window > 0 && tok < pos1 - p.window + 1));
-      constexpr int kRowB = D < 128 ? D : 128, kCh = kRowB / 16;
-      if (fix) {
-        if (!wait_warp(full((2 * t + 1) % NS), ((2 * t + 1) / NS) & 1)) fail = true;
-        if (dead || partly) {
+        if (t > 0) {  // O = V^T P^T of tile t - 1
+          const int u = t - 1, slot = (2 * u + 1) % NS;
+          ok = mbar_wait_parked(p_full(u & 1), (u >> 1) & 1) && mbar_wait_parked(full(slot), ((2 * u + 1) / NS) & 1) &&
+               (u == 0 || mbar_wait_parked(o_free, (u - 1) & 1));
+          if (!ok) break;
+          tc_fence_after_sync();
 #pragma unroll
           for (int c = 0; c < NP; ++c)
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) {
-              uint4* w = reinterpret_cast<uint4*>(v_row + c * X::kPanelBytes + tid * kRowB + ((i + tid) % kCh) * 16);
-              if (dead) {
-                *w = make_uint4(0, 0, 0, 0);
-              } else {
-                const uint4 u = *w;
-                const uint32_t any = (((u.x & 0x7F7F7F7Fu) + 0x01010101u) | ((u.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                                      ((u.z & 0x7F7F7F7Fu) + 0x01010101u) | ((u.w & 0x7F7F7F7Fu) + 0x01010101u)) &
-                                     0x80808080u;
-                nan_code |= any != 0;
-              }
+            for (int k = 0; k < kTile / 32; ++k) {
+              const uint32_t va = slots + slot * X::kSlot + c * X::kPanelBytes + k * 32 * X::kRowB;
+              // heads of 64: the MMA's rows 64 .. 127 repeat whatever lies 512 bytes on, and nobody reads them
+              const uint64_t ad = D < 128 ? umma_desc(va, 512, 512, 4) : umma_desc(va, 1024, 1024, 2);
+              const uint64_t bd = umma_desc(p_s + (u & 1) * X::kP + k * 512, 128, 2048, 0);
+              umma_f8(o_col + c * 2 * RP, ad, bd, id_o, k > 0);
             }
+          umma_commit(o_full);
+          umma_commit(empty(slot));
         }
       }
-      if (softmax_sync(fail)) {
-        fail = true;
-        break;
-      }
-      uint32_t taint[NP];
+      if (!ok) give_up();
+    }
+  } else {
+    // ---- softmax and fold: thread = token of the tile, then = output column; rows R grp .. R grp + R - 1 ----
+    const int grp = warp >> 2, w4 = warp & 3, tt = tid & 127;
+    const uint32_t lane_col = ((uint32_t)(32 * w4) << 16) + 16 * grp;  // this group's columns: 8 first terms, 8 second
+    float acc[NP][R];
 #pragma unroll
-      for (int c = 0; c < NP; ++c) taint[c] = 0;
-      if (masked && toks > 1) {
-        if (softmax_sync(nan_code)) {
-          // (rare) this thread's columns: which tokens hold NaN, which rows see one
+    for (int c = 0; c < NP; ++c)
 #pragma unroll
-          for (int c = 0; c < NP; ++c) {
-            uint32_t hit[4] = {0, 0, 0, 0};
-            if (tid < kRowB)
-              for (int k = 0; k < kTile; ++k) {
-                const int sw = D < 128 ? (k >> 1) & 3 : k & 7;
-                const uint8_t code = v_row[c * X::kPanelBytes + k * kRowB + (((tid >> 4) ^ sw) << 4) + (tid & 15)];
-                if ((code & 0x7F) == 0x7F) hit[k >> 5] |= 1u << (k & 31);
-              }
-            for (int i = 0; i < RP; ++i) {
-              const int lo = s_lim[i].x - tile * kTile, hi = s_lim[i].y - tile * kTile;
-              bool sees = false;
-              for (int k = 0; k < kTile; ++k) sees |= k >= lo && k <= hi && ((hit[k >> 5] >> (k & 31)) & 1);
-              if (sees) taint[c] |= 1u << i;
+      for (int i = 0; i < R; ++i) acc[c][i] = 0.f;
+    float m_run = -INFINITY, l_run = 0.f;  // lane i (< R) of every warp: row i of the group
+    uint32_t poison = 0;  // bit c R + i: row i of the last tile sees a NaN in column c of this thread
+    int4 pd = make_int4(0, 0, 0, 0), pe = pd;  // the last tile's descriptor
+    uint32_t n_grp = 0, n_all = 0;             // barrier phases
+    bool ok = true;
+    auto sync_group = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(grp_sync(grp));
+      ok &= wait_warp(grp_sync(grp), n_grp++ & 1);
+    };
+    auto sync_all = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(all_sync);
+      ok &= wait_warp(all_sync, n_all++ & 1);
+    };
+
+    for (int t = 0;; ++t) {
+      const int ds = t % kDescs, par = t & 1;
+      if (!(ok = wait_warp(d_full(ds), (t / kDescs) & 1))) break;
+      const Desc& de = descs[ds];
+      const int4 dd = *reinterpret_cast<const int4*>(&de.flags), dx = *reinterpret_cast<const int4*>(&de.base);
+      const int fl = dd.x;
+      uint32_t taint = 0;
+      if (!(fl & kEnd)) {
+        const int h = dd.y, j0 = dd.z, tile = dd.w, base_tok = dx.x, fresh = dx.y, c0 = dx.z;
+        const int toks = min(p.TQ, fresh - j0);
+        if (fl & kNewSeg) {
+          sync_all();  // nobody looks at the last segment's limits and factors any more
+          if (!ok) break;
+          // query rows as e4m3 terms: 16 threads a row
+          constexpr int CPT = (D / 8 + 15) / 16;
+          const int r = tid / 16, c = tid % 16;
+          const int j = r / p.G, g = r - j * p.G;
+          const bool live = j < toks;
+          uint4 v[CPT];
+          uint32_t peak = 0;
+#pragma unroll
+          for (int i = 0; i < CPT; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            const int ch = c + i * 16;
+            if (live && ch < D / 8)
+              v[i] = ld_nc_v4(p.q + (int64_t)(c0 + j0 + j) * p.q_stride + (int64_t)(h * p.G + g) * D + 8 * ch);
+          }
+#pragma unroll
+          for (int i = 0; i < CPT; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t u = word_of(v[i], w) & 0x7FFF7FFFu;
+              peak = max(peak, max(u & 0xFFFF, u >> 16));
+            }
+#pragma unroll
+          for (int d = 8; d; d >>= 1) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, d));
+          // largest element into (224, 448]: 448 = 1.75 * 2^8
+          const int e = min(max((int)(peak >> 7) - 127 - 8 + ((peak & 127) > 96 ? 1 : 0), -120), 120);
+          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < CPT; ++i) {
+            const int ch = c + i * 16;
+            if (ch < D / 8) {
+              float f[8];
+              widen8(v[i], f);
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int w = 0; w < 4; ++w) split2(__fmul_rn(f[2 * w], inv), __fmul_rn(f[2 * w + 1], inv), hi[w], lo[w]);
+              // K-major, 128-byte swizzle: row n = 16 (r / 8) + r % 8 (second terms 8 further) of panel ch / 16
+              const int n = (r / R) * 16 + r % R;
+              uint8_t* at = q_mem + (ch / 16) * 2 * RP * 128 + n * 128 + ((((ch % 16) >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8;
+              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+              *reinterpret_cast<uint2*>(at + 8 * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             }
           }
-          softmax_sync(false);
-          if (nan_code) {
-#pragma unroll 1
+          if (c == 0) {
+            const float unit = __uint_as_float((uint32_t)(127 + e) << 23);
+            // a row with a NaN or an infinity is NaN as a whole
+            s_qf[r] = peak >= 0x7F80 ? __uint_as_float(0x7FC00000u) : __fmul_rn(unit, p.qk_scale);
+            const int pos = base_tok + j0 + j;
+            s_lim[r] = live ? make_int2(p.window > 0 ? pos - p.window + 1 : 0, pos) : make_int2(0, -1);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+          sync_all();
+          if (!ok) break;
+        }
+        // token of this thread
+        const int tok = tile * kTile + tt, blk = tt >> p.shift;
+        const float ks = de.ks[blk];
+        const int pos0 = base_tok + j0, pos1 = pos0 + toks - 1;  // positions of the first and last row
+        const bool masked = tile * kTile + kTile - 1 > pos0 || (p.window > 0 && tile * kTile < pos1 - p.window + 1);
+        const bool fix = masked || (fl & kBadBlock);
+        const bool dead = ks == 0.f || tok > pos1 || (p.window > 0 && tok < pos0 - p.window + 1);
+        // the V scale is a power of two: its exponent, and its reciprocal
+        const int ve = dead ? 0 : (int)(__float_as_uint(de.vs[blk]) >> 23) - 127;
+        const float lv = (float)ve, iv = __uint_as_float((uint32_t)(127 - ve) << 23);
+        ok = wait_warp(s_full(par), (t >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after_sync();
+        float s[R];
+        {
+          float raw[16];
+          tmem_ld16(s_col + par * 2 * RP + lane_col, raw);
+          tmem_wait_ld();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free(par));
+#pragma unroll
+          for (int i = 0; i < R; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(s_qf + R * grp + i);
+            const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              s[i + k] = __fmaf_rn(__fmul_rn(__fmaf_rn(raw[R + i + k], 0.0625f, raw[i + k]), ff[k]), ks, lv);
+          }
+        }
+        if (fix) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const int2 lim = s_lim[R * grp + i];
+            if (dead || tok < lim.x || tok > lim.y) s[i] = -INFINITY;
+          }
+        }
+        float* sm = s_max + (t % kRing) * 4 * RP + R * grp;
+        {
+          float m[R];
+#pragma unroll
+          for (int i = 0; i < R; ++i) m[i] = warp_max(s[i]);
+          if (lane == 0) {
+            *reinterpret_cast<float4*>(sm + w4 * RP) = make_float4(m[0], m[1], m[2], m[3]);
+            *reinterpret_cast<float4*>(sm + w4 * RP + 4) = make_float4(m[4], m[5], m[6], m[7]);
+          }
+        }
+        if (fix) {
+          // V rows that no row sees (stale shared memory, unset blocks) become
+          // zeros; NaN codes that only some rows see are taken out of V and
+          // put into those rows' results
+          uint8_t* v_row = base + ((2 * t + 1) % NS) * X::kSlot;
+          constexpr int kRowB = X::kRowB, kCh = kRowB / 16;
+          ok = wait_warp(full((2 * t + 1) % NS), ((2 * t + 1) / NS) & 1);
+          if (!ok) break;
+          bool nan_code = false;
+          const bool partly = toks > 1 && !dead && (tok > pos0 || (p.window > 0 && tok < pos1 - p.window + 1));
+          if (grp == 0 && (dead || partly)) {
+#pragma unroll
             for (int c = 0; c < NP; ++c)
-              for (int i = 0; i < kRowB; ++i) {
-                uint8_t& code = v_row[c * X::kPanelBytes + tid * kRowB + i];
-                if ((code & 0x7F) == 0x7F) code = 0;
+#pragma unroll
+              for (int i = 0; i < kCh; ++i) {
+                uint4* w = reinterpret_cast<uint4*>(v_row + c * X::kPanelBytes + tt * kRowB + ((i + tt) % kCh) * 16);
+                if (dead) {
+                  *w = make_uint4(0, 0, 0, 0);
+                } else {
+                  const uint4 u = *w;
+                  const uint32_t any = (((u.x & 0x7F7F7F7Fu) + 0x01010101u) | ((u.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                                        ((u.z & 0x7F7F7F7Fu) + 0x01010101u) | ((u.w & 0x7F7F7F7Fu) + 0x01010101u)) &
+                                       0x80808080u;
+                  nan_code |= any != 0;
+                }
               }
           }
+          if (masked && toks > 1) {
+            if (nan_code) s_nan[par] = t + 1;
+            sync_all();
+            if (!ok) break;
+            if (s_nan[par] == t + 1) {
+              // (rare) which tokens hold NaN in this thread's columns, which rows see one
+#pragma unroll 1
+              for (int c = 0; c < NP; ++c) {
+                uint32_t hit[4] = {0, 0, 0, 0};
+                if (tt < kRowB)
+                  for (int k = 0; k < kTile; ++k) {
+                    const int sw = D < 128 ? (k >> 1) & 3 : k & 7;
+                    const uint8_t code = v_row[c * X::kPanelBytes + k * kRowB + (((tt >> 4) ^ sw) << 4) + (tt & 15)];
+                    if ((code & 0x7F) == 0x7F) hit[k >> 5] |= 1u << (k & 31);
+                  }
+                for (int i = 0; i < R; ++i) {
+                  const int2 lim = s_lim[R * grp + i];
+                  bool sees = false;
+                  for (int k = max(0, lim.x - tile * kTile); k < kTile && k <= lim.y - tile * kTile; ++k)
+                    sees |= (hit[k >> 5] >> (k & 31)) & 1;
+                  if (sees) taint |= 1u << (c * R + i);
+                }
+              }
+              sync_all();
+              if (!ok) break;
+              if (nan_code) {
+#pragma unroll 1
+                for (int c = 0; c < NP; ++c)
+                  for (int i = 0; i < kRowB; ++i) {
+                    uint8_t& code = v_row[c * X::kPanelBytes + tt * kRowB + i];
+                    if ((code & 0x7F) == 0x7F) code = 0;
+                  }
+              }
+            }
+          }
         }
-      }
-      // weights, their sums, and their two terms
-      uint32_t hi[RP / 2], lo[RP / 2];
+        sync_group();
+        if (!ok) break;
+        // weights times 256 (sums and O carry the factor, their quotient does not), and their two terms
+        uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
-      for (int i = 0; i < RP; i += 4) {
-        const float* sm = s_max + par * 4 * RP + i;
-        float4 mx = *reinterpret_cast<const float4*>(sm);
+        for (int i = 0; i < R; i += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(sm + i), b = *reinterpret_cast<const float4*>(sm + RP + i);
+          const float4 c = *reinterpret_cast<const float4*>(sm + 2 * RP + i), d = *reinterpret_cast<const float4*>(sm + 3 * RP + i);
+          const float mx[4] = {fmaxf(fmaxf(a.x, b.x), fmaxf(c.x, d.x)), fmaxf(fmaxf(a.y, b.y), fmaxf(c.y, d.y)),
+                               fmaxf(fmaxf(a.z, b.z), fmaxf(c.z, d.z)), fmaxf(fmaxf(a.w, b.w), fmaxf(c.w, d.w))};
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
-          const float4 o = *reinterpret_cast<const float4*>(sm + w * RP);
-          mx.x = fmaxf(mx.x, o.x);
-          mx.y = fmaxf(mx.y, o.y);
-          mx.z = fmaxf(mx.z, o.z);
-          mx.w = fmaxf(mx.w, o.w);
+          for (int k = 0; k < 4; ++k) s[i + k] = ex2(s[i + k] - (mx[k] == -INFINITY ? 0.f : mx[k] - 8.f));
         }
-        s[i + 0] = exp2f(s[i + 0] - (mx.x == -INFINITY ? 0.f : mx.x));
-        s[i + 1] = exp2f(s[i + 1] - (mx.y == -INFINITY ? 0.f : mx.y));
-        s[i + 2] = exp2f(s[i + 2] - (mx.z == -INFINITY ? 0.f : mx.z));
-        s[i + 3] = exp2f(s[i + 3] - (mx.w == -INFINITY ? 0.f : mx.w));
-      }
 #pragma unroll
-      for (int i = 0; i < RP; i += 2)
-        split2(__fmul_rn(s[i], 256.f), __fmul_rn(s[i + 1], 256.f), hi[i / 2], lo[i / 2]);
-      {
-        // row n of the weights: n % 16 within 16-byte rows of tokens, n / 16 2048 bytes apart; hi rows, then lo
-        uint32_t w[RP / 2];
+        for (int i = 0; i < R; i += 2) split2h(s[i], s[i + 1], hi[i / 2], lo[i / 2]);
+        // row 16 grp + (0 .. 7 first terms, 8 .. 15 second) of the weights: 16 bytes a token
+        *reinterpret_cast<uint4*>(p_mem + par * X::kP + grp * 2048 + tt * 16) =
+            make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        fence_proxy_async();
+        // row sums of p / vs over the warp: halves exchanged, lane 4 i ends with row i's
 #pragma unroll
-        for (int i = 0; i < RP / 4; ++i) {
-          w[i] = hi[2 * i] | hi[2 * i + 1] << 16;
-          w[RP / 4 + i] = lo[2 * i] | lo[2 * i + 1] << 16;
-        }
-        uint8_t* dst = p_mem + par * X::kP + tid * 16;
+        for (int i = 0; i < R; ++i) s[i] = __fmul_rn(s[i], iv);
 #pragma unroll
-        for (int i = 0; i < RP / 8; ++i)
-          *reinterpret_cast<uint4*>(dst + i * 2048) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      }
-      fence_proxy_async();
-      // row sums of p / vs over the warp: halves exchanged, so that lane r ends with row r's (the same tree for every RP)
-#pragma unroll
-      for (int i = 0; i < RP; ++i) s[i] = __fmul_rn(s[i], iv);
-      {
-        int off = 16;
-#pragma unroll
-        for (int n = RP; n > 1; n >>= 1, off >>= 1) {
+        for (int n = R / 2, off = 16; n; n >>= 1, off >>= 1) {
           const bool up = lane & off;
 #pragma unroll
-          for (int i = 0; i < n / 2; ++i) {
-            const float give = up ? s[i] : s[i + n / 2], keep = up ? s[i + n / 2] : s[i];
+          for (int i = 0; i < n; ++i) {
+            const float give = up ? s[i] : s[i + n], keep = up ? s[i + n] : s[i];
             s[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, off));
           }
         }
+        s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], 2));
+        s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], 1));
+        if (lane % 4 == 0) s_sum[((t % kRing) * 4 + w4) * RP + R * grp + lane / 4] = s[0];
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(p_full(par));
+          mbar_arrive(d_free(ds));
+        }
+      } else if (t > 0) {
+        sync_group();  // the last tile's sums are written
+        if (!ok) break;
+      }
+
+      if (t > 0) {
+        // ---- O of tile t - 1: into the accumulators, or out to the workspace ----
+        const int pf = pd.x, u = t - 1;
+        float mt = -INFINITY, lt = 0.f;
+        if (lane < R) {
+          const float* a = s_max + (u % kRing) * 4 * RP + R * grp + lane;
+          const float* b = s_sum + (u % kRing) * 4 * RP + R * grp + lane;
+          mt = fmaxf(fmaxf(a[0], a[RP]), fmaxf(a[2 * RP], a[3 * RP]));
+          lt = __fadd_rn(__fadd_rn(b[0], b[RP]), __fadd_rn(b[2 * RP], b[3 * RP]));
+        }
+        const bool part = pf & kPart;
+        if (pf & kGroupBegin) {
+          m_run = -INFINITY;
+          l_run = 0.f;
 #pragma unroll
-        for (; off; off >>= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], off));
-        constexpr int kRep = 32 / RP;  // lanes with the same row
-        if (lane % kRep == 0) s_sum[(par * 4 + warp) * RP + lane / kRep] = s[0];
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(p_full(par));
-        mbar_arrive(d_free(ds));
-      }
-      if (t > 0 && !(fl & kNewSeg)) {
-        fold(t - 1);
-        if (fail) break;
-      }
-      prev.flags = fl;
-      prev.h = h;
-      prev.j0 = j0;
-      prev.tile = tile;
-      prev.fresh = fresh;
-      prev.c0 = c0;
-      prev.gi = gi;
+          for (int c = 0; c < NP; ++c)
 #pragma unroll
-      for (int c = 0; c < NP; ++c) poison[c] = taint[c];
+            for (int i = 0; i < R; ++i) acc[c][i] = 0.f;
+        }
+        if (!part) {
+          float al, be;
+          fold_ml(m_run, l_run, mt, lt, al, be);
+          if (lane < R) s_ab[w4 * RP + R * grp + lane] = make_float2(al, be);
+          __syncwarp();
+        }
+        const int rows = min(p.TQ, pe.y - pd.z) * p.G - R * grp;  // of this group
+        ok = wait_warp(o_full, u & 1);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const int part_slot = (blockIdx.x * 2 + (pf & kTail ? 1 : 0)) * kGroupTiles + pd.w % kGroupTiles;
+#pragma unroll
+        for (int c = 0; c < NP; ++c) {
+          float raw[16];
+          tmem_ld16(o_col + c * 2 * RP + lane_col, raw);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < R; ++i) raw[i] = __fmaf_rn(raw[R + i], 0.0625f, raw[i]);
+          if (poison) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+              if ((poison >> (c * R + i)) & 1) raw[i] = __uint_as_float(0x7FC00000u);
+          }
+          if (part) {
+            float* dst = p.t_acc + ((int64_t)part_slot * RP + R * grp) * D + c * 128 + tt;
+            if (D >= 128 || tt < D) {
+#pragma unroll
+              for (int i = 0; i < R; ++i)
+                if (i < rows) dst[i * D] = raw[i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < R; i += 2) {
+              const float4 ab = *reinterpret_cast<const float4*>(s_ab + w4 * RP + R * grp + i);
+              acc[c][i] = __fmaf_rn(acc[c][i], ab.x, __fmul_rn(raw[i], ab.y));
+              acc[c][i + 1] = __fmaf_rn(acc[c][i + 1], ab.z, __fmul_rn(raw[i + 1], ab.w));
+            }
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+        if (part) {
+          if (w4 == 0 && lane < R && lane < rows) p.t_ml[(int64_t)part_slot * RP + R * grp + lane] = make_float2(mt, lt);
+        } else if (pf & kGroupEnd) {
+          const int64_t row0 = ((int64_t)pe.w * p.T + pe.z + pd.z) * p.q_heads + pd.y * p.G;
+          int j = R * grp / p.G, g = R * grp - j * p.G;
+          const int jl = (R * grp + lane) / p.G, gl = R * grp + lane - jl * p.G;
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            if (i < rows && (D >= 128 || tt < D)) {
+              float* dst = p.g_acc + (row0 + (int64_t)j * p.q_heads + g) * D + tt;
+#pragma unroll
+              for (int c = 0; c < NP; ++c) dst[c * 128] = acc[c][i];
+            }
+            if (++g == p.G) {
+              g = 0;
+              ++j;
+            }
+          }
+          if (w4 == 0 && lane < R && lane < rows) p.g_ml[row0 + (int64_t)jl * p.q_heads + gl] = make_float2(m_run, l_run);
+        }
+      }
+      if (fl & kEnd) break;
+      pd = dd;
+      pe = dx;
+      poison = taint;
     }
-    if (!fail && t > 0) fold(t - 1);
-    if (fail && lane == 0) give_up();
+    if (!ok && lane == 0) give_up();
   }
 
   // ---- teardown: copies and MMAs in flight land before memory is released ----
   __syncthreads();
   if (*s_abort) {
-    if (warp == 4) asm volatile("cp.async.wait_all;" ::: "memory");
-    if (warp == 4 && lane == 0)
-      for (int i = max(0, loads - NS); i < loads; ++i) mbar_wait_parked(full(i % NS), (i / NS) & 1);
-    if (warp == 5 && lane == 0) {  // one more commit covers every MMA issued
+    if (warp == W_LOAD) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0)
+        for (int i = max(0, loads - NS); i < loads; ++i) mbar_wait_parked(full(i % NS), (i / NS) & 1);
+    }
+    if (warp == W_MMA && lane == 0) {  // one more commit covers every MMA issued
       umma_commit(drained);
       mbar_wait_parked(drained, 0);
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == W_MMA) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, X::kTmem);
   }
@@ -936,10 +921,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, RP>::kCtas)
 
 // ---- combine -----------------------------------------------------------------------------------
 //
-// A row's groups, in eight interleaved chains (group i in chain i % 8), then
-// ((0+1)+(2+3))+((4+5)+(6+7)).  WIDE: a thread set per chain (long caches, few
-// rows); otherwise each thread runs all chains of four columns (many rows of
-// few groups).  Reads what the attention kernel wrote a moment ago (L2).
+// A row's groups, counted from the first it sees: group i in chain i % 32,
+// the chains joined pairwise as a tree.  SETS thread sets share a row's
+// chains: 1 (a thread runs a row's chains itself; at most eight groups), 8 or
+// 32 (long caches, few rows).  Reads what the attention kernel wrote a moment
+// ago (L2): the loads of a cut group's tiles are issued together.
 
 struct State {
   float m, l;
@@ -955,99 +941,137 @@ __device__ __forceinline__ void fold_state(State& s, float m, float l, const flo
   s.a.w = __fmaf_rn(s.a.w, al, __fmul_rn(a.w, be));
 }
 
-template <int D, int RP, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 2 * D : 256) kv_combine_kernel(const __grid_constant__ Params p) {
-  constexpr int kLanes = D / 4, kSets = WIDE ? kChains : 256 / kLanes;  // thread sets: chains, or rows
-  __shared__ float s_m[kSets][kLanes], s_l[kSets][kLanes];
-  __shared__ float4 s_a[WIDE ? kSets : 1][kLanes];
+template <int N>
+__device__ __forceinline__ void join(State (&st)[N]) {  // into st[0]
+#pragma unroll
+  for (int n = 1; n < N; n <<= 1)
+#pragma unroll
+    for (int i = 0; i + n < N; i += 2 * n) fold_state(st[i], st[i + n].m, st[i + n].l, st[i + n].a);
+}
+
+// The last b with cu[b] <= t, by the whole warp (32 probes a step).
+__device__ __forceinline__ int find_request(const Params& p, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.B;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, lane * step < n && p.cu[min(at, p.B)] <= t);
+    const int k = le ? 31 - __clz(le) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+template <int D, int RP, int SETS>
+__global__ void __launch_bounds__(SETS == 32 ? 1024 : 256) kv_combine_kernel(const __grid_constant__ Params p) {
+  constexpr int kCols = D < 128 ? D : 128;          // columns of a CTA's thread set (SETS > 1)
+  constexpr int kLanes = (SETS == 1 ? D : kCols) / 4;
+  constexpr int kPer = SETS == 1 ? 8 : kChains / SETS;  // chains of a thread
+  constexpr int kThreads = SETS == 1 ? 256 : SETS * kLanes;
+  __shared__ float2 s_ml[SETS == 1 ? 1 : SETS][kLanes];
+  __shared__ float4 s_a[SETS == 1 ? 1 : SETS][kLanes];
   const int set = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
-  const int64_t row = WIDE ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kSets + set;
+  const int64_t row = SETS == 1 ? (int64_t)blockIdx.x * (kThreads / kLanes) + set : (int64_t)blockIdx.x;
+  const int col = (SETS == 1 ? 0 : (int)blockIdx.y * kCols) + 4 * c;
   pdl_launch_dependents();
   pdl_wait();
-  const State none{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  State out = none;
-  if (row < (int64_t)p.T * p.q_heads) {
-    const int t = (int)(row / p.q_heads), hq = (int)(row % p.q_heads);
-    // the request of row t: the last b with cu[b] <= t
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    bool bad = false;
-    const Req r = load_req(p, lo, &bad);
-    const int j = t - r.c0;
-    if (j >= 0 && j < r.fresh) {
-      const int rt = j / p.TQ, h = hq / p.G;
-      const int tf = first_tile(p, r, rt), tl = last_tile(p, r, rt);
-      const int64_t total = p.starts[p.B];
-      const int64_t seg0 = p.starts[lo] + (rt ? tiles_before(p, r, rt) * p.heads : 0) + (int64_t)h * (tl - tf + 1);
-      const int g0 = first_tile(p, r, 0) / kGroupTiles;  // slot 0
-      const int rr = (j - rt * p.TQ) * p.G + hq % p.G;   // row within the row tile
-      auto owner = [&](int64_t x) { return ((x + 1) * p.grid - 1) / total; };  // the CTA whose range holds tile x
-      State st[WIDE ? 1 : kChains];
+  State st[kPer];
 #pragma unroll
-      for (int i = 0; i < (WIDE ? 1 : kChains); ++i) st[i] = none;
-      auto take = [&](int g, State& s) {  // one group
-        const int ta = max(tf, g * kGroupTiles), tb = min(tl, g * kGroupTiles + kGroupTiles - 1);
-        const int64_t xa = seg0 + ta - tf, oa = owner(xa), ob = owner(seg0 + tb - tf);
-        if (oa == ob) {
-          const int64_t at = ((int64_t)(g - g0) * p.T + t) * p.q_heads + hq;
-          const float2 ml = p.g_ml[at];
-          fold_state(s, ml.x, ml.y, *reinterpret_cast<const float4*>(p.g_acc + at * D + 4 * c));
-        } else {
-          State gs = none;
-          for (int k = ta; k <= tb; ++k) {
-            const int64_t o = owner(xa + k - ta);
-            // at the owner's end unless the group began in an earlier range
-            const int64_t at = ((o * 2 + (o == oa ? 1 : 0)) * kGroupTiles + k % kGroupTiles) * RP + rr;
-            const float2 ml = p.t_ml[at];
-            fold_state(gs, ml.x, ml.y, *reinterpret_cast<const float4*>(p.t_acc + at * D + 4 * c));
+  for (int i = 0; i < kPer; ++i) st[i] = State{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const bool inside = row < (int64_t)p.T * p.q_heads;
+  const int t = inside ? (int)(row / p.q_heads) : p.T - 1, hq = (int)(row - (int64_t)t * p.q_heads);
+  // (heads of 64 put two rows on a warp: perhaps of two tokens)
+  const int t_a = __shfl_sync(0xffffffffu, t, 0), t_b = __shfl_sync(0xffffffffu, t, 31);
+  int b = find_request(p, t_a);
+  if (t_b != t_a) {
+    const int b2 = find_request(p, t_b);
+    if (t == t_b) b = b2;
+  }
+  bool bad = false;
+  const Req r = load_req(p, b, &bad);
+  const int j = t - r.c0;
+  if (inside && j >= 0 && j < r.fresh) {
+    const int rt = j / p.TQ, h = hq / p.G;
+    const int tf = first_tile(p, r, rt), tl = last_tile(p, r, rt);
+    const int seg0 = p.starts[b] + (rt ? tiles_before(p, r, rt) * p.heads : 0) + h * (tl - tf + 1);
+    const Cut cut(p.starts[p.B], p.grid);
+    const int g0 = first_tile(p, r, 0) / kGroupTiles;  // slot 0
+    const int rr = (j - rt * p.TQ) * p.G + hq - h * p.G;  // row within the row tile
+    const int pos = r.base + j;
+    const int ga = p.window > 0 ? max(0, pos - p.window + 1) / kGroupTokens : 0, n = pos / kGroupTokens - ga + 1;
+    auto take = [&](int i, State& s) {  // the row's group i
+      const int g = ga + i;
+      const int ta = max(tf, g * kGroupTiles), tb = min(tl, g * kGroupTiles + kGroupTiles - 1);
+      const int xa = seg0 + ta - tf, o = cut.owner(xa), left = cut.begin(o + 1) - xa;  // tiles in the first range
+      if (tb - ta < left) {
+        const int64_t at = ((int64_t)(g - g0) * p.T + t) * p.q_heads + hq;
+        const float2 ml = p.g_ml[at];
+        fold_state(s, ml.x, ml.y, *reinterpret_cast<const float4*>(p.g_acc + at * D + col));
+        return;
+      }
+      float2 ml[kGroupTiles];
+      float4 a[kGroupTiles];
+      int own = o, end = left;
+#pragma unroll
+      for (int k = 0; k < kGroupTiles; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ta + k <= tb) {
+          if (k >= end) {  // (ranges may be single tiles)
+            ++own;
+            end = cut.begin(own + 1) - xa;
           }
-          fold_state(s, gs.m, gs.l, gs.a);
+          // at the owner's end where the group began in its range, else at its beginning
+          const int64_t at = (int64_t)((own * 2 + (own == o ? 1 : 0)) * kGroupTiles + (ta + k) % kGroupTiles) * RP + rr;
+          ml[k] = p.t_ml[at];
+          a[k] = *reinterpret_cast<const float4*>(p.t_acc + at * D + col);
         }
-      };
-      const int ga = tf / kGroupTiles, gb = tl / kGroupTiles;
-      if (WIDE) {
-        for (int g = ga + ((set - ga) & (kChains - 1)); g <= gb; g += kChains) take(g, st[0]);
-        out = st[0];
-      } else {
-        for (int gg = ga & ~(kChains - 1); gg <= gb; gg += kChains)
+      }
+      State gs{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < kChains; ++i)
-            if (gg + i >= ga && gg + i <= gb) take(gg + i, st[i]);
+      for (int k = 0; k < kGroupTiles; ++k) fold_state(gs, ml[k].x, ml[k].y, a[k]);
+      fold_state(s, gs.m, gs.l, gs.a);
+    };
+    if (SETS == 1) {
+      for (int i = 0; i < n; ++i) {  // n <= 8: one group a chain
+        State s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        take(i, s);
 #pragma unroll
-        for (int n = 1; n < kChains; n <<= 1)
+        for (int k = 0; k < kPer; ++k)
+          if (k == i) st[k] = s;
+      }
+    } else {
 #pragma unroll
-          for (int i = 0; i + n < (WIDE ? 1 : kChains); i += 2 * n) fold_state(st[i], st[i + n].m, st[i + n].l, st[i + n].a);
-        out = st[0];
+      for (int k = 0; k < kPer; ++k)
+        for (int i = set * kPer + k; i < n; i += kChains) take(i, st[k]);
+    }
+  }
+  join(st);
+  State out = st[0];
+  if (SETS > 1) {
+    s_ml[set][c] = make_float2(out.m, out.l);
+    s_a[set][c] = out.a;
+    // the tree over the sets, in shared memory
+    for (int k = 1; k < SETS; k <<= 1) {
+      __syncthreads();
+      if (set % (2 * k) == 0) {
+        const float2 ml = s_ml[set + k][c];
+        fold_state(out, ml.x, ml.y, s_a[set + k][c]);
+        s_ml[set][c] = make_float2(out.m, out.l);
+        s_a[set][c] = out.a;
       }
     }
-  }
-  if (WIDE) {
-    s_m[set][c] = out.m;
-    s_l[set][c] = out.l;
-    s_a[set][c] = out.a;
-    __syncthreads();
     if (set != 0) return;
-    State st[kChains];
-#pragma unroll
-    for (int i = 0; i < kChains; ++i) st[i] = State{s_m[i][c], s_l[i][c], s_a[i][c]};
-#pragma unroll
-    for (int n = 1; n < kChains; n <<= 1)
-#pragma unroll
-      for (int i = 0; i + n < kChains; i += 2 * n) fold_state(st[i], st[i + n].m, st[i + n].l, st[i + n].a);
-    out = st[0];
   }
-  if (row < (int64_t)p.T * p.q_heads) {
+  if (inside) {
     const bool any = out.l != 0.f;  // (NaN: yes)
     uint2 w;
     w.x = (uint32_t)f32_to_bf16_bits(any ? __fdiv_rn(out.a.x, out.l) : 0.f) |
           (uint32_t)f32_to_bf16_bits(any ? __fdiv_rn(out.a.y, out.l) : 0.f) << 16;
     w.y = (uint32_t)f32_to_bf16_bits(any ? __fdiv_rn(out.a.z, out.l) : 0.f) |
           (uint32_t)f32_to_bf16_bits(any ? __fdiv_rn(out.a.w, out.l) : 0.f) << 16;
-    *reinterpret_cast<uint2*>(p.out + row * D + 4 * c) = w;
+    *reinterpret_cast<uint2*>(p.out + row * D + col) = w;
   }
 }
 
@@ -1055,10 +1079,15 @@ __global__ void __launch_bounds__(WIDE ? 2 * D : 256) kv_combine_kernel(const __
 
 struct Layout {
   int RP, TQ, gmax, grid;
+  bool fits;  // positions on the line and rows of group results fit in 31 bits
   size_t starts, g_acc, g_ml, t_acc, t_ml, bytes;
 };
 
-int ctas_per_sm(int dim, int RP) { return dim == 256 && RP > 8 ? 1 : 2; }
+template <int D>
+int ctas_d(int RP) {
+  return RP == 8 ? Geo<D, 8>::kCtas : RP == 16 ? Geo<D, 16>::kCtas : Geo<D, 32>::kCtas;
+}
+int ctas_per_sm(int dim, int RP) { return dim == 64 ? ctas_d<64>(RP) : dim == 128 ? ctas_d<128>(RP) : ctas_d<256>(RP); }
 
 Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, int max_len, int window) {
   Layout y;
@@ -1068,20 +1097,24 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   y.RP = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   if (y.RP < G) y.RP = G <= 16 ? 16 : 32;
   y.TQ = y.RP / G;
-  int64_t groups = ((int64_t)max_len + kTile * kGroupTiles - 1) / (kTile * kGroupTiles);
+  int64_t groups = ((int64_t)max_len + kGroupTokens - 1) / kGroupTokens;
   if (window > 0) {
-    const int64_t span = ((int64_t)window + max_new - 2) / (kTile * kGroupTiles) + 2;
+    const int64_t span = ((int64_t)window + max_new - 2) / kGroupTokens + 2;
     if (span < groups) groups = span;
   }
   y.gmax = (int)groups;
   // no more CTAs than tiles
   const int64_t per = ((int64_t)max_len + kTile - 1) / kTile;
-  const int64_t most = (int64_t)(T < B ? T : B) * heads * (((int64_t)max_new + y.TQ - 1) / y.TQ) * per;
+  int64_t row_tiles = (int64_t)(T < B ? T : B) * (((int64_t)max_new + y.TQ - 1) / y.TQ);
+  const int64_t by_rows = (T < B ? T : B) + (int64_t)T / y.TQ;
+  if (by_rows < row_tiles) row_tiles = by_rows;
+  const int64_t most = row_tiles * heads * per;
+  y.fits = most <= INT32_MAX && (int64_t)y.gmax * T * q_heads <= INT32_MAX;
   const int full = kSms * ctas_per_sm(dim, y.RP);
   y.grid = most < full ? (int)most : full;
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   y.starts = 0;
-  y.g_acc = up(8 * ((size_t)B + 1));
+  y.g_acc = up(4 * ((size_t)B + 1));
   y.g_ml = y.g_acc + up((size_t)y.gmax * T * q_heads * dim * 4);
   y.t_acc = y.g_ml + up((size_t)y.gmax * T * q_heads * 8);
   y.t_ml = y.t_acc + up((size_t)y.grid * 2 * kGroupTiles * y.RP * dim * 4);
@@ -1095,7 +1128,6 @@ bool g_attr[64][9] = {};
 template <int D, int RP>
 cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int pdl, cudaStream_t s) {
   using X = Geo<D, RP>;
-  static_assert(X::kCtas == (D == 256 && RP > 8 ? 1 : 2), "ctas_per_sm");
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1122,21 +1154,27 @@ cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int 
   cfg.numAttrs = pdl > 0 ? 1 : 0;
   cfg.stream = s;
   cfg.gridDim = dim3((unsigned)y.grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(X::kThreads);
   cfg.dynamicSmemBytes = (size_t)X::kSmem;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, RP>, maps, p)) return e;
   const int64_t out_rows = (int64_t)a.T * a.q_heads;
   cfg.dynamicSmemBytes = 0;
-  // few rows of many groups: a thread set per chain; else a thread runs all chains
-  if (y.gmax > kChains && out_rows <= 4096) {
-    cfg.gridDim = dim3((unsigned)out_rows);
-    cfg.blockDim = dim3(2 * D);
-    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, RP, true>, p);
+  // at most eight groups a row: a thread set per row; else the row's chains over eight sets, or over 32 where that
+  // would leave SMs without a CTA
+  if (y.gmax <= 8) {
+    constexpr int kRowsPer = 256 / (D / 4);
+    cfg.gridDim = dim3((unsigned)((out_rows + kRowsPer - 1) / kRowsPer));
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, RP, 1>, p);
   }
-  constexpr int kRowsPer = 256 / (D / 4);
-  cfg.gridDim = dim3((unsigned)((out_rows + kRowsPer - 1) / kRowsPer));
-  cfg.blockDim = dim3(256);
-  return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, RP, false>, p);
+  constexpr int kCols = D < 128 ? D : 128;
+  cfg.gridDim = dim3((unsigned)out_rows, D / kCols);
+  if (out_rows * (D / kCols) >= kSms) {
+    cfg.blockDim = dim3(8 * kCols / 4);
+    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, RP, 8>, p);
+  }
+  cfg.blockDim = dim3(32 * kCols / 4);
+  return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, RP, 32>, p);
 }
 
 template <int D>
@@ -1151,7 +1189,8 @@ cudaError_t run_d(const KvAttentionArgs& a, const Layout& y, const Params& p, in
 }  // namespace
 
 size_t kv_attention_workspace(int B, int T, int q_heads, int kv_heads, int dim, int max_new, int max_len, int window) {
-  return make_layout(B, T, q_heads, kv_heads, dim, max_new, max_len, window).bytes;
+  const Layout y = make_layout(B, T, q_heads, kv_heads, dim, max_new, max_len, window);
+  return y.fits ? y.bytes : 0;
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t s) {
@@ -1181,7 +1220,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t 
   p.qk_scale = a.scale * kLog2e;
   p.gmax = y.gmax;
   p.grid = y.grid;
-  p.starts = reinterpret_cast<int64_t*>(w + y.starts);
+  p.starts = reinterpret_cast<int*>(w + y.starts);
   p.g_acc = reinterpret_cast<float*>(w + y.g_acc);
   p.g_ml = reinterpret_cast<float2*>(w + y.g_ml);
   p.t_acc = reinterpret_cast<float*>(w + y.t_acc);
