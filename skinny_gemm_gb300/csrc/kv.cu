@@ -180,13 +180,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
 //
 // A run is a maximal stretch of consecutive tokens of the call with
 // consecutive slots of one block; one (run, head, K or V) sets the scale of
-// one (block, head), so it belongs to one warp (up to kShortRun tokens, no
-// requantisation: decode and verify) or, after a barrier, to the whole CTA.
-// Bytes: 2 in and 1 out per element; nothing is read twice: a run's rows
-// stay in registers between the maximum and the codes.
+// one (block, head), so it belongs to one warp (up to kWarpChunks 16-byte
+// chunks a lane) or, if it is longer or the block's earlier rows have to be
+// re-coded, to the whole CTA.  A CTA looks at `per` consecutive tokens for one
+// head of K or V: eight where few tokens are new (a warp each: decode and
+// verify are one latency chain), 64 for prompt chunks, whose runs are long.
+// Bytes: 2 in and 1 out per element; a run's rows stay in registers between
+// the maximum and the codes.
 
-constexpr int kAppendThreads = 256, kAppendWarps = 8;  // a CTA looks at eight tokens
-constexpr int kShortRun = 4;
+constexpr int kAppendThreads = 256, kAppendWarps = 8;
+constexpr int kMaxPer = 64;     // tokens of a CTA
+constexpr int kWarpChunks = 8;  // 16-byte chunks a lane holds
+constexpr int kCtaChunks = 8;   // a thread holds of a run that the CTA takes; the rest of a longer one (more than
+                                // 64 rows of 256) is read again, from L2
 constexpr int kMinExp = -64;
 
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
@@ -252,14 +258,17 @@ struct AppendParams {
   int shift;   // log2(block)
   int lpr;     // log2(16-byte chunks of a row): dim = 8 << lpr
   int slots;   // blocks * block
+  int per;     // tokens per CTA
 };
 
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams p) {
-  __shared__ int s_job[kAppendWarps][2];  // (first slot, tokens) of a run left to the CTA; tokens 0: none
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendParams p) {
+  __shared__ int s_slot[1 + kMaxPer + 128];  // from the token before this CTA's on, as far as a run can reach
+  __shared__ int2 s_job[kMaxPer];            // (token, length) of the runs left to the CTA
+  __shared__ int s_jobs;
   __shared__ uint32_t s_peak[kAppendWarps];
   const KvAppendArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y, val = blockIdx.z;
+  const int h = blockIdx.y, val = blockIdx.z, t0 = blockIdx.x * p.per;
   const int heads = a.cache.heads, dim = a.cache.dim, block = a.cache.block, lpr = p.lpr;
   const uint16_t* src = (val ? a.v : a.k) + (int64_t)h * dim;
   const int64_t stride = val ? a.v_stride : a.k_stride;
@@ -268,96 +277,104 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
   pdl_launch_dependents();
   pdl_wait();
 
-  const int t = blockIdx.x * kAppendWarps + warp;
-  int slot = -1, n = 0;
-  if (t < a.T) {
-    // lane 0 the slot before, lane 1 this token's, lanes 2.. the next ones
-    const int tt = t - 1 + lane;
-    const int s = tt >= 0 && tt < a.T ? a.slots[tt] : -1;
-    const int prev = __shfl_sync(0xffffffffu, s, 0);
-    slot = __shfl_sync(0xffffffffu, s, 1);
-    const bool valid = slot >= 0 && slot < p.slots;
-    if (slot < -1 || slot >= p.slots) {
-      if (h == 0 && val == 0 && lane == 0) atomicOr(a.flags, W4A16_DEVICE_KV_RANGE);
+  if (tid == 0) s_jobs = 0;
+  for (int i = tid; i < 1 + p.per + block; i += kAppendThreads) {
+    const int t = t0 - 1 + i;
+    int s = t >= 0 && t < a.T ? a.slots[t] : -1;
+    if (s < -1 || s >= p.slots) {
+      if (h == 0 && val == 0 && i > 0 && i <= p.per) atomicOr(a.flags, W4A16_DEVICE_KV_RANGE);
+      s = -1;
     }
-    const bool joins = prev >= 0 && prev + 1 == slot && (prev >> p.shift) == (slot >> p.shift);
-    if (valid && !joins) {
-      const int room = block - (slot & (block - 1));
-      // tokens of the run: consecutive slots up to the block's end
-      const unsigned same = __ballot_sync(0xffffffffu, lane == 0 || s == slot + lane - 1);
-      n = min(same == 0xffffffffu ? 31 : __ffs(~same) - 2, room);
-      while (n >= 31 && n < room) {  // longer than this warp's look ahead
-        const int more = t + n + lane;
-        const unsigned go = __ballot_sync(0xffffffffu, more < a.T && a.slots[min(more, a.T - 1)] == slot + n + lane);
-        const int k = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
-        n = min(n + k, room);
-        if (k < 32) break;
-      }
-    }
+    s_slot[i] = s;
   }
-  const int blk = slot >> p.shift, off = slot & (block - 1);
-  bool job = n > kShortRun;
-  if (n > 0 && !job) {
-    // a warp's run: dim / 8 lanes a row, 32 * 8 / dim rows a pass
-    const int rpp = 32 >> lpr, sub = lane >> lpr, c = lane & ((1 << lpr) - 1);
-    uint4 v[kShortRun];
-    uint32_t peak = 0;
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < kShortRun; ++i) {
-      const int r = i * rpp + sub;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (r < n) v[i] = ld_nc_v4(src + (t + r) * stride + 8 * c);
-    }
-    const int64_t at = (int64_t)blk * heads + h;
-    const float old = off ? scales[at] : 0.f;
-#pragma unroll
-    for (int i = 0; i < kShortRun; ++i) peak = max(peak, peak8(v[i], odd));
-    peak = __reduce_max_sync(0xffffffffu, peak);
-    int e = scale_exp(peak);
-    if (off) {
-      const int eo = exp_of(old);
-      job = e > eo;  // earlier codes move to a larger scale: the whole CTA's work
-      e = max(e, eo);
-    }
-    if (!job) {
-      const float inv = exp2i(-e);
-#pragma unroll
-      for (int i = 0; i < kShortRun; ++i) {
-        const int r = i * rpp + sub;
-        if (r < n)
-          *reinterpret_cast<uint2*>(codes + ((at << p.shift) + off + r) * dim + 8 * c) = codes8(v[i], inv, odd);
+  __syncthreads();
+  const int* slot_of = s_slot + 1;
+  // the tokens that begin a run, 32 at a time; warp w takes every eighth
+  int nth = 0;
+  for (int i0 = 0; i0 < p.per; i0 += 32) {
+    const int i = i0 + lane, s = i < p.per ? slot_of[i] : -1, before = i < p.per ? slot_of[i - 1] : -1;
+    const bool joins = before >= 0 && before + 1 == s && (before >> p.shift) == (s >> p.shift);
+    unsigned leaders = __ballot_sync(0xffffffffu, s >= 0 && !joins);
+    for (; leaders; leaders &= leaders - 1, ++nth) {
+      if ((nth & (kAppendWarps - 1)) != warp) continue;
+      const int ti = i0 + __ffs(leaders) - 1, slot = slot_of[ti];
+      const int blk = slot >> p.shift, off = slot & (block - 1), room = block - off;
+      int n = 0;  // tokens of the run
+      for (;;) {
+        const unsigned go = __ballot_sync(0xffffffffu, n + lane < room && slot_of[ti + n + lane] == slot + n + lane);
+        n += go == 0xffffffffu ? 32 : __ffs(~go) - 1;
+        if (go != 0xffffffffu) break;
       }
-      if (off == 0 && lane == 0) scales[at] = exp2i(e);
+      const int chunks = n << lpr;
+      bool job = chunks > 32 * kWarpChunks;
+      if (!job) {
+        const uint16_t* from = src + (int64_t)(t0 + ti) * stride;
+        const int64_t at = (int64_t)blk * heads + h;
+        uint4 v[kWarpChunks];
+        const float old = off ? scales[at] : 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarpChunks; ++k) {
+          if (32 * k >= chunks) break;
+          const int x = 32 * k + lane;
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (x < chunks) v[k] = ld_nc_v4(from + (x >> lpr) * stride + 8 * (x & ((1 << lpr) - 1)));
+        }
+        uint32_t peak = 0;
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < kWarpChunks; ++k) {
+          if (32 * k >= chunks) break;
+          peak = max(peak, peak8(v[k], odd));
+        }
+        peak = __reduce_max_sync(0xffffffffu, peak);
+        int e = scale_exp(peak);
+        if (off) {
+          const int eo = exp_of(old);
+          job = e > eo;  // earlier codes move to a larger scale
+          e = max(e, eo);
+        }
+        if (!job) {
+          const float inv = exp2i(-e);
+          uint8_t* to = codes + ((at << p.shift) + off) * dim;
+#pragma unroll
+          for (int k = 0; k < kWarpChunks; ++k) {
+            if (32 * k >= chunks) break;
+            const int x = 32 * k + lane;
+            if (x < chunks) *reinterpret_cast<uint2*>(to + 8 * x) = codes8(v[k], inv, odd);
+          }
+          if (off == 0 && lane == 0) scales[at] = exp2i(e);
+        }
+      }
+      if (job && lane == 0) s_job[atomicAdd(&s_jobs, 1)] = make_int2(ti, n);
     }
-  }
-  if (lane == 0) {
-    s_job[warp][0] = slot;
-    s_job[warp][1] = job ? n : 0;
   }
   __syncthreads();
 
-  // long runs and requantisations, the CTA on one after another
-  for (int w = 0; w < kAppendWarps; ++w) {
-    const int jn = s_job[w][1];
-    if (jn == 0) continue;
-    const int js = s_job[w][0], jt = blockIdx.x * kAppendWarps + w;
-    const int jo = js & (block - 1);
-    const int64_t at = (int64_t)(js >> p.shift) * heads + h;
-    constexpr int kPer = 128 * 32 / kAppendThreads;  // chunks a thread holds of the largest run (128 tokens of 256)
-    uint4 v[kPer];
+  // the CTA's runs, one after another (in no fixed order: they touch different blocks)
+  const int jobs = s_jobs;
+  for (int w = 0; w < jobs; ++w) {
+    const int ti = s_job[w].x, n = s_job[w].y, slot = slot_of[ti], off = slot & (block - 1);
+    const int64_t at = (int64_t)(slot >> p.shift) * heads + h;
+    const uint16_t* from = src + (int64_t)(t0 + ti) * stride;
+    uint4 v[kCtaChunks];
     uint32_t peak = 0;
     bool odd = false;
-    const int chunks = jn << lpr;
+    const int chunks = n << lpr;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int x = i * kAppendThreads + tid;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (x < chunks) v[i] = ld_nc_v4(src + (jt + (x >> lpr)) * stride + 8 * (x & ((1 << lpr) - 1)));
+    for (int k = 0; k < kCtaChunks; ++k) {
+      if (k * kAppendThreads >= chunks) break;
+      const int x = k * kAppendThreads + tid;
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (x < chunks) v[k] = ld_nc_v4(from + (x >> lpr) * stride + 8 * (x & ((1 << lpr) - 1)));
     }
-    const float old = jo ? scales[at] : 0.f;
+    const float old = off ? scales[at] : 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) peak = max(peak, peak8(v[i], odd));
+    for (int k = 0; k < kCtaChunks; ++k) {
+      if (k * kAppendThreads >= chunks) break;
+      peak = max(peak, peak8(v[k], odd));
+    }
+    auto rest = [&](int x) { return ld_nc_v4(from + (x >> lpr) * stride + 8 * (x & ((1 << lpr) - 1))); };
+    for (int x = kCtaChunks * kAppendThreads + tid; x < chunks; x += kAppendThreads) peak = max(peak, peak8(rest(x), odd));
     peak = __reduce_max_sync(0xffffffffu, peak);
     if (lane == 0) s_peak[warp] = peak;
     __syncthreads();
@@ -365,12 +382,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
     for (int i = 0; i < kAppendWarps; ++i) peak = max(peak, s_peak[i]);
     int e = scale_exp(peak);
     uint8_t* base = codes + (at << p.shift) * dim;
-    if (jo) {
+    if (off) {
       const int eo = exp_of(old);
       if (e > eo) {
         const float ratio = exp2i(max(eo - e, -126));
         uint4* q = reinterpret_cast<uint4*>(base);
-        for (int x = tid; x < jo << (lpr - 1); x += kAppendThreads) {
+        for (int x = tid; x < off << (lpr - 1); x += kAppendThreads) {
           uint4 w4 = q[x];
           w4.x = recode4(w4.x, ratio);
           w4.y = recode4(w4.y, ratio);
@@ -383,10 +400,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
     }
     const float inv = exp2i(-e);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int x = i * kAppendThreads + tid;
-      if (x < chunks) *reinterpret_cast<uint2*>(base + jo * dim + 8 * (int64_t)x) = codes8(v[i], inv, odd);
+    for (int k = 0; k < kCtaChunks; ++k) {
+      if (k * kAppendThreads >= chunks) break;
+      const int x = k * kAppendThreads + tid;
+      if (x < chunks) *reinterpret_cast<uint2*>(base + off * dim + 8 * x) = codes8(v[k], inv, odd);
     }
+    for (int x = kCtaChunks * kAppendThreads + tid; x < chunks; x += kAppendThreads)
+      *reinterpret_cast<uint2*>(base + off * dim + 8 * x) = codes8(rest(x), inv, odd);
     __syncthreads();  // every thread has read the old scale (and s_peak)
     if (tid == 0) scales[at] = exp2i(e);
   }
@@ -406,11 +426,10 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, int pdl, cudaStream_t s) {
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int pdl, cudaStream_t s) {
   AppendParams p{a, __builtin_ctz((unsigned)a.cache.block), __builtin_ctz((unsigned)a.cache.dim) - 3,
-                 a.cache.blocks * a.cache.block};
+                 a.cache.blocks * a.cache.block, a.T >= 2048 ? kMaxPer : kAppendWarps};
   void* args[] = {&p};
-  return launch((const void*)kv_append_kernel,
-                dim3((unsigned)((a.T + kAppendWarps - 1) / kAppendWarps), (unsigned)a.cache.heads, 2), kAppendThreads, args,
-                pdl, s);
+  return launch((const void*)kv_append_kernel, dim3((unsigned)((a.T + p.per - 1) / p.per), (unsigned)a.cache.heads, 2),
+                kAppendThreads, args, pdl, s);
 }
 
 }  // namespace w4a16
