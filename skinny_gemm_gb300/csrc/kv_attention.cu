@@ -28,12 +28,15 @@
 // Bound: HBM.  A 128-token tile of heads of 256 is 64 KB; one CTA has one to
 // two tiles in flight, two CTAs an SM where shared memory allows.
 //
-// CTA: six warps.
-//   warps 0-3  a thread per token: scores from TMEM, mask, maximum, weights
-//              into shared memory; then a thread per output column (TMEM lane
-//              again): O from TMEM folded into registers
-//   warp 4     work list, block table, TMA of K and V blocks, scales
-//   warp 5     tensor memory, MMA issue (lane 0)
+// CTA: 4 NG + 4 NG + 2 warps (NG groups of R query rows).
+//   softmax warps  a thread per token: scores from TMEM, mask, maximum,
+//                  weights into shared memory, row sums
+//   fold warps     a thread per output column (TMEM lane): O from TMEM into the
+//                  running accumulators, partial results out
+//   one warp       work list, block table, TMA of K and V blocks, scales, queries
+//   one warp       tensor memory, MMA issue
+// A tile passes load -> S -> softmax -> O -> fold; softmax of one tile, fold of
+// the one before and the copies of the next run side by side.
 // Every wait is bounded: one that gives up raises W4A16_DEVICE_TIMEOUT, the
 // roles leave their loops, copies and MMAs in flight are waited for (bounded)
 // and the tensor memory is freed.
@@ -42,6 +45,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv.cuh"
@@ -57,53 +61,59 @@ constexpr int kTile = 128;      // tokens per tile (the M of the MMAs)
 constexpr int kGroupTiles = 8;  // tiles per group
 constexpr int kGroupTokens = kTile * kGroupTiles;
 constexpr int kChains = 32;     // interleaved chains over a row's groups
-constexpr int kRows = 8;        // query rows of a softmax warp group
-constexpr int kDescs = 4;       // tile descriptors in flight
-constexpr int kRing = 3;        // maxima and sums: a warp may write tile t + 1 while another still folds t - 1
+constexpr int kDescs = 8;       // tile descriptors in flight
+constexpr int kRing = 4;        // row sums and weights' barriers: softmax may be two tiles ahead of the fold
 constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // flags of a tile descriptor
 constexpr int kNewSeg = 1;     // another (request, row tile, head) than the tile before
 constexpr int kEnd = 2;        // no tile: the CTA's range is done
-constexpr int kBadBlock = 4;   // some needed block is not in the cache
+constexpr int kFix = 4;        // some token of the tile is not seen by some row, or its block is not in the cache
 constexpr int kGroupBegin = 8; // first tile of a group folded here
 constexpr int kGroupEnd = 16;  // its last tile
 constexpr int kPart = 32;      // tile of a group that a cut divides
-constexpr int kTail = 64;      // ... at this CTA's end (else at its beginning)
 
 struct Desc {
   int flags, h, j0, tile;      // key head, first token of the row tile in its request
-  int base, fresh, c0, gi;     // tokens before the step, new tokens, first row, group slot
+  int base, fresh, c0, at;     // tokens before the step, new tokens, first row, group slot (kPart: tile slot)
   int pad[8];
   float ks[8], vs[8];          // scales of the tile's blocks (0: no such block)
 };
 static_assert(sizeof(Desc) == 128, "two 64-byte halves");
 
-// RP rows of a row tile (query tokens x heads of a group), eight to a softmax
-// warp group, so that threads hold the same registers whatever RP.
+// RP rows of a row tile (query tokens x heads of a group), R to a softmax warp
+// group: more rows a thread spread its fixed work per tile (waits, exchange of
+// maxima) over more of them, as far as registers go.
 // CTAs per SM and K/V slots (128 tokens each): as many bytes in flight as the
-// shared memory holds, in as many CTAs as its queries, weights and registers
-// leave room for; more CTAs hide more of the chain S -> weights -> O.
+// shared memory holds, in as many CTAs as registers leave room for.
 template <int D, int RP>
 struct Geo {
-  static constexpr int kGroups = RP / kRows;                   // softmax warp groups
-  static constexpr int kThreads = 128 * kGroups + 64;
+  static constexpr int R = RP < 16 ? RP : 16;
+  static constexpr int kGroups = RP / R;
+  static constexpr int kThreads = 256 * kGroups + 64;
+  static constexpr int kCols = RP < 8 ? 16 : 2 * RP;           // columns of S and O: first and second terms
   static constexpr int kPanels = D <= 128 ? 1 : D / 128;       // 128-byte column panels of K and V
   static constexpr int kRowB = D <= 128 ? D : 128;             // bytes of a panel's row
   static constexpr int kPanelBytes = kTile * kRowB;
   static constexpr int kSlot = kTile * D;
-  static constexpr int kQ = kPanels * 2 * RP * 128;
-  static constexpr int kP = kTile * 2 * RP;
-  static constexpr int kCtas = RP == 8 ? (D == 256 ? 2 : D == 128 ? 3 : 4) : RP == 16 ? (D == 256 ? 1 : 2) : 1;
-  static constexpr int kSlots = RP == 8 ? (D == 256 ? 3 : D == 128 ? 4 : 5)
+  static constexpr int kQ = kPanels * kCols * 128;
+  static constexpr int kStage = RP * D * 2;                    // a segment's query rows as they come
+  static constexpr int kP = kTile * kCols;
+  static constexpr int kCtas = RP == 4 ? (D == 256 ? 2 : 3) : RP == 8 ? 2 : RP == 16 ? (D == 256 ? 1 : 2) : 1;
+  static constexpr int kSlots = RP <= 8 ? (D == 256 ? 3 : D == 128 ? (RP == 4 ? 4 : 6) : 6)
                                 : RP == 16 ? (D == 256 ? 6 : D == 128 ? 5 : 8) : D == 256 ? 5 : D == 128 ? 10 : 12;
-  static constexpr int kBars = 2 * kSlots + 2 * kDescs + 6 + 4 + kGroups + 1;
-  // maxima and sums (kRing tiles x four warps), fold factors per warp, row factors and limits
-  static constexpr int kRowData = RP * 4 * (2 * 4 * kRing + 2 * 4 + 3);
-  static constexpr int kSmem = kSlots * kSlot + kQ + 2 * kP + kDescs * (int)sizeof(Desc) + kRowData + 8 * kBars + 16 + 1024;
-  static constexpr uint32_t kTmem = RP == 8 ? 64 : RP == 16 ? 128 : 256;  // S twice, O once
+  static constexpr int kBars = 2 * kSlots + 2 * kDescs + 4 + kRing + 4 + 5 + kGroups;
+  // rows (bits) of a tile that see a NaN in a thread's columns
+  using Marks = std::conditional_t<(kPanels * R > 16), uint32_t, uint16_t>;
+  // warps' maxima (two tiles), sums (kRing tiles x four warps), maxima (kRing), fold factors per warp, row factors and
+  // limits; NaN marks (kRing tiles)
+  static constexpr int kRowData = RP * 4 * (2 * 4 + kRing * 4 + kRing + 2 * 4 + 3) + kRing * 128 * kGroups * (int)sizeof(Marks);
+  static constexpr int kSmem = kSlots * kSlot + kQ + 2 * kP + kStage + kDescs * (int)sizeof(Desc) + kRowData + 8 * kBars + 32;
+  static constexpr int kTmemCols = 2 * kCols * (1 + kPanels);  // S twice, O twice
+  static constexpr uint32_t kTmem = kTmemCols <= 64 ? 64 : kTmemCols <= 128 ? 128 : kTmemCols <= 256 ? 256 : 512;
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert(kCtas * kTmem <= 512, "tensor memory of an SM");
 };
 
 struct Params {
@@ -120,12 +130,13 @@ struct Params {
   float qk_scale;  // scale * log2(e)
   int gmax;        // group slots per row
   int grid;
+  int RP, t_slots;  // rows of a row tile; tile slots per CTA
   // workspace
   int* starts;   // [B + 1] tiles before each request
   float* g_acc;  // [gmax][T][q_heads][D]
   float2* g_ml;  // [gmax][T][q_heads]
-  float* t_acc;  // [grid][2 * kGroupTiles][RP][D]
-  float2* t_ml;  // [grid][2 * kGroupTiles][RP]
+  float* t_acc;  // [grid][t_slots][RP][D]
+  float2* t_ml;  // [grid][t_slots][RP]
   int* flags;
 };
 
@@ -205,6 +216,11 @@ struct Cut {
   int per, rem;
   __device__ __forceinline__ Cut(int total, int grid) : per(total / grid), rem(total - per * grid) {}
   __device__ __forceinline__ int begin(int c) const { return c * per + min(c, rem); }
+  // The slot of tile x of a divided group among range c's: the group began in an earlier range (its tiles are the
+  // range's first), or goes on in the next (its last; a range has at most seven of each).
+  __device__ __forceinline__ int slot(int c, int x, bool tail, int slots) const {
+    return c * slots + (tail ? slots - (begin(c + 1) - x) : x - begin(c));
+  }
   __device__ __forceinline__ int owner(int x) const {
     const int big = rem * (per + 1);
     return x < big ? x / (per + 1) : rem + (x - big) / max(per, 1);
@@ -253,74 +269,61 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
+  if constexpr (N == 8) {
+    tmem_ld8(addr, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 16) {
+      float t[16];
+      tmem_ld16(addr + i, t);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[i + k] = t[k];
+    }
+  }
+}
+
 // ---- the kernel -----------------------------------------------------------------------------------
 
 template <int D, int RP>
 __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     kv_attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using X = Geo<D, RP>;
-  constexpr int NS = X::kSlots, NP = X::kPanels, NG = X::kGroups, R = kRows;
-  constexpr int W_LOAD = 4 * NG, W_MMA = 4 * NG + 1;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int NS = X::kSlots, NP = X::kPanels, NG = X::kGroups, R = X::R, C = X::kCols, ND = kDescs;
+  constexpr int W_FOLD = 4 * NG, W_LOAD = 8 * NG, W_MMA = 8 * NG + 1;
+  extern __shared__ __align__(1024) uint8_t base[];
   uint8_t* q_mem = base + NS * X::kSlot;
   uint8_t* p_mem = q_mem + X::kQ;
-  Desc* descs = reinterpret_cast<Desc*>(p_mem + 2 * X::kP);
-  float* s_max = reinterpret_cast<float*>(descs + kDescs);           // [kRing][4 warps][RP]
-  float* s_sum = s_max + kRing * 4 * RP;                             // [kRing][4 warps][RP]
-  float2* s_ab = reinterpret_cast<float2*>(s_sum + kRing * 4 * RP);  // [4 warps][RP]
+  uint8_t* stage = p_mem + 2 * X::kP;
+  Desc* descs = reinterpret_cast<Desc*>(stage + X::kStage);
+  float* s_max = reinterpret_cast<float*>(descs + ND);               // [2][4 warps][RP]
+  float* s_sum = s_max + 2 * 4 * RP;                                 // [kRing][4 warps][RP]
+  float* s_top = s_sum + kRing * 4 * RP;                             // [kRing][RP]
+  float2* s_ab = reinterpret_cast<float2*>(s_top + kRing * RP);      // [4 warps][RP]
   float* s_qf = reinterpret_cast<float*>(s_ab + 4 * RP);             // [RP] score factor of a row
   int2* s_lim = reinterpret_cast<int2*>(s_qf + RP);                  // [RP] first and last token a row sees
-  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(s_lim + RP);
+  auto* s_taint = reinterpret_cast<typename X::Marks*>(s_lim + RP);  // [kRing][128 NG]
+  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(s_taint + kRing * 128 * NG);
   const uint32_t slots = smem_u32(base), q_s = smem_u32(q_mem), p_s = smem_u32(p_mem), bars = smem_u32(bar_mem);
-  auto full = [&](int i) { return bars + 8u * i; };                   // slot: copies landed
-  auto empty = [&](int i) { return bars + 8u * (NS + i); };           // slot: MMAs done with it
-  auto d_full = [&](int i) { return bars + 8u * (2 * NS + i); };      // descriptor and scales written
-  auto d_free = [&](int i) { return bars + 8u * (2 * NS + kDescs + i); };
-  auto s_full = [&](int i) { return bars + 8u * (2 * NS + 2 * kDescs + i); };
-  auto s_free = [&](int i) { return bars + 8u * (2 * NS + 2 * kDescs + 2 + i); };
-  auto p_full = [&](int i) { return bars + 8u * (2 * NS + 2 * kDescs + 4 + i); };
-  const uint32_t o_full = bars + 8u * (2 * NS + 2 * kDescs + 6), o_free = o_full + 8, q_full = o_full + 16;
-  const uint32_t drained = o_full + 24, all_sync = o_full + 32;  // all_sync: every softmax warp
-  auto grp_sync = [&](int g) { return o_full + 40 + 8u * g; };   // the four warps of a group
+  auto full = [&](int i) { return bars + 8u * i; };                  // slot: copies landed
+  auto empty = [&](int i) { return bars + 8u * (NS + i); };          // slot: MMAs done with it
+  auto d_full = [&](int i) { return bars + 8u * (2 * NS + i); };     // descriptor and scales written
+  auto d_free = [&](int i) { return bars + 8u * (2 * NS + ND + i); };
+  const uint32_t bars2 = bars + 8u * (2 * NS + 2 * ND);
+  auto s_full = [&](int i) { return bars2 + 8u * i; };
+  auto s_free = [&](int i) { return bars2 + 8u * (2 + i); };
+  auto o_full = [&](int i) { return bars2 + 8u * (4 + i); };         // (the weights were read, too)
+  auto o_free = [&](int i) { return bars2 + 8u * (6 + i); };
+  auto p_full = [&](int i) { return bars2 + 8u * (8 + i); };         // [kRing] weights, sums and maxima written
+  const uint32_t q_full = bars2 + 8u * (8 + kRing), drained = q_full + 8, all_sync = q_full + 16;
+  const uint32_t st_full = q_full + 24, st_free = q_full + 32;       // staged query rows
+  auto grp_sync = [&](int g) { return q_full + 40 + 8u * g; };       // the four softmax warps of a group
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_mem + X::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  volatile int* s_nan = reinterpret_cast<volatile int*>(s_tmem + 2);  // [2] 1 + the last (even, odd) tile with NaN codes in partly seen tokens
+  volatile int* s_nan = reinterpret_cast<volatile int*>(s_tmem + 2);  // [kRing] 1 + a tile whose marks are in s_taint
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), 1);
-      mbar_init(empty(i), 1);
-    }
-    for (int i = 0; i < kDescs; ++i) {
-      mbar_init(d_full(i), 33);
-      mbar_init(d_free(i), 4 * NG + 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full(i), 1);
-      mbar_init(s_free(i), 4 * NG);
-      mbar_init(p_full(i), 4 * NG);
-    }
-    mbar_init(o_full, 1);
-    mbar_init(o_free, 4 * NG);
-    mbar_init(q_full, 4 * NG);
-    mbar_init(drained, 1);
-    mbar_init(all_sync, 4 * NG);
-    for (int i = 0; i < NG; ++i) mbar_init(grp_sync(i), 4);
-    *s_abort = 0;
-    s_nan[0] = s_nan[1] = 0;
-    fence_barrier_init();
-  }
-  if (warp == W_MMA) {
-    tmem_alloc(smem_u32(s_tmem), X::kTmem);
-    tmem_relinquish();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = *s_tmem;
-  const uint32_t s_col = tmem, o_col = tmem + 4 * RP;
   auto give_up = [&]() {
     atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
     *s_abort = 1;
@@ -328,18 +331,43 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {  // all lanes; the same answer for all
     return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity));
   };
-  pdl_launch_dependents();
-  pdl_wait();
-  int loads = 0;  // producer: slots requested
 
+  // ---- set-up; meanwhile the loading warp finds its range of the line ----
+  const int nb = kTile >> p.shift, block = 1 << p.shift;  // blocks per tile
+  bool bad = false;
+  int total = 0, beg = 0, end = 0, b0 = 0;
+  Req mine{0, 0, 0}, r{0, 0, 0};  // the loading warp: this lane's request of 32, and the current one
+  int b = 0, rt = 0, h = 0, tile = 0, t_first = 0, t_last = -1;
+  int seg0 = 0;  // position of the segment's first tile
+  int id = -2;
+  int loads = 0;  // slots requested
+  auto take = [&](int bl) {  // request b0 + bl becomes the current one
+    b = b0 + bl;
+    r.c0 = __shfl_sync(0xffffffffu, mine.c0, bl);
+    r.fresh = __shfl_sync(0xffffffffu, mine.fresh, bl);
+    r.base = __shfl_sync(0xffffffffu, mine.base, bl);
+  };
+  auto enter = [&]() {
+    t_first = first_tile(p, r, rt);
+    t_last = last_tile(p, r, rt);
+  };
+  // block id of this lane for a tile: -2 not needed, -1 (or any bad id) not in the cache
+  auto load_id = [&]() {
+    const int lo = p.window > 0 ? max(0, r.base + rt * p.TQ - p.window + 1) : 0;
+    const int hi = r.base + min((rt + 1) * p.TQ, r.fresh) - 1;
+    const int j = tile * nb + lane;
+    if (lane >= nb || (j + 1) * block <= lo || j * block > hi) return -2;
+    return j < p.max_blocks ? p.table[(int64_t)b * p.max_blocks + j] : -1;
+  };
   if (warp == W_LOAD) {
-    // ---- work list and copies ----
-    const int nb = kTile >> p.shift, block = 1 << p.shift;  // blocks per tile
-    bool bad = false;
-    int total = 0;
-    Req mine{0, 0, 0};
-    int mine_end = 0;  // inclusive prefix of this lane's request
-    auto scan = [&](int b0) {  // loads 32 requests; their inclusive prefix of tiles after `total`
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    int mine_end = 0;         // inclusive prefix of this lane's request
+    auto scan = [&]() {       // loads 32 requests; their inclusive prefix of tiles after `total`
       mine = load_req(p, b0 + lane, &bad);
       int n = mine.fresh > 0 ? tiles_before(p, mine, row_tiles(p, mine)) * p.heads : 0;
 #pragma unroll
@@ -349,41 +377,27 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
       mine_end = total + n;
     };
-    int b0 = 0;
     for (; b0 < p.B; b0 += 32) {
-      scan(b0);
+      scan();
       if (blockIdx.x == 0 && b0 + lane < p.B) p.starts[b0 + lane + 1] = mine_end;
       total = __shfl_sync(0xffffffffu, mine_end, 31);
     }
     if (blockIdx.x == 0 && lane == 0) p.starts[0] = 0;
     if (bad && blockIdx.x == 0) atomicOr(p.flags, W4A16_DEVICE_KV_RANGE);
     const Cut cut(total, p.grid);
-    const int beg = cut.begin(blockIdx.x), end = cut.begin(blockIdx.x + 1);
+    beg = cut.begin(blockIdx.x);
+    end = cut.begin(blockIdx.x + 1);
     // the request of `beg`
     total = 0;
     b0 = 0;
     if (p.B > 32) {
       for (; b0 < p.B; b0 += 32) {
-        scan(b0);
+        scan();
         const int e = __shfl_sync(0xffffffffu, mine_end, 31);
         if (e > beg) break;
         total = e;
       }
     }
-    int b = 0, rt = 0, h = 0, tile = 0, t_first = 0, t_last = -1;
-    int x = beg;   // position on the line
-    int seg0 = 0;  // position of the segment's first tile
-    Req r{0, 0, 0};
-    auto take = [&](int bl) {  // request b0 + bl becomes the current one
-      b = b0 + bl;
-      r.c0 = __shfl_sync(0xffffffffu, mine.c0, bl);
-      r.fresh = __shfl_sync(0xffffffffu, mine.fresh, bl);
-      r.base = __shfl_sync(0xffffffffu, mine.base, bl);
-    };
-    auto enter = [&]() {
-      t_first = first_tile(p, r, rt);
-      t_last = last_tile(p, r, rt);
-    };
     if (beg < end) {
       const unsigned past = __ballot_sync(0xffffffffu, mine_end > beg);
       const int bl = __ffs(past) - 1;
@@ -403,34 +417,70 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       h = off / n;
       tile = t_first + off - h * n;
       seg0 = beg - (tile - t_first);
+      id = load_id();
     }
-    // block id of this lane for a tile: -2 not needed, -1 (or any bad id) not in the cache
-    auto load_id = [&]() {
-      const int lo = p.window > 0 ? max(0, r.base + rt * p.TQ - p.window + 1) : 0;
-      const int hi = r.base + min((rt + 1) * p.TQ, r.fresh) - 1;
-      const int j = tile * nb + lane;
-      if (lane >= nb || (j + 1) * block <= lo || j * block > hi) return -2;
-      return j < p.max_blocks ? p.table[(int64_t)b * p.max_blocks + j] : -1;
-    };
-    int id = beg < end ? load_id() : -2;
+  } else if (warp == W_MMA) {
+    tmem_alloc(smem_u32(s_tmem), X::kTmem);
+    tmem_relinquish();
+  } else if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 1);
+    }
+    for (int i = 0; i < ND; ++i) {
+      mbar_init(d_full(i), 33);
+      mbar_init(d_free(i), 8 * NG + 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(s_free(i), 4 * NG);
+      mbar_init(o_full(i), 1);
+      mbar_init(o_free(i), 4 * NG);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(p_full(i), 4 * NG);
+      s_nan[i] = 0;
+    }
+    mbar_init(q_full, 4 * NG);
+    mbar_init(drained, 1);
+    mbar_init(all_sync, 4 * NG);
+    mbar_init(st_full, 1);
+    mbar_init(st_free, 4 * NG);
+    for (int i = 0; i < NG; ++i) mbar_init(grp_sync(i), 4);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t s_col = tmem, o_col = tmem + 2 * C;  // S: two tiles of C columns; O: two tiles of NP panels of C
+
+  if (warp == W_LOAD) {
+    // ---- work list and copies ----
     bool fresh_seg = true, ok = true;
-    int t = 0;
+    int x = beg, t = 0, seg = 0;
     for (; x < end && ok; ++x, ++t) {
       // this tile's descriptor
-      const int ds = t % kDescs, ch = h;
+      const int ds = t % ND, ch = h;
       const int g_lo = max(seg0, x - tile % kGroupTiles), g_hi = min(seg0 + t_last - t_first, x - tile % kGroupTiles + kGroupTiles - 1);
-      int fl = fresh_seg ? kNewSeg : 0;
-      if (g_lo >= beg && g_hi < end) fl |= (x == g_lo ? kGroupBegin : 0) | (x == g_hi ? kGroupEnd : 0);
-      else fl |= kPart | (g_lo >= beg ? kTail : 0);
+      const int j0 = rt * p.TQ, toks = min(p.TQ, r.fresh - j0), pos0 = r.base + j0, pos1 = pos0 + toks - 1;
+      int fl = fresh_seg ? kNewSeg : 0, at;
+      if (g_lo >= beg && g_hi < end) {
+        fl |= (x == g_lo ? kGroupBegin : 0) | (x == g_hi ? kGroupEnd : 0);
+        at = tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles;
+      } else {
+        fl |= kPart;
+        at = (int)blockIdx.x * p.t_slots + (g_lo >= beg ? p.t_slots - (end - x) : x - beg);
+      }
       const bool valid = id >= 0 && id < p.blocks;
       const unsigned need = __ballot_sync(0xffffffffu, id != -2), have = __ballot_sync(0xffffffffu, valid);
-      if (need != have) fl |= kBadBlock;
-      if (t >= kDescs && !(ok = wait_warp(d_free(ds), ((t / kDescs) - 1) & 1))) break;
+      if (need != have || tile * kTile + kTile - 1 > pos0 || (p.window > 0 && tile * kTile < pos1 - p.window + 1)) fl |= kFix;
+      if (t >= ND && !(ok = wait_warp(d_free(ds), ((t / ND) - 1) & 1))) break;
       Desc& de = descs[ds];
       if (lane == 0) {
-        *reinterpret_cast<int4*>(&de.flags) = make_int4(fl, ch, rt * p.TQ, tile);
-        *reinterpret_cast<int4*>(&de.base) =
-            make_int4(r.base, r.fresh, r.c0, tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles);
+        *reinterpret_cast<int4*>(&de.flags) = make_int4(fl, ch, j0, tile);
+        *reinterpret_cast<int4*>(&de.base) = make_int4(r.base, r.fresh, r.c0, at);
         if (need != have) atomicOr(p.flags, W4A16_DEVICE_KV_RANGE);
       }
       if (lane < nb) {
@@ -445,6 +495,16 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       __syncwarp();
       cp_async_arrive(d_full(ds));
       if (lane == 0) mbar_arrive(d_full(ds));
+      if (fresh_seg) {  // the segment's query rows, a copy per token
+        if (seg > 0 && !(ok = wait_warp(st_free, (seg - 1) & 1))) break;
+        const uint32_t bytes = (uint32_t)(p.G * D * 2);
+        if (lane == 0) mbar_expect_tx(st_full, toks * bytes);
+        __syncwarp();
+        if (lane < toks)
+          bulk_load(smem_u32(stage) + lane * bytes, p.q + (int64_t)(r.c0 + j0 + lane) * p.q_stride + (int64_t)ch * p.G * D,
+                    bytes, st_full, policy_evict_first());
+        ++seg;
+      }
       // the next tile, its block ids requested before this one's slots are waited for
       const bool same = tile < t_last;
       int next_id = -2;
@@ -497,8 +557,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       fresh_seg = !same;
     }
     if (ok) {  // the end mark
-      const int ds = t % kDescs;
-      ok = t < kDescs || wait_warp(d_free(ds), ((t / kDescs) - 1) & 1);
+      const int ds = t % ND;
+      ok = t < ND || wait_warp(d_free(ds), ((t / ND) - 1) & 1);
       if (ok) {
         if (lane == 0) descs[ds].flags = kEnd;
         __syncwarp();
@@ -507,73 +567,67 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
     }
     if (!ok && lane == 0) give_up();
-  } else if (warp == W_MMA) {
-    // ---- MMA issue: S of tile t, then O of tile t - 1 ----
-    if (lane == 0) {
-      constexpr uint32_t id_s = umma_idesc_e4m3(128, 2 * RP, false, false);
-      constexpr uint32_t id_o = umma_idesc_e4m3(128, 2 * RP, true, true);
-      bool ok = true;
-      int seg = 0, t = 0;
-      bool more = true;
-      for (; ok && more; ++t) {
-        const int ds = t % kDescs;
-        ok = mbar_wait_parked(d_full(ds), (t / kDescs) & 1);
-        if (!ok) break;
-        const int fl = descs[ds].flags;
-        mbar_arrive(d_free(ds));
-        more = !(fl & kEnd);
-        if (more) {
-          const int slot = (2 * t) % NS;
-          if (fl & kNewSeg) ok = mbar_wait_parked(q_full, seg++ & 1);
-          ok = ok && mbar_wait_parked(full(slot), ((2 * t) / NS) & 1) &&
-               (t < 2 || mbar_wait_parked(s_free(t & 1), ((t >> 1) - 1) & 1));
-          if (!ok) break;
-          tc_fence_after_sync();
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            const uint32_t ka = slots + slot * X::kSlot + (k / 4) * X::kPanelBytes + (k % 4) * 32;
-            const uint64_t ad = D < 128 ? umma_desc(ka, 16, 512, 4) : umma_desc(ka, 16, 1024, 2);
-            const uint64_t bd = umma_desc(q_s + (k / 4) * 2 * RP * 128 + (k % 4) * 32, 16, 1024, 2);
-            umma_f8(s_col + (t & 1) * 2 * RP, ad, bd, id_s, k > 0);
-          }
-          umma_commit(s_full(t & 1));
-          umma_commit(empty(slot));
-        }
-        if (t > 0) {  // O = V^T P^T of tile t - 1
-          const int u = t - 1, slot = (2 * u + 1) % NS;
-          ok = mbar_wait_parked(p_full(u & 1), (u >> 1) & 1) && mbar_wait_parked(full(slot), ((2 * u + 1) / NS) & 1) &&
-               (u == 0 || mbar_wait_parked(o_free, (u - 1) & 1));
-          if (!ok) break;
-          tc_fence_after_sync();
-#pragma unroll
-          for (int c = 0; c < NP; ++c)
-#pragma unroll
-            for (int k = 0; k < kTile / 32; ++k) {
-              const uint32_t va = slots + slot * X::kSlot + c * X::kPanelBytes + k * 32 * X::kRowB;
-              // heads of 64: the MMA's rows 64 .. 127 repeat whatever lies 512 bytes on, and nobody reads them
-              const uint64_t ad = D < 128 ? umma_desc(va, 512, 512, 4) : umma_desc(va, 1024, 1024, 2);
-              const uint64_t bd = umma_desc(p_s + (u & 1) * X::kP + k * 512, 128, 2048, 0);
-              umma_f8(o_col + c * 2 * RP, ad, bd, id_o, k > 0);
-            }
-          umma_commit(o_full);
-          umma_commit(empty(slot));
-        }
-      }
-      if (!ok) give_up();
+    if (!ok) {  // staged rows in flight
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (seg > 0 && lane == 0) mbar_wait_parked(st_full, (seg - 1) & 1);
     }
-  } else {
-    // ---- softmax and fold: thread = token of the tile, then = output column; rows R grp .. R grp + R - 1 ----
+  } else if (warp == W_MMA) {
+    // ---- MMA issue: S of tile t, then O of tile t - 1 (the warp together, one thread issues) ----
+    constexpr uint32_t id_s = umma_idesc_e4m3(128, C, false, false);
+    constexpr uint32_t id_o = umma_idesc_e4m3(128, C, true, true);
+    const uint32_t go = elect_one();
+    bool ok = true, more = true;
+    int seg = 0;
+    for (int t = 0; more; ++t) {
+      const int ds = t % ND;
+      if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
+      const int fl = descs[ds].flags;
+      __syncwarp();
+      if (go) mbar_arrive(d_free(ds));
+      more = !(fl & kEnd);
+      if (more) {
+        const int slot = (2 * t) % NS;
+        if (fl & kNewSeg) ok = wait_warp(q_full, seg++ & 1);
+        ok = ok && wait_warp(full(slot), ((2 * t) / NS) & 1) && (t < 2 || wait_warp(s_free(t & 1), ((t >> 1) - 1) & 1));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t ka = slots + slot * X::kSlot, d = s_col + (t & 1) * C;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          const uint32_t kk = ka + (k / 4) * X::kPanelBytes + (k % 4) * 32;
+          const uint64_t ad = D < 128 ? umma_desc(kk, 16, 512, 4) : umma_desc(kk, 16, 1024, 2);
+          umma_f8(go, d, ad, umma_desc(q_s + (k / 4) * C * 128 + (k % 4) * 32, 16, 1024, 2), id_s, k > 0);
+        }
+        umma_commit_if(go, s_full(t & 1));
+        umma_commit_if(go, empty(slot));
+      }
+      if (t > 0) {  // O = V^T P^T of tile t - 1
+        const int u = t - 1, slot = (2 * u + 1) % NS;
+        ok = wait_warp(p_full(u % kRing), (u / kRing) & 1) && wait_warp(full(slot), ((2 * u + 1) / NS) & 1) &&
+             (u < 2 || wait_warp(o_free(u & 1), ((u >> 1) - 1) & 1));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t va = slots + slot * X::kSlot, pa = p_s + (u & 1) * X::kP, d = o_col + (u & 1) * NP * C;
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k) {
+            const uint32_t vk = va + c * X::kPanelBytes + k * 32 * X::kRowB;
+            // heads of 64: the MMA's rows 64 .. 127 repeat whatever lies 512 bytes on, and nobody reads them
+            const uint64_t ad = D < 128 ? umma_desc(vk, 512, 512, 4) : umma_desc(vk, 1024, 1024, 2);
+            umma_f8(go, d + c * C, ad, umma_desc(pa + k * 512, 128, 2048, 0), id_o, k > 0);
+          }
+        umma_commit_if(go, o_full(u & 1));
+        umma_commit_if(go, empty(slot));
+      }
+    }
+    if (!ok && lane == 0) give_up();
+  } else if (warp < W_FOLD) {
+    // ---- softmax: thread = token of the tile; rows R grp .. R grp + R - 1 ----
     const int grp = warp >> 2, w4 = warp & 3, tt = tid & 127;
-    const uint32_t lane_col = ((uint32_t)(32 * w4) << 16) + 16 * grp;  // this group's columns: 8 first terms, 8 second
-    float acc[NP][R];
-#pragma unroll
-    for (int c = 0; c < NP; ++c)
-#pragma unroll
-      for (int i = 0; i < R; ++i) acc[c][i] = 0.f;
-    float m_run = -INFINITY, l_run = 0.f;  // lane i (< R) of every warp: row i of the group
-    uint32_t poison = 0;  // bit c R + i: row i of the last tile sees a NaN in column c of this thread
-    int4 pd = make_int4(0, 0, 0, 0), pe = pd;  // the last tile's descriptor
-    uint32_t n_grp = 0, n_all = 0;             // barrier phases
+    const uint32_t lane_col = ((uint32_t)(32 * w4) << 16) + 2 * R * grp;  // this group's columns: R first terms, R second
+    uint32_t n_grp = 0, n_all = 0;  // barrier phases
+    int seg = 0;
     bool ok = true;
     auto sync_group = [&]() {
       __syncwarp();
@@ -587,207 +641,231 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     };
 
     for (int t = 0;; ++t) {
-      const int ds = t % kDescs, par = t & 1;
-      if (!(ok = wait_warp(d_full(ds), (t / kDescs) & 1))) break;
+      const int ds = t % ND, par = t & 1, ring = t % kRing;
+      if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
       const Desc& de = descs[ds];
-      const int4 dd = *reinterpret_cast<const int4*>(&de.flags), dx = *reinterpret_cast<const int4*>(&de.base);
-      const int fl = dd.x;
-      uint32_t taint = 0;
-      if (!(fl & kEnd)) {
-        const int h = dd.y, j0 = dd.z, tile = dd.w, base_tok = dx.x, fresh = dx.y, c0 = dx.z;
-        const int toks = min(p.TQ, fresh - j0);
-        if (fl & kNewSeg) {
-          sync_all();  // nobody looks at the last segment's limits and factors any more
-          if (!ok) break;
-          // query rows as e4m3 terms: 16 threads a row
-          constexpr int CPT = (D / 8 + 15) / 16;
-          const int r = tid / 16, c = tid % 16;
-          const int j = r / p.G, g = r - j * p.G;
-          const bool live = j < toks;
-          uint4 v[CPT];
-          uint32_t peak = 0;
-#pragma unroll
-          for (int i = 0; i < CPT; ++i) {
-            v[i] = make_uint4(0, 0, 0, 0);
-            const int ch = c + i * 16;
-            if (live && ch < D / 8)
-              v[i] = ld_nc_v4(p.q + (int64_t)(c0 + j0 + j) * p.q_stride + (int64_t)(h * p.G + g) * D + 8 * ch);
-          }
-#pragma unroll
-          for (int i = 0; i < CPT; ++i)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t u = word_of(v[i], w) & 0x7FFF7FFFu;
-              peak = max(peak, max(u & 0xFFFF, u >> 16));
-            }
-#pragma unroll
-          for (int d = 8; d; d >>= 1) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, d));
-          // largest element into (224, 448]: 448 = 1.75 * 2^8
-          const int e = min(max((int)(peak >> 7) - 127 - 8 + ((peak & 127) > 96 ? 1 : 0), -120), 120);
-          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-          for (int i = 0; i < CPT; ++i) {
-            const int ch = c + i * 16;
-            if (ch < D / 8) {
-              float f[8];
-              widen8(v[i], f);
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int w = 0; w < 4; ++w) split2(__fmul_rn(f[2 * w], inv), __fmul_rn(f[2 * w + 1], inv), hi[w], lo[w]);
-              // K-major, 128-byte swizzle: row n = 16 (r / 8) + r % 8 (second terms 8 further) of panel ch / 16
-              const int n = (r / R) * 16 + r % R;
-              uint8_t* at = q_mem + (ch / 16) * 2 * RP * 128 + n * 128 + ((((ch % 16) >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8;
-              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-              *reinterpret_cast<uint2*>(at + 8 * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            }
-          }
-          if (c == 0) {
-            const float unit = __uint_as_float((uint32_t)(127 + e) << 23);
-            // a row with a NaN or an infinity is NaN as a whole
-            s_qf[r] = peak >= 0x7F80 ? __uint_as_float(0x7FC00000u) : __fmul_rn(unit, p.qk_scale);
-            const int pos = base_tok + j0 + j;
-            s_lim[r] = live ? make_int2(p.window > 0 ? pos - p.window + 1 : 0, pos) : make_int2(0, -1);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full);
-          sync_all();
-          if (!ok) break;
-        }
-        // token of this thread
-        const int tok = tile * kTile + tt, blk = tt >> p.shift;
-        const float ks = de.ks[blk];
-        const int pos0 = base_tok + j0, pos1 = pos0 + toks - 1;  // positions of the first and last row
-        const bool masked = tile * kTile + kTile - 1 > pos0 || (p.window > 0 && tile * kTile < pos1 - p.window + 1);
-        const bool fix = masked || (fl & kBadBlock);
-        const bool dead = ks == 0.f || tok > pos1 || (p.window > 0 && tok < pos0 - p.window + 1);
-        // the V scale is a power of two: its exponent, and its reciprocal
-        const int ve = dead ? 0 : (int)(__float_as_uint(de.vs[blk]) >> 23) - 127;
-        const float lv = (float)ve, iv = __uint_as_float((uint32_t)(127 - ve) << 23);
-        ok = wait_warp(s_full(par), (t >> 1) & 1);
+      const int fl = de.flags;
+      if (fl & kEnd) break;
+      if (fl & kNewSeg) {
+        const int j0 = de.j0, toks = min(p.TQ, de.fresh - j0);
+        sync_all();  // nobody looks at the last segment's limits and factors any more
+        ok &= wait_warp(st_full, seg++ & 1);
         if (!ok) break;
-        tc_fence_after_sync();
-        float s[R];
-        {
-          float raw[16];
-          tmem_ld16(s_col + par * 2 * RP + lane_col, raw);
-          tmem_wait_ld();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free(par));
+        // query rows as e4m3 terms: TPR threads a row
+        constexpr int TPR = 128 * NG / RP, CPT = (D / 8 + TPR - 1) / TPR;
+        const int row = tid / TPR, c = tid % TPR;
+        const int j = row / p.G;
+        const bool live = j < toks;
+        uint4 v[CPT];
+        uint32_t peak = 0;
 #pragma unroll
-          for (int i = 0; i < R; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(s_qf + R * grp + i);
-            const float ff[4] = {f.x, f.y, f.z, f.w};
+        for (int i = 0; i < CPT; ++i) {
+          v[i] = make_uint4(0, 0, 0, 0);
+          const int ch = c + i * TPR;
+          if (live && ch < D / 8) v[i] = *reinterpret_cast<const uint4*>(stage + row * (2 * D) + ch * 16);
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              s[i + k] = __fmaf_rn(__fmul_rn(__fmaf_rn(raw[R + i + k], 0.0625f, raw[i + k]), ff[k]), ks, lv);
+        for (int i = 0; i < CPT; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t u = word_of(v[i], w) & 0x7FFF7FFFu;
+            peak = max(peak, max(u & 0xFFFF, u >> 16));
+          }
+#pragma unroll
+        for (int d = TPR / 2; d; d >>= 1) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, d));
+        // largest element into (224, 448]: 448 = 1.75 * 2^8
+        const int e = min(max((int)(peak >> 7) - 127 - 8 + ((peak & 127) > 96 ? 1 : 0), -120), 120);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          const int ch = c + i * TPR;
+          if (ch < D / 8) {
+            float f[8];
+            widen8(v[i], f);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) split2(__fmul_rn(f[2 * w], inv), __fmul_rn(f[2 * w + 1], inv), hi[w], lo[w]);
+            // K-major, 128-byte swizzle: row n = 2 R (row / R) + row % R (second terms R further) of panel ch / 16
+            const int n = (row / R) * 2 * R + row % R;
+            auto at = [&](int m) {
+              return reinterpret_cast<uint2*>(q_mem + (ch / 16) * C * 128 + m * 128 + ((((ch % 16) >> 1) ^ (m & 7)) << 4) +
+                                              (ch & 1) * 8);
+            };
+            *at(n) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *at(n + R) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
           }
         }
-        if (fix) {
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
-            const int2 lim = s_lim[R * grp + i];
-            if (dead || tok < lim.x || tok > lim.y) s[i] = -INFINITY;
-          }
+        if (c == 0) {
+          const float unit = __uint_as_float((uint32_t)(127 + e) << 23);
+          // a row with a NaN or an infinity is NaN as a whole
+          s_qf[row] = peak >= 0x7F80 ? __uint_as_float(0x7FC00000u) : __fmul_rn(unit, p.qk_scale);
+          const int pos = de.base + j0 + j;
+          s_lim[row] = live ? make_int2(p.window > 0 ? pos - p.window + 1 : 0, pos) : make_int2(0, -1);
         }
-        float* sm = s_max + (t % kRing) * 4 * RP + R * grp;
-        {
-          float m[R];
-#pragma unroll
-          for (int i = 0; i < R; ++i) m[i] = warp_max(s[i]);
-          if (lane == 0) {
-            *reinterpret_cast<float4*>(sm + w4 * RP) = make_float4(m[0], m[1], m[2], m[3]);
-            *reinterpret_cast<float4*>(sm + w4 * RP + 4) = make_float4(m[4], m[5], m[6], m[7]);
-          }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(q_full);
+          mbar_arrive(st_free);
         }
-        if (fix) {
-          // V rows that no row sees (stale shared memory, unset blocks) become
-          // zeros; NaN codes that only some rows see are taken out of V and
-          // put into those rows' results
-          uint8_t* v_row = base + ((2 * t + 1) % NS) * X::kSlot;
-          constexpr int kRowB = X::kRowB, kCh = kRowB / 16;
-          ok = wait_warp(full((2 * t + 1) % NS), ((2 * t + 1) / NS) & 1);
-          if (!ok) break;
-          bool nan_code = false;
-          const bool partly = toks > 1 && !dead && (tok > pos0 || (p.window > 0 && tok < pos1 - p.window + 1));
-          if (grp == 0 && (dead || partly)) {
-#pragma unroll
-            for (int c = 0; c < NP; ++c)
-#pragma unroll
-              for (int i = 0; i < kCh; ++i) {
-                uint4* w = reinterpret_cast<uint4*>(v_row + c * X::kPanelBytes + tt * kRowB + ((i + tt) % kCh) * 16);
-                if (dead) {
-                  *w = make_uint4(0, 0, 0, 0);
-                } else {
-                  const uint4 u = *w;
-                  const uint32_t any = (((u.x & 0x7F7F7F7Fu) + 0x01010101u) | ((u.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                                        ((u.z & 0x7F7F7F7Fu) + 0x01010101u) | ((u.w & 0x7F7F7F7Fu) + 0x01010101u)) &
-                                       0x80808080u;
-                  nan_code |= any != 0;
-                }
-              }
-          }
-          if (masked && toks > 1) {
-            if (nan_code) s_nan[par] = t + 1;
-            sync_all();
-            if (!ok) break;
-            if (s_nan[par] == t + 1) {
-              // (rare) which tokens hold NaN in this thread's columns, which rows see one
-#pragma unroll 1
-              for (int c = 0; c < NP; ++c) {
-                uint32_t hit[4] = {0, 0, 0, 0};
-                if (tt < kRowB)
-                  for (int k = 0; k < kTile; ++k) {
-                    const int sw = D < 128 ? (k >> 1) & 3 : k & 7;
-                    const uint8_t code = v_row[c * X::kPanelBytes + k * kRowB + (((tt >> 4) ^ sw) << 4) + (tt & 15)];
-                    if ((code & 0x7F) == 0x7F) hit[k >> 5] |= 1u << (k & 31);
-                  }
-                for (int i = 0; i < R; ++i) {
-                  const int2 lim = s_lim[R * grp + i];
-                  bool sees = false;
-                  for (int k = max(0, lim.x - tile * kTile); k < kTile && k <= lim.y - tile * kTile; ++k)
-                    sees |= (hit[k >> 5] >> (k & 31)) & 1;
-                  if (sees) taint |= 1u << (c * R + i);
-                }
-              }
-              sync_all();
-              if (!ok) break;
-              if (nan_code) {
-#pragma unroll 1
-                for (int c = 0; c < NP; ++c)
-                  for (int i = 0; i < kRowB; ++i) {
-                    uint8_t& code = v_row[c * X::kPanelBytes + tt * kRowB + i];
-                    if ((code & 0x7F) == 0x7F) code = 0;
-                  }
-              }
-            }
-          }
-        }
-        sync_group();
+        sync_all();
         if (!ok) break;
-        // weights times 256 (sums and O carry the factor, their quotient does not), and their two terms
-        uint32_t hi[R / 2], lo[R / 2];
+      }
+      // the V scale is a power of two: its exponent, and its reciprocal
+      const int blk = tt >> p.shift;
+      const float ks = de.ks[blk];
+      int ve = (int)(__float_as_uint(de.vs[blk]) >> 23) - 127;
+      // (the weights' buffer is free once O of tile t - 2 is done)
+      ok = (t < 2 || wait_warp(o_full(par), ((t >> 1) - 1) & 1)) && wait_warp(s_full(par), (t >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after_sync();
+      float s[R];
+      {
+        float raw[2 * R];
+        tmem_ld<2 * R>(s_col + par * C + lane_col, raw);
+        tmem_wait_ld();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free(par));
 #pragma unroll
         for (int i = 0; i < R; i += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(sm + i), b = *reinterpret_cast<const float4*>(sm + RP + i);
-          const float4 c = *reinterpret_cast<const float4*>(sm + 2 * RP + i), d = *reinterpret_cast<const float4*>(sm + 3 * RP + i);
-          const float mx[4] = {fmaxf(fmaxf(a.x, b.x), fmaxf(c.x, d.x)), fmaxf(fmaxf(a.y, b.y), fmaxf(c.y, d.y)),
-                               fmaxf(fmaxf(a.z, b.z), fmaxf(c.z, d.z)), fmaxf(fmaxf(a.w, b.w), fmaxf(c.w, d.w))};
+          const float4 f = *reinterpret_cast<const float4*>(s_qf + R * grp + i);
+          const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[i + k] = ex2(s[i + k] - (mx[k] == -INFINITY ? 0.f : mx[k] - 8.f));
+          for (int k = 0; k < 4; ++k) s[i + k] = __fmul_rn(__fmaf_rn(raw[R + i + k], 0.0625f, raw[i + k]), ff[k]);
         }
+      }
+      if (fl & kFix) {
+        // scores that a row does not see; V rows that no row sees (stale shared
+        // memory, unset blocks) become zeros; NaN codes that only some rows see
+        // are taken out of V and put into those rows' results
+        const int tile = de.tile, tok = tile * kTile + tt;
+        const int j0 = de.j0, toks = min(p.TQ, de.fresh - j0), pos0 = de.base + j0, pos1 = pos0 + toks - 1;
+        const bool dead = ks == 0.f || tok > pos1 || (p.window > 0 && tok < pos0 - p.window + 1);
+        if (dead) ve = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int2 lim = s_lim[R * grp + i];
+          s[i] = dead || tok < lim.x || tok > lim.y ? -INFINITY : __fmaf_rn(s[i], ks, (float)ve);
+        }
+        uint8_t* v_row = base + ((2 * t + 1) % NS) * X::kSlot;
+        constexpr int kRowB = X::kRowB, kCh = kRowB / 16;
+        ok = wait_warp(full((2 * t + 1) % NS), ((2 * t + 1) / NS) & 1);
+        if (!ok) break;
+        bool nan_code = false;
+        const bool partly = toks > 1 && !dead && (tok > pos0 || (p.window > 0 && tok < pos1 - p.window + 1));
+        if (grp == 0 && (dead || partly)) {
+#pragma unroll
+          for (int c = 0; c < NP; ++c)
+#pragma unroll
+            for (int i = 0; i < kCh; ++i) {
+              uint4* w = reinterpret_cast<uint4*>(v_row + c * X::kPanelBytes + tt * kRowB + ((i + tt) % kCh) * 16);
+              if (dead) {
+                *w = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 u = *w;
+                const uint32_t any = (((u.x & 0x7F7F7F7Fu) + 0x01010101u) | ((u.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                                      ((u.z & 0x7F7F7F7Fu) + 0x01010101u) | ((u.w & 0x7F7F7F7Fu) + 0x01010101u)) &
+                                     0x80808080u;
+                nan_code |= any != 0;
+              }
+            }
+        }
+        if (toks > 1) {
+          if (nan_code) s_nan[ring] = t + 1;
+          sync_all();
+          if (!ok) break;
+          if (s_nan[ring] == t + 1) {
+            // (rare) which tokens hold NaN in this thread's columns, which rows see one
+            uint32_t taint = 0;
+#pragma unroll 1
+            for (int c = 0; c < NP; ++c) {
+              uint32_t hit[4] = {0, 0, 0, 0};
+              if (tt < kRowB)
+                for (int k = 0; k < kTile; ++k) {
+                  const int sw = D < 128 ? (k >> 1) & 3 : k & 7;
+                  const uint8_t code = v_row[c * X::kPanelBytes + k * kRowB + (((tt >> 4) ^ sw) << 4) + (tt & 15)];
+                  if ((code & 0x7F) == 0x7F) hit[k >> 5] |= 1u << (k & 31);
+                }
+              for (int i = 0; i < R; ++i) {
+                const int2 lim = s_lim[R * grp + i];
+                bool sees = false;
+                for (int k = max(0, lim.x - tile * kTile); k < kTile && k <= lim.y - tile * kTile; ++k)
+                  sees |= (hit[k >> 5] >> (k & 31)) & 1;
+                if (sees) taint |= 1u << (c * R + i);
+              }
+            }
+            s_taint[ring * 128 * NG + tid] = (typename X::Marks)taint;
+            sync_all();
+            if (!ok) break;
+            if (nan_code) {
+#pragma unroll 1
+              for (int c = 0; c < NP; ++c)
+                for (int i = 0; i < kRowB; ++i) {
+                  uint8_t& code = v_row[c * X::kPanelBytes + tt * kRowB + i];
+                  if ((code & 0x7F) == 0x7F) code = 0;
+                }
+            }
+          }
+        }
+      } else {
+        const float lv = (float)ve;
+#pragma unroll
+        for (int i = 0; i < R; ++i) s[i] = __fmaf_rn(s[i], ks, lv);
+      }
+      // maxima over the tile: the warp, then the group's four
+      float* sm = s_max + par * 4 * RP + R * grp;
+      {
+        float m[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) m[i] = warp_max(s[i]);
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < R; i += 4)
+            *reinterpret_cast<float4*>(sm + w4 * RP + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+        }
+      }
+      sync_group();
+      if (!ok) break;
+      float top;
+      {
+        const float* a = sm + lane % R;
+        top = fmaxf(fmaxf(a[0], a[RP]), fmaxf(a[2 * RP], a[3 * RP]));
+        if (w4 == 0 && lane < R) s_top[ring * RP + R * grp + lane] = top;
+        top = top == -INFINITY ? 0.f : __fsub_rn(top, 8.f);
+      }
+      // weights times 256 (sums and O carry the factor, their quotient does not), and their two terms
+#pragma unroll
+      for (int i = 0; i < R; ++i) s[i] = ex2(__fsub_rn(s[i], __shfl_sync(0xffffffffu, top, i)));
+      {
+        uint32_t hi[R / 2], lo[R / 2], w[R / 2];
 #pragma unroll
         for (int i = 0; i < R; i += 2) split2h(s[i], s[i + 1], hi[i / 2], lo[i / 2]);
-        // row 16 grp + (0 .. 7 first terms, 8 .. 15 second) of the weights: 16 bytes a token
-        *reinterpret_cast<uint4*>(p_mem + par * X::kP + grp * 2048 + tt * 16) =
-            make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-        fence_proxy_async();
-        // row sums of p / vs over the warp: halves exchanged, lane 4 i ends with row i's
 #pragma unroll
-        for (int i = 0; i < R; ++i) s[i] = __fmul_rn(s[i], iv);
+        for (int i = 0; i < R / 4; ++i) {
+          w[i] = hi[2 * i] | hi[2 * i + 1] << 16;
+          w[R / 4 + i] = lo[2 * i] | lo[2 * i + 1] << 16;
+        }
+        // column 2 R grp + (R first terms, R second) of the weights: 16 columns a 16-byte row of a token, 2048 bytes on
+        // the next 16
+        uint8_t* dst = p_mem + par * X::kP + (2 * R * grp / 16) * 2048 + tt * 16;
+        if (R == 4) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], 0, 0);
+        } else {
 #pragma unroll
-        for (int n = R / 2, off = 16; n; n >>= 1, off >>= 1) {
+          for (int i = 0; i < R / 8; ++i)
+            *reinterpret_cast<uint4*>(dst + i * 2048) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      }
+      fence_proxy_async();
+      // row sums of p / vs over the warp: halves exchanged until a lane has one row, then added (one tree for every R)
+      const float iv = __uint_as_float((uint32_t)(127 - ve) << 23);
+#pragma unroll
+      for (int i = 0; i < R; ++i) s[i] = __fmul_rn(s[i], iv);
+      {
+        int off = 16;
+#pragma unroll
+        for (int n = R / 2; n; n >>= 1, off >>= 1) {
           const bool up = lane & off;
 #pragma unroll
           for (int i = 0; i < n; ++i) {
@@ -795,105 +873,113 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
             s[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, off));
           }
         }
-        s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], 2));
-        s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], 1));
-        if (lane % 4 == 0) s_sum[((t % kRing) * 4 + w4) * RP + R * grp + lane / 4] = s[0];
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(p_full(par));
-          mbar_arrive(d_free(ds));
-        }
-      } else if (t > 0) {
-        sync_group();  // the last tile's sums are written
-        if (!ok) break;
+#pragma unroll
+        for (; off; off >>= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], off));
+        constexpr int kRep = 32 / R;  // lanes with the same row
+        if (lane % kRep == 0) s_sum[(ring * 4 + w4) * RP + R * grp + lane / kRep] = s[0];
       }
-
-      if (t > 0) {
-        // ---- O of tile t - 1: into the accumulators, or out to the workspace ----
-        const int pf = pd.x, u = t - 1;
-        float mt = -INFINITY, lt = 0.f;
-        if (lane < R) {
-          const float* a = s_max + (u % kRing) * 4 * RP + R * grp + lane;
-          const float* b = s_sum + (u % kRing) * 4 * RP + R * grp + lane;
-          mt = fmaxf(fmaxf(a[0], a[RP]), fmaxf(a[2 * RP], a[3 * RP]));
-          lt = __fadd_rn(__fadd_rn(b[0], b[RP]), __fadd_rn(b[2 * RP], b[3 * RP]));
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(p_full(ring));
+        mbar_arrive(d_free(ds));
+      }
+    }
+    if (!ok && lane == 0) give_up();
+  } else {
+    // ---- fold: thread = output column; O of tile t into the accumulators, or out to the workspace ----
+    const int fw = warp - W_FOLD, grp = fw >> 2, w4 = fw & 3, tt = 32 * w4 + lane;
+    const uint32_t lane_col = ((uint32_t)(32 * w4) << 16) + 2 * R * grp;
+    const bool live = D >= 128 || tt < D;
+    float acc[NP][R];
+    float m_run = -INFINITY, l_run = 0.f;  // lane i (< R) of every warp: row i of the group
+    bool ok = true;
+    for (int t = 0;; ++t) {
+      const int ds = t % ND, par = t & 1, ring = t % kRing;
+      if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
+      const Desc& de = descs[ds];
+      const int fl = de.flags;
+      if (fl & kEnd) break;
+      if (!(ok = wait_warp(p_full(ring), (t / kRing) & 1))) break;
+      float mt = -INFINITY, lt = 0.f;
+      if (lane < R) {
+        const float* a = s_sum + ring * 4 * RP + R * grp + lane;
+        mt = s_top[ring * RP + R * grp + lane];
+        lt = __fadd_rn(__fadd_rn(a[0], a[RP]), __fadd_rn(a[2 * RP], a[3 * RP]));
+      }
+      const bool part = fl & kPart;
+      if (fl & kGroupBegin) {
+        m_run = -INFINITY;
+        l_run = 0.f;
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+#pragma unroll
+          for (int i = 0; i < R; ++i) acc[c][i] = 0.f;
+      }
+      if (!part) {
+        float al, be;
+        fold_ml(m_run, l_run, mt, lt, al, be);
+        if (lane < R) s_ab[w4 * RP + R * grp + lane] = make_float2(al, be);
+        __syncwarp();
+      }
+      if (!(ok = wait_warp(o_full(par), (t >> 1) & 1))) break;
+      tc_fence_after_sync();
+      const uint32_t poison = s_nan[ring] == t + 1 ? s_taint[ring * 128 * NG + 128 * grp + tt] : 0;
+#pragma unroll
+      for (int c = 0; c < NP; ++c) {
+        float raw[2 * R];
+        tmem_ld<2 * R>(o_col + (par * NP + c) * C + lane_col, raw);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < R; ++i) raw[i] = __fmaf_rn(raw[R + i], 0.0625f, raw[i]);
+        if (poison) {
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+            if ((poison >> (c * R + i)) & 1) raw[i] = __uint_as_float(0x7FC00000u);
         }
-        const bool part = pf & kPart;
-        if (pf & kGroupBegin) {
-          m_run = -INFINITY;
-          l_run = 0.f;
-#pragma unroll
-          for (int c = 0; c < NP; ++c)
-#pragma unroll
-            for (int i = 0; i < R; ++i) acc[c][i] = 0.f;
-        }
-        if (!part) {
-          float al, be;
-          fold_ml(m_run, l_run, mt, lt, al, be);
-          if (lane < R) s_ab[w4 * RP + R * grp + lane] = make_float2(al, be);
-          __syncwarp();
-        }
-        const int rows = min(p.TQ, pe.y - pd.z) * p.G - R * grp;  // of this group
-        ok = wait_warp(o_full, u & 1);
-        if (!ok) break;
-        tc_fence_after_sync();
-        const int part_slot = (blockIdx.x * 2 + (pf & kTail ? 1 : 0)) * kGroupTiles + pd.w % kGroupTiles;
-#pragma unroll
-        for (int c = 0; c < NP; ++c) {
-          float raw[16];
-          tmem_ld16(o_col + c * 2 * RP + lane_col, raw);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < R; ++i) raw[i] = __fmaf_rn(raw[R + i], 0.0625f, raw[i]);
-          if (poison) {
+        if (part) {
+          const int rows = min(p.TQ, de.fresh - de.j0) * p.G - R * grp;
+          float* dst = p.t_acc + ((int64_t)de.at * RP + R * grp) * D + c * 128 + tt;
+          if (live) {
 #pragma unroll
             for (int i = 0; i < R; ++i)
-              if ((poison >> (c * R + i)) & 1) raw[i] = __uint_as_float(0x7FC00000u);
+              if (i < rows) dst[i * D] = raw[i];
           }
-          if (part) {
-            float* dst = p.t_acc + ((int64_t)part_slot * RP + R * grp) * D + c * 128 + tt;
-            if (D >= 128 || tt < D) {
+        } else {
 #pragma unroll
-              for (int i = 0; i < R; ++i)
-                if (i < rows) dst[i * D] = raw[i];
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < R; i += 2) {
-              const float4 ab = *reinterpret_cast<const float4*>(s_ab + w4 * RP + R * grp + i);
-              acc[c][i] = __fmaf_rn(acc[c][i], ab.x, __fmul_rn(raw[i], ab.y));
-              acc[c][i + 1] = __fmaf_rn(acc[c][i + 1], ab.z, __fmul_rn(raw[i + 1], ab.w));
-            }
+          for (int i = 0; i < R; i += 2) {
+            const float4 ab = *reinterpret_cast<const float4*>(s_ab + w4 * RP + R * grp + i);
+            acc[c][i] = __fmaf_rn(acc[c][i], ab.x, __fmul_rn(raw[i], ab.y));
+            acc[c][i + 1] = __fmaf_rn(acc[c][i + 1], ab.z, __fmul_rn(raw[i + 1], ab.w));
           }
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_free);
-        if (part) {
-          if (w4 == 0 && lane < R && lane < rows) p.t_ml[(int64_t)part_slot * RP + R * grp + lane] = make_float2(mt, lt);
-        } else if (pf & kGroupEnd) {
-          const int64_t row0 = ((int64_t)pe.w * p.T + pe.z + pd.z) * p.q_heads + pd.y * p.G;
-          int j = R * grp / p.G, g = R * grp - j * p.G;
-          const int jl = (R * grp + lane) / p.G, gl = R * grp + lane - jl * p.G;
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
-            if (i < rows && (D >= 128 || tt < D)) {
-              float* dst = p.g_acc + (row0 + (int64_t)j * p.q_heads + g) * D + tt;
-#pragma unroll
-              for (int c = 0; c < NP; ++c) dst[c * 128] = acc[c][i];
-            }
-            if (++g == p.G) {
-              g = 0;
-              ++j;
-            }
-          }
-          if (w4 == 0 && lane < R && lane < rows) p.g_ml[row0 + (int64_t)jl * p.q_heads + gl] = make_float2(m_run, l_run);
         }
       }
-      if (fl & kEnd) break;
-      pd = dd;
-      pe = dx;
-      poison = taint;
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free(par));
+      if (part) {
+        const int rows = min(p.TQ, de.fresh - de.j0) * p.G - R * grp;
+        if (w4 == 0 && lane < R && lane < rows) p.t_ml[(int64_t)de.at * RP + R * grp + lane] = make_float2(mt, lt);
+      } else if (fl & kGroupEnd) {
+        const int rows = min(p.TQ, de.fresh - de.j0) * p.G - R * grp;
+        const int64_t row0 = ((int64_t)de.at * p.T + de.c0 + de.j0) * p.q_heads + de.h * p.G;
+        int j = R * grp / p.G, g = R * grp - j * p.G;
+        const int jl = (R * grp + lane) / p.G, gl = R * grp + lane - jl * p.G;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if (i < rows && live) {
+            float* dst = p.g_acc + (row0 + (int64_t)j * p.q_heads + g) * D + tt;
+#pragma unroll
+            for (int c = 0; c < NP; ++c) dst[c * 128] = acc[c][i];
+          }
+          if (++g == p.G) {
+            g = 0;
+            ++j;
+          }
+        }
+        if (w4 == 0 && lane < R && lane < rows) p.g_ml[row0 + (int64_t)jl * p.q_heads + gl] = make_float2(m_run, l_run);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(d_free(ds));
     }
     if (!ok && lane == 0) give_up();
   }
@@ -901,12 +987,9 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   // ---- teardown: copies and MMAs in flight land before memory is released ----
   __syncthreads();
   if (*s_abort) {
-    if (warp == W_LOAD) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (lane == 0)
-        for (int i = max(0, loads - NS); i < loads; ++i) mbar_wait_parked(full(i % NS), (i / NS) & 1);
-    }
-    if (warp == W_MMA && lane == 0) {  // one more commit covers every MMA issued
+    if (warp == W_LOAD && lane == 0)
+      for (int i = max(0, loads - NS); i < loads; ++i) mbar_wait_parked(full(i % NS), (i / NS) & 1);
+    if (warp == W_MMA && elect_one()) {  // one more commit covers every MMA that this thread issued
       umma_commit(drained);
       mbar_wait_parked(drained, 0);
     }
@@ -963,7 +1046,7 @@ __device__ __forceinline__ int find_request(const Params& p, int t) {
   return lo;
 }
 
-template <int D, int RP, int SETS>
+template <int D, int SETS>
 __global__ void __launch_bounds__(SETS == 32 ? 1024 : 256) kv_combine_kernel(const __grid_constant__ Params p) {
   constexpr int kCols = D < 128 ? D : 128;          // columns of a CTA's thread set (SETS > 1)
   constexpr int kLanes = (SETS == 1 ? D : kCols) / 4;
@@ -1022,8 +1105,7 @@ __global__ void __launch_bounds__(SETS == 32 ? 1024 : 256) kv_combine_kernel(con
             ++own;
             end = cut.begin(own + 1) - xa;
           }
-          // at the owner's end where the group began in its range, else at its beginning
-          const int64_t at = (int64_t)((own * 2 + (own == o ? 1 : 0)) * kGroupTiles + (ta + k) % kGroupTiles) * RP + rr;
+          const int64_t at = (int64_t)cut.slot(own, xa + k, own == o, p.t_slots) * p.RP + rr;
           ml[k] = p.t_ml[at];
           a[k] = *reinterpret_cast<const float4*>(p.t_acc + at * D + col);
         }
@@ -1078,14 +1160,14 @@ __global__ void __launch_bounds__(SETS == 32 ? 1024 : 256) kv_combine_kernel(con
 // ---- host side -----------------------------------------------------------------------------------
 
 struct Layout {
-  int RP, TQ, gmax, grid;
+  int RP, TQ, gmax, grid, t_slots;
   bool fits;  // positions on the line and rows of group results fit in 31 bits
   size_t starts, g_acc, g_ml, t_acc, t_ml, bytes;
 };
 
 template <int D>
 int ctas_d(int RP) {
-  return RP == 8 ? Geo<D, 8>::kCtas : RP == 16 ? Geo<D, 16>::kCtas : Geo<D, 32>::kCtas;
+  return RP == 4 ? Geo<D, 4>::kCtas : RP == 8 ? Geo<D, 8>::kCtas : RP == 16 ? Geo<D, 16>::kCtas : Geo<D, 32>::kCtas;
 }
 int ctas_per_sm(int dim, int RP) { return dim == 64 ? ctas_d<64>(RP) : dim == 128 ? ctas_d<128>(RP) : ctas_d<256>(RP); }
 
@@ -1094,8 +1176,8 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   const int G = q_heads / heads;
   if (max_new > T) max_new = T;
   const int64_t rows = (int64_t)G * max_new;
-  y.RP = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  if (y.RP < G) y.RP = G <= 16 ? 16 : 32;
+  y.RP = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  while (y.RP < G) y.RP *= 2;
   y.TQ = y.RP / G;
   int64_t groups = ((int64_t)max_len + kGroupTokens - 1) / kGroupTokens;
   if (window > 0) {
@@ -1112,18 +1194,20 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   y.fits = most <= INT32_MAX && (int64_t)y.gmax * T * q_heads <= INT32_MAX;
   const int full = kSms * ctas_per_sm(dim, y.RP);
   y.grid = most < full ? (int)most : full;
+  const int64_t range = (most + y.grid - 1) / y.grid;
+  y.t_slots = (int)(range < 2 * (kGroupTiles - 1) ? range : 2 * (kGroupTiles - 1));
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   y.starts = 0;
   y.g_acc = up(4 * ((size_t)B + 1));
   y.g_ml = y.g_acc + up((size_t)y.gmax * T * q_heads * dim * 4);
   y.t_acc = y.g_ml + up((size_t)y.gmax * T * q_heads * 8);
-  y.t_ml = y.t_acc + up((size_t)y.grid * 2 * kGroupTiles * y.RP * dim * 4);
-  y.bytes = y.t_ml + up((size_t)y.grid * 2 * kGroupTiles * y.RP * 8);
+  y.t_ml = y.t_acc + up((size_t)y.grid * y.t_slots * y.RP * dim * 4);
+  y.bytes = y.t_ml + up((size_t)y.grid * y.t_slots * y.RP * 8);
   return y;
 }
 
 std::mutex g_attr_mu;
-bool g_attr[64][9] = {};
+bool g_attr[64][12] = {};
 
 template <int D, int RP>
 cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int pdl, cudaStream_t s) {
@@ -1133,7 +1217,7 @@ cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int 
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   {
     std::lock_guard<std::mutex> lk(g_attr_mu);
-    bool& done = g_attr[dev][(D == 64 ? 0 : D == 128 ? 3 : 6) + (RP == 8 ? 0 : RP == 16 ? 1 : 2)];
+    bool& done = g_attr[dev][(D == 64 ? 0 : D == 128 ? 4 : 8) + (RP == 4 ? 0 : RP == 8 ? 1 : RP == 16 ? 2 : 3)];
     if (!done) {
       if (cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, X::kSmem))
         return e;
@@ -1165,21 +1249,22 @@ cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int 
     constexpr int kRowsPer = 256 / (D / 4);
     cfg.gridDim = dim3((unsigned)((out_rows + kRowsPer - 1) / kRowsPer));
     cfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, RP, 1>, p);
+    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 1>, p);
   }
   constexpr int kCols = D < 128 ? D : 128;
   cfg.gridDim = dim3((unsigned)out_rows, D / kCols);
   if (out_rows * (D / kCols) >= kSms) {
     cfg.blockDim = dim3(8 * kCols / 4);
-    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, RP, 8>, p);
+    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 8>, p);
   }
   cfg.blockDim = dim3(32 * kCols / 4);
-  return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, RP, 32>, p);
+  return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 32>, p);
 }
 
 template <int D>
 cudaError_t run_d(const KvAttentionArgs& a, const Layout& y, const Params& p, int pdl, cudaStream_t s) {
   switch (y.RP) {
+    case 4: return run<D, 4>(a, y, p, pdl, s);
     case 8: return run<D, 8>(a, y, p, pdl, s);
     case 16: return run<D, 16>(a, y, p, pdl, s);
     default: return run<D, 32>(a, y, p, pdl, s);
@@ -1220,6 +1305,8 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t 
   p.qk_scale = a.scale * kLog2e;
   p.gmax = y.gmax;
   p.grid = y.grid;
+  p.RP = y.RP;
+  p.t_slots = y.t_slots;
   p.starts = reinterpret_cast<int*>(w + y.starts);
   p.g_acc = reinterpret_cast<float*>(w + y.g_acc);
   p.g_ml = reinterpret_cast<float2*>(w + y.g_ml);

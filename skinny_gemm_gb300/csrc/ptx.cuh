@@ -300,12 +300,29 @@ __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int m, int n, bool a_mn, 
          ((uint32_t)(m >> 4) << 24);
 }
 
-// The 8-bit form of umma_bf16 (32 elements of K per instruction).
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+// One thread of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e;
+}
+
+// The 8-bit form of umma_bf16 (32 elements of K per instruction), executed by
+// the whole warp and issued by the thread with `go`: the warp stays converged,
+// so the descriptors stay in uniform registers (39 cycles an instruction
+// against 61 from a one-lane branch).
+__device__ __forceinline__ void umma_f8(uint32_t go, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        bool accumulate) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }"
-      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t go, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(go)
       : "memory");
 }
 

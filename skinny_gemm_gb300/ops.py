@@ -15,6 +15,7 @@ projections: ``kv_plan``, ``kv_append`` and ``kv_attention`` over a ``KVCache``
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import threading
 from dataclasses import dataclass
@@ -150,6 +151,13 @@ def _raise(rc: int) -> None:
 def _stream_ptr(stream) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(s.cuda_stream)
+
+
+def _raw_stream(stream) -> int:
+    """_stream_ptr without a Stream object for the common case (the current stream)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _dev_tensor(t: torch.Tensor, dtype: torch.dtype, name: str) -> torch.Tensor:
@@ -569,7 +577,7 @@ def stq1_get_plan(N: int, K: int) -> dict:
 KV_BLOCKS, KV_DIMS, KV_MAX_GROUP = (16, 32, 64, 128), (64, 128, 256), 32
 
 
-@dataclass
+@dataclass(frozen=True)
 class KVCache:
     """Keys and values of one layer: e4m3 codes ``k``, ``v`` (torch.float8_e4m3fn
     [blocks, heads, block, dim]) with one power-of-two scale per (block, head)
@@ -586,7 +594,8 @@ class KVCache:
             t = _dev_tensor(getattr(self, name), torch.float8_e4m3fn, name)
             if t.dim() != 4 or t.shape != self.k.shape:
                 raise ValueError(f"{name} must be [blocks, heads, block, dim] (got {tuple(t.shape)})")
-        self.blocks, self.heads, self.block, self.dim = self.k.shape
+        for name, n in zip(("blocks", "heads", "block", "dim"), self.k.shape):
+            object.__setattr__(self, name, n)
         if self.block not in KV_BLOCKS or self.dim not in KV_DIMS:
             raise ValueError(f"block {self.block} must be one of {KV_BLOCKS}, dim {self.dim} one of {KV_DIMS}")
         for name in ("k_scale", "v_scale"):
@@ -595,9 +604,10 @@ class KVCache:
                 raise ValueError(f"{name} must be [blocks, heads] (got {tuple(t.shape)})")
         if any(t.device != self.k.device for t in (self.v, self.k_scale, self.v_scale)):
             raise ValueError("the cache's tensors must be on one device")
-        self._c = KvCacheStruct(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                                self.blocks, self.heads, self.block, self.dim)
-        self._ptr = ctypes.addressof(self._c)
+        c = KvCacheStruct(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                          self.blocks, self.heads, self.block, self.dim)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ptr", ctypes.addressof(c))
 
     @classmethod
     def empty(cls, blocks: int, heads: int, block: int, dim: int, device="cuda") -> "KVCache":
@@ -624,12 +634,13 @@ class KVPlan:
 
     @classmethod
     def empty(cls, B: int, T: int, device="cuda") -> "KVPlan":
-        return cls(*torch.empty(2 * B + 2 * T + 2, dtype=torch.int32, device=device).split((B + 1, B, T, T, 1)))
+        flat = torch.empty(2 * B + 2 * T + 2, dtype=torch.int32, device=device)
+        return cls(*torch.unsafe_split_with_sizes(flat, (B + 1, B, T, T, 1)))  # (whole numbers: nothing to differentiate)
 
 
 def _i32(t: torch.Tensor, name: str, n: int | None = None) -> int:
     """The address of a contiguous int32 CUDA tensor of n elements (None: any)."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32 and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda and t.is_contiguous()):
         _dev_tensor(t, torch.int32, name)
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} must have {n} elements (got {t.numel()})")
@@ -639,14 +650,15 @@ def _i32(t: torch.Tensor, name: str, n: int | None = None) -> int:
 def _kv_rows(t: torch.Tensor, name: str, heads: int, dim: int) -> int:
     """The token stride of a bf16 CUDA tensor [T, heads, dim] whose rows are dense
     (the tokens may be further apart: columns of a fused projection)."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda):
         raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [T, {heads}, {dim}] (got {tuple(t.shape)})")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}] (got {tuple(shape)})")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != dim and heads > 1):
         raise ValueError(f"{name}: each token's heads * dim values must be contiguous")
-    return s0 if t.shape[0] > 1 else heads * dim
+    return s0 if shape[0] > 1 else heads * dim
 
 
 def kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: torch.Tensor, T: int, block: int,
@@ -658,17 +670,26 @@ def kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: 
     place; free: int32 block ids to take from, beginning at entry ``head``
     (int32 [1] on the device; None is 0; the plan's ``head`` is the next one).
     T rows: the sum of ``new``, or more (the rest get slot -1)."""
+    tp = _i32(table, "table")
     if table.dim() != 2:
         raise ValueError("table must be [B, max_blocks]")
     B, max_blocks = table.shape
     if out is None:
+        if T < 0:
+            raise ValueError("T must not be negative")
         out = KVPlan.empty(B, T, table.device)
-    rc = lib().w4a16_kv_plan(
-        _i32(cached, "cached", B), _i32(new, "new", B), _i32(table, "table"), _i32(free, "free"),
-        None if head is None else _i32(head, "head", 1), _i32(out.cu, "cu", B + 1), _i32(out.lens, "lens", B),
-        _i32(out.slots, "slots", T), _i32(out.positions, "positions", T), _i32(out.head, "head_out", 1),
-        B, T, block, max_blocks, free.numel(), _stream_ptr(stream))
-    _raise(rc)
+        cu = out.cu.data_ptr()  # the arrays lie one after another
+        lens = cu + 4 * (B + 1)
+        slots = lens + 4 * B
+        outs = (cu, lens, slots, slots + 4 * T, slots + 8 * T)
+    else:
+        outs = (_i32(out.cu, "cu", B + 1), _i32(out.lens, "lens", B), _i32(out.slots, "slots", T),
+                _i32(out.positions, "positions", T), _i32(out.head, "head_out", 1))
+    rc = lib().w4a16_kv_plan(_i32(cached, "cached", B), _i32(new, "new", B), tp, _i32(free, "free"),
+                             None if head is None else _i32(head, "head", 1), *outs, B, T, block, max_blocks,
+                             free.numel(), _raw_stream(stream))
+    if rc:
+        _raise(rc)
     return out
 
 
@@ -679,13 +700,20 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Ten
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError("k and v must have the same number of tokens")
-    _raise(lib().w4a16_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _i32(slots, "slots", T), cache._ptr, T,
-                                 _stream_ptr(stream)))
+    rc = lib().w4a16_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _i32(slots, "slots", T), cache._ptr, T,
+                               _raw_stream(stream))
+    if rc:
+        _raise(rc)
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv_attention_bytes(*sizes: int) -> int:
+    return int(lib().w4a16_kv_attention_workspace_bytes(*sizes))
 
 
 def kv_attention_workspace_bytes(B: int, T: int, q_heads: int, cache: KVCache, max_new: int, max_len: int,
                                  window: int = 0) -> int:
-    return int(lib().w4a16_kv_attention_workspace_bytes(B, T, q_heads, cache.heads, cache.dim, max_new, max_len, window))
+    return _kv_attention_bytes(B, T, q_heads, cache.heads, cache.dim, max_new, max_len, window)
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
@@ -702,26 +730,31 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
         raise ValueError("q must be [T, q_heads, dim]")
     T, hq, dim = q.shape
     qs = _kv_rows(q, "q", hq, cache.dim)
+    tp = _i32(table, "table")
     if table.dim() != 2:
         raise ValueError("table must be [B, max_blocks]")
     B, max_blocks = table.shape
+    dev = q.device
     if out is None:
-        out = torch.empty(T, hq, dim, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, hq, dim), dtype=torch.bfloat16, device=dev)
     else:
         _dev_tensor(out, torch.bfloat16, "out")
         if out.shape != q.shape:
             raise ValueError(f"out must be {tuple(q.shape)}")
-    L = lib()
-    n = L.w4a16_kv_attention_workspace_bytes(B, T, hq, cache.heads, dim, max_new, max_len, window)
-    if workspace is None and n:
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-        if stream is not None and stream != torch.cuda.current_stream():
-            workspace.record_stream(stream)
-    wp, wn = _ws_args(workspace)
-    rc = L.w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, _i32(table, "table"), _i32(cu, "cu", B + 1),
-                              _i32(lens, "lens", B), out.data_ptr(), B, T, hq, max_blocks, max_new, max_len, window,
-                              1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, _stream_ptr(stream))
-    _raise(rc)
+    if workspace is None:
+        wn = _kv_attention_bytes(B, T, hq, cache.heads, dim, max_new, max_len, window)
+        if wn:
+            workspace = torch.empty(wn, dtype=torch.uint8, device=dev)
+            if stream is not None and stream != torch.cuda.current_stream():
+                workspace.record_stream(stream)
+        wp = workspace.data_ptr() if wn else None
+    else:
+        wp, wn = _ws_args(workspace)
+    rc = lib().w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, tp, _i32(cu, "cu", B + 1), _i32(lens, "lens", B),
+                                  out.data_ptr(), B, T, hq, max_blocks, max_new, max_len, window,
+                                  1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, _raw_stream(stream))
+    if rc:
+        _raise(rc)
     return out
 
 
