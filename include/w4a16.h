@@ -410,15 +410,20 @@ int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, 
  * not overlap on the GPU.  0 bytes: the arguments are invalid, or the step
  * is too large for one call (row tiles x heads x 128-token tiles, or groups of
  * 1024 tokens x T x q_heads, of max_len tokens, above 2^31); the call then
- * returns W4A16_ERR_SHAPE. */
-#define W4A16_KV_MAX_GROUP 32 /* query heads per key/value head */
+ * returns W4A16_ERR_SHAPE.
+ *
+ * counters: int32 [W4A16_KV_COUNTERS], zero before the first call; every call
+ * that completes leaves them zero, and after W4A16_DEVICE_TIMEOUT they must be
+ * zeroed again.  Calls that share them must not overlap on the GPU. */
+#define W4A16_KV_MAX_GROUP 32   /* query heads per key/value head */
+#define W4A16_KV_COUNTERS 512
 
 size_t w4a16_kv_attention_workspace_bytes(int B, int T, int q_heads, int heads, int dim, int max_new, int max_len,
                                           int window);
 int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cache* cache, const int32_t* table,
                        const int32_t* cu, const int32_t* lens, w4a16_bf16* out, int B, int T, int q_heads,
                        int max_blocks, int max_new, int max_len, int window, float scale, void* workspace,
-                       size_t workspace_bytes, void* stream);
+                       size_t workspace_bytes, int32_t* counters, void* stream);
 
 /* Debug: q[N][K] (one byte per code) from Wq[N][K/8].  Bit-exact
  * ([W2D2 "Packed Storage Layout"]). */

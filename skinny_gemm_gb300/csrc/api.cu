@@ -626,7 +626,7 @@ size_t w4a16_kv_attention_workspace_bytes(int B, int T, int q_heads, int heads, 
 int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cache* cache, const int32_t* table,
                        const int32_t* cu, const int32_t* lens, w4a16_bf16* out, int B, int T, int q_heads,
                        int max_blocks, int max_new, int max_len, int window, float scale, void* workspace,
-                       size_t workspace_bytes, void* stream) {
+                       size_t workspace_bytes, int32_t* counters, void* stream) {
   if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
   if (int rc = check_kv_cache(cache)) return rc;
   if (B < 0 || B >= kMaxDim || T < 0 || T >= kMaxDim)
@@ -653,13 +653,15 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
   if (need == 0)
     return fail(W4A16_ERR_SHAPE, "T = %d rows over max_len = %d tokens: too many for one call (2^31 tiles or group rows)",
                 T, max_len);
-  if (!workspace) return fail(W4A16_ERR_NULL, "w4a16_kv_attention needs a workspace of %zu bytes", need);
-  if (misaligned(workspace, 256)) return fail(W4A16_ERR_ALIGN, "the workspace must be 256-byte aligned");
+  if (!workspace || !counters)
+    return fail(W4A16_ERR_NULL, "w4a16_kv_attention needs a workspace of %zu bytes, and counters", need);
+  if (misaligned(workspace, 256) || misaligned(counters, 4))
+    return fail(W4A16_ERR_ALIGN, "the workspace must be 256-byte and counters 4-byte aligned");
   if (workspace_bytes < need)
     return fail(W4A16_ERR_SHAPE, "a workspace of %zu bytes is too small (%zu)", workspace_bytes, need);
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
   KvAttentionArgs a{q, q_stride, *cache, table, cu, lens, out, B, T, q_heads, max_blocks, max_new, max_len, window,
-                    scale, workspace, nullptr};
+                    scale, workspace, counters, nullptr};
   if (int rc = flag_pointer(&a.flags)) return rc;
   cudaError_t e = launch_kv_attention(a, env().pdl, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_kv_attention launch");

@@ -48,6 +48,7 @@ struct KvAttentionArgs {
   int B, T, q_heads, max_blocks, max_new, max_len, window;
   float scale;
   void* ws;
+  int* counters;
   int* flags;
 };
 size_t kv_attention_workspace(int B, int T, int q_heads, int kv_heads, int dim, int max_new, int max_len, int window);

@@ -17,23 +17,26 @@
 // e4m3's range whatever the blocks' scales; the row sum takes p / vs.
 //
 // Split.  A tile is 128 tokens at a fixed position; a group eight tiles.  A
-// tile gives (maximum m, sum l, O) per row; a group folds its tiles in order,
-// a row its groups in eight interleaved chains joined as a tree
-// (kv_combine_kernel).  All tiles of the call form one line (request, row
-// tile, key head, tile) cut into equal ranges, one per CTA: a group that lies
-// in one range is folded in registers and written as one partial result, one
-// that a cut divides is written tile by tile and folded by the combine kernel
-// with the same operations.  So the cut follows the load and the bits do not.
+// tile gives (maximum m, sum l, O) per row; a group folds its tiles in order, a
+// row joins its groups pairwise as a binary tree.  All tiles of the call form
+// one line (request, row tile, key head, tile) cut into equal ranges, one per
+// CTA: a group that lies in one range is folded in registers, one that a cut
+// divides is written tile by tile, and the CTA that completes it (a counter)
+// folds the tiles with the same operations at its end.  So the cut follows the
+// load and the bits do not.  Rows of one group are finished there; several
+// groups are joined by kv_combine_kernel.
 //
 // Bound: HBM.  A 128-token tile of heads of 256 is 64 KB; one CTA has one to
 // two tiles in flight, two CTAs an SM where shared memory allows.
 //
-// CTA: 4 NG + 4 NG + 2 warps (NG groups of R query rows).
+// CTA: 4 NG + 4 NG + 3 warps (NG groups of R query rows).
 //   softmax warps  a thread per token: scores from TMEM, mask, maximum,
 //                  weights into shared memory, row sums
 //   fold warps     a thread per output column (TMEM lane): O from TMEM into the
 //                  running accumulators, partial results out
-//   one warp       work list, block table, TMA of K and V blocks, scales, queries
+//   one warp       work list: descriptors with block ids and scales, up to eight
+//                  tiles ahead
+//   one warp       copies: TMA of K and V blocks as slots become free, queries
 //   one warp       tensor memory, MMA issue
 // A tile passes load -> S -> softmax -> O -> fold; softmax of one tile, fold of
 // the one before and the copies of the next run side by side.
@@ -60,7 +63,6 @@ using namespace ptx;
 constexpr int kTile = 128;      // tokens per tile (the M of the MMAs)
 constexpr int kGroupTiles = 8;  // tiles per group
 constexpr int kGroupTokens = kTile * kGroupTiles;
-constexpr int kChains = 32;     // interleaved chains over a row's groups
 constexpr int kDescs = 8;       // tile descriptors in flight
 constexpr int kRing = 4;        // row sums and weights' barriers: softmax may be two tiles ahead of the fold
 constexpr int kSms = 152;
@@ -72,15 +74,23 @@ constexpr int kEnd = 2;        // no tile: the CTA's range is done
 constexpr int kFix = 4;        // some token of the tile is not seen by some row, or its block is not in the cache
 constexpr int kGroupBegin = 8; // first tile of a group folded here
 constexpr int kGroupEnd = 16;  // its last tile
-constexpr int kPart = 32;      // tile of a group that a cut divides
+constexpr int kPart = 32;      // the result goes to a slot for parts of divided groups
+constexpr int kDirect = 64;    // the segment is this one group, and whole
 
 struct Desc {
   int flags, h, j0, tile;      // key head, first token of the row tile in its request
-  int base, fresh, c0, at;     // tokens before the step, new tokens, first row, group slot (kPart: tile slot)
-  int pad[8];
+  int base, fresh, c0, at;     // tokens before the step, new tokens, first row, group slot (kPart: slot for parts)
+  int id[8];                   // block ids; -1: not needed or not in the cache
   float ks[8], vs[8];          // scales of the tile's blocks (0: no such block)
 };
-static_assert(sizeof(Desc) == 128, "two 64-byte halves");
+static_assert(sizeof(Desc) % 16 == 0, "16-byte rows");
+
+// A group that a cut divides, as a CTA's end needs it.
+struct CutGroup {
+  int owner, first, count, mine;  // CTA of its first tile, that tile's position, its tiles, those in this range (0: none)
+  int c0, j0, h, toks;            // rows: first of the request, first token of the row tile, key head, tokens
+  int gi, single;                 // group slot; the segment's only group
+};
 
 // RP rows of a row tile (query tokens x heads of a group), R to a softmax warp
 // group: more rows a thread spread its fixed work per tile (waits, exchange of
@@ -91,7 +101,7 @@ template <int D, int RP>
 struct Geo {
   static constexpr int R = RP < 16 ? RP : 16;
   static constexpr int kGroups = RP / R;
-  static constexpr int kThreads = 256 * kGroups + 64;
+  static constexpr int kThreads = 256 * kGroups + 96;
   static constexpr int kCols = RP < 8 ? 16 : 2 * RP;           // columns of S and O: first and second terms
   static constexpr int kPanels = D <= 128 ? 1 : D / 128;       // 128-byte column panels of K and V
   static constexpr int kRowB = D <= 128 ? D : 128;             // bytes of a panel's row
@@ -103,13 +113,13 @@ struct Geo {
   static constexpr int kCtas = RP == 4 ? (D == 256 ? 2 : 3) : RP == 8 ? 2 : RP == 16 ? (D == 256 ? 1 : 2) : 1;
   static constexpr int kSlots = RP <= 8 ? (D == 256 ? 3 : D == 128 ? (RP == 4 ? 4 : 6) : 6)
                                 : RP == 16 ? (D == 256 ? 6 : D == 128 ? 5 : 8) : D == 256 ? 5 : D == 128 ? 10 : 12;
-  static constexpr int kBars = 2 * kSlots + 2 * kDescs + 4 + kRing + 4 + 5 + kGroups;
+  static constexpr int kBars = 2 * kSlots + 3 * kDescs + 4 + kRing + 4 + 5 + kGroups;
   // rows (bits) of a tile that see a NaN in a thread's columns
   using Marks = std::conditional_t<(kPanels * R > 16), uint32_t, uint16_t>;
   // warps' maxima (two tiles), sums (kRing tiles x four warps), maxima (kRing), fold factors per warp, row factors and
   // limits; NaN marks (kRing tiles)
   static constexpr int kRowData = RP * 4 * (2 * 4 + kRing * 4 + kRing + 2 * 4 + 3) + kRing * 128 * kGroups * (int)sizeof(Marks);
-  static constexpr int kSmem = kSlots * kSlot + kQ + 2 * kP + kStage + kDescs * (int)sizeof(Desc) + kRowData + 8 * kBars + 32;
+  static constexpr int kSmem = kSlots * kSlot + kQ + 2 * kP + kStage + kDescs * (int)sizeof(Desc) + kRowData + 8 * kBars + 48 + 2 * (int)sizeof(CutGroup);
   static constexpr int kTmemCols = 2 * kCols * (1 + kPanels);  // S twice, O twice
   static constexpr uint32_t kTmem = kTmemCols <= 64 ? 64 : kTmemCols <= 128 ? 128 : kTmemCols <= 256 ? 256 : 512;
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
@@ -130,13 +140,13 @@ struct Params {
   float qk_scale;  // scale * log2(e)
   int gmax;        // group slots per row
   int grid;
-  int RP, t_slots;  // rows of a row tile; tile slots per CTA
+  int t_slots;     // slots for parts per CTA
   // workspace
-  int* starts;   // [B + 1] tiles before each request
   float* g_acc;  // [gmax][T][q_heads][D]
   float2* g_ml;  // [gmax][T][q_heads]
   float* t_acc;  // [grid][t_slots][RP][D]
   float2* t_ml;  // [grid][t_slots][RP]
+  int* counters;  // [grid] tiles done of divided groups, by the CTA of the first; zero between calls
   int* flags;
 };
 
@@ -216,11 +226,6 @@ struct Cut {
   int per, rem;
   __device__ __forceinline__ Cut(int total, int grid) : per(total / grid), rem(total - per * grid) {}
   __device__ __forceinline__ int begin(int c) const { return c * per + min(c, rem); }
-  // The slot of tile x of a divided group among range c's: the group began in an earlier range (its tiles are the
-  // range's first), or goes on in the next (its last; a range has at most seven of each).
-  __device__ __forceinline__ int slot(int c, int x, bool tail, int slots) const {
-    return c * slots + (tail ? slots - (begin(c + 1) - x) : x - begin(c));
-  }
   __device__ __forceinline__ int owner(int x) const {
     const int big = rem * (per + 1);
     return x < big ? x / (per + 1) : rem + (x - big) / max(per, 1);
@@ -284,6 +289,105 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
   }
 }
 
+// ---- joining a row's groups --------------------------------------------------------------------
+
+struct State {
+  float m, l;
+  float4 a;
+};
+
+__device__ __forceinline__ State empty_state() { return State{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)}; }
+
+__device__ __forceinline__ void fold_state(State& s, const State& o) {
+  float al, be;
+  fold_ml(s.m, s.l, o.m, o.l, al, be);
+  s.a.x = __fmaf_rn(s.a.x, al, __fmul_rn(o.a.x, be));
+  s.a.y = __fmaf_rn(s.a.y, al, __fmul_rn(o.a.y, be));
+  s.a.z = __fmaf_rn(s.a.z, al, __fmul_rn(o.a.z, be));
+  s.a.w = __fmaf_rn(s.a.w, al, __fmul_rn(o.a.w, be));
+}
+
+__device__ __forceinline__ void write_out(const Params& p, int64_t at, const State& s) {  // four columns
+  const float f = s.l != 0.f ? __frcp_rn(s.l) : 0.f;  // (NaN: stays)
+  uint2 w;
+  w.x = (uint32_t)f32_to_bf16_bits(__fmul_rn(s.a.x, f)) | (uint32_t)f32_to_bf16_bits(__fmul_rn(s.a.y, f)) << 16;
+  w.y = (uint32_t)f32_to_bf16_bits(__fmul_rn(s.a.z, f)) | (uint32_t)f32_to_bf16_bits(__fmul_rn(s.a.w, f)) << 16;
+  *reinterpret_cast<uint2*>(p.out + at) = w;
+}
+
+// The groups of a row that the call computed: n of them, the first one's
+// result at at0 (rows of D floats), `stride` rows from one to the next.
+template <int D>
+struct RowGroups {
+  int64_t at0, stride;
+  int n;
+  __device__ __forceinline__ RowGroups(const Params& p, const Req& r, int j, int hq) {
+    const int pos = r.base + j;
+    const int ga = p.window > 0 ? max(0, pos - p.window + 1) / kGroupTokens : 0;
+    n = pos / kGroupTokens - ga + 1;
+    at0 = ((int64_t)(ga - first_tile(p, r, 0) / kGroupTiles) * p.T + r.c0 + j) * p.q_heads + hq;
+    stride = (int64_t)p.T * p.q_heads;
+  }
+  __device__ __forceinline__ State group(const Params& p, int i, int col) const {
+    if (i >= n) return empty_state();
+    const int64_t at = at0 + i * stride;
+    const float2 ml = p.g_ml[at];
+    return State{ml.x, ml.y, *reinterpret_cast<const float4*>(p.g_acc + at * D + col)};
+  }
+  // The join of groups i .. i + m - 1 (m a power of two; those from n on are
+  // empty), four requested together: a binary counter of joined pairs.
+  __device__ __forceinline__ State tree(const Params& p, int i, int m, int col) const {
+    if (m < 4) {
+      State s = group(p, i, col);
+      if (m == 2) fold_state(s, group(p, i + 1, col));
+      return s;
+    }
+    State level[20];  // (local memory: only rows of more than four groups a set come here)
+    const int fours = (min(i + m, n) - i + 3) / 4;
+    if (fours == 1) return four(p, i, col);
+#pragma unroll 1
+    for (int f = 0; f < fours; ++f) {
+      State s = four(p, i + 4 * f, col);
+      int k = 0;
+      for (; (f >> k) & 1; ++k) {
+        State left = level[k];
+        fold_state(left, s);
+        s = left;
+      }
+      level[k] = s;
+    }
+    State s = level[__ffs(fours) - 1];  // what is left, from the right
+#pragma unroll 1
+    for (int k = __ffs(fours); fours >> k; ++k)
+      if ((fours >> k) & 1) {
+        State left = level[k];
+        fold_state(left, s);
+        s = left;
+      }
+    return s;
+  }
+  __device__ __forceinline__ State four(const Params& p, int i, int col) const {
+    State st[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) st[k] = group(p, i + k, col);
+    fold_state(st[0], st[1]);
+    fold_state(st[2], st[3]);
+    fold_state(st[0], st[2]);
+    return st[0];
+  }
+};
+
+// The last b with cu[b] <= t.
+__device__ __forceinline__ int find_request(const int32_t* cu, int B, int t) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // ---- the kernel -----------------------------------------------------------------------------------
 
 template <int D, int RP>
@@ -291,7 +395,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     kv_attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using X = Geo<D, RP>;
   constexpr int NS = X::kSlots, NP = X::kPanels, NG = X::kGroups, R = X::R, C = X::kCols, ND = kDescs;
-  constexpr int W_FOLD = 4 * NG, W_LOAD = 8 * NG, W_MMA = 8 * NG + 1;
+  constexpr int W_FOLD = 4 * NG, W_LIST = 8 * NG, W_LOAD = 8 * NG + 1, W_MMA = 8 * NG + 2;
   extern __shared__ __align__(1024) uint8_t base[];
   uint8_t* q_mem = base + NS * X::kSlot;
   uint8_t* p_mem = q_mem + X::kQ;
@@ -308,9 +412,10 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   const uint32_t slots = smem_u32(base), q_s = smem_u32(q_mem), p_s = smem_u32(p_mem), bars = smem_u32(bar_mem);
   auto full = [&](int i) { return bars + 8u * i; };                  // slot: copies landed
   auto empty = [&](int i) { return bars + 8u * (NS + i); };          // slot: MMAs done with it
-  auto d_full = [&](int i) { return bars + 8u * (2 * NS + i); };     // descriptor and scales written
+  auto d_full = [&](int i) { return bars + 8u * (2 * NS + i); };     // descriptor written
   auto d_free = [&](int i) { return bars + 8u * (2 * NS + ND + i); };
-  const uint32_t bars2 = bars + 8u * (2 * NS + 2 * ND);
+  auto d_scales = [&](int i) { return bars + 8u * (2 * NS + 2 * ND + i); };  // its scales landed
+  const uint32_t bars2 = bars + 8u * (2 * NS + 3 * ND);
   auto s_full = [&](int i) { return bars2 + 8u * i; };
   auto s_free = [&](int i) { return bars2 + 8u * (2 + i); };
   auto o_full = [&](int i) { return bars2 + 8u * (4 + i); };         // (the weights were read, too)
@@ -322,6 +427,9 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_mem + X::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_nan = reinterpret_cast<volatile int*>(s_tmem + 2);  // [kRing] 1 + a tile whose marks are in s_taint
+  volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 6);  // [2] this CTA completed the divided group
+  volatile int* s_rest = reinterpret_cast<volatile int*>(s_tmem + 8);  // rows of no (valid) request, all tiles
+  CutGroup* s_cut = reinterpret_cast<CutGroup*>(s_tmem + 12);          // [2] at the range's beginning, at its end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   auto give_up = [&]() {
@@ -332,11 +440,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity));
   };
 
-  // ---- set-up; meanwhile the loading warp finds its range of the line ----
+  // ---- set-up; meanwhile the listing warp finds the CTA's range of the line ----
   const int nb = kTile >> p.shift, block = 1 << p.shift;  // blocks per tile
   bool bad = false;
   int total = 0, beg = 0, end = 0, b0 = 0;
-  Req mine{0, 0, 0}, r{0, 0, 0};  // the loading warp: this lane's request of 32, and the current one
+  Req mine{0, 0, 0}, r{0, 0, 0};  // the listing warp: this lane's request of 32, and the current one
   int b = 0, rt = 0, h = 0, tile = 0, t_first = 0, t_last = -1;
   int seg0 = 0;  // position of the segment's first tile
   int id = -2;
@@ -364,9 +472,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
     }
+  } else if (warp == W_LIST) {
     pdl_launch_dependents();
     pdl_wait();
     int mine_end = 0;         // inclusive prefix of this lane's request
+    int rows = 0;             // of valid requests
     auto scan = [&]() {       // loads 32 requests; their inclusive prefix of tiles after `total`
       mine = load_req(p, b0 + lane, &bad);
       int n = mine.fresh > 0 ? tiles_before(p, mine, row_tiles(p, mine)) * p.heads : 0;
@@ -379,10 +489,14 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     };
     for (; b0 < p.B; b0 += 32) {
       scan();
-      if (blockIdx.x == 0 && b0 + lane < p.B) p.starts[b0 + lane + 1] = mine_end;
       total = __shfl_sync(0xffffffffu, mine_end, 31);
+      rows += mine.fresh;
     }
-    if (blockIdx.x == 0 && lane == 0) p.starts[0] = 0;
+    rows = __reduce_add_sync(0xffffffffu, rows);
+    if (lane == 0) {
+      s_rest[0] = p.T - rows;
+      s_rest[1] = total;
+    }
     if (bad && blockIdx.x == 0) atomicOr(p.flags, W4A16_DEVICE_KV_RANGE);
     const Cut cut(total, p.grid);
     beg = cut.begin(blockIdx.x);
@@ -428,8 +542,9 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       mbar_init(empty(i), 1);
     }
     for (int i = 0; i < ND; ++i) {
-      mbar_init(d_full(i), 33);
-      mbar_init(d_free(i), 8 * NG + 1);
+      mbar_init(d_full(i), 1);
+      mbar_init(d_scales(i), 32);
+      mbar_init(d_free(i), 8 * NG + 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
@@ -448,6 +563,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     mbar_init(st_free, 4 * NG);
     for (int i = 0; i < NG; ++i) mbar_init(grp_sync(i), 4);
     *s_abort = 0;
+    s_cut[0].mine = s_cut[1].mine = 0;
     fence_barrier_init();
   }
   tc_fence_before_sync();
@@ -456,58 +572,56 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   const uint32_t tmem = *s_tmem;
   const uint32_t s_col = tmem, o_col = tmem + 2 * C;  // S: two tiles of C columns; O: two tiles of NP panels of C
 
-  if (warp == W_LOAD) {
-    // ---- work list and copies ----
+  if (warp == W_LIST) {
+    // ---- work list ----
     bool fresh_seg = true, ok = true;
-    int x = beg, t = 0, seg = 0;
-    for (; x < end && ok; ++x, ++t) {
-      // this tile's descriptor
-      const int ds = t % ND, ch = h;
+    const Cut cut(s_rest[1], p.grid);
+    int x = beg, t = 0;
+    for (; x < end; ++x, ++t) {
+      const int ds = t % ND;
       const int g_lo = max(seg0, x - tile % kGroupTiles), g_hi = min(seg0 + t_last - t_first, x - tile % kGroupTiles + kGroupTiles - 1);
       const int j0 = rt * p.TQ, toks = min(p.TQ, r.fresh - j0), pos0 = r.base + j0, pos1 = pos0 + toks - 1;
-      int fl = fresh_seg ? kNewSeg : 0, at;
-      if (g_lo >= beg && g_hi < end) {
-        fl |= (x == g_lo ? kGroupBegin : 0) | (x == g_hi ? kGroupEnd : 0);
-        at = tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles;
-      } else {
-        fl |= kPart;
-        at = (int)blockIdx.x * p.t_slots + (g_lo >= beg ? p.t_slots - (end - x) : x - beg);
-      }
+      // the group's first tile begins a fold, its last ends it; a cut ends it, too, and after one every tile is by itself
+      const bool late = g_lo < beg, part = late || g_hi >= end;
+      int fl = (fresh_seg ? kNewSeg : 0) | (part ? kPart : 0) | (x == g_lo || late ? kGroupBegin : 0) |
+               (x == g_hi || x + 1 == end || late ? kGroupEnd : 0);
+      const int at = !part ? tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles
+                           : (int)blockIdx.x * p.t_slots + (late ? x - beg : p.t_slots - 1);
+      const bool single = t_first / kGroupTiles == t_last / kGroupTiles;
+      if (!(fl & kPart) && single) fl |= kDirect;
       const bool valid = id >= 0 && id < p.blocks;
       const unsigned need = __ballot_sync(0xffffffffu, id != -2), have = __ballot_sync(0xffffffffu, valid);
       if (need != have || tile * kTile + kTile - 1 > pos0 || (p.window > 0 && tile * kTile < pos1 - p.window + 1)) fl |= kFix;
       if (t >= ND && !(ok = wait_warp(d_free(ds), ((t / ND) - 1) & 1))) break;
       Desc& de = descs[ds];
       if (lane == 0) {
-        *reinterpret_cast<int4*>(&de.flags) = make_int4(fl, ch, j0, tile);
+        *reinterpret_cast<int4*>(&de.flags) = make_int4(fl, h, j0, tile);
         *reinterpret_cast<int4*>(&de.base) = make_int4(r.base, r.fresh, r.c0, at);
         if (need != have) atomicOr(p.flags, W4A16_DEVICE_KV_RANGE);
       }
+      if (lane < 8) de.id[lane] = valid ? id : -1;
       if (lane < nb) {
         if (valid) {
-          cp_async4(smem_u32(&de.ks[lane]), p.k_scale + (int64_t)id * p.heads + ch);
-          cp_async4(smem_u32(&de.vs[lane]), p.v_scale + (int64_t)id * p.heads + ch);
+          cp_async4(smem_u32(&de.ks[lane]), p.k_scale + (int64_t)id * p.heads + h);
+          cp_async4(smem_u32(&de.vs[lane]), p.v_scale + (int64_t)id * p.heads + h);
         } else {
           de.ks[lane] = 0.f;
           de.vs[lane] = 0.f;
         }
       }
       __syncwarp();
-      cp_async_arrive(d_full(ds));
       if (lane == 0) mbar_arrive(d_full(ds));
-      if (fresh_seg) {  // the segment's query rows, a copy per token
-        if (seg > 0 && !(ok = wait_warp(st_free, (seg - 1) & 1))) break;
-        const uint32_t bytes = (uint32_t)(p.G * D * 2);
-        if (lane == 0) mbar_expect_tx(st_full, toks * bytes);
-        __syncwarp();
-        if (lane < toks)
-          bulk_load(smem_u32(stage) + lane * bytes, p.q + (int64_t)(r.c0 + j0 + lane) * p.q_stride + (int64_t)ch * p.G * D,
-                    bytes, st_full, policy_evict_first());
-        ++seg;
+      cp_async_arrive(d_scales(ds));
+      if (fl & kPart) {  // for the CTA's end
+        const int k = !late;
+        if (lane == 0) {
+          const int owner = k ? (int)blockIdx.x : cut.owner(g_lo);
+          s_cut[k] = CutGroup{owner, g_lo, g_hi - g_lo + 1, min(end, g_hi + 1) - max(beg, g_lo), r.c0, j0, h, toks,
+                              tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles, single};
+        }
       }
-      // the next tile, its block ids requested before this one's slots are waited for
+      // the next tile
       const bool same = tile < t_last;
-      int next_id = -2;
       if (x + 1 < end) {
         if (same) {
           ++tile;
@@ -534,43 +648,61 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           enter();
           tile = t_first;
         }
-        next_id = load_id();
+        id = load_id();
       }
-      // lane (block, panel): one copy each of K, then of V
-      const int nv = __popc(have);
-      const int src = lane / NP, panel = lane % NP;
-      const int nth = src < nv ? (have == (1u << nv) - 1 ? src : __fns(have, 0, src + 1)) : 0;
-      const int my_id = __shfl_sync(0xffffffffu, id, nth & 31);
-      const int row = (my_id * p.heads + ch) << p.shift;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int slot = loads % NS;
-        if (loads >= NS && !(ok = wait_warp(empty(slot), ((loads / NS) - 1) & 1))) break;
-        if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(nv * block * D));
-        __syncwarp();
-        if (lane < nv * NP)
-          tma_load_2d(slots + slot * X::kSlot + panel * X::kPanelBytes + nth * block * X::kRowB, kv ? &maps.v : &maps.k,
-                      panel * 128, row, full(slot));
-        ++loads;
-      }
-      id = next_id;
       fresh_seg = !same;
     }
     if (ok) {  // the end mark
       const int ds = t % ND;
       ok = t < ND || wait_warp(d_free(ds), ((t / ND) - 1) & 1);
-      if (ok) {
-        if (lane == 0) descs[ds].flags = kEnd;
-        __syncwarp();
-        cp_async_arrive(d_full(ds));
-        if (lane == 0) mbar_arrive(d_full(ds));
+      if (ok && lane == 0) {
+        descs[ds].flags = kEnd;
+        mbar_arrive(d_full(ds));
       }
     }
     if (!ok && lane == 0) give_up();
-    if (!ok) {  // staged rows in flight
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (seg > 0 && lane == 0) mbar_wait_parked(st_full, (seg - 1) & 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == W_LOAD) {
+    // ---- copies ----
+    bool ok = true;
+    int seg = 0;
+    for (int t = 0; ok; ++t) {
+      const int ds = t % ND;
+      if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
+      const Desc& de = descs[ds];
+      const int4 dd = *reinterpret_cast<const int4*>(&de.flags), dx = *reinterpret_cast<const int4*>(&de.base);
+      if (dd.x & kEnd) break;
+      // lane (block, panel): one copy each of K, then of V
+      const int blk = lane / NP, panel = lane % NP;
+      const int my_id = blk < nb ? de.id[blk & 7] : -1;
+      const int row = (my_id * p.heads + dd.y) << p.shift;
+      const int copies = __popc(__ballot_sync(0xffffffffu, my_id >= 0));  // of kRowB bytes x block rows
+      if (lane == 0) mbar_arrive(d_free(ds));
+      const int toks = min(p.TQ, dx.y - dd.z);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int slot = loads % NS;
+        if (loads >= NS && !(ok = wait_warp(empty(slot), ((loads / NS) - 1) & 1))) break;
+        if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(copies * block * X::kRowB));
+        __syncwarp();
+        if (my_id >= 0)
+          tma_load_2d(slots + slot * X::kSlot + panel * X::kPanelBytes + blk * block * X::kRowB, kv ? &maps.v : &maps.k,
+                      panel * 128, row, full(slot));
+        ++loads;
+        if (kv == 0 && (dd.x & kNewSeg)) {  // the segment's query rows, a copy per token
+          if (seg > 0 && !(ok = wait_warp(st_free, (seg - 1) & 1))) break;
+          const uint32_t bytes = (uint32_t)(p.G * D * 2);
+          if (lane == 0) mbar_expect_tx(st_full, toks * bytes);
+          __syncwarp();
+          if (lane < toks)
+            bulk_load(smem_u32(stage) + lane * bytes, p.q + (int64_t)(dx.z + dd.z + lane) * p.q_stride + (int64_t)dd.y * p.G * D,
+                      bytes, st_full, policy_evict_first());
+          ++seg;
+        }
+      }
     }
+    if (!ok && lane == 0) give_up();
+    if (!ok && seg > 0 && lane == 0) mbar_wait_parked(st_full, (seg - 1) & 1);  // staged rows in flight
   } else if (warp == W_MMA) {
     // ---- MMA issue: S of tile t, then O of tile t - 1 (the warp together, one thread issues) ----
     constexpr uint32_t id_s = umma_idesc_e4m3(128, C, false, false);
@@ -712,6 +844,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         if (!ok) break;
       }
       // the V scale is a power of two: its exponent, and its reciprocal
+      if (!(ok = wait_warp(d_scales(ds), (t / ND) & 1))) break;
       const int blk = tt >> p.shift;
       const float ks = de.ks[blk];
       int ve = (int)(__float_as_uint(de.vs[blk]) >> 23) - 127;
@@ -755,9 +888,9 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         bool nan_code = false;
         const bool partly = toks > 1 && !dead && (tok > pos0 || (p.window > 0 && tok < pos1 - p.window + 1));
         if (grp == 0 && (dead || partly)) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < NP; ++c)
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < kCh; ++i) {
               uint4* w = reinterpret_cast<uint4*>(v_row + c * X::kPanelBytes + tt * kRowB + ((i + tt) % kCh) * 16);
               if (dead) {
@@ -906,7 +1039,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         mt = s_top[ring * RP + R * grp + lane];
         lt = __fadd_rn(__fadd_rn(a[0], a[RP]), __fadd_rn(a[2 * RP], a[3 * RP]));
       }
-      const bool part = fl & kPart;
       if (fl & kGroupBegin) {
         m_run = -INFINITY;
         l_run = 0.f;
@@ -915,7 +1047,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
           for (int i = 0; i < R; ++i) acc[c][i] = 0.f;
       }
-      if (!part) {
+      {
         float al, be;
         fold_ml(m_run, l_run, mt, lt, al, be);
         if (lane < R) s_ab[w4 * RP + R * grp + lane] = make_float2(al, be);
@@ -936,47 +1068,49 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           for (int i = 0; i < R; ++i)
             if ((poison >> (c * R + i)) & 1) raw[i] = __uint_as_float(0x7FC00000u);
         }
-        if (part) {
-          const int rows = min(p.TQ, de.fresh - de.j0) * p.G - R * grp;
-          float* dst = p.t_acc + ((int64_t)de.at * RP + R * grp) * D + c * 128 + tt;
-          if (live) {
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-              if (i < rows) dst[i * D] = raw[i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < R; i += 2) {
-            const float4 ab = *reinterpret_cast<const float4*>(s_ab + w4 * RP + R * grp + i);
-            acc[c][i] = __fmaf_rn(acc[c][i], ab.x, __fmul_rn(raw[i], ab.y));
-            acc[c][i + 1] = __fmaf_rn(acc[c][i + 1], ab.z, __fmul_rn(raw[i + 1], ab.w));
-          }
+        for (int i = 0; i < R; i += 2) {
+          const float4 ab = *reinterpret_cast<const float4*>(s_ab + w4 * RP + R * grp + i);
+          acc[c][i] = __fmaf_rn(acc[c][i], ab.x, __fmul_rn(raw[i], ab.y));
+          acc[c][i + 1] = __fmaf_rn(acc[c][i + 1], ab.z, __fmul_rn(raw[i + 1], ab.w));
         }
       }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free(par));
-      if (part) {
+      if (fl & kGroupEnd) {
+        // the result: out (the segment's only group), its group slot, or its tile slot
         const int rows = min(p.TQ, de.fresh - de.j0) * p.G - R * grp;
-        if (w4 == 0 && lane < R && lane < rows) p.t_ml[(int64_t)de.at * RP + R * grp + lane] = make_float2(mt, lt);
-      } else if (fl & kGroupEnd) {
-        const int rows = min(p.TQ, de.fresh - de.j0) * p.G - R * grp;
-        const int64_t row0 = ((int64_t)de.at * p.T + de.c0 + de.j0) * p.q_heads + de.h * p.G;
-        int j = R * grp / p.G, g = R * grp - j * p.G;
-        const int jl = (R * grp + lane) / p.G, gl = R * grp + lane - jl * p.G;
+        const bool direct = fl & kDirect, part = fl & kPart;
+        const int j = R * grp / p.G, g0 = R * grp - j * p.G;
+        const int64_t row0 = part ? (int64_t)de.at * RP + R * grp
+                                  : ((int64_t)(direct ? 0 : de.at) * p.T + de.c0 + de.j0 + j) * p.q_heads + de.h * p.G + g0;
+        const int jump = part ? 0 : (p.q_heads - p.G) * D;  // from a token's last head to the next token's first
+        int64_t at = row0 * D + tt;
+        int g = g0;
+        float* dst = part ? p.t_acc : p.g_acc;
+        const float rl = l_run != 0.f ? __frcp_rn(l_run) : 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+          const float f = __shfl_sync(0xffffffffu, rl, i);
           if (i < rows && live) {
-            float* dst = p.g_acc + (row0 + (int64_t)j * p.q_heads + g) * D + tt;
 #pragma unroll
-            for (int c = 0; c < NP; ++c) dst[c * 128] = acc[c][i];
+            for (int c = 0; c < NP; ++c) {
+              if (direct) p.out[at + c * 128] = f32_to_bf16_bits(__fmul_rn(acc[c][i], f));
+              else dst[at + c * 128] = acc[c][i];
+            }
           }
+          at += D;
           if (++g == p.G) {
             g = 0;
-            ++j;
+            at += jump;
           }
         }
-        if (w4 == 0 && lane < R && lane < rows) p.g_ml[row0 + (int64_t)jl * p.q_heads + gl] = make_float2(m_run, l_run);
+        if (!direct && w4 == 0 && lane < R && lane < rows) {
+          const int jl = (g0 + lane) / p.G;
+          const int64_t row = row0 + lane + (part ? 0 : (int64_t)jl * (p.q_heads - p.G));
+          (part ? p.t_ml : p.g_ml)[row] = make_float2(m_run, l_run);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(d_free(ds));
@@ -994,166 +1128,186 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       mbar_wait_parked(drained, 0);
     }
   }
-  tc_fence_before_sync();
-  __syncthreads();
   if (warp == W_MMA) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, X::kTmem);
+  }
+  if (*s_abort) return;
+
+  // ---- the CTA's end: divided groups, rows that nobody computes ----
+  //
+  // A divided group's fold, acc = acc al_k + O_k be_k over its parts k (the
+  // first range's fold, then tiles), takes its factors from the parts' (m, l)
+  // alone: a thread per row works them out, while a thread per four columns has
+  // all its loads in flight at once.
+  constexpr int NT = X::kThreads, V = X::kCtas > 2 ? 2 : 4;  // columns a thread takes (registers)
+  if (s_cut[0].mine | s_cut[1].mine) {
+    float2* w_ab = reinterpret_cast<float2*>(base);   // [2][RP][kGroupTiles]
+    float2* w_ml = w_ab + 2 * RP * kGroupTiles;       // [2][RP]
+    int* w_slot = reinterpret_cast<int*>(w_ml + 2 * RP);  // [2][kGroupTiles]
+    int* w_parts = w_slot + 2 * kGroupTiles;              // [2]
+    if (tid < 2 * kGroupTiles) {
+      const CutGroup& c = s_cut[tid / kGroupTiles];
+      const int z = tid % kGroupTiles;
+      if (c.mine) {
+        const Cut cut(s_rest[1], p.grid);
+        const int x = cut.begin(c.owner + 1) + z - 1, own = z ? cut.owner(x) : c.owner;  // part z: a tile after the first range
+        w_slot[tid] = own * p.t_slots + (z ? x - cut.begin(own) : p.t_slots - 1);
+        if (z == 0) w_parts[tid / kGroupTiles] = c.first + c.count - x;
+      }
+    }
+    __threadfence();  // this CTA's tile results
+    __syncthreads();
+    if (tid < 2) {
+      const CutGroup& c = s_cut[tid];
+      bool last = false;
+      if (c.mine) {
+        last = atomicAdd(p.counters + c.owner, c.mine) + c.mine == c.count;
+        if (last) p.counters[c.owner] = 0;
+        __threadfence();
+      }
+      s_last[tid] = last;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      if (!s_last[k]) continue;
+      const CutGroup& c = s_cut[k];
+      const int count = w_parts[k], rows = c.toks * p.G;
+      bool weights = false;
+      for (int i = tid; i < (rows * (D / V) + NT - 1) / NT * NT; i += NT) {
+        const int rr = i / (D / V), col = V * (i - rr * (D / V)), jj = rr / p.G;
+        float v[kGroupTiles][V];
+#pragma unroll
+        for (int z = 0; z < kGroupTiles; ++z) {
+          const bool is = z < count && rr < rows;
+          const float* from = p.t_acc + ((int64_t)(is ? w_slot[k * kGroupTiles + z] : 0) * RP + (is ? rr : 0)) * D + col;
+          if constexpr (V == 4) {
+            const float4 u = is ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
+          } else {
+            const float2 u = is ? __ldcg(reinterpret_cast<const float2*>(from)) : make_float2(0.f, 0.f);
+            v[z][0] = u.x, v[z][1] = u.y;
+          }
+        }
+        if (!weights) {  // (the first time round, while those are on their way)
+          weights = true;
+          if (tid < rows) {
+            float2 ml[kGroupTiles];
+#pragma unroll
+            for (int z = 0; z < kGroupTiles; ++z)
+              ml[z] = z < count ? __ldcg(p.t_ml + w_slot[k * kGroupTiles + z] * RP + tid) : make_float2(-INFINITY, 0.f);
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int z = 0; z < kGroupTiles; ++z) {
+              float al, be;
+              fold_ml(m, l, ml[z].x, ml[z].y, al, be);
+              w_ab[(k * RP + tid) * kGroupTiles + z] = make_float2(al, be);
+            }
+            w_ml[k * RP + tid] = make_float2(m, l);
+          }
+          __syncthreads();
+        }
+        if (rr >= rows) continue;
+        float a[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) a[q] = 0.f;
+#pragma unroll
+        for (int z = 0; z < kGroupTiles; ++z) {
+          const float2 ab = w_ab[(k * RP + rr) * kGroupTiles + z];
+#pragma unroll
+          for (int q = 0; q < V; ++q) a[q] = __fmaf_rn(a[q], ab.x, __fmul_rn(v[z][q], ab.y));
+        }
+        const float2 ml = w_ml[k * RP + rr];
+        const int64_t row = (int64_t)(c.c0 + c.j0 + jj) * p.q_heads + c.h * p.G + rr - jj * p.G;
+        if (c.single) {
+          const float f = ml.y != 0.f ? __frcp_rn(ml.y) : 0.f;
+#pragma unroll
+          for (int q = 0; q < V; q += 2)
+            *reinterpret_cast<uint32_t*>(p.out + row * D + col + q) =
+                (uint32_t)f32_to_bf16_bits(__fmul_rn(a[q], f)) | (uint32_t)f32_to_bf16_bits(__fmul_rn(a[q + 1], f)) << 16;
+        } else {
+          const int64_t at = row + (int64_t)c.gi * p.T * p.q_heads;
+#pragma unroll
+          for (int q = 0; q < V; q += 2) *reinterpret_cast<float2*>(p.g_acc + at * D + col + q) = make_float2(a[q], a[q + 1]);
+          if (col == 0) p.g_ml[at] = ml;
+        }
+      }
+    }
+  }
+  if (s_rest[0] > 0) {
+    // (rare) padding rows and rows of requests that were left out: zeros
+    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+      bool bad_req = false;
+      const Req rq = load_req(p, find_request(p.cu, p.B, t), &bad_req);
+      if (t >= rq.c0 && t < rq.c0 + rq.fresh) continue;
+      for (int i = tid; i < p.q_heads * (D / 8); i += NT)
+        *reinterpret_cast<uint4*>(p.out + (int64_t)t * p.q_heads * D + 8 * i) = make_uint4(0, 0, 0, 0);
+    }
   }
 }
 
 // ---- combine -----------------------------------------------------------------------------------
 //
-// A row's groups, counted from the first it sees: group i in chain i % 32,
-// the chains joined pairwise as a tree.  SETS thread sets share a row's
-// chains: 1 (a thread runs a row's chains itself; at most eight groups), 8 or
-// 32 (long caches, few rows).  Reads what the attention kernel wrote a moment
-// ago (L2): the loads of a cut group's tiles are issued together.
-
-struct State {
-  float m, l;
-  float4 a;
-};
-
-__device__ __forceinline__ void fold_state(State& s, float m, float l, const float4& a) {
-  float al, be;
-  fold_ml(s.m, s.l, m, l, al, be);
-  s.a.x = __fmaf_rn(s.a.x, al, __fmul_rn(a.x, be));
-  s.a.y = __fmaf_rn(s.a.y, al, __fmul_rn(a.y, be));
-  s.a.z = __fmaf_rn(s.a.z, al, __fmul_rn(a.z, be));
-  s.a.w = __fmaf_rn(s.a.w, al, __fmul_rn(a.w, be));
-}
-
-template <int N>
-__device__ __forceinline__ void join(State (&st)[N]) {  // into st[0]
-#pragma unroll
-  for (int n = 1; n < N; n <<= 1)
-#pragma unroll
-    for (int i = 0; i + n < N; i += 2 * n) fold_state(st[i], st[i + n].m, st[i + n].l, st[i + n].a);
-}
-
-// The last b with cu[b] <= t, by the whole warp (32 probes a step).
-__device__ __forceinline__ int find_request(const Params& p, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = p.B;
-  while (n > 1) {
-    const int step = (n + 31) >> 5, at = lo + lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, lane * step < n && p.cu[min(at, p.B)] <= t);
-    const int k = le ? 31 - __clz(le) : 0;
-    lo += k * step;
-    n = min(step, n - k * step);
-  }
-  return lo;
-}
+// The join of rows of several groups.  A thread has four columns; SETS thread
+// sets share a row's groups, neighbouring ones each, and join as a tree in
+// shared memory: 1 (at most eight groups, all requested at once), 4, or 128
+// (few rows of very many, 32 columns a CTA).  Reads what the attention kernel
+// wrote a moment ago (L2), so it is a chain of latencies: request (guessed,
+// then checked), its lengths, results.
 
 template <int D, int SETS>
-__global__ void __launch_bounds__(SETS == 32 ? 1024 : 256) kv_combine_kernel(const __grid_constant__ Params p) {
-  constexpr int kCols = D < 128 ? D : 128;          // columns of a CTA's thread set (SETS > 1)
-  constexpr int kLanes = (SETS == 1 ? D : kCols) / 4;
-  constexpr int kPer = SETS == 1 ? 8 : kChains / SETS;  // chains of a thread
-  constexpr int kThreads = SETS == 1 ? 256 : SETS * kLanes;
-  __shared__ float2 s_ml[SETS == 1 ? 1 : SETS][kLanes];
-  __shared__ float4 s_a[SETS == 1 ? 1 : SETS][kLanes];
-  const int set = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
-  const int64_t row = SETS == 1 ? (int64_t)blockIdx.x * (kThreads / kLanes) + set : (int64_t)blockIdx.x;
-  const int col = (SETS == 1 ? 0 : (int)blockIdx.y * kCols) + 4 * c;
+__global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(const __grid_constant__ Params p) {
+  constexpr int LANES = SETS == 128 ? 8 : D / 4, kPer = SETS == 128 ? 1 : 256 / LANES / SETS;  // rows of a CTA
+  __shared__ State s_set[SETS == 1 ? 1 : kPer * SETS][LANES];
+  const int set = threadIdx.x / LANES % SETS, sub = threadIdx.x / (LANES * SETS), c = threadIdx.x % LANES;
+  const int col = (SETS == 128 ? (int)blockIdx.y * 32 : 0) + 4 * c, rows = p.T * p.q_heads;
   pdl_launch_dependents();
   pdl_wait();
-  State st[kPer];
+  for (int row0 = (int)blockIdx.x * kPer; row0 < rows; row0 += kPer * (int)gridDim.x) {
+    const int row = min(row0 + sub, rows - 1), t = row / p.q_heads, hq = row - t * p.q_heads;
+    int b = min(t / p.max_new, p.B - 1);  // right where every request has max_new new tokens
+    bool bad = false;
+    Req r = load_req(p, b, &bad);
+    if (p.cu[b] > t || p.cu[b + 1] <= t) {
+      b = find_request(p.cu, p.B, t);
+      r = load_req(p, b, &bad);
+    }
+    const int j = t - r.c0;
+    const int rt = r.fresh <= p.TQ ? 0 : j / p.TQ;
+    // (other rows are written already)
+    const bool mine = row0 + sub < rows && j >= 0 && j < r.fresh &&
+                      first_tile(p, r, rt) / kGroupTiles != last_tile(p, r, rt) / kGroupTiles;
+    State out = empty_state();
+    if (mine) {
+      const RowGroups<D> g(p, r, j, hq);
+      if constexpr (SETS == 1) {
+        State st[8];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) st[i] = State{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  const bool inside = row < (int64_t)p.T * p.q_heads;
-  const int t = inside ? (int)(row / p.q_heads) : p.T - 1, hq = (int)(row - (int64_t)t * p.q_heads);
-  // (heads of 64 put two rows on a warp: perhaps of two tokens)
-  const int t_a = __shfl_sync(0xffffffffu, t, 0), t_b = __shfl_sync(0xffffffffu, t, 31);
-  int b = find_request(p, t_a);
-  if (t_b != t_a) {
-    const int b2 = find_request(p, t_b);
-    if (t == t_b) b = b2;
-  }
-  bool bad = false;
-  const Req r = load_req(p, b, &bad);
-  const int j = t - r.c0;
-  if (inside && j >= 0 && j < r.fresh) {
-    const int rt = j / p.TQ, h = hq / p.G;
-    const int tf = first_tile(p, r, rt), tl = last_tile(p, r, rt);
-    const int seg0 = p.starts[b] + (rt ? tiles_before(p, r, rt) * p.heads : 0) + h * (tl - tf + 1);
-    const Cut cut(p.starts[p.B], p.grid);
-    const int g0 = first_tile(p, r, 0) / kGroupTiles;  // slot 0
-    const int rr = (j - rt * p.TQ) * p.G + hq - h * p.G;  // row within the row tile
-    const int pos = r.base + j;
-    const int ga = p.window > 0 ? max(0, pos - p.window + 1) / kGroupTokens : 0, n = pos / kGroupTokens - ga + 1;
-    auto take = [&](int i, State& s) {  // the row's group i
-      const int g = ga + i;
-      const int ta = max(tf, g * kGroupTiles), tb = min(tl, g * kGroupTiles + kGroupTiles - 1);
-      const int xa = seg0 + ta - tf, o = cut.owner(xa), left = cut.begin(o + 1) - xa;  // tiles in the first range
-      if (tb - ta < left) {
-        const int64_t at = ((int64_t)(g - g0) * p.T + t) * p.q_heads + hq;
-        const float2 ml = p.g_ml[at];
-        fold_state(s, ml.x, ml.y, *reinterpret_cast<const float4*>(p.g_acc + at * D + col));
-        return;
+        for (int k = 0; k < 8; ++k) st[k] = g.group(p, k, col);
+#pragma unroll
+        for (int n = 1; n < 8; n <<= 1)
+#pragma unroll
+          for (int k = 0; k + n < 8; k += 2 * n) fold_state(st[k], st[k + n]);
+        out = st[0];
+      } else {
+        int per = 1;
+        while (per * SETS < g.n) per *= 2;
+        if (per * set < g.n) out = g.tree(p, per * set, per, col);
       }
-      float2 ml[kGroupTiles];
-      float4 a[kGroupTiles];
-      int own = o, end = left;
-#pragma unroll
-      for (int k = 0; k < kGroupTiles; ++k) {
-        ml[k] = make_float2(-INFINITY, 0.f);
-        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ta + k <= tb) {
-          if (k >= end) {  // (ranges may be single tiles)
-            ++own;
-            end = cut.begin(own + 1) - xa;
-          }
-          const int64_t at = (int64_t)cut.slot(own, xa + k, own == o, p.t_slots) * p.RP + rr;
-          ml[k] = p.t_ml[at];
-          a[k] = *reinterpret_cast<const float4*>(p.t_acc + at * D + col);
+    }
+    if constexpr (SETS > 1) {
+      s_set[sub * SETS + set][c] = out;
+      for (int k = 1; k < SETS; k <<= 1) {
+        __syncthreads();
+        if (set % (2 * k) == 0) {
+          fold_state(out, s_set[sub * SETS + set + k][c]);
+          s_set[sub * SETS + set][c] = out;
         }
       }
-      State gs{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll
-      for (int k = 0; k < kGroupTiles; ++k) fold_state(gs, ml[k].x, ml[k].y, a[k]);
-      fold_state(s, gs.m, gs.l, gs.a);
-    };
-    if (SETS == 1) {
-      for (int i = 0; i < n; ++i) {  // n <= 8: one group a chain
-        State s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-        take(i, s);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if (k == i) st[k] = s;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        for (int i = set * kPer + k; i < n; i += kChains) take(i, st[k]);
     }
-  }
-  join(st);
-  State out = st[0];
-  if (SETS > 1) {
-    s_ml[set][c] = make_float2(out.m, out.l);
-    s_a[set][c] = out.a;
-    // the tree over the sets, in shared memory
-    for (int k = 1; k < SETS; k <<= 1) {
-      __syncthreads();
-      if (set % (2 * k) == 0) {
-        const float2 ml = s_ml[set + k][c];
-        fold_state(out, ml.x, ml.y, s_a[set + k][c]);
-        s_ml[set][c] = make_float2(out.m, out.l);
-        s_a[set][c] = out.a;
-      }
-    }
-    if (set != 0) return;
-  }
-  if (inside) {
-    const bool any = out.l != 0.f;  // (NaN: yes)
-    uint2 w;
-    w.x = (uint32_t)f32_to_bf16_bits(any ? __fdiv_rn(out.a.x, out.l) : 0.f) |
-          (uint32_t)f32_to_bf16_bits(any ? __fdiv_rn(out.a.y, out.l) : 0.f) << 16;
-    w.y = (uint32_t)f32_to_bf16_bits(any ? __fdiv_rn(out.a.z, out.l) : 0.f) |
-          (uint32_t)f32_to_bf16_bits(any ? __fdiv_rn(out.a.w, out.l) : 0.f) << 16;
-    *reinterpret_cast<uint2*>(p.out + row * D + col) = w;
+    if (mine && set == 0) write_out(p, (int64_t)row * D + col, out);
+    if constexpr (SETS > 1) __syncthreads();
   }
 }
 
@@ -1162,7 +1316,7 @@ __global__ void __launch_bounds__(SETS == 32 ? 1024 : 256) kv_combine_kernel(con
 struct Layout {
   int RP, TQ, gmax, grid, t_slots;
   bool fits;  // positions on the line and rows of group results fit in 31 bits
-  size_t starts, g_acc, g_ml, t_acc, t_ml, bytes;
+  size_t g_acc, g_ml, t_acc, t_ml, bytes;
 };
 
 template <int D>
@@ -1195,10 +1349,9 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   const int full = kSms * ctas_per_sm(dim, y.RP);
   y.grid = most < full ? (int)most : full;
   const int64_t range = (most + y.grid - 1) / y.grid;
-  y.t_slots = (int)(range < 2 * (kGroupTiles - 1) ? range : 2 * (kGroupTiles - 1));
+  y.t_slots = (int)(range < kGroupTiles ? range : kGroupTiles);  // a range's first seven tiles at most, and its end
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-  y.starts = 0;
-  y.g_acc = up(4 * ((size_t)B + 1));
+  y.g_acc = 0;
   y.g_ml = y.g_acc + up((size_t)y.gmax * T * q_heads * dim * 4);
   y.t_acc = y.g_ml + up((size_t)y.gmax * T * q_heads * 8);
   y.t_ml = y.t_acc + up((size_t)y.grid * y.t_slots * y.RP * dim * 4);
@@ -1241,24 +1394,19 @@ cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int 
   cfg.blockDim = dim3(X::kThreads);
   cfg.dynamicSmemBytes = (size_t)X::kSmem;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, RP>, maps, p)) return e;
+  if (y.gmax == 1) return cudaSuccess;
   const int64_t out_rows = (int64_t)a.T * a.q_heads;
   cfg.dynamicSmemBytes = 0;
-  // at most eight groups a row: a thread set per row; else the row's chains over eight sets, or over 32 where that
-  // would leave SMs without a CTA
-  if (y.gmax <= 8) {
-    constexpr int kRowsPer = 256 / (D / 4);
-    cfg.gridDim = dim3((unsigned)((out_rows + kRowsPer - 1) / kRowsPer));
-    cfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 1>, p);
+  if (y.gmax > 16 && out_rows * (D / 32) <= 2 * kSms) {
+    cfg.gridDim = dim3((unsigned)out_rows, D / 32);
+    cfg.blockDim = dim3(1024);
+    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 128>, p);
   }
-  constexpr int kCols = D < 128 ? D : 128;
-  cfg.gridDim = dim3((unsigned)out_rows, D / kCols);
-  if (out_rows * (D / kCols) >= kSms) {
-    cfg.blockDim = dim3(8 * kCols / 4);
-    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 8>, p);
-  }
-  cfg.blockDim = dim3(32 * kCols / 4);
-  return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 32>, p);
+  const int sets = y.gmax <= 8 ? 1 : 4, per = 256 / (D / 4) / sets;
+  const int64_t ctas = (out_rows + per - 1) / per;
+  cfg.gridDim = dim3((unsigned)(ctas < 4 * kSms ? ctas : 4 * kSms));
+  cfg.blockDim = dim3(256);
+  return sets == 1 ? cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 1>, p) : cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 4>, p);
 }
 
 template <int D>
@@ -1305,14 +1453,13 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t 
   p.qk_scale = a.scale * kLog2e;
   p.gmax = y.gmax;
   p.grid = y.grid;
-  p.RP = y.RP;
   p.t_slots = y.t_slots;
-  p.starts = reinterpret_cast<int*>(w + y.starts);
   p.g_acc = reinterpret_cast<float*>(w + y.g_acc);
   p.g_ml = reinterpret_cast<float2*>(w + y.g_ml);
   p.t_acc = reinterpret_cast<float*>(w + y.t_acc);
   p.t_ml = reinterpret_cast<float2*>(w + y.t_ml);
   p.flags = a.flags;
+  p.counters = a.counters;
   switch (a.cache.dim) {
     case 64: return run_d<64>(a, y, p, pdl, s);
     case 128: return run_d<128>(a, y, p, pdl, s);

@@ -116,7 +116,7 @@ def lib() -> ctypes.CDLL:
             ll, f = ctypes.c_int64, ctypes.c_float
             L.w4a16_kv_plan.argtypes = [P] * 10 + [i] * 5 + [P]
             L.w4a16_kv_append.argtypes = [P, ll, P, ll, P, P, i, P]
-            L.w4a16_kv_attention.argtypes = [P, ll, P, P, P, P, P] + [i] * 7 + [f, P, z, P]
+            L.w4a16_kv_attention.argtypes = [P, ll, P, P, P, P, P] + [i] * 7 + [f, P, z, P, P]
             L.w4a16_kv_attention_workspace_bytes.argtypes = [i] * 8
             L.w4a16_kv_attention_workspace_bytes.restype = z
             L.stq1_packed_bytes.argtypes = [i, i]
@@ -574,7 +574,7 @@ def stq1_get_plan(N: int, K: int) -> dict:
 
 # ---- paged key/value cache in 8 bits (include/w4a16.h "Paged key/value cache") --------------
 
-KV_BLOCKS, KV_DIMS, KV_MAX_GROUP = (16, 32, 64, 128), (64, 128, 256), 32
+KV_BLOCKS, KV_DIMS, KV_MAX_GROUP, KV_COUNTERS = (16, 32, 64, 128), (64, 128, 256), 32, 512
 
 
 @dataclass(frozen=True)
@@ -706,6 +706,25 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Ten
         _raise(rc)
 
 
+_kv_counter_cache: dict = {}
+
+
+def _kv_counters(raw_stream: int, device: torch.device) -> int:
+    """The zeroed counters of a stream (kept here, as its workspace is), made on
+    its first use outside graph capture.  A call captured before that gets
+    counters of its own from the graph's memory, zeroed in the graph."""
+    key = (device.index, raw_stream)
+    c = _kv_counter_cache.get(key)
+    if c is None:
+        zeros = torch.zeros(KV_COUNTERS, dtype=torch.int32, device=device)
+        if _capturing():
+            return zeros.data_ptr()
+        torch.cuda.current_stream(device).synchronize()
+        with _ws_lock:
+            c = _kv_counter_cache.setdefault(key, (zeros, zeros.data_ptr()))
+    return c[1]
+
+
 @functools.lru_cache(maxsize=1024)
 def _kv_attention_bytes(*sizes: int) -> int:
     return int(lib().w4a16_kv_attention_workspace_bytes(*sizes))
@@ -750,9 +769,10 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
         wp = workspace.data_ptr() if wn else None
     else:
         wp, wn = _ws_args(workspace)
+    raw = _raw_stream(stream)
     rc = lib().w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, tp, _i32(cu, "cu", B + 1), _i32(lens, "lens", B),
                                   out.data_ptr(), B, T, hq, max_blocks, max_new, max_len, window,
-                                  1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, _raw_stream(stream))
+                                  1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, _kv_counters(raw, dev), raw)
     if rc:
         _raise(rc)
     return out

@@ -83,7 +83,7 @@ def _attend(L, cache_over=None, **over):
     ptr, keep = _cache(**(cache_over or {}))
     return L.w4a16_kv_attention(f["q"], f["qs"], f.get("cache", ptr), f["table"], f["cu"], f["lens"], f["out"], f["B"],
                                 f["T"], f["hq"], f["max_blocks"], f["max_new"], f["max_len"], f["window"], f["scale"],
-                                f["ws"], f["wn"], None)
+                                f["ws"], f["wn"], f.get("counters", P), None)
 
 
 def test_attention_refusals(L, monkeypatch):
@@ -99,10 +99,10 @@ def test_attention_refusals(L, monkeypatch):
         assert _attend(L, **{name: None}) == ops.ERR_NULL, name
         assert _attend(L, **{name: P + 2}) == ops.ERR_ALIGN, name
     assert _attend(L, qs=1028) == ops.ERR_ALIGN and _attend(L, out=P + 8) == ops.ERR_ALIGN
-    assert _attend(L, ws=P + 128) == ops.ERR_ALIGN
+    assert _attend(L, ws=P + 128) == ops.ERR_ALIGN and _attend(L, counters=P + 2) == ops.ERR_ALIGN
     n = L.w4a16_kv_attention_workspace_bytes(2, 3, 8, 2, 128, 2, 64, 0)
-    if n:
-        assert _attend(L, ws=None, wn=0) == ops.ERR_NULL and _attend(L, wn=n - 1) == ops.ERR_SHAPE
+    assert n > 0 and _attend(L, ws=None, wn=0) == ops.ERR_NULL and _attend(L, wn=n - 1) == ops.ERR_SHAPE
+    assert _attend(L, counters=None) == ops.ERR_NULL
     monkeypatch.setenv("W4A16_FAULT", "launch")
     L.w4a16_debug_reload_env()
     assert _attend(L) == ops.ERR_CUDA and "injected" in L.w4a16_last_error().decode()
