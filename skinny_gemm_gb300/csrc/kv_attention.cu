@@ -76,6 +76,8 @@ constexpr int kGroupBegin = 8; // first tile of a group folded here
 constexpr int kGroupEnd = 16;  // its last tile
 constexpr int kPart = 32;      // the result goes to a slot for parts of divided groups
 constexpr int kDirect = 64;    // the segment is this one group, and whole
+constexpr int kLastPart = 128; // the range's last part of a divided group
+constexpr int kTail = 256;     // ... which goes on in the next range (else it began in an earlier one)
 
 struct Desc {
   int flags, h, j0, tile;      // key head, first token of the row tile in its request
@@ -99,21 +101,22 @@ struct CutGroup {
 // shared memory holds, in as many CTAs as registers leave room for.
 template <int D, int RP>
 struct Geo {
-  static constexpr int R = RP < 16 ? RP : 16;
+  static constexpr int R = RP == 24 ? 12 : RP < 16 ? RP : 16;
   static constexpr int kGroups = RP / R;
   static constexpr int kThreads = 256 * kGroups + 96;
-  static constexpr int kCols = RP < 8 ? 16 : 2 * RP;           // columns of S and O: first and second terms
+  static constexpr int kCols = (2 * RP + 15) / 16 * 16;        // columns of S and O: first and second terms
   static constexpr int kPanels = D <= 128 ? 1 : D / 128;       // 128-byte column panels of K and V
   static constexpr int kRowB = D <= 128 ? D : 128;             // bytes of a panel's row
   static constexpr int kPanelBytes = kTile * kRowB;
   static constexpr int kSlot = kTile * D;
   static constexpr int kQ = kPanels * kCols * 128;
-  static constexpr int kStage = RP * D * 2;                    // a segment's query rows as they come
+  // a segment's query rows as they come, ahead of its turn; larger row tiles have fewer segments and better uses for it
+  static constexpr int kStage = RP <= 8 ? RP * D * 2 : 0;
   static constexpr int kP = kTile * kCols;
-  static constexpr int kCtas = RP == 4 ? (D == 256 ? 2 : 3) : RP == 8 ? 2 : RP == 16 ? (D == 256 ? 1 : 2) : 1;
-  static constexpr int kSlots = RP <= 8 ? (D == 256 ? 3 : D == 128 ? (RP == 4 ? 4 : 6) : 6)
-                                : RP == 16 ? (D == 256 ? 6 : D == 128 ? 5 : 8) : D == 256 ? 5 : D == 128 ? 10 : 12;
-  static constexpr int kBars = 2 * kSlots + 3 * kDescs + 4 + kRing + 4 + 5 + kGroups;
+  static constexpr int kCtas = RP == 4 ? (D == 256 ? 2 : 3) : RP == 8 ? 2 : RP <= 16 ? (D == 256 ? 1 : 2) : 1;
+  static constexpr int kSlots = D == 256 ? (RP <= 8 ? 3 : RP <= 24 ? 6 : 5)
+                                : D == 128 ? (RP == 4 ? 4 : RP == 8 ? 6 : RP <= 16 ? 5 : 10) : RP <= 8 ? 6 : RP <= 16 ? 8 : 12;
+  static constexpr int kBars = 2 * kSlots + 3 * kDescs + 4 + kRing + 4 + 6 + kGroups;
   // rows (bits) of a tile that see a NaN in a thread's columns
   using Marks = std::conditional_t<(kPanels * R > 16), uint32_t, uint16_t>;
   // warps' maxima (two tiles), sums (kRing tiles x four warps), maxima (kRing), fold factors per warp, row factors and
@@ -280,11 +283,17 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
     tmem_ld8(addr, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 16) {
+    for (int i = 0; i + 16 <= N; i += 16) {
       float t[16];
       tmem_ld16(addr + i, t);
 #pragma unroll
       for (int k = 0; k < 16; ++k) v[i + k] = t[k];
+    }
+    if constexpr (N % 16 == 8) {
+      float t[8];
+      tmem_ld8(addr + N - 8, t);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[N - 8 + k] = t[k];
     }
   }
 }
@@ -423,7 +432,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   auto p_full = [&](int i) { return bars2 + 8u * (8 + i); };         // [kRing] weights, sums and maxima written
   const uint32_t q_full = bars2 + 8u * (8 + kRing), drained = q_full + 8, all_sync = q_full + 16;
   const uint32_t st_full = q_full + 24, st_free = q_full + 32;       // staged query rows
-  auto grp_sync = [&](int g) { return q_full + 40 + 8u * g; };       // the four softmax warps of a group
+  const uint32_t landed = q_full + 40;                               // parts, at the CTA's end
+  auto grp_sync = [&](int g) { return q_full + 48 + 8u * g; };       // the four softmax warps of a group
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_mem + X::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_nan = reinterpret_cast<volatile int*>(s_tmem + 2);  // [kRing] 1 + a tile whose marks are in s_taint
@@ -473,8 +483,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
     }
   } else if (warp == W_LIST) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // (after the wait: what the next kernel reads of this call's inputs is there when it starts)
     int mine_end = 0;         // inclusive prefix of this lane's request
     int rows = 0;             // of valid requests
     auto scan = [&]() {       // loads 32 requests; their inclusive prefix of tiles after `total`
@@ -558,12 +568,13 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     }
     mbar_init(q_full, 4 * NG);
     mbar_init(drained, 1);
+    mbar_init(landed, 1);
     mbar_init(all_sync, 4 * NG);
     mbar_init(st_full, 1);
     mbar_init(st_free, 4 * NG);
     for (int i = 0; i < NG; ++i) mbar_init(grp_sync(i), 4);
     *s_abort = 0;
-    s_cut[0].mine = s_cut[1].mine = 0;
+    s_last[0] = s_last[1] = 0;
     fence_barrier_init();
   }
   tc_fence_before_sync();
@@ -584,11 +595,18 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       // the group's first tile begins a fold, its last ends it; a cut ends it, too, and after one every tile is by itself
       const bool late = g_lo < beg, part = late || g_hi >= end;
       int fl = (fresh_seg ? kNewSeg : 0) | (part ? kPart : 0) | (x == g_lo || late ? kGroupBegin : 0) |
-               (x == g_hi || x + 1 == end || late ? kGroupEnd : 0);
+               (x == g_hi || x + 1 == end || late ? kGroupEnd : 0) |
+               (part && (x == g_hi || x + 1 == end) ? kLastPart : 0) | (late ? 0 : kTail);
       const int at = !part ? tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles
                            : (int)blockIdx.x * p.t_slots + (late ? x - beg : p.t_slots - 1);
       const bool single = t_first / kGroupTiles == t_last / kGroupTiles;
       if (!(fl & kPart) && single) fl |= kDirect;
+      if (part && lane == 0) {  // for the CTA's end
+        const int k = !late;
+          const int owner = k ? (int)blockIdx.x : cut.owner(g_lo);
+          s_cut[k] = CutGroup{owner, g_lo, g_hi - g_lo + 1, min(end, g_hi + 1) - max(beg, g_lo), r.c0, j0, h, toks,
+                              tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles, single};
+      }
       const bool valid = id >= 0 && id < p.blocks;
       const unsigned need = __ballot_sync(0xffffffffu, id != -2), have = __ballot_sync(0xffffffffu, valid);
       if (need != have || tile * kTile + kTile - 1 > pos0 || (p.window > 0 && tile * kTile < pos1 - p.window + 1)) fl |= kFix;
@@ -612,14 +630,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       __syncwarp();
       if (lane == 0) mbar_arrive(d_full(ds));
       cp_async_arrive(d_scales(ds));
-      if (fl & kPart) {  // for the CTA's end
-        const int k = !late;
-        if (lane == 0) {
-          const int owner = k ? (int)blockIdx.x : cut.owner(g_lo);
-          s_cut[k] = CutGroup{owner, g_lo, g_hi - g_lo + 1, min(end, g_hi + 1) - max(beg, g_lo), r.c0, j0, h, toks,
-                              tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles, single};
-        }
-      }
       // the next tile
       const bool same = tile < t_last;
       if (x + 1 < end) {
@@ -689,7 +699,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           tma_load_2d(slots + slot * X::kSlot + panel * X::kPanelBytes + blk * block * X::kRowB, kv ? &maps.v : &maps.k,
                       panel * 128, row, full(slot));
         ++loads;
-        if (kv == 0 && (dd.x & kNewSeg)) {  // the segment's query rows, a copy per token
+        if (X::kStage > 0 && kv == 0 && (dd.x & kNewSeg)) {  // the segment's query rows, a copy per token
           if (seg > 0 && !(ok = wait_warp(st_free, (seg - 1) & 1))) break;
           const uint32_t bytes = (uint32_t)(p.G * D * 2);
           if (lane == 0) mbar_expect_tx(st_full, toks * bytes);
@@ -781,20 +791,23 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       if (fl & kNewSeg) {
         const int j0 = de.j0, toks = min(p.TQ, de.fresh - j0);
         sync_all();  // nobody looks at the last segment's limits and factors any more
-        ok &= wait_warp(st_full, seg++ & 1);
+        if (X::kStage > 0) ok &= wait_warp(st_full, seg++ & 1);
         if (!ok) break;
         // query rows as e4m3 terms: TPR threads a row
-        constexpr int TPR = 128 * NG / RP, CPT = (D / 8 + TPR - 1) / TPR;
+        constexpr int TPR = RP <= 8 ? 128 / RP : 8, CPT = (D / 8 + TPR - 1) / TPR;
         const int row = tid / TPR, c = tid % TPR;
         const int j = row / p.G;
-        const bool live = j < toks;
+        const bool live = row < RP && j < toks;
         uint4 v[CPT];
         uint32_t peak = 0;
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
           v[i] = make_uint4(0, 0, 0, 0);
           const int ch = c + i * TPR;
-          if (live && ch < D / 8) v[i] = *reinterpret_cast<const uint4*>(stage + row * (2 * D) + ch * 16);
+          if (live && ch < D / 8)
+            v[i] = X::kStage > 0 ? *reinterpret_cast<const uint4*>(stage + row * (2 * D) + ch * 16)
+                                 : ld_nc_v4(p.q + (int64_t)(de.c0 + j0 + j) * p.q_stride +
+                                            (int64_t)(de.h * p.G + row - j * p.G) * D + 8 * ch);
         }
 #pragma unroll
         for (int i = 0; i < CPT; ++i)
@@ -811,7 +824,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
           const int ch = c + i * TPR;
-          if (ch < D / 8) {
+          if (row < RP && ch < D / 8) {
             float f[8];
             widen8(v[i], f);
             uint32_t hi[4], lo[4];
@@ -827,7 +840,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
             *at(n + R) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
           }
         }
-        if (c == 0) {
+        if (c == 0 && row < RP) {
           const float unit = __uint_as_float((uint32_t)(127 + e) << 23);
           // a row with a NaN or an infinity is NaN as a whole
           s_qf[row] = peak >= 0x7F80 ? __uint_as_float(0x7FC00000u) : __fmul_rn(unit, p.qk_scale);
@@ -838,7 +851,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(q_full);
-          mbar_arrive(st_free);
+          if (X::kStage > 0) mbar_arrive(st_free);
         }
         sync_all();
         if (!ok) break;
@@ -982,8 +995,16 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         // column 2 R grp + (R first terms, R second) of the weights: 16 columns a 16-byte row of a token, 2048 bytes on
         // the next 16
         uint8_t* dst = p_mem + par * X::kP + (2 * R * grp / 16) * 2048 + tt * 16;
-        if (R == 4) {
+        if constexpr (R == 4) {
           *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], 0, 0);
+        } else if constexpr (R == 12) {  // 24 bytes: the second group's begin in the middle of a 16-byte row
+          if (grp == 0) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint2*>(dst + 2048) = make_uint2(w[4], w[5]);
+          } else {
+            *reinterpret_cast<uint2*>(dst + 8) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint4*>(dst + 2048) = make_uint4(w[2], w[3], w[4], w[5]);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < R / 8; ++i)
@@ -993,23 +1014,25 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       fence_proxy_async();
       // row sums of p / vs over the warp: halves exchanged until a lane has one row, then added (one tree for every R)
       const float iv = __uint_as_float((uint32_t)(127 - ve) << 23);
-#pragma unroll
-      for (int i = 0; i < R; ++i) s[i] = __fmul_rn(s[i], iv);
       {
+        constexpr int N = R == 12 ? 16 : R;  // (a power of two)
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < R ? __fmul_rn(s[i < R ? i : 0], iv) : 0.f;
         int off = 16;
 #pragma unroll
-        for (int n = R / 2; n; n >>= 1, off >>= 1) {
+        for (int n = N / 2; n; n >>= 1, off >>= 1) {
           const bool up = lane & off;
 #pragma unroll
           for (int i = 0; i < n; ++i) {
-            const float give = up ? s[i] : s[i + n], keep = up ? s[i + n] : s[i];
-            s[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, off));
+            const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, off));
           }
         }
 #pragma unroll
-        for (; off; off >>= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], off));
-        constexpr int kRep = 32 / R;  // lanes with the same row
-        if (lane % kRep == 0) s_sum[(ring * 4 + w4) * RP + R * grp + lane / kRep] = s[0];
+        for (; off; off >>= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
+        constexpr int kRep = 32 / N;  // lanes with the same row
+        if (lane % kRep == 0 && lane / kRep < R) s_sum[(ring * 4 + w4) * RP + R * grp + lane / kRep] = v[0];
       }
       __syncwarp();
       if (lane == 0) {
@@ -1111,6 +1134,22 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           const int64_t row = row0 + lane + (part ? 0 : (int64_t)jl * (p.q_heads - p.G));
           (part ? p.t_ml : p.g_ml)[row] = make_float2(m_run, l_run);
         }
+        if (fl & kLastPart) {
+          // this range's parts are written: counted warp by warp; whoever counts the last will go on with the fold
+          const int k = fl & kTail ? 1 : 0;
+          asm volatile("fence.proxy.async;" ::: "memory");  // (they are read by bulk copies)
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) {
+            int* n = p.counters + s_cut[k].owner;
+            const int mine = s_cut[k].mine;
+            if (atomicAdd(n, mine) + mine == 4 * NG * s_cut[k].count) {
+              *n = 0;
+              s_last[k] = 1;
+              __threadfence();
+            }
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(d_free(ds));
@@ -1138,10 +1177,12 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   //
   // A divided group's fold, acc = acc al_k + O_k be_k over its parts k (the
   // first range's fold, then tiles), takes its factors from the parts' (m, l)
-  // alone: a thread per row works them out, while a thread per four columns has
-  // all its loads in flight at once.
+  // alone: a thread per row works them out while the O_k are on their way, to a
+  // thread per few columns (few rows: all its loads in flight at once) or by
+  // bulk copy to shared memory (16 rows x 1 KB a part and more: 90 KB in 1.8
+  // instead of 4 us).
   constexpr int NT = X::kThreads, V = X::kCtas > 2 ? 2 : 4;  // columns a thread takes (registers)
-  if (s_cut[0].mine | s_cut[1].mine) {
+  if (s_last[0] | s_last[1]) {
     float2* w_ab = reinterpret_cast<float2*>(base);   // [2][RP][kGroupTiles]
     float2* w_ml = w_ab + 2 * RP * kGroupTiles;       // [2][RP]
     int* w_slot = reinterpret_cast<int*>(w_ml + 2 * RP);  // [2][kGroupTiles]
@@ -1149,75 +1190,38 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     if (tid < 2 * kGroupTiles) {
       const CutGroup& c = s_cut[tid / kGroupTiles];
       const int z = tid % kGroupTiles;
-      if (c.mine) {
+      if (s_last[tid / kGroupTiles]) {
         const Cut cut(s_rest[1], p.grid);
         const int x = cut.begin(c.owner + 1) + z - 1, own = z ? cut.owner(x) : c.owner;  // part z: a tile after the first range
         w_slot[tid] = own * p.t_slots + (z ? x - cut.begin(own) : p.t_slots - 1);
         if (z == 0) w_parts[tid / kGroupTiles] = c.first + c.count - x;
       }
     }
-    __threadfence();  // this CTA's tile results
     __syncthreads();
-    if (tid < 2) {
-      const CutGroup& c = s_cut[tid];
-      bool last = false;
-      if (c.mine) {
-        last = atomicAdd(p.counters + c.owner, c.mine) + c.mine == c.count;
-        if (last) p.counters[c.owner] = 0;
-        __threadfence();
-      }
-      s_last[tid] = last;
-    }
-    __syncthreads();
+    uint32_t n_landed = 0;
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       if (!s_last[k]) continue;
       const CutGroup& c = s_cut[k];
       const int count = w_parts[k], rows = c.toks * p.G;
-      bool weights = false;
-      for (int i = tid; i < (rows * (D / V) + NT - 1) / NT * NT; i += NT) {
-        const int rr = i / (D / V), col = V * (i - rr * (D / V)), jj = rr / p.G;
-        float v[kGroupTiles][V];
+      auto weights = [&]() {  // of the parts, row by row
+        if (tid < rows) {
+          float2 ml[kGroupTiles];
 #pragma unroll
-        for (int z = 0; z < kGroupTiles; ++z) {
-          const bool is = z < count && rr < rows;
-          const float* from = p.t_acc + ((int64_t)(is ? w_slot[k * kGroupTiles + z] : 0) * RP + (is ? rr : 0)) * D + col;
-          if constexpr (V == 4) {
-            const float4 u = is ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
-          } else {
-            const float2 u = is ? __ldcg(reinterpret_cast<const float2*>(from)) : make_float2(0.f, 0.f);
-            v[z][0] = u.x, v[z][1] = u.y;
+          for (int z = 0; z < kGroupTiles; ++z)
+            ml[z] = z < count ? __ldcg(p.t_ml + w_slot[k * kGroupTiles + z] * RP + tid) : make_float2(-INFINITY, 0.f);
+          float m = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int z = 0; z < kGroupTiles; ++z) {
+            float al, be;
+            fold_ml(m, l, ml[z].x, ml[z].y, al, be);
+            w_ab[(k * RP + tid) * kGroupTiles + z] = make_float2(al, be);
           }
+          w_ml[k * RP + tid] = make_float2(m, l);
         }
-        if (!weights) {  // (the first time round, while those are on their way)
-          weights = true;
-          if (tid < rows) {
-            float2 ml[kGroupTiles];
-#pragma unroll
-            for (int z = 0; z < kGroupTiles; ++z)
-              ml[z] = z < count ? __ldcg(p.t_ml + w_slot[k * kGroupTiles + z] * RP + tid) : make_float2(-INFINITY, 0.f);
-            float m = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int z = 0; z < kGroupTiles; ++z) {
-              float al, be;
-              fold_ml(m, l, ml[z].x, ml[z].y, al, be);
-              w_ab[(k * RP + tid) * kGroupTiles + z] = make_float2(al, be);
-            }
-            w_ml[k * RP + tid] = make_float2(m, l);
-          }
-          __syncthreads();
-        }
-        if (rr >= rows) continue;
-        float a[V];
-#pragma unroll
-        for (int q = 0; q < V; ++q) a[q] = 0.f;
-#pragma unroll
-        for (int z = 0; z < kGroupTiles; ++z) {
-          const float2 ab = w_ab[(k * RP + rr) * kGroupTiles + z];
-#pragma unroll
-          for (int q = 0; q < V; ++q) a[q] = __fmaf_rn(a[q], ab.x, __fmul_rn(v[z][q], ab.y));
-        }
+      };
+      auto put = [&](int rr, int col, const float (&a)[V]) {
+        const int jj = rr / p.G;
         const float2 ml = w_ml[k * RP + rr];
         const int64_t row = (int64_t)(c.c0 + c.j0 + jj) * p.q_heads + c.h * p.G + rr - jj * p.G;
         if (c.single) {
@@ -1231,6 +1235,91 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
           for (int q = 0; q < V; q += 2) *reinterpret_cast<float2*>(p.g_acc + at * D + col + q) = make_float2(a[q], a[q + 1]);
           if (col == 0) p.g_ml[at] = ml;
+        }
+      };
+      if constexpr (RP >= 12) {
+        constexpr int kItems = (RP * (D / V) + NT - 1) / NT;        // of a thread, at most
+        constexpr int kFrom = 8192, kPartBytes = RP * D * 4;        // copies land after the factors
+        constexpr int kBatch = (NS * X::kSlot - kFrom) / kPartBytes;  // parts at once
+        static_assert(kBatch >= 4 && 2 * RP * (kGroupTiles + 1) * 8 + 128 <= kFrom, "shared memory of a CTA's end");
+        float a[kItems][V];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+#pragma unroll
+          for (int q = 0; q < V; ++q) a[i][q] = 0.f;
+#pragma unroll 1
+        for (int z0 = 0; z0 < count; z0 += kBatch) {
+          const int n = min(kBatch, count - z0);
+          if (tid == 0) {
+            asm volatile("fence.proxy.async;" ::: "memory");
+            mbar_expect_tx(landed, (uint32_t)(n * rows * D * 4));
+            for (int z = 0; z < n; ++z)
+              bulk_load(smem_u32(base) + kFrom + z * kPartBytes, p.t_acc + (int64_t)w_slot[k * kGroupTiles + z0 + z] * RP * D,
+                        (uint32_t)(rows * D * 4), landed, policy_evict_first());
+          }
+          if (z0 == 0) weights();
+          const bool there = mbar_wait_parked(landed, n_landed++ & 1);
+          if (!__syncthreads_and(there)) {
+            if (tid == 0) {
+              atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
+              mbar_wait_parked(landed, (n_landed - 1) & 1);
+            }
+            __syncthreads();
+            return;
+          }
+#pragma unroll
+          for (int i = 0; i < kItems; ++i) {
+            const int at = tid + i * NT, rr = at / (D / V), col = V * (at - rr * (D / V));
+            if (rr < rows)
+              for (int z = 0; z < n; ++z) {
+                const float4 v = *reinterpret_cast<const float4*>(base + kFrom + z * kPartBytes + (rr * D + col) * 4);
+                const float2 ab = w_ab[(k * RP + rr) * kGroupTiles + z0 + z];
+                a[i][0] = __fmaf_rn(a[i][0], ab.x, __fmul_rn(v.x, ab.y));
+                a[i][1] = __fmaf_rn(a[i][1], ab.x, __fmul_rn(v.y, ab.y));
+                a[i][2] = __fmaf_rn(a[i][2], ab.x, __fmul_rn(v.z, ab.y));
+                a[i][3] = __fmaf_rn(a[i][3], ab.x, __fmul_rn(v.w, ab.y));
+              }
+          }
+          __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          const int at = tid + i * NT, rr = at / (D / V);
+          if (rr < rows) put(rr, V * (at - rr * (D / V)), a[i]);
+        }
+      } else {
+        bool first = true;
+        for (int i = tid; i < (rows * (D / V) + NT - 1) / NT * NT; i += NT) {
+          const int rr = i / (D / V), col = V * (i - rr * (D / V));
+          float v[kGroupTiles][V];
+#pragma unroll
+          for (int z = 0; z < kGroupTiles; ++z) {
+            const bool is = z < count && rr < rows;
+            const float* from = p.t_acc + ((int64_t)(is ? w_slot[k * kGroupTiles + z] : 0) * RP + (is ? rr : 0)) * D + col;
+            if constexpr (V == 4) {
+              const float4 u = is ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
+              v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
+            } else {
+              const float2 u = is ? __ldcg(reinterpret_cast<const float2*>(from)) : make_float2(0.f, 0.f);
+              v[z][0] = u.x, v[z][1] = u.y;
+            }
+          }
+          if (first) {
+            first = false;
+            weights();
+            __syncthreads();
+          }
+          if (rr >= rows) continue;
+          float a[V];
+#pragma unroll
+          for (int q = 0; q < V; ++q) a[q] = 0.f;
+#pragma unroll
+          for (int z = 0; z < kGroupTiles; ++z) {
+            const float2 ab = w_ab[(k * RP + rr) * kGroupTiles + z];
+#pragma unroll
+            for (int q = 0; q < V; ++q) a[q] = __fmaf_rn(a[q], ab.x, __fmul_rn(v[z][q], ab.y));
+          }
+          put(rr, col, a);
         }
       }
     }
@@ -1263,7 +1352,7 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
   const int set = threadIdx.x / LANES % SETS, sub = threadIdx.x / (LANES * SETS), c = threadIdx.x % LANES;
   const int col = (SETS == 128 ? (int)blockIdx.y * 32 : 0) + 4 * c, rows = p.T * p.q_heads;
   pdl_launch_dependents();
-  pdl_wait();
+  bool waited = false;  // the first row's request is looked up before the wait (the attention kernel has waited for those)
   for (int row0 = (int)blockIdx.x * kPer; row0 < rows; row0 += kPer * (int)gridDim.x) {
     const int row = min(row0 + sub, rows - 1), t = row / p.q_heads, hq = row - t * p.q_heads;
     int b = min(t / p.max_new, p.B - 1);  // right where every request has max_new new tokens
@@ -1279,8 +1368,10 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
     const bool mine = row0 + sub < rows && j >= 0 && j < r.fresh &&
                       first_tile(p, r, rt) / kGroupTiles != last_tile(p, r, rt) / kGroupTiles;
     State out = empty_state();
+    const RowGroups<D> g(p, r, j, hq);
+    if (!waited) pdl_wait();
+    waited = true;
     if (mine) {
-      const RowGroups<D> g(p, r, j, hq);
       if constexpr (SETS == 1) {
         State st[8];
 #pragma unroll
@@ -1309,6 +1400,7 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
     if (mine && set == 0) write_out(p, (int64_t)row * D + col, out);
     if constexpr (SETS > 1) __syncthreads();
   }
+  if (!waited) pdl_wait();
 }
 
 // ---- host side -----------------------------------------------------------------------------------
@@ -1321,7 +1413,14 @@ struct Layout {
 
 template <int D>
 int ctas_d(int RP) {
-  return RP == 4 ? Geo<D, 4>::kCtas : RP == 8 ? Geo<D, 8>::kCtas : RP == 16 ? Geo<D, 16>::kCtas : Geo<D, 32>::kCtas;
+  switch (RP) {
+    case 4: return Geo<D, 4>::kCtas;
+    case 8: return Geo<D, 8>::kCtas;
+    case 12: return Geo<D, 12>::kCtas;
+    case 16: return Geo<D, 16>::kCtas;
+    case 24: return Geo<D, 24>::kCtas;
+    default: return Geo<D, 32>::kCtas;
+  }
 }
 int ctas_per_sm(int dim, int RP) { return dim == 64 ? ctas_d<64>(RP) : dim == 128 ? ctas_d<128>(RP) : ctas_d<256>(RP); }
 
@@ -1330,8 +1429,9 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   const int G = q_heads / heads;
   if (max_new > T) max_new = T;
   const int64_t rows = (int64_t)G * max_new;
-  y.RP = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  while (y.RP < G) y.RP *= 2;
+  // the smallest row tile that holds the step's rows of a key head, or 32 rows, and at least one token
+  const int64_t hold = rows < 32 ? rows : G > 32 ? G : 32;
+  y.RP = hold <= 4 ? 4 : hold <= 8 ? 8 : hold <= 12 ? 12 : hold <= 16 ? 16 : hold <= 24 ? 24 : 32;
   y.TQ = y.RP / G;
   int64_t groups = ((int64_t)max_len + kGroupTokens - 1) / kGroupTokens;
   if (window > 0) {
@@ -1360,7 +1460,7 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
 }
 
 std::mutex g_attr_mu;
-bool g_attr[64][12] = {};
+bool g_attr[64][3][33] = {};
 
 template <int D, int RP>
 cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int pdl, cudaStream_t s) {
@@ -1370,7 +1470,7 @@ cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int 
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   {
     std::lock_guard<std::mutex> lk(g_attr_mu);
-    bool& done = g_attr[dev][(D == 64 ? 0 : D == 128 ? 4 : 8) + (RP == 4 ? 0 : RP == 8 ? 1 : RP == 16 ? 2 : 3)];
+    bool& done = g_attr[dev][D == 64 ? 0 : D == 128 ? 1 : 2][RP];
     if (!done) {
       if (cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, X::kSmem))
         return e;
@@ -1404,7 +1504,7 @@ cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int 
   }
   const int sets = y.gmax <= 8 ? 1 : 4, per = 256 / (D / 4) / sets;
   const int64_t ctas = (out_rows + per - 1) / per;
-  cfg.gridDim = dim3((unsigned)(ctas < 4 * kSms ? ctas : 4 * kSms));
+  cfg.gridDim = dim3((unsigned)(ctas < 6 * kSms ? ctas : 6 * kSms));
   cfg.blockDim = dim3(256);
   return sets == 1 ? cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 1>, p) : cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 4>, p);
 }
@@ -1414,6 +1514,8 @@ cudaError_t run_d(const KvAttentionArgs& a, const Layout& y, const Params& p, in
   switch (y.RP) {
     case 4: return run<D, 4>(a, y, p, pdl, s);
     case 8: return run<D, 8>(a, y, p, pdl, s);
+    case 12: return run<D, 12>(a, y, p, pdl, s);
+    case 24: return run<D, 24>(a, y, p, pdl, s);
     case 16: return run<D, 16>(a, y, p, pdl, s);
     default: return run<D, 32>(a, y, p, pdl, s);
   }
