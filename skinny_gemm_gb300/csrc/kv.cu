@@ -184,12 +184,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
 // chunks a lane) or, if it is longer or the block's earlier rows have to be
 // re-coded, to the whole CTA.  A CTA looks at `per` consecutive tokens for one
 // head of K or V: eight where few tokens are new (a warp each: decode and
-// verify are one latency chain), 64 for prompt chunks, whose runs are long.
+// verify are one latency chain), 128 for prompt chunks, whose runs are long.
 // Bytes: 2 in and 1 out per element; a run's rows stay in registers between
 // the maximum and the codes.
 
 constexpr int kAppendThreads = 256, kAppendWarps = 8;
-constexpr int kMaxPer = 64;     // tokens of a CTA
+constexpr int kMaxPer = 128;    // tokens of a CTA
 constexpr int kWarpChunks = 8;  // 16-byte chunks a lane holds
 constexpr int kCtaChunks = 8;   // a thread holds of a run that the CTA takes; the rest of a longer one (more than
                                 // 64 rows of 256) is read again, from L2

@@ -113,9 +113,9 @@ struct Geo {
   // a segment's query rows as they come, ahead of its turn; larger row tiles have fewer segments and better uses for it
   static constexpr int kStage = RP <= 8 ? RP * D * 2 : 0;
   static constexpr int kP = kTile * kCols;
-  static constexpr int kCtas = RP == 4 ? (D == 256 ? 2 : 3) : RP == 8 ? 2 : RP <= 16 ? (D == 256 ? 1 : 2) : 1;
+  static constexpr int kCtas = RP <= 8 ? 2 : RP <= 16 ? (D == 256 ? 1 : 2) : 1;
   static constexpr int kSlots = D == 256 ? (RP <= 8 ? 3 : RP <= 24 ? 6 : 5)
-                                : D == 128 ? (RP == 4 ? 4 : RP == 8 ? 6 : RP <= 16 ? 5 : 10) : RP <= 8 ? 6 : RP <= 16 ? 8 : 12;
+                                : D == 128 ? (RP <= 8 ? 6 : RP <= 16 ? 5 : 10) : RP <= 16 ? 10 : 12;
   static constexpr int kBars = 2 * kSlots + 3 * kDescs + 4 + kRing + 4 + 6 + kGroups;
   // rows (bits) of a tile that see a NaN in a thread's columns
   using Marks = std::conditional_t<(kPanels * R > 16), uint32_t, uint16_t>;
@@ -1181,7 +1181,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   // thread per few columns (few rows: all its loads in flight at once) or by
   // bulk copy to shared memory (16 rows x 1 KB a part and more: 90 KB in 1.8
   // instead of 4 us).
-  constexpr int NT = X::kThreads, V = X::kCtas > 2 ? 2 : 4;  // columns a thread takes (registers)
+  constexpr int NT = X::kThreads, V = 4;  // columns a thread takes
   if (s_last[0] | s_last[1]) {
     float2* w_ab = reinterpret_cast<float2*>(base);   // [2][RP][kGroupTiles]
     float2* w_ml = w_ab + 2 * RP * kGroupTiles;       // [2][RP]
@@ -1226,14 +1226,13 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         const int64_t row = (int64_t)(c.c0 + c.j0 + jj) * p.q_heads + c.h * p.G + rr - jj * p.G;
         if (c.single) {
           const float f = ml.y != 0.f ? __frcp_rn(ml.y) : 0.f;
-#pragma unroll
-          for (int q = 0; q < V; q += 2)
-            *reinterpret_cast<uint32_t*>(p.out + row * D + col + q) =
-                (uint32_t)f32_to_bf16_bits(__fmul_rn(a[q], f)) | (uint32_t)f32_to_bf16_bits(__fmul_rn(a[q + 1], f)) << 16;
+          uint2 w;
+          w.x = (uint32_t)f32_to_bf16_bits(__fmul_rn(a[0], f)) | (uint32_t)f32_to_bf16_bits(__fmul_rn(a[1], f)) << 16;
+          w.y = (uint32_t)f32_to_bf16_bits(__fmul_rn(a[2], f)) | (uint32_t)f32_to_bf16_bits(__fmul_rn(a[3], f)) << 16;
+          *reinterpret_cast<uint2*>(p.out + row * D + col) = w;
         } else {
           const int64_t at = row + (int64_t)c.gi * p.T * p.q_heads;
-#pragma unroll
-          for (int q = 0; q < V; q += 2) *reinterpret_cast<float2*>(p.g_acc + at * D + col + q) = make_float2(a[q], a[q + 1]);
+          *reinterpret_cast<float4*>(p.g_acc + at * D + col) = make_float4(a[0], a[1], a[2], a[3]);
           if (col == 0) p.g_ml[at] = ml;
         }
       };
@@ -1296,13 +1295,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           for (int z = 0; z < kGroupTiles; ++z) {
             const bool is = z < count && rr < rows;
             const float* from = p.t_acc + ((int64_t)(is ? w_slot[k * kGroupTiles + z] : 0) * RP + (is ? rr : 0)) * D + col;
-            if constexpr (V == 4) {
-              const float4 u = is ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
-              v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
-            } else {
-              const float2 u = is ? __ldcg(reinterpret_cast<const float2*>(from)) : make_float2(0.f, 0.f);
-              v[z][0] = u.x, v[z][1] = u.y;
-            }
+            const float4 u = is ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
           }
           if (first) {
             first = false;
@@ -1351,7 +1345,8 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
   __shared__ State s_set[SETS == 1 ? 1 : kPer * SETS][LANES];
   const int set = threadIdx.x / LANES % SETS, sub = threadIdx.x / (LANES * SETS), c = threadIdx.x % LANES;
   const int col = (SETS == 128 ? (int)blockIdx.y * 32 : 0) + 4 * c, rows = p.T * p.q_heads;
-  pdl_launch_dependents();
+  // (no early launch of what follows: a next attention call's CTAs would fill the SMs unevenly around this kernel's:
+  // 32 ragged requests to 8k back to back 73 instead of 54 us)
   bool waited = false;  // the first row's request is looked up before the wait (the attention kernel has waited for those)
   for (int row0 = (int)blockIdx.x * kPer; row0 < rows; row0 += kPer * (int)gridDim.x) {
     const int row = min(row0 + sub, rows - 1), t = row / p.q_heads, hq = row - t * p.q_heads;

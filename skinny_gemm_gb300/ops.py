@@ -725,6 +725,29 @@ def _kv_counters(raw_stream: int, device: torch.device) -> int:
     return c[1]
 
 
+KV_WORKSPACE_KEPT = 64 << 20  # larger workspaces are not kept between calls
+_kv_ws_cache: dict = {}
+
+
+def _kv_workspace(n: int, raw_stream: int, device: torch.device, stream):
+    """(tensor, address) of n bytes for a call on a stream: the stream's own,
+    kept here and grown when a call needs more, or (large, or under graph
+    capture) one for this call.  It needs no initial contents."""
+    key = (device.index, raw_stream)
+    kept = _kv_ws_cache.get(key)
+    if kept is not None and kept[2] >= n and not _capturing():
+        return kept
+    if stream is None:
+        t = torch.empty(n, dtype=torch.uint8, device=device)
+    else:  # memory of that stream: freed blocks come back in its order
+        with torch.cuda.stream(stream):
+            t = torch.empty(n, dtype=torch.uint8, device=device)
+    kept = (t, t.data_ptr(), n)
+    if n <= KV_WORKSPACE_KEPT and not _capturing():
+        _kv_ws_cache[key] = kept
+    return kept
+
+
 @functools.lru_cache(maxsize=1024)
 def _kv_attention_bytes(*sizes: int) -> int:
     return int(lib().w4a16_kv_attention_workspace_bytes(*sizes))
@@ -743,8 +766,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
 
     table, cu, lens: a plan's; max_new, max_len: the caller's bounds on the
     requests' new tokens and lengths; scale: 1 / sqrt(dim) by default; window:
-    tokens that a row sees, itself included (0: all).  The workspace is
-    allocated here unless one (uint8) is given."""
+    tokens that a row sees, itself included (0: all).  The workspace is this
+    stream's, kept by this module, unless one (uint8) is given."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [T, q_heads, dim]")
     T, hq, dim = q.shape
@@ -760,16 +783,12 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
         _dev_tensor(out, torch.bfloat16, "out")
         if out.shape != q.shape:
             raise ValueError(f"out must be {tuple(q.shape)}")
+    raw = _raw_stream(stream)
     if workspace is None:
         wn = _kv_attention_bytes(B, T, hq, cache.heads, dim, max_new, max_len, window)
-        if wn:
-            workspace = torch.empty(wn, dtype=torch.uint8, device=dev)
-            if stream is not None and stream != torch.cuda.current_stream():
-                workspace.record_stream(stream)
-        wp = workspace.data_ptr() if wn else None
+        workspace, wp, _ = _kv_workspace(wn, raw, dev, stream) if wn else (None, None, 0)
     else:
         wp, wn = _ws_args(workspace)
-    raw = _raw_stream(stream)
     rc = lib().w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, tp, _i32(cu, "cu", B + 1), _i32(lens, "lens", B),
                                   out.data_ptr(), B, T, hq, max_blocks, max_new, max_len, window,
                                   1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, _kv_counters(raw, dev), raw)
