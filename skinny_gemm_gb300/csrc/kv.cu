@@ -182,14 +182,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
 // consecutive slots of one block; one (run, head, K or V) sets the scale of
 // one (block, head), so it belongs to one warp (up to kWarpChunks 16-byte
 // chunks a lane) or, if it is longer or the block's earlier rows have to be
-// re-coded, to the whole CTA.  A CTA looks at `per` consecutive tokens for one
-// head of K or V: eight where few tokens are new (a warp each: decode and
-// verify are one latency chain), 128 for prompt chunks, whose runs are long.
+// re-coded, to the whole CTA.  A CTA looks at `per` consecutive tokens and
+// `hg` heads of K or V, a warp taking every eighth (run, head): neighbouring
+// heads of a token side by side (its row is read in one stretch), as many
+// tokens as give each warp about one run; single heads of 112 tokens where runs
+// are long enough for the whole CTA.
 // Bytes: 2 in and 1 out per element; a run's rows stay in registers between
 // the maximum and the codes.
 
 constexpr int kAppendThreads = 256, kAppendWarps = 8;
-constexpr int kMaxPer = 128;    // tokens of a CTA
+constexpr int kMaxPer = 112, kMaxHeads = 8;  // tokens and heads of a CTA
 constexpr int kWarpChunks = 8;  // 16-byte chunks a lane holds
 constexpr int kCtaChunks = 8;   // a thread holds of a run that the CTA takes; the rest of a longer one (more than
                                 // 64 rows of 256) is read again, from L2
@@ -206,37 +208,40 @@ __device__ __forceinline__ int scale_exp(uint32_t bits) {
   return max(e, kMinExp);
 }
 
-// The largest finite magnitude (bf16 bits) of eight values, and whether any is not finite.
-__device__ __forceinline__ uint32_t peak8(const uint4& v, bool& odd) {
-  uint32_t m = 0;
+// The larger magnitudes (bf16 bits) of eight values and of those before, a pair a word.
+__device__ __forceinline__ uint32_t peak8(const uint4& v, uint32_t m) {
+  m = __vmaxu2(m, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
+  return __vmaxu2(m, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+}
+// (rare) the same without NaN and infinities.
+__device__ __forceinline__ uint32_t finite_peak8(const uint4& v, uint32_t m) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t w = word_of(v, i) & 0x7FFF7FFFu;
-    const uint32_t lo = w & 0xFFFF, hi = w >> 16;
-    const bool blo = lo >= 0x7F80, bhi = hi >= 0x7F80;
-    odd |= blo | bhi;
-    m = max(m, max(blo ? 0u : lo, bhi ? 0u : hi));
+    m = __vmaxu2(m, ((w & 0xFFFFu) >= 0x7F80u ? 0u : w & 0xFFFFu) | (w >= 0x7F800000u ? 0u : w & 0xFFFF0000u));
   }
   return m;
 }
+__device__ __forceinline__ uint32_t larger(uint32_t pair) { return max(pair & 0xFFFFu, pair >> 16); }
 
 // Eight bf16 values times `inv` as e4m3 codes, round to nearest even (one
-// rounding: the product with a power of two is exact).  NaN and infinities
-// become the NaN code (the conversion alone would clamp infinities to 448).
+// rounding: the product with a power of two is exact).  odd: some are not
+// finite; NaN and infinities become the NaN code (the conversion alone would
+// clamp infinities to 448).
 __device__ __forceinline__ uint2 codes8(const uint4& v, float inv, bool odd) {
   float f[8];
   widen8(v, f);
-  uint16_t c[4];
+  if (odd) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x = f[2 * i], y = f[2 * i + 1];
-    if (odd) {
-      if (isinf(x)) x = __uint_as_float(0x7FC00000u);
-      if (isinf(y)) y = __uint_as_float(0x7FC00000u);
-    }
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x, inv), __fmul_rn(y, inv)), __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 8; ++i)
+      if (isinf(f[i])) f[i] = __uint_as_float(0x7FC00000u);
   }
-  return make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f[2 * i], inv), __fmul_rn(f[2 * i + 1], inv)), __NV_SATFINITE,
+                                    __NV_E4M3);
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 // Four e4m3 codes at a larger scale: times `ratio` (a power of two below 1).
@@ -258,19 +263,20 @@ struct AppendParams {
   int shift;   // log2(block)
   int lpr;     // log2(16-byte chunks of a row): dim = 8 << lpr
   int slots;   // blocks * block
-  int per;     // tokens per CTA
+  int per, hg;  // tokens and heads per CTA
 };
 
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendParams p) {
   __shared__ int s_slot[1 + kMaxPer + 128];  // from the token before this CTA's on, as far as a run can reach
-  __shared__ int2 s_job[kMaxPer];            // (token, length) of the runs left to the CTA
+  __shared__ int2 s_job[kMaxPer * kMaxHeads];  // (token << 16 | head, length) of the runs left to the CTA
   __shared__ int s_jobs;
   __shared__ uint32_t s_peak[kAppendWarps];
   const KvAppendArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y, val = blockIdx.z, t0 = blockIdx.x * p.per;
+  const int h0 = blockIdx.y * p.hg, val = blockIdx.z, t0 = blockIdx.x * p.per;
   const int heads = a.cache.heads, dim = a.cache.dim, block = a.cache.block, lpr = p.lpr;
-  const uint16_t* src = (val ? a.v : a.k) + (int64_t)h * dim;
+  const uint16_t* src = val ? a.v : a.k;
+  const int hg = min(p.hg, heads - h0);
   const int64_t stride = val ? a.v_stride : a.k_stride;
   uint8_t* codes = val ? a.cache.v : a.cache.k;
   float* scales = val ? a.cache.v_scale : a.cache.k_scale;
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendPara
     const int t = t0 - 1 + i;
     int s = t >= 0 && t < a.T ? a.slots[t] : -1;
     if (s < -1 || s >= p.slots) {
-      if (h == 0 && val == 0 && i > 0 && i <= p.per) atomicOr(a.flags, W4A16_DEVICE_KV_RANGE);
+      if (h0 == 0 && val == 0 && i > 0 && i <= p.per) atomicOr(a.flags, W4A16_DEVICE_KV_RANGE);
       s = -1;
     }
     s_slot[i] = s;
@@ -294,10 +300,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendPara
   for (int i0 = 0; i0 < p.per; i0 += 32) {
     const int i = i0 + lane, s = i < p.per ? slot_of[i] : -1, before = i < p.per ? slot_of[i - 1] : -1;
     const bool joins = before >= 0 && before + 1 == s && (before >> p.shift) == (s >> p.shift);
-    unsigned leaders = __ballot_sync(0xffffffffu, s >= 0 && !joins);
-    for (; leaders; leaders &= leaders - 1, ++nth) {
-      if ((nth & (kAppendWarps - 1)) != warp) continue;
-      const int ti = i0 + __ffs(leaders) - 1, slot = slot_of[ti];
+    const unsigned leaders = __ballot_sync(0xffffffffu, s >= 0 && !joins);
+    const int count = __popc(leaders) * hg;
+    // (run, head) number nth + q of the CTA, this warp's q
+    for (int q = (warp - nth) & (kAppendWarps - 1); q < count; q += kAppendWarps) {
+      const int which = q / hg, h = h0 + q - which * hg;
+      const int ti = i0 + __fns(leaders, 0, which + 1), slot = slot_of[ti];
       const int blk = slot >> p.shift, off = slot & (block - 1), room = block - off;
       int n = 0;  // tokens of the run
       for (;;) {
@@ -308,25 +316,36 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendPara
       const int chunks = n << lpr;
       bool job = chunks > 32 * kWarpChunks;
       if (!job) {
-        const uint16_t* from = src + (int64_t)(t0 + ti) * stride;
+        // chunk 32 k + lane: the lane's column stays, its row advances
+        const int64_t step = (32 >> lpr) * stride;
+        const uint16_t* from = src + (t0 + ti + (lane >> lpr)) * stride + h * dim + 8 * (lane & ((1 << lpr) - 1));
         const int64_t at = (int64_t)blk * heads + h;
         uint4 v[kWarpChunks];
         const float old = off ? scales[at] : 0.f;
 #pragma unroll
         for (int k = 0; k < kWarpChunks; ++k) {
           if (32 * k >= chunks) break;
-          const int x = 32 * k + lane;
           v[k] = make_uint4(0, 0, 0, 0);
-          if (x < chunks) v[k] = ld_nc_v4(from + (x >> lpr) * stride + 8 * (x & ((1 << lpr) - 1)));
+          if (32 * k + lane < chunks) v[k] = ld_nc_v4(from);
+          from += step;
         }
-        uint32_t peak = 0;
-        bool odd = false;
+        uint32_t pair = 0;
 #pragma unroll
         for (int k = 0; k < kWarpChunks; ++k) {
           if (32 * k >= chunks) break;
-          peak = max(peak, peak8(v[k], odd));
+          pair = peak8(v[k], pair);
         }
-        peak = __reduce_max_sync(0xffffffffu, peak);
+        uint32_t peak = __reduce_max_sync(0xffffffffu, larger(pair));
+        const bool odd = peak >= 0x7F80u;
+        if (odd) {
+          pair = 0;
+#pragma unroll
+          for (int k = 0; k < kWarpChunks; ++k) {
+            if (32 * k >= chunks) break;
+            pair = finite_peak8(v[k], pair);
+          }
+          peak = __reduce_max_sync(0xffffffffu, larger(pair));
+        }
         int e = scale_exp(peak);
         if (off) {
           const int eo = exp_of(old);
@@ -335,51 +354,67 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendPara
         }
         if (!job) {
           const float inv = exp2i(-e);
-          uint8_t* to = codes + ((at << p.shift) + off) * dim;
+          uint8_t* to = codes + ((at << p.shift) + off) * dim + 8 * lane;
 #pragma unroll
           for (int k = 0; k < kWarpChunks; ++k) {
             if (32 * k >= chunks) break;
-            const int x = 32 * k + lane;
-            if (x < chunks) *reinterpret_cast<uint2*>(to + 8 * x) = codes8(v[k], inv, odd);
+            if (32 * k + lane < chunks) *reinterpret_cast<uint2*>(to + 256 * k) = codes8(v[k], inv, odd);
           }
           if (off == 0 && lane == 0) scales[at] = exp2i(e);
         }
       }
-      if (job && lane == 0) s_job[atomicAdd(&s_jobs, 1)] = make_int2(ti, n);
+      if (job && lane == 0) s_job[atomicAdd(&s_jobs, 1)] = make_int2(ti << 16 | h, n);
     }
+    nth += count;
   }
   __syncthreads();
 
   // the CTA's runs, one after another (in no fixed order: they touch different blocks)
   const int jobs = s_jobs;
   for (int w = 0; w < jobs; ++w) {
-    const int ti = s_job[w].x, n = s_job[w].y, slot = slot_of[ti], off = slot & (block - 1);
+    const int ti = s_job[w].x >> 16, h = s_job[w].x & 0xFFFF, n = s_job[w].y, slot = slot_of[ti], off = slot & (block - 1);
     const int64_t at = (int64_t)(slot >> p.shift) * heads + h;
-    const uint16_t* from = src + (int64_t)(t0 + ti) * stride;
+    const int64_t step = (kAppendThreads >> lpr) * stride;
+    const uint16_t* from = src + (t0 + ti + (tid >> lpr)) * stride + h * dim + 8 * (tid & ((1 << lpr) - 1));
     uint4 v[kCtaChunks];
-    uint32_t peak = 0;
-    bool odd = false;
+    uint32_t pair = 0;
     const int chunks = n << lpr;
 #pragma unroll
     for (int k = 0; k < kCtaChunks; ++k) {
       if (k * kAppendThreads >= chunks) break;
-      const int x = k * kAppendThreads + tid;
       v[k] = make_uint4(0, 0, 0, 0);
-      if (x < chunks) v[k] = ld_nc_v4(from + (x >> lpr) * stride + 8 * (x & ((1 << lpr) - 1)));
+      if (k * kAppendThreads + tid < chunks) v[k] = ld_nc_v4(from + k * step);
     }
     const float old = off ? scales[at] : 0.f;
 #pragma unroll
     for (int k = 0; k < kCtaChunks; ++k) {
       if (k * kAppendThreads >= chunks) break;
-      peak = max(peak, peak8(v[k], odd));
+      pair = peak8(v[k], pair);
     }
-    auto rest = [&](int x) { return ld_nc_v4(from + (x >> lpr) * stride + 8 * (x & ((1 << lpr) - 1))); };
-    for (int x = kCtaChunks * kAppendThreads + tid; x < chunks; x += kAppendThreads) peak = max(peak, peak8(rest(x), odd));
-    peak = __reduce_max_sync(0xffffffffu, peak);
-    if (lane == 0) s_peak[warp] = peak;
-    __syncthreads();
+    auto rest = [&](int x) { return ld_nc_v4(from + (x / kAppendThreads) * step); };
+    for (int x = kCtaChunks * kAppendThreads + tid; x < chunks; x += kAppendThreads) pair = peak8(rest(x), pair);
+    auto over_cta = [&]() {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, larger(pair));
+      if (lane == 0) s_peak[warp] = m;
+      __syncthreads();
+      uint32_t all = 0;
 #pragma unroll
-    for (int i = 0; i < kAppendWarps; ++i) peak = max(peak, s_peak[i]);
+      for (int i = 0; i < kAppendWarps; ++i) all = max(all, s_peak[i]);
+      __syncthreads();
+      return all;
+    };
+    uint32_t peak = over_cta();
+    const bool odd = peak >= 0x7F80u;
+    if (odd) {
+      pair = 0;
+#pragma unroll
+      for (int k = 0; k < kCtaChunks; ++k) {
+        if (k * kAppendThreads >= chunks) break;
+        pair = finite_peak8(v[k], pair);
+      }
+      for (int x = kCtaChunks * kAppendThreads + tid; x < chunks; x += kAppendThreads) pair = finite_peak8(rest(x), pair);
+      peak = over_cta();
+    }
     int e = scale_exp(peak);
     uint8_t* base = codes + (at << p.shift) * dim;
     if (off) {
@@ -426,10 +461,22 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, int pdl, cudaStream_t s) {
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int pdl, cudaStream_t s) {
   AppendParams p{a, __builtin_ctz((unsigned)a.cache.block), __builtin_ctz((unsigned)a.cache.dim) - 3,
-                 a.cache.blocks * a.cache.block, a.T >= 2048 ? kMaxPer : kAppendWarps};
+                 a.cache.blocks * a.cache.block, 0, 0};
+  const int heads = a.cache.heads;
+  p.hg = heads < kMaxHeads ? heads : kMaxHeads;
+  // few tokens are taken for runs of one (decode); many for runs of a block, which a warp holds up to 2048 values of
+  if (a.T < 2048) {
+    p.per = kAppendWarps / p.hg;
+  } else if (a.cache.block * a.cache.dim <= 32 * kWarpChunks * 8) {
+    p.per = a.cache.block * (kAppendWarps / p.hg);
+    if (p.per > kMaxPer) p.per = kMaxPer;
+  } else {
+    p.per = kMaxPer;
+    p.hg = 1;
+  }
   void* args[] = {&p};
-  return launch((const void*)kv_append_kernel, dim3((unsigned)((a.T + p.per - 1) / p.per), (unsigned)a.cache.heads, 2),
-                kAppendThreads, args, pdl, s);
+  return launch((const void*)kv_append_kernel,
+                dim3((unsigned)((a.T + p.per - 1) / p.per), (unsigned)((heads + p.hg - 1) / p.hg), 2), kAppendThreads, args, pdl, s);
 }
 
 }  // namespace w4a16
