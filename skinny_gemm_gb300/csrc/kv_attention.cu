@@ -70,7 +70,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // flags of a tile descriptor
 constexpr int kNewSeg = 1;     // another (request, row tile, head) than the tile before
-constexpr int kEnd = 2;        // no tile: the CTA's range is done
+constexpr int kEnd = 2;        // no tile: the CTA's range is empty
 constexpr int kFix = 4;        // some token of the tile is not seen by some row, or its block is not in the cache
 constexpr int kGroupBegin = 8; // first tile of a group folded here
 constexpr int kGroupEnd = 16;  // its last tile
@@ -78,6 +78,8 @@ constexpr int kPart = 32;      // the result goes to a slot for parts of divided
 constexpr int kDirect = 64;    // the segment is this one group, and whole
 constexpr int kLastPart = 128; // the range's last part of a divided group
 constexpr int kTail = 256;     // ... which goes on in the next range (else it began in an earlier one)
+constexpr int kNextSeg = 512;  // the range's next tile begins another segment
+constexpr int kFinal = 1024;   // the range's last tile
 
 struct Desc {
   int flags, h, j0, tile;      // key head, first token of the row tile in its request
@@ -116,7 +118,7 @@ struct Geo {
   static constexpr int kCtas = RP <= 8 ? 2 : RP <= 16 ? (D == 256 ? 1 : 2) : 1;
   static constexpr int kSlots = D == 256 ? (RP <= 8 ? 3 : RP <= 24 ? 6 : 5)
                                 : D == 128 ? (RP <= 8 ? 6 : RP <= 16 ? 5 : 10) : RP <= 16 ? 10 : 12;
-  static constexpr int kBars = 2 * kSlots + 3 * kDescs + 4 + kRing + 4 + 6 + kGroups;
+  static constexpr int kBars = 2 * kSlots + 3 * kDescs + 2 + kRing + 4 + 6 + kGroups;
   // rows (bits) of a tile that see a NaN in a thread's columns
   using Marks = std::conditional_t<(kPanels * R > 16), uint32_t, uint16_t>;
   // warps' maxima (two tiles), sums (kRing tiles x four warps), maxima (kRing), fold factors per warp, row factors and
@@ -426,11 +428,10 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   auto d_scales = [&](int i) { return bars + 8u * (2 * NS + 2 * ND + i); };  // its scales landed
   const uint32_t bars2 = bars + 8u * (2 * NS + 3 * ND);
   auto s_full = [&](int i) { return bars2 + 8u * i; };
-  auto s_free = [&](int i) { return bars2 + 8u * (2 + i); };
-  auto o_full = [&](int i) { return bars2 + 8u * (4 + i); };         // (the weights were read, too)
-  auto o_free = [&](int i) { return bars2 + 8u * (6 + i); };
-  auto p_full = [&](int i) { return bars2 + 8u * (8 + i); };         // [kRing] weights, sums and maxima written
-  const uint32_t q_full = bars2 + 8u * (8 + kRing), drained = q_full + 8, all_sync = q_full + 16;
+  auto o_full = [&](int i) { return bars2 + 8u * (2 + i); };
+  auto o_free = [&](int i) { return bars2 + 8u * (4 + i); };
+  auto p_full = [&](int i) { return bars2 + 8u * (6 + i); };         // [kRing] weights, sums and maxima written
+  const uint32_t q_full = bars2 + 8u * (6 + kRing), drained = q_full + 8, all_sync = q_full + 16;
   const uint32_t st_full = q_full + 24, st_free = q_full + 32;       // staged query rows
   const uint32_t landed = q_full + 40;                               // parts, at the CTA's end
   auto grp_sync = [&](int g) { return q_full + 48 + 8u * g; };       // the four softmax warps of a group
@@ -558,7 +559,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
-      mbar_init(s_free(i), 4 * NG);
       mbar_init(o_full(i), 1);
       mbar_init(o_free(i), 4 * NG);
     }
@@ -596,7 +596,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       const bool late = g_lo < beg, part = late || g_hi >= end;
       int fl = (fresh_seg ? kNewSeg : 0) | (part ? kPart : 0) | (x == g_lo || late ? kGroupBegin : 0) |
                (x == g_hi || x + 1 == end || late ? kGroupEnd : 0) |
-               (part && (x == g_hi || x + 1 == end) ? kLastPart : 0) | (late ? 0 : kTail);
+               (part && (x == g_hi || x + 1 == end) ? kLastPart : 0) | (late ? 0 : kTail) |
+               (x + 1 == end ? kFinal : tile == t_last ? kNextSeg : 0);
       const int at = !part ? tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles
                            : (int)blockIdx.x * p.t_slots + (late ? x - beg : p.t_slots - 1);
       const bool single = t_first / kGroupTiles == t_last / kGroupTiles;
@@ -662,26 +663,23 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
       fresh_seg = !same;
     }
-    if (ok) {  // the end mark
-      const int ds = t % ND;
-      ok = t < ND || wait_warp(d_free(ds), ((t / ND) - 1) & 1);
-      if (ok && lane == 0) {
-        descs[ds].flags = kEnd;
-        mbar_arrive(d_full(ds));
-      }
+    if (t == 0 && lane == 0) {  // no tile
+      descs[0].flags = kEnd;
+      mbar_arrive(d_full(0));
     }
     if (!ok && lane == 0) give_up();
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == W_LOAD) {
     // ---- copies ----
     bool ok = true;
-    int seg = 0;
-    for (int t = 0; ok; ++t) {
+    int seg = 0, fl = 0;
+    for (int t = 0; ok && !(fl & kFinal); ++t) {
       const int ds = t % ND;
       if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
       const Desc& de = descs[ds];
       const int4 dd = *reinterpret_cast<const int4*>(&de.flags), dx = *reinterpret_cast<const int4*>(&de.base);
-      if (dd.x & kEnd) break;
+      fl = dd.x;
+      if (fl & kEnd) break;
       // lane (block, panel): one copy each of K, then of V
       const int blk = lane / NP, panel = lane % NP;
       const int my_id = blk < nb ? de.id[blk & 7] : -1;
@@ -699,7 +697,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           tma_load_2d(slots + slot * X::kSlot + panel * X::kPanelBytes + blk * block * X::kRowB, kv ? &maps.v : &maps.k,
                       panel * 128, row, full(slot));
         ++loads;
-        if (X::kStage > 0 && kv == 0 && (dd.x & kNewSeg)) {  // the segment's query rows, a copy per token
+        if (X::kStage > 0 && kv == 0 && (fl & kNewSeg)) {  // the segment's query rows, a copy per token
           if (seg > 0 && !(ok = wait_warp(st_free, (seg - 1) & 1))) break;
           const uint32_t bytes = (uint32_t)(p.G * D * 2);
           if (lane == 0) mbar_expect_tx(st_full, toks * bytes);
@@ -719,19 +717,20 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     constexpr uint32_t id_o = umma_idesc_e4m3(128, C, true, true);
     const uint32_t go = elect_one();
     bool ok = true, more = true;
-    int seg = 0;
+    int seg = 0, fl = 0;
     for (int t = 0; more; ++t) {
       const int ds = t % ND;
-      if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
-      const int fl = descs[ds].flags;
-      __syncwarp();
-      if (go) mbar_arrive(d_free(ds));
-      more = !(fl & kEnd);
+      more = !(fl & kFinal);
       if (more) {
         const int slot = (2 * t) % NS;
+        if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
+        fl = descs[ds].flags;
+        if (fl & kEnd) break;
         if (fl & kNewSeg) ok = wait_warp(q_full, seg++ & 1);
-        ok = ok && wait_warp(full(slot), ((2 * t) / NS) & 1) && (t < 2 || wait_warp(s_free(t & 1), ((t >> 1) - 1) & 1));
+        // (the scores of tile t - 2 were read before its weights were complete)
+        ok = ok && wait_warp(d_scales(ds), (t / ND) & 1) && wait_warp(full(slot), ((2 * t) / NS) & 1);
         if (!ok) break;
+        if (go) mbar_arrive(d_free(ds));
         tc_fence_after_sync();
         const uint32_t ka = slots + slot * X::kSlot, d = s_col + (t & 1) * C;
 #pragma unroll
@@ -745,8 +744,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
       if (t > 0) {  // O = V^T P^T of tile t - 1
         const int u = t - 1, slot = (2 * u + 1) % NS;
-        ok = wait_warp(p_full(u % kRing), (u / kRing) & 1) && wait_warp(full(slot), ((2 * u + 1) / NS) & 1) &&
-             (u < 2 || wait_warp(o_free(u & 1), ((u >> 1) - 1) & 1));
+        ok = wait_warp(full(slot), ((2 * u + 1) / NS) & 1) && (u < 2 || wait_warp(o_free(u & 1), ((u >> 1) - 1) & 1)) &&
+             wait_warp(p_full(u % kRing), (u / kRing) & 1);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t va = slots + slot * X::kSlot, pa = p_s + (u & 1) * X::kP, d = o_col + (u & 1) * NP * C;
@@ -782,13 +781,15 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       ok &= wait_warp(all_sync, n_all++ & 1);
     };
 
-    for (int t = 0;; ++t) {
+    // one wait a tile: its scores are there once its descriptor, its scales and O of tile t - 2 (and with it the weights'
+    // buffer) are, too, as the MMA warp waits for the first two and the MMAs run in order
+    int fl = kNextSeg;
+    for (int t = 0; !(fl & kFinal); ++t) {
       const int ds = t % ND, par = t & 1, ring = t % kRing;
-      if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
       const Desc& de = descs[ds];
-      const int fl = de.flags;
-      if (fl & kEnd) break;
-      if (fl & kNewSeg) {
+      if (fl & kNextSeg) {
+        if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
+        if (de.flags & kEnd) break;
         const int j0 = de.j0, toks = min(p.TQ, de.fresh - j0);
         sync_all();  // nobody looks at the last segment's limits and factors any more
         if (X::kStage > 0) ok &= wait_warp(st_full, seg++ & 1);
@@ -856,23 +857,19 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         sync_all();
         if (!ok) break;
       }
+      if (!(ok = wait_warp(s_full(par), (t >> 1) & 1))) break;
+      tc_fence_after_sync();
       // the V scale is a power of two: its exponent, and its reciprocal
-      if (!(ok = wait_warp(d_scales(ds), (t / ND) & 1))) break;
+      fl = de.flags;
       const int blk = tt >> p.shift;
       const float ks = de.ks[blk];
       int ve = (int)(__float_as_uint(de.vs[blk]) >> 23) - 127;
-      // (the weights' buffer is free once O of tile t - 2 is done)
-      ok = (t < 2 || wait_warp(o_full(par), ((t >> 1) - 1) & 1)) && wait_warp(s_full(par), (t >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after_sync();
       float s[R];
       {
         float raw[2 * R];
         tmem_ld<2 * R>(s_col + par * C + lane_col, raw);
         tmem_wait_ld();
         tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free(par));
 #pragma unroll
         for (int i = 0; i < R; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(s_qf + R * grp + i);
@@ -1049,13 +1046,13 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     float acc[NP][R];
     float m_run = -INFINITY, l_run = 0.f;  // lane i (< R) of every warp: row i of the group
     bool ok = true;
-    for (int t = 0;; ++t) {
+    ok = wait_warp(d_full(0), 0);
+    int fl = ok ? descs[0].flags & kEnd : kEnd;
+    for (int t = 0; !(fl & (kFinal | kEnd)); ++t) {
       const int ds = t % ND, par = t & 1, ring = t % kRing;
-      if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
-      const Desc& de = descs[ds];
-      const int fl = de.flags;
-      if (fl & kEnd) break;
       if (!(ok = wait_warp(p_full(ring), (t / kRing) & 1))) break;
+      const Desc& de = descs[ds];
+      fl = de.flags;
       float mt = -INFINITY, lt = 0.f;
       if (lane < R) {
         const float* a = s_sum + ring * 4 * RP + R * grp + lane;
