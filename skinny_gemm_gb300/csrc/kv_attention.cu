@@ -447,9 +447,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
     *s_abort = 1;
   };
-  auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {  // all lanes; the same answer for all
-    return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity));
-  };
 
   // ---- set-up; meanwhile the listing warp finds the CTA's range of the line ----
   const int nb = kTile >> p.shift, block = 1 << p.shift;  // blocks per tile
@@ -611,7 +608,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       const bool valid = id >= 0 && id < p.blocks;
       const unsigned need = __ballot_sync(0xffffffffu, id != -2), have = __ballot_sync(0xffffffffu, valid);
       if (need != have || tile * kTile + kTile - 1 > pos0 || (p.window > 0 && tile * kTile < pos1 - p.window + 1)) fl |= kFix;
-      if (t >= ND && !(ok = wait_warp(d_free(ds), ((t / ND) - 1) & 1))) break;
+      if (t >= ND && !(ok = mbar_wait_warp(d_free(ds), ((t / ND) - 1) & 1))) break;
       Desc& de = descs[ds];
       if (lane == 0) {
         *reinterpret_cast<int4*>(&de.flags) = make_int4(fl, h, j0, tile);
@@ -675,7 +672,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     int seg = 0, fl = 0;
     for (int t = 0; ok && !(fl & kFinal); ++t) {
       const int ds = t % ND;
-      if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
+      if (!(ok = mbar_wait_warp(d_full(ds), (t / ND) & 1))) break;
       const Desc& de = descs[ds];
       const int4 dd = *reinterpret_cast<const int4*>(&de.flags), dx = *reinterpret_cast<const int4*>(&de.base);
       fl = dd.x;
@@ -690,7 +687,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int slot = loads % NS;
-        if (loads >= NS && !(ok = wait_warp(empty(slot), ((loads / NS) - 1) & 1))) break;
+        if (loads >= NS && !(ok = mbar_wait_warp(empty(slot), ((loads / NS) - 1) & 1))) break;
         if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(copies * block * X::kRowB));
         __syncwarp();
         if (my_id >= 0)
@@ -698,7 +695,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
                       panel * 128, row, full(slot));
         ++loads;
         if (X::kStage > 0 && kv == 0 && (fl & kNewSeg)) {  // the segment's query rows, a copy per token
-          if (seg > 0 && !(ok = wait_warp(st_free, (seg - 1) & 1))) break;
+          if (seg > 0 && !(ok = mbar_wait_warp(st_free, (seg - 1) & 1))) break;
           const uint32_t bytes = (uint32_t)(p.G * D * 2);
           if (lane == 0) mbar_expect_tx(st_full, toks * bytes);
           __syncwarp();
@@ -723,12 +720,12 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       more = !(fl & kFinal);
       if (more) {
         const int slot = (2 * t) % NS;
-        if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
+        if (!(ok = mbar_wait_warp(d_full(ds), (t / ND) & 1))) break;
         fl = descs[ds].flags;
         if (fl & kEnd) break;
-        if (fl & kNewSeg) ok = wait_warp(q_full, seg++ & 1);
+        if (fl & kNewSeg) ok = mbar_wait_warp(q_full, seg++ & 1);
         // (the scores of tile t - 2 were read before its weights were complete)
-        ok = ok && wait_warp(d_scales(ds), (t / ND) & 1) && wait_warp(full(slot), ((2 * t) / NS) & 1);
+        ok = ok && mbar_wait_warp(d_scales(ds), (t / ND) & 1) && mbar_wait_warp(full(slot), ((2 * t) / NS) & 1);
         if (!ok) break;
         if (go) mbar_arrive(d_free(ds));
         tc_fence_after_sync();
@@ -744,8 +741,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
       if (t > 0) {  // O = V^T P^T of tile t - 1
         const int u = t - 1, slot = (2 * u + 1) % NS;
-        ok = wait_warp(full(slot), ((2 * u + 1) / NS) & 1) && (u < 2 || wait_warp(o_free(u & 1), ((u >> 1) - 1) & 1)) &&
-             wait_warp(p_full(u % kRing), (u / kRing) & 1);
+        ok = mbar_wait_warp(full(slot), ((2 * u + 1) / NS) & 1) && (u < 2 || mbar_wait_warp(o_free(u & 1), ((u >> 1) - 1) & 1)) &&
+             mbar_wait_warp(p_full(u % kRing), (u / kRing) & 1);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t va = slots + slot * X::kSlot, pa = p_s + (u & 1) * X::kP, d = o_col + (u & 1) * NP * C;
@@ -773,12 +770,12 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     auto sync_group = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(grp_sync(grp));
-      ok &= wait_warp(grp_sync(grp), n_grp++ & 1);
+      ok &= mbar_wait_warp(grp_sync(grp), n_grp++ & 1);
     };
     auto sync_all = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(all_sync);
-      ok &= wait_warp(all_sync, n_all++ & 1);
+      ok &= mbar_wait_warp(all_sync, n_all++ & 1);
     };
 
     // one wait a tile: its scores are there once its descriptor, its scales and O of tile t - 2 (and with it the weights'
@@ -788,11 +785,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       const int ds = t % ND, par = t & 1, ring = t % kRing;
       const Desc& de = descs[ds];
       if (fl & kNextSeg) {
-        if (!(ok = wait_warp(d_full(ds), (t / ND) & 1))) break;
+        if (!(ok = mbar_wait_warp(d_full(ds), (t / ND) & 1))) break;
         if (de.flags & kEnd) break;
         const int j0 = de.j0, toks = min(p.TQ, de.fresh - j0);
         sync_all();  // nobody looks at the last segment's limits and factors any more
-        if (X::kStage > 0) ok &= wait_warp(st_full, seg++ & 1);
+        if (X::kStage > 0) ok &= mbar_wait_warp(st_full, seg++ & 1);
         if (!ok) break;
         // query rows as e4m3 terms: TPR threads a row
         constexpr int TPR = RP <= 8 ? 128 / RP : 8, CPT = (D / 8 + TPR - 1) / TPR;
@@ -857,7 +854,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         sync_all();
         if (!ok) break;
       }
-      if (!(ok = wait_warp(s_full(par), (t >> 1) & 1))) break;
+      if (!(ok = mbar_wait_warp(s_full(par), (t >> 1) & 1))) break;
       tc_fence_after_sync();
       // the V scale is a power of two: its exponent, and its reciprocal
       fl = de.flags;
@@ -893,7 +890,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         }
         uint8_t* v_row = base + ((2 * t + 1) % NS) * X::kSlot;
         constexpr int kRowB = X::kRowB, kCh = kRowB / 16;
-        ok = wait_warp(full((2 * t + 1) % NS), ((2 * t + 1) / NS) & 1);
+        ok = mbar_wait_warp(full((2 * t + 1) % NS), ((2 * t + 1) / NS) & 1);
         if (!ok) break;
         bool nan_code = false;
         const bool partly = toks > 1 && !dead && (tok > pos0 || (p.window > 0 && tok < pos1 - p.window + 1));
@@ -1046,11 +1043,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     float acc[NP][R];
     float m_run = -INFINITY, l_run = 0.f;  // lane i (< R) of every warp: row i of the group
     bool ok = true;
-    ok = wait_warp(d_full(0), 0);
+    ok = mbar_wait_warp(d_full(0), 0);
     int fl = ok ? descs[0].flags & kEnd : kEnd;
     for (int t = 0; !(fl & (kFinal | kEnd)); ++t) {
       const int ds = t % ND, par = t & 1, ring = t % kRing;
-      if (!(ok = wait_warp(p_full(ring), (t / kRing) & 1))) break;
+      if (!(ok = mbar_wait_warp(p_full(ring), (t / kRing) & 1))) break;
       const Desc& de = descs[ds];
       fl = de.flags;
       float mt = -INFINITY, lt = 0.f;
@@ -1073,7 +1070,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         if (lane < R) s_ab[w4 * RP + R * grp + lane] = make_float2(al, be);
         __syncwarp();
       }
-      if (!(ok = wait_warp(o_full(par), (t >> 1) & 1))) break;
+      if (!(ok = mbar_wait_warp(o_full(par), (t >> 1) & 1))) break;
       tc_fence_after_sync();
       const uint32_t poison = s_nan[ring] == t + 1 ? s_taint[ring * 128 * NG + 128 * grp + tt] : 0;
 #pragma unroll

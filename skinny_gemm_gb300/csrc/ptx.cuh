@@ -62,6 +62,25 @@ __device__ __forceinline__ bool mbar_wait_parked(uint32_t bar, uint32_t parity, 
   return false;
 }
 
+// Bounded wait of a whole warp (all lanes call; the same answer for all): the
+// vote on the phase comes with the try, and the first try stands by itself, as
+// most waits of a pipeline in step find their phase complete.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  auto attempt = [&]() {
+    asm volatile(
+        "{ .reg .pred p, q; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; "
+        "vote.sync.all.pred q, p, 0xffffffff; selp.u32 %0, 1, 0, q; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  };
+  attempt();
+#pragma unroll 1
+  for (uint32_t i = 0; !ok && i < kWaitLimit; ++i) attempt();
+  return ok;
+}
+
 // Non-suspending probe of a phase (test_wait never parks the thread).
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
