@@ -166,10 +166,16 @@ struct Req {
   int c0, fresh, base;  // first row, new tokens (0: nothing to do), tokens before them
 };
 
-__device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) {
+struct RawReq {
+  int c0, c1, len;
+  __device__ __forceinline__ RawReq(const Params& p, int b) : c0(0), c1(0), len(0) {
+    if (b < p.B) c0 = p.cu[b], c1 = p.cu[b + 1], len = p.lens[b];
+  }
+};
+
+__device__ __forceinline__ Req check_req(const Params& p, const RawReq& w, bool* bad) {
   Req r{0, 0, 0};
-  if (b >= p.B) return r;
-  const int c0 = p.cu[b], c1 = p.cu[b + 1], len = p.lens[b];
+  const int c0 = w.c0, c1 = w.c1, len = w.len;
   const bool ok = c0 >= 0 && c0 <= c1 && c1 <= p.T && c1 - c0 <= p.max_new && c1 - c0 <= len && len <= p.max_len;
   if (!ok) {
     if (c1 != c0) *bad = true;
@@ -180,6 +186,8 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) {
   r.base = len - r.fresh;
   return r;
 }
+
+__device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) { return check_req(p, RawReq(p, b), bad); }
 
 __device__ __forceinline__ int row_tiles(const Params& p, const Req& r) {
   return r.fresh <= p.TQ ? (r.fresh > 0) : (r.fresh + p.TQ - 1) / p.TQ;
@@ -243,6 +251,30 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x; results below 2^-126 ar
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// Two fp32 operations an instruction, each rounded as by itself.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c; "
+      "mov.b64 {%0, %1}, d; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // a, b as hi + lo / 16 (each two e4m3 codes, a in the low byte), in fp32: exact for bf16 values in range
@@ -485,8 +517,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     pdl_launch_dependents();  // (after the wait: what the next kernel reads of this call's inputs is there when it starts)
     int mine_end = 0;         // inclusive prefix of this lane's request
     int rows = 0;             // of valid requests
-    auto scan = [&]() {       // loads 32 requests; their inclusive prefix of tiles after `total`
-      mine = load_req(p, b0 + lane, &bad);
+    auto scan = [&](const RawReq& w) {  // 32 requests; their inclusive prefix of tiles after `total`
+      mine = check_req(p, w, &bad);
       int n = mine.fresh > 0 ? tiles_before(p, mine, row_tiles(p, mine)) * p.heads : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -495,10 +527,15 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
       mine_end = total + n;
     };
+    int ends = 0;  // lane i: tiles up to the end of the i-th 32 requests (the first 1024)
+    RawReq ahead(p, lane);
     for (; b0 < p.B; b0 += 32) {
-      scan();
+      const RawReq w = ahead;
+      if (b0 + 32 < p.B) ahead = RawReq(p, b0 + 32 + lane);
+      scan(w);
       total = __shfl_sync(0xffffffffu, mine_end, 31);
       rows += mine.fresh;
+      if (b0 == 32 * lane) ends = total;
     }
     rows = __reduce_add_sync(0xffffffffu, rows);
     if (lane == 0) {
@@ -513,8 +550,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     total = 0;
     b0 = 0;
     if (p.B > 32) {
-      for (; b0 < p.B; b0 += 32) {
-        scan();
+      const unsigned after = __ballot_sync(0xffffffffu, 32 * lane < p.B && ends > beg);
+      const int skip = after ? __ffs(after) - 1 : 32;
+      if (skip > 0) total = __shfl_sync(0xffffffffu, ends, skip - 1);
+      for (b0 = 32 * skip; b0 < p.B; b0 += 32) {
+        scan(RawReq(p, b0 + lane));
         const int e = __shfl_sync(0xffffffffu, mine_end, 31);
         if (e > beg) break;
         total = e;
@@ -870,9 +910,14 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
         for (int i = 0; i < R; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(s_qf + R * grp + i);
-          const float ff[4] = {f.x, f.y, f.z, f.w};
+          const float2 ff[2] = {make_float2(f.x, f.y), make_float2(f.z, f.w)};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[i + k] = __fmul_rn(__fmaf_rn(raw[R + i + k], 0.0625f, raw[i + k]), ff[k]);
+          for (int k = 0; k < 4; k += 2) {
+            const float2 z = mul2(fma2(make_float2(raw[R + i + k], raw[R + i + k + 1]), make_float2(0.0625f, 0.0625f),
+                                       make_float2(raw[i + k], raw[i + k + 1])), ff[k / 2]);
+            s[i + k] = z.x;
+            s[i + k + 1] = z.y;
+          }
         }
       }
       if (fl & kFix) {
@@ -951,7 +996,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       } else {
         const float lv = (float)ve;
 #pragma unroll
-        for (int i = 0; i < R; ++i) s[i] = __fmaf_rn(s[i], ks, lv);
+        for (int i = 0; i < R; i += 2) {
+          const float2 z = fma2(make_float2(s[i], s[i + 1]), make_float2(ks, ks), make_float2(lv, lv));
+          s[i] = z.x;
+          s[i + 1] = z.y;
+        }
       }
       // maxima over the tile: the warp, then the group's four
       float* sm = s_max + par * 4 * RP + R * grp;
@@ -1067,7 +1116,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       {
         float al, be;
         fold_ml(m_run, l_run, mt, lt, al, be);
-        if (lane < R) s_ab[w4 * RP + R * grp + lane] = make_float2(al, be);
+        if (lane < R) {  // (al, al', be, be') of two rows
+          float* ab = reinterpret_cast<float*>(s_ab + w4 * RP + R * grp) + (lane & ~1) * 2 + (lane & 1);
+          ab[0] = al;
+          ab[2] = be;
+        }
         __syncwarp();
       }
       if (!(ok = mbar_wait_warp(o_full(par), (t >> 1) & 1))) break;
@@ -1079,7 +1132,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         tmem_ld<2 * R>(o_col + (par * NP + c) * C + lane_col, raw);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < R; ++i) raw[i] = __fmaf_rn(raw[R + i], 0.0625f, raw[i]);
+        for (int i = 0; i < R; i += 2) {
+          const float2 z = fma2(make_float2(raw[R + i], raw[R + i + 1]), make_float2(0.0625f, 0.0625f), make_float2(raw[i], raw[i + 1]));
+          raw[i] = z.x;
+          raw[i + 1] = z.y;
+        }
         if (poison) {
 #pragma unroll
           for (int i = 0; i < R; ++i)
@@ -1088,8 +1145,10 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
         for (int i = 0; i < R; i += 2) {
           const float4 ab = *reinterpret_cast<const float4*>(s_ab + w4 * RP + R * grp + i);
-          acc[c][i] = __fmaf_rn(acc[c][i], ab.x, __fmul_rn(raw[i], ab.y));
-          acc[c][i + 1] = __fmaf_rn(acc[c][i + 1], ab.z, __fmul_rn(raw[i + 1], ab.w));
+          const float2 z = fma2(make_float2(acc[c][i], acc[c][i + 1]), make_float2(ab.x, ab.y),
+                                mul2(make_float2(raw[i], raw[i + 1]), make_float2(ab.z, ab.w)));
+          acc[c][i] = z.x;
+          acc[c][i + 1] = z.y;
         }
       }
       tc_fence_before_sync();
