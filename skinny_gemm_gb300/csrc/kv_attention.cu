@@ -91,9 +91,10 @@ static_assert(sizeof(Desc) % 16 == 0, "16-byte rows");
 
 // A group that a cut divides, as a CTA's end needs it.
 struct CutGroup {
-  int owner, first, count, mine;  // CTA of its first tile, that tile's position, its tiles, those in this range (0: none)
+  int owner, count, mine;         // CTA of its first tile, its tiles, those in this range
   int c0, j0, h, toks;            // rows: first of the request, first token of the row tile, key head, tokens
   int gi, single;                 // group slot; the segment's only group
+  int parts, slot[kGroupTiles];   // its parts in order: the first range's fold, then tiles
 };
 
 // RP rows of a row tile (query tokens x heads of a group), R to a softmax warp
@@ -639,11 +640,21 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
                            : (int)blockIdx.x * p.t_slots + (late ? x - beg : p.t_slots - 1);
       const bool single = t_first / kGroupTiles == t_last / kGroupTiles;
       if (!(fl & kPart) && single) fl |= kDirect;
-      if (part && lane == 0) {  // for the CTA's end
-        const int k = !late;
-          const int owner = k ? (int)blockIdx.x : cut.owner(g_lo);
-          s_cut[k] = CutGroup{owner, g_lo, g_hi - g_lo + 1, min(end, g_hi + 1) - max(beg, g_lo), r.c0, j0, h, toks,
-                              tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles, single};
+      if (fl & kLastPart) {  // for the CTA's end
+        CutGroup& c = s_cut[!late];
+        const int owner = late ? cut.owner(g_lo) : (int)blockIdx.x;
+        const int rest = cut.begin(owner + 1);  // the first tile after the first range
+        if (lane == 0) {
+          c.owner = owner, c.count = g_hi - g_lo + 1, c.mine = min(end, g_hi + 1) - max(beg, g_lo);
+          c.c0 = r.c0, c.j0 = j0, c.h = h, c.toks = toks;
+          c.gi = tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles, c.single = single;
+          c.parts = g_hi - rest + 2;
+        }
+        if (lane < kGroupTiles && rest + lane - 1 <= g_hi) {
+          const int y = rest + lane - 1, own = lane ? cut.owner(y) : owner;
+          c.slot[lane] = own * p.t_slots + (lane ? y - cut.begin(own) : p.t_slots - 1);
+        }
+        __syncwarp();
       }
       const bool valid = id >= 0 && id < p.blocks;
       const unsigned need = __ballot_sync(0xffffffffu, id != -2), have = __ballot_sync(0xffffffffu, valid);
@@ -1238,41 +1249,28 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   if (s_last[0] | s_last[1]) {
     float2* w_ab = reinterpret_cast<float2*>(base);   // [2][RP][kGroupTiles]
     float2* w_ml = w_ab + 2 * RP * kGroupTiles;       // [2][RP]
-    int* w_slot = reinterpret_cast<int*>(w_ml + 2 * RP);  // [2][kGroupTiles]
-    int* w_parts = w_slot + 2 * kGroupTiles;              // [2]
-    if (tid < 2 * kGroupTiles) {
-      const CutGroup& c = s_cut[tid / kGroupTiles];
-      const int z = tid % kGroupTiles;
-      if (s_last[tid / kGroupTiles]) {
-        const Cut cut(s_rest[1], p.grid);
-        const int x = cut.begin(c.owner + 1) + z - 1, own = z ? cut.owner(x) : c.owner;  // part z: a tile after the first range
-        w_slot[tid] = own * p.t_slots + (z ? x - cut.begin(own) : p.t_slots - 1);
-        if (z == 0) w_parts[tid / kGroupTiles] = c.first + c.count - x;
+    auto weights = [&](int k, int rr) {  // of group k's parts, row rr
+      const CutGroup& c = s_cut[k];
+      if (rr < 0 || rr >= c.toks * p.G) return;
+      float2 ml[kGroupTiles];
+#pragma unroll
+      for (int z = 0; z < kGroupTiles; ++z)
+        ml[z] = z < c.parts ? __ldcg(p.t_ml + c.slot[z] * RP + rr) : make_float2(-INFINITY, 0.f);
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int z = 0; z < kGroupTiles; ++z) {
+        float al, be;
+        fold_ml(m, l, ml[z].x, ml[z].y, al, be);
+        w_ab[(k * RP + rr) * kGroupTiles + z] = make_float2(al, be);
       }
-    }
-    __syncthreads();
+      w_ml[k * RP + rr] = make_float2(m, l);
+    };
     uint32_t n_landed = 0;
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       if (!s_last[k]) continue;
       const CutGroup& c = s_cut[k];
-      const int count = w_parts[k], rows = c.toks * p.G;
-      auto weights = [&]() {  // of the parts, row by row
-        if (tid < rows) {
-          float2 ml[kGroupTiles];
-#pragma unroll
-          for (int z = 0; z < kGroupTiles; ++z)
-            ml[z] = z < count ? __ldcg(p.t_ml + w_slot[k * kGroupTiles + z] * RP + tid) : make_float2(-INFINITY, 0.f);
-          float m = -INFINITY, l = 0.f;
-#pragma unroll
-          for (int z = 0; z < kGroupTiles; ++z) {
-            float al, be;
-            fold_ml(m, l, ml[z].x, ml[z].y, al, be);
-            w_ab[(k * RP + tid) * kGroupTiles + z] = make_float2(al, be);
-          }
-          w_ml[k * RP + tid] = make_float2(m, l);
-        }
-      };
+      const int count = c.parts, rows = c.toks * p.G;
       auto put = [&](int rr, int col, const float (&a)[V]) {
         const int jj = rr / p.G;
         const float2 ml = w_ml[k * RP + rr];
@@ -1293,38 +1291,49 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         constexpr int kItems = (RP * (D / V) + NT - 1) / NT;        // of a thread, at most
         constexpr int kFrom = 8192, kPartBytes = RP * D * 4;        // copies land after the factors
         constexpr int kBatch = (NS * X::kSlot - kFrom) / kPartBytes;  // parts at once
-        static_assert(kBatch >= 4 && 2 * RP * (kGroupTiles + 1) * 8 + 128 <= kFrom, "shared memory of a CTA's end");
+        static_assert(kBatch >= 4 && 2 * RP * (kGroupTiles + 1) * 8 <= kFrom, "shared memory of a CTA's end");
         float a[kItems][V];
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
 #pragma unroll
           for (int q = 0; q < V; ++q) a[i][q] = 0.f;
+        // both groups' parts come at once where they fit
+        const bool both = s_last[0] && s_last[1] && s_cut[0].parts + s_cut[1].parts <= kBatch;
 #pragma unroll 1
         for (int z0 = 0; z0 < count; z0 += kBatch) {
-          const int n = min(kBatch, count - z0);
-          if (tid == 0) {
-            asm volatile("fence.proxy.async;" ::: "memory");
-            mbar_expect_tx(landed, (uint32_t)(n * rows * D * 4));
-            for (int z = 0; z < n; ++z)
-              bulk_load(smem_u32(base) + kFrom + z * kPartBytes, p.t_acc + (int64_t)w_slot[k * kGroupTiles + z0 + z] * RP * D,
-                        (uint32_t)(rows * D * 4), landed, policy_evict_first());
-          }
-          if (z0 == 0) weights();
-          const bool there = mbar_wait_parked(landed, n_landed++ & 1);
-          if (!__syncthreads_and(there)) {
+          const int n = min(kBatch, count - z0), skip = both && k ? s_cut[0].parts : 0;
+          if (skip == 0) {
             if (tid == 0) {
-              atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
-              mbar_wait_parked(landed, (n_landed - 1) & 1);
+              asm volatile("fence.proxy.async;" ::: "memory");
+              const int more = both ? s_cut[1].parts : 0, bytes = rows * D * 4, bytes1 = s_cut[1].toks * p.G * D * 4;
+              mbar_expect_tx(landed, (uint32_t)(n * bytes + (both ? more * bytes1 : 0)));
+              const uint64_t pol = policy_evict_first();
+#pragma unroll 1
+              for (int z = 0; z < n + more; ++z)
+                bulk_load(smem_u32(base) + kFrom + z * kPartBytes,
+                          p.t_acc + (int64_t)(z < n ? c.slot[z0 + z] : s_cut[1].slot[z - n]) * RP * D,
+                          (uint32_t)(z < n ? bytes : bytes1), landed, pol);
             }
-            __syncthreads();
-            return;
+            if (z0 == 0) {
+              weights(k, tid);
+              if (both) weights(1, tid - 128);
+            }
+            const bool there = mbar_wait_parked(landed, n_landed++ & 1);
+            if (!__syncthreads_and(there)) {
+              if (tid == 0) {
+                atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
+                mbar_wait_parked(landed, (n_landed - 1) & 1);
+              }
+              __syncthreads();
+              return;
+            }
           }
 #pragma unroll
           for (int i = 0; i < kItems; ++i) {
             const int at = tid + i * NT, rr = at / (D / V), col = V * (at - rr * (D / V));
             if (rr < rows)
               for (int z = 0; z < n; ++z) {
-                const float4 v = *reinterpret_cast<const float4*>(base + kFrom + z * kPartBytes + (rr * D + col) * 4);
+                const float4 v = *reinterpret_cast<const float4*>(base + kFrom + (skip + z) * kPartBytes + (rr * D + col) * 4);
                 const float2 ab = w_ab[(k * RP + rr) * kGroupTiles + z0 + z];
                 a[i][0] = __fmaf_rn(a[i][0], ab.x, __fmul_rn(v.x, ab.y));
                 a[i][1] = __fmaf_rn(a[i][1], ab.x, __fmul_rn(v.y, ab.y));
@@ -1332,7 +1341,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
                 a[i][3] = __fmaf_rn(a[i][3], ab.x, __fmul_rn(v.w, ab.y));
               }
           }
-          __syncthreads();
+          if (!both) __syncthreads();
         }
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
@@ -1347,13 +1356,13 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
           for (int z = 0; z < kGroupTiles; ++z) {
             const bool is = z < count && rr < rows;
-            const float* from = p.t_acc + ((int64_t)(is ? w_slot[k * kGroupTiles + z] : 0) * RP + (is ? rr : 0)) * D + col;
+            const float* from = p.t_acc + ((int64_t)(is ? c.slot[z] : 0) * RP + (is ? rr : 0)) * D + col;
             const float4 u = is ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
             v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
           }
           if (first) {
             first = false;
-            weights();
+            weights(k, tid);
             __syncthreads();
           }
           if (rr >= rows) continue;
