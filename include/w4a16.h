@@ -386,9 +386,10 @@ int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, 
  * cu[b]) + t - cu[b] and sees tokens s in max(0, p - window + 1) .. p
  * (window 0: all of 0 .. p):
  *   out[t][j] = bf16( sum_s exp(z_s) V_s / sum_s exp(z_s) ),  z_s = scale * q . K_s
- * with fp32 scores, maxima, sums and accumulators; the weights exp(z) enter
- * the product with V rounded to 8 significant bits, as bf16 would, and q
- * enters exactly.  Tokens that a row does not see have no effect on it,
+ * with fp32 scores, maxima, sums and accumulators.  q enters to 2^-22 of its
+ * row's largest element; a weight exp(z), times its token's V scale, enters
+ * the product with V rounded to 8 significant bits, as bf16 would, and to
+ * 2^-22 of the largest such product of its 128-token tile.  Tokens that a row does not see have no effect on it,
  * whatever their bytes (NaN codes included); nor have tokens whose table
  * entry is not a block of the cache (those raise W4A16_DEVICE_KV_RANGE).  A
  * row that sees nothing, and a row t >= cu[B], is written as zeros.

@@ -470,6 +470,9 @@ def device_status(stream=None) -> int:
     rc = lib().w4a16_device_status(_stream_ptr(stream), ctypes.byref(flags))
     if rc not in (OK, ERR_DEVICE):
         _raise(rc)
+    if flags.value & DEVICE_TIMEOUT and (_kv_counter_cache or _kv_capture_sets):
+        torch.cuda.synchronize()
+        _kv_reset_counters()
     return flags.value
 
 
@@ -706,23 +709,40 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Ten
         _raise(rc)
 
 
+KV_CAPTURE_SETS = 1024  # counters for captured calls, per device (2 MB)
 _kv_counter_cache: dict = {}
+_kv_capture_sets: dict = {}
 
 
 def _kv_counters(raw_stream: int, device: torch.device) -> int:
-    """The zeroed counters of a stream (kept here, as its workspace is), made on
-    its first use outside graph capture.  A call captured before that gets
-    counters of its own from the graph's memory, zeroed in the graph."""
+    """Zeroed counters: a stream's, kept here as its workspace is; for a captured
+    call, whose graph may be replayed beside that stream, a set of its own.  Those
+    are made with the device's first call outside capture and handed out once;
+    without one left, the graph zeroes a set from its own memory."""
     key = (device.index, raw_stream)
+    if _capturing():
+        with _ws_lock:
+            sets = _kv_capture_sets.get(device.index)
+            if sets is not None and sets[1] < KV_CAPTURE_SETS:
+                sets[1] += 1
+                return sets[0].data_ptr() + 4 * KV_COUNTERS * (sets[1] - 1)
+        return torch.zeros(KV_COUNTERS, dtype=torch.int32, device=device).data_ptr()
     c = _kv_counter_cache.get(key)
     if c is None:
         zeros = torch.zeros(KV_COUNTERS, dtype=torch.int32, device=device)
-        if _capturing():
-            return zeros.data_ptr()
-        torch.cuda.current_stream(device).synchronize()
         with _ws_lock:
+            if device.index not in _kv_capture_sets:
+                _kv_capture_sets[device.index] = [torch.zeros(KV_CAPTURE_SETS * KV_COUNTERS, dtype=torch.int32, device=device), 0]
+            torch.cuda.current_stream(device).synchronize()
             c = _kv_counter_cache.setdefault(key, (zeros, zeros.data_ptr()))
     return c[1]
+
+
+def _kv_reset_counters() -> None:
+    """After a wait ran out: a call may have left counters behind (the GPU is idle)."""
+    for t in [c[0] for c in _kv_counter_cache.values()] + [s[0] for s in _kv_capture_sets.values()]:
+        t.zero_()
+        torch.cuda.current_stream(t.device).synchronize()
 
 
 KV_WORKSPACE_KEPT = 64 << 20  # larger workspaces are not kept between calls
