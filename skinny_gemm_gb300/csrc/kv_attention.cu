@@ -113,7 +113,7 @@ struct Geo {
   static constexpr int kPanelBytes = kTile * kRowB;
   static constexpr int kSlot = kTile * D;
   static constexpr int kQ = kPanels * kCols * 128;
-  // a segment's query rows as they come, ahead of its turn; larger row tiles have fewer segments and better uses for it
+  // a segment's query rows as they come, ahead of its turn (no gain for larger row tiles: prompt chunks 222.8, without 220.6 us)
   static constexpr int kStage = RP <= 8 ? RP * D * 2 : 0;
   static constexpr int kP = kTile * kCols;
   static constexpr int kCtas = RP <= 8 ? 2 : RP <= 16 ? (D == 256 ? 1 : 2) : 1;
@@ -146,6 +146,7 @@ struct Params {
   float qk_scale;  // scale * log2(e)
   int gmax;        // group slots per row
   int grid;
+  int seg_cost;    // positions before a segment's first tile
   int t_slots;     // slots for parts per CTA
   // workspace
   float* g_acc;  // [gmax][T][q_heads][D]
@@ -200,20 +201,22 @@ __device__ __forceinline__ int last_tile(const Params& p, const Req& r, int rt) 
   return (r.base + min((rt + 1) * p.TQ, r.fresh) - 1) / kTile;
 }
 
-// sum over 0 <= i < n of floor((b + i a) / m), all >= 0: whole parts are
-// taken out, then the lattice points under the line are counted along the
-// other axis, as in Euclid's algorithm.
-__device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t s = 0;
+// sum over 0 <= i < n of floor((b + i a) / m), for sums below 2^32: whole
+// parts are taken out, then the lattice points under the line are counted
+// along the other axis, as in Euclid's algorithm.
+__device__ __noinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  uint32_t s = 0;
   while (n > 0) {
-    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t y = a * n + b;
+    const uint32_t qa = a / m, qb = b / m;
+    if (qa) s += (uint32_t)((uint64_t)n * (n - 1) / 2) * qa;
+    s += n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
-    b = y % m;
-    const int64_t t = a;
+    b = y - n * m;
+    const uint32_t t = a;
     a = m;
     m = t;
   }
@@ -225,14 +228,14 @@ __device__ inline int tiles_before(const Params& p, const Req& r, int rt) {
   const int n = row_tiles(p, r);
   if (rt <= 0) return 0;
   if (rt == 1) return last_tile(p, r, 0) - first_tile(p, r, 0) + 1;
-  int64_t s = rt + floor_sum(rt == n ? n - 1 : rt, kTile, p.TQ, r.base + p.TQ - 1);
+  int s = rt + (int)floor_sum(rt == n ? n - 1 : rt, kTile, p.TQ, r.base + p.TQ - 1);
   if (rt == n) s += last_tile(p, r, n - 1);
   if (p.window > 0) {
     const int x = r.base - p.window + 1;  // first token of row tile i: max(0, x + i TQ)
     const int i0 = x >= 0 ? 0 : min(rt, (-x + p.TQ - 1) / p.TQ);
-    s -= floor_sum(rt - i0, kTile, p.TQ, max(0, x + i0 * p.TQ));
+    s -= (int)floor_sum(rt - i0, kTile, p.TQ, max(0, x + i0 * p.TQ));
   }
-  return (int)s;
+  return s;
 }
 
 // The cut of `total` tiles into grid ranges that differ by at most one tile.
@@ -520,7 +523,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     int rows = 0;             // of valid requests
     auto scan = [&](const RawReq& w) {  // 32 requests; their inclusive prefix of tiles after `total`
       mine = check_req(p, w, &bad);
-      int n = mine.fresh > 0 ? tiles_before(p, mine, row_tiles(p, mine)) * p.heads : 0;
+      const int rts = row_tiles(p, mine);
+      int n = rts > 0 ? (tiles_before(p, mine, rts) + p.seg_cost * rts) * p.heads : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, n, d);
@@ -567,19 +571,23 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       const int before = __shfl_sync(0xffffffffu, mine_end, max(bl - 1, 0));
       take(bl);
       int off = beg - (bl > 0 ? before : total);
-      int lo = 0, hi = row_tiles(p, r);
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tiles_before(p, r, mid) * p.heads <= off) lo = mid;
-        else hi = mid;
+      // its row tile: a lane looks at every step-th
+      int skipped = 0;  // tiles before it
+      for (int hi = row_tiles(p, r); hi - rt > 1;) {
+        const int step = (hi - rt + 31) / 32, mid = rt + lane * step;
+        const int first = mid < hi ? (tiles_before(p, r, mid) + p.seg_cost * mid) * p.heads : 0;
+        const int le = __popc(__ballot_sync(0xffffffffu, mid < hi && first <= off)) - 1;
+        skipped = __shfl_sync(0xffffffffu, first, le);
+        rt += le * step;
+        hi = min(hi, rt + step);
       }
-      rt = lo;
-      if (rt > 0) off -= tiles_before(p, r, rt) * p.heads;
+      off -= skipped;
       enter();
-      const int n = t_last - t_first + 1;
+      const int n = p.seg_cost + t_last - t_first + 1;
       h = off / n;
-      tile = t_first + off - h * n;
-      seg0 = beg - (tile - t_first);
+      off -= h * n + p.seg_cost;  // (below 0: in the segment's positions before its first tile)
+      tile = t_first + max(off, 0);
+      seg0 = beg - off;
       id = load_id();
     }
   } else if (warp == W_MMA) {
@@ -625,9 +633,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     // ---- work list ----
     bool fresh_seg = true, ok = true;
     const Cut cut(s_rest[1], p.grid);
-    int x = beg, t = 0;
-    for (; x < end; ++x, ++t) {
+    int x = beg < end ? seg0 + tile - t_first : end, t = 0, next;
+    for (; x < end; x = next, ++t) {
       const int ds = t % ND;
+      const bool same = tile < t_last;
+      next = same ? x + 1 : x + 1 + p.seg_cost;
       const int g_lo = max(seg0, x - tile % kGroupTiles), g_hi = min(seg0 + t_last - t_first, x - tile % kGroupTiles + kGroupTiles - 1);
       const int j0 = rt * p.TQ, toks = min(p.TQ, r.fresh - j0), pos0 = r.base + j0, pos1 = pos0 + toks - 1;
       // the group's first tile begins a fold, its last ends it; a cut ends it, too, and after one every tile is by itself
@@ -635,7 +645,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       int fl = (fresh_seg ? kNewSeg : 0) | (part ? kPart : 0) | (x == g_lo || late ? kGroupBegin : 0) |
                (x == g_hi || x + 1 == end || late ? kGroupEnd : 0) |
                (part && (x == g_hi || x + 1 == end) ? kLastPart : 0) | (late ? 0 : kTail) |
-               (x + 1 == end ? kFinal : tile == t_last ? kNextSeg : 0);
+               (next >= end ? kFinal : same ? 0 : kNextSeg);
       const int at = !part ? tile / kGroupTiles - first_tile(p, r, 0) / kGroupTiles
                            : (int)blockIdx.x * p.t_slots + (late ? x - beg : p.t_slots - 1);
       const bool single = t_first / kGroupTiles == t_last / kGroupTiles;
@@ -680,12 +690,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       if (lane == 0) mbar_arrive(d_full(ds));
       cp_async_arrive(d_scales(ds));
       // the next tile
-      const bool same = tile < t_last;
-      if (x + 1 < end) {
+      if (next < end) {
         if (same) {
           ++tile;
         } else {
-          seg0 = x + 1;
+          seg0 = next;
           if (++h == p.heads) {
             h = 0;
             if (++rt == row_tiles(p, r)) {
@@ -1463,7 +1472,7 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
 // ---- host side -----------------------------------------------------------------------------------
 
 struct Layout {
-  int RP, TQ, gmax, grid, t_slots;
+  int RP, TQ, gmax, grid, t_slots, seg_cost;
   bool fits;  // positions on the line and rows of group results fit in 31 bits
   size_t g_acc, g_ml, t_acc, t_ml, bytes;
 };
@@ -1481,6 +1490,14 @@ int ctas_d(int RP) {
 }
 int ctas_per_sm(int dim, int RP) { return dim == 64 ? ctas_d<64>(RP) : dim == 128 ? ctas_d<128>(RP) : ctas_d<256>(RP); }
 
+// Positions of the line that a segment takes besides its tiles: a new segment's
+// queries have to be split before its first scores, which the tiles of its first
+// CTA pay for.  Measured with 0 / 1 / 2 / 3: 32 rows, segments of 12 to 48
+// tiles 222 / 210 / 202 / 202 us; 12 rows, 9 tiles 26.2 / 25.2 / 24.1 / 25.5; 24
+// rows, 125 tiles 63.5 / 61.7 / 61.6 / 61.3; 4 rows, 62 tiles 53.0 / 53.3 /
+// 53.6 / 54.4 (two CTAs an SM hide it).
+int seg_cost(int RP) { return RP < 12 ? 0 : 2; }
+
 Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, int max_len, int window) {
   Layout y;
   const int G = q_heads / heads;
@@ -1496,12 +1513,13 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
     if (span < groups) groups = span;
   }
   y.gmax = (int)groups;
+  y.seg_cost = seg_cost(y.RP);
   // no more CTAs than tiles
   const int64_t per = ((int64_t)max_len + kTile - 1) / kTile;
   int64_t row_tiles = (int64_t)(T < B ? T : B) * (((int64_t)max_new + y.TQ - 1) / y.TQ);
   const int64_t by_rows = (T < B ? T : B) + (int64_t)T / y.TQ;
   if (by_rows < row_tiles) row_tiles = by_rows;
-  const int64_t most = row_tiles * heads * per;
+  const int64_t most = row_tiles * heads * (per + y.seg_cost);
   y.fits = most <= INT32_MAX && (int64_t)y.gmax * T * q_heads <= INT32_MAX;
   const int full = kSms * ctas_per_sm(dim, y.RP);
   y.grid = most < full ? (int)most : full;
@@ -1612,6 +1630,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t 
   p.qk_scale = a.scale * kLog2e;
   p.gmax = y.gmax;
   p.grid = y.grid;
+  p.seg_cost = y.seg_cost;
   p.t_slots = y.t_slots;
   p.g_acc = reinterpret_cast<float*>(w + y.g_acc);
   p.g_ml = reinterpret_cast<float2*>(w + y.g_ml);
