@@ -124,7 +124,7 @@ struct Geo {
   using Marks = std::conditional_t<(kPanels * R > 16), uint32_t, uint16_t>;
   // warps' maxima (two tiles), sums (kRing tiles x four warps), maxima (kRing), fold factors per warp, row factors and
   // limits; NaN marks (kRing tiles)
-  static constexpr int kRowData = RP * 4 * (2 * 4 + kRing * 4 + kRing + 2 * 4 + 3) + kRing * 128 * kGroups * (int)sizeof(Marks);
+  static constexpr int kRowData = RP * 4 * (2 * 4 + kRing * 4 + kRing + 2 * 4 + 2 * 3) + kRing * 128 * kGroups * (int)sizeof(Marks);
   static constexpr int kSmem = kSlots * kSlot + kQ + 2 * kP + kStage + kDescs * (int)sizeof(Desc) + kRowData + 8 * kBars + 48 + 2 * (int)sizeof(CutGroup);
   static constexpr int kTmemCols = 2 * kCols * (1 + kPanels);  // S twice, O twice
   static constexpr uint32_t kTmem = kTmemCols <= 64 ? 64 : kTmemCols <= 128 ? 128 : kTmemCols <= 256 ? 256 : 512;
@@ -452,9 +452,9 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   float* s_sum = s_max + 2 * 4 * RP;                                 // [kRing][4 warps][RP]
   float* s_top = s_sum + kRing * 4 * RP;                             // [kRing][RP]
   float2* s_ab = reinterpret_cast<float2*>(s_top + kRing * RP);      // [4 warps][RP]
-  float* s_qf = reinterpret_cast<float*>(s_ab + 4 * RP);             // [RP] score factor of a row
-  int2* s_lim = reinterpret_cast<int2*>(s_qf + RP);                  // [RP] first and last token a row sees
-  auto* s_taint = reinterpret_cast<typename X::Marks*>(s_lim + RP);  // [kRing][128 NG]
+  float* s_qf2 = reinterpret_cast<float*>(s_ab + 4 * RP);            // [2][RP] score factor of a row, by segment
+  int2* s_lim2 = reinterpret_cast<int2*>(s_qf2 + 2 * RP);            // [2][RP] first and last token a row sees
+  auto* s_taint = reinterpret_cast<typename X::Marks*>(s_lim2 + 2 * RP);  // [kRing][128 NG]
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(s_taint + kRing * 128 * NG);
   const uint32_t slots = smem_u32(base), q_s = smem_u32(q_mem), p_s = smem_u32(p_mem), bars = smem_u32(bar_mem);
   auto full = [&](int i) { return bars + 8u * i; };                  // slot: copies landed
@@ -841,6 +841,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     // one wait a tile: its scores are there once its descriptor, its scales and O of tile t - 2 (and with it the weights'
     // buffer) are, too, as the MMA warp waits for the first two and the MMAs run in order
     int fl = kNextSeg;
+    float* s_qf = s_qf2;  // this segment's (no warp is two segments ahead of another: scores wait for all)
+    int2* s_lim = s_lim2;
     for (int t = 0; !(fl & kFinal); ++t) {
       const int ds = t % ND, par = t & 1, ring = t % kRing;
       const Desc& de = descs[ds];
@@ -848,9 +850,10 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         if (!(ok = mbar_wait_warp(d_full(ds), (t / ND) & 1))) break;
         if (de.flags & kEnd) break;
         const int j0 = de.j0, toks = min(p.TQ, de.fresh - j0);
-        sync_all();  // nobody looks at the last segment's limits and factors any more
-        if (X::kStage > 0) ok &= mbar_wait_warp(st_full, seg++ & 1);
-        if (!ok) break;
+        if (X::kStage > 0 && !(ok = mbar_wait_warp(st_full, seg & 1))) break;
+        s_qf = s_qf2 + (seg & 1) * RP;
+        s_lim = s_lim2 + (seg & 1) * RP;
+        ++seg;
         // query rows as e4m3 terms: TPR threads a row
         constexpr int TPR = RP <= 8 ? 128 / RP : 8, CPT = (D / 8 + TPR - 1) / TPR;
         const int row = tid / TPR, c = tid % TPR;
@@ -911,8 +914,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           mbar_arrive(q_full);
           if (X::kStage > 0) mbar_arrive(st_free);
         }
-        sync_all();
-        if (!ok) break;
       }
       if (!(ok = mbar_wait_warp(s_full(par), (t >> 1) & 1))) break;
       tc_fence_after_sync();
