@@ -113,8 +113,9 @@ struct Geo {
   static constexpr int kPanelBytes = kTile * kRowB;
   static constexpr int kSlot = kTile * D;
   static constexpr int kQ = kPanels * kCols * 128;
-  // a segment's query rows as they come, ahead of its turn (no gain for larger row tiles: prompt chunks 222.8, without 220.6 us)
-  static constexpr int kStage = RP <= 8 ? RP * D * 2 : 0;
+  // a segment's query rows as they come, ahead of its turn, where the slots leave room (32 rows of 128: 196.5 us, read
+  // by the softmax warps themselves 198.6)
+  static constexpr int kStage = D == 256 && RP == 24 ? 0 : RP * D * 2;
   static constexpr int kP = kTile * kCols;
   static constexpr int kCtas = RP <= 8 ? 2 : RP <= 16 ? (D == 256 ? 1 : 2) : 1;
   static constexpr int kSlots = D == 256 ? (RP <= 8 ? 3 : RP <= 24 ? 6 : 5)
