@@ -26,8 +26,12 @@
 // load and the bits do not.  Rows of one group are finished there; several
 // groups are joined by kv_combine_kernel.
 //
-// Bound: HBM.  A 128-token tile of heads of 256 is 64 KB; one CTA has one to
-// two tiles in flight, two CTAs an SM where shared memory allows.
+// Bound: HBM for a few rows a key head.  64 requests of 1 x 4 rows to 16k tokens
+// of 2 heads x 256: 87 us, 5.66 TB/s; one of 131k tokens 34 us, 3.9 TB/s, where
+// set-up (2 us), the first copies (2 us), the groups that a cut divides (2 to 5
+// us) and the join (4 us) weigh more.  A CTA has two to five tiles (64 KB each with
+// heads of 256) in flight.  Instruction issue from 16 rows on: 32 rows a tile
+// take about 2000 clocks whatever the head size (prompt chunks 236 TFLOP/s).
 //
 // CTA: 4 NG + 4 NG + 3 warps (NG groups of R query rows).
 //   softmax warps  a thread per token: scores from TMEM, mask, maximum,
@@ -99,9 +103,14 @@ struct CutGroup {
 
 // RP rows of a row tile (query tokens x heads of a group), R to a softmax warp
 // group: more rows a thread spread its fixed work per tile (waits, exchange of
-// maxima) over more of them, as far as registers go.
+// maxima) over more of them, as far as registers go (32 rows in groups of 8:
+// 240 instead of 231 us).  Row tiles of 4, 8, 12, 16, 24 and 32: without 12 and
+// 24, 40 x 12 rows take 25.5 instead of 24.2 and 16 x 20 rows 68.6 instead of
+// 62.1; without 4, 32 x 4 rows 53.5 instead of 52.9.
 // CTAs per SM and K/V slots (128 tokens each): as many bytes in flight as the
-// shared memory holds, in as many CTAs as registers leave room for.
+// shared memory holds, in two CTAs where registers leave room and both have
+// work side by side.  One CTA instead: 4 rows of 128 61.0 (two: 52.9), 12 rows of
+// 128 61.1 (56.3), 16 rows of 64 59.0 (48.5); but 16 rows of 128 27.1 (28.1).
 template <int D, int RP>
 struct Geo {
   static constexpr int R = RP == 24 ? 12 : RP < 16 ? RP : 16;
@@ -117,10 +126,10 @@ struct Geo {
   // by the softmax warps themselves 198.6)
   static constexpr int kStage = D == 256 && RP == 24 ? 0 : RP * D * 2;
   static constexpr int kP = kTile * kCols;
-  static constexpr int kCtas = RP <= 8 ? 2 : RP <= 16 ? (D == 256 ? 1 : 2) : 1;
+  static constexpr int kCtas = RP <= 8 || (D == 128 && RP == 12) || (D == 64 && RP <= 16) ? 2 : 1;
   static constexpr int kSlots = D == 256 ? (RP <= 8 ? 3 : RP <= 24 ? 6 : 5)
-                                : D == 128 ? (RP <= 8 ? 6 : RP <= 16 ? 5 : 10) : RP <= 16 ? 10 : 12;
-  static constexpr int kBars = 2 * kSlots + 3 * kDescs + 2 + kRing + 4 + 6 + kGroups;
+                                : D == 128 ? (RP <= 8 ? 6 : RP == 12 ? 5 : 10) : RP <= 16 ? 10 : 12;
+  static constexpr int kBars = 2 * kSlots + 3 * kDescs + 2 + kRing + 4 + 5 + kGroups;
   // rows (bits) of a tile that see a NaN in a thread's columns
   using Marks = std::conditional_t<(kPanels * R > 16), uint32_t, uint16_t>;
   // warps' maxima (two tiles), sums (kRing tiles x four warps), maxima (kRing), fold factors per warp, row factors and
@@ -274,14 +283,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // a, b as hi + lo / 16 (each two e4m3 codes, a in the low byte), in fp32: exact for bf16 values in range
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -470,8 +471,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   auto p_full = [&](int i) { return bars2 + 8u * (6 + i); };         // [kRing] weights, sums and maxima written
   const uint32_t q_full = bars2 + 8u * (6 + kRing), drained = q_full + 8, all_sync = q_full + 16;
   const uint32_t st_full = q_full + 24, st_free = q_full + 32;       // staged query rows
-  const uint32_t landed = q_full + 40;                               // parts, at the CTA's end
-  auto grp_sync = [&](int g) { return q_full + 48 + 8u * g; };       // the four softmax warps of a group
+  auto grp_sync = [&](int g) { return q_full + 40 + 8u * g; };       // the four softmax warps of a group
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_mem + X::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_nan = reinterpret_cast<volatile int*>(s_tmem + 2);  // [kRing] 1 + a tile whose marks are in s_taint
@@ -615,7 +615,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     }
     mbar_init(q_full, 4 * NG);
     mbar_init(drained, 1);
-    mbar_init(landed, 1);
     mbar_init(all_sync, 4 * NG);
     mbar_init(st_full, 1);
     mbar_init(st_free, 4 * NG);
@@ -1212,7 +1211,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         if (fl & kLastPart) {
           // this range's parts are written: counted warp by warp; whoever counts the last will go on with the fold
           const int k = fl & kTail ? 1 : 0;
-          asm volatile("fence.proxy.async;" ::: "memory");  // (they are read by bulk copies)
           __threadfence();
           __syncwarp();
           if (lane == 0) {
@@ -1252,10 +1250,10 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   //
   // A divided group's fold, acc = acc al_k + O_k be_k over its parts k (the
   // first range's fold, then tiles), takes its factors from the parts' (m, l)
-  // alone: a thread per row works them out while the O_k are on their way, to a
-  // thread per few columns (few rows: all its loads in flight at once) or by
-  // bulk copy to shared memory (16 rows x 1 KB a part and more: 90 KB in 1.8
-  // instead of 4 us).
+  // alone: a thread per row works them out while the O_k are on their way to a
+  // thread per four columns, all its loads in flight at once (parts by bulk copy
+  // to shared memory: 16 x 20 rows over 16k tokens 62.1 instead of 61.3 us, 16 x
+  // 16 rows over 4k 30.5 instead of 28.5).
   constexpr int NT = X::kThreads, V = 4;  // columns a thread takes
   if (s_last[0] | s_last[1]) {
     float2* w_ab = reinterpret_cast<float2*>(base);   // [2][RP][kGroupTiles]
@@ -1276,7 +1274,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
       w_ml[k * RP + rr] = make_float2(m, l);
     };
-    uint32_t n_landed = 0;
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       if (!s_last[k]) continue;
@@ -1298,96 +1295,33 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           if (col == 0) p.g_ml[at] = ml;
         }
       };
-      if constexpr (RP >= 12) {
-        constexpr int kItems = (RP * (D / V) + NT - 1) / NT;        // of a thread, at most
-        constexpr int kFrom = 8192, kPartBytes = RP * D * 4;        // copies land after the factors
-        constexpr int kBatch = (NS * X::kSlot - kFrom) / kPartBytes;  // parts at once
-        static_assert(kBatch >= 4 && 2 * RP * (kGroupTiles + 1) * 8 <= kFrom, "shared memory of a CTA's end");
-        float a[kItems][V];
+      bool first = true;
+      for (int i = tid; i < (rows * (D / V) + NT - 1) / NT * NT; i += NT) {
+        const int rr = i / (D / V), col = V * (i - rr * (D / V));
+        float v[kGroupTiles][V];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i)
-#pragma unroll
-          for (int q = 0; q < V; ++q) a[i][q] = 0.f;
-        // both groups' parts come at once where they fit
-        const bool both = s_last[0] && s_last[1] && s_cut[0].parts + s_cut[1].parts <= kBatch;
-#pragma unroll 1
-        for (int z0 = 0; z0 < count; z0 += kBatch) {
-          const int n = min(kBatch, count - z0), skip = both && k ? s_cut[0].parts : 0;
-          if (skip == 0) {
-            if (tid == 0) {
-              asm volatile("fence.proxy.async;" ::: "memory");
-              const int more = both ? s_cut[1].parts : 0, bytes = rows * D * 4, bytes1 = s_cut[1].toks * p.G * D * 4;
-              mbar_expect_tx(landed, (uint32_t)(n * bytes + (both ? more * bytes1 : 0)));
-              const uint64_t pol = policy_evict_first();
-#pragma unroll 1
-              for (int z = 0; z < n + more; ++z)
-                bulk_load(smem_u32(base) + kFrom + z * kPartBytes,
-                          p.t_acc + (int64_t)(z < n ? c.slot[z0 + z] : s_cut[1].slot[z - n]) * RP * D,
-                          (uint32_t)(z < n ? bytes : bytes1), landed, pol);
-            }
-            if (z0 == 0) {
-              weights(k, tid);
-              if (both) weights(1, tid - 128);
-            }
-            const bool there = mbar_wait_parked(landed, n_landed++ & 1);
-            if (!__syncthreads_and(there)) {
-              if (tid == 0) {
-                atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
-                mbar_wait_parked(landed, (n_landed - 1) & 1);
-              }
-              __syncthreads();
-              return;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kItems; ++i) {
-            const int at = tid + i * NT, rr = at / (D / V), col = V * (at - rr * (D / V));
-            if (rr < rows)
-              for (int z = 0; z < n; ++z) {
-                const float4 v = *reinterpret_cast<const float4*>(base + kFrom + (skip + z) * kPartBytes + (rr * D + col) * 4);
-                const float2 ab = w_ab[(k * RP + rr) * kGroupTiles + z0 + z];
-                a[i][0] = __fmaf_rn(a[i][0], ab.x, __fmul_rn(v.x, ab.y));
-                a[i][1] = __fmaf_rn(a[i][1], ab.x, __fmul_rn(v.y, ab.y));
-                a[i][2] = __fmaf_rn(a[i][2], ab.x, __fmul_rn(v.z, ab.y));
-                a[i][3] = __fmaf_rn(a[i][3], ab.x, __fmul_rn(v.w, ab.y));
-              }
-          }
-          if (!both) __syncthreads();
+        for (int z = 0; z < kGroupTiles; ++z) {
+          const bool is = z < count && rr < rows;
+          const float* from = p.t_acc + ((int64_t)(is ? c.slot[z] : 0) * RP + (is ? rr : 0)) * D + col;
+          const float4 u = is ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
         }
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-          const int at = tid + i * NT, rr = at / (D / V);
-          if (rr < rows) put(rr, V * (at - rr * (D / V)), a[i]);
+        if (first) {
+          first = false;
+          weights(k, tid);
+          __syncthreads();
         }
-      } else {
-        bool first = true;
-        for (int i = tid; i < (rows * (D / V) + NT - 1) / NT * NT; i += NT) {
-          const int rr = i / (D / V), col = V * (i - rr * (D / V));
-          float v[kGroupTiles][V];
+        if (rr >= rows) continue;
+        float a[V];
 #pragma unroll
-          for (int z = 0; z < kGroupTiles; ++z) {
-            const bool is = z < count && rr < rows;
-            const float* from = p.t_acc + ((int64_t)(is ? c.slot[z] : 0) * RP + (is ? rr : 0)) * D + col;
-            const float4 u = is ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
-          }
-          if (first) {
-            first = false;
-            weights(k, tid);
-            __syncthreads();
-          }
-          if (rr >= rows) continue;
-          float a[V];
+        for (int q = 0; q < V; ++q) a[q] = 0.f;
 #pragma unroll
-          for (int q = 0; q < V; ++q) a[q] = 0.f;
+        for (int z = 0; z < kGroupTiles; ++z) {
+          const float2 ab = w_ab[(k * RP + rr) * kGroupTiles + z];
 #pragma unroll
-          for (int z = 0; z < kGroupTiles; ++z) {
-            const float2 ab = w_ab[(k * RP + rr) * kGroupTiles + z];
-#pragma unroll
-            for (int q = 0; q < V; ++q) a[q] = __fmaf_rn(a[q], ab.x, __fmul_rn(v[z][q], ab.y));
-          }
-          put(rr, col, a);
+          for (int q = 0; q < V; ++q) a[q] = __fmaf_rn(a[q], ab.x, __fmul_rn(v[z][q], ab.y));
         }
+        put(rr, col, a);
       }
     }
   }
@@ -1407,10 +1341,13 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 //
 // The join of rows of several groups.  A thread has four columns; SETS thread
 // sets share a row's groups, neighbouring ones each, and join as a tree in
-// shared memory: 1 (at most eight groups, all requested at once), 4, or 128
-// (few rows of very many, 32 columns a CTA).  Reads what the attention kernel
-// wrote a moment ago (L2), so it is a chain of latencies: request (guessed,
-// then checked), its lengths, results.
+// shared memory: 4; 1 for many rows of at most eight groups, all requested at
+// once; or 128 for few rows of very many, 32 columns a CTA.  Reads what the
+// attention kernel wrote a moment ago (L2), so it is a chain of latencies:
+// request (guessed, then checked), its lengths, results; about 4 us of a call.
+// Whole calls with 1 and 4 sets: 1024 rows of 8 groups 52.9 and 52.0 us, 17.5k
+// rows of 6 groups 192.8 and 210.6; with 4 and 128: 8 rows of 128 groups 43.8
+// and 34.7.
 
 template <int D, int SETS>
 __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(const __grid_constant__ Params p) {
@@ -1579,7 +1516,8 @@ cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int 
     cfg.blockDim = dim3(1024);
     return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 128>, p);
   }
-  const int sets = y.gmax <= 8 ? 1 : 4, per = 256 / (D / 4) / sets;
+  const int per4 = 256 / (D / 4) / 4;
+  const int sets = y.gmax <= 8 && out_rows > 12 * kSms * per4 ? 1 : 4, per = 4 / sets * per4;  // (1: more than two rounds of 4)
   const int64_t ctas = (out_rows + per - 1) / per;
   cfg.gridDim = dim3((unsigned)(ctas < 6 * kSms ? ctas : 6 * kSms));
   cfg.blockDim = dim3(256);
