@@ -617,7 +617,8 @@ int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, 
 
 size_t w4a16_kv_attention_workspace_bytes(int B, int T, int q_heads, int heads, int dim, int max_new, int max_len,
                                           int window) {
-  if (B < 1 || T < 1 || heads < 1 || q_heads < heads || q_heads % heads || max_new < 1 || max_len < 1 || window < 0 ||
+  if (B < 1 || T < 1 || heads < 1 || q_heads < heads || q_heads % heads || q_heads / heads > W4A16_KV_MAX_GROUP ||
+      max_new < 1 || max_len < 1 || window < 0 ||
       (dim != 64 && dim != 128 && dim != 256))
     return 0;
   return kv_attention_workspace(B, T, q_heads, heads, dim, max_new, max_len, window);

@@ -49,3 +49,22 @@ def test_more_requests_than_lanes():
                 assert torch.equal(_alone(step, b, cache, 0), out[step.cu[b]:step.cu[b + 1]]), b
         ref, bound = step.reference()
         assert_close(out, ref, bound, str(B))
+
+
+@pytest.mark.parametrize("heads,dim,block", [(9, 64, 16), (20, 128, 16), (12, 128, 32), (33, 64, 64), (5, 256, 16)])
+@pytest.mark.parametrize("T", [70, 2300])
+def test_append_heads_in_several_ctas(heads, dim, block, T):
+    """More heads than a CTA takes, few tokens and many; runs that begin inside blocks and cross CTAs."""
+    import test_gpu_kv_append as A
+
+    runs, at = [], 0
+    for i in range(10 ** 6):
+        n = min(1 + (7 * i * i) % (2 * block), block, T - at)
+        runs.append((i, (3 * i) % (block - n + 1), n))
+        at += n
+        if at == T:
+            break
+    slots = [b * block + o + k for b, o, n in runs for k in range(n)]
+    g = torch.Generator().manual_seed(T + heads)
+    k, v = ((torch.randn(T, heads, dim, generator=g) * torch.rand(T, heads, 1, generator=g) * 4).to(torch.bfloat16) for _ in "kv")
+    A._check(k, v, slots, heads, dim, block, len(runs), seed=heads)

@@ -116,3 +116,27 @@ def test_kernels_without_dependent_launch(monkeypatch):
     finally:
         monkeypatch.delenv("W4A16_PDL")
         ops.lib().w4a16_debug_reload_env()
+
+
+def test_counters_are_zeroed_after_a_timeout(monkeypatch):
+    """What device_status does when a wait ran out (the flag word is faked; no kernel waits)."""
+    step = Step(8, 2, 128, 32, [9000], [1], seed=21)
+    cache = step.cache()
+    want = step.run(cache=cache)
+    for c, _ in ops._kv_counter_cache.values():
+        c.fill_(3)
+    ops._kv_capture_sets[0][0].fill_(5)
+
+    class Lib:
+        def __getattr__(self, name):
+            return getattr(real, name)
+
+        def w4a16_device_status(self, stream, flags):
+            flags._obj.value = ops.DEVICE_TIMEOUT
+            return ops.ERR_DEVICE
+
+    real = ops.lib()
+    with monkeypatch.context() as m:
+        m.setattr(ops, "lib", lambda: Lib())
+        assert ops.device_status() == ops.DEVICE_TIMEOUT
+    assert torch.equal(step.run(cache=cache), want) and ops.device_status() == 0

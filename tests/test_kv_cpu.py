@@ -116,6 +116,14 @@ def test_workspace_query(L):
     assert f(4, 4, 8, 2, 128, 1, 50000, 512) <= f(4, 4, 8, 2, 128, 1, 50000, 0)
 
 
+def test_workspace_query_refuses_what_the_call_refuses(L):
+    """Too many query heads a key head; steps whose sizes pass 64 bits."""
+    f = L.w4a16_kv_attention_workspace_bytes
+    assert f(1, 1, 64, 2, 128, 1, 64, 0) > 0 and f(1, 1, 66, 2, 128, 1, 64, 0) == 0 and f(1, 1, 64, 1, 128, 1, 64, 0) == 0
+    big = 2 ** 30 - 1
+    assert f(big, big, 65535, 65535, 64, 1, 2 ** 31 - 1, 0) == 0 and f(big, big, 64, 2, 64, big, 2 ** 31 - 1, 0) == 0
+
+
 def test_python_layer_checks_before_any_launch():
     bf, f8 = torch.bfloat16, torch.float8_e4m3fn
     with pytest.raises(ValueError):  # host tensors
