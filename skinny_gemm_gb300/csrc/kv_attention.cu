@@ -30,8 +30,10 @@
 // of 2 heads x 256: 87 us, 5.66 TB/s; one of 131k tokens 34 us, 3.9 TB/s, where
 // set-up (2 us), the first copies (2 us), the groups that a cut divides (2 to 5
 // us) and the join (4 us) weigh more.  A CTA has two to five tiles (64 KB each with
-// heads of 256) in flight.  Instruction issue from 16 rows on: 32 rows a tile
-// take about 2000 clocks whatever the head size (prompt chunks 236 TFLOP/s).
+// heads of 256) in flight.  From 16 rows on the softmax warps' instructions and
+// the chain of waits and issues in the MMA warp, each about 2000 clocks a tile of
+// 32 rows (3 prompt chunks of 300 over 6k tokens, 28/4 heads of 128: 194 us, 234
+// TFLOP/s; S and O issued by two warps: 208).
 //
 // CTA: 4 NG + 4 NG + 3 warps (NG groups of R query rows).
 //   softmax warps  a thread per token: scores from TMEM, mask, maximum,
@@ -815,8 +817,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
             const uint64_t ad = D < 128 ? umma_desc(vk, 512, 512, 4) : umma_desc(vk, 1024, 1024, 2);
             umma_f8(go, d + c * C, ad, umma_desc(pa + k * 512, 128, 2048, 0), id_o, k > 0);
           }
+        umma_commit_if(go, empty(slot));  // (first: whoever sees O done knows that no arrival is on its way)
         umma_commit_if(go, o_full(u & 1));
-        umma_commit_if(go, empty(slot));
       }
     }
     if (!ok && lane == 0) give_up();
