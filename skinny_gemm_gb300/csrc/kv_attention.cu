@@ -58,6 +58,7 @@
 
 #include "common.cuh"
 #include "kv.cuh"
+#include "kv_line.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -66,7 +67,6 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTile = 128;      // tokens per tile (the M of the MMAs)
 constexpr int kGroupTiles = 8;  // tiles per group
 constexpr int kGroupTokens = kTile * kGroupTiles;
 constexpr int kDescs = 8;       // tile descriptors in flight
@@ -144,17 +144,15 @@ struct Geo {
   static_assert(kCtas * kTmem <= 512, "tensor memory of an SM");
 };
 
-struct Params {
+struct Params : Line {
   const uint16_t* q;
   int64_t q_stride;
   const float* k_scale;
   const float* v_scale;
   const int32_t* table;
-  const int32_t* cu;
-  const int32_t* lens;
   uint16_t* out;
-  int B, T, q_heads, heads, G, TQ;  // G query heads per key head, TQ tokens per row tile
-  int blocks, shift, max_blocks, max_new, max_len, window;
+  int q_heads, heads, G;  // G query heads per key head
+  int blocks, shift, max_blocks;
   float qk_scale;  // scale * log2(e)
   int gmax;        // group slots per row
   int grid;
@@ -171,94 +169,6 @@ struct Params {
 
 struct Maps {
   CUtensorMap k, v;
-};
-
-// ---- the line of tiles -----------------------------------------------------------------------
-
-// One request of the step: its row tiles and their ranges of 128-token tiles.
-struct Req {
-  int c0, fresh, base;  // first row, new tokens (0: nothing to do), tokens before them
-};
-
-struct RawReq {
-  int c0, c1, len;
-  __device__ __forceinline__ RawReq(const Params& p, int b) : c0(0), c1(0), len(0) {
-    if (b < p.B) c0 = p.cu[b], c1 = p.cu[b + 1], len = p.lens[b];
-  }
-};
-
-__device__ __forceinline__ Req check_req(const Params& p, const RawReq& w, bool* bad) {
-  Req r{0, 0, 0};
-  const int c0 = w.c0, c1 = w.c1, len = w.len;
-  const bool ok = c0 >= 0 && c0 <= c1 && c1 <= p.T && c1 - c0 <= p.max_new && c1 - c0 <= len && len <= p.max_len;
-  if (!ok) {
-    if (c1 != c0) *bad = true;
-    return r;
-  }
-  r.c0 = c0;
-  r.fresh = c1 - c0;
-  r.base = len - r.fresh;
-  return r;
-}
-
-__device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) { return check_req(p, RawReq(p, b), bad); }
-
-__device__ __forceinline__ int row_tiles(const Params& p, const Req& r) {
-  return r.fresh <= p.TQ ? (r.fresh > 0) : (r.fresh + p.TQ - 1) / p.TQ;
-}
-__device__ __forceinline__ int first_tile(const Params& p, const Req& r, int rt) {
-  return p.window > 0 ? max(0, r.base + rt * p.TQ - p.window + 1) / kTile : 0;
-}
-__device__ __forceinline__ int last_tile(const Params& p, const Req& r, int rt) {
-  return (r.base + min((rt + 1) * p.TQ, r.fresh) - 1) / kTile;
-}
-
-// sum over 0 <= i < n of floor((b + i a) / m), for sums below 2^32: whole
-// parts are taken out, then the lattice points under the line are counted
-// along the other axis, as in Euclid's algorithm.
-__device__ __noinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  uint32_t s = 0;
-  while (n > 0) {
-    const uint32_t qa = a / m, qb = b / m;
-    if (qa) s += (uint32_t)((uint64_t)n * (n - 1) / 2) * qa;
-    s += n * qb;
-    a -= qa * m;
-    b -= qb * m;
-    const uint32_t y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y - n * m;
-    const uint32_t t = a;
-    a = m;
-    m = t;
-  }
-  return s;
-}
-
-// Tiles of the row tiles before rt (of one key head).
-__device__ inline int tiles_before(const Params& p, const Req& r, int rt) {
-  const int n = row_tiles(p, r);
-  if (rt <= 0) return 0;
-  if (rt == 1) return last_tile(p, r, 0) - first_tile(p, r, 0) + 1;
-  int s = rt + (int)floor_sum(rt == n ? n - 1 : rt, kTile, p.TQ, r.base + p.TQ - 1);
-  if (rt == n) s += last_tile(p, r, n - 1);
-  if (p.window > 0) {
-    const int x = r.base - p.window + 1;  // first token of row tile i: max(0, x + i TQ)
-    const int i0 = x >= 0 ? 0 : min(rt, (-x + p.TQ - 1) / p.TQ);
-    s -= (int)floor_sum(rt - i0, kTile, p.TQ, max(0, x + i0 * p.TQ));
-  }
-  return s;
-}
-
-// The cut of `total` tiles into grid ranges that differ by at most one tile.
-struct Cut {
-  int per, rem;
-  __device__ __forceinline__ Cut(int total, int grid) : per(total / grid), rem(total - per * grid) {}
-  __device__ __forceinline__ int begin(int c) const { return c * per + min(c, rem); }
-  __device__ __forceinline__ int owner(int x) const {
-    const int big = rem * (per + 1);
-    return x < big ? x / (per + 1) : rem + (x - big) / max(per, 1);
-  }
 };
 
 // ---- shared pieces -----------------------------------------------------------------------------

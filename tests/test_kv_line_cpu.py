@@ -1,0 +1,65 @@
+"""The line of tiles of the paged attention (csrc/kv_line.cuh), built for the host: whole numbers against plain loops."""
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "skinny_gemm_gb300", "csrc")
+SOURCE = r"""
+#include "kv_line.cuh"
+using namespace w4a16;
+extern "C" int tiles(int TQ, int window, int base, int fresh, int rt) {
+  Line p{};
+  p.TQ = TQ;
+  p.window = window;
+  return tiles_before(p, Req{0, fresh, base}, rt);
+}
+"""
+TOP = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def line(tmp_path_factory):
+    d = tmp_path_factory.mktemp("line")
+    src, lib = d / "line.cpp", d / "line.so"
+    src.write_text(SOURCE)
+    # (-fwrapv: an overflow gives what the device gives)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)], check=True)
+    return ctypes.CDLL(str(lib))
+
+
+def _tiles(TQ, window, base, fresh, rt):
+    """Tiles of the row tiles before rt: from the first token that their first row sees to their last row's own."""
+    n = 0
+    for i in range(rt):
+        last = base + min((i + 1) * TQ, fresh) - 1
+        first = max(0, base + i * TQ - window + 1) if window else 0
+        n += last // 128 - first // 128 + 1
+    return n
+
+
+def _check(line, TQ, window, base, fresh):
+    n = -(-fresh // TQ)
+    for rt in sorted({0, 1, 2, n // 3, n // 2, n - 1, n} & set(range(n + 1))):
+        assert line.tiles(TQ, window, base, fresh, rt) == _tiles(TQ, window, base, fresh, rt), (TQ, window, base, fresh, rt)
+
+
+@pytest.mark.parametrize("TQ", [1, 2, 3, 4, 5, 6, 8, 12, 24, 32])
+def test_tiles_before(line, TQ):
+    r = np.random.RandomState(TQ)
+    for _ in range(200):
+        fresh = int(r.randint(1, 700))
+        base = int(r.choice([0, 1, 127, 128, int(r.randint(0, 5000))]))
+        window = int(r.choice([0, 1, 2, 100, 128, 129, int(r.randint(1, 6000)), 10 ** 9]))
+        _check(line, TQ, window, base, fresh)
+
+
+@pytest.mark.parametrize("TQ", [1, 8, 32])
+@pytest.mark.parametrize("window", [TOP, TOP - 1, TOP - 7, TOP - 8, TOP - 31, TOP - 40, 2 ** 30])
+def test_windows_up_to_the_largest_number(line, TQ, window):
+    """A window near 2^31 ("no limit"), from an empty cache on and near the longest request (within 2^31 tiles, as the
+    call checks)."""
+    for base, fresh in ((0, 300), (0, 9), (1, 64), (5, 700), (TQ, 300), (TOP - 400, 3 * TQ), (TOP - 3 * TQ, 3 * TQ)):
+        _check(line, TQ, window, base, fresh)
