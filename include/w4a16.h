@@ -399,7 +399,8 @@ int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, 
  * tokens and lens[b] <= max_len (max_len <= max_blocks * block).  They only
  * size the launch and the workspace.  All rows of a request that exceeds one
  * of them (or is shorter than its new tokens) are written as zeros, and
- * W4A16_DEVICE_KV_RANGE is raised.
+ * W4A16_DEVICE_KV_RANGE is raised; so are all rows of a step whose cu steps
+ * back anywhere.
  *
  * Batch invariance.  The tokens are taken in tiles at fixed positions and
  * joined in a fixed order, whatever the batch: out[t] depends, bit for bit,

@@ -163,6 +163,7 @@ struct Params : Line {
   float2* g_ml;  // [gmax][T][q_heads]
   float* t_acc;  // [grid][t_slots][RP][D]
   float2* t_ml;  // [grid][t_slots][RP]
+  int* refused;   // [1] the step's offsets step back (written by every call)
   int* counters;  // [grid] tiles done of divided groups, by the CTA of the first; zero between calls
   int* flags;
 };
@@ -434,6 +435,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     pdl_launch_dependents();  // (after the wait: what the next kernel reads of this call's inputs is there when it starts)
     int mine_end = 0;         // inclusive prefix of this lane's request
     int rows = 0;             // of valid requests
+    bool back = false;
     auto scan = [&](const RawReq& w) {  // 32 requests; their inclusive prefix of tiles after `total`
       mine = check_req(p, w, &bad);
       const int rts = row_tiles(p, mine);
@@ -450,15 +452,19 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     for (; b0 < p.B; b0 += 32) {
       const RawReq w = ahead;
       if (b0 + 32 < p.B) ahead = RawReq(p, b0 + 32 + lane);
+      back |= steps_back(w);
       scan(w);
       total = __shfl_sync(0xffffffffu, mine_end, 31);
       rows += mine.fresh;
       if (b0 == 32 * lane) ends = total;
     }
     rows = __reduce_add_sync(0xffffffffu, rows);
+    const bool refused = __any_sync(0xffffffffu, back);
+    if (refused) rows = total = 0;
     if (lane == 0) {
       s_rest[0] = p.T - rows;
       s_rest[1] = total;
+      if (blockIdx.x == 0) *p.refused = refused;
     }
     if (bad && blockIdx.x == 0) atomicOr(p.flags, W4A16_DEVICE_KV_RANGE);
     const Cut cut(total, p.grid);
@@ -1242,7 +1248,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
       bool bad_req = false;
       const Req rq = load_req(p, find_request(p.cu, p.B, t), &bad_req);
-      if (t >= rq.c0 && t < rq.c0 + rq.fresh) continue;
+      if (s_rest[1] > 0 && t >= rq.c0 && t < rq.c0 + rq.fresh) continue;  // (no tiles: a refused step)
       for (int i = tid; i < p.q_heads * (D / 8); i += NT)
         *reinterpret_cast<uint4*>(p.out + (int64_t)t * p.q_heads * D + 8 * i) = make_uint4(0, 0, 0, 0);
     }
@@ -1294,9 +1300,10 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
       out = empty_state();
       const RowGroups<D> g(p, r, j, hq);
       RawReq now = raw;
+      int odd = 0;
       if (!waited) {
         pdl_wait();
-        if (set == 0 && c == 0) now = RawReq(p, b);
+        if (set == 0 && c == 0) now = RawReq(p, b), odd = __ldcg(p.refused);
       }
       if (mine) {
         if constexpr (SETS == 1) {
@@ -1314,8 +1321,9 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
           if (per * set < g.n) out = g.tree(p, per * set, per, col);
         }
       }
-      again = !waited && __syncthreads_or(now.c0 != raw.c0 || now.c1 != raw.c1 || now.len != raw.len);
+      again = !waited && __syncthreads_or(now.c0 != raw.c0 || now.c1 != raw.c1 || now.len != raw.len || odd);
       waited = true;
+      if (again && __ldcg(p.refused)) return;  // the attention kernel wrote zeros, and no groups
     }
     if constexpr (SETS > 1) {
       s_set[sub * SETS + set][c] = out;
@@ -1338,7 +1346,7 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
 struct Layout {
   int RP, TQ, gmax, grid, t_slots, seg_cost;
   bool fits;  // positions on the line and rows of group results fit in 31 bits
-  size_t g_acc, g_ml, t_acc, t_ml, bytes;
+  size_t g_acc, g_ml, t_acc, t_ml, refused, bytes;
 };
 
 template <int D>
@@ -1380,9 +1388,7 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   y.seg_cost = seg_cost(y.RP);
   // no more CTAs than tiles
   const int64_t per = ((int64_t)max_len + kTile - 1) / kTile;
-  int64_t row_tiles = (int64_t)(T < B ? T : B) * (((int64_t)max_new + y.TQ - 1) / y.TQ);
-  const int64_t by_rows = (T < B ? T : B) + (int64_t)T / y.TQ;
-  if (by_rows < row_tiles) row_tiles = by_rows;
+  const int64_t row_tiles = most_row_tiles(B, T, y.TQ, max_new);
   y.fits = (double)row_tiles * heads * (double)(per + y.seg_cost) <= INT32_MAX && (double)y.gmax * T * q_heads <= INT32_MAX;
   if (!y.fits) return y;
   const int64_t most = row_tiles * heads * (per + y.seg_cost);
@@ -1395,7 +1401,8 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   y.g_ml = y.g_acc + up((size_t)y.gmax * T * q_heads * dim * 4);
   y.t_acc = y.g_ml + up((size_t)y.gmax * T * q_heads * 8);
   y.t_ml = y.t_acc + up((size_t)y.grid * y.t_slots * y.RP * dim * 4);
-  y.bytes = y.t_ml + up((size_t)y.grid * y.t_slots * y.RP * 8);
+  y.refused = y.t_ml + up((size_t)y.grid * y.t_slots * y.RP * 8);
+  y.bytes = y.refused + up(4);
   return y;
 }
 
@@ -1502,6 +1509,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t 
   p.g_ml = reinterpret_cast<float2*>(w + y.g_ml);
   p.t_acc = reinterpret_cast<float*>(w + y.t_acc);
   p.t_ml = reinterpret_cast<float2*>(w + y.t_ml);
+  p.refused = reinterpret_cast<int*>(w + y.refused);
   p.flags = a.flags;
   p.counters = a.counters;
   switch (a.cache.dim) {

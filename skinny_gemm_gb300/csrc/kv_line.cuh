@@ -58,6 +58,17 @@ KV_LINE Req check_req(const Line& p, const RawReq& w, bool* bad) {
   return r;
 }
 
+// Offsets that step back anywhere make requests overlap, each of them valid by
+// itself, and a line longer than the call's arrays are made for: such a step is
+// refused as a whole.
+KV_LINE bool steps_back(const RawReq& w) { return w.c1 < w.c0; }
+
+// The most row tiles of a step whose offsets do not step back.
+inline int64_t most_row_tiles(int B, int T, int TQ, int max_new) {
+  const int64_t reqs = T < B ? T : B, each = reqs * (((int64_t)max_new + TQ - 1) / TQ), by_rows = reqs + (int64_t)T / TQ;
+  return by_rows < each ? by_rows : each;
+}
+
 KV_LINE Req load_req(const Line& p, int b, bool* bad) { return check_req(p, RawReq(p, b), bad); }
 
 KV_LINE int row_tiles(const Line& p, const Req& r) {

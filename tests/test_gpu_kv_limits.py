@@ -21,3 +21,31 @@ def test_windows_longer_than_any_request(hq, hkv, dim):
     for window in (max(step.lens), TOP - 33, TOP - 8, TOP - 1, TOP):
         assert torch.equal(step.run(window=window, cache=cache), want), window
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("B,cut,T,hq,dim,max_len", [(5, 2, 1, 8, 128, 1024), (21, 2, 2, 8, 256, 384), (3, 2, 2, 4, 64, 5000),
+                                                    (70, 50, 69, 8, 128, 2000), (2, 1, 40, 8, 128, 3000)])
+def test_offsets_that_step_back_refuse_the_step(B, cut, T, hq, dim, max_len):
+    """cu that decreases somewhere: the flag, zeros in every row, nothing outside the workspace; the next call is right."""
+    hkv, block = 2, 16
+    step = Step(hq, hkv, dim, block, [max_len - 1], [1], seed=B)
+    cache = step.cache()
+    table = torch.from_numpy(step.table).cuda().repeat(B, 1)
+    q = torch.randn(T, hq, dim, device="cuda").to(torch.bfloat16)
+    if B == T + 1:  # one request's end before its beginning, the others in order
+        cu = [i if i < cut else i - 1 for i in range(B + 1)]
+        cu[cut] = cut - 2
+    else:
+        cu = [T * (i % 2) for i in range(B + 1)]
+    cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), max_len, dtype=torch.int32, device="cuda")
+    n = ops.kv_attention_workspace_bytes(B, T, hq, cache, T, max_len)
+    ws = torch.full((n + (1 << 20),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 7.0)
+    ops.kv_attention(q, cache, table, cu, lens, T, max_len, out=out, workspace=ws[:n])
+    assert ops.device_status() & ops.DEVICE_KV_RANGE
+    assert bool((ws[n:] == 0xFF).all())
+    assert torch.equal(out, torch.zeros_like(out))
+    ref, bound = step.reference()
+    assert_close(step.run(cache=cache, workspace=ws), ref, bound)
+    assert ops.device_status() == 0

@@ -16,6 +16,18 @@ extern "C" int tiles(int TQ, int window, int base, int fresh, int rt) {
   p.window = window;
   return tiles_before(p, Req{0, fresh, base}, rt);
 }
+// Row tiles of a step's accepted requests; -1: refused.
+extern "C" long long row_tiles_of(const int* cu, const int* lens, int B, int T, int TQ, int max_new, int max_len) {
+  Line p{cu, lens, B, T, TQ, max_new, max_len, 0};
+  long long n = 0;
+  bool bad = false, back = false;
+  for (int b = 0; b < B; ++b) {
+    back |= steps_back(RawReq(p, b));
+    n += row_tiles(p, load_req(p, b, &bad));
+  }
+  return back ? -1 : n;
+}
+extern "C" long long most(int B, int T, int TQ, int max_new) { return most_row_tiles(B, T, TQ, max_new); }
 """
 TOP = 2 ** 31 - 1
 
@@ -27,7 +39,10 @@ def line(tmp_path_factory):
     src.write_text(SOURCE)
     # (-fwrapv: an overflow gives what the device gives)
     subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)], check=True)
-    return ctypes.CDLL(str(lib))
+    L = ctypes.CDLL(str(lib))
+    for f in (L.row_tiles_of, L.most):
+        f.restype = ctypes.c_longlong
+    return L
 
 
 def _tiles(TQ, window, base, fresh, rt):
@@ -63,3 +78,23 @@ def test_windows_up_to_the_largest_number(line, TQ, window):
     call checks)."""
     for base, fresh in ((0, 300), (0, 9), (1, 64), (5, 700), (TQ, 300), (TOP - 400, 3 * TQ), (TOP - 3 * TQ, 3 * TQ)):
         _check(line, TQ, window, base, fresh)
+
+
+def _row_tiles(line, cu, lens, T, TQ, max_new, max_len):
+    a, b = ((ctypes.c_int * len(x))(*x) for x in (cu, lens))
+    return line.row_tiles_of(a, b, len(lens), T, TQ, max_new, max_len)
+
+
+def test_no_step_has_more_row_tiles_than_its_arrays_are_made_for(line):
+    """Any offsets: requests accepted by themselves, bounds that do not hold, offsets out of range or stepping back."""
+    r = np.random.RandomState(1)
+    for _ in range(4000):
+        B, T, TQ = int(r.randint(1, 40)), int(r.randint(1, 50)), int(r.choice([1, 2, 3, 8, 32]))
+        max_new, max_len = int(r.randint(1, 20)), 100
+        cu = np.sort(r.randint(-3, T + 4, B + 1)) if r.rand() < 0.6 else r.randint(-3, T + 4, B + 1)
+        lens = r.randint(-2, 110, B)
+        n = _row_tiles(line, [int(x) for x in cu], [int(x) for x in lens], T, TQ, max_new, max_len)
+        assert n <= line.most(B, T, TQ, min(max_new, T)), (cu, lens, T, TQ, max_new)
+        assert (n == -1) == bool(np.any(np.diff(cu) < 0))
+    assert _row_tiles(line, [0, 1, 0, 1, 0, 1], [1024] * 5, 1, 4, 1, 1024) == -1
+    assert _row_tiles(line, [0, 2] * 11, [384] * 21, 2, 8, 2, 384) == -1
