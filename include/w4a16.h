@@ -345,7 +345,8 @@ typedef struct {
  * ids) in request order, beginning at entry *head (a device int32; NULL is
  * 0), and written to their entries of table (int32 [B][max_blocks]; entries
  * of earlier blocks are read, later ones left alone); *head_out = *head +
- * blocks taken (head_out must not be head).  For token t < cu[B] of request
+ * blocks taken.  No array that the call writes may overlap another, but lens
+ * may be cached itself (lengths advanced in place).  For token t < cu[B] of request
  * b: positions[t] = cached[b] + t - cu[b], slots[t] its slot (int32 [T]); for
  * cu[B] <= t < T (a padded batch) both are -1.
  * Out-of-range inputs raise W4A16_DEVICE_KV_RANGE and never lead outside the

@@ -591,6 +591,22 @@ int w4a16_kv_plan(const int32_t* cached, const int32_t* fresh, int32_t* table, c
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
   KvPlanArgs a{cached, fresh, table, free_blocks, head, cu, lens, slots, positions, head_out,
                B, T, block, max_blocks, n_free, nullptr};
+  // (the CTAs read all of the inputs while others write outputs)
+  const struct {
+    const void* p;
+    int64_t n;
+    const char* name;
+  } arrays[] = {{cached, B, "cached"}, {fresh, B, "fresh"}, {free_blocks, n_free, "free_blocks"}, {head, head ? 1 : 0, "head"},
+                {table, (int64_t)B * max_blocks, "table"}, {cu, (int64_t)B + 1, "cu"}, {lens, B, "lens"},
+                {slots, T, "slots"}, {positions, T, "positions"}, {head_out, 1, "head_out"}};
+  for (int i = 4; i < 10; ++i)  // what the call writes
+    for (int j = 0; j < i; ++j) {
+      const auto &x = arrays[i], &y = arrays[j];
+      const uintptr_t at = reinterpret_cast<uintptr_t>(x.p), bt = reinterpret_cast<uintptr_t>(y.p);
+      const bool in_place = i == 6 && j == 0 && lens == cached;
+      if (!in_place && x.n > 0 && y.n > 0 && at < bt + 4 * (uintptr_t)y.n && bt < at + 4 * (uintptr_t)x.n)
+        return fail(W4A16_ERR_SHAPE, "%s and %s overlap (only lens may be cached itself)", x.name, y.name);
+    }
   if (int rc = flag_pointer(&a.flags)) return rc;
   cudaError_t e = launch_kv_plan(a, env().pdl, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_kv_plan launch");

@@ -41,8 +41,12 @@ constexpr int kPlanTokens = 2048;  // tokens per CTA
 
 struct PlanParams {
   KvPlanArgs a;
-  int shift;  // log2(block)
+  int shift;    // log2(block)
+  int advance;  // lens is cached, and several CTAs read it: kv_advance_kernel writes it
 };
+
+// What is taken for request b's cached tokens, whatever its entry says.
+__device__ __forceinline__ int cached_of(const KvPlanArgs& a, int cached) { return min(max(cached, 0), INT32_MAX - a.T); }
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
   __shared__ int s_cu[kPlanThreads + 1], s_first[kPlanThreads + 1], s_cached[kPlanThreads];
@@ -64,7 +68,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
       fresh = a.fresh[b];
       if (cached < 0 || fresh < 0 || fresh > a.T || cached > INT32_MAX - a.T) {
         bad = true;
-        cached = min(max(cached, 0), INT32_MAX - a.T);
+        cached = cached_of(a, cached);
         fresh = min(max(fresh, 0), a.T);
       }
     }
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
     s_cached[tid] = cached;
     if (blockIdx.x == 0 && b < a.B) {
       a.cu[b] = s_cu[tid];
-      a.lens[b] = len;
+      if (!p.advance) a.lens[b] = len;
     }
     __syncthreads();
     // request of item x: the last i with sums[i] <= x (x is below the chunk's total)
@@ -175,6 +179,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
     *a.head_out = (int)min((int64_t)head + taken, (int64_t)max(head, a.n_free));
   }
   if (bad) atomicOr(a.flags, W4A16_DEVICE_KV_RANGE);
+}
+
+// Lengths advanced in place, after every CTA of the plan has read them.
+__global__ void __launch_bounds__(256) kv_advance_kernel(KvPlanArgs a) {
+  for (int b = blockIdx.x * 256 + threadIdx.x; b < a.B; b += gridDim.x * 256)
+    a.lens[b] = cached_of(a, a.cached[b]) + a.cu[b + 1] - a.cu[b];
 }
 
 // ---- append --------------------------------------------------------------------------------
@@ -454,13 +464,20 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendPara
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, int pdl, cudaStream_t s) {
-  PlanParams p{a, __builtin_ctz((unsigned)a.block)};
+  PlanParams p{a, __builtin_ctz((unsigned)a.block), 0};
   // a thread per request and per token up to the CTA's size, at least four warps
   int threads = a.B > a.T ? a.B : a.T;
   threads = threads < 128 ? 128 : threads > kPlanThreads ? kPlanThreads : (threads + 31) / 32 * 32;
   const int grid = a.T > 0 ? (a.T + kPlanTokens - 1) / kPlanTokens : 1;
+  // One CTA reads its requests' lengths before it writes them; where several read them all, a second launch advances
+  // them when they are done (333 prompt chunks 1.1 us more than with lens apart).
+  p.advance = grid > 1 && a.lens == a.cached;
   void* args[] = {&p};
-  return launch((const void*)kv_plan_kernel, dim3((unsigned)grid), threads, args, pdl, s);
+  cudaError_t e = launch((const void*)kv_plan_kernel, dim3((unsigned)grid), threads, args, pdl, s);
+  if (e != cudaSuccess || !p.advance) return e;
+  void* advance[] = {&p.a};
+  const int ctas = a.B / 256 + 1;
+  return launch((const void*)kv_advance_kernel, dim3((unsigned)(ctas < 608 ? ctas : 608)), 256, advance, 0, s);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int pdl, cudaStream_t s) {

@@ -672,7 +672,9 @@ def kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: 
     table: int32 [B, max_blocks], its entries for the new blocks written in
     place; free: int32 block ids to take from, beginning at entry ``head``
     (int32 [1] on the device; None is 0; the plan's ``head`` is the next one).
-    T rows: the sum of ``new``, or more (the rest get slot -1)."""
+    T rows: the sum of ``new``, or more (the rest get slot -1).  ``out``: a plan
+    to write; its arrays overlap nothing else, but its ``lens`` may be ``cached``
+    (lengths advanced in place)."""
     tp = _i32(table, "table")
     if table.dim() != 2:
         raise ValueError("table must be [B, max_blocks]")

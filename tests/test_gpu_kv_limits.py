@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from kv_cases import Step, assert_close
+from kv_cases import Step, assert_close, make_lengths, ref_plan
 from skinny_gemm_gb300 import ops
 
 pytestmark = pytest.mark.gpu
@@ -48,4 +48,40 @@ def test_offsets_that_step_back_refuse_the_step(B, cut, T, hq, dim, max_len):
     assert torch.equal(out, torch.zeros_like(out))
     ref, bound = step.reference()
     assert_close(step.run(cache=cache, workspace=ws), ref, bound)
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("B,new_max", [(6, 2), (5, 3000), (300, 60), (1500, 40)])
+def test_lengths_advanced_in_place(B, new_max):
+    """lens is the cached array, in steps of one and of many CTAs; twice in one captured graph."""
+    block = 16
+    cached, new = make_lengths(B, 300, new_max, B, block)
+    need = sum(-(-(c + 2 * n) // block) for c, n in zip(cached, new))
+    width = max(-(-(c + 2 * n) // block) for c, n in zip(cached, new))
+    table = [[1000 + b * width + j if j * block < c else -1 for j in range(width)] for b, c in enumerate(cached)]
+    free, T = list(range(500000, 500000 + need)), sum(new)
+    lens, fresh, t, f = (torch.tensor(x, dtype=torch.int32).cuda() for x in (cached, new, table, free))
+    plans = [ops.KVPlan.empty(B, T) for _ in range(2)]
+    for p in plans:
+        p.lens = lens
+    start = lens.clone()
+
+    def steps():
+        ops.kv_plan(lens, fresh, t, f, T, block, out=plans[0])
+        ops.kv_plan(lens, fresh, t, f, T, block, head=plans[0].head, out=plans[1])
+
+    steps()
+    for captured in (False, True):
+        if captured:
+            lens.copy_(start)
+            t.copy_(torch.tensor(table, dtype=torch.int32))
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                steps()
+            g.replay()
+        tw, c, h = table, cached, 0
+        for p in plans:
+            tw, cu, c, slots, pos, h = ref_plan(c, new, tw, free, h, T, block)
+            assert p.cu.tolist() == cu and p.slots.tolist() == slots and p.positions.tolist() == pos and p.head.tolist() == [h]
+        assert t.tolist() == tw and lens.tolist() == c
     assert ops.device_status() == 0
