@@ -14,7 +14,10 @@
 // MMA's N and not its 128-row M; O^T = V^T [hi | lo] takes V as it lies too (an
 // M-major operand).  With z in log2 units, a token's V scale vs joins its
 // weight before the maximum is taken (z + log2 vs), so the terms stay in
-// e4m3's range whatever the blocks' scales; the row sum takes p / vs.
+// e4m3's range whatever the blocks' scales; the row sum takes the weight
+// without vs, over all of 2^-64 to 2^120 (an exponential of z - max, from which
+// the product's weight follows by a power of two; taken the other way round, it
+// was lost where vs was 2^134 below another's).
 //
 // Split.  A tile is 128 tokens at a fixed position; a group eight tiles.  A
 // tile gives (maximum m, sum l, O) per row; a group folds its tiles in order, a
@@ -189,6 +192,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
@@ -215,12 +225,16 @@ __device__ __forceinline__ void split2h(float a, float b, uint32_t& hi, uint32_t
 
 // One step of a fold: the running (m, l) takes in (mt, lt); al and be are
 // what the running and the new accumulators are multiplied by.  An empty
-// side (m = -inf) leaves the other as it is, bit for bit.
+// side (m = -inf) leaves the other as it is, bit for bit.  Each factor is a
+// square, and the sum takes its root twice: below 2^-126 the accumulators it
+// stands for vanish beside the others, but the sum, which does not hold the V
+// scales that m holds, may be as large as 2^80 then.
 __device__ __forceinline__ void fold_ml(float& m, float& l, float mt, float lt, float& al, float& be) {
   const float top = fmaxf(m, mt), ref = top == -INFINITY ? 0.f : top;
-  al = ex2(m - ref);
-  be = ex2(mt - ref);
-  l = __fmaf_rn(l, al, __fmul_rn(lt, be));
+  const float a = ex2(__fmul_rn(m - ref, 0.5f)), b = ex2(__fmul_rn(mt - ref, 0.5f));
+  al = __fmul_rn(a, a);
+  be = __fmul_rn(b, b);
+  l = __fmaf_rn(__fmul_rn(l, a), a, __fmul_rn(__fmul_rn(lt, b), b));
   m = top;
 }
 
@@ -870,7 +884,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const int2 lim = s_lim[R * grp + i];
-          s[i] = dead || tok < lim.x || tok > lim.y ? -INFINITY : __fmaf_rn(s[i], ks, (float)ve);
+          s[i] = dead || tok < lim.x || tok > lim.y ? -INFINITY : __fmul_rn(s[i], ks);
         }
         uint8_t* v_row = base + ((2 * t + 1) % NS) * X::kSlot;
         constexpr int kRowB = X::kRowB, kCh = kRowB / 16;
@@ -933,10 +947,9 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           }
         }
       } else {
-        const float lv = (float)ve;
 #pragma unroll
         for (int i = 0; i < R; i += 2) {
-          const float2 z = fma2(make_float2(s[i], s[i + 1]), make_float2(ks, ks), make_float2(lv, lv));
+          const float2 z = mul2(make_float2(s[i], s[i + 1]), make_float2(ks, ks));
           s[i] = z.x;
           s[i + 1] = z.y;
         }
@@ -944,9 +957,14 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       // maxima over the tile: the warp, then the group's four
       float* sm = s_max + par * 4 * RP + R * grp;
       {
+        const float lv = (float)ve;
         float m[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) m[i] = warp_max(s[i]);
+        for (int i = 0; i < R; i += 2) {
+          const float2 z = add2(make_float2(s[i], s[i + 1]), make_float2(lv, lv));
+          m[i] = warp_max(z.x);
+          m[i + 1] = warp_max(z.y);
+        }
         if (lane == 0) {
 #pragma unroll
           for (int i = 0; i < R; i += 4)
@@ -960,15 +978,21 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         const float* a = sm + lane % R;
         top = fmaxf(fmaxf(a[0], a[RP]), fmaxf(a[2 * RP], a[3 * RP]));
         if (w4 == 0 && lane < R) s_top[ring * RP + R * grp + lane] = top;
-        top = top == -INFINITY ? 0.f : __fsub_rn(top, 8.f);
+        top = top == -INFINITY ? 0.f : __fsub_rn(top, 28.f);
       }
-      // weights times 256 (sums and O carry the factor, their quotient does not), and their two terms
+      // exp(z) in the sum's unit; times vs, it is the weight in the product's: 256 for the tile's largest (sums and O
+      // carry that factor, their quotient does not).  The sum's is 2^20 of it more, so that neither is flushed where
+      // it counts for vs from 2^-64 to 2^120: the largest terms of a sum are 2^(28 - log2 vs) = 2^-92 to 2^92.
 #pragma unroll
       for (int i = 0; i < R; ++i) s[i] = ex2(__fsub_rn(s[i], __shfl_sync(0xffffffffu, top, i)));
       {
+        const float w_unit = __uint_as_float((uint32_t)max(ve + 127 - 20, 0) << 23);
         uint32_t hi[R / 2], lo[R / 2], w[R / 2];
 #pragma unroll
-        for (int i = 0; i < R; i += 2) split2h(s[i], s[i + 1], hi[i / 2], lo[i / 2]);
+        for (int i = 0; i < R; i += 2) {
+          const float2 pw = mul2(make_float2(s[i], s[i + 1]), make_float2(w_unit, w_unit));
+          split2h(pw.x, pw.y, hi[i / 2], lo[i / 2]);
+        }
 #pragma unroll
         for (int i = 0; i < R / 4; ++i) {
           w[i] = hi[2 * i] | hi[2 * i + 1] << 16;
@@ -994,13 +1018,12 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         }
       }
       fence_proxy_async();
-      // row sums of p / vs over the warp: halves exchanged until a lane has one row, then added (one tree for every R)
-      const float iv = __uint_as_float((uint32_t)(127 - ve) << 23);
+      // row sums over the warp: halves exchanged until a lane has one row, then added (one tree for every R)
       {
         constexpr int N = R == 12 ? 16 : R;  // (a power of two)
         float v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = i < R ? __fmul_rn(s[i < R ? i : 0], iv) : 0.f;
+        for (int i = 0; i < N; ++i) v[i] = i < R ? s[i < R ? i : 0] : 0.f;
         int off = 16;
 #pragma unroll
         for (int n = N / 2; n; n >>= 1, off >>= 1) {
@@ -1042,7 +1065,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       if (lane < R) {
         const float* a = s_sum + ring * 4 * RP + R * grp + lane;
         mt = s_top[ring * RP + R * grp + lane];
-        lt = __fadd_rn(__fadd_rn(a[0], a[RP]), __fadd_rn(a[2 * RP], a[3 * RP]));
+        lt = __fmul_rn(__fadd_rn(__fadd_rn(a[0], a[RP]), __fadd_rn(a[2 * RP], a[3 * RP])), 0x1p-20f);  // in O's unit
       }
       if (fl & kGroupBegin) {
         m_run = -INFINITY;

@@ -85,3 +85,55 @@ def test_lengths_advanced_in_place(B, new_max):
             assert p.cu.tolist() == cu and p.slots.tolist() == slots and p.positions.tolist() == pos and p.head.tolist() == [h]
         assert t.tolist() == tw and lens.tolist() == c
     assert ops.device_status() == 0
+
+
+def _with_scales(step, exponents, zeros=()):
+    """The step with V scales 2^e for its blocks in order of position (codes small enough for bf16 outputs), and blocks
+    of zeros."""
+    step.v = step.v.float().clamp(-200, 200).to(torch.float8_e4m3fn)
+    for b, n in enumerate(step.lens):
+        for j in range(-(-n // step.block)):
+            i = int(step.table[b, j])
+            step.vs[i] = 2.0 ** exponents[j % len(exponents)]
+            if j in zeros:
+                step.v[i] = 0
+    return step
+
+
+@pytest.mark.parametrize("high", [40, 70, 71, 100, 120])
+@pytest.mark.parametrize("cached", [16, 130, 1030, 5000])
+def test_value_scales_far_apart_keep_their_weight_in_the_sum(high, cached):
+    """A block of zeros (scale 2^-64) beside scales up to 2^120, in one tile, in two, in two groups and in many: equal
+    scores weigh the same whatever their V scales."""
+    step = Step(4, 2, 128, 16, [cached], [1], seed=high)
+    n = -(-step.lens[0] // 16)
+    _with_scales(step, [-64] * (n - 1) + [high], zeros=range(n - 1))
+    step.q[0, 0] = 0  # equal weights
+    out = step.run()
+    ref, bound = step.reference()
+    assert_close(out, ref, bound, f"{high} {cached}")
+    i = int(step.table[0, n - 1])
+    m = step.lens[0] - 16 * (n - 1)
+    want = step.v[i, 0, :m].double().sum(0) * 2.0 ** high / step.lens[0]
+    assert bool(((out[0, 0].double().cpu() - want).abs() <= 2.0 ** -7 * step.v[i, 0, :m].double().abs().sum(0) * 2.0 ** high / step.lens[0]).all())
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,dim,block", [(8, 2, 128, 16), (8, 2, 256, 64), (28, 4, 64, 32)])
+@pytest.mark.parametrize("exponents", [(-64, 120), (120, -64, 0, 37, -30), (-64, 3, 71), (0, -60, 60, 100)])
+def test_value_scales_over_the_whole_range(hq, hkv, dim, block, exponents):
+    """Scales from 2^-64 to 2^120 in any order, peaked and flat rows; and a verify row is the one-token step."""
+    cached, M = [5, 300, 2600, 1020], 3
+    step = _with_scales(Step(hq, hkv, dim, block, cached, [M] * 4, seed=block), exponents)
+    cache = step.cache()
+    for scale in (0.002, None, 1.0):
+        out = step.run(cache=cache, scale=scale)
+        ref, bound = step.reference(scale=scale)
+        assert_close(out, ref, bound, f"{scale}")
+        table = torch.from_numpy(step.table).cuda()
+        cu = torch.arange(5, dtype=torch.int32).cuda()
+        for m in range(M):
+            lens = torch.tensor([c + m + 1 for c in cached], dtype=torch.int32).cuda()
+            one = ops.kv_attention(step.q.view(4, M, hq, dim)[:, m].contiguous().cuda(), cache, table, cu, lens, 1,
+                                   max(step.lens), scale=scale)
+            assert torch.equal(one, out.view(4, M, hq, dim)[:, m]), (scale, m)
