@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     const int lo = p.window > 0 ? max(0, r.base + rt * p.TQ - p.window + 1) : 0;
     const int hi = r.base + min((rt + 1) * p.TQ, r.fresh) - 1;
     const int j = tile * nb + lane;
-    if (lane >= nb || (j + 1) * block <= lo || j * block > hi) return -2;
+    if (lane >= nb || j * block + (block - 1) < lo || j * block > hi) return -2;  // (below 2^31 in every tile)
     return j < p.max_blocks ? p.table[(int64_t)b * p.max_blocks + j] : -1;
   };
   if (warp == W_LOAD) {

@@ -137,3 +137,28 @@ def test_value_scales_over_the_whole_range(hq, hkv, dim, block, exponents):
             one = ops.kv_attention(step.q.view(4, M, hq, dim)[:, m].contiguous().cuda(), cache, table, cu, lens, 1,
                                    max(step.lens), scale=scale)
             assert torch.equal(one, out.view(4, M, hq, dim)[:, m]), (scale, m)
+
+
+@pytest.mark.parametrize("block", [64, 128])
+@pytest.mark.parametrize("new,window", [(1, 200), (3, 1), (5, 130), (2, 1500)])
+def test_the_longest_request(block, new, window):
+    """The last tokens of a request of 2^31 - 1, seen through a window (its table repeats a few blocks)."""
+    hq, hkv, dim, few = 4, 2, 64, 7
+    step = Step(hq, hkv, dim, block, [few * block - 1], [1], seed=block + new)  # a cache of seven full blocks
+    ids = [int(i) for i in step.table[0, :few]]
+    width = (TOP + block) // block
+    table = torch.tensor(ids, dtype=torch.int32, device="cuda").repeat(-(-width // few))[:width].view(1, -1)
+    q = torch.randn(new, hq, dim, generator=torch.Generator().manual_seed(new)).to(torch.bfloat16)
+    cu, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, new], [TOP]))
+    out = ops.kv_attention(q.cuda(), step.cache(), table, cu, lens, new, TOP, window=window)
+    assert ops.device_status() == 0
+    for m in range(new):
+        see = range(TOP - new + m - window + 1, TOP - new + m + 1)
+        at = [(ids[p // block % few], p % block) for p in see]
+        for h in range(hkv):
+            k, v = (torch.stack([c[i, h, o].double() * s[i, h].double() for i, o in at]) for c, s in
+                    ((step.k, step.ks), (step.v, step.vs)))
+            w = torch.softmax(q[m, 2 * h:2 * h + 2].double() @ k.T / dim ** 0.5, 1)
+            # as in the reference of these tests: the output's and the weights' rounding (the rest is below a hundredth)
+            bound = 1.02 * 2.0 ** -8 * ((w @ v).abs() + w @ v.abs()) + 2.0 ** -20 * (w @ v.abs()).amax()
+            assert bool(((out[m, 2 * h:2 * h + 2].double().cpu() - w @ v).abs() <= bound).all()), (m, h)
