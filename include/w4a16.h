@@ -350,7 +350,7 @@ typedef struct {
  * b: positions[t] = cached[b] + t - cu[b], slots[t] its slot (int32 [T]); for
  * cu[B] <= t < T (a padded batch) both are -1.
  * Out-of-range inputs raise W4A16_DEVICE_KV_RANGE and never lead outside the
- * arrays: negative lengths count as 0, tokens past T are dropped from the
+ * arrays: negative lengths and a negative *head count as 0, tokens past T are dropped from the
  * step (cu is cut at T), and a token whose block is missing (the free list
  * has run out, the request is longer than max_blocks * block, or its table
  * entry is negative) gets slot -1.  A missing block's entry is -1.

@@ -56,10 +56,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
   const int t0 = blockIdx.x * kPlanTokens, t1 = min(t0 + kPlanTokens, a.T);
   pdl_launch_dependents();
   pdl_wait();
-  const int head = a.head ? max(*a.head, 0) : 0;
+  const int start = a.head ? *a.head : 0, head = max(start, 0);
   int tok = 0;  // tokens and blocks of the requests before this chunk; both stay within T
   int taken = 0;
-  bool bad = false;
+  bool bad = start < 0;
   for (int b0 = 0; b0 < a.B; b0 += n_thr) {
     const int b = b0 + tid, n = min(n_thr, a.B - b0);
     int cached = 0, fresh = 0;

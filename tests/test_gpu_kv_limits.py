@@ -162,3 +162,13 @@ def test_the_longest_request(block, new, window):
             # as in the reference of these tests: the output's and the weights' rounding (the rest is below a hundredth)
             bound = 1.02 * 2.0 ** -8 * ((w @ v).abs() + w @ v.abs()) + 2.0 ** -20 * (w @ v.abs()).amax()
             assert bool(((out[m, 2 * h:2 * h + 2].double().cpu() - w @ v).abs() <= bound).all()), (m, h)
+
+
+def test_a_negative_head_counts_as_zero_and_is_flagged():
+    cached, new, table, free = [16, 0], [3, 20], [[5, -1], [-1, -1]], [7, 8, 9, 10]
+    t, f = (torch.tensor(x, dtype=torch.int32).cuda() for x in (table, free))
+    p = ops.kv_plan(*(torch.tensor(x, dtype=torch.int32).cuda() for x in (cached, new)), t, f, 23, 16,
+                    head=torch.tensor([-3], dtype=torch.int32).cuda())
+    assert ops.device_status() == ops.DEVICE_KV_RANGE
+    want = ref_plan(cached, new, table, free, 0, 23, 16)
+    assert (t.tolist(), p.cu.tolist(), p.lens.tolist(), p.slots.tolist(), p.positions.tolist(), int(p.head)) == want
