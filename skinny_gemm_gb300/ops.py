@@ -153,13 +153,6 @@ def _stream_ptr(stream) -> int:
     return int(s.cuda_stream)
 
 
-def _raw_stream(stream) -> int:
-    """_stream_ptr without a Stream object for the common case (the current stream)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
-
-
 def _dev_tensor(t: torch.Tensor, dtype: torch.dtype, name: str) -> torch.Tensor:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -611,6 +604,7 @@ class KVCache:
                           self.blocks, self.heads, self.block, self.dim)
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ptr", ctypes.addressof(c))
+        object.__setattr__(self, "_dev", self.k.get_device())
 
     @classmethod
     def empty(cls, blocks: int, heads: int, block: int, dim: int, device="cuda") -> "KVCache":
@@ -641,13 +635,31 @@ class KVPlan:
         return cls(*torch.unsafe_split_with_sizes(flat, (B + 1, B, T, T, 1)))  # (whole numbers: nothing to differentiate)
 
 
-def _i32(t: torch.Tensor, name: str, n: int | None = None) -> int:
-    """The address of a contiguous int32 CUDA tensor of n elements (None: any)."""
+def _on_device(t: torch.Tensor, name: str, dev: int) -> None:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors of the call on cuda:{dev}")
+
+
+def _i32(t: torch.Tensor, name: str, n: int | None = None, dev: int | None = None) -> int:
+    """The address of a contiguous int32 CUDA tensor of n elements on device dev (None: any)."""
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda and t.is_contiguous()):
         _dev_tensor(t, torch.int32, name)
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} must have {n} elements (got {t.numel()})")
+    if dev is not None and t.get_device() != dev:
+        _on_device(t, name, dev)
     return t.data_ptr()
+
+
+def _stream_on(stream, dev: int) -> int:
+    """The stream of a call whose tensors are on device dev: the current device's, or one given."""
+    if stream is None:
+        if torch._C._cuda_getDevice() != dev:
+            raise ValueError(f"the call's tensors are on cuda:{dev}, which is not the current device")
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev or torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"the call's tensors are on cuda:{dev}; the stream, or the current device, is another's")
+    return stream.cuda_stream
 
 
 def _kv_rows(t: torch.Tensor, name: str, heads: int, dim: int) -> int:
@@ -679,6 +691,7 @@ def kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: 
     if table.dim() != 2:
         raise ValueError("table must be [B, max_blocks]")
     B, max_blocks = table.shape
+    dev = table.get_device()
     if out is None:
         if T < 0:
             raise ValueError("T must not be negative")
@@ -688,11 +701,11 @@ def kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: 
         slots = lens + 4 * B
         outs = (cu, lens, slots, slots + 4 * T, slots + 8 * T)
     else:
-        outs = (_i32(out.cu, "cu", B + 1), _i32(out.lens, "lens", B), _i32(out.slots, "slots", T),
-                _i32(out.positions, "positions", T), _i32(out.head, "head_out", 1))
-    rc = lib().w4a16_kv_plan(_i32(cached, "cached", B), _i32(new, "new", B), tp, _i32(free, "free"),
-                             None if head is None else _i32(head, "head", 1), *outs, B, T, block, max_blocks,
-                             free.numel(), _raw_stream(stream))
+        outs = (_i32(out.cu, "cu", B + 1, dev), _i32(out.lens, "lens", B, dev), _i32(out.slots, "slots", T, dev),
+                _i32(out.positions, "positions", T, dev), _i32(out.head, "head_out", 1, dev))
+    rc = lib().w4a16_kv_plan(_i32(cached, "cached", B, dev), _i32(new, "new", B, dev), tp, _i32(free, "free", None, dev),
+                             None if head is None else _i32(head, "head", 1, dev), *outs, B, T, block, max_blocks,
+                             free.numel(), _stream_on(stream, dev))
     if rc:
         _raise(rc)
     return out
@@ -705,8 +718,11 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Ten
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError("k and v must have the same number of tokens")
-    rc = lib().w4a16_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _i32(slots, "slots", T), cache._ptr, T,
-                               _raw_stream(stream))
+    dev = cache._dev
+    _on_device(k, "k", dev)
+    _on_device(v, "v", dev)
+    rc = lib().w4a16_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _i32(slots, "slots", T, dev), cache._ptr, T,
+                               _stream_on(stream, dev))
     if rc:
         _raise(rc)
 
@@ -798,20 +814,25 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
     if table.dim() != 2:
         raise ValueError("table must be [B, max_blocks]")
     B, max_blocks = table.shape
-    dev = q.device
+    dev, di = q.device, cache._dev
+    _on_device(q, "q", di)
+    _on_device(table, "table", di)
+    cup, lp = _i32(cu, "cu", B + 1, di), _i32(lens, "lens", B, di)
+    raw = _stream_on(stream, di)
     if out is None:
         out = torch.empty((T, hq, dim), dtype=torch.bfloat16, device=dev)
     else:
         _dev_tensor(out, torch.bfloat16, "out")
+        _on_device(out, "out", di)
         if out.shape != q.shape:
             raise ValueError(f"out must be {tuple(q.shape)}")
-    raw = _raw_stream(stream)
     if workspace is None:
         wn = _kv_attention_bytes(B, T, hq, cache.heads, dim, max_new, max_len, window)
         workspace, wp, _ = _kv_workspace(wn, raw, dev, stream) if wn else (None, None, 0)
     else:
         wp, wn = _ws_args(workspace)
-    rc = lib().w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, tp, _i32(cu, "cu", B + 1), _i32(lens, "lens", B),
+        _on_device(workspace, "workspace", di)
+    rc = lib().w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, tp, cup, lp,
                                   out.data_ptr(), B, T, hq, max_blocks, max_new, max_len, window,
                                   1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, _kv_counters(raw, dev), raw)
     if rc:
