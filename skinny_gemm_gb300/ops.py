@@ -464,8 +464,7 @@ def device_status(stream=None) -> int:
     if rc not in (OK, ERR_DEVICE):
         _raise(rc)
     if flags.value & DEVICE_TIMEOUT and (_kv_counter_cache or _kv_capture_sets):
-        torch.cuda.synchronize()
-        _kv_reset_counters()
+        _kv_reset_counters(torch.cuda.current_device())
     return flags.value
 
 
@@ -756,11 +755,13 @@ def _kv_counters(raw_stream: int, device: torch.device) -> int:
     return c[1]
 
 
-def _kv_reset_counters() -> None:
-    """After a wait ran out: a call may have left counters behind (the GPU is idle)."""
-    for t in [c[0] for c in _kv_counter_cache.values()] + [s[0] for s in _kv_capture_sets.values()]:
+def _kv_reset_counters(dev: int) -> None:
+    """After a wait ran out on device dev, the current one: a call there may have left counters behind.  Other
+    devices' calls may be running; their counters are as they should be."""
+    torch.cuda.synchronize()
+    for t in [c[0] for key, c in _kv_counter_cache.items() if key[0] == dev] + [s[0] for i, s in _kv_capture_sets.items() if i == dev]:
         t.zero_()
-        torch.cuda.current_stream(t.device).synchronize()
+    torch.cuda.synchronize()
 
 
 KV_WORKSPACE_KEPT = 64 << 20  # larger workspaces are not kept between calls

@@ -95,3 +95,26 @@ def test_one_device(current, call, names):
     with pytest.raises(ValueError, match="cuda:1"):
         call(at=1, stream=Stream(1))  # (the library launches on the current device)
     assert Lib.calls == 2
+
+
+def test_counters_of_the_device_whose_wait_ran_out(current, monkeypatch):
+    """Only they are zeroed, and only when that device is idle: another device's calls may be running."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: type("S", (), {"cuda_stream": 3, "synchronize": lambda self: None})())
+    idle = []
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: idle.append(0))
+    counters = {(d, s): (torch.full((4,), 9), 0) for d in (0, 1) for s in (5, 6)}
+    sets = {d: [torch.full((8,), 9), 2] for d in (0, 1)}
+    monkeypatch.setattr(ops, "_kv_counter_cache", counters)
+    monkeypatch.setattr(ops, "_kv_capture_sets", sets)
+
+    class Out(Lib):
+        def w4a16_device_status(self, stream, flags):
+            flags._obj.value = ops.DEVICE_TIMEOUT
+            return ops.ERR_DEVICE
+
+    monkeypatch.setattr(ops, "lib", lambda: Out())
+    assert ops.device_status() == ops.DEVICE_TIMEOUT and idle
+    for d in (0, 1):
+        for t in [c[0] for k, c in counters.items() if k[0] == d] + [sets[d][0]]:
+            assert bool((t == 9 * d).all()), d
