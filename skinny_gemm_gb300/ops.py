@@ -14,6 +14,7 @@ projections: ``kv_plan``, ``kv_append`` and ``kv_attention`` over a ``KVCache``
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -731,19 +732,21 @@ _kv_counter_cache: dict = {}
 _kv_capture_sets: dict = {}
 
 
-def _kv_counters(raw_stream: int, device: torch.device) -> int:
-    """Zeroed counters: a stream's, kept here as its workspace is; for a captured
-    call, whose graph may be replayed beside that stream, a set of its own.  Those
-    are made with the device's first call outside capture and handed out once;
-    without one left, the graph zeroes a set from its own memory."""
+def _kv_counters(raw_stream: int, device: torch.device):
+    """(tensor, address) of zeroed counters of a call on the current stream: the stream's, kept here as
+    its workspace is; for a captured call, whose graph may be replayed beside that
+    stream, a set of its own.  Those are made with the device's first call outside
+    capture and handed out once; without one left, the graph zeroes a set from its
+    own memory."""
     key = (device.index, raw_stream)
     if _capturing():
         with _ws_lock:
             sets = _kv_capture_sets.get(device.index)
             if sets is not None and sets[1] < KV_CAPTURE_SETS:
                 sets[1] += 1
-                return sets[0].data_ptr() + 4 * KV_COUNTERS * (sets[1] - 1)
-        return torch.zeros(KV_COUNTERS, dtype=torch.int32, device=device).data_ptr()
+                return sets[0], sets[0].data_ptr() + 4 * KV_COUNTERS * (sets[1] - 1)
+        t = torch.zeros(KV_COUNTERS, dtype=torch.int32, device=device)
+        return t, t.data_ptr()
     c = _kv_counter_cache.get(key)
     if c is None:
         zeros = torch.zeros(KV_COUNTERS, dtype=torch.int32, device=device)
@@ -752,7 +755,7 @@ def _kv_counters(raw_stream: int, device: torch.device) -> int:
                 _kv_capture_sets[device.index] = [torch.zeros(KV_CAPTURE_SETS * KV_COUNTERS, dtype=torch.int32, device=device), 0]
             torch.cuda.current_stream(device).synchronize()
             c = _kv_counter_cache.setdefault(key, (zeros, zeros.data_ptr()))
-    return c[1]
+    return c
 
 
 def _kv_reset_counters(dev: int) -> None:
@@ -768,19 +771,16 @@ KV_WORKSPACE_KEPT = 64 << 20  # larger workspaces are not kept between calls
 _kv_ws_cache: dict = {}
 
 
-def _kv_workspace(n: int, raw_stream: int, device: torch.device, stream):
-    """(tensor, address) of n bytes for a call on a stream: the stream's own,
-    kept here and grown when a call needs more, or (large, or under graph
-    capture) one for this call.  It needs no initial contents."""
+def _kv_workspace(n: int, raw_stream: int, device: torch.device):
+    """(tensor, address) of n bytes for a call on the current stream: the stream's
+    own, kept here and grown when a call needs more, or (large, or under graph
+    capture) one for this call, whose memory comes back in the stream's order.  It
+    needs no initial contents."""
     key = (device.index, raw_stream)
     kept = _kv_ws_cache.get(key)
     if kept is not None and kept[2] >= n and not _capturing():
         return kept
-    if stream is None:
-        t = torch.empty(n, dtype=torch.uint8, device=device)
-    else:  # memory of that stream: freed blocks come back in its order
-        with torch.cuda.stream(stream):
-            t = torch.empty(n, dtype=torch.uint8, device=device)
+    t = torch.empty(n, dtype=torch.uint8, device=device)
     kept = (t, t.data_ptr(), n)
     if n <= KV_WORKSPACE_KEPT and not _capturing():
         _kv_ws_cache[key] = kept
@@ -827,15 +827,18 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
         _on_device(out, "out", di)
         if out.shape != q.shape:
             raise ValueError(f"out must be {tuple(q.shape)}")
-    if workspace is None:
-        wn = _kv_attention_bytes(B, T, hq, cache.heads, dim, max_new, max_len, window)
-        workspace, wp, _ = _kv_workspace(wn, raw, dev, stream) if wn else (None, None, 0)
-    else:
-        wp, wn = _ws_args(workspace)
+    wn = _kv_attention_bytes(B, T, hq, cache.heads, dim, max_new, max_len, window) if workspace is None else 0
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # the call's stream is the current one
+        counters, cp = _kv_counters(raw, dev)  # (both tensors are held until the launch: neither may get the other's memory)
+        if wn:
+            workspace, wp, _ = _kv_workspace(wn, raw, dev)
+        else:
+            wp, wn = _ws_args(workspace)
+    if workspace is not None:
         _on_device(workspace, "workspace", di)
     rc = lib().w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, tp, cup, lp,
                                   out.data_ptr(), B, T, hq, max_blocks, max_new, max_len, window,
-                                  1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, _kv_counters(raw, dev), raw)
+                                  1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, cp, raw)
     if rc:
         _raise(rc)
     return out

@@ -1,4 +1,6 @@
 """The paged cache's calls take tensors of one device, the current one (stand-ins for CUDA tensors; no GPU)."""
+import contextlib
+
 import pytest
 import torch
 
@@ -45,7 +47,8 @@ def current(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 5, raising=False)
     monkeypatch.setattr(ops, "lib", lambda: Lib())
-    monkeypatch.setattr(ops, "_kv_counters", lambda raw, device: 0)
+    monkeypatch.setattr(ops, "_kv_counters", lambda raw, device: (None, 0))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     Lib.calls = 0
 
 
