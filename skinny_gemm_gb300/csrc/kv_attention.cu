@@ -1270,7 +1270,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     // (rare) padding rows and rows of requests that were left out: zeros
     for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
       bool bad_req = false;
-      const Req rq = load_req(p, find_request(p.cu, p.B, t), &bad_req);
+      const Req rq = load_req(p, find_request(p.cu, p.B, p.t0 + t), &bad_req);
       if (s_rest[1] > 0 && t >= rq.c0 && t < rq.c0 + rq.fresh) continue;  // (no tiles: a refused step)
       for (int i = tid; i < p.q_heads * (D / 8); i += NT)
         *reinterpret_cast<uint4*>(p.out + (int64_t)t * p.q_heads * D + 8 * i) = make_uint4(0, 0, 0, 0);
@@ -1307,10 +1307,10 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
     State out;
     bool mine;
     for (bool again = true; again;) {
-      int b = min(t / p.max_new, p.B - 1);  // right where every request has max_new new tokens
+      int b = min((p.t0 + t) / p.max_new, p.B - 1);  // right where every request has max_new new tokens
       RawReq raw(p, b);
-      if (raw.c0 > t || raw.c1 <= t) {
-        b = find_request(p.cu, p.B, t);
+      if (raw.c0 > p.t0 + t || raw.c1 <= p.t0 + t) {
+        b = find_request(p.cu, p.B, p.t0 + t);
         raw = RawReq(p, b);
       }
       bool bad = false;
@@ -1366,7 +1366,13 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
 
 // ---- host side -----------------------------------------------------------------------------------
 
+// A row has a slot for every group of the longest request, 4 dim + 8 bytes a query head.  So that the workspace stays
+// bounded, a call whose rows need more takes them in several launches, a row tile's at least (8192 rows of 32 x 128
+// over 131,072 tokens would take 17 GB; a launch that fills this is a millisecond of work).
+constexpr int64_t kGroupBytes = (int64_t)1 << 30;
+
 struct Layout {
+  int rows;  // of a launch
   int RP, TQ, gmax, grid, t_slots, seg_cost;
   bool fits;  // positions on the line and rows of group results fit in 31 bits
   size_t g_acc, g_ml, t_acc, t_ml, refused, bytes;
@@ -1397,22 +1403,31 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   Layout y;
   const int G = q_heads / heads;
   if (max_new > T) max_new = T;
-  const int64_t rows = (int64_t)G * max_new;
-  // the smallest row tile that holds the step's rows of a key head, or 32 rows, and at least one token
-  const int64_t hold = rows < 32 ? rows : 32;
-  y.RP = hold <= 4 ? 4 : hold <= 8 ? 8 : hold <= 12 ? 12 : hold <= 16 ? 16 : hold <= 24 ? 24 : 32;
-  y.TQ = y.RP / G;
   int64_t groups = ((int64_t)max_len + kGroupTokens - 1) / kGroupTokens;
   if (window > 0) {
     const int64_t span = ((int64_t)window + max_new - 2) / kGroupTokens + 2;
     if (span < groups) groups = span;
   }
   y.gmax = (int)groups;
+  const int all = T;
+  const int64_t row_bytes = groups > 1 ? groups * q_heads * ((int64_t)dim * 4 + 8) : 0;  // (one group: written out at once)
+  if (row_bytes * T > kGroupBytes) {
+    int64_t most = kGroupBytes / row_bytes;
+    if (most < 32 / G) most = 32 / G;
+    const int64_t launches = (T + most - 1) / most;
+    T = (int)((T + launches - 1) / launches);
+    if (max_new > T) max_new = T;
+  }
+  y.rows = T;
+  // the smallest row tile that holds the step's rows of a key head, or 32 rows, and at least one token
+  const int64_t hold = (int64_t)G * max_new < 32 ? (int64_t)G * max_new : 32;
+  y.RP = hold <= 4 ? 4 : hold <= 8 ? 8 : hold <= 12 ? 12 : hold <= 16 ? 16 : hold <= 24 ? 24 : 32;
+  y.TQ = y.RP / G;
   y.seg_cost = seg_cost(y.RP);
   // no more CTAs than tiles
   const int64_t per = ((int64_t)max_len + kTile - 1) / kTile;
   const int64_t row_tiles = most_row_tiles(B, T, y.TQ, max_new);
-  y.fits = (double)row_tiles * heads * (double)(per + y.seg_cost) <= INT32_MAX && (double)y.gmax * T * q_heads <= INT32_MAX;
+  y.fits = (double)row_tiles * heads * (double)(per + y.seg_cost) <= INT32_MAX && (double)y.gmax * all * q_heads <= INT32_MAX;
   if (!y.fits) return y;
   const int64_t most = row_tiles * heads * (per + y.seg_cost);
   const int full = kSms * ctas_per_sm(dim, y.RP);
@@ -1421,8 +1436,9 @@ Layout make_layout(int B, int T, int q_heads, int heads, int dim, int max_new, i
   y.t_slots = (int)(range < kGroupTiles ? range : kGroupTiles);  // a range's first seven tiles at most, and its end
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   y.g_acc = 0;
-  y.g_ml = y.g_acc + up((size_t)y.gmax * T * q_heads * dim * 4);
-  y.t_acc = y.g_ml + up((size_t)y.gmax * T * q_heads * 8);
+  const size_t group_rows = y.gmax > 1 ? (size_t)y.gmax * T * q_heads : 0;
+  y.g_ml = y.g_acc + up(group_rows * dim * 4);
+  y.t_acc = y.g_ml + up(group_rows * 8);
   y.t_ml = y.t_acc + up((size_t)y.grid * y.t_slots * y.RP * dim * 4);
   y.refused = y.t_ml + up((size_t)y.grid * y.t_slots * y.RP * 8);
   y.bytes = y.refused + up(4);
@@ -1433,7 +1449,7 @@ std::mutex g_attr_mu;
 bool g_attr[64][3][33] = {};
 
 template <int D, int RP>
-cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int pdl, cudaStream_t s) {
+cudaError_t run(const KvAttentionArgs& a, const Layout& y, Params p, int pdl, cudaStream_t s) {
   using X = Geo<D, RP>;
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
@@ -1460,24 +1476,33 @@ cudaError_t run(const KvAttentionArgs& a, const Layout& y, const Params& p, int 
   cfg.attrs = attr;
   cfg.numAttrs = pdl > 0 ? 1 : 0;
   cfg.stream = s;
-  cfg.gridDim = dim3((unsigned)y.grid);
-  cfg.blockDim = dim3(X::kThreads);
-  cfg.dynamicSmemBytes = (size_t)X::kSmem;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, RP>, maps, p)) return e;
-  if (y.gmax == 1) return cudaSuccess;
-  const int64_t out_rows = (int64_t)a.T * a.q_heads;
-  cfg.dynamicSmemBytes = 0;
-  if (y.gmax > 16 && out_rows * (D / 32) <= 2 * kSms) {
-    cfg.gridDim = dim3((unsigned)out_rows, D / 32);
-    cfg.blockDim = dim3(1024);
-    return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 128>, p);
+  for (p.t0 = 0; p.t0 < a.T; p.t0 += y.rows) {
+    p.T = a.T - p.t0 < y.rows ? a.T - p.t0 : y.rows;
+    p.q = a.q + p.t0 * a.q_stride;
+    p.out = a.out + (int64_t)p.t0 * a.q_heads * D;
+    cfg.gridDim = dim3((unsigned)y.grid);
+    cfg.blockDim = dim3(X::kThreads);
+    cfg.dynamicSmemBytes = (size_t)X::kSmem;
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, RP>, maps, p)) return e;
+    if (y.gmax == 1) continue;
+    const int64_t out_rows = (int64_t)p.T * a.q_heads;
+    cfg.dynamicSmemBytes = 0;
+    cudaError_t e;
+    if (y.gmax > 16 && out_rows * (D / 32) <= 2 * kSms) {
+      cfg.gridDim = dim3((unsigned)out_rows, D / 32);
+      cfg.blockDim = dim3(1024);
+      e = cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 128>, p);
+    } else {
+      const int per4 = 256 / (D / 4) / 4;
+      const int sets = y.gmax <= 8 && out_rows > 12 * kSms * per4 ? 1 : 4, per = 4 / sets * per4;  // (1: more than two rounds of 4)
+      const int64_t ctas = (out_rows + per - 1) / per;
+      cfg.gridDim = dim3((unsigned)(ctas < 6 * kSms ? ctas : 6 * kSms));
+      cfg.blockDim = dim3(256);
+      e = sets == 1 ? cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 1>, p) : cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 4>, p);
+    }
+    if (e) return e;
   }
-  const int per4 = 256 / (D / 4) / 4;
-  const int sets = y.gmax <= 8 && out_rows > 12 * kSms * per4 ? 1 : 4, per = 4 / sets * per4;  // (1: more than two rounds of 4)
-  const int64_t ctas = (out_rows + per - 1) / per;
-  cfg.gridDim = dim3((unsigned)(ctas < 6 * kSms ? ctas : 6 * kSms));
-  cfg.blockDim = dim3(256);
-  return sets == 1 ? cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 1>, p) : cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, 4>, p);
+  return cudaSuccess;
 }
 
 template <int D>
@@ -1503,16 +1528,14 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t 
   const Layout y = make_layout(a.B, a.T, a.q_heads, a.cache.heads, a.cache.dim, a.max_new, a.max_len, a.window);
   uint8_t* w = static_cast<uint8_t*>(a.ws);
   Params p;
-  p.q = a.q;
   p.q_stride = a.q_stride;
   p.k_scale = a.cache.k_scale;
   p.v_scale = a.cache.v_scale;
   p.table = a.table;
   p.cu = a.cu;
   p.lens = a.lens;
-  p.out = a.out;
   p.B = a.B;
-  p.T = a.T;
+  p.all = a.T;
   p.q_heads = a.q_heads;
   p.heads = a.cache.heads;
   p.G = a.q_heads / a.cache.heads;

@@ -28,13 +28,17 @@ constexpr int kTile = 128;  // tokens per tile (the M of the MMAs)
 struct Line {
   const int32_t* cu;
   const int32_t* lens;
-  int B, T, TQ;  // TQ tokens per row tile
+  int B, TQ;   // TQ tokens per row tile
+  int all;     // rows of the call
+  int t0, T;   // this launch's rows: the first, and how many
   int max_new, max_len, window;
 };
 
-// One request of the step: its row tiles and their ranges of 128-token tiles.
+// A request's part of the launch: its row tiles and their ranges of 128-token
+// tiles.  (Rows of a request do not depend on one another, so a part is a request
+// with fewer new tokens.)
 struct Req {
-  int c0, fresh, base;  // first row, new tokens (0: nothing to do), tokens before them
+  int c0, fresh, base;  // first row from t0 on, new tokens (0: nothing to do), tokens before them
 };
 
 struct RawReq {
@@ -47,14 +51,13 @@ struct RawReq {
 KV_LINE Req check_req(const Line& p, const RawReq& w, bool* bad) {
   Req r{0, 0, 0};
   const int c0 = w.c0, c1 = w.c1, len = w.len;
-  const bool ok = c0 >= 0 && c0 <= c1 && c1 <= p.T && c1 - c0 <= p.max_new && c1 - c0 <= len && len <= p.max_len;
+  const bool ok = c0 >= 0 && c0 <= c1 && c1 <= p.all && c1 - c0 <= p.max_new && c1 - c0 <= len && len <= p.max_len;
   if (!ok) {
     if (c1 != c0) *bad = true;
     return r;
   }
-  r.c0 = c0;
-  r.fresh = c1 - c0;
-  r.base = len - r.fresh;
+  const int a = max(c0, p.t0), e = min(c1, p.t0 + p.T);
+  if (a < e) r = Req{a - p.t0, e - a, len - (c1 - a)};
   return r;
 }
 

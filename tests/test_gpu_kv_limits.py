@@ -172,3 +172,36 @@ def test_a_negative_head_counts_as_zero_and_is_flagged():
     assert ops.device_status() == ops.DEVICE_KV_RANGE
     want = ref_plan(cached, new, table, free, 0, 23, 16)
     assert (t.tolist(), p.cu.tolist(), p.lens.tolist(), p.slots.tolist(), p.positions.tolist(), int(p.head)) == want
+
+
+@pytest.mark.parametrize("hq,hkv,dim,loose", [(32, 8, 64, 1 << 23), (64, 2, 256, 1 << 20), (12, 4, 128, 1 << 24)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_rows_in_several_launches(hq, hkv, dim, loose, window):
+    """A bound on the lengths that makes partial results outgrow one launch: the same bits as with a tight one, in ragged
+    steps whose requests lie across launches, with padding rows and with requests that are left out."""
+    block = 128
+    cached, new = [0, 700, 3000, 5, 64, 1100, 0, 2500], [30, 1, 7, 0, 3, 40, 1, 9]
+    step = Step(hq, hkv, dim, block, cached, new, seed=hq)
+    cache, T = step.cache(), step.T + 3
+    table, cu, lens = step.dev()
+    wide = torch.full((len(new), loose // block), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = torch.cat([step.q, torch.ones(3, hq, dim, dtype=torch.bfloat16)]).cuda()
+    want = ops.kv_attention(q, cache, table, cu, lens, max(new), max(step.lens), window=window)
+    one = ops.kv_attention_workspace_bytes(len(new), 1, hq, cache, max(new), loose, window)
+    n = ops.kv_attention_workspace_bytes(len(new), T, hq, cache, max(new), loose, window)
+    assert n < 1.2 * (1 << 30) and (window > 0 or T * one > 2 * n)  # (several launches)
+    out = torch.full_like(q, 7.0)
+    assert torch.equal(ops.kv_attention(q, cache, wide, cu, lens, max(new), loose, window=window, out=out), want)
+    assert bool((want[step.T:] == 0).all()) and ops.device_status() == 0
+    ref, bound = step.reference(window=window)
+    assert_close(out[:step.T], ref, bound)
+    # the 30 and the 40 rows are too many, or the offsets step back
+    few = ops.kv_attention(q, cache, wide, cu, lens, 9, loose, window=window)
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[:30] = keep[41:81] = False
+    assert ops.device_status() == ops.DEVICE_KV_RANGE
+    assert torch.equal(few[keep], want[keep]) and bool((few[~keep] == 0).all())
+    cu[4] = 3
+    assert bool((ops.kv_attention(q, cache, wide, cu, lens, max(new), loose, window=window) == 0).all())
+    assert ops.device_status() == ops.DEVICE_KV_RANGE

@@ -18,7 +18,7 @@ extern "C" int tiles(int TQ, int window, int base, int fresh, int rt) {
 }
 // Row tiles of a step's accepted requests; -1: refused.
 extern "C" long long row_tiles_of(const int* cu, const int* lens, int B, int T, int TQ, int max_new, int max_len) {
-  Line p{cu, lens, B, T, TQ, max_new, max_len, 0};
+  Line p{cu, lens, B, TQ, T, 0, T, max_new, max_len, 0};
   long long n = 0;
   bool bad = false, back = false;
   for (int b = 0; b < B; ++b) {
@@ -26,6 +26,16 @@ extern "C" long long row_tiles_of(const int* cu, const int* lens, int B, int T, 
     n += row_tiles(p, load_req(p, b, &bad));
   }
   return back ? -1 : n;
+}
+// The rows t0 .. t0 + n - 1 of a step: each row's position, -1 where no request has it, -2 where two have it.
+extern "C" void positions(const int* cu, const int* lens, int B, int all, int t0, int n, int max_new, int max_len, int* pos) {
+  Line p{cu, lens, B, 1, all, t0, n, max_new, max_len, 0};
+  bool bad = false;
+  for (int t = 0; t < n; ++t) pos[t] = -1;
+  for (int b = 0; b < B; ++b) {
+    const Req r = load_req(p, b, &bad);
+    for (int j = 0; j < r.fresh; ++j) pos[r.c0 + j] = pos[r.c0 + j] == -1 ? r.base + j : -2;
+  }
 }
 extern "C" long long most(int B, int T, int TQ, int max_new) { return most_row_tiles(B, T, TQ, max_new); }
 """
@@ -98,3 +108,27 @@ def test_no_step_has_more_row_tiles_than_its_arrays_are_made_for(line):
         assert (n == -1) == bool(np.any(np.diff(cu) < 0))
     assert _row_tiles(line, [0, 1, 0, 1, 0, 1], [1024] * 5, 1, 4, 1, 1024) == -1
     assert _row_tiles(line, [0, 2] * 11, [384] * 21, 2, 8, 2, 384) == -1
+
+
+def test_a_launch_of_some_of_the_rows(line):
+    """Rows keep their positions however the call's rows are divided over launches."""
+    r = np.random.RandomState(2)
+    for _ in range(500):
+        B = int(r.randint(1, 12))
+        cu = np.concatenate([[0], np.cumsum(r.randint(0, 9, B))])
+        T = int(cu[-1] + r.randint(0, 4))
+        lens = np.diff(cu) + r.randint(-1, 200, B)
+        max_new, max_len = int(r.randint(1, 10)), 150
+        want = [-1] * T
+        for b in range(B):
+            n = int(cu[b + 1] - cu[b])
+            if n <= min(max_new, lens[b]) and lens[b] <= max_len:
+                want[cu[b]:cu[b + 1]] = range(lens[b] - n, lens[b])
+        per = int(r.randint(1, T + 2))
+        got, a, b = [], *((ctypes.c_int * len(x))(*(int(v) for v in x)) for x in (cu, lens))
+        for t0 in range(0, T, per):
+            n = min(per, T - t0)
+            pos = (ctypes.c_int * n)()
+            line.positions(a, b, B, T, t0, n, max_new, max_len, pos)
+            got += list(pos)
+        assert got == want
