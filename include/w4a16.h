@@ -480,7 +480,8 @@ const char* w4a16_last_error(void);
  * wait: in every persistent-grid launch of w4a16_mm one stage of one warp
  * expects 16 bytes more than its copies deliver, so that warp's bounded wait
  * gives up, raises W4A16_DEVICE_TIMEOUT and leaves its rows unwritten; every
- * copy still lands, so nothing is in flight when the kernel exits) and
+ * copy still lands, so nothing is in flight when the kernel exits; in every
+ * w4a16_kv_attention launch the first slot of keys of one CTA, likewise) and
  * W4A16_FORCE_KERNEL (simt | tc | vanilla).  They are read once, at the
  * first call, otherwise. */
 void w4a16_debug_reload_env(void);

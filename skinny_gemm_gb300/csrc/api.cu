@@ -678,7 +678,7 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
     return fail(W4A16_ERR_SHAPE, "a workspace of %zu bytes is too small (%zu)", workspace_bytes, need);
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
   KvAttentionArgs a{q, q_stride, *cache, table, cu, lens, out, B, T, q_heads, max_blocks, max_new, max_len, window,
-                    scale, workspace, counters, nullptr};
+                    scale, workspace, counters, nullptr, env().fault == kFaultWait};
   if (int rc = flag_pointer(&a.flags)) return rc;
   cudaError_t e = launch_kv_attention(a, env().pdl, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_kv_attention launch");

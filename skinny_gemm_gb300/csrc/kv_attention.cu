@@ -75,6 +75,7 @@ constexpr int kGroupTokens = kTile * kGroupTiles;
 constexpr int kDescs = 8;       // tile descriptors in flight
 constexpr int kRing = 4;        // row sums and weights' barriers: softmax may be two tiles ahead of the fold
 constexpr int kSms = 152;
+constexpr uint32_t kTries = 1u << 18;  // of a wait: about a second (a limit in the parameters: prompt chunks 200 -> 213 us)
 constexpr float kLog2e = 1.4426950408889634f;
 
 // flags of a tile descriptor
@@ -167,6 +168,7 @@ struct Params : Line {
   float* t_acc;  // [grid][t_slots][RP][D]
   float2* t_ml;  // [grid][t_slots][RP]
   int* refused;   // [1] the step's offsets step back (written by every call)
+  uint32_t fault_tx;  // see KvAttentionArgs::fault_wait
   int* counters;  // [grid] tiles done of divided groups, by the CTA of the first; zero between calls
   int* flags;
 };
@@ -407,6 +409,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   CutGroup* s_cut = reinterpret_cast<CutGroup*>(s_tmem + 12);          // [2] at the range's beginning, at its end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  auto wait = [](uint32_t bar, uint32_t parity) { return mbar_wait_warp(bar, parity, kTries); };
   auto give_up = [&]() {
     atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
     *s_abort = 1;
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   int b = 0, rt = 0, h = 0, tile = 0, t_first = 0, t_last = -1;
   int seg0 = 0;  // position of the segment's first tile
   int id = -2;
-  int loads = 0;  // slots requested
+  int loads = 0, staged = 0;  // slots requested, segments whose query rows were
   auto take = [&](int bl) {  // request b0 + bl becomes the current one
     b = b0 + bl;
     r.c0 = __shfl_sync(0xffffffffu, mine.c0, bl);
@@ -601,7 +604,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       const bool valid = id >= 0 && id < p.blocks;
       const unsigned need = __ballot_sync(0xffffffffu, id != -2), have = __ballot_sync(0xffffffffu, valid);
       if (need != have || tile * kTile + kTile - 1 > pos0 || (p.window > 0 && tile * kTile < pos1 - p.window + 1)) fl |= kFix;
-      if (t >= ND && !(ok = mbar_wait_warp(d_free(ds), ((t / ND) - 1) & 1))) break;
+      if (t >= ND && !(ok = wait(d_free(ds), ((t / ND) - 1) & 1))) break;
       Desc& de = descs[ds];
       if (lane == 0) {
         *reinterpret_cast<int4*>(&de.flags) = make_int4(fl, h, j0, tile);
@@ -661,10 +664,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   } else if (warp == W_LOAD) {
     // ---- copies ----
     bool ok = true;
-    int seg = 0, fl = 0;
+    int fl = 0;
+    uint32_t late = blockIdx.x == 0 ? p.fault_tx : 0;  // (debug: bytes that the first copies do not bring)
     for (int t = 0; ok && !(fl & kFinal); ++t) {
       const int ds = t % ND;
-      if (!(ok = mbar_wait_warp(d_full(ds), (t / ND) & 1))) break;
+      if (!(ok = wait(d_full(ds), (t / ND) & 1))) break;
       const Desc& de = descs[ds];
       const int4 dd = *reinterpret_cast<const int4*>(&de.flags), dx = *reinterpret_cast<const int4*>(&de.base);
       fl = dd.x;
@@ -679,27 +683,27 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int slot = loads % NS;
-        if (loads >= NS && !(ok = mbar_wait_warp(empty(slot), ((loads / NS) - 1) & 1))) break;
-        if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(copies * block * X::kRowB));
+        if (loads >= NS && !(ok = wait(empty(slot), ((loads / NS) - 1) & 1))) break;
+        if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(copies * block * X::kRowB) + late);
+        late = 0;
         __syncwarp();
         if (my_id >= 0)
           tma_load_2d(slots + slot * X::kSlot + panel * X::kPanelBytes + blk * block * X::kRowB, kv ? &maps.v : &maps.k,
                       panel * 128, row, full(slot));
         ++loads;
         if (X::kStage > 0 && kv == 0 && (fl & kNewSeg)) {  // the segment's query rows, a copy per token
-          if (seg > 0 && !(ok = mbar_wait_warp(st_free, (seg - 1) & 1))) break;
+          if (staged > 0 && !(ok = wait(st_free, (staged - 1) & 1))) break;
           const uint32_t bytes = (uint32_t)(p.G * D * 2);
           if (lane == 0) mbar_expect_tx(st_full, toks * bytes);
           __syncwarp();
           if (lane < toks)
             bulk_load(smem_u32(stage) + lane * bytes, p.q + (int64_t)(dx.z + dd.z + lane) * p.q_stride + (int64_t)dd.y * p.G * D,
                       bytes, st_full, policy_evict_first());
-          ++seg;
+          ++staged;
         }
       }
     }
     if (!ok && lane == 0) give_up();
-    if (!ok && seg > 0 && lane == 0) mbar_wait_parked(st_full, (seg - 1) & 1);  // staged rows in flight
   } else if (warp == W_MMA) {
     // ---- MMA issue: S of tile t, then O of tile t - 1 (the warp together, one thread issues) ----
     constexpr uint32_t id_s = umma_idesc_e4m3(128, C, false, false);
@@ -712,12 +716,12 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       more = !(fl & kFinal);
       if (more) {
         const int slot = (2 * t) % NS;
-        if (!(ok = mbar_wait_warp(d_full(ds), (t / ND) & 1))) break;
+        if (!(ok = wait(d_full(ds), (t / ND) & 1))) break;
         fl = descs[ds].flags;
         if (fl & kEnd) break;
-        if (fl & kNewSeg) ok = mbar_wait_warp(q_full, seg++ & 1);
+        if (fl & kNewSeg) ok = wait(q_full, seg++ & 1);
         // (the scores of tile t - 2 were read before its weights were complete)
-        ok = ok && mbar_wait_warp(d_scales(ds), (t / ND) & 1) && mbar_wait_warp(full(slot), ((2 * t) / NS) & 1);
+        ok = ok && wait(d_scales(ds), (t / ND) & 1) && wait(full(slot), ((2 * t) / NS) & 1);
         if (!ok) break;
         if (go) mbar_arrive(d_free(ds));
         tc_fence_after_sync();
@@ -733,8 +737,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
       if (t > 0) {  // O = V^T P^T of tile t - 1
         const int u = t - 1, slot = (2 * u + 1) % NS;
-        ok = mbar_wait_warp(full(slot), ((2 * u + 1) / NS) & 1) && (u < 2 || mbar_wait_warp(o_free(u & 1), ((u >> 1) - 1) & 1)) &&
-             mbar_wait_warp(p_full(u % kRing), (u / kRing) & 1);
+        ok = wait(full(slot), ((2 * u + 1) / NS) & 1) && (u < 2 || wait(o_free(u & 1), ((u >> 1) - 1) & 1)) &&
+             wait(p_full(u % kRing), (u / kRing) & 1);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t va = slots + slot * X::kSlot, pa = p_s + (u & 1) * X::kP, d = o_col + (u & 1) * NP * C;
@@ -762,12 +766,12 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     auto sync_group = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(grp_sync(grp));
-      ok &= mbar_wait_warp(grp_sync(grp), n_grp++ & 1);
+      ok &= wait(grp_sync(grp), n_grp++ & 1);
     };
     auto sync_all = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(all_sync);
-      ok &= mbar_wait_warp(all_sync, n_all++ & 1);
+      ok &= wait(all_sync, n_all++ & 1);
     };
 
     // one wait a tile: its scores are there once its descriptor, its scales and O of tile t - 2 (and with it the weights'
@@ -779,10 +783,10 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       const int ds = t % ND, par = t & 1, ring = t % kRing;
       const Desc& de = descs[ds];
       if (fl & kNextSeg) {
-        if (!(ok = mbar_wait_warp(d_full(ds), (t / ND) & 1))) break;
+        if (!(ok = wait(d_full(ds), (t / ND) & 1))) break;
         if (de.flags & kEnd) break;
         const int j0 = de.j0, toks = min(p.TQ, de.fresh - j0);
-        if (X::kStage > 0 && !(ok = mbar_wait_warp(st_full, seg & 1))) break;
+        if (X::kStage > 0 && !(ok = wait(st_full, seg & 1))) break;
         s_qf = s_qf2 + (seg & 1) * RP;
         s_lim = s_lim2 + (seg & 1) * RP;
         ++seg;
@@ -847,7 +851,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
           if (X::kStage > 0) mbar_arrive(st_free);
         }
       }
-      if (!(ok = mbar_wait_warp(s_full(par), (t >> 1) & 1))) break;
+      if (!(ok = wait(s_full(par), (t >> 1) & 1))) break;
       tc_fence_after_sync();
       // the V scale is a power of two: its exponent, and its reciprocal
       fl = de.flags;
@@ -888,7 +892,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         }
         uint8_t* v_row = base + ((2 * t + 1) % NS) * X::kSlot;
         constexpr int kRowB = X::kRowB, kCh = kRowB / 16;
-        ok = mbar_wait_warp(full((2 * t + 1) % NS), ((2 * t + 1) / NS) & 1);
+        ok = wait(full((2 * t + 1) % NS), ((2 * t + 1) / NS) & 1);
         if (!ok) break;
         bool nan_code = false;
         const bool partly = toks > 1 && !dead && (tok > pos0 || (p.window > 0 && tok < pos1 - p.window + 1));
@@ -1054,11 +1058,11 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     float acc[NP][R];
     float m_run = -INFINITY, l_run = 0.f;  // lane i (< R) of every warp: row i of the group
     bool ok = true;
-    ok = mbar_wait_warp(d_full(0), 0);
+    ok = wait(d_full(0), 0);
     int fl = ok ? descs[0].flags & kEnd : kEnd;
     for (int t = 0; !(fl & (kFinal | kEnd)); ++t) {
       const int ds = t % ND, par = t & 1, ring = t % kRing;
-      if (!(ok = mbar_wait_warp(p_full(ring), (t / kRing) & 1))) break;
+      if (!(ok = wait(p_full(ring), (t / kRing) & 1))) break;
       const Desc& de = descs[ds];
       fl = de.flags;
       float mt = -INFINITY, lt = 0.f;
@@ -1085,7 +1089,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
         }
         __syncwarp();
       }
-      if (!(ok = mbar_wait_warp(o_full(par), (t >> 1) & 1))) break;
+      if (!(ok = wait(o_full(par), (t >> 1) & 1))) break;
       tc_fence_after_sync();
       const uint32_t poison = s_nan[ring] == t + 1 ? s_taint[ring * 128 * NG + 128 * grp + tt] : 0;
 #pragma unroll
@@ -1174,14 +1178,17 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   // ---- teardown: copies and MMAs in flight land before memory is released ----
   __syncthreads();
   if (*s_abort) {
-    if (warp == W_LOAD && lane == 0)
-      for (int i = max(0, loads - NS); i < loads; ++i) mbar_wait_parked(full(i % NS), (i / NS) & 1);
+    if (warp == W_LOAD && lane == 0) {
+      for (int i = max(0, loads - NS); i < loads; ++i) mbar_wait_parked(full(i % NS), (i / NS) & 1, 1000, kTries);
+      if (staged > 0) mbar_wait_parked(st_full, (staged - 1) & 1, 1000, kTries);
+    }
     if (warp == W_MMA && elect_one()) {  // one more commit covers every MMA that this thread issued
       umma_commit(drained);
-      mbar_wait_parked(drained, 0);
+      mbar_wait_parked(drained, 0, 1000, kTries);
     }
   }
   if (warp == W_MMA) {
+    __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tmem, X::kTmem);
   }
@@ -1556,6 +1563,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t 
   p.t_acc = reinterpret_cast<float*>(w + y.t_acc);
   p.t_ml = reinterpret_cast<float2*>(w + y.t_ml);
   p.refused = reinterpret_cast<int*>(w + y.refused);
+  p.fault_tx = a.fault_wait ? 16 : 0;
   p.flags = a.flags;
   p.counters = a.counters;
   switch (a.cache.dim) {

@@ -39,7 +39,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait: true when the phase completed, false after kWaitLimit tries.
+// Bounded wait: true when the phase completed, false after kWaitLimit tries
+// (a try that fails takes 4 us: about four seconds).
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitLimit; ++i)
     if (mbar_try_wait(bar, parity)) return true;
@@ -48,9 +49,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
 
 // Bounded wait that parks the thread between tries: each try_wait may
 // suspend it for up to `hint_ns` until the phase completes, so waiting warps
-// leave the issue slots to the working ones; false after kWaitLimit tries.
-__device__ __forceinline__ bool mbar_wait_parked(uint32_t bar, uint32_t parity, uint32_t hint_ns = 1000) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+// leave the issue slots to the working ones; false after `limit` tries.
+__device__ __forceinline__ bool mbar_wait_parked(uint32_t bar, uint32_t parity, uint32_t hint_ns = 1000,
+                                                 uint32_t limit = kWaitLimit) {
+  for (uint32_t i = 0; i < limit; ++i) {
     uint32_t ok;
     asm volatile(
         "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
@@ -65,7 +67,7 @@ __device__ __forceinline__ bool mbar_wait_parked(uint32_t bar, uint32_t parity, 
 // Bounded wait of a whole warp (all lanes call; the same answer for all): the
 // vote on the phase comes with the try, and the first try stands by itself, as
 // most waits of a pipeline in step find their phase complete.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t limit = kWaitLimit) {
   uint32_t ok;
   auto attempt = [&]() {
     asm volatile(
@@ -77,7 +79,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
   };
   attempt();
 #pragma unroll 1
-  for (uint32_t i = 0; !ok && i < kWaitLimit; ++i) attempt();
+  for (uint32_t i = 0; !ok && i < limit; ++i) attempt();
   return ok;
 }
 
