@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   int b = 0, rt = 0, h = 0, tile = 0, t_first = 0, t_last = -1;
   int seg0 = 0;  // position of the segment's first tile
   int id = -2;
-  int loads = 0, staged = 0;  // slots requested, segments whose query rows were
+  int loads = 0;  // slots requested
   auto take = [&](int bl) {  // request b0 + bl becomes the current one
     b = b0 + bl;
     r.c0 = __shfl_sync(0xffffffffu, mine.c0, bl);
@@ -664,8 +664,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   } else if (warp == W_LOAD) {
     // ---- copies ----
     bool ok = true;
-    int fl = 0;
-    uint32_t late = blockIdx.x == 0 ? p.fault_tx : 0;  // (debug: bytes that the first copies do not bring)
+    int fl = 0, staged = 0;  // segments whose query rows were requested
+    if (p.fault_tx && blockIdx.x == 0 && lane == 0) mbar_more_tx(full(0), p.fault_tx);  // (debug: bytes that never come)
     for (int t = 0; ok && !(fl & kFinal); ++t) {
       const int ds = t % ND;
       if (!(ok = wait(d_full(ds), (t / ND) & 1))) break;
@@ -684,8 +684,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       for (int kv = 0; kv < 2; ++kv) {
         const int slot = loads % NS;
         if (loads >= NS && !(ok = wait(empty(slot), ((loads / NS) - 1) & 1))) break;
-        if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(copies * block * X::kRowB) + late);
-        late = 0;
+        if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(copies * block * X::kRowB));
         __syncwarp();
         if (my_id >= 0)
           tma_load_2d(slots + slot * X::kSlot + panel * X::kPanelBytes + blk * block * X::kRowB, kv ? &maps.v : &maps.k,
@@ -704,6 +703,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
       }
     }
     if (!ok && lane == 0) give_up();
+    if (staged > 0) wait(st_full, (staged - 1) & 1);  // (nobody else may be left to wait for them)
   } else if (warp == W_MMA) {
     // ---- MMA issue: S of tile t, then O of tile t - 1 (the warp together, one thread issues) ----
     constexpr uint32_t id_s = umma_idesc_e4m3(128, C, false, false);
@@ -1178,10 +1178,8 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   // ---- teardown: copies and MMAs in flight land before memory is released ----
   __syncthreads();
   if (*s_abort) {
-    if (warp == W_LOAD && lane == 0) {
+    if (warp == W_LOAD && lane == 0)
       for (int i = max(0, loads - NS); i < loads; ++i) mbar_wait_parked(full(i % NS), (i / NS) & 1, 1000, kTries);
-      if (staged > 0) mbar_wait_parked(st_full, (staged - 1) & 1, 1000, kTries);
-    }
     if (warp == W_MMA && elect_one()) {  // one more commit covers every MMA that this thread issued
       umma_commit(drained);
       mbar_wait_parked(drained, 0, 1000, kTries);
