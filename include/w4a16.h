@@ -481,7 +481,8 @@ const char* w4a16_last_error(void);
  * expects 16 bytes more than its copies deliver, so that warp's bounded wait
  * gives up, raises W4A16_DEVICE_TIMEOUT and leaves its rows unwritten; every
  * copy still lands, so nothing is in flight when the kernel exits; in every
- * w4a16_kv_attention launch the first slot of keys of one CTA, likewise) and
+ * w4a16_kv_attention launch the first slot of keys of one CTA waits for an
+ * arrival that never comes, to the same end) and
  * W4A16_FORCE_KERNEL (simt | tc | vanilla).  They are read once, at the
  * first call, otherwise. */
 void w4a16_debug_reload_env(void);

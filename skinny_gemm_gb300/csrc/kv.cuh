@@ -50,7 +50,7 @@ struct KvAttentionArgs {
   void* ws;
   int* counters;
   int* flags;
-  int fault_wait;  // debug (W4A16_FAULT=wait): the first CTA's first copies never complete
+  int fault_wait;  // debug (W4A16_FAULT=wait): the first CTA's first slot waits for an arrival that never comes
 };
 size_t kv_attention_workspace(int B, int T, int q_heads, int kv_heads, int dim, int max_new, int max_len, int window);
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t s);

@@ -168,7 +168,7 @@ struct Params : Line {
   float* t_acc;  // [grid][t_slots][RP][D]
   float2* t_ml;  // [grid][t_slots][RP]
   int* refused;   // [1] the step's offsets step back (written by every call)
-  uint32_t fault_tx;  // see KvAttentionArgs::fault_wait
+  int arrivals;  // that complete the first CTA's first slot: 1 (see KvAttentionArgs::fault_wait)
   int* counters;  // [grid] tiles done of divided groups, by the CTA of the first; zero between calls
   int* flags;
 };
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     tmem_relinquish();
   } else if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), 1);
+      mbar_init(full(i), i == 0 && blockIdx.x == 0 ? p.arrivals : 1);
       mbar_init(empty(i), 1);
     }
     for (int i = 0; i < ND; ++i) {
@@ -665,7 +665,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     // ---- copies ----
     bool ok = true;
     int fl = 0, staged = 0;  // segments whose query rows were requested
-    if (p.fault_tx && blockIdx.x == 0 && lane == 0) mbar_more_tx(full(0), p.fault_tx);  // (debug: bytes that never come)
     for (int t = 0; ok && !(fl & kFinal); ++t) {
       const int ds = t % ND;
       if (!(ok = wait(d_full(ds), (t / ND) & 1))) break;
@@ -1561,7 +1560,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int pdl, cudaStream_t 
   p.t_acc = reinterpret_cast<float*>(w + y.t_acc);
   p.t_ml = reinterpret_cast<float2*>(w + y.t_ml);
   p.refused = reinterpret_cast<int*>(w + y.refused);
-  p.fault_tx = a.fault_wait ? 16 : 0;
+  p.arrivals = a.fault_wait ? 2 : 1;
   p.flags = a.flags;
   p.counters = a.counters;
   switch (a.cache.dim) {

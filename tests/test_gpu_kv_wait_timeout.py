@@ -1,7 +1,7 @@
 """The paged attention's bounded waits run out, on the GPU, without faulting it.
 
-W4A16_FAULT=wait makes the first slot of keys of one CTA expect 16 bytes more
-than its copies bring.  Every copy still lands; all roles of that CTA give up
+W4A16_FAULT=wait makes the first slot of keys of one CTA wait for an arrival
+more than there will be.  Every copy still lands; all roles of that CTA give up
 after about a second, wait (bounded) for what is in flight, free their tensor
 memory and leave, and the flag is raised."""
 import time
