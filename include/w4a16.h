@@ -411,13 +411,14 @@ int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, 
  * workspace: w4a16_kv_attention_workspace_bytes(...) bytes of device memory,
  * 256-byte aligned, no initial contents needed; calls that share one must
  * not overlap on the GPU.  With G groups of 1024 tokens in max_len (or in a
- * window and max_new), G * T * q_heads * (4 dim + 8) bytes hold partial results
- * where G > 1, and some tens of MB at most the rest.  Above 2^30 the rows are taken in several
- * launches that share that much (more only where 32 rows of a key head need
- * it): 2048 rows of 32 x 128 over max_len = 131,072 in five.  0 bytes: the arguments
- * are invalid, or the step is too large for one call (G x T x q_heads, or a
- * launch's row tiles x heads x 128-token tiles of max_len, above 2^31); the
- * call then returns W4A16_ERR_SHAPE.
+ * window and max_new), G * T * q_heads * (4 dim + 8) bytes hold partial
+ * results where G > 1, and some tens of MB at most the rest.  Above 2^32 the
+ * rows are taken in several launches that share that much (more only where 32
+ * rows of a key head need it): 8192 rows of 32 x 128 over max_len = 131,072 in
+ * five, which share 3.6 GB.  So max_len is best not far above the lengths.  0
+ * bytes: the arguments are invalid, or the step is too large for one call
+ * (G x T x q_heads, or a launch's row tiles x heads x 128-token tiles of
+ * max_len, above 2^31); the call then returns W4A16_ERR_SHAPE.
  *
  * counters: int32 [W4A16_KV_COUNTERS], zero before the first call; every call
  * that completes leaves them zero, and after W4A16_DEVICE_TIMEOUT they must be

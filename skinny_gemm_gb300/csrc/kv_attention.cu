@@ -1372,8 +1372,11 @@ __global__ void __launch_bounds__(SETS == 128 ? 1024 : 256) kv_combine_kernel(co
 
 // A row has a slot for every group of the longest request, 4 dim + 8 bytes a query head.  So that the workspace stays
 // bounded, a call whose rows need more takes them in several launches, a row tile's at least (8192 rows of 32 x 128
-// over 131,072 tokens would take 17 GB; a launch that fills this is a millisecond of work).
-constexpr int64_t kGroupBytes = (int64_t)1 << 30;
+// over 131,072 tokens would take 17 GB).  Where the longest request is as long as max_len, a launch that fills this is
+// milliseconds of work and the division costs nothing (8192 rows after 100k tokens: 46.1 ms, undivided 47.0); where
+// it is much shorter, launches are short (2048 rows from an empty cache with a max_len of 131,072: 264 us in two
+// launches, 241 undivided; 284 with half of this, 319 with a quarter).
+constexpr int64_t kGroupBytes = (int64_t)1 << 32;
 
 struct Layout {
   int rows;  // of a launch

@@ -174,7 +174,7 @@ def test_a_negative_head_counts_as_zero_and_is_flagged():
     assert (t.tolist(), p.cu.tolist(), p.lens.tolist(), p.slots.tolist(), p.positions.tolist(), int(p.head)) == want
 
 
-@pytest.mark.parametrize("hq,hkv,dim,loose", [(32, 8, 64, 1 << 23), (64, 2, 256, 1 << 20), (12, 4, 128, 1 << 24)])
+@pytest.mark.parametrize("hq,hkv,dim,loose", [(32, 8, 64, 1 << 25), (64, 2, 256, 1 << 22), (12, 4, 128, 1 << 26)])
 @pytest.mark.parametrize("window", [0, 700])
 def test_rows_in_several_launches(hq, hkv, dim, loose, window):
     """A bound on the lengths that makes partial results outgrow one launch: the same bits as with a tight one, in ragged
@@ -190,7 +190,7 @@ def test_rows_in_several_launches(hq, hkv, dim, loose, window):
     want = ops.kv_attention(q, cache, table, cu, lens, max(new), max(step.lens), window=window)
     one = ops.kv_attention_workspace_bytes(len(new), 1, hq, cache, max(new), loose, window)
     n = ops.kv_attention_workspace_bytes(len(new), T, hq, cache, max(new), loose, window)
-    assert n < 1.2 * (1 << 30) and (window > 0 or T * one > 2 * n)  # (several launches)
+    assert n < 4.2 * (1 << 30) and (window > 0 or T * one > 2 * n)  # (several launches)
     out = torch.full_like(q, 7.0)
     assert torch.equal(ops.kv_attention(q, cache, wide, cu, lens, max(new), loose, window=window, out=out), want)
     assert bool((want[step.T:] == 0).all()) and ops.device_status() == 0
