@@ -449,7 +449,6 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
     }
   } else if (warp == W_LIST) {
     pdl_wait();
-    pdl_launch_dependents();  // (after the wait: what the next kernel reads of this call's inputs is there when it starts)
     int mine_end = 0;         // inclusive prefix of this lane's request
     int rows = 0;             // of valid requests
     bool back = false;
@@ -565,6 +564,9 @@ __global__ void __launch_bounds__(Geo<D, RP>::kThreads, Geo<D, RP>::kCtas)
   const uint32_t s_col = tmem, o_col = tmem + 2 * C;  // S: two tiles of C columns; O: two tiles of NP panels of C
 
   if (warp == W_LIST) {
+    // (after the wait, so that what the next kernel reads of this call's inputs is there when it starts; and after the
+    // set-up: a next kernel's CTA must not hold tensor memory that a CTA it waits for has yet to get)
+    pdl_launch_dependents();
     // ---- work list ----
     bool fresh_seg = true, ok = true;
     const Cut cut(s_rest[1], p.grid);
