@@ -390,10 +390,12 @@ int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, 
  * with fp32 scores, maxima, sums and accumulators.  q enters to 2^-22 of its
  * row's largest element; a weight exp(z), times its token's V scale, enters
  * the product with V rounded to 8 significant bits, as bf16 would, and to
- * 2^-22 of the largest such product of its 128-token tile.  Tokens that a row does not see have no effect on it,
- * whatever their bytes (NaN codes included); nor have tokens whose table
- * entry is not a block of the cache (those raise W4A16_DEVICE_KV_RANGE).  A
- * row that sees nothing, and a row t >= cu[B], is written as zeros.
+ * 2^-22 of the largest such product of its 128-token tile; the sum of the
+ * weights keeps each of them, whatever the V scales beside it.  Tokens that a
+ * row does not see have no effect on it, whatever their bytes (NaN codes
+ * included); nor have tokens whose table entry is not a block of the cache
+ * (those raise W4A16_DEVICE_KV_RANGE).  A row that sees nothing, and a row
+ * t >= cu[B], is written as zeros.
  * out is bf16 [T][q_heads][dim], 16-byte aligned.
  *
  * max_new and max_len bound the step: requests have at most max_new new

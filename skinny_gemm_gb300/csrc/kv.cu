@@ -33,8 +33,8 @@ cudaError_t launch(const void* fn, dim3 grid, int threads, void** args, int pdl,
 // dependent loads (lengths, table or free list, store).  Every CTA computes
 // the sums itself (requests in chunks of kPlanThreads, the running totals
 // carried in registers), so nothing is handed between CTAs and one launch
-// does it all.  On the GPU 8 requests take 2.4 us, 200 requests of five tokens
-// 3.8 us, 333 prompt chunks (0.57 MB in and out) 5.3 us.
+// does it all.  On the GPU 8 requests take 2.2 us, 200 requests of five tokens
+// 3.7 us, 333 prompt chunks (0.57 MB in and out) 5.2 us.
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanTokens = 2048;  // tokens per CTA
@@ -200,9 +200,10 @@ __global__ void __launch_bounds__(256) kv_advance_kernel(KvPlanArgs a) {
 // are long enough for the whole CTA.
 // Bytes: 2 in and 1 out per element; a run's rows stay in registers between
 // the maximum and the codes.  10k tokens of 8 heads x 128 in blocks of 16 (64 MB):
-// 14.9 us, 4.3 TB/s (one head a CTA 17.6); 48 tokens 2.5 us.  Bound by the
-// instructions of maxima and codes (issue slots half full, ALU 49%) and by the
-// wait between the slots' arrival and the rows'.
+// 14.7 us, 4.4 TB/s (one head a CTA 17.6); 48 tokens 2.2 us.  No unit is full
+// (issue slots 54%, ALU 49%, DRAM 29%): a warp requests one run's rows, waits,
+// reduces and stores before the next run's, and 1304 CTAs are 2.1 rounds of the
+// 608 that fit.
 
 constexpr int kAppendThreads = 256, kAppendWarps = 8;
 constexpr int kMaxPer = 112, kMaxHeads = 8;  // tokens and heads of a CTA
@@ -485,7 +486,12 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, int pdl, cudaStream_t s) {
                  a.cache.blocks * a.cache.block, 0, 0};
   const int heads = a.cache.heads;
   p.hg = heads < kMaxHeads ? heads : kMaxHeads;
-  // few tokens are taken for runs of one (decode); many for runs of a block, which a warp holds up to 2048 values of
+  // Which tokens make runs is known on the device only, so the rule goes by their number: few are taken for runs of one
+  // or a few (decode, verify), many for runs of a block, which a warp holds up to 2048 values of.  Measured as (first /
+  // second / third form), us, 8 heads of 128.  Few: 48 single tokens 2.4 / 17 / 7.6; 200 x 5 5.8 / 7.2 / 7.0; but one
+  // prompt of 1024, which the rule takes for short runs, 5.9 / 3.9 / 4.8 in blocks of 16, 13 / 9.6 / 5.4 of 64, 17 / 13 /
+  // 4.9 of 128 (2 heads of 256 in blocks of 64: 5.5 / 7.8 / 5.2).  Many: a prompt of 10k in blocks of 16 34 / 9.9 / 11.8; of
+  // 64 44 / 19 / 15; of 128 47 / 28 / 13; 2 heads of 256, blocks of 64, 14 / 14 / 9.0.  4000 single tokens 28 / 25 / 23.
   if (a.T < 2048) {
     p.per = kAppendWarps / p.hg;
   } else if (a.cache.block * a.cache.dim <= 32 * kWarpChunks * 8) {

@@ -30,13 +30,14 @@
 // groups are joined by kv_combine_kernel.
 //
 // Bound: HBM for a few rows a key head.  64 requests of 1 x 4 rows to 16k tokens
-// of 2 heads x 256: 87 us, 5.66 TB/s; one of 131k tokens 34 us, 3.9 TB/s, where
+// of 2 heads x 256: 87 us, 5.67 TB/s; one of 131k tokens 35 us, 3.9 TB/s, where
 // set-up (2 us), the first copies (2 us), the groups that a cut divides (2 to 5
 // us) and the join (4 us) weigh more.  A CTA has two to five tiles (64 KB each with
 // heads of 256) in flight.  From 16 rows on the softmax warps' instructions and
 // the chain of waits and issues in the MMA warp, each about 2000 clocks a tile of
-// 32 rows (3 prompt chunks of 300 over 6k tokens, 28/4 heads of 128: 194 us, 234
-// TFLOP/s; S and O issued by two warps: 208).
+// 32 rows (3 prompt chunks of 300 over 6k tokens, 28/4 heads of 128: 198 us, 229
+// TFLOP/s; a prompt of 8192 from an empty cache, 32/8 of 128, 2.0 ms, 271; S and O
+// issued by two warps: 208 instead of 194 of the chunks).
 //
 // CTA: 4 NG + 4 NG + 3 warps (NG groups of R query rows).
 //   softmax warps  a thread per token: scores from TMEM, mask, maximum,
