@@ -435,6 +435,81 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
                        int max_blocks, int max_new, int max_len, int window, float scale, void* workspace,
                        size_t workspace_bytes, int32_t* counters, void* stream);
 
+/* ---- Microscaled 4-bit floating point --------------------------------------------
+ *
+ * Matrices of e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; bit
+ * 3 the sign) with one scale per block of a row, as weights and, quantised by
+ * the call, as activations: both operands go to the tensor cores as they lie.
+ *   W4A16_FP4_MX  blocks of 32, e8m0 scales: value = code * 2^(byte - 127)
+ *   W4A16_FP4_NV  blocks of 16, e4m3 scales, a factor per row:
+ *                 value = code * scale * row_scale
+ * Code k of a row lies in bits 4 (k % 2) of byte k / 2.  Scales lie in atoms
+ * of 512 bytes, 128 rows by 4 blocks: block b of row r is byte
+ *   (r / 128 * ceil(blocks / 4) + b / 4) * 512 + 16 (r % 32) + 4 (r % 128 / 32) + b % 4
+ * of its expert's w4a16_fp4_scale_bytes(rows, K, format).  Bytes of blocks past K
+ * up to a multiple of four must not be NaN (w4a16_fp4_quant writes 0); bytes of
+ * rows past the last one may be anything. */
+#define W4A16_FP4_NV 1
+#define W4A16_FP4_MX 2
+
+typedef struct {
+  uint8_t* codes;   /* [experts * rows][K / 2], 16-byte aligned */
+  uint8_t* scales;  /* experts times w4a16_fp4_scale_bytes(rows, K, format), 16-byte aligned */
+  float* row_scale; /* [experts * rows]; NULL: 1 (mx has none) */
+  int rows;         /* rows of one expert (N of a weight matrix, M of activations) */
+  int K;            /* a multiple of 32 */
+  int experts;      /* 1 for a plain matrix */
+  int format;       /* W4A16_FP4_NV or W4A16_FP4_MX */
+} w4a16_fp4;
+
+/* Bytes of the scales of `rows` rows of K codes; 0 if the arguments are invalid. */
+size_t w4a16_fp4_scale_bytes(int rows, int K, int format);
+
+/* Quantise out->experts * out->rows rows of bf16, row r at x + r * x_stride
+ * (elements, a multiple of 8; x 16-byte aligned), into out's codes, scales and
+ * (nv) row_scale.  With p = max |x| of a block, q = max |x| of a row:
+ *   mx  scale = 2^e, e = max(floor(log2 p) - 2, -127)
+ *   nv  row_scale = f, the smallest power of two >= 2^-126 with q <= 6 * 448 f;
+ *       scale = e4m3(p / f / 6), to nearest even; a block of scale 0 has codes +0
+ *   code = e2m1(x / scale [/ f]), to nearest, ties to the even code, at most 6
+ * A block with a NaN or an infinity gets a NaN scale and codes 0; q is over a
+ * row's finite values.  Zero rows is a no-op. */
+int w4a16_fp4_quant(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* out, void* stream);
+
+/* y[r][k] = bf16(code * scale * row_scale), bf16 [experts * rows][K], 16-byte
+ * aligned.  Exact for what w4a16_fp4_quant writes, but for values past bf16's
+ * range; a NaN scale makes its block NaN. */
+int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream);
+
+/* What a product gives per row: W's rows n as they are, or pairs of them,
+ * gate 2i and up 2i + 1 (w->rows even), as y[m][i] = act(gate) * up. */
+#define W4A16_FP4_LINEAR 0
+#define W4A16_FP4_SILU 1 /* g / (1 + exp(-g)) */
+#define W4A16_FP4_GELU 2 /* g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
+
+/* y[m][n] = bf16( x'[m] . W[n] ), x' = x quantised row by row as above, in w's
+ * format; products of codes and scales are exact, their sums fp32.  x bf16, row
+ * m at x + m * x_stride (a multiple of 8; 16-byte aligned), y bf16 [M][w->rows] (or
+ * [M][w->rows / 2] for an act), 2-byte aligned.  workspace: device memory of
+ * w4a16_fp4_mm_workspace_bytes(M, K, format) bytes, 256-byte aligned, no initial
+ * contents needed; calls that share one must not overlap on the GPU.  M >= 0;
+ * M == 0 is a no-op. */
+size_t w4a16_fp4_mm_workspace_bytes(int M, int K, int format);
+int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a16_bf16* y, int M, int act,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for activations already quantised (several products of one x):
+ * x->rows rows, x->experts 1, of w's K and format. */
+int w4a16_fp4_mm_q(const w4a16_fp4* x, const w4a16_fp4* w, w4a16_bf16* y, int act, void* stream);
+
+/* Routed experts: y[t][j] = W[ids[t * top + j]] x'[t] for T tokens of `top`
+ * choices each (an expert may occur twice); ids int32 [T][top] on the device, y
+ * bf16 [T][top][rows or rows / 2].  An id outside 0..experts-1 gives a row of
+ * zeros and raises W4A16_DEVICE_BAD_ID.  experts <= 4096.  T >= 0, top >= 1. */
+size_t w4a16_fp4_mm_id_workspace_bytes(int T, int top, int K, int experts, int format);
+int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, const int32_t* ids, w4a16_bf16* y,
+                    int T, int top, int act, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Debug: q[N][K] (one byte per code) from Wq[N][K/8].  Bit-exact
  * ([W2D2 "Packed Storage Layout"]). */
 int w4a16_unpack(const uint32_t* Wq, uint8_t* q, int N, int K, void* stream);

@@ -13,6 +13,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "kv.cuh"
 #include "launch.h"
 #include "stq1.cuh"
@@ -682,6 +683,245 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
   if (int rc = flag_pointer(&a.flags)) return rc;
   cudaError_t e = launch_kv_attention(a, env().pdl, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_kv_attention launch");
+}
+
+// ---- microscaled 4-bit floating point ------------------------------------------------
+
+namespace {
+
+constexpr int kFp4MaxExperts = 4096;
+
+int check_fp4_shape(int rows, int K, int experts, int format) {
+  if (format != W4A16_FP4_NV && format != W4A16_FP4_MX)
+    return fail(W4A16_ERR_SHAPE, "format = %d must be W4A16_FP4_NV or W4A16_FP4_MX", format);
+  if (K <= 0 || K > kMaxDim || K % 32) return fail(W4A16_ERR_SHAPE, "K = %d must be a positive multiple of 32", K);
+  if (experts < 1 || experts > kFp4MaxExperts)
+    return fail(W4A16_ERR_EXPERTS, "experts = %d must be in 1..%d", experts, kFp4MaxExperts);
+  if (rows < 0 || (int64_t)rows * experts > kMaxDim)
+    return fail(W4A16_ERR_SHAPE, "rows = %d: experts * rows must be in 0..2^30", rows);
+  return W4A16_OK;
+}
+
+// A matrix with rows, its pointers there and aligned.
+int check_fp4(const w4a16_fp4* m, const char* name) {
+  if (!m) return fail(W4A16_ERR_NULL, "null %s", name);
+  if (int rc = check_fp4_shape(m->rows, m->K, m->experts, m->format)) return rc;
+  if (m->rows == 0) return W4A16_OK;
+  if (!m->codes || !m->scales) return fail(W4A16_ERR_NULL, "%s: null codes or scales", name);
+  if (misaligned(m->codes, 16) || misaligned(m->scales, 16) || misaligned(m->row_scale, 4))
+    return fail(W4A16_ERR_ALIGN, "%s: codes and scales must be 16-byte and row_scale 4-byte aligned", name);
+  return W4A16_OK;
+}
+
+int check_fp4_rows(const void* x, int64_t x_stride, int64_t rows, int K) {
+  if (!x) return fail(W4A16_ERR_NULL, "null tensor pointer");
+  if (rows > 1 && x_stride < K) return fail(W4A16_ERR_SHAPE, "x_stride must be at least K = %d elements", K);
+  if (misaligned(x, 16) || x_stride % 8) return fail(W4A16_ERR_ALIGN, "rows of x must be 16-byte aligned");
+  return W4A16_OK;
+}
+
+int check_fp4_act(const w4a16_fp4* w, int act) {
+  if (act != W4A16_FP4_LINEAR && act != W4A16_FP4_SILU && act != W4A16_FP4_GELU)
+    return fail(W4A16_ERR_KERNEL, "unknown activation %d", act);
+  if (w->rows < 1) return fail(W4A16_ERR_SHAPE, "a weight matrix needs rows");
+  if (act != W4A16_FP4_LINEAR && w->rows % 2)
+    return fail(W4A16_ERR_SHAPE, "rows = %d: gate and up rows come in pairs", w->rows);
+  return W4A16_OK;
+}
+
+size_t up256(int64_t n) { return (size_t)((n + 255) / 256 * 256); }
+
+// Workspace of quantised rows: codes, scales, row factors.
+struct Fp4Space {
+  size_t codes, scales, factor, place, row, tiles, count, total;
+};
+Fp4Space fp4_space(int64_t places, int64_t rows, int64_t tiles, int K, int format) {
+  Fp4Space s = {};
+  s.scales = up256(places * (K / 2));
+  s.factor = s.scales + up256((places + kFp4Rows - 1) / kFp4Rows * fp4_atoms(K, format) * kFp4Atom);
+  s.place = s.factor + up256(places * 4);
+  if (tiles == 0) {
+    s.total = s.place;
+    return s;
+  }
+  s.row = s.place + up256(rows * 4);
+  s.tiles = s.row + up256(places * 4);
+  s.count = s.tiles + up256(tiles * (int64_t)sizeof(Fp4Tile));
+  s.total = s.count + 256;
+  return s;
+}
+
+// Routed: rows of an activation tile, and the most tiles that there can be.
+int fp4_id_tile(int64_t rows, int experts) {
+  const int64_t share = 2 * ((rows + experts - 1) / experts);
+  return fp4_mm_tile((int)(share < 128 ? share : 128));
+}
+int64_t fp4_id_tiles(int64_t rows, int experts) {
+  // an expert with rows wastes less than one tile
+  return (rows < experts ? rows : experts) + rows / fp4_id_tile(rows, experts);
+}
+
+int check_fp4_space(const void* ws, size_t bytes, size_t need) {
+  if (!ws) return fail(W4A16_ERR_NULL, "the call needs a workspace of %zu bytes", need);
+  if (misaligned(ws, 256)) return fail(W4A16_ERR_ALIGN, "the workspace must be 256-byte aligned");
+  if (bytes < need) return fail(W4A16_ERR_SHAPE, "a workspace of %zu bytes is too small (%zu)", bytes, need);
+  return W4A16_OK;
+}
+
+}  // namespace
+
+size_t w4a16_fp4_scale_bytes(int rows, int K, int format) {
+  if (check_fp4_shape(rows, K, 1, format)) return 0;
+  return (size_t)fp4_scale_bytes(rows, K, format);
+}
+
+int w4a16_fp4_quant(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* out, void* stream) {
+  if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
+  if (int rc = check_fp4(out, "out")) return rc;
+  if (out->rows == 0) return W4A16_OK;
+  if (out->format == W4A16_FP4_NV && !out->row_scale) return fail(W4A16_ERR_NULL, "out: nv needs row_scale");
+  const int rows = out->rows * out->experts;
+  if (int rc = check_fp4_rows(x, x_stride, rows, out->K)) return rc;
+  if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
+  Fp4QuantArgs a{x, x_stride, out->codes, out->scales, out->row_scale, rows, out->K, out->rows, out->format,
+                 nullptr, 1, nullptr, 0};
+  cudaError_t e = launch_fp4_quant(a, env().pdl, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_quant launch");
+}
+
+int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream) {
+  if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
+  if (int rc = check_fp4(w, "w")) return rc;
+  if (w->rows == 0) return W4A16_OK;
+  if (!y) return fail(W4A16_ERR_NULL, "null tensor pointer");
+  if (misaligned(y, 16)) return fail(W4A16_ERR_ALIGN, "y must be 16-byte aligned");
+  if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
+  cudaError_t e = launch_fp4_dequant(*w, y, env().pdl, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_dequant launch");
+}
+
+size_t w4a16_fp4_mm_workspace_bytes(int M, int K, int format) {
+  if (check_fp4_shape(M, K, 1, format)) return 0;
+  return fp4_space(M, M, 0, K, format).total;
+}
+
+int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a16_bf16* y, int M, int act,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
+  if (int rc = check_fp4(w, "w")) return rc;
+  if (int rc = check_fp4_act(w, act)) return rc;
+  if (w->experts != 1) return fail(W4A16_ERR_EXPERTS, "experts = %d: w4a16_fp4_mm_id takes stacked experts", w->experts);
+  if (M < 0 || M > kMaxDim) return fail(W4A16_ERR_SHAPE, "M = %d must be in 0..2^30", M);
+  if (M == 0) return W4A16_OK;
+  if (int rc = check_fp4_rows(x, x_stride, M, w->K)) return rc;
+  if (!y) return fail(W4A16_ERR_NULL, "null tensor pointer");
+  if (misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "y must be 2-byte aligned");
+  const Fp4Space sp = fp4_space(M, M, 0, w->K, w->format);
+  if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total)) return rc;
+  if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
+  int* flags = nullptr;
+  if (int rc = flag_pointer(&flags)) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* factor = w->format == W4A16_FP4_NV ? reinterpret_cast<float*>(ws + sp.factor) : nullptr;
+  Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, M, w->K, M, w->format, nullptr, 1, nullptr, 0};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaError_t e = launch_fp4_quant(q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm launch");
+  Fp4MmArgs a = {};
+  a.xc = ws;
+  a.xs = ws + sp.scales;
+  a.xf = factor;
+  a.x_rows = M;
+  a.w = *w;
+  a.y = y;
+  a.M = M;
+  a.act = act;
+  a.early = true;
+  a.flags = flags;
+  a.fault_wait = env().fault == kFaultWait;
+  cudaError_t e = launch_fp4_mm(a, env().pdl, s);
+  return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_mm launch");
+}
+
+int w4a16_fp4_mm_q(const w4a16_fp4* x, const w4a16_fp4* w, w4a16_bf16* y, int act, void* stream) {
+  if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
+  if (int rc = check_fp4(x, "x")) return rc;
+  if (int rc = check_fp4(w, "w")) return rc;
+  if (int rc = check_fp4_act(w, act)) return rc;
+  if (x->experts != 1 || w->experts != 1)
+    return fail(W4A16_ERR_EXPERTS, "experts = %d and %d: w4a16_fp4_mm_id takes stacked experts", x->experts, w->experts);
+  if (x->K != w->K || x->format != w->format)
+    return fail(W4A16_ERR_SHAPE, "x has K = %d and format %d, w K = %d and format %d", x->K, x->format, w->K, w->format);
+  if (x->rows == 0) return W4A16_OK;
+  if (!y) return fail(W4A16_ERR_NULL, "null tensor pointer");
+  if (misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "y must be 2-byte aligned");
+  if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
+  Fp4MmArgs a = {};
+  a.xc = x->codes;
+  a.xs = x->scales;
+  a.xf = x->row_scale;
+  a.x_rows = x->rows;
+  a.w = *w;
+  a.y = y;
+  a.M = x->rows;
+  a.act = act;
+  if (int rc = flag_pointer(&a.flags)) return rc;
+  a.fault_wait = env().fault == kFaultWait;
+  cudaError_t e = launch_fp4_mm(a, env().pdl, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_mm_q launch");
+}
+
+size_t w4a16_fp4_mm_id_workspace_bytes(int T, int top, int K, int experts, int format) {
+  if (check_fp4_shape(0, K, experts, format) || T < 0 || top < 1 || (int64_t)T * top > kMaxDim) return 0;
+  const int64_t rows = (int64_t)T * top, tiles = fp4_id_tiles(rows, experts);
+  return rows ? fp4_space(tiles * kFp4Rows, rows, tiles, K, format).total : 256;
+}
+
+int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, const int32_t* ids, w4a16_bf16* y,
+                    int T, int top, int act, void* workspace, size_t workspace_bytes, void* stream) {
+  if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
+  if (int rc = check_fp4(w, "w")) return rc;
+  if (int rc = check_fp4_act(w, act)) return rc;
+  if (T < 0 || top < 1 || (int64_t)T * top > kMaxDim)
+    return fail(W4A16_ERR_EXPERTS, "T = %d must not be negative, top = %d positive, T * top at most 2^30", T, top);
+  if (T == 0) return W4A16_OK;
+  if (int rc = check_fp4_rows(x, x_stride, T, w->K)) return rc;
+  if (!ids || !y) return fail(W4A16_ERR_NULL, "null tensor pointer");
+  if (misaligned(ids, 4) || misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "ids must be 4-byte and y 2-byte aligned");
+  const int64_t rows = (int64_t)T * top, tiles = fp4_id_tiles(rows, w->experts), places = tiles * kFp4Rows;
+  if (places > INT32_MAX) return fail(W4A16_ERR_EXPERTS, "T * top = %lld rows are too many for one call", (long long)rows);
+  const Fp4Space sp = fp4_space(places, rows, tiles, w->K, w->format);
+  if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total)) return rc;
+  if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
+  int* flags = nullptr;
+  if (int rc = flag_pointer(&flags)) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* factor = w->format == W4A16_FP4_NV ? reinterpret_cast<float*>(ws + sp.factor) : nullptr;
+  int32_t* place = reinterpret_cast<int32_t*>(ws + sp.place);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Fp4RouteArgs r{ids, (int)rows, w->experts, fp4_id_tile(rows, w->experts), place, reinterpret_cast<int32_t*>(ws + sp.row),
+                 reinterpret_cast<Fp4Tile*>(ws + sp.tiles), reinterpret_cast<int32_t*>(ws + sp.count), flags};
+  if (cudaError_t e = launch_fp4_route(r, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm_id launch");
+  Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, T, w->K, T, w->format, place, top, y,
+                 act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2};
+  if (cudaError_t e = launch_fp4_quant(q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm_id launch");
+  Fp4MmArgs a = {};
+  a.xc = ws;
+  a.xs = ws + sp.scales;
+  a.xf = factor;
+  a.x_rows = places;
+  a.w = *w;
+  a.y = y;
+  a.M = (int)rows;
+  a.act = act;
+  a.tiles = r.tiles;
+  a.tile_count = r.count;
+  a.row = r.row;
+  a.max_tiles = (int)tiles;
+  a.nt = r.nt;
+  a.flags = flags;
+  a.fault_wait = env().fault == kFaultWait;
+  cudaError_t e = launch_fp4_mm(a, env().pdl, s);
+  return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_mm_id launch");
 }
 
 const char* w4a16_last_error(void) { return g_last_error.c_str(); }

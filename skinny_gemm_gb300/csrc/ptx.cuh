@@ -340,6 +340,50 @@ __device__ __forceinline__ void umma_f8(uint32_t go, uint32_t d_tmem, uint64_t a
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(go)
       : "memory");
 }
+// ---- 4-bit operands with block scales ----
+//
+// Operands are e2m1 codes, two a byte, K-major; scales lie in tensor memory,
+// one 32-bit column of four scales for each of 32 lanes and 32 rows, the same in
+// all four lane quarters.  Instruction descriptor: e2m1 A and B (bits 7-9 and
+// 10-11 = 1), bit 23 the scales' type (0 e4m3, 1 e8m0), N >> 3 in bits 17-22,
+// M >> 4 in 24-28, and which of a column's bytes the instruction's first
+// scale is: B in bits 4-5, A in 29-30.
+__host__ __device__ constexpr uint32_t umma_idesc_e2m1(int m, int n, bool e8m0) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)e8m0 << 23) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t umma_idesc_scale_byte(int byte) {
+  return ((uint32_t)byte << 4) | ((uint32_t)byte << 29);
+}
+
+// Blocks of 16 with e4m3 scales (four to a row and instruction): 64 codes of K.
+__device__ __forceinline__ void umma_nvf4(uint32_t go, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t a_scale, uint32_t b_scale, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %6, 0; setp.ne.b32 q, %7, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p; }"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"((uint32_t)accumulate), "r"(go)
+      : "memory");
+}
+// Blocks of 32 with e8m0 scales (two to a row and instruction).
+__device__ __forceinline__ void umma_mxf4(uint32_t go, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t a_scale, uint32_t b_scale, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %6, 0; setp.ne.b32 q, %7, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"((uint32_t)accumulate), "r"(go)
+      : "memory");
+}
+
+// 32 rows of 16 bytes (a 512-byte scale atom) from shared memory to four
+// columns of all four lane quarters.  Runs in the order of the same thread's
+// MMAs that follow.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t go, uint32_t taddr, uint64_t sdesc) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %2, 0;\n"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1; }" ::"r"(taddr), "l"(sdesc), "r"(go)
+      : "memory");
+}
+
 __device__ __forceinline__ void umma_commit_if(uint32_t go, uint32_t bar) {
   asm volatile(
       "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"

@@ -10,7 +10,9 @@ Names follow the C ABI in ``include/w4a16.h``: ``mm``, ``mm_group``,
 ``stq1_mm_id``, ``stq1_get_rows``, ``stq1_get_plan`` over an ``STQ1Matrix``
 (repacked on the device by ``stq1_pack``).  Between a layer's q/k/v and o
 projections: ``kv_plan``, ``kv_append`` and ``kv_attention`` over a ``KVCache``
-(paged keys and values in 8 bits).
+(paged keys and values in 8 bits).  Microscaled 4-bit floating point on both
+operands: ``fp4_quant``, ``fp4_dequant``, ``fp4_mm``, ``fp4_gated`` and
+``fp4_mm_id`` over an ``FP4Matrix``.
 """
 from __future__ import annotations
 
@@ -36,6 +38,8 @@ EXPORTS = ("w4a16_mm", "w4a16_mm_ws", "w4a16_mm_g", "w4a16_workspace_bytes", "w4
            "w4a16_mm_id", "w4a16_mm_id_kernel", "w4a16_unpack", "w4a16_dequant", "w4a16_get_plan", "w4a16_device_status", "w4a16_last_error",
            "w4a16_debug_reload_env", "w4a16_version",
            "w4a16_kv_plan", "w4a16_kv_append", "w4a16_kv_attention", "w4a16_kv_attention_workspace_bytes",
+           "w4a16_fp4_scale_bytes", "w4a16_fp4_quant", "w4a16_fp4_dequant", "w4a16_fp4_mm_workspace_bytes", "w4a16_fp4_mm",
+           "w4a16_fp4_mm_q", "w4a16_fp4_mm_id_workspace_bytes", "w4a16_fp4_mm_id",
            "stq1_packed_bytes", "stq1_pack", "stq1_mm", "stq1_mm_id", "stq1_get_rows", "stq1_get_plan")
 MAX_GROUP = 8
 STQ1_BLOCK_WEIGHTS, STQ1_BLOCK_BYTES = 256, 42
@@ -81,6 +85,12 @@ class KvCacheStruct(ctypes.Structure):
                 ("block", ctypes.c_int), ("dim", ctypes.c_int)]
 
 
+class Fp4Struct(ctypes.Structure):
+    """w4a16_fp4 (device pointers)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row_scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int), ("K", ctypes.c_int), ("experts", ctypes.c_int), ("format", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 
@@ -120,6 +130,16 @@ def lib() -> ctypes.CDLL:
             L.w4a16_kv_attention.argtypes = [P, ll, P, P, P, P, P] + [i] * 7 + [f, P, z, P, P]
             L.w4a16_kv_attention_workspace_bytes.argtypes = [i] * 8
             L.w4a16_kv_attention_workspace_bytes.restype = z
+            L.w4a16_fp4_scale_bytes.argtypes = [i, i, i]
+            L.w4a16_fp4_quant.argtypes = [P, ll, P, P]
+            L.w4a16_fp4_dequant.argtypes = [P, P, P]
+            L.w4a16_fp4_mm_workspace_bytes.argtypes = [i, i, i]
+            L.w4a16_fp4_mm.argtypes = [P, ll, P, P, i, i, P, z, P]
+            L.w4a16_fp4_mm_q.argtypes = [P, P, P, i, P]
+            L.w4a16_fp4_mm_id_workspace_bytes.argtypes = [i, i, i, i, i]
+            L.w4a16_fp4_mm_id.argtypes = [P, ll, P, P, P, i, i, i, P, z, P]
+            for f in ("w4a16_fp4_scale_bytes", "w4a16_fp4_mm_workspace_bytes", "w4a16_fp4_mm_id_workspace_bytes"):
+                getattr(L, f).restype = z
             L.stq1_packed_bytes.argtypes = [i, i]
             L.stq1_packed_bytes.restype = ctypes.c_size_t
             L.stq1_pack.argtypes = [P, P, i, i, P]
@@ -130,6 +150,7 @@ def lib() -> ctypes.CDLL:
             for f in ("w4a16_mm", "w4a16_mm_ws", "w4a16_mm_g", "w4a16_mm_kernel", "w4a16_mm_noalloc", "w4a16_mm_group", "w4a16_mm_argmax",
                       "w4a16_embed", "w4a16_expand_groups", "w4a16_mm_id", "w4a16_mm_id_kernel", "w4a16_unpack", "w4a16_dequant",
                       "w4a16_get_plan", "w4a16_device_status", "w4a16_kv_plan", "w4a16_kv_append", "w4a16_kv_attention",
+                      "w4a16_fp4_quant", "w4a16_fp4_dequant", "w4a16_fp4_mm", "w4a16_fp4_mm_q", "w4a16_fp4_mm_id",
                       "stq1_pack", "stq1_mm", "stq1_mm_id", "stq1_get_rows",
                       "stq1_get_plan"):
                 getattr(L, f).restype = ctypes.c_int
@@ -839,6 +860,255 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
     rc = lib().w4a16_kv_attention(q.data_ptr(), qs, cache._ptr, tp, cup, lp,
                                   out.data_ptr(), B, T, hq, max_blocks, max_new, max_len, window,
                                   1.0 / math.sqrt(dim) if scale is None else scale, wp, wn, cp, raw)
+    if rc:
+        _raise(rc)
+    return out
+
+
+# ---- microscaled 4-bit floating point (include/w4a16.h "Microscaled 4-bit floating point") ----
+
+FP4_FORMATS, FP4_BLOCK = {"nv": 1, "mx": 2}, {"nv": 16, "mx": 32}
+FP4_ACTS = {None: 0, "silu": 1, "gelu": 2}
+
+
+def fp4_scale_bytes(N: int, K: int, format: str) -> int:
+    """Bytes of the scales of one expert's N rows of K codes."""
+    if format not in FP4_FORMATS:
+        raise ValueError(f"unknown format {format!r}; one of {sorted(FP4_FORMATS)}")
+    b = 4 * FP4_BLOCK[format]
+    return -(-N // 128) * -(-K // b) * 512
+
+
+@dataclass(frozen=True)
+class FP4Matrix:
+    """A matrix of e2m1 codes with block scales on the GPU: codes uint8 [E * N, K / 2],
+    two a byte, low nibble first; scales uint8 [E * fp4_scale_bytes(N, K, format)], in
+    the order of include/w4a16.h; row_scale float32 [E * N] (format "nv"; None: 1).
+
+    ``fp4_quant`` makes one from bf16 rows, ``gated`` from gate and up rows of a
+    feed-forward block, ``from_rows`` from scales in row order (a checkpoint's)."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    row_scale: torch.Tensor | None
+    N: int
+    K: int
+    E: int = 1
+    format: str = "nv"
+
+    def __post_init__(self):
+        n = fp4_scale_bytes(self.N, self.K, self.format)
+        if self.K <= 0 or self.K % 32 or self.N < 0 or self.E < 1:
+            raise ValueError(f"N = {self.N}, K = {self.K} (a positive multiple of 32), E = {self.E}")
+        dev = _dev_tensor(self.codes, torch.uint8, "codes").get_device()
+        _dev_tensor(self.scales, torch.uint8, "scales")
+        if self.codes.numel() != self.E * self.N * (self.K // 2):
+            raise ValueError(f"codes must hold E * N * K / 2 = {self.E * self.N * (self.K // 2)} bytes")
+        if self.scales.numel() != self.E * n:
+            raise ValueError(f"scales must hold E * fp4_scale_bytes = {self.E * n} bytes")
+        _on_device(self.scales, "scales", dev)
+        if self.row_scale is not None:
+            _dev_tensor(self.row_scale, torch.float32, "row_scale")
+            if self.row_scale.numel() != self.E * self.N:
+                raise ValueError("row_scale must have one factor per row")
+            _on_device(self.row_scale, "row_scale", dev)
+        c = Fp4Struct(self.codes.data_ptr(), self.scales.data_ptr(), None if self.row_scale is None else self.row_scale.data_ptr(),
+                      self.N, self.K, self.E, FP4_FORMATS[self.format])
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ptr", ctypes.addressof(c))
+        object.__setattr__(self, "_dev", dev)
+
+    @classmethod
+    def empty(cls, N: int, K: int, E: int = 1, format: str = "nv", device="cuda") -> "FP4Matrix":
+        n = fp4_scale_bytes(N, K, format)
+        codes = torch.empty(E * N, K // 2, dtype=torch.uint8, device=device)
+        scales = torch.empty(E * n, dtype=torch.uint8, device=device)
+        f = torch.empty(E * N, dtype=torch.float32, device=device) if format == "nv" else None
+        return cls(codes, scales, f, N, K, E, format)
+
+    @classmethod
+    def gated(cls, gate: torch.Tensor, up: torch.Tensor, format: str = "nv", stream=None) -> "FP4Matrix":
+        """Gate and up weights (bf16 [F, K], or [E, F, K]) quantised into the one matrix of
+        2 F rows that ``fp4_gated`` takes: row 2 i is gate's row i, row 2 i + 1 up's."""
+        if gate.shape != up.shape or gate.dim() not in (2, 3):
+            raise ValueError("gate and up must both be [F, K] or [E, F, K]")
+        return fp4_quant(torch.stack((gate, up), -2).flatten(-3, -2), format, stream=stream)
+
+    @classmethod
+    def from_rows(cls, codes: torch.Tensor, scales: torch.Tensor, row_scale: torch.Tensor | None = None,
+                  format: str = "nv") -> "FP4Matrix":
+        """From codes uint8 [N, K / 2] or [E, N, K / 2] and scale bytes uint8 [.., N, K / block]
+        in row order; row_scale float32 [.., N], or one number for all rows."""
+        E, N, K = (1 if codes.dim() == 2 else codes.shape[0]), codes.shape[-2], 2 * codes.shape[-1]
+        fp4_scale_bytes(N, K, format)
+        nb = K // FP4_BLOCK[format]
+        if tuple(scales.shape) != tuple(codes.shape[:-1]) + (nb,) or scales.dtype is not torch.uint8:
+            raise ValueError(f"scales must be uint8 {tuple(codes.shape[:-1]) + (nb,)}")
+        rows, cols = -(-N // 128) * 128, -(-nb // 4) * 4
+        full = torch.zeros(E, rows, cols, dtype=torch.uint8, device=scales.device)
+        full[:, :N, :nb] = scales.view(E, N, nb)
+        tiled = full.view(E, rows // 128, 4, 32, cols // 4, 4).permute(0, 1, 4, 3, 2, 5).reshape(-1).contiguous()
+        if row_scale is not None:
+            row_scale = row_scale.to(torch.float32).expand(codes.shape[:-1]).reshape(-1).contiguous()
+        return cls(codes.reshape(E * N, K // 2), tiled, row_scale, N, K, E, format)
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.row_scale) if t is not None)
+
+
+def _fp4_x(x: torch.Tensor, K: int, dev: int | None):
+    """(rows, row stride) of bf16 activations [.., K]: dense rows, which may be apart where x is [M, K]."""
+    if not (isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16 and x.is_cuda):
+        _dev_tensor(x, torch.bfloat16, "x")
+    if x.dim() < 1 or x.shape[-1] != K:
+        raise ValueError(f"x must be [.., {K}] (got {tuple(x.shape)})")
+    if dev is not None and x.get_device() != dev:
+        _on_device(x, "x", dev)
+    if x.is_contiguous():
+        return x.numel() // K, K
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be contiguous, or [M, K] with contiguous rows")
+    return x.shape[0], x.stride(0) if x.shape[0] > 1 else K
+
+
+def fp4_quant(x: torch.Tensor, format: str = "nv", out: FP4Matrix | None = None, stream=None) -> FP4Matrix:
+    """Rows of x (bf16 [.., K]; [M, K] rows may be strided) as e2m1 codes and block scales
+    through ``w4a16_fp4_quant``.  A contiguous [E, N, K] is E experts of N rows."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or format not in FP4_FORMATS:
+        raise ValueError(f"x must be a tensor [.., K], format one of {sorted(FP4_FORMATS)}")
+    K = x.shape[-1]
+    if K <= 0 or K % 32:
+        raise ValueError(f"K = {K} must be a positive multiple of 32")
+    M, stride = _fp4_x(x, K, None)
+    E = x.shape[0] if x.dim() == 3 else 1
+    if out is None:
+        out = FP4Matrix.empty(M // max(E, 1), K, max(E, 1), format, x.device)
+    elif (out.N * out.E, out.K, out.format) != (M, K, format):
+        raise ValueError(f"out must have {M} rows of {K} codes, format {format}")
+    dev = x.get_device()
+    _on_device(out.codes, "out", dev)
+    rc = lib().w4a16_fp4_quant(x.data_ptr(), stride, out._ptr, _stream_on(stream, dev))
+    if rc:
+        _raise(rc)
+    return out
+
+
+def fp4_dequant(w: FP4Matrix, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of w as bf16 [N, K] (or [E, N, K]) through ``w4a16_fp4_dequant``."""
+    shape = (w.N, w.K) if w.E == 1 else (w.E, w.N, w.K)
+    raw = _stream_on(stream, w._dev)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=w.codes.device)
+    else:
+        _fp4_out(out, shape, w._dev)
+    rc = lib().w4a16_fp4_dequant(w._ptr, out.data_ptr(), raw)
+    if rc:
+        _raise(rc)
+    return out
+
+
+def _fp4_out(out: torch.Tensor, shape, dev: int) -> None:
+    _dev_tensor(out, torch.bfloat16, "out")
+    _on_device(out, "out", dev)
+    if out.numel() != math.prod(shape):
+        raise ValueError(f"out must be {tuple(shape)}")
+
+
+@functools.lru_cache(maxsize=1024)
+def _fp4_mm_bytes(M: int, K: int, format: int) -> int:
+    return int(lib().w4a16_fp4_mm_workspace_bytes(M, K, format))
+
+
+@functools.lru_cache(maxsize=1024)
+def _fp4_mm_id_bytes(*sizes: int) -> int:
+    return int(lib().w4a16_fp4_mm_id_workspace_bytes(*sizes))
+
+
+def _fp4_act(w: FP4Matrix, act) -> int:
+    if act not in FP4_ACTS:
+        raise ValueError(f"unknown activation {act!r}; one of {list(FP4_ACTS)}")
+    if act is not None and w.N % 2:
+        raise ValueError(f"N = {w.N}: gate and up rows come in pairs")
+    return FP4_ACTS[act]
+
+
+def _fp4_space(need: int, workspace, raw: int, stream, w: FP4Matrix):
+    """(tensor, address, bytes) of a call's workspace: the stream's own, or the given one."""
+    if workspace is not None:
+        _on_device(workspace, "workspace", w._dev)
+        return (workspace, *_ws_args(workspace))
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # the call's stream is the current one
+        t, at, n = _kv_workspace(need, raw, w.codes.device)
+    return t, at, n
+
+
+def _fp4_product(x, w: FP4Matrix, act, out, stream, workspace):
+    if w.E != 1:
+        raise ValueError("stacked experts: use fp4_mm_id")
+    a = _fp4_act(w, act)
+    cols = w.N if a == 0 else w.N // 2
+    raw = _stream_on(stream, w._dev)
+    if isinstance(x, FP4Matrix):
+        M, lead = x.N, (x.N,)
+        if x.K != w.K or x.format != w.format or x.E != 1:
+            raise ValueError(f"x has K={x.K}, format {x.format}, E={x.E}; weights have K={w.K}, format {w.format}")
+        _on_device(x.codes, "x", w._dev)
+    else:
+        M, stride = _fp4_x(x, w.K, w._dev)
+        lead = x.shape[:-1]
+    if out is None:
+        out = torch.empty((*lead, cols), dtype=torch.bfloat16, device=w.codes.device)
+    else:
+        _fp4_out(out, (M, cols), w._dev)
+    if isinstance(x, FP4Matrix):
+        rc = lib().w4a16_fp4_mm_q(x._ptr, w._ptr, out.data_ptr(), a, raw)
+    else:
+        keep, ws, wn = _fp4_space(_fp4_mm_bytes(M, w.K, w._c.format), workspace, raw, stream, w)
+        rc = lib().w4a16_fp4_mm(x.data_ptr(), stride, w._ptr, out.data_ptr(), M, a, ws, wn, raw)
+    if rc:
+        _raise(rc)
+    return out
+
+
+def fp4_mm(x, w: FP4Matrix, out: torch.Tensor | None = None, stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y[.., N] = x'[.., K] W^T in bf16 through ``w4a16_fp4_mm``: x bf16 (leading dims
+    flatten into rows; [M, K] rows may be strided), quantised row by row in w's format;
+    or an ``FP4Matrix`` already (``w4a16_fp4_mm_q``).  The workspace is this stream's,
+    kept by this module, unless one (uint8) is given."""
+    return _fp4_product(x, w, None, out, stream, workspace)
+
+
+def fp4_gated(x, w: FP4Matrix, act: str = "silu", out: torch.Tensor | None = None, stream=None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The first half of a gated feed-forward block: act(x' G^T) * (x' U^T), bf16 [.., N / 2],
+    over the interleaved rows of ``FP4Matrix.gated``; act "silu" or "gelu" (tanh form)."""
+    if act is None:
+        raise ValueError("fp4_gated needs an activation; fp4_mm has none")
+    return _fp4_product(x, w, act, out, stream, workspace)
+
+
+def fp4_mm_id(x: torch.Tensor, w: FP4Matrix, ids: torch.Tensor, act: str | None = None, out: torch.Tensor | None = None,
+              stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y[t, j] = W[ids[t, j]] x'[t] through ``w4a16_fp4_mm_id``: x bf16 [T, K], ids int32 [T, top]
+    (or [T]), y bf16 [T, top, N] (or [T, N]); with an ``act``, the gated form of each
+    expert, [.., N / 2].  An id outside 0..E-1 gives a row of zeros and raises DEVICE_BAD_ID."""
+    a = _fp4_act(w, act)
+    T, stride = _fp4_x(x, w.K, w._dev)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    ip = _i32(ids, "ids", None, w._dev)
+    if ids.dim() not in (1, 2) or ids.shape[0] != T or ids.dim() == 2 and ids.shape[1] < 1:
+        raise ValueError(f"ids must be [{T}, top] or [{T}]")
+    top = ids.shape[1] if ids.dim() == 2 else 1
+    shape = (*ids.shape, w.N if a == 0 else w.N // 2)
+    raw = _stream_on(stream, w._dev)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=w.codes.device)
+    else:
+        _fp4_out(out, shape, w._dev)
+    keep, ws, wn = _fp4_space(_fp4_mm_id_bytes(T, top, w.K, w.E, w._c.format), workspace, raw, stream, w)
+    rc = lib().w4a16_fp4_mm_id(x.data_ptr(), stride, w._ptr, ip, out.data_ptr(), T, top, a, ws, wn, raw)
     if rc:
         _raise(rc)
     return out
