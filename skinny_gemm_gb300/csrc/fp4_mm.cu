@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "fp4.cuh"
+#include "fp4_mm.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -35,7 +36,6 @@ namespace {
 using namespace ptx;
 
 constexpr int kWRows = 128;
-constexpr int kStageK = 256;                  // codes of K per stage: 128 bytes a row
 constexpr int kWTile = kWRows * 128;          // 16 KB
 constexpr int kScaleTile = 2048;              // scale atoms of a stage and 128 rows (mx: half of it)
 constexpr int kSets = 4;                      // scale sets in tensor memory
@@ -60,30 +60,8 @@ struct Maps {
   CUtensorMap x;  // u8 [x rows][K / 2], box 128 bytes x NT rows
 };
 
-struct Params {
-  const uint8_t* ws;
-  const uint8_t* xs;
-  const float* wf;
-  const float* xf;
-  uint16_t* y;
-  const Fp4Tile* tiles;
-  const int32_t* tile_count;
-  const int32_t* row;
-  int* flags;
-  int N, K, M, act;
-  int row_tiles, x_tiles;  // W row tiles of an expert; activation tiles (not routed)
-  int atoms, stages;       // scale atoms along K; stages along K
-  int early, fault_wait;
-};
-
-__device__ __forceinline__ float activate(float g, int act) {
-  if (act == W4A16_FP4_SILU) return __fdiv_rn(g, 1.0f + expf(-g));
-  const float u = 0.7978845608028654f * __fmaf_rn(0.044715f * g * g, g, g);
-  return 0.5f * g * (1.0f + tanhf(u));
-}
-
 template <int NT, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_constant__ Maps maps, Params p) {
+__global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_constant__ Maps maps, Fp4MmParams p) {
   using G = Geo<NT>;
   constexpr int S = G::kStages, NB = G::kAcc;
   constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;  // of a stage and 128 rows
@@ -194,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
         const uint64_t sw = umma_desc(SW_of(s), 128, 128, 0), sx = umma_desc(SX_of(s), 128, 128, 0);
         const uint64_t wd = umma_desc_sw128(W_of(s)), xd = umma_desc_sw128(X_of(s));
         const int atoms = min(kAtoms, p.atoms - k * kAtoms);
-        const int steps = min(4, (p.K - k * kStageK + 63) / 64);
+        const int steps = min(4, (p.K - k * kFp4StageK + 63) / 64);
 #pragma unroll
         for (int a = 0; a < kAtoms; ++a)
           if (a < atoms) {
@@ -255,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
             if (mine) p.y[m * p.N + row] = f32_to_bf16_bits(t);
           } else {
             const float up = __shfl_down_sync(0xffffffffu, t, 1);
-            if (mine && !(row & 1)) p.y[m * (p.N / 2) + row / 2] = f32_to_bf16_bits(activate(t, p.act) * up);
+            if (mine && !(row & 1)) p.y[m * (p.N / 2) + row / 2] = f32_to_bf16_bits(fp4_activate(t, p.act) * up);
           }
         }
       }
@@ -290,7 +268,7 @@ struct Device {
 Device g_dev[64];
 
 template <int NT, int FMT>
-cudaError_t launch_t(const Fp4MmArgs& a, const Params& p, int pdl, cudaStream_t s) {
+cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStream_t s) {
   using G = Geo<NT>;
   auto* fn = fp4_mm_kernel<NT, FMT>;
   constexpr int kIndex = (NT == 16 ? 0 : NT == 32 ? 1 : NT == 64 ? 2 : 3) * 2 + (FMT == W4A16_FP4_MX);
@@ -332,30 +310,12 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Params& p, int pdl, cudaStream_t 
 
 }  // namespace
 
-int fp4_mm_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+int fp4_mm_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
 cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   const int nt = a.tiles ? a.nt : fp4_mm_tile(a.M);
-  Params p;
-  p.ws = a.w.scales;
-  p.xs = a.xs;
-  p.wf = a.w.row_scale;
-  p.xf = a.xf;
-  p.y = a.y;
-  p.tiles = a.tiles;
-  p.tile_count = a.tile_count;
-  p.row = a.row;
-  p.flags = a.flags;
-  p.N = a.w.rows;
-  p.K = a.w.K;
-  p.M = a.M;
-  p.act = a.act;
-  p.row_tiles = (int)fp4_row_tiles(a.w.rows);
-  p.x_tiles = a.tiles ? 0 : (a.M + nt - 1) / nt;
-  p.atoms = fp4_atoms(a.w.K, a.w.format);
-  p.stages = (a.w.K + kStageK - 1) / kStageK;
-  p.early = a.early;
-  p.fault_wait = a.fault_wait;
+  if (nt == 256) return launch_fp4_pair(a, pdl, s);
+  const Fp4MmParams p = fp4_params(a, nt);
   const bool mx = a.w.format == W4A16_FP4_MX;
   switch (nt) {
     case 16: return mx ? launch_t<16, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<16, W4A16_FP4_NV>(a, p, pdl, s);

@@ -1,0 +1,61 @@
+// fp4_mm.cuh -- what the two product kernels of microscaled 4-bit matrices
+// (fp4_mm.cu, fp4_pair.cu) share.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "fp4.cuh"
+
+namespace w4a16 {
+
+constexpr int kFp4StageK = 256;  // codes of K per stage: 128 bytes a row
+
+struct Fp4MmParams {
+  const uint8_t* ws;  // scales and row factors (nullptr: 1) of W and of x
+  const uint8_t* xs;
+  const float* wf;
+  const float* xf;
+  uint16_t* y;
+  const Fp4Tile* tiles;  // routed, or nullptr
+  const int32_t* tile_count;
+  const int32_t* row;
+  int* flags;
+  int N, K, M, act;
+  int row_tiles, x_tiles;  // 128-row tiles of an expert's W; activation tiles (not routed)
+  int atoms, stages;       // scale atoms along K; stages along K
+  int fault_wait;
+};
+
+__device__ __forceinline__ float fp4_activate(float g, int act) {
+  if (act == W4A16_FP4_SILU) return __fdiv_rn(g, 1.0f + expf(-g));
+  const float u = 0.7978845608028654f * __fmaf_rn(0.044715f * g * g, g, g);
+  return 0.5f * g * (1.0f + tanhf(u));
+}
+
+inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
+  Fp4MmParams p;
+  p.ws = a.w.scales;
+  p.xs = a.xs;
+  p.wf = a.w.row_scale;
+  p.xf = a.xf;
+  p.y = a.y;
+  p.tiles = a.tiles;
+  p.tile_count = a.tile_count;
+  p.row = a.row;
+  p.flags = a.flags;
+  p.N = a.w.rows;
+  p.K = a.w.K;
+  p.M = a.M;
+  p.act = a.act;
+  p.row_tiles = (int)fp4_row_tiles(a.w.rows);
+  p.x_tiles = a.tiles ? 0 : (a.M + x_tile - 1) / x_tile;
+  p.atoms = fp4_atoms(a.w.K, a.w.format);
+  p.stages = (a.w.K + kFp4StageK - 1) / kFp4StageK;
+  p.fault_wait = a.fault_wait;
+  return p;
+}
+
+cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s);
+
+}  // namespace w4a16

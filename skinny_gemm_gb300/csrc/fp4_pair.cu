@@ -1,0 +1,410 @@
+// fp4_pair.cu -- the product of microscaled 4-bit matrices for many activation
+// rows: tiles of 256 rows of x by up to 256 rows of W on pairs of SMs.
+//
+// The arithmetic is fp4_mm.cu's.  Here x is the MMA's M: a tensor-memory lane
+// is a row of x and the columns run along y's row, so that a thread holds
+// neighbours of y (stores of 16 bytes; gate and up of a pair side by side).
+// tcgen05.mma.cta_group::2 multiplies 256 rows of x (128 in each CTA) with TN
+// rows of W (half of them in each CTA's shared memory): a CTA takes 38 KB from
+// L2 for each 128 x 256 x 256 products, half of what one alone would.
+//
+// CTA: ten warps, persistent over tiles.
+//   warp 0     TMA producer of this CTA's x and W rows and their scales
+//   warp 1     leader: scales from shared to tensor memory of both CTAs, MMAs
+//              and commits; the other CTA: passes "stage landed" on
+//   warps 2-9  epilogue: 32 lanes x half of the columns each
+// Tensor memory: two accumulators of 256 columns that share 96, beside two
+// sets of scales (48 columns each).  The epilogue reads the shared columns
+// first, and lets the next tile's MMAs go when it has them.
+// Waits are bounded as in fp4_mm.cu; the two CTAs leave together.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "fp4_mm.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace w4a16 {
+namespace {
+
+using namespace ptx;
+
+constexpr int kXTile = 128 * 128;  // 16 KB: this CTA's 128 rows of x
+constexpr int kWTile = 128 * 128;  // its half of W's rows (up to 128)
+constexpr int kXScale = 2048, kWScale = 4096;
+constexpr int kStage = kXTile + kWTile + kXScale + kWScale;
+constexpr int S = 5;
+constexpr int kEpi = 8;  // epilogue warps
+constexpr int kThreads = 32 * (2 + kEpi);
+constexpr int kSetCols = 48;                        // 4 atoms of x's scales (4 columns) and W's (8)
+constexpr int kAccStep = 160, kSetsAt = 416;        // the second accumulator's first column, the scales'
+constexpr int kBars = 3 * S + 6;
+constexpr int kSmem = S * kStage + kBars * 8 + 16 + 1024;
+static_assert(kSmem <= 227 * 1024 && kSetsAt + 2 * kSetCols <= 512, "a CTA's shared memory and the SM's tensor memory");
+
+struct Maps {
+  CUtensorMap w;  // u8 [experts * N][K / 2], box 128 bytes x TN / 2 rows, 128-byte swizzle
+  CUtensorMap x;  // u8 [x rows][K / 2], box 128 bytes x 128 rows
+};
+
+struct PairParams {
+  Fp4MmParams p;
+  int tn;       // rows of W per tile: 128, 192 or 256
+  int n_tiles;  // tiles along W's rows
+  int vec;      // y's rows take 16-byte stores
+};
+
+// Which tile a pair's unit is: eight activation tiles by all of W's, then the next eight, so that the pairs at work at a
+// time share what they read.
+__device__ __forceinline__ void unit_tile(int64_t u, int x_tiles, int n_tiles, int& xt, int& nt) {
+  const int64_t per = 8LL * n_tiles;
+  const int g = (int)(u / per), r = (int)(u % per);
+  const int wide = min(8, x_tiles - 8 * g);
+  xt = 8 * g + r % wide;
+  nt = r / wide;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_constant__ Maps maps, PairParams pp) {
+  constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;
+  const Fp4MmParams& p = pp.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t bars = sb + S * kStage;
+  auto X_of = [&](int s) { return sb + (uint32_t)(s * kStage); };
+  auto W_of = [&](int s) { return X_of(s) + kXTile; };
+  auto SX_of = [&](int s) { return W_of(s) + kWTile; };
+  auto SW_of = [&](int s) { return SX_of(s) + kXScale; };
+  auto full = [&](int s) { return bars + 8u * s; };            // this CTA's copies landed
+  auto empty = [&](int s) { return bars + 8u * (S + s); };     // the MMAs are done with it (both CTAs)
+  auto peer = [&](int s) { return bars + 8u * (2 * S + s); };  // leader: the other CTA's copies landed
+  auto acc_full = [&](int b) { return bars + 8u * (3 * S + b); };
+  auto acc_free = [&](int b) { return bars + 8u * (3 * S + 2 + b); };   // leader: all of it read, by both CTAs
+  auto part_free = [&](int b) { return bars + 8u * (3 * S + 4 + b); };  // leader: the shared columns read
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (bars - sb) + 8 * kBars);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1 + (p.fault_wait && blockIdx.x == 0 && s == 0));  // (debug: an arrival that never comes)
+      mbar_init(empty(s), 1);
+      mbar_init(peer(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_free(b), 2 * kEpi);
+      mbar_init(part_free(b), 2 * kEpi);
+    }
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc2(smem_u32(s_tmem), 512);
+    tmem_relinquish2();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after_sync();
+  const uint32_t tmem = *s_tmem;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int x_tiles = p.tiles ? *p.tile_count : p.x_tiles;
+  const int64_t units = (int64_t)x_tiles * pp.n_tiles;
+  const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int ns = p.stages, tn = pp.tn;
+  const uint32_t limit = p.fault_wait ? 4096u : 1u << 18;  // tries of a wait: about a second
+  auto timeout = [&]() {
+    atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
+    *s_abort = 1;
+  };
+  uint32_t it = 0;  // stages so far
+
+  if (warp == 0) {
+    // ---- TMA producer ----
+    if (lane == 0) {
+      const uint64_t keep = policy_evict_last();
+      for (int64_t u = first; u < units && !*s_abort; u += step) {
+        int xt, nt;
+        unit_tile(u, x_tiles, pp.n_tiles, xt, nt);
+        int64_t expert = 0;
+        int place = xt * 256;
+        if (p.tiles) {
+          expert = p.tiles[xt].expert;
+          place = p.tiles[xt].place;
+        }
+        place += 128 * (int)rank;
+        const int wrow = (int)(expert * p.N) + nt * tn + (int)rank * (tn / 2);
+        // 128-row tiles of W's scales that the tile's rows touch: one or two, fewer past the end
+        const int wt = nt * tn / 128, wtiles = min((nt * tn % 128 + tn + 127) / 128, p.row_tiles - wt);
+        const uint8_t* ws = p.ws + (expert * p.row_tiles + wt) * p.atoms * kFp4Atom;
+        const uint8_t* xs = p.xs + (int64_t)(place / kFp4Rows) * p.atoms * kFp4Atom;
+        // the last tile may have no rows of x in the second CTA, nor scales
+        const bool has_x = p.tiles || place < p.M;
+        for (int k = 0; k < ns; ++k, ++it) {
+          const int s = (int)(it % S);
+          if (it >= (uint32_t)S && !mbar_wait_parked(empty(s), ((it / S) - 1) & 1, 1000, limit)) {
+            timeout();
+            break;
+          }
+          const uint32_t bytes = (uint32_t)(min(kAtoms, p.atoms - k * kAtoms) * kFp4Atom);
+          mbar_expect_tx(full(s), kXTile + (uint32_t)(tn / 2) * 128 + ((has_x ? 1 : 0) + (uint32_t)wtiles) * bytes);
+          tma_load_2d(X_of(s), &maps.x, k * 128, place, full(s), keep);
+          tma_load_2d(W_of(s), &maps.w, k * 128, wrow, full(s), keep);
+          if (has_x) bulk_load(SX_of(s), xs + k * kAtoms * kFp4Atom, bytes, full(s), keep);
+          for (int i = 0; i < wtiles; ++i)
+            bulk_load(SW_of(s) + i * 2048, ws + ((int64_t)i * p.atoms + k * kAtoms) * kFp4Atom, bytes, full(s), keep);
+        }
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---- leader: scales and MMAs ----
+    const uint32_t go = elect_one();
+    const uint32_t idesc = umma_idesc_e2m1(256, tn, FMT == W4A16_FP4_MX);
+    uint32_t n = 0;  // tiles
+    for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
+      int xt, nt;
+      unit_tile(u, x_tiles, pp.n_tiles, xt, nt);
+      const int b = (int)(n & 1);
+      // this accumulator's last tile is read, and the columns it shares with the other's
+      if ((n >= 2 && !mbar_wait_cluster(acc_free(b), ((n >> 1) - 1) & 1, limit)) ||
+          (n >= 1 && !mbar_wait_cluster(part_free(b ^ 1), ((n - 1) >> 1) & 1, limit))) {
+        if (lane == 0) timeout();
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t acc = tmem + (uint32_t)(b * kAccStep);
+      const uint32_t w_col = (uint32_t)(nt * tn % 128 / 32);
+      bool ok = true;
+      for (int k = 0; k < ns; ++k, ++it) {
+        const int s = (int)(it % S);
+        const uint32_t set = tmem + (uint32_t)(kSetsAt + (int)(it & 1) * kSetCols);
+        const uint32_t before = it - 2;  // the set's last MMAs
+        ok = mbar_wait_warp(full(s), (it / S) & 1, limit) && mbar_wait_cluster(peer(s), (it / S) & 1, limit) &&
+             (it < 2 || mbar_wait_warp(empty((int)(before % S)), (before / S) & 1, limit));
+        if (!ok) {
+          if (lane == 0) timeout();
+          break;
+        }
+        tc_fence_after_sync();
+        const uint64_t sx = umma_desc(SX_of(s), 128, 128, 0), sw = umma_desc(SW_of(s), 128, 128, 0);
+        const uint64_t xd = umma_desc_sw128(X_of(s)), wd = umma_desc_sw128(W_of(s));
+        const int atoms = min(kAtoms, p.atoms - k * kAtoms);
+        const int steps = min(4, (p.K - k * kFp4StageK + 63) / 64);
+#pragma unroll
+        for (int a = 0; a < kAtoms; ++a)
+          if (a < atoms) {
+            tmem_copy_scales2(go, set + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
+            tmem_copy_scales2(go, set + 16 + 8 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
+            tmem_copy_scales2(go, set + 16 + 8 * a + 4, sw + (uint64_t)((2048 + a * kFp4Atom) >> 4));
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < steps) {
+            if (FMT == W4A16_FP4_MX)
+              umma2_mxf4(go, acc, xd + 2 * j, wd + 2 * j, idesc | umma_idesc_scale_byte(2 * (j & 1)), set + 4 * (j / 2),
+                         set + 16 + 8 * (j / 2) + w_col, k > 0 || j > 0);
+            else
+              umma2_nvf4(go, acc, xd + 2 * j, wd + 2 * j, idesc, set + 4 * j, set + 16 + 8 * j + w_col, k > 0 || j > 0);
+          }
+        umma_commit2_if(go, empty(s));
+      }
+      if (!ok) break;
+      umma_commit2_if(go, acc_full(b));
+    }
+  } else if (warp == 1) {
+    // ---- the other CTA: its stages landed ----
+    const uint32_t to = cluster_map(bars, 0) - bars;
+    for (int64_t u = first; u < units && !*s_abort; u += step) {
+      bool ok = true;
+      for (int k = 0; k < ns; ++k, ++it) {
+        const int s = (int)(it % S);
+        if (!(ok = mbar_wait_warp(full(s), (it / S) & 1, limit))) break;
+        if (lane == 0) mbar_arrive_cluster(peer(s) + to);
+      }
+      if (!ok) {
+        if (lane == 0) timeout();
+        break;
+      }
+    }
+  } else {
+    // ---- epilogue ----
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t to = cluster_map(bars, 0) - bars;
+    uint32_t n = 0;
+    for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
+      int xt, nt;
+      unit_tile(u, x_tiles, pp.n_tiles, xt, nt);
+      const int b = (int)(n & 1);
+      int64_t expert = 0;
+      int place = xt * 256, count = p.M - place;
+      if (p.tiles) {
+        expert = p.tiles[xt].expert;
+        place = p.tiles[xt].place;
+        count = p.tiles[xt].count;
+      }
+      const int r = 128 * (int)rank + 32 * q + lane;
+      const bool mine = r < count;
+      const int64_t m = mine ? (p.row ? p.row[place + r] : place + r) : 0;
+      const float fx = mine && p.xf ? p.xf[place + r] : 1.0f;
+      const float* wf = p.wf ? p.wf + expert * p.N : nullptr;
+      const int64_t cols = p.act == W4A16_FP4_LINEAR ? p.N : p.N / 2;
+      if (!mbar_wait_warp(acc_full(b), (n >> 1) & 1, limit)) {
+        if (lane == 0) timeout();
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t acc = tmem + (uint32_t)(b * kAccStep) + ((uint32_t)(32 * q) << 16);
+      // columns 160 .. 255 of tensor memory are both accumulators': 16 at a time, those first.  Accumulator 0 has them
+      // last and accumulator 1 first; the warps' halves take every other 16.
+      for (int i = half; i < 16; i += 2) {
+        const int c = 16 * (b ? i : (i + 10) % 16);
+        if (c < tn) {
+          float v[16];
+          tmem_ld16(acc + c, v);
+          tmem_wait_ld();
+          const int n0 = nt * tn + c;
+          if (mine && n0 < p.N) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] *= fx;
+            if (wf) {
+              if (n0 + 16 <= p.N) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] *= wf[n0 + j];
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (n0 + j < p.N) v[j] *= wf[n0 + j];
+              }
+            }
+            if (p.act == W4A16_FP4_LINEAR) {
+              uint16_t* y = p.y + m * cols + n0;
+              if (pp.vec && n0 + 16 <= p.N) {
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  o[j] = (uint32_t)f32_to_bf16_bits(v[2 * j]) | (uint32_t)f32_to_bf16_bits(v[2 * j + 1]) << 16;
+                *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(y + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (n0 + j < p.N) y[j] = f32_to_bf16_bits(v[j]);
+              }
+            } else {
+              uint16_t* y = p.y + m * cols + n0 / 2;
+              float h[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) h[j] = fp4_activate(v[2 * j], p.act) * v[2 * j + 1];
+              if (pp.vec && n0 + 16 <= p.N) {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  o[j] = (uint32_t)f32_to_bf16_bits(h[2 * j]) | (uint32_t)f32_to_bf16_bits(h[2 * j + 1]) << 16;
+                *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (n0 + 2 * j < p.N) y[j] = f32_to_bf16_bits(h[j]);
+              }
+            }
+          }
+        }
+        if (i >= 4 && i < 6) {  // columns of the first six have been read by this warp (three of its own)
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(part_free(b) + to);
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_free(b) + to);
+    }
+  }
+
+  // ---- teardown: everything in flight lands before the memories are released ----
+  __syncthreads();
+  if (*s_abort) {
+    if (warp == 0 && lane == 0)
+      for (uint32_t i = it > (uint32_t)S ? it - S : 0; i < it; ++i) mbar_wait_parked(full((int)(i % S)), (i / S) & 1, 1000, limit);
+    if (warp == 1 && rank == 0 && it > 0) mbar_wait_warp(empty((int)((it - 1) % S)), ((it - 1) / S) & 1, limit);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_arrive();  // the other CTA's memories are read by this one's MMAs, and barriers here written by it
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc2(tmem, 512);
+  }
+}
+
+// ---- host side ------------------------------------------------------------------------
+
+std::mutex g_mu;
+int g_sms[64] = {};
+bool g_attr[64][2] = {};
+
+template <int FMT>
+cudaError_t launch_t(const Fp4MmArgs& a, const PairParams& p, int64_t units, int pdl, cudaStream_t s) {
+  auto* fn = fp4_pair_kernel<FMT>;
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int sms;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_sms[dev])
+      if (cudaError_t e = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev)) return e;
+    bool& done = g_attr[dev][FMT == W4A16_FP4_MX];
+    if (!done) {
+      if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
+      done = true;
+    }
+    sms = g_sms[dev];
+  }
+  Maps maps;
+  if (cudaError_t e = encode_map_2d(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w.codes, a.w.K / 2, (int64_t)a.w.rows * a.w.experts,
+                                    a.w.K / 2, 128, p.tn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+    return e;
+  if (cudaError_t e = encode_map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.xc, a.w.K / 2, a.x_rows, a.w.K / 2, 128, 128,
+                                    CU_TENSOR_MAP_SWIZZLE_128B))
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (units < sms / 2 ? units : sms / 2)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, maps, p);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
+  PairParams p;
+  p.p = fp4_params(a, 256);
+  p.tn = 256;
+  p.n_tiles = (a.w.rows + p.tn - 1) / p.tn;
+  const int cols = a.act == W4A16_FP4_LINEAR ? a.w.rows : a.w.rows / 2;
+  p.vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+  const int64_t units = (int64_t)p.n_tiles * (a.tiles ? a.max_tiles : p.p.x_tiles);
+  return a.w.format == W4A16_FP4_MX ? launch_t<W4A16_FP4_MX>(a, p, units, pdl, s) : launch_t<W4A16_FP4_NV>(a, p, units, pdl, s);
+}
+
+}  // namespace w4a16

@@ -384,6 +384,65 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t go, uint32_t taddr, ui
       : "memory");
 }
 
+// ---- pairs of CTAs (cta_group::2): one thread of the even CTA issues for both;
+// each has half of A's rows, half of B's and all of B's scales, at the same
+// shared-memory offsets, and 128 rows of D ----
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void umma2_nvf4(uint32_t go, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t a_scale, uint32_t b_scale, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %6, 0; setp.ne.b32 q, %7, 0;\n"
+      "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p; }"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"((uint32_t)accumulate), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void umma2_mxf4(uint32_t go, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t a_scale, uint32_t b_scale, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %6, 0; setp.ne.b32 q, %7, 0;\n"
+      "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"((uint32_t)accumulate), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_copy_scales2(uint32_t go, uint32_t taddr, uint64_t sdesc) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %2, 0;\n"
+      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1; }" ::"r"(taddr), "l"(sdesc), "r"(go)
+      : "memory");
+}
+// One arrival on the barrier at this offset of both CTAs.
+__device__ __forceinline__ void umma_commit2_if(uint32_t go, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; .reg .b16 m; setp.ne.b32 q, %1, 0; mov.b16 m, 3;\n"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m; }" ::"r"(bar), "r"(go)
+      : "memory");
+}
+// An arrival on a barrier of another CTA of the cluster (a cluster_map address), and
+// the wait for such arrivals.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint32_t limit = kWaitLimit) {
+  uint32_t ok = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; !ok && i < limit; ++i)
+    asm volatile(
+        "{ .reg .pred p, q; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
+        "vote.sync.all.pred q, p, 0xffffffff; selp.u32 %0, 1, 0, q; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  return ok;
+}
+
 __device__ __forceinline__ void umma_commit_if(uint32_t go, uint32_t bar) {
   asm volatile(
       "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"

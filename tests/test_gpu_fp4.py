@@ -192,3 +192,29 @@ def test_empty_and_out():
     assert (guard[0] == 3).all() and (guard[5] == 3).all() and torch.equal(guard[1:5], ops.fp4_mm(x, w))
     x3 = x.view(2, 2, 64)
     assert torch.equal(ops.fp4_mm(x3, w).view(4, 100), guard[1:5])
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("M,N,K", [(256, 256, 256), (256, 256, 512), (130, 100, 96), (257, 520, 2304), (1000, 1300, 320), (2100, 2570, 64), (600, 4104, 2816)])
+def test_mm_many_rows(fmt, M, N, K):
+    """The pair kernel: one tile, ragged edges of both sides, several tiles a pair."""
+    from skinny_gemm_gb300 import ops
+
+    x, w, xv, wv = product(ops, fmt, M, N, K)
+    y = ops.fp4_mm(x, w)
+    assert ops.device_status() == 0
+    want = xv @ wv.T
+    check(y, want, fc.product_bound(want, xv, wv))
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gated_many_rows(fmt, act):
+    from skinny_gemm_gb300 import ops
+
+    for M, F, K in ((300, 200, 288), (700, 1111, 96)):
+        x, w, xv, wv = product(ops, fmt, M, 2 * F, K, act)
+        y = ops.fp4_gated(x, w, act)
+        assert ops.device_status() == 0
+        gate, up = xv @ wv[0::2].T, xv @ wv[1::2].T
+        check(y, fc.act64(gate, act) * up, fc.gated_bound(gate, up, xv, wv[0::2], wv[1::2], act))
