@@ -471,7 +471,8 @@ size_t w4a16_fp4_scale_bytes(int rows, int K, int format);
  *   mx  scale = 2^e, e = max(floor(log2 p) - 2, -127)
  *   nv  row_scale = f, the smallest power of two >= 2^-126 with q <= 6 * 448 f;
  *       scale = e4m3(p / f / 6), to nearest even; a block of scale 0 has codes +0
- *   code = e2m1(x / scale [/ f]), to nearest, ties to the even code, at most 6
+ *   code = e2m1(x / scale [/ f]), to nearest, ties to the even code, at most 6;
+ *          a code of 0 may have either sign
  * A block with a NaN or an infinity gets a NaN scale and codes 0; q is over a
  * row's finite values.  Zero rows is a no-op. */
 int w4a16_fp4_quant(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* out, void* stream);

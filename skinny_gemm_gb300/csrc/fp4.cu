@@ -7,6 +7,7 @@
 //       smallest power of two (at least 2^-126) with max |x| of the row
 //       <= 6 * 448 f;  s = e4m3(max |x| of the block / f / 6)
 // and code = e2m1(x / scale), to nearest, ties to the even code, at most 6.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -32,7 +33,7 @@ cudaError_t launch(const void* fn, dim3 grid, int threads, void** args, int pdl,
 }
 
 // Eight values to eight codes, value i in bits 4 i.
-__device__ __forceinline__ uint32_t codes8(const float (&y)[8]) {
+__device__ __forceinline__ uint32_t codes8(const float* y) {
   uint32_t d;
   asm("{ .reg .b8 a, b, c, e;\n"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
@@ -44,6 +45,13 @@ __device__ __forceinline__ uint32_t codes8(const float (&y)[8]) {
       : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return d;
 }
+
+// Sixteen bf16 values, 32 bytes.
+struct Vec16 {
+  uint4 a, b;
+};
+__device__ __forceinline__ Vec16 load16(const uint16_t* p) { return Vec16{ld_nc_v4(p), ld_nc_v4(p + 8)}; }
+__device__ __forceinline__ Vec16 zero16() { return Vec16{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
 
 // The largest |x| of eight bf16 values as bits (bf16 magnitudes order like integers).
 __device__ __forceinline__ uint32_t peak8(const uint4& v) {
@@ -75,118 +83,219 @@ __device__ __forceinline__ int factor_exp(uint32_t peak) {
   return max(e, -126);
 }
 
+__device__ __forceinline__ uint32_t peak16(const Vec16& v) { return max(peak8(v.a), peak8(v.b)); }
+__device__ __forceinline__ uint32_t finite_peak16(const Vec16& v) { return max(finite_peak8(v.a), finite_peak8(v.b)); }
+
+__device__ __forceinline__ float rcp(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// Two sums a b + c at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 a, a, b, c; mov.b64 {%0, %1}, a; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 constexpr int kQuantThreads = 256;
 
-// One CTA a row.  A thread takes eight values (16 bytes) at a time; two (nv) or four (mx) neighbours hold a block.
+// Sixteen values to codes and their block's scale byte; peak is the block's largest |x| (bf16 bits).
+//
+// nv.  The codes depend on which side of a border (a multiple of 1/4 up to 5) the quotient y = x / (s f) lies, ties
+// included.  x has 8 significant bits and s 4, so that a y that is not on a border is at least 2^-10 from it.  x times an
+// approximate reciprocal is off by 2^-20 at most; rounded to a multiple of 2^-12 (by adding and taking off 1.5 * 2^11) it is
+// on a border where y is, and on y's side of it elsewhere.  The same for the scale: p / f / 6 against the borders of
+// e4m3, 5 significant bits: at least 2^-9 of it away, or on it; kept to 2^-16 of it.
 template <int FMT>
-__global__ void __launch_bounds__(kQuantThreads) fp4_quant_kernel(Fp4QuantArgs p) {
-  constexpr int kLanes = FMT == W4A16_FP4_MX ? 4 : 2;
-  const int tid = threadIdx.x, chunks = p.K / 8;
-  const int r = blockIdx.x;
+__device__ __forceinline__ uint2 block16(const Vec16& v, uint32_t peak, int e, uint32_t& byte) {
+  float y[16];
+  widen8(v.a, y);
+  widen8(v.b, y + 8);
+  if (FMT == W4A16_FP4_MX) {
+    // floor(log2 peak) - 2 + 127 is the exponent field less 2; a subnormal peak gives 0
+    byte = max((int)(peak >> 7) - 2, 0);
+    const float s = exp2i(127 - (int)byte);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], s);
+    if (peak >= 0x7F80u) byte = 0xFFu;
+  } else {
+    const float p = __fmul_rn(bf16_bits_to_f32((uint16_t)peak), exp2i(-e));
+    const float want = __uint_as_float((__float_as_uint(__fmul_rn(p, 1.0f / 6.0f)) + 64u) & ~127u);
+    uint16_t pair;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.0f), "f"(want));
+    byte = pair & 0xFFu;
+    // the scale in fp32: e4m3's bits at half the place of fp32's, times 2^120
+    float s = __fmul_rn(__uint_as_float(byte << 20), exp2i(120));
+    if (e < -90) {  // s f might leave fp32's normal range
+      const float inv = exp2i(-e);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], inv);
+    } else {
+      s = __fmul_rn(s, exp2i(e));
+    }
+    const float r = byte ? rcp(s) : 0.0f;
+    const float2 rr = make_float2(r, r), up = make_float2(3072.0f, 3072.0f), down = make_float2(-3072.0f, -3072.0f);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float2 q = add2(fma2(make_float2(y[i], y[i + 1]), rr, up), down);
+      y[i] = q.x;
+      y[i + 1] = q.y;
+    }
+    if (peak >= 0x7F80u) byte = 0x7Fu;
+  }
+  if (peak >= 0x7F80u) return make_uint2(0, 0);
+  return make_uint2(codes8(y), codes8(y + 8));
+}
+
+// TPR threads a row, which hold up to C x TPR units of sixteen values (32 bytes) in registers between the row's peak and
+// its codes; longer rows are read again.  A thread has a whole nv block, two neighbours an mx one.  What bounds it is HBM
+// (2 bytes a value in, 0.56 out) for many rows, and a load, the row's reduction and the launch for few.
+template <int FMT, int TPR, int C>
+__global__ void __launch_bounds__(kQuantThreads, 3) fp4_quant_kernel(Fp4QuantArgs p) {
+  constexpr int kWarps = TPR / 32, kRows = kQuantThreads / TPR;
+  constexpr int kWord = FMT == W4A16_FP4_MX ? 8 : 4;  // units of an atom's word of four scales
+  const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR, units = p.K / 16;
+  const int64_t r = (int64_t)blockIdx.x * kRows + group;
+  const bool live = r < p.rows;
   __shared__ uint32_t s_peak[kQuantThreads / 32];
   pdl_wait();
   pdl_launch_dependents();  // (not before: what the next kernel reads early is then complete)
-  const uint16_t* x = p.x + (int64_t)r * p.x_stride;
+  const uint16_t* x = p.x + (live ? r : 0) * p.x_stride;
+  Vec16 v[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = i * TPR + tid;
+    v[i] = c < units ? load16(x + 16 * (int64_t)c) : zero16();
+  }
   int e = 0;
   if (FMT == W4A16_FP4_NV) {
-    uint32_t peak = 0;
-    for (int c = tid; c < chunks; c += kQuantThreads) peak = max(peak, finite_peak8(*reinterpret_cast<const uint4*>(x + 8 * c)));
-    peak = __reduce_max_sync(0xffffffffu, peak);
-    if ((tid & 31) == 0) s_peak[tid >> 5] = peak;
-    __syncthreads();
+    auto over_row = [&](uint32_t peak) {
+      peak = __reduce_max_sync(0xffffffffu, peak);
+      if (kWarps > 1) {
+        if ((threadIdx.x & 31) == 0) s_peak[threadIdx.x >> 5] = peak;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQuantThreads / 32; ++i) peak = max(peak, s_peak[i]);
+        for (int i = 0; i < kWarps; ++i) peak = max(peak, s_peak[group * kWarps + i]);
+        __syncthreads();
+      }
+      return peak;
+    };
+    uint32_t peak = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) peak = max(peak, peak16(v[i]));
+    for (int c = C * TPR + tid; c < units; c += TPR) peak = max(peak, peak16(load16(x + 16 * (int64_t)c)));
+    peak = over_row(peak);
+    // (a row with a NaN or an infinity, rare: all of the CTA's threads take part in the second reduction)
+    if (kWarps > 1 ? __syncthreads_or(peak >= 0x7F80u) : peak >= 0x7F80u) {
+      peak = 0;
+#pragma unroll
+      for (int i = 0; i < C; ++i) peak = max(peak, finite_peak16(v[i]));
+      for (int c = C * TPR + tid; c < units; c += TPR) peak = max(peak, finite_peak16(load16(x + 16 * (int64_t)c)));
+      peak = over_row(peak);
+    }
     e = factor_exp(peak);
   }
-  const float inv = exp2i(-e);
-  const int atoms = fp4_atoms(p.K, FMT);
+  if (!live) return;
+  const int atoms = fp4_atoms(p.K, FMT), all = atoms * kWord;  // units with those past K that fill the last atom
   for (int j = 0; j < (p.place ? p.top : 1); ++j) {
-    int64_t at = r;
-    int64_t tile = (int64_t)(r / p.group) * fp4_row_tiles(p.group) + r % p.group / kFp4Rows;
-    int lane_row = r % p.group % kFp4Rows;
+    int64_t at = r, tile;
+    int lane_row;
     if (p.place) {
-      at = p.place[(int64_t)r * p.top + j];
+      at = p.place[r * p.top + j];
       if (at < 0) {  // no such expert: a row of zeros
-        uint16_t* y = p.y + ((int64_t)r * p.top + j) * p.y_row;
-        for (int64_t i = tid; i < p.y_row; i += kQuantThreads) y[i] = 0;
+        uint16_t* y = p.y + (r * p.top + j) * p.y_row;
+        for (int64_t i = tid; i < p.y_row; i += TPR) y[i] = 0;
         continue;
       }
       tile = at / kFp4Rows;
       lane_row = (int)(at % kFp4Rows);
+    } else {
+      const int n = (int)(r % p.group);
+      tile = r / p.group * fp4_row_tiles(p.group) + n / kFp4Rows;
+      lane_row = n % kFp4Rows;
     }
-    uint32_t* codes = reinterpret_cast<uint32_t*>(p.codes + at * (p.K / 2));
+    uint2* codes = reinterpret_cast<uint2*>(p.codes + at * (p.K / 2));
     uint8_t* scales = p.scales + tile * atoms * kFp4Atom + 16 * (lane_row & 31) + 4 * (lane_row >> 5);
     if (FMT == W4A16_FP4_NV && tid == 0) p.row_scale[at] = exp2i(e);
-    // whole warps: blocks past K, up to the last atom's end, get scale 0
-    for (int c0 = 0; c0 < atoms * 4 * kLanes; c0 += kQuantThreads) {
+    auto write = [&](int c, const Vec16& w) {  // (whole warps)
+      uint32_t peak = peak16(w);
+      if (FMT == W4A16_FP4_MX) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+      uint32_t byte;
+      const uint2 code = block16<FMT>(w, peak, e, byte);
+      if (c < units) codes[c] = code;
+      uint32_t word = byte << (8 * (FMT == W4A16_FP4_MX ? c / 2 % 4 : c % 4));
+      word |= __shfl_xor_sync(0xffffffffu, word, kWord / 4);
+      word |= __shfl_xor_sync(0xffffffffu, word, kWord / 2);
+      if (c < all && c % kWord == 0) *reinterpret_cast<uint32_t*>(scales + (int64_t)(c / kWord) * kFp4Atom) = word;
+    };
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i * TPR < all) write(i * TPR + tid, v[i]);
+    for (int c0 = C * TPR; c0 < all; c0 += TPR) {
       const int c = c0 + tid;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (c < chunks) v = *reinterpret_cast<const uint4*>(x + 8 * c);
-      uint32_t peak = peak8(v);
-#pragma unroll
-      for (int d = 1; d < kLanes; d *= 2) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, d));
-      float y[8];
-      widen8(v, y);
-      uint32_t byte, code;
-      if (FMT == W4A16_FP4_MX) {
-        // floor(log2 peak) - 2 + 127 is the exponent field less 2; a subnormal peak gives 0
-        byte = max((int)(peak >> 7) - 2, 0);
-        const float s = exp2i(127 - (int)byte);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(y[i], s);
-        code = codes8(y);
-        if (peak >= 0x7F80u) byte = 0xFFu, code = 0;
-      } else {
-        const float want = __fdiv_rn(__fmul_rn(bf16_bits_to_f32((uint16_t)peak), inv), 6.0f);
-        uint16_t pair;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.0f), "f"(want));
-        byte = pair & 0xFFu;
-        // s back in fp32: e4m3's bits at half the place of fp32's, times 2^120
-        const float s = __fmul_rn(__uint_as_float(byte << 20), exp2i(120));
-        if (byte == 0) {
-          code = 0;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(__fmul_rn(y[i], inv), s);
-          code = codes8(y);
-        }
-        if (peak >= 0x7F80u) byte = 0x7Fu, code = 0;
-      }
-      if (c < chunks) codes[c] = code;
-      if (c < atoms * 4 * kLanes && c % kLanes == 0) {
-        const int b = c / kLanes;
-        scales[(int64_t)(b / 4) * kFp4Atom + b % 4] = (uint8_t)byte;
-      }
+      write(c, c < units ? load16(x + 16 * (int64_t)c) : zero16());
     }
   }
 }
 
-// One CTA a row, eight values a thread: value = bf16(code * scale * factor), exact unless it leaves bf16's range.
-__global__ void __launch_bounds__(kQuantThreads) fp4_dequant_kernel(w4a16_fp4 w, uint16_t* y) {
+// Units of sixteen values: value = bf16(code * scale * factor), exact unless it leaves bf16's range.  code * scale is
+// exact in fp16 for nv (6 significant bits, 2^-10 to 2688).
+constexpr int kBack = 2;  // units a thread
+
+__global__ void __launch_bounds__(kQuantThreads) fp4_dequant_kernel(w4a16_fp4 w, uint16_t* y, int parts) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t r = blockIdx.x;
-  const int atoms = fp4_atoms(w.K, w.format), lanes = fp4_block(w.format) / 8;
+  const int64_t r = blockIdx.x / parts;
+  const int part = (int)(blockIdx.x % parts);
+  const bool mx = w.format == W4A16_FP4_MX;
+  const int atoms = fp4_atoms(w.K, w.format), units = w.K / 16;
   const int64_t n = r % w.rows, tile = r / w.rows * fp4_row_tiles(w.rows) + n / kFp4Rows;
   const uint8_t* scales = w.scales + tile * atoms * kFp4Atom + 16 * (n & 31) + 4 * (n % kFp4Rows >> 5);
-  const float f = w.row_scale ? w.row_scale[r] : 1.0f;
-  for (int c = threadIdx.x; c < w.K / 8; c += kQuantThreads) {
-    const uint32_t code = *reinterpret_cast<const uint32_t*>(w.codes + r * (w.K / 2) + 4 * c);
-    const int b = c / lanes;
-    const uint32_t byte = scales[(int64_t)(b / 4) * kFp4Atom + b % 4];
-    float s;
-    if (w.format == W4A16_FP4_MX) s = byte == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte - 127);
-    else s = (byte & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte & 0x7Fu) << 20 | (byte & 0x80u) << 24), exp2i(120));
-    uint32_t out[4];
+  const float factor = w.row_scale ? w.row_scale[r] : 1.0f;
+  uint2 code[kBack];
+  uint32_t byte[kBack];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t pair;
-      asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(pair) : "r"(code >> (8 * i)));
-      const __half2 h = *reinterpret_cast<const __half2*>(&pair);
-      const float lo = __fmul_rn(__fmul_rn(__low2float(h), s), f), hi = __fmul_rn(__fmul_rn(__high2float(h), s), f);
-      out[i] = (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+  for (int i = 0; i < kBack; ++i) {
+    const int c = (part * kBack + i) * kQuantThreads + threadIdx.x, b = mx ? c / 2 : c;
+    code[i] = make_uint2(0, 0);
+    byte[i] = 0;
+    if (c < units) {
+      code[i] = *reinterpret_cast<const uint2*>(w.codes + r * (w.K / 2) + 8 * (int64_t)c);
+      byte[i] = scales[(int64_t)(b / 4) * kFp4Atom + b % 4];
     }
-    *reinterpret_cast<uint4*>(y + r * w.K + 8 * c) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < kBack; ++i) {
+    const int c = (part * kBack + i) * kQuantThreads + threadIdx.x;
+    if (c >= units) break;
+    float s = 1.0f, f = factor;
+    if (mx) f = __fmul_rn(byte[i] == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte[i] - 127), factor);
+    else s = (byte[i] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte[i] & 0x7Fu) << 20 | (byte[i] & 0x80u) << 24), exp2i(120));
+    const __half2 sh = __float2half2_rn(s);
+    uint32_t out[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t pair;
+      asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(pair) : "r"((k < 4 ? code[i].x : code[i].y) >> (8 * (k % 4))));
+      const float2 h = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&pair), sh));
+      const __nv_bfloat162 o = __floats2bfloat162_rn(__fmul_rn(h.x, f), __fmul_rn(h.y, f));
+      out[k] = *reinterpret_cast<const uint32_t*>(&o);
+    }
+    uint4* to = reinterpret_cast<uint4*>(y + r * w.K + 16 * (int64_t)c);
+    to[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    to[1] = make_uint4(out[4], out[5], out[6], out[7]);
   }
 }
 
@@ -250,15 +359,38 @@ __global__ void __launch_bounds__(kRouteThreads) fp4_route_kernel(Fp4RouteArgs p
 
 }  // namespace
 
-cudaError_t launch_fp4_quant(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
+namespace {
+
+template <int FMT, int TPR, int C>
+cudaError_t quant_t(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
   void* args[] = {const_cast<Fp4QuantArgs*>(&a)};
-  const void* fn = a.format == W4A16_FP4_MX ? (const void*)fp4_quant_kernel<W4A16_FP4_MX> : (const void*)fp4_quant_kernel<W4A16_FP4_NV>;
-  return launch(fn, dim3((unsigned)a.rows), kQuantThreads, args, pdl, s);
+  constexpr int kRows = kQuantThreads / TPR;
+  return launch((const void*)fp4_quant_kernel<FMT, TPR, C>, dim3((unsigned)((a.rows + kRows - 1) / kRows)), kQuantThreads, args, pdl, s);
+}
+
+template <int FMT>
+cudaError_t quant_f(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
+  // few rows: as many threads as units, for the latency; many: up to four units a thread in flight
+  const int units = a.K / 16;
+  if (a.rows <= 152) return units <= 256 ? quant_t<FMT, 256, 1>(a, pdl, s) : quant_t<FMT, 256, 4>(a, pdl, s);
+  if (units <= 128) return quant_t<FMT, 32, 4>(a, pdl, s);
+  if (units <= 256) return quant_t<FMT, 64, 4>(a, pdl, s);
+  if (units <= 512) return quant_t<FMT, 128, 4>(a, pdl, s);
+  return quant_t<FMT, 256, 4>(a, pdl, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_quant(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
+  return a.format == W4A16_FP4_MX ? quant_f<W4A16_FP4_MX>(a, pdl, s) : quant_f<W4A16_FP4_NV>(a, pdl, s);
 }
 
 cudaError_t launch_fp4_dequant(const w4a16_fp4& w, uint16_t* y, int pdl, cudaStream_t s) {
-  void* args[] = {const_cast<w4a16_fp4*>(&w), &y};
-  return launch((const void*)fp4_dequant_kernel, dim3((unsigned)(w.rows * w.experts)), kQuantThreads, args, pdl, s);
+  int parts = (w.K / 16 + kBack * kQuantThreads - 1) / (kBack * kQuantThreads);
+  void* args[] = {const_cast<w4a16_fp4*>(&w), &y, &parts};
+  const int64_t ctas = (int64_t)w.rows * w.experts * parts;
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch((const void*)fp4_dequant_kernel, dim3((unsigned)ctas), kQuantThreads, args, pdl, s);
 }
 
 cudaError_t launch_fp4_route(const Fp4RouteArgs& a, int pdl, cudaStream_t s) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "fp4.cuh"
@@ -27,10 +28,17 @@ struct Fp4MmParams {
   int fault_wait;
 };
 
+// Both activations are g / (1 + exp(-t)): t = g, and for the tanh form of gelu, as (1 + tanh u) / 2 = 1 / (1 + exp(-2u)),
+// t = 2 sqrt(2 / pi) (g + 0.044715 g^3).  exp by the hardware's 2^x (2 ulp) and the division by its reciprocal: some
+// 2^-22 of |g| off, the output keeps 2^-8.
 __device__ __forceinline__ float fp4_activate(float g, int act) {
-  if (act == W4A16_FP4_SILU) return __fdiv_rn(g, 1.0f + expf(-g));
-  const float u = 0.7978845608028654f * __fmaf_rn(0.044715f * g * g, g, g);
-  return 0.5f * g * (1.0f + tanhf(u));
+  const float t = act == W4A16_FP4_SILU ? g : 1.5957691216057308f * __fmaf_rn(0.044715f * g * g, g, g);
+  return __fdividef(g, 1.0f + __expf(-t));
+}
+
+__device__ __forceinline__ uint32_t fp4_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {

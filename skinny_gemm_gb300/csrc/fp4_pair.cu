@@ -13,9 +13,11 @@
 //   warp 1     leader: scales from shared to tensor memory of both CTAs, MMAs
 //              and commits; the other CTA: passes "stage landed" on
 //   warps 2-9  epilogue: 32 lanes x half of the columns each
-// Tensor memory: two accumulators of 256 columns that share 96, beside two
-// sets of scales (48 columns each).  The epilogue reads the shared columns
-// first, and lets the next tile's MMAs go when it has them.
+// Tensor memory: two accumulators of 256 columns that share 160, beside three
+// sets of scales (48 columns each; a set is written again when the MMAs of three
+// stages before are done: with two the MMAs waited for the copies).  The
+// epilogue reads the shared columns first, and lets the next tile's MMAs go when
+// it has them.
 // Waits are bounded as in fp4_mm.cu; the two CTAs leave together.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -41,10 +43,11 @@ constexpr int S = 5;
 constexpr int kEpi = 8;  // epilogue warps
 constexpr int kThreads = 32 * (2 + kEpi);
 constexpr int kSetCols = 48;                        // 4 atoms of x's scales (4 columns) and W's (8)
-constexpr int kAccStep = 160, kSetsAt = 416;        // the second accumulator's first column, the scales'
+constexpr int kAccStep = 96, kSetsAt = 352, kSets = 3;  // the second accumulator's first column, the scales'
 constexpr int kBars = 3 * S + 6;
-constexpr int kSmem = S * kStage + kBars * 8 + 16 + 1024;
-static_assert(kSmem <= 227 * 1024 && kSetsAt + 2 * kSetCols <= 512, "a CTA's shared memory and the SM's tensor memory");
+constexpr int kTurn = 2048;  // bytes in which an epilogue warp turns 32 rows x 32 columns
+constexpr int kSmem = S * kStage + kEpi * (kTurn + 512) + kBars * 8 + 16 + 1024;
+static_assert(kSmem <= 227 * 1024 && kSetsAt + kSets * kSetCols <= 512, "a CTA's shared memory and the SM's tensor memory");
 
 struct Maps {
   CUtensorMap w;  // u8 [experts * N][K / 2], box 128 bytes x TN / 2 rows, 128-byte swizzle
@@ -77,7 +80,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   const uint32_t sb = smem_u32(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const uint32_t bars = sb + S * kStage;
+  const uint32_t turns = sb + S * kStage, bars = turns + kEpi * (kTurn + 512);
+  float* s_wf = reinterpret_cast<float*>(base + S * kStage + kEpi * kTurn);  // W's factors for an epilogue warp's columns: four 32s each
   auto X_of = [&](int s) { return sb + (uint32_t)(s * kStage); };
   auto W_of = [&](int s) { return X_of(s) + kXTile; };
   auto SX_of = [&](int s) { return W_of(s) + kWTile; };
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   cluster_arrive();
   cluster_wait();
   tc_fence_after_sync();
-  const uint32_t tmem = *s_tmem;
+  // (all 512 columns of tensor memory: they begin at 0, and the addresses below are constants)
   pdl_launch_dependents();
   pdl_wait();
   const int x_tiles = p.tiles ? *p.tile_count : p.x_tiles;
@@ -169,53 +173,66 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     // ---- leader: scales and MMAs ----
     const uint32_t go = elect_one();
     const uint32_t idesc = umma_idesc_e2m1(256, tn, FMT == W4A16_FP4_MX);
-    uint32_t n = 0;  // tiles
+    const uint64_t xd0 = umma_desc_sw128(X_of(0)), wd0 = umma_desc_sw128(W_of(0));
+    const uint64_t sx0 = umma_desc(SX_of(0), 128, 128, 0), sw0 = umma_desc(SW_of(0), 128, 128, 0);
+    uint32_t n = 0;                     // tiles
+    int s = 0, set = 0, old = S - kSets;  // slot, scale set, and the slot of kSets stages before
+    uint32_t parity = 0, old_parity = 1;
     for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
       int xt, nt;
       unit_tile(u, x_tiles, pp.n_tiles, xt, nt);
       const int b = (int)(n & 1);
       // this accumulator's last tile is read, and the columns it shares with the other's
-      if ((n >= 2 && !mbar_wait_cluster(acc_free(b), ((n >> 1) - 1) & 1, limit)) ||
-          (n >= 1 && !mbar_wait_cluster(part_free(b ^ 1), ((n - 1) >> 1) & 1, limit))) {
+      if ((n >= 2 && !mbar_wait_warp(acc_free(b), ((n >> 1) - 1) & 1, limit)) ||
+          (n >= 1 && !mbar_wait_warp(part_free(b ^ 1), ((n - 1) >> 1) & 1, limit))) {
         if (lane == 0) timeout();
         break;
       }
       tc_fence_after_sync();
-      const uint32_t acc = tmem + (uint32_t)(b * kAccStep);
+      const uint32_t acc = (uint32_t)(b * kAccStep);
       const uint32_t w_col = (uint32_t)(nt * tn % 128 / 32);
       bool ok = true;
       for (int k = 0; k < ns; ++k, ++it) {
-        const int s = (int)(it % S);
-        const uint32_t set = tmem + (uint32_t)(kSetsAt + (int)(it & 1) * kSetCols);
-        const uint32_t before = it - 2;  // the set's last MMAs
-        ok = mbar_wait_warp(full(s), (it / S) & 1, limit) && mbar_wait_cluster(peer(s), (it / S) & 1, limit) &&
-             (it < 2 || mbar_wait_warp(empty((int)(before % S)), (before / S) & 1, limit));
+        ok = mbar_wait_warp(full(s), parity, limit) && mbar_wait_warp(peer(s), parity, limit) &&
+             (it < (uint32_t)kSets || mbar_wait_warp(empty(old), old_parity, limit));
         if (!ok) {
           if (lane == 0) timeout();
           break;
         }
         tc_fence_after_sync();
-        const uint64_t sx = umma_desc(SX_of(s), 128, 128, 0), sw = umma_desc(SW_of(s), 128, 128, 0);
-        const uint64_t xd = umma_desc_sw128(X_of(s)), wd = umma_desc_sw128(W_of(s));
-        const int atoms = min(kAtoms, p.atoms - k * kAtoms);
-        const int steps = min(4, (p.K - k * kFp4StageK + 63) / 64);
+        const uint64_t at = (uint64_t)(uint32_t)(s * (kStage >> 4));
+        const uint64_t xd = xd0 + at, wd = wd0 + at, sx = sx0 + at, sw = sw0 + at;
+        const uint32_t cx = (uint32_t)(kSetsAt + set * kSetCols), cw = cx + 16;
+        const int atoms = p.atoms - k * kAtoms, steps = (p.K - k * kFp4StageK + 63) / 64;
+        auto copy = [&](int a) {
+          tmem_copy_scales2(go, cx + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
+          tmem_copy_scales2(go, cw + 8 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
+          tmem_copy_scales2(go, cw + 8 * a + 4, sw + (uint64_t)((2048 + a * kFp4Atom) >> 4));
+        };
+        auto mma = [&](int j) {
+          if (FMT == W4A16_FP4_MX)
+            umma2_mxf4(go, acc, xd + 2 * j, wd + 2 * j, idesc | umma_idesc_scale_byte(2 * (j & 1)), cx + 4 * (j / 2),
+                       cw + 8 * (j / 2) + w_col, k > 0 || j > 0);
+          else
+            umma2_nvf4(go, acc, xd + 2 * j, wd + 2 * j, idesc, cx + 4 * j, cw + 8 * j + w_col, k > 0 || j > 0);
+        };
+        if (steps >= 4) {
 #pragma unroll
-        for (int a = 0; a < kAtoms; ++a)
-          if (a < atoms) {
-            tmem_copy_scales2(go, set + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
-            tmem_copy_scales2(go, set + 16 + 8 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
-            tmem_copy_scales2(go, set + 16 + 8 * a + 4, sw + (uint64_t)((2048 + a * kFp4Atom) >> 4));
-          }
+          for (int a = 0; a < kAtoms; ++a) copy(a);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < steps) {
-            if (FMT == W4A16_FP4_MX)
-              umma2_mxf4(go, acc, xd + 2 * j, wd + 2 * j, idesc | umma_idesc_scale_byte(2 * (j & 1)), set + 4 * (j / 2),
-                         set + 16 + 8 * (j / 2) + w_col, k > 0 || j > 0);
-            else
-              umma2_nvf4(go, acc, xd + 2 * j, wd + 2 * j, idesc, set + 4 * j, set + 16 + 8 * j + w_col, k > 0 || j > 0);
-          }
+          for (int j = 0; j < 4; ++j) mma(j);
+        } else {  // the end of K
+#pragma unroll
+          for (int a = 0; a < kAtoms; ++a)
+            if (a < atoms) copy(a);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < steps) mma(j);
+        }
         umma_commit2_if(go, empty(s));
+        if (++s == S) s = 0, parity ^= 1;
+        if (++old == S) old = 0, old_parity ^= 1;
+        if (++set == kSets) set = 0;
       }
       if (!ok) break;
       umma_commit2_if(go, acc_full(b));
@@ -253,75 +270,95 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       }
       const int r = 128 * (int)rank + 32 * q + lane;
       const bool mine = r < count;
-      const int64_t m = mine ? (p.row ? p.row[place + r] : place + r) : 0;
+      const int m = mine ? (p.row ? p.row[place + r] : place + r) : 0;
       const float fx = mine && p.xf ? p.xf[place + r] : 1.0f;
-      const float* wf = p.wf ? p.wf + expert * p.N : nullptr;
       const int64_t cols = p.act == W4A16_FP4_LINEAR ? p.N : p.N / 2;
+      float* wf = s_wf + 128 * (warp - 2);
+      const bool factors = p.wf || p.xf;
+      if (factors) {
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int i = half + 2 * g, c = nt * tn + 32 * (b ? i : (i + 3) % 8) + lane;
+          wf[32 * g + lane] = !p.wf ? 1.0f : c < p.N ? p.wf[expert * p.N + c] : 0.f;
+        }
+        __syncwarp();
+      }
       if (!mbar_wait_warp(acc_full(b), (n >> 1) & 1, limit)) {
         if (lane == 0) timeout();
         break;
       }
       tc_fence_after_sync();
-      const uint32_t acc = tmem + (uint32_t)(b * kAccStep) + ((uint32_t)(32 * q) << 16);
-      // columns 160 .. 255 of tensor memory are both accumulators': 16 at a time, those first.  Accumulator 0 has them
-      // last and accumulator 1 first; the warps' halves take every other 16.
-      for (int i = half; i < 16; i += 2) {
-        const int c = 16 * (b ? i : (i + 10) % 16);
-        if (c < tn) {
-          float v[16];
-          tmem_ld16(acc + c, v);
+      const uint32_t acc = (uint32_t)(b * kAccStep) + ((uint32_t)(32 * q) << 16);
+      // Columns 96 .. 255 of tensor memory are both accumulators', the last five 32s of the first and the first five of
+      // the second: those first.  The warps' halves take every other 32.
+#pragma unroll 1
+      for (int i = half; i < 8; i += 2) {
+        const int c = 32 * (b ? i : (i + 3) % 8);
+        const int n0 = nt * tn + c;
+        const bool any = c < tn && n0 < p.N;
+        float v[32];
+        if (any) {
+          tmem_ld32(acc + c, v);
           tmem_wait_ld();
-          const int n0 = nt * tn + c;
-          if (mine && n0 < p.N) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] *= fx;
-            if (wf) {
-              if (n0 + 16 <= p.N) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] *= wf[n0 + j];
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (n0 + j < p.N) v[j] *= wf[n0 + j];
-              }
-            }
-            if (p.act == W4A16_FP4_LINEAR) {
-              uint16_t* y = p.y + m * cols + n0;
-              if (pp.vec && n0 + 16 <= p.N) {
-                uint32_t o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  o[j] = (uint32_t)f32_to_bf16_bits(v[2 * j]) | (uint32_t)f32_to_bf16_bits(v[2 * j + 1]) << 16;
-                *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(y + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (n0 + j < p.N) y[j] = f32_to_bf16_bits(v[j]);
-              }
-            } else {
-              uint16_t* y = p.y + m * cols + n0 / 2;
-              float h[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) h[j] = fp4_activate(v[2 * j], p.act) * v[2 * j + 1];
-              if (pp.vec && n0 + 16 <= p.N) {
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  o[j] = (uint32_t)f32_to_bf16_bits(h[2 * j]) | (uint32_t)f32_to_bf16_bits(h[2 * j + 1]) << 16;
-                *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if (n0 + 2 * j < p.N) y[j] = f32_to_bf16_bits(h[j]);
-              }
-            }
-          }
         }
-        if (i >= 4 && i < 6) {  // columns of the first six have been read by this warp (three of its own)
+        if (i == 3 || i == 4) {  // this warp's last of the five
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(part_free(b) + to);
+        }
+        if (!any) continue;
+        if (factors) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(wf + 16 * (i - half) + j);
+            v[j] *= fx * f.x;
+            v[j + 1] *= fx * f.y;
+            v[j + 2] *= fx * f.z;
+            v[j + 3] *= fx * f.w;
+          }
+        }
+        // A lane holds a row of the tile; stored as they are, the 32 rows of a warp would be 32 lines an instruction.
+        // They go through shared memory so that four lanes (gated: two) store 64 (32) bytes of a row.
+        const bool linear = p.act == W4A16_FP4_LINEAR;
+        uint32_t o[16];
+        if (linear) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = fp4_bf16x2(v[2 * j], v[2 * j + 1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o[j] = fp4_bf16x2(fp4_activate(v[4 * j], p.act) * v[4 * j + 1], fp4_activate(v[4 * j + 2], p.act) * v[4 * j + 3]);
+        }
+        const int n1 = linear ? n0 : n0 / 2;
+        if (pp.vec && n0 + 32 <= p.N) {
+          const uint32_t turn = turns + (uint32_t)((warp - 2) * kTurn);
+          auto at = [&](int row, int unit) { return turn + (uint32_t)(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4)); };
+          const int units = linear ? 4 : 2;  // 16 bytes each
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < units) sts128(at(lane, j), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          __syncwarp();
+          const int unit = lane % units, per = 32 / units;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < units) {
+              const int row = per * j + lane / units;
+              const uint4 w = lds128(at(row, unit));
+              const int64_t to_m = __shfl_sync(0xffffffffu, m, row);
+              if (r - lane + row < count) *reinterpret_cast<uint4*>(p.y + to_m * cols + n1 + 8 * unit) = w;
+            }
+          __syncwarp();
+        } else if (mine) {
+          uint16_t* y = p.y + m * cols + n1;
+          const int left = (linear ? p.N - n0 : (p.N - n0) / 2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (linear || j < 8) {
+              if (2 * j < left) y[2 * j] = (uint16_t)o[j];
+              if (2 * j + 1 < left) y[2 * j + 1] = (uint16_t)(o[j] >> 16);
+            }
+          }
         }
       }
       tc_fence_before_sync();
@@ -343,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   cluster_wait();
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc2(tmem, 512);
+    tmem_dealloc2(*s_tmem, 512);
   }
 }
 
@@ -401,7 +438,7 @@ cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   p.p = fp4_params(a, 256);
   p.tn = 256;
   p.n_tiles = (a.w.rows + p.tn - 1) / p.tn;
-  const int cols = a.act == W4A16_FP4_LINEAR ? a.w.rows : a.w.rows / 2;
+  const int cols = a.act == W4A16_FP4_LINEAR ? a.w.rows : a.w.rows / 2;  // of a row of y
   p.vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
   const int64_t units = (int64_t)p.n_tiles * (a.tiles ? a.max_tiles : p.p.x_tiles);
   return a.w.format == W4A16_FP4_MX ? launch_t<W4A16_FP4_MX>(a, p, units, pdl, s) : launch_t<W4A16_FP4_NV>(a, p, units, pdl, s);
