@@ -13,9 +13,19 @@
 //   warp 0      TMA producer
 //   warp 1      scales from shared to tensor memory, MMAs, commits
 //   warps 2-5   epilogue: accumulator -> registers, factors, activation, bf16
-//               stores; two accumulators, so that the next tile's MMAs run
-// Scales in tensor memory have four sets: a set is written again when the MMAs
-// of the stage that used it have completed.
+//               stores; two accumulators (one for NT = 128), so that the next
+//               tile's MMAs run
+// Two CTAs an SM: what a stage costs beside its bytes is the issue of eight
+// copies of scales and four MMAs, and two warps issue side by side.
+//
+// K split over a cluster.  Where W has few row tiles, `split` CTAs take a
+// tile's stages between them; every CTA then sends each other one its columns
+// through distributed shared memory, and the sums are added in the order of K.
+// The split depends on W's shape alone: up to 128 rows of x a row's result is
+// the same, bit for bit, whatever the other rows of the call.
+//
+// Scales in tensor memory have a set for each slot of the ring: a stage that
+// landed in a slot says that the MMAs which read the slot before are done.
 // Every wait is bounded: one that gives up raises W4A16_DEVICE_TIMEOUT, all
 // roles leave their loops, outstanding copies and MMAs are waited for (also
 // bounded) and the tensor memory is freed before the CTA exits.
@@ -36,23 +46,24 @@ namespace {
 using namespace ptx;
 
 constexpr int kWRows = 128;
-constexpr int kWTile = kWRows * 128;          // 16 KB
-constexpr int kScaleTile = 2048;              // scale atoms of a stage and 128 rows (mx: half of it)
-constexpr int kSets = 4;                      // scale sets in tensor memory
+constexpr int kWTile = kWRows * 128;  // 16 KB
+constexpr int kScaleTile = 2048;      // scale atoms of a stage and 128 rows (mx: half of it)
+constexpr int kSetCols = 32;          // 16 columns of W's scales, 16 of x's
 constexpr int kThreads = 192;
+constexpr int kMaxSplit = 8;
+constexpr int kCtaSmem = 113 * 1024;  // of which two fit an SM
 
 template <int NT>
 struct Geo {
   static constexpr int kX = NT * 128;
   static constexpr int kStage = kWTile + kX + 2 * kScaleTile;
-  static constexpr int kStages = (225 * 1024) / kStage > 10 ? 10 : (225 * 1024) / kStage;
-  static constexpr int kAcc = 2;
-  static constexpr int kSetCols = 32;  // 16 columns of W's scales, 16 of x's
-  static constexpr int kCols = kAcc * NT + kSets * kSetCols;
-  static constexpr uint32_t kTmemCols = kCols <= 256 ? 256 : 512;
+  static constexpr int kStages = (kCtaSmem - 1280) / kStage;
+  static constexpr int kAcc = NT == 128 ? 1 : 2;
+  static constexpr uint32_t kTmemCols = 256;
   static constexpr int kBars = 2 * kStages + 2 * kAcc;
   static constexpr int kSmem = kStages * kStage + kBars * 8 + 16 + 1024;
-  static_assert(kSmem <= 227 * 1024 && kCols <= 512, "a CTA's shared memory and the SM's tensor memory");
+  static_assert(kSmem <= kCtaSmem && kAcc * NT + kStages * kSetCols <= (int)kTmemCols, "half an SM's shared and tensor memory");
+  static_assert(NT * kWRows * 4 <= kStages * kStage, "the partial sums of a split tile take the stages' place");
 };
 
 struct Maps {
@@ -60,8 +71,41 @@ struct Maps {
   CUtensorMap x;  // u8 [x rows][K / 2], box 128 bytes x NT rows
 };
 
+// One sum of row `row` of W and place `at` of x, whole warps (gate and up rows are neighbours).
+__device__ __forceinline__ void store(const Fp4MmParams& p, float v, float fw, int at, int row, bool mine) {
+  const int64_t m = p.row ? p.row[at] : at;
+  float t = v * fw;
+  if (p.xf) t *= p.xf[at];
+  if (p.act == W4A16_FP4_LINEAR) {
+    if (mine) p.y[m * p.N + row] = f32_to_bf16_bits(t);
+  } else {
+    const float up = __shfl_down_sync(0xffffffffu, t, 1);
+    if (mine && !(row & 1)) p.y[m * (p.N / 2) + row / 2] = f32_to_bf16_bits(fp4_activate(t, p.act) * up);
+  }
+}
+
+// Four neighbouring rows of W, `row` a multiple of four, and place `at` of x.
+__device__ __forceinline__ void store4(const Fp4MmParams& p, const float (&v)[4], int at, int row) {
+  const int64_t m = p.row ? p.row[at] : at;
+  if (p.act == W4A16_FP4_LINEAR) {
+    uint16_t* y = p.y + m * p.N + row;
+    if (p.vec && row + 4 <= p.N) {
+      *reinterpret_cast<uint2*>(y) = make_uint2(fp4_bf16x2(v[0], v[1]), fp4_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row + i < p.N) y[i] = f32_to_bf16_bits(v[i]);
+    }
+  } else {
+    uint16_t* y = p.y + m * (p.N / 2) + row / 2;
+    const uint32_t two = fp4_bf16x2(fp4_activate(v[0], p.act) * v[1], fp4_activate(v[2], p.act) * v[3]);
+    if (row < p.N) y[0] = (uint16_t)two;
+    if (row + 2 < p.N) y[1] = (uint16_t)(two >> 16);
+  }
+}
+
 template <int NT, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_constant__ Maps maps, Fp4MmParams p) {
+__global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_constant__ Maps maps, Fp4MmParams p) {
   using G = Geo<NT>;
   constexpr int S = G::kStages, NB = G::kAcc;
   constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;  // of a stage and 128 rows
@@ -102,11 +146,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
   tc_fence_after_sync();
   const uint32_t tmem = *s_tmem;
   pdl_launch_dependents();
-  pdl_wait();
+  const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
+  const int64_t first = blockIdx.x / (unsigned)split, step = gridDim.x / (unsigned)split;
+  // this CTA's stages of a tile
+  const int k0 = p.stages * rank / split, k1 = p.stages * (rank + 1) / split;
+  const uint32_t limit = p.fault_wait ? 4096u : 1u << 18;  // tries of a wait: about a second
+  // What comes before the wait for the kernel before: nothing but W, and that only where it is complete already.
+  if (!(p.early && warp == 0)) pdl_wait();
   const int x_tiles = p.tiles ? *p.tile_count : p.x_tiles;
   const int64_t units = (int64_t)x_tiles * p.row_tiles;
-  const int ns = p.stages;
-  const uint32_t limit = p.fault_wait ? 4096u : 1u << 18;  // tries of a wait: about a second
   auto timeout = [&]() {
     atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
     *s_abort = 1;
@@ -117,7 +165,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
     // ---- TMA producer ----
     if (lane == 0) {
       const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
-      for (int64_t u = blockIdx.x; u < units && !*s_abort; u += gridDim.x) {
+      auto scale_bytes = [&](int k) { return (uint32_t)(min(kAtoms, p.atoms - k * kAtoms) * kFp4Atom); };
+      auto load_w = [&](int s, int k, int wrow, const uint8_t* ws) {
+        mbar_expect_tx(full(s), kWTile + G::kX + 2 * scale_bytes(k));
+        tma_load_2d(W_of(s), &maps.w, k * 128, wrow, full(s), stream);
+        bulk_load(SW_of(s), ws + k * kAtoms * kFp4Atom, scale_bytes(k), full(s), stream);
+      };
+      int ahead = 0;  // stages whose W is requested already
+      if (p.early) {
+        if (first < units) {
+          const int wt = (int)(first % p.row_tiles);
+          for (; ahead < S && k0 + ahead < k1; ++ahead)
+            load_w(ahead, k0 + ahead, wt * kWRows, p.ws + (int64_t)wt * p.atoms * kFp4Atom);
+        }
+        pdl_wait();
+      }
+      int s = 0;
+      uint32_t parity = 1;
+      for (int64_t u = first; u < units && !*s_abort; u += step) {
         const int xt = (int)(u / p.row_tiles), wt = (int)(u % p.row_tiles);
         int64_t expert = 0;
         int place = xt * NT;
@@ -128,18 +193,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
         const int wrow = (int)(expert * p.N + (int64_t)wt * kWRows);
         const uint8_t* ws = p.ws + (expert * p.row_tiles + wt) * p.atoms * kFp4Atom;
         const uint8_t* xs = p.xs + (int64_t)(place / kFp4Rows) * p.atoms * kFp4Atom;
-        for (int k = 0; k < ns; ++k, ++it) {
-          const int s = (int)(it % S);
-          if (it >= (uint32_t)S && !mbar_wait_parked(empty(s), ((it / S) - 1) & 1, 1000, limit)) {
+        for (int k = k0; k < k1; ++k, ++it) {
+          if (it >= (uint32_t)S && !mbar_wait_parked(empty(s), parity, 1000, limit)) {
             timeout();
             break;
           }
-          const uint32_t scale_bytes = (uint32_t)(min(kAtoms, p.atoms - k * kAtoms) * kFp4Atom);
-          mbar_expect_tx(full(s), kWTile + G::kX + 2 * scale_bytes);
-          tma_load_2d(W_of(s), &maps.w, k * 128, wrow, full(s), stream);
-          bulk_load(SW_of(s), ws + k * kAtoms * kFp4Atom, scale_bytes, full(s), stream);
+          if (it >= (uint32_t)ahead) load_w(s, k, wrow, ws);
           tma_load_2d(X_of(s), &maps.x, k * 128, place, full(s), keep);
-          bulk_load(SX_of(s), xs + k * kAtoms * kFp4Atom, scale_bytes, full(s), keep);
+          bulk_load(SX_of(s), xs + k * kAtoms * kFp4Atom, scale_bytes(k), full(s), keep);
+          if (++s == S) s = 0, parity ^= 1;
         }
       }
     }
@@ -147,8 +209,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
     // ---- scales and MMAs ----
     const uint32_t go = elect_one();
     constexpr uint32_t kIdesc = umma_idesc_e2m1(kWRows, NT, FMT == W4A16_FP4_MX);
+    const uint64_t wd0 = umma_desc_sw128(W_of(0)), xd0 = umma_desc_sw128(X_of(0));
+    const uint64_t sw0 = umma_desc(SW_of(0), 128, 128, 0), sx0 = umma_desc(SX_of(0), 128, 128, 0);
     uint32_t n = 0;  // tiles
-    for (int64_t u = blockIdx.x; u < units && !*s_abort; u += gridDim.x, ++n) {
+    int s = 0;
+    uint32_t parity = 0;
+    for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
       const int b = (int)(n % NB);
       if (n >= (uint32_t)NB && !mbar_wait_warp(acc_free(b), ((n / NB) - 1) & 1, limit)) {
         if (lane == 0) timeout();
@@ -157,38 +223,42 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
       tc_fence_after_sync();
       const uint32_t acc = tmem + (uint32_t)(b * NT);
       bool ok = true;
-      for (int k = 0; k < ns; ++k, ++it) {
-        const int s = (int)(it % S);
-        const uint32_t set = tmem + (uint32_t)(NB * NT + (int)(it % kSets) * G::kSetCols);
-        // the set's last MMAs: those of the stage kSets before
-        const uint32_t before = it - kSets;
-        ok = mbar_wait_warp(full(s), (it / S) & 1, limit) &&
-             (it < (uint32_t)kSets || mbar_wait_warp(empty((int)(before % S)), (before / S) & 1, limit));
-        if (!ok) {
+      for (int k = k0; k < k1; ++k, ++it) {
+        if (!(ok = mbar_wait_warp(full(s), parity, limit))) {
           if (lane == 0) timeout();
           break;
         }
         tc_fence_after_sync();
-        const uint64_t sw = umma_desc(SW_of(s), 128, 128, 0), sx = umma_desc(SX_of(s), 128, 128, 0);
-        const uint64_t wd = umma_desc_sw128(W_of(s)), xd = umma_desc_sw128(X_of(s));
-        const int atoms = min(kAtoms, p.atoms - k * kAtoms);
-        const int steps = min(4, (p.K - k * kFp4StageK + 63) / 64);
+        const uint64_t at = (uint64_t)(uint32_t)(s * (G::kStage >> 4));
+        const uint64_t wd = wd0 + at, xd = xd0 + at, sw = sw0 + at, sx = sx0 + at;
+        const uint32_t cw = tmem + (uint32_t)(NB * NT + s * kSetCols), cx = cw + 16;
+        const int atoms = p.atoms - k * kAtoms, steps = (p.K - k * kFp4StageK + 63) / 64;
+        auto copy = [&](int a) {
+          tmem_copy_scales(go, cw + 4 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
+          tmem_copy_scales(go, cx + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
+        };
+        auto mma = [&](int j) {
+          const bool add = k > k0 || j > 0;
+          if (FMT == W4A16_FP4_MX)
+            umma_mxf4(go, acc, wd + 2 * j, xd + 2 * j, kIdesc | umma_idesc_scale_byte(2 * (j & 1)), cw + 4 * (j / 2), cx + 4 * (j / 2), add);
+          else
+            umma_nvf4(go, acc, wd + 2 * j, xd + 2 * j, kIdesc, cw + 4 * j, cx + 4 * j, add);
+        };
+        if (steps >= 4) {
 #pragma unroll
-        for (int a = 0; a < kAtoms; ++a)
-          if (a < atoms) {
-            tmem_copy_scales(go, set + 4 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
-            tmem_copy_scales(go, set + 16 + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
-          }
+          for (int a = 0; a < kAtoms; ++a) copy(a);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < steps) {
-            if (FMT == W4A16_FP4_MX)
-              umma_mxf4(go, acc, wd + 2 * j, xd + 2 * j, kIdesc | umma_idesc_scale_byte(2 * (j & 1)), set + 4 * (j / 2),
-                        set + 16 + 4 * (j / 2), k > 0 || j > 0);
-            else
-              umma_nvf4(go, acc, wd + 2 * j, xd + 2 * j, kIdesc, set + 4 * j, set + 16 + 4 * j, k > 0 || j > 0);
-          }
+          for (int j = 0; j < 4; ++j) mma(j);
+        } else {  // the end of K
+#pragma unroll
+          for (int a = 0; a < kAtoms; ++a)
+            if (a < atoms) copy(a);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < steps) mma(j);
+        }
         umma_commit_if(go, empty(s));
+        if (++s == S) s = 0, parity ^= 1;
       }
       if (!ok) break;
       umma_commit_if(go, acc_full(b));
@@ -197,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
     // ---- epilogue ----
     const int q = warp & 3, r = 32 * q + lane;
     uint32_t n = 0;
-    for (int64_t u = blockIdx.x; u < units && !*s_abort; u += gridDim.x, ++n) {
+    for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
       const int b = (int)(n % NB);
       const int xt = (int)(u / p.row_tiles), wt = (int)(u % p.row_tiles);
       int64_t expert = 0;
@@ -214,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
         if (lane == 0) timeout();
         break;
       }
+      if (split > 1) break;  // (one tile a cluster: the rest below)
       tc_fence_after_sync();
       const uint32_t acc = tmem + (uint32_t)(b * NT) + ((uint32_t)(32 * q) << 16);
 #pragma unroll 1
@@ -226,15 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
         for (int i = 0; i < 16; ++i) {
           if (c + i >= count) break;
           const int at = place + c + i;
-          const int64_t m = p.row ? p.row[at] : at;
-          float t = v[i] * fw;
-          if (p.xf) t *= p.xf[at];
-          if (p.act == W4A16_FP4_LINEAR) {
-            if (mine) p.y[m * p.N + row] = f32_to_bf16_bits(t);
-          } else {
-            const float up = __shfl_down_sync(0xffffffffu, t, 1);
-            if (mine && !(row & 1)) p.y[m * (p.N / 2) + row / 2] = f32_to_bf16_bits(fp4_activate(t, p.act) * up);
-          }
+          store(p, v[i], fw, at, row, mine);
         }
       }
       tc_fence_before_sync();
@@ -243,8 +306,59 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_mm_kernel(const __grid_consta
     }
   }
 
-  // ---- teardown: everything in flight lands before the memories are released ----
   __syncthreads();
+  if (split > 1) {
+    // ---- a split tile: partial sums to the CTAs that add them up ----
+    // Rank g adds the columns [g per, (g + 1) per).  The sums take the stages' place when no MMA of the cluster reads
+    // those any more; a CTA that gave up takes part in the barriers all the same.
+    const int q = warp & 3, xt = (int)(first / p.row_tiles), wt = (int)(first % p.row_tiles);
+    const bool live = first < units && !*s_abort;
+    const int count = min(NT, p.M - xt * NT), per = (count + split - 1) / split;
+    cluster_arrive();
+    cluster_wait();
+    if (live && warp >= 2) {
+      tc_fence_after_sync();
+      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
+      int g = 0, col = 0;  // column c is the col-th of rank g's
+#pragma unroll 1
+      for (int c = 0; c < count; c += 16) {
+        float v[16];
+        tmem_ld16(acc + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (c + i >= count) break;
+          st_cluster_f32(cluster_map(sb + (uint32_t)(((rank * per + col) * kWRows + 32 * q + lane) * 4), (uint32_t)g), v[i]);
+          if (++col == per) col = 0, ++g;
+        }
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (live) {  // a warp a column, a lane four rows
+      const int row = wt * kWRows + 4 * lane, place = xt * NT + rank * per;
+      float fw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fw[i] = p.wf && row + i < p.N ? p.wf[row + i] : 1.0f;
+#pragma unroll 2
+      for (int c = warp; c < min(per, count - rank * per); c += kThreads / 32) {
+        const float fx = p.xf ? p.xf[place + c] : 1.0f;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < split; ++g) {
+          const float4 f = lds128f(sb + (uint32_t)(((g * per + c) * kWRows + 4 * lane) * 4));
+          v[0] += f.x;
+          v[1] += f.y;
+          v[2] += f.z;
+          v[3] += f.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = v[i] * fw[i] * fx;
+        store4(p, v, place + c, row);
+      }
+    }
+  }
+
+  // ---- teardown: everything in flight lands before the memories are released ----
   if (*s_abort) {
     if (warp == 0 && lane == 0)
       for (uint32_t i = it > (uint32_t)S ? it - S : 0; i < it; ++i) mbar_wait_parked(full((int)(i % S)), (i / S) & 1, 1000, limit);
@@ -296,15 +410,24 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
     return e;
   const int64_t units = (int64_t)p.row_tiles * (a.tiles ? a.max_tiles : p.x_tiles);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units < sms ? units : sms));
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? units * p.split : units < 2 * sms ? units : 2 * sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)G::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = pdl > 0 ? 1 : 0;
+  cfg.numAttrs = 0;
+  if (p.split > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)p.split;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (pdl > 0) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, fn, maps, p);
 }
 
@@ -315,7 +438,12 @@ int fp4_mm_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <
 cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   const int nt = a.tiles ? a.nt : fp4_mm_tile(a.M);
   if (nt == 256) return launch_fp4_pair(a, pdl, s);
-  const Fp4MmParams p = fp4_params(a, nt);
+  Fp4MmParams p = fp4_params(a, nt);
+  p.early = a.early && pdl > 1 && !a.tiles;
+  p.vec = a.w.rows % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 8 == 0;
+  // K is split where that leaves no CTA without a place (two an SM of 152) or a stage.  By W's shape alone.
+  if (!a.tiles)
+    while (p.split < kMaxSplit && 2 * p.split * p.row_tiles <= 304 && 2 * p.split <= p.stages) p.split *= 2;
   const bool mx = a.w.format == W4A16_FP4_MX;
   switch (nt) {
     case 16: return mx ? launch_t<16, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<16, W4A16_FP4_NV>(a, p, pdl, s);

@@ -25,6 +25,8 @@ struct Fp4MmParams {
   int N, K, M, act;
   int row_tiles, x_tiles;  // 128-row tiles of an expert's W; activation tiles (not routed)
   int atoms, stages;       // scale atoms along K; stages along K
+  int vec;                 // y's rows take 8-byte stores (fp4_pair.cu: 16)
+  int split, early;        // CTAs that share a tile's K; W may be fetched before the wait for the kernel before
   int fault_wait;
 };
 
@@ -60,6 +62,9 @@ inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
   p.x_tiles = a.tiles ? 0 : (a.M + x_tile - 1) / x_tile;
   p.atoms = fp4_atoms(a.w.K, a.w.format);
   p.stages = (a.w.K + kFp4StageK - 1) / kFp4StageK;
+  p.vec = 0;
+  p.split = 1;
+  p.early = 0;
   p.fault_wait = a.fault_wait;
   return p;
 }

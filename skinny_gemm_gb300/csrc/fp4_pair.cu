@@ -58,7 +58,6 @@ struct PairParams {
   Fp4MmParams p;
   int tn;       // rows of W per tile: 128, 192 or 256
   int n_tiles;  // tiles along W's rows
-  int vec;      // y's rows take 16-byte stores
 };
 
 // Which tile a pair's unit is: eight activation tiles by all of W's, then the next eight, so that the pairs at work at a
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
             o[j] = fp4_bf16x2(fp4_activate(v[4 * j], p.act) * v[4 * j + 1], fp4_activate(v[4 * j + 2], p.act) * v[4 * j + 3]);
         }
         const int n1 = linear ? n0 : n0 / 2;
-        if (pp.vec && n0 + 32 <= p.N) {
+        if (p.vec && n0 + 32 <= p.N) {
           const uint32_t turn = turns + (uint32_t)((warp - 2) * kTurn);
           auto at = [&](int row, int unit) { return turn + (uint32_t)(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4)); };
           const int units = linear ? 4 : 2;  // 16 bytes each
@@ -439,7 +438,7 @@ cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   p.tn = 256;
   p.n_tiles = (a.w.rows + p.tn - 1) / p.tn;
   const int cols = a.act == W4A16_FP4_LINEAR ? a.w.rows : a.w.rows / 2;  // of a row of y
-  p.vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+  p.p.vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
   const int64_t units = (int64_t)p.n_tiles * (a.tiles ? a.max_tiles : p.p.x_tiles);
   return a.w.format == W4A16_FP4_MX ? launch_t<W4A16_FP4_MX>(a, p, units, pdl, s) : launch_t<W4A16_FP4_NV>(a, p, units, pdl, s);
 }
