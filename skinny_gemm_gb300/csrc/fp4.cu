@@ -76,6 +76,9 @@ __device__ __forceinline__ float exp2i(int e) {
   return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(1u << (e + 149));
 }
 
+// 2^e for e in -126 .. 127.
+__device__ __forceinline__ float exp2n(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // The nv factor's exponent from the row's largest finite |x| (bf16 bits): 2688 = 1.3125 * 2^11, and 1.3125 has
 // significand bits 0x28 of 7.  Subnormal peaks are below every bound that counts.
 __device__ __forceinline__ int factor_exp(uint32_t peak) {
@@ -109,7 +112,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-constexpr int kQuantThreads = 256;
+constexpr int kQuantThreads = 256;  // of the way back
+constexpr int kQuantMost = 768;     // threads of a row: 80 registers each
 
 // Sixteen values to codes and their block's scale byte; peak is the block's largest |x| (bf16 bits).
 //
@@ -126,24 +130,24 @@ __device__ __forceinline__ uint2 block16(const Vec16& v, uint32_t peak, int e, u
   if (FMT == W4A16_FP4_MX) {
     // floor(log2 peak) - 2 + 127 is the exponent field less 2; a subnormal peak gives 0
     byte = max((int)(peak >> 7) - 2, 0);
-    const float s = exp2i(127 - (int)byte);
+    const float s = exp2n(127 - (int)byte);
 #pragma unroll
     for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], s);
     if (peak >= 0x7F80u) byte = 0xFFu;
   } else {
-    const float p = __fmul_rn(bf16_bits_to_f32((uint16_t)peak), exp2i(-e));
+    const float p = __fmul_rn(bf16_bits_to_f32((uint16_t)peak), exp2n(-e));
     const float want = __uint_as_float((__float_as_uint(__fmul_rn(p, 1.0f / 6.0f)) + 64u) & ~127u);
     uint16_t pair;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.0f), "f"(want));
     byte = pair & 0xFFu;
     // the scale in fp32: e4m3's bits at half the place of fp32's, times 2^120
-    float s = __fmul_rn(__uint_as_float(byte << 20), exp2i(120));
+    float s = __fmul_rn(__uint_as_float(byte << 20), exp2n(120));
     if (e < -90) {  // s f might leave fp32's normal range
-      const float inv = exp2i(-e);
+      const float inv = exp2n(-e);
 #pragma unroll
       for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], inv);
     } else {
-      s = __fmul_rn(s, exp2i(e));
+      s = __fmul_rn(s, exp2n(e));
     }
     const float r = byte ? rcp(s) : 0.0f;
     const float2 rr = make_float2(r, r), up = make_float2(3072.0f, 3072.0f), down = make_float2(-3072.0f, -3072.0f);
@@ -159,35 +163,33 @@ __device__ __forceinline__ uint2 block16(const Vec16& v, uint32_t peak, int e, u
   return make_uint2(codes8(y), codes8(y + 8));
 }
 
-// TPR threads a row, which hold up to C x TPR units of sixteen values (32 bytes) in registers between the row's peak and
-// its codes; longer rows are read again.  A thread has a whole nv block, two neighbours an mx one.  What bounds it is HBM
-// (2 bytes a value in, 0.56 out) for many rows, and a load, the row's reduction and the launch for few.
-template <int FMT, int TPR, int C>
-__global__ void __launch_bounds__(kQuantThreads, 3) fp4_quant_kernel(Fp4QuantArgs p) {
-  constexpr int kWarps = TPR / 32, kRows = kQuantThreads / TPR;
+// One CTA a row; a thread holds up to C units of sixteen values (32 bytes) in registers between the row's peak and its
+// codes, longer rows are read again.  A thread has a whole nv block, two neighbours an mx one.  What bounds it is HBM (2
+// bytes a value in, 0.56 out) for many rows, and a load, the row's reduction and the launch for few.
+template <int FMT, int C, bool ROUTED>
+__global__ void __launch_bounds__(kQuantMost, 1) fp4_quant_kernel(Fp4QuantArgs p) {
   constexpr int kWord = FMT == W4A16_FP4_MX ? 8 : 4;  // units of an atom's word of four scales
-  const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR, units = p.K / 16;
-  const int64_t r = (int64_t)blockIdx.x * kRows + group;
-  const bool live = r < p.rows;
-  __shared__ uint32_t s_peak[kQuantThreads / 32];
+  const int tid = threadIdx.x, threads = blockDim.x, units = p.K / 16;
+  const int n = blockIdx.x;  // row of expert blockIdx.y
+  const int64_t r = (int64_t)blockIdx.y * p.group + n;
+  __shared__ uint32_t s_peak[32];
   pdl_wait();
   pdl_launch_dependents();  // (not before: what the next kernel reads early is then complete)
-  const uint16_t* x = p.x + (live ? r : 0) * p.x_stride;
+  const uint16_t* x = p.x + r * p.x_stride;
   Vec16 v[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const int c = i * TPR + tid;
-    v[i] = c < units ? load16(x + 16 * (int64_t)c) : zero16();
+    const int c = i * threads + tid;
+    v[i] = c < units ? load16(x + 16 * c) : zero16();
   }
   int e = 0;
   if (FMT == W4A16_FP4_NV) {
     auto over_row = [&](uint32_t peak) {
       peak = __reduce_max_sync(0xffffffffu, peak);
-      if (kWarps > 1) {
-        if ((threadIdx.x & 31) == 0) s_peak[threadIdx.x >> 5] = peak;
+      if (threads > 32) {
+        if ((tid & 31) == 0) s_peak[tid >> 5] = peak;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) peak = max(peak, s_peak[group * kWarps + i]);
+        peak = __reduce_max_sync(0xffffffffu, (tid & 31) < threads / 32 ? s_peak[tid & 31] : 0u);
         __syncthreads();
       }
       return peak;
@@ -195,73 +197,72 @@ __global__ void __launch_bounds__(kQuantThreads, 3) fp4_quant_kernel(Fp4QuantArg
     uint32_t peak = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) peak = max(peak, peak16(v[i]));
-    for (int c = C * TPR + tid; c < units; c += TPR) peak = max(peak, peak16(load16(x + 16 * (int64_t)c)));
+    for (int c = C * threads + tid; c < units; c += threads) peak = max(peak, peak16(load16(x + 16 * c)));
     peak = over_row(peak);
-    // (a row with a NaN or an infinity, rare: all of the CTA's threads take part in the second reduction)
-    if (kWarps > 1 ? __syncthreads_or(peak >= 0x7F80u) : peak >= 0x7F80u) {
+    if (peak >= 0x7F80u) {  // a NaN or an infinity in the row
       peak = 0;
 #pragma unroll
       for (int i = 0; i < C; ++i) peak = max(peak, finite_peak16(v[i]));
-      for (int c = C * TPR + tid; c < units; c += TPR) peak = max(peak, finite_peak16(load16(x + 16 * (int64_t)c)));
+      for (int c = C * threads + tid; c < units; c += threads) peak = max(peak, finite_peak16(load16(x + 16 * c)));
       peak = over_row(peak);
     }
     e = factor_exp(peak);
   }
-  if (!live) return;
   const int atoms = fp4_atoms(p.K, FMT), all = atoms * kWord;  // units with those past K that fill the last atom
-  for (int j = 0; j < (p.place ? p.top : 1); ++j) {
+#pragma unroll 1
+  for (int j = 0; j < (ROUTED ? p.top : 1); ++j) {
     int64_t at = r, tile;
     int lane_row;
-    if (p.place) {
+    if (ROUTED) {
       at = p.place[r * p.top + j];
       if (at < 0) {  // no such expert: a row of zeros
         uint16_t* y = p.y + (r * p.top + j) * p.y_row;
-        for (int64_t i = tid; i < p.y_row; i += TPR) y[i] = 0;
+        for (int64_t i = tid; i < p.y_row; i += threads) y[i] = 0;
         continue;
       }
       tile = at / kFp4Rows;
       lane_row = (int)(at % kFp4Rows);
     } else {
-      const int n = (int)(r % p.group);
-      tile = r / p.group * fp4_row_tiles(p.group) + n / kFp4Rows;
+      tile = (int64_t)blockIdx.y * fp4_row_tiles(p.group) + n / kFp4Rows;
       lane_row = n % kFp4Rows;
     }
-    uint2* codes = reinterpret_cast<uint2*>(p.codes + at * (p.K / 2));
-    uint8_t* scales = p.scales + tile * atoms * kFp4Atom + 16 * (lane_row & 31) + 4 * (lane_row >> 5);
-    if (FMT == W4A16_FP4_NV && tid == 0) p.row_scale[at] = exp2i(e);
-    auto write = [&](int c, const Vec16& w) {  // (whole warps)
+    uint2* codes = reinterpret_cast<uint2*>(p.codes + at * (p.K / 2)) + tid;
+    if (FMT == W4A16_FP4_NV && tid == 0) p.row_scale[at] = exp2n(e);
+    // a word of an atom is four blocks' bytes, kWord threads' units; the CTA's threads are a multiple of that
+    uint8_t* words = p.scales + tile * atoms * kFp4Atom + 16 * (lane_row & 31) + 4 * (lane_row >> 5) + tid / kWord * kFp4Atom;
+    const int place = 8 * (tid / (kWord / 4) % 4);
+    const bool first = tid % kWord == 0;
+    auto write = [&](int c0, const Vec16& w) {  // units c0 + tid (whole warps)
       uint32_t peak = peak16(w);
       if (FMT == W4A16_FP4_MX) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
       uint32_t byte;
       const uint2 code = block16<FMT>(w, peak, e, byte);
-      if (c < units) codes[c] = code;
-      uint32_t word = byte << (8 * (FMT == W4A16_FP4_MX ? c / 2 % 4 : c % 4));
+      if (tid < units - c0) codes[c0] = code;
+      uint32_t word = byte << place;
       word |= __shfl_xor_sync(0xffffffffu, word, kWord / 4);
       word |= __shfl_xor_sync(0xffffffffu, word, kWord / 2);
-      if (c < all && c % kWord == 0) *reinterpret_cast<uint32_t*>(scales + (int64_t)(c / kWord) * kFp4Atom) = word;
+      if (first && tid < all - c0) *reinterpret_cast<uint32_t*>(words + c0 / kWord * kFp4Atom) = word;
     };
 #pragma unroll
     for (int i = 0; i < C; ++i)
-      if (i * TPR < all) write(i * TPR + tid, v[i]);
-    for (int c0 = C * TPR; c0 < all; c0 += TPR) {
-      const int c = c0 + tid;
-      write(c, c < units ? load16(x + 16 * (int64_t)c) : zero16());
-    }
+      if (i * threads < all) write(i * threads, v[i]);
+#pragma unroll 1
+    for (int c0 = C * threads; c0 < all; c0 += threads) write(c0, c0 + tid < units ? load16(x + 16 * (c0 + tid)) : zero16());
   }
 }
 
 // Units of sixteen values: value = bf16(code * scale * factor), exact unless it leaves bf16's range.  code * scale is
 // exact in fp16 for nv (6 significant bits, 2^-10 to 2688).
-constexpr int kBack = 2;  // units a thread
+constexpr int kBack = 1;  // units a thread
 
-__global__ void __launch_bounds__(kQuantThreads) fp4_dequant_kernel(w4a16_fp4 w, uint16_t* y, int parts) {
+__global__ void __launch_bounds__(kQuantThreads) fp4_dequant_kernel(w4a16_fp4 w, uint16_t* y) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t r = blockIdx.x / parts;
-  const int part = (int)(blockIdx.x % parts);
+  const int n = blockIdx.x, part = blockIdx.z;  // row of expert blockIdx.y
+  const int64_t r = (int64_t)blockIdx.y * w.rows + n;
   const bool mx = w.format == W4A16_FP4_MX;
   const int atoms = fp4_atoms(w.K, w.format), units = w.K / 16;
-  const int64_t n = r % w.rows, tile = r / w.rows * fp4_row_tiles(w.rows) + n / kFp4Rows;
+  const int64_t tile = (int64_t)blockIdx.y * fp4_row_tiles(w.rows) + n / kFp4Rows;
   const uint8_t* scales = w.scales + tile * atoms * kFp4Atom + 16 * (n & 31) + 4 * (n % kFp4Rows >> 5);
   const float factor = w.row_scale ? w.row_scale[r] : 1.0f;
   uint2 code[kBack];
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_dequant_kernel(w4a16_fp4 w,
     if (c >= units) break;
     float s = 1.0f, f = factor;
     if (mx) f = __fmul_rn(byte[i] == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte[i] - 127), factor);
-    else s = (byte[i] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte[i] & 0x7Fu) << 20 | (byte[i] & 0x80u) << 24), exp2i(120));
+    else s = (byte[i] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte[i] & 0x7Fu) << 20 | (byte[i] & 0x80u) << 24), exp2n(120));
     const __half2 sh = __float2half2_rn(s);
     uint32_t out[8];
 #pragma unroll
@@ -361,22 +362,20 @@ __global__ void __launch_bounds__(kRouteThreads) fp4_route_kernel(Fp4RouteArgs p
 
 namespace {
 
-template <int FMT, int TPR, int C>
-cudaError_t quant_t(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
-  void* args[] = {const_cast<Fp4QuantArgs*>(&a)};
-  constexpr int kRows = kQuantThreads / TPR;
-  return launch((const void*)fp4_quant_kernel<FMT, TPR, C>, dim3((unsigned)((a.rows + kRows - 1) / kRows)), kQuantThreads, args, pdl, s);
-}
-
 template <int FMT>
 cudaError_t quant_f(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
-  // few rows: as many threads as units, for the latency; many: up to four units a thread in flight
-  const int units = a.K / 16;
-  if (a.rows <= 152) return units <= 256 ? quant_t<FMT, 256, 1>(a, pdl, s) : quant_t<FMT, 256, 4>(a, pdl, s);
-  if (units <= 128) return quant_t<FMT, 32, 4>(a, pdl, s);
-  if (units <= 256) return quant_t<FMT, 64, 4>(a, pdl, s);
-  if (units <= 512) return quant_t<FMT, 128, 4>(a, pdl, s);
-  return quant_t<FMT, 256, 4>(a, pdl, s);
+  void* args[] = {const_cast<Fp4QuantArgs*>(&a)};
+  // Few rows: a thread a unit, for the latency (1 x 2560 1.4 us; 333 x 2304 1.6 us so and with four units a thread).
+  // Many: four, whose loads are in flight together; us with one / two / four, nv: 4096 x 2560 6.9 / 6.2 / 6.2, 4001 x
+  // 10240 47 / 22.5 / 20.1, 8192 x 16384 119 / 71 / 55 (HBM's 51).
+  const int all = fp4_atoms(a.K, FMT) * 4 * fp4_block(FMT) / 16;
+  const bool one = !a.place && a.rows <= 152 && all <= kQuantMost;
+  int threads = ((one ? all : (all + 3) / 4) + 31) / 32 * 32;
+  threads = threads > kQuantMost ? kQuantMost : threads;
+  const void* fn = a.place ? (const void*)fp4_quant_kernel<FMT, 4, true>
+                   : one   ? (const void*)fp4_quant_kernel<FMT, 1, false>
+                           : (const void*)fp4_quant_kernel<FMT, 4, false>;
+  return launch(fn, dim3((unsigned)a.group, (unsigned)(a.rows / a.group)), threads, args, pdl, s);
 }
 
 }  // namespace
@@ -386,11 +385,10 @@ cudaError_t launch_fp4_quant(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
 }
 
 cudaError_t launch_fp4_dequant(const w4a16_fp4& w, uint16_t* y, int pdl, cudaStream_t s) {
-  int parts = (w.K / 16 + kBack * kQuantThreads - 1) / (kBack * kQuantThreads);
-  void* args[] = {const_cast<w4a16_fp4*>(&w), &y, &parts};
-  const int64_t ctas = (int64_t)w.rows * w.experts * parts;
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch((const void*)fp4_dequant_kernel, dim3((unsigned)ctas), kQuantThreads, args, pdl, s);
+  const int64_t parts = (w.K / 16 + kBack * kQuantThreads - 1) / (kBack * kQuantThreads);
+  void* args[] = {const_cast<w4a16_fp4*>(&w), &y};
+  if (parts > 65535) return cudaErrorInvalidConfiguration;
+  return launch((const void*)fp4_dequant_kernel, dim3((unsigned)w.rows, (unsigned)w.experts, (unsigned)parts), kQuantThreads, args, pdl, s);
 }
 
 cudaError_t launch_fp4_route(const Fp4RouteArgs& a, int pdl, cudaStream_t s) {

@@ -879,52 +879,72 @@ def fp4_scale_bytes(N: int, K: int, format: str) -> int:
     return -(-N // 128) * -(-K // b) * 512
 
 
-@dataclass(frozen=True)
 class FP4Matrix:
-    """A matrix of e2m1 codes with block scales on the GPU: codes uint8 [E * N, K / 2],
-    two a byte, low nibble first; scales uint8 [E * fp4_scale_bytes(N, K, format)], in
-    the order of include/w4a16.h; row_scale float32 [E * N] (format "nv"; None: 1).
+    """A matrix of e2m1 codes with block scales on the GPU: ``codes`` uint8 [E * N, K / 2],
+    two a byte, low nibble first; ``scales`` uint8 [E * fp4_scale_bytes(N, K, format)], in
+    the order of include/w4a16.h; ``row_scale`` float32 [E * N] (format "nv"; None: 1).
 
     ``fp4_quant`` makes one from bf16 rows, ``gated`` from gate and up rows of a
     feed-forward block, ``from_rows`` from scales in row order (a checkpoint's)."""
 
-    codes: torch.Tensor
-    scales: torch.Tensor
-    row_scale: torch.Tensor | None
-    N: int
-    K: int
-    E: int = 1
-    format: str = "nv"
+    __slots__ = ("N", "K", "E", "format", "_codes", "_scales", "_row_scale", "_flat", "_c", "_ptr", "_dev", "_device")
 
-    def __post_init__(self):
-        n = fp4_scale_bytes(self.N, self.K, self.format)
-        if self.K <= 0 or self.K % 32 or self.N < 0 or self.E < 1:
-            raise ValueError(f"N = {self.N}, K = {self.K} (a positive multiple of 32), E = {self.E}")
-        dev = _dev_tensor(self.codes, torch.uint8, "codes").get_device()
-        _dev_tensor(self.scales, torch.uint8, "scales")
-        if self.codes.numel() != self.E * self.N * (self.K // 2):
-            raise ValueError(f"codes must hold E * N * K / 2 = {self.E * self.N * (self.K // 2)} bytes")
-        if self.scales.numel() != self.E * n:
-            raise ValueError(f"scales must hold E * fp4_scale_bytes = {self.E * n} bytes")
-        _on_device(self.scales, "scales", dev)
-        if self.row_scale is not None:
-            _dev_tensor(self.row_scale, torch.float32, "row_scale")
-            if self.row_scale.numel() != self.E * self.N:
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, row_scale: torch.Tensor | None, N: int, K: int,
+                 E: int = 1, format: str = "nv"):
+        n = fp4_scale_bytes(N, K, format)
+        if K <= 0 or K % 32 or N < 0 or E < 1:
+            raise ValueError(f"N = {N}, K = {K} (a positive multiple of 32), E = {E}")
+        dev = _dev_tensor(codes, torch.uint8, "codes").get_device()
+        _dev_tensor(scales, torch.uint8, "scales")
+        if codes.numel() != E * N * (K // 2):
+            raise ValueError(f"codes must hold E * N * K / 2 = {E * N * (K // 2)} bytes")
+        if scales.numel() != E * n:
+            raise ValueError(f"scales must hold E * fp4_scale_bytes = {E * n} bytes")
+        _on_device(scales, "scales", dev)
+        if row_scale is not None:
+            _dev_tensor(row_scale, torch.float32, "row_scale")
+            if row_scale.numel() != E * N:
                 raise ValueError("row_scale must have one factor per row")
-            _on_device(self.row_scale, "row_scale", dev)
-        c = Fp4Struct(self.codes.data_ptr(), self.scales.data_ptr(), None if self.row_scale is None else self.row_scale.data_ptr(),
-                      self.N, self.K, self.E, FP4_FORMATS[self.format])
-        object.__setattr__(self, "_c", c)
-        object.__setattr__(self, "_ptr", ctypes.addressof(c))
-        object.__setattr__(self, "_dev", dev)
+            _on_device(row_scale, "row_scale", dev)
+        self.N, self.K, self.E, self.format = N, K, E, format
+        self._codes, self._scales, self._row_scale, self._flat = codes, scales, row_scale, None
+        self._bind(codes.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(), codes.device, dev)
+
+    def _bind(self, codes, scales, row_scale, device, dev) -> None:
+        self._c = Fp4Struct(codes, scales, row_scale, self.N, self.K, self.E, FP4_FORMATS[self.format])
+        self._ptr, self._device, self._dev = ctypes.addressof(self._c), device, dev
 
     @classmethod
     def empty(cls, N: int, K: int, E: int = 1, format: str = "nv", device="cuda") -> "FP4Matrix":
         n = fp4_scale_bytes(N, K, format)
-        codes = torch.empty(E * N, K // 2, dtype=torch.uint8, device=device)
-        scales = torch.empty(E * n, dtype=torch.uint8, device=device)
+        if K <= 0 or K % 32 or N < 0 or E < 1:
+            raise ValueError(f"N = {N}, K = {K} (a positive multiple of 32), E = {E}")
+        self = cls.__new__(cls)
+        self.N, self.K, self.E, self.format = N, K, E, format
+        # scales (a multiple of 512 bytes) and codes in one block of memory; their tensors are made when asked for
+        flat = torch.empty(E * n + E * N * (K // 2), dtype=torch.uint8, device=device)
         f = torch.empty(E * N, dtype=torch.float32, device=device) if format == "nv" else None
-        return cls(codes, scales, f, N, K, E, format)
+        self._flat, self._codes, self._scales, self._row_scale = flat, None, None, f
+        at = flat.data_ptr()
+        self._bind(at + E * n, at, None if f is None else f.data_ptr(), flat.device, flat.get_device())
+        return self
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._flat[:self.E * fp4_scale_bytes(self.N, self.K, self.format)]
+        return self._scales
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n = self.E * fp4_scale_bytes(self.N, self.K, self.format)
+            self._codes = self._flat[n:].view(self.E * self.N, self.K // 2)
+        return self._codes
+
+    @property
+    def row_scale(self) -> torch.Tensor | None:
+        return self._row_scale
 
     @classmethod
     def gated(cls, gate: torch.Tensor, up: torch.Tensor, format: str = "nv", stream=None) -> "FP4Matrix":
@@ -955,6 +975,9 @@ class FP4Matrix:
     @property
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.row_scale) if t is not None)
+
+    def __repr__(self) -> str:
+        return f"FP4Matrix(N={self.N}, K={self.K}, E={self.E}, format={self.format!r}, device={self._device})"
 
 
 def _fp4_x(x: torch.Tensor, K: int, dev: int | None):
@@ -987,7 +1010,8 @@ def fp4_quant(x: torch.Tensor, format: str = "nv", out: FP4Matrix | None = None,
     elif (out.N * out.E, out.K, out.format) != (M, K, format):
         raise ValueError(f"out must have {M} rows of {K} codes, format {format}")
     dev = x.get_device()
-    _on_device(out.codes, "out", dev)
+    if out._dev != dev:
+        raise ValueError(f"out is on cuda:{out._dev}, x on cuda:{dev}")
     rc = lib().w4a16_fp4_quant(x.data_ptr(), stride, out._ptr, _stream_on(stream, dev))
     if rc:
         _raise(rc)
@@ -999,7 +1023,7 @@ def fp4_dequant(w: FP4Matrix, out: torch.Tensor | None = None, stream=None) -> t
     shape = (w.N, w.K) if w.E == 1 else (w.E, w.N, w.K)
     raw = _stream_on(stream, w._dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=w.codes.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=w._device)
     else:
         _fp4_out(out, shape, w._dev)
     rc = lib().w4a16_fp4_dequant(w._ptr, out.data_ptr(), raw)
@@ -1038,9 +1062,10 @@ def _fp4_space(need: int, workspace, raw: int, stream, w: FP4Matrix):
     if workspace is not None:
         _on_device(workspace, "workspace", w._dev)
         return (workspace, *_ws_args(workspace))
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # the call's stream is the current one
-        t, at, n = _kv_workspace(need, raw, w.codes.device)
-    return t, at, n
+    if stream is None:
+        return _kv_workspace(need, raw, w._device)
+    with torch.cuda.stream(stream):  # the call's stream is the current one
+        return _kv_workspace(need, raw, w._device)
 
 
 def _fp4_product(x, w: FP4Matrix, act, out, stream, workspace):
@@ -1053,12 +1078,13 @@ def _fp4_product(x, w: FP4Matrix, act, out, stream, workspace):
         M, lead = x.N, (x.N,)
         if x.K != w.K or x.format != w.format or x.E != 1:
             raise ValueError(f"x has K={x.K}, format {x.format}, E={x.E}; weights have K={w.K}, format {w.format}")
-        _on_device(x.codes, "x", w._dev)
+        if x._dev != w._dev:
+            raise ValueError(f"x is on cuda:{x._dev}, w on cuda:{w._dev}")
     else:
         M, stride = _fp4_x(x, w.K, w._dev)
         lead = x.shape[:-1]
     if out is None:
-        out = torch.empty((*lead, cols), dtype=torch.bfloat16, device=w.codes.device)
+        out = torch.empty((*lead, cols), dtype=torch.bfloat16, device=w._device)
     else:
         _fp4_out(out, (M, cols), w._dev)
     if isinstance(x, FP4Matrix):
@@ -1104,7 +1130,7 @@ def fp4_mm_id(x: torch.Tensor, w: FP4Matrix, ids: torch.Tensor, act: str | None 
     shape = (*ids.shape, w.N if a == 0 else w.N // 2)
     raw = _stream_on(stream, w._dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=w.codes.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=w._device)
     else:
         _fp4_out(out, shape, w._dev)
     keep, ws, wn = _fp4_space(_fp4_mm_id_bytes(T, top, w.K, w.E, w._c.format), workspace, raw, stream, w)
