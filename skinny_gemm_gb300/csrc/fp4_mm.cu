@@ -69,6 +69,8 @@ struct Geo {
 struct Maps {
   CUtensorMap w;  // u8 [experts * N][K / 2], box 128 bytes x 128 rows, 128-byte swizzle
   CUtensorMap x;  // u8 [x rows][K / 2], box 128 bytes x NT rows
+  CUtensorMap ws;  // scales, boxes of one row tile
+  CUtensorMap xs;
 };
 
 // One sum of row `row` of W and place `at` of x, whole warps (gate and up rows are neighbours).
@@ -165,18 +167,17 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
     // ---- TMA producer ----
     if (lane == 0) {
       const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
-      auto scale_bytes = [&](int k) { return (uint32_t)(min(kAtoms, p.atoms - k * kAtoms) * kFp4Atom); };
-      auto load_w = [&](int s, int k, int wrow, const uint8_t* ws) {
-        mbar_expect_tx(full(s), kWTile + G::kX + 2 * scale_bytes(k));
+      auto load_w = [&](int s, int k, int wrow, int ws) {
+        mbar_expect_tx(full(s), kWTile + G::kX + 2 * kAtoms * kFp4Atom);
         tma_load_2d(W_of(s), &maps.w, k * 128, wrow, full(s), stream);
-        bulk_load(SW_of(s), ws + k * kAtoms * kFp4Atom, scale_bytes(k), full(s), stream);
+        tma_load_3d(SW_of(s), &maps.ws, 0, k * kAtoms, ws, full(s), stream);
       };
       int ahead = 0;  // stages whose W is requested already
       if (p.early) {
         if (first < units) {
           const int wt = (int)(first % p.row_tiles);
           for (; ahead < S && k0 + ahead < k1; ++ahead)
-            load_w(ahead, k0 + ahead, wt * kWRows, p.ws + (int64_t)wt * p.atoms * kFp4Atom);
+            load_w(ahead, k0 + ahead, wt * kWRows, wt);
         }
         pdl_wait();
       }
@@ -191,8 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
           place = p.tiles[xt].place;
         }
         const int wrow = (int)(expert * p.N + (int64_t)wt * kWRows);
-        const uint8_t* ws = p.ws + (expert * p.row_tiles + wt) * p.atoms * kFp4Atom;
-        const uint8_t* xs = p.xs + (int64_t)(place / kFp4Rows) * p.atoms * kFp4Atom;
+        const int ws = (int)(expert * p.row_tiles) + wt, xs = place / kFp4Rows;
         for (int k = k0; k < k1; ++k, ++it) {
           if (it >= (uint32_t)S && !mbar_wait_parked(empty(s), parity, 1000, limit)) {
             timeout();
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
           }
           if (it >= (uint32_t)ahead) load_w(s, k, wrow, ws);
           tma_load_2d(X_of(s), &maps.x, k * 128, place, full(s), keep);
-          bulk_load(SX_of(s), xs + k * kAtoms * kFp4Atom, scale_bytes(k), full(s), keep);
+          tma_load_3d(SX_of(s), &maps.xs, 0, k * kAtoms, xs, full(s), keep);
           if (++s == S) s = 0, parity ^= 1;
         }
       }
@@ -408,6 +408,8 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
   if (cudaError_t e = encode_map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.xc, a.w.K / 2, a.x_rows, a.w.K / 2, 128, NT,
                                     CU_TENSOR_MAP_SWIZZLE_128B))
     return e;
+  if (cudaError_t e = fp4_scale_map(&maps.ws, a.w.scales, (int64_t)p.row_tiles * a.w.experts, a.w.K, FMT, 1)) return e;
+  if (cudaError_t e = fp4_scale_map(&maps.xs, a.xs, (a.x_rows + 127) / 128, a.w.K, FMT, 1)) return e;
   const int64_t units = (int64_t)p.row_tiles * (a.tiles ? a.max_tiles : p.x_tiles);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.split > 1 ? units * p.split : units < 2 * sms ? units : 2 * sms));

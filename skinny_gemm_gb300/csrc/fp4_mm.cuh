@@ -7,15 +7,14 @@
 #include <cuda_runtime.h>
 
 #include "fp4.cuh"
+#include "launch.h"
 
 namespace w4a16 {
 
 constexpr int kFp4StageK = 256;  // codes of K per stage: 128 bytes a row
 
 struct Fp4MmParams {
-  const uint8_t* ws;  // scales and row factors (nullptr: 1) of W and of x
-  const uint8_t* xs;
-  const float* wf;
+  const float* wf;  // row factors of W and of x (nullptr: 1)
   const float* xf;
   uint16_t* y;
   const Fp4Tile* tiles;  // routed, or nullptr
@@ -45,8 +44,6 @@ __device__ __forceinline__ uint32_t fp4_bf16x2(float lo, float hi) {
 
 inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
   Fp4MmParams p;
-  p.ws = a.w.scales;
-  p.xs = a.xs;
   p.wf = a.w.row_scale;
   p.xf = a.xf;
   p.y = a.y;
@@ -67,6 +64,15 @@ inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
   p.early = 0;
   p.fault_wait = a.fault_wait;
   return p;
+}
+
+// The scales' map: [row tiles][atoms along K][128 words], boxes of `tiles` x a stage's atoms (what lies past the end
+// is read as zeros).  Tiled copies: as untiled ones of 2 KB, three a stage, they took 330 cycles of the copy engine.
+inline cudaError_t fp4_scale_map(CUtensorMap* map, const void* scales, int64_t row_tiles, int K, int format, int tiles) {
+  const int atoms = fp4_atoms(K, format);
+  const int64_t dims[3] = {kFp4Atom / 4, atoms, row_tiles}, strides[2] = {kFp4Atom, (int64_t)atoms * kFp4Atom};
+  const int box[3] = {kFp4Atom / 4, format == W4A16_FP4_MX ? 2 : 4, tiles};
+  return encode_map_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s);

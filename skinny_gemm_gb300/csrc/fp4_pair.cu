@@ -8,16 +8,16 @@
 // rows of W (half of them in each CTA's shared memory): a CTA takes 38 KB from
 // L2 for each 128 x 256 x 256 products, half of what one alone would.
 //
-// CTA: ten warps, persistent over tiles.
+// CTA: fourteen warps, persistent over tiles.
 //   warp 0     TMA producer of this CTA's x and W rows and their scales
 //   warp 1     leader: scales from shared to tensor memory of both CTAs, MMAs
 //              and commits; the other CTA: passes "stage landed" on
-//   warps 2-9  epilogue: 32 lanes x half of the columns each
-// Tensor memory: two accumulators of 256 columns that share 160, beside three
-// sets of scales (48 columns each; a set is written again when the MMAs of three
-// stages before are done: with two the MMAs waited for the copies).  The
-// epilogue reads the shared columns first, and lets the next tile's MMAs go when
-// it has them.
+//   warps 2-13 epilogue: 32 lanes x a third of the columns each
+// Tensor memory: two accumulators of 256 columns that share 160 (mx: 128), beside
+// three sets of scales of 48 columns (mx: five of 24).  A set is written again
+// when the MMAs that read it are done; with two sets the MMAs waited for the
+// copies.  The epilogue takes the shared columns into registers first, and lets
+// the next tile's MMAs go when it has them.
 // Waits are bounded as in fp4_mm.cu; the two CTAs leave together.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -40,18 +40,30 @@ constexpr int kWTile = 128 * 128;  // its half of W's rows (up to 128)
 constexpr int kXScale = 2048, kWScale = 4096;
 constexpr int kStage = kXTile + kWTile + kXScale + kWScale;
 constexpr int S = 5;
-constexpr int kEpi = 8;  // epilogue warps
+constexpr int kEpi = 12;  // epilogue warps, three for each 32 lanes
 constexpr int kThreads = 32 * (2 + kEpi);
-constexpr int kSetCols = 48;                        // 4 atoms of x's scales (4 columns) and W's (8)
-constexpr int kAccStep = 96, kSetsAt = 352, kSets = 3;  // the second accumulator's first column, the scales'
+// Tensor memory's columns: two accumulators of 256, the second from kAccStep on, then the scale sets (a stage's atoms of
+// x's scales, 4 columns each, and of W's, 8).
+template <int FMT>
+struct Cols {
+  static constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;  // of a stage
+  static constexpr int kSet = 12 * kAtoms;
+  static constexpr int kSets = FMT == W4A16_FP4_MX ? 5 : 3;
+  static constexpr int kAccStep = FMT == W4A16_FP4_MX ? 128 : 96;
+  static constexpr int kSetsAt = kAccStep + 256;
+  static constexpr int kShared = 8 - kAccStep / 32;  // 32s of columns that both accumulators have
+  static_assert(kSetsAt + kSets * kSet <= 512 && kShared <= 6, "the SM's tensor memory");
+};
 constexpr int kBars = 3 * S + 6;
 constexpr int kTurn = 2048;  // bytes in which an epilogue warp turns 32 rows x 32 columns
-constexpr int kSmem = S * kStage + kEpi * (kTurn + 512) + kBars * 8 + 16 + 1024;
-static_assert(kSmem <= 227 * 1024 && kSetsAt + kSets * kSetCols <= 512, "a CTA's shared memory and the SM's tensor memory");
+constexpr int kSmem = S * kStage + kEpi * (kTurn + 384) + kBars * 8 + 16 + 1024;
+static_assert(kSmem <= 227 * 1024, "a CTA's shared memory");
 
 struct Maps {
   CUtensorMap w;  // u8 [experts * N][K / 2], box 128 bytes x TN / 2 rows, 128-byte swizzle
   CUtensorMap x;  // u8 [x rows][K / 2], box 128 bytes x 128 rows
+  CUtensorMap ws;  // scales, boxes of two row tiles
+  CUtensorMap xs;  // ... of one
 };
 
 struct PairParams {
@@ -72,15 +84,16 @@ __device__ __forceinline__ void unit_tile(int64_t u, int x_tiles, int n_tiles, i
 
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_constant__ Maps maps, PairParams pp) {
-  constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;
+  using T = Cols<FMT>;
+  constexpr int kAtoms = T::kAtoms, kSets = T::kSets;
   const Fp4MmParams& p = pp.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const uint32_t turns = sb + S * kStage, bars = turns + kEpi * (kTurn + 512);
-  float* s_wf = reinterpret_cast<float*>(base + S * kStage + kEpi * kTurn);  // W's factors for an epilogue warp's columns: four 32s each
+  const uint32_t turns = sb + S * kStage, bars = turns + kEpi * (kTurn + 384);
+  float* s_wf = reinterpret_cast<float*>(base + S * kStage + kEpi * kTurn);  // W's factors for an epilogue warp's columns: three 32s each
   auto X_of = [&](int s) { return sb + (uint32_t)(s * kStage); };
   auto W_of = [&](int s) { return X_of(s) + kXTile; };
   auto SX_of = [&](int s) { return W_of(s) + kWTile; };
@@ -146,25 +159,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
         }
         place += 128 * (int)rank;
         const int wrow = (int)(expert * p.N) + nt * tn + (int)rank * (tn / 2);
-        // 128-row tiles of W's scales that the tile's rows touch: one or two, fewer past the end
-        const int wt = nt * tn / 128, wtiles = min((nt * tn % 128 + tn + 127) / 128, p.row_tiles - wt);
-        const uint8_t* ws = p.ws + (expert * p.row_tiles + wt) * p.atoms * kFp4Atom;
-        const uint8_t* xs = p.xs + (int64_t)(place / kFp4Rows) * p.atoms * kFp4Atom;
-        // the last tile may have no rows of x in the second CTA, nor scales
-        const bool has_x = p.tiles || place < p.M;
+        // (the tile's rows of W touch one or two 128-row tiles of scales)
+        const int wt = (int)(expert * p.row_tiles) + nt * tn / 128, xs = place / kFp4Rows;
         for (int k = 0; k < ns; ++k, ++it) {
           const int s = (int)(it % S);
           if (it >= (uint32_t)S && !mbar_wait_parked(empty(s), ((it / S) - 1) & 1, 1000, limit)) {
             timeout();
             break;
           }
-          const uint32_t bytes = (uint32_t)(min(kAtoms, p.atoms - k * kAtoms) * kFp4Atom);
-          mbar_expect_tx(full(s), kXTile + (uint32_t)(tn / 2) * 128 + ((has_x ? 1 : 0) + (uint32_t)wtiles) * bytes);
+          mbar_expect_tx(full(s), kXTile + (uint32_t)(tn / 2) * 128 + 3 * kAtoms * kFp4Atom);
           tma_load_2d(X_of(s), &maps.x, k * 128, place, full(s), keep);
           tma_load_2d(W_of(s), &maps.w, k * 128, wrow, full(s), keep);
-          if (has_x) bulk_load(SX_of(s), xs + k * kAtoms * kFp4Atom, bytes, full(s), keep);
-          for (int i = 0; i < wtiles; ++i)
-            bulk_load(SW_of(s) + i * 2048, ws + ((int64_t)i * p.atoms + k * kAtoms) * kFp4Atom, bytes, full(s), keep);
+          tma_load_3d(SX_of(s), &maps.xs, 0, k * kAtoms, xs, full(s), keep);
+          tma_load_3d(SW_of(s), &maps.ws, 0, k * kAtoms, wt, full(s), keep);
         }
       }
     }
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
         break;
       }
       tc_fence_after_sync();
-      const uint32_t acc = (uint32_t)(b * kAccStep);
+      const uint32_t acc = (uint32_t)(b * T::kAccStep);
       const uint32_t w_col = (uint32_t)(nt * tn % 128 / 32);
       bool ok = true;
       for (int k = 0; k < ns; ++k, ++it) {
@@ -201,12 +208,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
         tc_fence_after_sync();
         const uint64_t at = (uint64_t)(uint32_t)(s * (kStage >> 4));
         const uint64_t xd = xd0 + at, wd = wd0 + at, sx = sx0 + at, sw = sw0 + at;
-        const uint32_t cx = (uint32_t)(kSetsAt + set * kSetCols), cw = cx + 16;
+        const uint32_t cx = (uint32_t)(T::kSetsAt + set * T::kSet), cw = cx + 4 * kAtoms;
         const int atoms = p.atoms - k * kAtoms, steps = (p.K - k * kFp4StageK + 63) / 64;
         auto copy = [&](int a) {
           tmem_copy_scales2(go, cx + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
           tmem_copy_scales2(go, cw + 8 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
-          tmem_copy_scales2(go, cw + 8 * a + 4, sw + (uint64_t)((2048 + a * kFp4Atom) >> 4));
+          tmem_copy_scales2(go, cw + 8 * a + 4, sw + (uint64_t)((kAtoms + a) * (kFp4Atom >> 4)));
         };
         auto mma = [&](int j) {
           if (FMT == W4A16_FP4_MX)
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     }
   } else {
     // ---- epilogue ----
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int q = warp & 3, third = (warp - 2) >> 2;
     const uint32_t to = cluster_map(bars, 0) - bars;
     uint32_t n = 0;
     for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
@@ -272,13 +279,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       const int m = mine ? (p.row ? p.row[place + r] : place + r) : 0;
       const float fx = mine && p.xf ? p.xf[place + r] : 1.0f;
       const int64_t cols = p.act == W4A16_FP4_LINEAR ? p.N : p.N / 2;
-      float* wf = s_wf + 128 * (warp - 2);
+      float* wf = s_wf + 96 * (warp - 2);
       const bool factors = p.wf || p.xf;
+      // The i-th 32 columns to be read, those that both accumulators have first: the second's first and the first's last
+      // ones.  Each of the three warps of 32 lanes takes every third.
+      auto column = [&](int i) { return 32 * (b ? i : (i + T::kAccStep / 32) % 8); };
       if (factors) {
         __syncwarp();
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int i = half + 2 * g, c = nt * tn + 32 * (b ? i : (i + 3) % 8) + lane;
+        for (int g = 0; g < 3; ++g) {
+          const int c = nt * tn + column(third + 3 * g) + lane;
           wf[32 * g + lane] = !p.wf ? 1.0f : c < p.N ? p.wf[expert * p.N + c] : 0.f;
         }
         __syncwarp();
@@ -288,29 +298,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
         break;
       }
       tc_fence_after_sync();
-      const uint32_t acc = (uint32_t)(b * kAccStep) + ((uint32_t)(32 * q) << 16);
-      // Columns 96 .. 255 of tensor memory are both accumulators', the last five 32s of the first and the first five of
-      // the second: those first.  The warps' halves take every other 32.
-#pragma unroll 1
-      for (int i = half; i < 8; i += 2) {
-        const int c = 32 * (b ? i : (i + 3) % 8);
-        const int n0 = nt * tn + c;
-        const bool any = c < tn && n0 < p.N;
-        float v[32];
-        if (any) {
-          tmem_ld32(acc + c, v);
-          tmem_wait_ld();
-        }
-        if (i == 3 || i == 4) {  // this warp's last of the five
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(part_free(b) + to);
-        }
-        if (!any) continue;
+      const uint32_t acc = (uint32_t)(b * T::kAccStep) + ((uint32_t)(32 * q) << 16);
+      auto exists = [&](int i) { return i < 8 && column(i) < tn && nt * tn + column(i) < p.N; };
+      auto put = [&](int i, float (&v)[32]) {
+        if (!exists(i)) return;
+        const int n0 = nt * tn + column(i);
         if (factors) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(wf + 16 * (i - half) + j);
+            const float4 f = *reinterpret_cast<const float4*>(wf + 32 * (i / 3) + j);
             v[j] *= fx * f.x;
             v[j + 1] *= fx * f.y;
             v[j + 2] *= fx * f.z;
@@ -359,10 +355,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
             }
           }
         }
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_free(b) + to);
+      };
+      auto arrive = [&](uint32_t bar) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(bar + to);
+      };
+      // this warp's 32s: third, third + 3, third + 6; the first is always shared, the second may be
+      float v[32], w[32];
+      const bool two = third + 3 < T::kShared;
+      if (exists(third)) tmem_ld32(acc + column(third), v);
+      if (two && exists(third + 3)) tmem_ld32(acc + column(third + 3), w);
+      tmem_wait_ld();
+      arrive(part_free(b));
+      put(third, v);
+      if (!two && exists(third + 3)) tmem_ld32(acc + column(third + 3), w);
+      if (exists(third + 6)) tmem_ld32(acc + column(third + 6), v);
+      tmem_wait_ld();
+      arrive(acc_free(b));
+      put(third + 3, w);
+      put(third + 6, v);
     }
   }
 
@@ -414,6 +426,8 @@ cudaError_t launch_t(const Fp4MmArgs& a, const PairParams& p, int64_t units, int
   if (cudaError_t e = encode_map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.xc, a.w.K / 2, a.x_rows, a.w.K / 2, 128, 128,
                                     CU_TENSOR_MAP_SWIZZLE_128B))
     return e;
+  if (cudaError_t e = fp4_scale_map(&maps.ws, a.w.scales, (int64_t)p.p.row_tiles * a.w.experts, a.w.K, FMT, 2)) return e;
+  if (cudaError_t e = fp4_scale_map(&maps.xs, a.xs, (a.x_rows + 127) / 128, a.w.K, FMT, 1)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (units < sms / 2 ? units : sms / 2)));
   cfg.blockDim = dim3(kThreads);

@@ -67,6 +67,9 @@ cudaError_t launch_tc_group(const GroupItem* items, int count, int M, int row0, 
 // `outer` rows, rows `row_bytes` apart) with boxes of box_inner x box_outer.
 cudaError_t encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t inner,
                           int64_t outer, int64_t row_bytes, int box_inner, int box_outer, CUtensorMapSwizzle swizzle);
+// ... of a 3-D tensor (strides in bytes of the two outer dimensions).
+cudaError_t encode_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, const int64_t (&dims)[3],
+                          const int64_t (&strides)[2], const int (&box)[3], CUtensorMapSwizzle swizzle);
 // Activation rows from which w4a16_mm runs the tcgen05 prefill kernel (below,
 // the skinny tile kernel taking eight rows at a time is faster).
 constexpr int kPrefillMinM = 33;

@@ -143,6 +143,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int cx, int cy, int cz, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+      ::"r"(dst), "l"(map), "r"(cx), "r"(cy), "r"(cz), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // Four bytes from global to shared memory; cp_async_arrive lets the thread's
 // copies so far count as one arrival on `bar` (included in its count) when
 // they have landed.

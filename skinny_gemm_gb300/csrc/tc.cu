@@ -2529,6 +2529,17 @@ cudaError_t encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, const int64_t (&dims)[3],
+                          const int64_t (&strides)[2], const int (&box)[3], CUtensorMapSwizzle swizzle) {
+  if (cudaError_t e = get_encoder()) return e;
+  cuuint64_t d[3], st[2] = {(cuuint64_t)strides[0], (cuuint64_t)strides[1]};
+  cuuint32_t b[3], estr[3] = {1, 1, 1};
+  for (int i = 0; i < 3; ++i) d[i] = (cuuint64_t)dims[i], b[i] = (cuuint32_t)box[i];
+  CUresult r = g_encode(map, type, 3, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // K % 512 != 0: the persistent kernel's per-unit parameter slots fit next to
 // a two-stage ring with per-stage copies of eight activation rows (the most
 // shared memory any chunk takes).
