@@ -234,28 +234,30 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
         const uint32_t cw = tmem + (uint32_t)(NB * NT + s * kSetCols), cx = cw + 16;
         const int atoms = p.atoms - k * kAtoms, steps = (p.K - k * kFp4StageK + 63) / 64;
         auto copy = [&](int a) {
-          tmem_copy_scales(go, cw + 4 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
-          tmem_copy_scales(go, cx + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
+          tmem_copy_scales(cw + 4 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
+          tmem_copy_scales(cx + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
         };
         auto mma = [&](int j) {
           const bool add = k > k0 || j > 0;
           if (FMT == W4A16_FP4_MX)
-            umma_mxf4(go, acc, wd + 2 * j, xd + 2 * j, kIdesc | umma_idesc_scale_byte(2 * (j & 1)), cw + 4 * (j / 2), cx + 4 * (j / 2), add);
+            umma_mxf4(acc, wd + 2 * j, xd + 2 * j, kIdesc | umma_idesc_scale_byte(2 * (j & 1)), cw + 4 * (j / 2), cx + 4 * (j / 2), add);
           else
-            umma_nvf4(go, acc, wd + 2 * j, xd + 2 * j, kIdesc, cw + 4 * j, cx + 4 * j, add);
+            umma_nvf4(acc, wd + 2 * j, xd + 2 * j, kIdesc, cw + 4 * j, cx + 4 * j, add);
         };
-        if (steps >= 4) {
+        if (elect_one()) {
+          if (steps >= 4) {
 #pragma unroll
-          for (int a = 0; a < kAtoms; ++a) copy(a);
+            for (int a = 0; a < kAtoms; ++a) copy(a);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma(j);
-        } else {  // the end of K
+            for (int j = 0; j < 4; ++j) mma(j);
+          } else {  // the end of K
 #pragma unroll
-          for (int a = 0; a < kAtoms; ++a)
-            if (a < atoms) copy(a);
+            for (int a = 0; a < kAtoms; ++a)
+              if (a < atoms) copy(a);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < steps) mma(j);
+            for (int j = 0; j < 4; ++j)
+              if (j < steps) mma(j);
+          }
         }
         umma_commit_if(go, empty(s));
         if (++s == S) s = 0, parity ^= 1;

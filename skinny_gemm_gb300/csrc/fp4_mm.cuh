@@ -24,7 +24,7 @@ struct Fp4MmParams {
   int N, K, M, act;
   int row_tiles, x_tiles;  // 128-row tiles of an expert's W; activation tiles (not routed)
   int atoms, stages;       // scale atoms along K; stages along K
-  int vec;                 // y's rows take 8-byte stores (fp4_pair.cu: 16)
+  int vec;                 // y's rows take 8-byte stores (fp4_pair.cu: of how many bytes, 32, 16 or 0)
   int split, early;        // CTAs that share a tile's K; W may be fetched before the wait for the kernel before
   int fault_wait;
 };

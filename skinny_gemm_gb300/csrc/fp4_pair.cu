@@ -3,7 +3,7 @@
 //
 // The arithmetic is fp4_mm.cu's.  Here x is the MMA's M: a tensor-memory lane
 // is a row of x and the columns run along y's row, so that a thread holds
-// neighbours of y (stores of 16 bytes; gate and up of a pair side by side).
+// neighbours of y (stores of 32 bytes; gate and up of a pair side by side).
 // tcgen05.mma.cta_group::2 multiplies 256 rows of x (128 in each CTA) with TN
 // rows of W (half of them in each CTA's shared memory): a CTA takes 38 KB from
 // L2 for each 128 x 256 x 256 products, half of what one alone would.
@@ -55,8 +55,7 @@ struct Cols {
   static_assert(kSetsAt + kSets * kSet <= 512 && kShared <= 6, "the SM's tensor memory");
 };
 constexpr int kBars = 3 * S + 6;
-constexpr int kTurn = 2048;  // bytes in which an epilogue warp turns 32 rows x 32 columns
-constexpr int kSmem = S * kStage + kEpi * (kTurn + 384) + kBars * 8 + 16 + 1024;
+constexpr int kSmem = S * kStage + kEpi * 384 + kBars * 8 + 16 + 1024;
 static_assert(kSmem <= 227 * 1024, "a CTA's shared memory");
 
 struct Maps {
@@ -72,13 +71,27 @@ struct PairParams {
   int n_tiles;  // tiles along W's rows
 };
 
-// Which tile a pair's unit is: eight activation tiles by all of W's, then the next eight, so that the pairs at work at a
-// time share what they read.
+// (a, b) times (x, y) and f, two products at a time.
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y, float f) {
+  asm("{ .reg .b64 p, q, r; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %3}; mov.b64 r, {%4, %4};\n"
+      "mul.rn.f32x2 q, q, r; mul.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p; }"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y), "f"(f));
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Which tile a pair's unit is: sixteen activation tiles by all of W's, then the next sixteen, so that the pairs at work at
+// a time share what they read (8192 x 16384 x 16384 with 4 / 8 / 16: 641 / 596 / 586 us).
 __device__ __forceinline__ void unit_tile(int64_t u, int x_tiles, int n_tiles, int& xt, int& nt) {
-  const int64_t per = 8LL * n_tiles;
+  const int64_t per = 16LL * n_tiles;
   const int g = (int)(u / per), r = (int)(u % per);
-  const int wide = min(8, x_tiles - 8 * g);
-  xt = 8 * g + r % wide;
+  const int wide = min(16, x_tiles - 16 * g);
+  xt = 16 * g + r % wide;
   nt = r / wide;
 }
 
@@ -92,8 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   const uint32_t sb = smem_u32(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const uint32_t turns = sb + S * kStage, bars = turns + kEpi * (kTurn + 384);
-  float* s_wf = reinterpret_cast<float*>(base + S * kStage + kEpi * kTurn);  // W's factors for an epilogue warp's columns: three 32s each
+  const uint32_t bars = sb + S * kStage + kEpi * 384;
+  float* s_wf = reinterpret_cast<float*>(base + S * kStage);  // W's factors for an epilogue warp's columns: three 32s each
   auto X_of = [&](int s) { return sb + (uint32_t)(s * kStage); };
   auto W_of = [&](int s) { return X_of(s) + kXTile; };
   auto SX_of = [&](int s) { return W_of(s) + kWTile; };
@@ -211,29 +224,31 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
         const uint32_t cx = (uint32_t)(T::kSetsAt + set * T::kSet), cw = cx + 4 * kAtoms;
         const int atoms = p.atoms - k * kAtoms, steps = (p.K - k * kFp4StageK + 63) / 64;
         auto copy = [&](int a) {
-          tmem_copy_scales2(go, cx + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
-          tmem_copy_scales2(go, cw + 8 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
-          tmem_copy_scales2(go, cw + 8 * a + 4, sw + (uint64_t)((kAtoms + a) * (kFp4Atom >> 4)));
+          tmem_copy_scales2(cx + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
+          tmem_copy_scales2(cw + 8 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
+          tmem_copy_scales2(cw + 8 * a + 4, sw + (uint64_t)((kAtoms + a) * (kFp4Atom >> 4)));
         };
         auto mma = [&](int j) {
           if (FMT == W4A16_FP4_MX)
-            umma2_mxf4(go, acc, xd + 2 * j, wd + 2 * j, idesc | umma_idesc_scale_byte(2 * (j & 1)), cx + 4 * (j / 2),
+            umma2_mxf4(acc, xd + 2 * j, wd + 2 * j, idesc | umma_idesc_scale_byte(2 * (j & 1)), cx + 4 * (j / 2),
                        cw + 8 * (j / 2) + w_col, k > 0 || j > 0);
           else
-            umma2_nvf4(go, acc, xd + 2 * j, wd + 2 * j, idesc, cx + 4 * j, cw + 8 * j + w_col, k > 0 || j > 0);
+            umma2_nvf4(acc, xd + 2 * j, wd + 2 * j, idesc, cx + 4 * j, cw + 8 * j + w_col, k > 0 || j > 0);
         };
-        if (steps >= 4) {
+        if (elect_one()) {
+          if (steps >= 4) {
 #pragma unroll
-          for (int a = 0; a < kAtoms; ++a) copy(a);
+            for (int a = 0; a < kAtoms; ++a) copy(a);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma(j);
-        } else {  // the end of K
+            for (int j = 0; j < 4; ++j) mma(j);
+          } else {  // the end of K
 #pragma unroll
-          for (int a = 0; a < kAtoms; ++a)
-            if (a < atoms) copy(a);
+            for (int a = 0; a < kAtoms; ++a)
+              if (a < atoms) copy(a);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < steps) mma(j);
+            for (int j = 0; j < 4; ++j)
+              if (j < steps) mma(j);
+          }
         }
         umma_commit2_if(go, empty(s));
         if (++s == S) s = 0, parity ^= 1;
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       }
       const int r = 128 * (int)rank + 32 * q + lane;
       const bool mine = r < count;
-      const int m = mine ? (p.row ? p.row[place + r] : place + r) : 0;
+      const int64_t m = mine ? (p.row ? p.row[place + r] : place + r) : 0;
       const float fx = mine && p.xf ? p.xf[place + r] : 1.0f;
       const int64_t cols = p.act == W4A16_FP4_LINEAR ? p.N : p.N / 2;
       float* wf = s_wf + 96 * (warp - 2);
@@ -307,14 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(wf + 32 * (i / 3) + j);
-            v[j] *= fx * f.x;
-            v[j + 1] *= fx * f.y;
-            v[j + 2] *= fx * f.z;
-            v[j + 3] *= fx * f.w;
+            mul2(v[j], v[j + 1], f.x, f.y, fx);
+            mul2(v[j + 2], v[j + 3], f.z, f.w, fx);
           }
         }
-        // A lane holds a row of the tile; stored as they are, the 32 rows of a warp would be 32 lines an instruction.
-        // They go through shared memory so that four lanes (gated: two) store 64 (32) bytes of a row.
+        // A lane holds a row of the tile and stores 32 bytes of it at a time: whole sectors.  (4096 x 10240 x 2560, us: 45
+        // so, 62 in stores of 16 bytes, 50 turned through shared memory to 64 bytes a row.)
         const bool linear = p.act == W4A16_FP4_LINEAR;
         uint32_t o[16];
         if (linear) {
@@ -325,27 +338,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
           for (int j = 0; j < 8; ++j)
             o[j] = fp4_bf16x2(fp4_activate(v[4 * j], p.act) * v[4 * j + 1], fp4_activate(v[4 * j + 2], p.act) * v[4 * j + 3]);
         }
-        const int n1 = linear ? n0 : n0 / 2;
-        if (p.vec && n0 + 32 <= p.N) {
-          const uint32_t turn = turns + (uint32_t)((warp - 2) * kTurn);
-          auto at = [&](int row, int unit) { return turn + (uint32_t)(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4)); };
-          const int units = linear ? 4 : 2;  // 16 bytes each
+        if (!mine) return;
+        uint16_t* y = p.y + m * cols + (linear ? n0 : n0 / 2);
+        const bool whole = n0 + 32 <= p.N;
+        if (whole && p.vec == 32) {
+          store32(y, o);
+          if (linear) store32(y + 16, o + 8);
+        } else if (whole && p.vec == 16) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (j < units) sts128(at(lane, j), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          __syncwarp();
-          const int unit = lane % units, per = 32 / units;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < units) {
-              const int row = per * j + lane / units;
-              const uint4 w = lds128(at(row, unit));
-              const int64_t to_m = __shfl_sync(0xffffffffu, m, row);
-              if (r - lane + row < count) *reinterpret_cast<uint4*>(p.y + to_m * cols + n1 + 8 * unit) = w;
-            }
-          __syncwarp();
-        } else if (mine) {
-          uint16_t* y = p.y + m * cols + n1;
+            if (linear || j < 2) *reinterpret_cast<uint4*>(y + 8 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        } else {
           const int left = (linear ? p.N - n0 : (p.N - n0) / 2);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -396,6 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
 }
 
 // ---- host side ------------------------------------------------------------------------
+
+constexpr int kPairs = 76;  // of SMs
 
 std::mutex g_mu;
 int g_sms[64] = {};
@@ -450,9 +455,16 @@ cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   PairParams p;
   p.p = fp4_params(a, 256);
   p.tn = 256;
+  int64_t best = INT64_MAX;
+  for (int tn = 256; tn >= 128; tn -= 64) {
+    const int64_t tiles = (int64_t)((a.w.rows + tn - 1) / tn) * (a.tiles ? a.max_tiles : p.p.x_tiles);
+    const int64_t cost = (tiles + kPairs - 1) / kPairs * (tn + 64);
+    if (cost < best) best = cost, p.tn = tn;
+  }
   p.n_tiles = (a.w.rows + p.tn - 1) / p.tn;
   const int cols = a.act == W4A16_FP4_LINEAR ? a.w.rows : a.w.rows / 2;  // of a row of y
-  p.p.vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.y);
+  p.p.vec = cols % 16 == 0 && at % 32 == 0 ? 32 : cols % 8 == 0 && at % 16 == 0 ? 16 : 0;
   const int64_t units = (int64_t)p.n_tiles * (a.tiles ? a.max_tiles : p.p.x_tiles);
   return a.w.format == W4A16_FP4_MX ? launch_t<W4A16_FP4_MX>(a, p, units, pdl, s) : launch_t<W4A16_FP4_NV>(a, p, units, pdl, s);
 }
