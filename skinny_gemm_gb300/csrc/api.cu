@@ -823,10 +823,15 @@ int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a1
   if (int rc = flag_pointer(&flags)) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* factor = w->format == W4A16_FP4_NV ? reinterpret_cast<float*>(ws + sp.factor) : nullptr;
-  Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, M, w->K, M, w->format, nullptr, 1, nullptr, 0};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaError_t e = launch_fp4_quant(q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm launch");
   Fp4MmArgs a = {};
+  if (fp4_mm_fuses(*w, M)) {
+    a.x = x;
+    a.x_stride = x_stride;
+  } else {
+    Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, M, w->K, M, w->format, nullptr, 1, nullptr, 0};
+    if (cudaError_t e = launch_fp4_quant(q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm launch");
+  }
   a.xc = ws;
   a.xs = ws + sp.scales;
   a.xf = factor;

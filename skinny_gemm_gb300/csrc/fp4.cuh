@@ -58,6 +58,8 @@ struct Fp4RouteArgs {
 cudaError_t launch_fp4_route(const Fp4RouteArgs& a, int pdl, cudaStream_t s);
 
 struct Fp4MmArgs {
+  const uint16_t* x;  // bf16 rows that the product quantises itself (fp4_mm_fuses), or nullptr and:
+  int64_t x_stride;
   const uint8_t* xc;  // codes of the activations
   const uint8_t* xs;
   const float* xf;    // row factors or nullptr
@@ -75,6 +77,7 @@ struct Fp4MmArgs {
   int fault_wait;     // debug (W4A16_FAULT=wait): the first CTA's first stage waits for bytes that never come
 };
 cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s);
+bool fp4_mm_fuses(const w4a16_fp4& w, int M);  // whether a product of M rows quantises them itself
 int fp4_mm_tile(int M);  // rows of the activation tile that a call of M rows takes
 
 }  // namespace w4a16

@@ -24,6 +24,11 @@
 // The split depends on W's shape alone: up to 128 rows of x a row's result is
 // the same, bit for bit, whatever the other rows of the call.
 //
+// A few activation rows (decode, verify) are quantised in the kernel, by the
+// epilogue's warps while W's first stages come: each CTA takes its own part of K
+// (and every row's peak, for nv's factor), as fp4.cu would have it, bit for bit.
+// That saves the quantiser's launch.
+//
 // Scales in tensor memory have a set for each slot of the ring: a stage that
 // landed in a slot says that the MMAs which read the slot before are done.
 // Every wait is bounded: one that gives up raises W4A16_DEVICE_TIMEOUT, all
@@ -37,6 +42,7 @@
 #include "common.cuh"
 #include "fp4.cuh"
 #include "fp4_mm.cuh"
+#include "fp4_quant.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -60,7 +66,7 @@ struct Geo {
   static constexpr int kStages = (kCtaSmem - 1280) / kStage;
   static constexpr int kAcc = NT == 128 ? 1 : 2;
   static constexpr uint32_t kTmemCols = 256;
-  static constexpr int kBars = 2 * kStages + 2 * kAcc;
+  static constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
   static constexpr int kSmem = kStages * kStage + kBars * 8 + 16 + 1024;
   static_assert(kSmem <= kCtaSmem && kAcc * NT + kStages * kSetCols <= (int)kTmemCols, "half an SM's shared and tensor memory");
   static_assert(NT * kWRows * 4 <= kStages * kStage, "the partial sums of a split tile take the stages' place");
@@ -73,11 +79,88 @@ struct Maps {
   CUtensorMap xs;
 };
 
+// Activation rows that a CTA quantises: codes of its stages as the tiles that TMA would have brought, their scales 16
+// rows at a time (an atom's other rows are what follows).
+constexpr int kOwnRows = 16, kOwnStage = kOwnRows * 128, kOwnAtom = 256, kOwnThreads = 128;
+constexpr int kOwnUnits = 512;  // of sixteen values: most of a CTA
+
+struct OwnRows {
+  uint32_t peak[kOwnRows], finite[kOwnRows];  // largest |x| of a row, and of its finite values where that is not
+  float factor[kOwnRows];
+};
+
+template <int FMT>
+__device__ __forceinline__ void quantise_own(const Fp4MmParams& p, OwnRows* own, uint32_t codes, uint32_t scales, int t, int k0, int k1) {
+  constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;
+  const int units = p.K / 16, lane = t & 31;
+  const int per = 16 * (k1 - k0), all = p.M * per;  // units of a row's part, whole stages (what lies past K is zero)
+  auto load = [&](int i) {  // the i-th unit of this CTA's part
+    const int m = i / per, c = 16 * k0 + i - m * per;
+    return i < all && c < units ? fp4::load16(p.x + m * p.x_stride + 16 * c) : fp4::zero16();
+  };
+  auto write = [&](int i, const fp4::Vec16& v) {  // (whole warps)
+    const int m = min(i / per, p.M - 1), u = i - i / per * per;
+    uint32_t peak = fp4::peak16(v);
+    if (FMT == W4A16_FP4_MX) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+    int e = 0;
+    if (FMT == W4A16_FP4_NV) e = (int)(__float_as_uint(own->factor[m]) >> 23) - 127;
+    uint32_t byte;
+    const uint2 code = fp4::block16<FMT>(v, peak, e, byte);
+    const int stage = u / 16, unit = u % 16, b = FMT == W4A16_FP4_MX ? unit / 2 : unit;
+    if (i < all) {
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(codes + (uint32_t)(stage * kOwnStage + m * 128 + (((unit >> 1) ^ (m & 7)) << 4) + (unit & 1) * 8)),
+                   "r"(code.x), "r"(code.y)
+                   : "memory");
+      if (FMT == W4A16_FP4_NV || !(unit & 1))
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + (uint32_t)((stage * kAtoms + b / 4) * kOwnAtom + m * 16 + b % 4)), "r"(byte) : "memory");
+    }
+  };
+  constexpr int kBatch = 4;
+  fp4::Vec16 mine[kOwnUnits / kOwnThreads];  // (requested before the peaks are known)
+#pragma unroll
+  for (int j = 0; j < kOwnUnits / kOwnThreads; ++j) mine[j] = load(t + j * kOwnThreads);
+  if (FMT == W4A16_FP4_NV) {
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kOwnThreads) : "memory"); };
+    // 128, 64, 32, 16 or 8 threads a row, each of which keeps its own peak until the end
+    int each = kOwnThreads;
+    while (each * p.M > kOwnThreads) each /= 2;
+    const int m = t / each, at = t % each;
+    auto peaks = [&](auto&& of, uint32_t* to) {
+      uint32_t peak = 0;
+      if (m < p.M)
+        for (int c0 = at; c0 < units; c0 += kBatch * each) {
+          fp4::Vec16 v[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            v[j] = c0 + j * each < units ? fp4::load16(p.x + m * p.x_stride + 16 * (c0 + j * each)) : fp4::zero16();
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) peak = max(peak, of(v[j]));
+        }
+      __syncwarp();
+      for (int d = 1; d < each && d < 32; d *= 2) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, d));
+      if (m < p.M && at % 32 == 0) atomicMax(to + m, peak);
+    };
+    peaks([](const fp4::Vec16& v) { return fp4::peak16(v); }, own->peak);
+    sync();
+    const uint32_t odd = __ballot_sync(0xffffffffu, lane < p.M && own->peak[lane & 15] >= 0x7F80u);
+    if (odd) {  // rows with a NaN or an infinity
+      peaks([](const fp4::Vec16& v) { return fp4::finite_peak16(v); }, own->finite);
+      sync();
+    }
+    if (t < p.M) own->factor[t] = fp4::exp2n(fp4::factor_exp(odd >> t & 1 ? own->finite[t] : own->peak[t]));
+    sync();
+  }
+#pragma unroll
+  for (int j = 0; j < kOwnUnits / kOwnThreads; ++j)
+    if (j * kOwnThreads < all) write(t + j * kOwnThreads, mine[j]);
+  fence_proxy_async();
+}
+
 // One sum of row `row` of W and place `at` of x, whole warps (gate and up rows are neighbours).
-__device__ __forceinline__ void store(const Fp4MmParams& p, float v, float fw, int at, int row, bool mine) {
+__device__ __forceinline__ void store(const Fp4MmParams& p, float v, float fw, const float* xf, int at, int row, bool mine) {
   const int64_t m = p.row ? p.row[at] : at;
   float t = v * fw;
-  if (p.xf) t *= p.xf[at];
+  if (xf) t *= xf[at];
   if (p.act == W4A16_FP4_LINEAR) {
     if (mine) p.y[m * p.N + row] = f32_to_bf16_bits(t);
   } else {
@@ -106,26 +189,35 @@ __device__ __forceinline__ void store4(const Fp4MmParams& p, const float (&v)[4]
   }
 }
 
-template <int NT, int FMT>
+template <int NT, int FMT, bool OWN>
 __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_constant__ Maps maps, Fp4MmParams p) {
   using G = Geo<NT>;
-  constexpr int S = G::kStages, NB = G::kAcc;
+  constexpr int NB = G::kAcc;
+  const int S = OWN ? p.slots : G::kStages;
+  constexpr int kStage = OWN ? kWTile + kScaleTile : G::kStage;
   constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;  // of a stage and 128 rows
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t bars = sb + S * G::kStage;
-  auto W_of = [&](int s) { return sb + (uint32_t)(s * G::kStage); };
-  auto X_of = [&](int s) { return W_of(s) + kWTile; };
-  auto SW_of = [&](int s) { return X_of(s) + G::kX; };
-  auto SX_of = [&](int s) { return SW_of(s) + kScaleTile; };
+  const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
+  // this CTA's stages of a tile
+  const int k0 = p.stages * rank / split, k1 = p.stages * (rank + 1) / split;
+  const int own_stages = OWN ? (p.stages + split - 1) / split : 0;
+  const uint32_t own_codes = sb + (uint32_t)(S * kStage), own_scales = own_codes + (uint32_t)(own_stages * kOwnStage);
+  const uint32_t bars = OWN ? own_scales + (uint32_t)(own_stages * kAtoms * kOwnAtom + kOwnAtom) : own_codes;
+  auto W_of = [&](int s) { return sb + (uint32_t)(s * kStage); };
+  auto SW_of = [&](int s) { return W_of(s) + kWTile; };
+  auto X_of = [&](int s) { return SW_of(s) + kScaleTile; };
+  auto SX_of = [&](int s) { return X_of(s) + G::kX; };
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (S + s); };
   auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };
   auto acc_free = [&](int b) { return bars + 8u * (2 * S + NB + b); };
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (bars - sb) + 8 * G::kBars);
+  const uint32_t own_full = bars + 8u * (2 * S + 2 * NB);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (own_full + 8 - sb));
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  OwnRows* own = reinterpret_cast<OwnRows*>(s_tmem + 2);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -136,9 +228,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
       mbar_init(acc_full(b), 1);
       mbar_init(acc_free(b), 4);
     }
+    mbar_init(own_full, kOwnThreads);
     *s_abort = 0;
     fence_barrier_init();
   }
+  if (OWN && threadIdx.x >= 32 && threadIdx.x < 32 + kOwnRows) own->peak[threadIdx.x - 32] = own->finite[threadIdx.x - 32] = 0;
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), G::kTmemCols);
     tmem_relinquish();
@@ -148,10 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   tc_fence_after_sync();
   const uint32_t tmem = *s_tmem;
   pdl_launch_dependents();
-  const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
   const int64_t first = blockIdx.x / (unsigned)split, step = gridDim.x / (unsigned)split;
-  // this CTA's stages of a tile
-  const int k0 = p.stages * rank / split, k1 = p.stages * (rank + 1) / split;
   const uint32_t limit = p.fault_wait ? 4096u : 1u << 18;  // tries of a wait: about a second
   // What comes before the wait for the kernel before: nothing but W, and that only where it is complete already.
   if (!(p.early && warp == 0)) pdl_wait();
@@ -168,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
     if (lane == 0) {
       const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
       auto load_w = [&](int s, int k, int wrow, int ws) {
-        mbar_expect_tx(full(s), kWTile + G::kX + 2 * kAtoms * kFp4Atom);
+        mbar_expect_tx(full(s), OWN ? kWTile + kAtoms * kFp4Atom : kWTile + G::kX + 2 * kAtoms * kFp4Atom);
         tma_load_2d(W_of(s), &maps.w, k * 128, wrow, full(s), stream);
         tma_load_3d(SW_of(s), &maps.ws, 0, k * kAtoms, ws, full(s), stream);
       };
@@ -199,8 +290,10 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
             break;
           }
           if (it >= (uint32_t)ahead) load_w(s, k, wrow, ws);
-          tma_load_2d(X_of(s), &maps.x, k * 128, place, full(s), keep);
-          tma_load_3d(SX_of(s), &maps.xs, 0, k * kAtoms, xs, full(s), keep);
+          if (!OWN) {
+            tma_load_2d(X_of(s), &maps.x, k * 128, place, full(s), keep);
+            tma_load_3d(SX_of(s), &maps.xs, 0, k * kAtoms, xs, full(s), keep);
+          }
           if (++s == S) s = 0, parity ^= 1;
         }
       }
@@ -209,8 +302,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
     // ---- scales and MMAs ----
     const uint32_t go = elect_one();
     constexpr uint32_t kIdesc = umma_idesc_e2m1(kWRows, NT, FMT == W4A16_FP4_MX);
-    const uint64_t wd0 = umma_desc_sw128(W_of(0)), xd0 = umma_desc_sw128(X_of(0));
-    const uint64_t sw0 = umma_desc(SW_of(0), 128, 128, 0), sx0 = umma_desc(SX_of(0), 128, 128, 0);
+    const uint64_t wd0 = umma_desc_sw128(W_of(0)), xd0 = umma_desc_sw128(OWN ? own_codes : X_of(0));
+    const uint64_t sw0 = umma_desc(SW_of(0), 128, 128, 0), sx0 = umma_desc(OWN ? own_scales : SX_of(0), 128, 128, 0);
+    if (OWN && !mbar_wait_warp(own_full, 0, limit) && lane == 0) timeout();
     uint32_t n = 0;  // tiles
     int s = 0;
     uint32_t parity = 0;
@@ -229,13 +323,15 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
           break;
         }
         tc_fence_after_sync();
-        const uint64_t at = (uint64_t)(uint32_t)(s * (G::kStage >> 4));
-        const uint64_t wd = wd0 + at, xd = xd0 + at, sw = sw0 + at, sx = sx0 + at;
+        const uint64_t at = (uint64_t)(uint32_t)(s * (kStage >> 4));
+        const uint64_t wd = wd0 + at, sw = sw0 + at;
+        const uint64_t xd = xd0 + (OWN ? (uint64_t)(uint32_t)((k - k0) * (kOwnStage >> 4)) : at);
+        const uint64_t sx = sx0 + (OWN ? (uint64_t)(uint32_t)((k - k0) * (kAtoms * kOwnAtom >> 4)) : at);
         const uint32_t cw = tmem + (uint32_t)(NB * NT + s * kSetCols), cx = cw + 16;
         const int atoms = p.atoms - k * kAtoms, steps = (p.K - k * kFp4StageK + 63) / 64;
         auto copy = [&](int a) {
           tmem_copy_scales(cw + 4 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
-          tmem_copy_scales(cx + 4 * a, sx + (uint64_t)(a * (kFp4Atom >> 4)));
+          tmem_copy_scales(cx + 4 * a, sx + (uint64_t)(a * ((OWN ? kOwnAtom : kFp4Atom) >> 4)));
         };
         auto mma = [&](int j) {
           const bool add = k > k0 || j > 0;
@@ -268,6 +364,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   } else {
     // ---- epilogue ----
     const int q = warp & 3, r = 32 * q + lane;
+    if (OWN) {
+      quantise_own<FMT>(p, own, own_codes, own_scales, threadIdx.x - 64, k0, k1);
+      mbar_arrive(own_full);
+    }
+    const float* xf = OWN ? (FMT == W4A16_FP4_NV ? own->factor : nullptr) : p.xf;
     uint32_t n = 0;
     for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
       const int b = (int)(n % NB);
@@ -299,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
         for (int i = 0; i < 16; ++i) {
           if (c + i >= count) break;
           const int at = place + c + i;
-          store(p, v[i], fw, at, row, mine);
+          store(p, v[i], fw, xf, at, row, mine);
         }
       }
       tc_fence_before_sync();
@@ -344,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
       for (int i = 0; i < 4; ++i) fw[i] = p.wf && row + i < p.N ? p.wf[row + i] : 1.0f;
 #pragma unroll 2
       for (int c = warp; c < min(per, count - rank * per); c += kThreads / 32) {
-        const float fx = p.xf ? p.xf[place + c] : 1.0f;
+        const float fx = OWN ? (FMT == W4A16_FP4_NV ? own->factor[rank * per + c] : 1.0f) : p.xf ? p.xf[place + c] : 1.0f;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         for (int g = 0; g < split; ++g) {
           const float4 f = lds128f(sb + (uint32_t)(((g * per + c) * kWRows + 4 * lane) * 4));
@@ -377,17 +478,34 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
 // ---- host side ------------------------------------------------------------------------
 
 std::mutex g_mu;
+// K is split where that leaves no CTA without a place (two an SM of 152) or a stage.  By W's shape alone.
+int split_of(int row_tiles, int stages) {
+  int split = 1;
+  while (split < kMaxSplit && 2 * split * row_tiles <= 304 && 2 * split <= stages) split *= 2;
+  return split;
+}
+
+// Where the kernel quantises: shared memory of a ring of `slots` beside a CTA's `stages` of x, and how many slots fit.
+constexpr int own_smem(int slots, int stages) {
+  return slots * (kWTile + kScaleTile) + stages * (kOwnStage + 4 * kOwnAtom) + kOwnAtom + (2 * slots + 5) * 8 + 8 + (int)sizeof(OwnRows) + 1024;
+}
+int own_slots(int stages) {
+  int slots = 5;
+  while (slots > 0 && own_smem(slots, stages) > kCtaSmem) --slots;
+  return slots;
+}
+
 struct Device {
   int sms = 0;
-  bool attr[8] = {};
+  bool attr[10] = {};
 };
 Device g_dev[64];
 
-template <int NT, int FMT>
+template <int NT, int FMT, bool OWN = false>
 cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStream_t s) {
   using G = Geo<NT>;
-  auto* fn = fp4_mm_kernel<NT, FMT>;
-  constexpr int kIndex = (NT == 16 ? 0 : NT == 32 ? 1 : NT == 64 ? 2 : 3) * 2 + (FMT == W4A16_FP4_MX);
+  auto* fn = fp4_mm_kernel<NT, FMT, OWN>;
+  constexpr int kIndex = (OWN ? 4 : NT == 16 ? 0 : NT == 32 ? 1 : NT == 64 ? 2 : 3) * 2 + (FMT == W4A16_FP4_MX);
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -398,7 +516,7 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
     if (!d.sms)
       if (cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) return e;
     if (!d.attr[kIndex]) {
-      if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem)) return e;
+      if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, OWN ? kCtaSmem : G::kSmem)) return e;
       d.attr[kIndex] = true;
     }
     sms = d.sms;
@@ -407,16 +525,18 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
   if (cudaError_t e = encode_map_2d(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w.codes, a.w.K / 2, (int64_t)a.w.rows * a.w.experts,
                                     a.w.K / 2, 128, kWRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return e;
-  if (cudaError_t e = encode_map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.xc, a.w.K / 2, a.x_rows, a.w.K / 2, 128, NT,
+  if (!OWN)
+    if (cudaError_t e = encode_map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.xc, a.w.K / 2, a.x_rows, a.w.K / 2, 128, NT,
                                     CU_TENSOR_MAP_SWIZZLE_128B))
     return e;
   if (cudaError_t e = fp4_scale_map(&maps.ws, a.w.scales, (int64_t)p.row_tiles * a.w.experts, a.w.K, FMT, 1)) return e;
-  if (cudaError_t e = fp4_scale_map(&maps.xs, a.xs, (a.x_rows + 127) / 128, a.w.K, FMT, 1)) return e;
+  if (!OWN)
+    if (cudaError_t e = fp4_scale_map(&maps.xs, a.xs, (a.x_rows + 127) / 128, a.w.K, FMT, 1)) return e;
   const int64_t units = (int64_t)p.row_tiles * (a.tiles ? a.max_tiles : p.x_tiles);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.split > 1 ? units * p.split : units < 2 * sms ? units : 2 * sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)G::kSmem;
+  cfg.dynamicSmemBytes = (size_t)(OWN ? own_smem(p.slots, (p.stages + p.split - 1) / p.split) : G::kSmem);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
@@ -437,6 +557,16 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
 
 }  // namespace
 
+bool fp4_mm_fuses(const w4a16_fp4& w, int M) {
+  const int stages = (w.K + kFp4StageK - 1) / kFp4StageK, split = split_of((int)fp4_row_tiles(w.rows), stages);
+  const int part = (stages + split - 1) / split;
+  if (M > kOwnRows || M * 16 * part > kOwnUnits || own_slots(part) < 3) return false;
+  // nv needs the peaks of whole rows, which all CTAs read: worth a launch for a row or so.  Us so / with the quantiser's
+  // launch: one row x 2560 to 10240 rows 6.4 / 6.7, 5 rows 9.9 / 7.4, 5 x 10240 17 / 7.7.  mx: 5 x 10240 to 2560 6.2 / 7.0;
+  // 16 x 2560 (past kOwnUnits) 9.4 / 7.7.  The host's part of a call is 2 to 3 us less in every case.
+  return w.format == W4A16_FP4_MX || (int64_t)M * w.K <= (M == 1 ? 16384 : 8192);
+}
+
 int fp4_mm_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
 cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
@@ -445,10 +575,13 @@ cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   Fp4MmParams p = fp4_params(a, nt);
   p.early = a.early && pdl > 1 && !a.tiles;
   p.vec = a.w.rows % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 8 == 0;
-  // K is split where that leaves no CTA without a place (two an SM of 152) or a stage.  By W's shape alone.
-  if (!a.tiles)
-    while (p.split < kMaxSplit && 2 * p.split * p.row_tiles <= 304 && 2 * p.split <= p.stages) p.split *= 2;
+  if (!a.tiles) p.split = split_of(p.row_tiles, p.stages);
   const bool mx = a.w.format == W4A16_FP4_MX;
+  if (a.x) {
+    p.slots = own_slots((p.stages + p.split - 1) / p.split);
+    p.early = 0;
+    return mx ? launch_t<16, W4A16_FP4_MX, true>(a, p, pdl, s) : launch_t<16, W4A16_FP4_NV, true>(a, p, pdl, s);
+  }
   switch (nt) {
     case 16: return mx ? launch_t<16, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<16, W4A16_FP4_NV>(a, p, pdl, s);
     case 32: return mx ? launch_t<32, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<32, W4A16_FP4_NV>(a, p, pdl, s);

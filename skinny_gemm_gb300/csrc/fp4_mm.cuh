@@ -14,6 +14,8 @@ namespace w4a16 {
 constexpr int kFp4StageK = 256;  // codes of K per stage: 128 bytes a row
 
 struct Fp4MmParams {
+  const uint16_t* x;  // bf16 rows that the kernel quantises itself, or nullptr
+  int64_t x_stride;
   const float* wf;  // row factors of W and of x (nullptr: 1)
   const float* xf;
   uint16_t* y;
@@ -26,6 +28,7 @@ struct Fp4MmParams {
   int atoms, stages;       // scale atoms along K; stages along K
   int vec;                 // y's rows take 8-byte stores (fp4_pair.cu: of how many bytes, 32, 16 or 0)
   int split, early;        // CTAs that share a tile's K; W may be fetched before the wait for the kernel before
+  int slots;               // of the ring, where the kernel quantises
   int fault_wait;
 };
 
@@ -44,6 +47,8 @@ __device__ __forceinline__ uint32_t fp4_bf16x2(float lo, float hi) {
 
 inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
   Fp4MmParams p;
+  p.x = a.x;
+  p.x_stride = a.x_stride;
   p.wf = a.w.row_scale;
   p.xf = a.xf;
   p.y = a.y;
@@ -62,6 +67,7 @@ inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
   p.vec = 0;
   p.split = 1;
   p.early = 0;
+  p.slots = 0;
   p.fault_wait = a.fault_wait;
   return p;
 }

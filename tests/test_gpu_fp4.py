@@ -234,3 +234,23 @@ def test_rows_do_not_depend_on_the_batch(fmt, N, K):
         for j, i in enumerate((0, 3, 31, 100, 127)):
             if i < M:
                 assert torch.equal(y[i], one[j]), (M, i)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("M,N,K", [(1, 200, 16384), (1, 3000, 4640), (2, 129, 4064), (3, 40, 2688), (5, 77, 10240), (7, 300, 1120), (16, 140, 512), (16, 5000, 320), (12, 60, 32)])
+def test_rows_quantised_in_the_product(fmt, M, N, K):
+    """Few rows, which the product may quantise itself: the same bits as from fp4_quant, NaN and infinities among the values."""
+    from skinny_gemm_gb300 import ops
+
+    x, w, xv, wv = product(ops, fmt, M, N, K)
+    y = ops.fp4_mm(x, w)
+    want = xv @ wv.T
+    check(y, want, fc.product_bound(want, xv, wv))
+    x[M // 2, K - 3] = float("nan")
+    x[0, 1] = float("-inf")
+    wide = torch.zeros(M, K + 64, dtype=torch.bfloat16, device="cuda")
+    wide[:, 32:32 + K] = x
+    y, z = ops.fp4_mm(wide[:, 32:32 + K], w), ops.fp4_mm(ops.fp4_quant(x, fmt), w)
+    assert y[0].isnan().all() and y[M // 2].isnan().all()
+    assert torch.equal(y.view(torch.int16), z.view(torch.int16)) or torch.equal(y.nan_to_num(7.0), z.nan_to_num(7.0))
+    assert ops.device_status() == 0
