@@ -689,7 +689,7 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
 
 namespace {
 
-constexpr int kFp4MaxExperts = 4096;
+constexpr int kFp4MaxExperts = 4096, kFp4MaxTop = 1024;
 
 int check_fp4_shape(int rows, int K, int experts, int format) {
   if (format != W4A16_FP4_NV && format != W4A16_FP4_MX)
@@ -751,11 +751,15 @@ Fp4Space fp4_space(int64_t places, int64_t rows, int64_t tiles, int K, int forma
   return s;
 }
 
-// Routed: rows of an activation tile, and the most tiles that there can be.
+// Routed: rows of an activation tile, and the most tiles that there can be.  Twice an expert's mean share, so that most
+// experts have one tile; from some 25 rows on the pair kernel's, however empty: K = 2048, N = 1536, us with the smaller
+// tiles / with it: 64 tokens x 8 of 64 experts (8 rows each) 21 / 30, 500 x 4 of 64 (32) 31.9 / 31.3, 1000 x 1 of 16 (63)
+// 24.8 / 20.1, 1600 x 1 of 16 24.8 / 21.6, 2000 x 2 of 16 40 / 26, 1500 x 6 of 90 84 / 55.
 int fp4_id_tile(int64_t rows, int experts) {
-  const int64_t share = 2 * ((rows + experts - 1) / experts);
-  return fp4_mm_tile((int)(share < 128 ? share : 128));
+  const int64_t mean = (rows + experts - 1) / experts;
+  return mean > 24 ? 256 : fp4_mm_tile(2 * (int)mean);
 }
+int fp4_id_span(int64_t rows, int experts) { return fp4_id_tile(rows, experts) > 128 ? 256 : 128; }
 int64_t fp4_id_tiles(int64_t rows, int experts) {
   // an expert with rows wastes less than one tile
   return (rows < experts ? rows : experts) + rows / fp4_id_tile(rows, experts);
@@ -783,8 +787,7 @@ int w4a16_fp4_quant(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* out,
   const int rows = out->rows * out->experts;
   if (int rc = check_fp4_rows(x, x_stride, rows, out->K)) return rc;
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
-  Fp4QuantArgs a{x, x_stride, out->codes, out->scales, out->row_scale, rows, out->K, out->rows, out->format,
-                 nullptr, 1, nullptr, 0};
+  Fp4QuantArgs a{x, x_stride, out->codes, out->scales, out->row_scale, rows, out->K, out->rows, out->format};
   cudaError_t e = launch_fp4_quant(a, env().pdl, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_quant launch");
 }
@@ -829,7 +832,7 @@ int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a1
     a.x = x;
     a.x_stride = x_stride;
   } else {
-    Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, M, w->K, M, w->format, nullptr, 1, nullptr, 0};
+    Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, M, w->K, M, w->format};
     if (cudaError_t e = launch_fp4_quant(q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm launch");
   }
   a.xc = ws;
@@ -876,9 +879,9 @@ int w4a16_fp4_mm_q(const w4a16_fp4* x, const w4a16_fp4* w, w4a16_bf16* y, int ac
 }
 
 size_t w4a16_fp4_mm_id_workspace_bytes(int T, int top, int K, int experts, int format) {
-  if (check_fp4_shape(0, K, experts, format) || T < 0 || top < 1 || (int64_t)T * top > kMaxDim) return 0;
+  if (check_fp4_shape(0, K, experts, format) || T < 0 || top < 1 || top > kFp4MaxTop || (int64_t)T * top > kMaxDim) return 0;
   const int64_t rows = (int64_t)T * top, tiles = fp4_id_tiles(rows, experts);
-  return rows ? fp4_space(tiles * kFp4Rows, rows, tiles, K, format).total : 256;
+  return rows ? fp4_space(tiles * fp4_id_span(rows, experts), rows, tiles, K, format).total : 256;
 }
 
 int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, const int32_t* ids, w4a16_bf16* y,
@@ -886,13 +889,13 @@ int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, c
   if (env().fault == kFaultValidate) return fail(W4A16_ERR_SHAPE, "injected validation fault (W4A16_FAULT)");
   if (int rc = check_fp4(w, "w")) return rc;
   if (int rc = check_fp4_act(w, act)) return rc;
-  if (T < 0 || top < 1 || (int64_t)T * top > kMaxDim)
-    return fail(W4A16_ERR_EXPERTS, "T = %d must not be negative, top = %d positive, T * top at most 2^30", T, top);
+  if (T < 0 || top < 1 || top > kFp4MaxTop || (int64_t)T * top > kMaxDim)
+    return fail(W4A16_ERR_EXPERTS, "T = %d must not be negative, top = %d in 1..%d, T * top at most 2^30", T, top, kFp4MaxTop);
   if (T == 0) return W4A16_OK;
   if (int rc = check_fp4_rows(x, x_stride, T, w->K)) return rc;
   if (!ids || !y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(ids, 4) || misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "ids must be 4-byte and y 2-byte aligned");
-  const int64_t rows = (int64_t)T * top, tiles = fp4_id_tiles(rows, w->experts), places = tiles * kFp4Rows;
+  const int64_t rows = (int64_t)T * top, tiles = fp4_id_tiles(rows, w->experts), places = tiles * fp4_id_span(rows, w->experts);
   if (places > INT32_MAX) return fail(W4A16_ERR_EXPERTS, "T * top = %lld rows are too many for one call", (long long)rows);
   const Fp4Space sp = fp4_space(places, rows, tiles, w->K, w->format);
   if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total)) return rc;
@@ -903,12 +906,11 @@ int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, c
   float* factor = w->format == W4A16_FP4_NV ? reinterpret_cast<float*>(ws + sp.factor) : nullptr;
   int32_t* place = reinterpret_cast<int32_t*>(ws + sp.place);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Fp4RouteArgs r{ids, (int)rows, w->experts, fp4_id_tile(rows, w->experts), place, reinterpret_cast<int32_t*>(ws + sp.row),
-                 reinterpret_cast<Fp4Tile*>(ws + sp.tiles), reinterpret_cast<int32_t*>(ws + sp.count), flags};
-  if (cudaError_t e = launch_fp4_route(r, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm_id launch");
-  Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, T, w->K, T, w->format, place, top, y,
-                 act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2};
-  if (cudaError_t e = launch_fp4_quant(q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm_id launch");
+  Fp4RouteArgs r{ids, (int)rows, top, w->experts, fp4_id_tile(rows, w->experts), fp4_id_span(rows, w->experts), place, reinterpret_cast<int32_t*>(ws + sp.row),
+                 reinterpret_cast<Fp4Tile*>(ws + sp.tiles), reinterpret_cast<int32_t*>(ws + sp.count), y,
+                 act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2, flags};
+  Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, T, w->K, T, w->format};
+  if (cudaError_t e = launch_fp4_route_quant(r, q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm_id launch");
   Fp4MmArgs a = {};
   a.xc = ws;
   a.xs = ws + sp.scales;

@@ -21,10 +21,11 @@ namespace {
 using namespace ptx;
 using namespace fp4;
 
-cudaError_t launch(const void* fn, dim3 grid, int threads, void** args, int pdl, cudaStream_t s) {
+cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** args, int pdl, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -36,16 +37,131 @@ cudaError_t launch(const void* fn, dim3 grid, int threads, void** args, int pdl,
 
 constexpr int kQuantThreads = 256;  // of the way back
 constexpr int kQuantMost = 768;     // threads of a row: 80 registers each
+constexpr int kFoundMost = 1 << 20; // tokens x routed rows, up to which every token's CTA finds its places itself
+
+// ---- routed rows ------------------------------------------------------------------------
+//
+// Rows are counted by expert, the experts' tiles numbered, every row given a place in its expert's tiles.  A tile starts
+// at a place that is a multiple of 128, as its scales do.
+
+// The tiles of the experts, from their counts of rows; count[e] becomes the expert's first tile.  All threads of a CTA
+// (whole warps); WRITE: the tiles are written down.
+template <bool WRITE>
+__device__ __forceinline__ void number_tiles(const Fp4RouteArgs& p, int* count) {
+  __shared__ int s_warp[32], s_base;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  if (tid == 0) s_base = 0;
+  __syncthreads();
+  for (int e0 = 0; e0 < p.E; e0 += threads) {
+    const int e = e0 + tid, n = e < p.E ? count[e] : 0;
+    const int tiles = (n + p.nt - 1) / p.nt;
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += up;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    int first = s_base + sum - tiles;
+    for (int w = 0; w < warp; ++w) first += s_warp[w];
+    if (WRITE)
+      for (int t = 0; t < tiles; ++t)
+        p.tiles[first + t] = Fp4Tile{e, (first + t) * p.span, min(p.nt, n - t * p.nt), 0};
+    if (e < p.E) count[e] = first;
+    __syncthreads();
+    if (tid == threads - 1) s_base = first + tiles;
+    __syncthreads();
+  }
+  if (WRITE && tid == 0) *p.count = s_base;
+}
+
+// The places of token t's choices into to[top], found by every CTA for itself: it counts all ids, and those of the
+// tokens before its own.  counts: [2 E].  (500 tokens x 4 of 64 experts: 5.7 us, the counting in a launch of its own and
+// the places read back 12.)
+__device__ __forceinline__ void place_rows(const Fp4RouteArgs& p, int t, int* to, int* counts) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  int *count = counts, *before = counts + p.E;
+  for (int e = tid; e < 2 * p.E; e += threads) counts[e] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int r = tid; r < p.rows; r += threads) {
+    const int e = p.ids[r];
+    if (e >= 0 && e < p.E) {
+      atomicAdd(count + e, 1);
+      if (r < t * p.top) atomicAdd(before + e, 1);
+    } else {
+      bad = true;
+    }
+  }
+  if (bad && t == 0) atomicOr(p.flags, W4A16_DEVICE_BAD_ID);
+  __syncthreads();
+  if (t == 0) number_tiles<true>(p, count);
+  else number_tiles<false>(p, count);
+  __syncthreads();
+  for (int j = tid; j < p.top; j += threads) {
+    const int r = t * p.top + j, e = p.ids[r];
+    int place = -1;
+    if (e >= 0 && e < p.E) {
+      int i = before[e];
+      for (int k = 0; k < j; ++k) i += p.ids[t * p.top + k] == e;  // (an expert may be chosen twice)
+      place = (count[e] + i / p.nt) * p.span + i % p.nt;
+      p.row[place] = r;
+    }
+    to[j] = place;
+  }
+  __syncthreads();
+}
+
+// The same in one CTA for many rows.  Which of an expert's rows takes which place is left to the order of the atomics: no
+// output depends on it.
+constexpr int kRouteThreads = 1024;
+
+__global__ void __launch_bounds__(kRouteThreads) fp4_route_kernel(Fp4RouteArgs p) {
+  extern __shared__ int s_count[];  // [E] rows, then the expert's first tile
+  int* s_next = s_count + p.E;      // [E] rows placed
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int e = tid; e < p.E; e += kRouteThreads) s_count[e] = s_next[e] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int r = tid; r < p.rows; r += kRouteThreads) {
+    const int e = p.ids[r];
+    if (e >= 0 && e < p.E) atomicAdd(&s_count[e], 1);
+    else bad = true;
+  }
+  if (bad) atomicOr(p.flags, W4A16_DEVICE_BAD_ID);
+  __syncthreads();
+  number_tiles<true>(p, s_count);
+  __syncthreads();
+  for (int r = tid; r < p.rows; r += kRouteThreads) {
+    const int e = p.ids[r];
+    int place = -1;
+    if (e >= 0 && e < p.E) {
+      const int i = atomicAdd(&s_next[e], 1);
+      place = (s_count[e] + i / p.nt) * p.span + i % p.nt;
+      p.row[place] = r;
+    }
+    p.place[r] = place;
+  }
+}
 
 // One CTA a row; a thread holds up to C units of sixteen values (32 bytes) in registers between the row's peak and its
 // codes, longer rows are read again.  A thread has a whole nv block, two neighbours an mx one.  What bounds it is HBM (2
 // bytes a value in, 0.56 out) for many rows, and a load, the row's reduction and the launch for few.
-template <int FMT, int C, bool ROUTED>
-__global__ void __launch_bounds__(kQuantMost, 1) fp4_quant_kernel(Fp4QuantArgs p) {
+//
+// ROUTE: the row is a token, whose codes go to the places of its choices; the places are read (kGiven) or found here
+// (kFound: every CTA counts all ids, see place_rows).
+enum Route { kNone, kGiven, kFound };
+
+template <int FMT, int C, int ROUTE>
+__global__ void __launch_bounds__(kQuantMost, 1) fp4_quant_kernel(Fp4QuantArgs p, Fp4RouteArgs route) {
   constexpr int kWord = FMT == W4A16_FP4_MX ? 8 : 4;  // units of an atom's word of four scales
   const int tid = threadIdx.x, threads = blockDim.x, units = p.K / 16;
   const int n = blockIdx.x;  // row of expert blockIdx.y
   const int64_t r = (int64_t)blockIdx.y * p.group + n;
+  extern __shared__ int s_route[];  // ROUTE: [top] places, then what place_rows counts
   __shared__ uint32_t s_peak[32];
   pdl_wait();
   pdl_launch_dependents();  // (not before: what the next kernel reads early is then complete)
@@ -56,6 +172,11 @@ __global__ void __launch_bounds__(kQuantMost, 1) fp4_quant_kernel(Fp4QuantArgs p
     const int c = i * threads + tid;
     v[i] = c < units ? load16(x + 16 * c) : zero16();
   }
+  if (ROUTE == kGiven) {
+    for (int j = tid; j < route.top; j += threads) s_route[j] = route.place[r * route.top + j];
+    __syncthreads();
+  }
+  if (ROUTE == kFound) place_rows(route, n, s_route, s_route + route.top);
   int e = 0;
   if (FMT == W4A16_FP4_NV) {
     auto over_row = [&](uint32_t peak) {
@@ -83,45 +204,46 @@ __global__ void __launch_bounds__(kQuantMost, 1) fp4_quant_kernel(Fp4QuantArgs p
     e = factor_exp(peak);
   }
   const int atoms = fp4_atoms(p.K, FMT), all = atoms * kWord;  // units with those past K that fill the last atom
-#pragma unroll 1
-  for (int j = 0; j < (ROUTED ? p.top : 1); ++j) {
-    int64_t at = r, tile;
-    int lane_row;
-    if (ROUTED) {
-      at = p.place[r * p.top + j];
-      if (at < 0) {  // no such expert: a row of zeros
-        uint16_t* y = p.y + (r * p.top + j) * p.y_row;
-        for (int64_t i = tid; i < p.y_row; i += threads) y[i] = 0;
-        continue;
-      }
-      tile = at / kFp4Rows;
-      lane_row = (int)(at % kFp4Rows);
-    } else {
-      tile = (int64_t)blockIdx.y * fp4_row_tiles(p.group) + n / kFp4Rows;
-      lane_row = n % kFp4Rows;
-    }
-    uint2* codes = reinterpret_cast<uint2*>(p.codes + at * (p.K / 2)) + tid;
-    if (FMT == W4A16_FP4_NV && tid == 0) p.row_scale[at] = exp2n(e);
-    // a word of an atom is four blocks' bytes, kWord threads' units; the CTA's threads are a multiple of that
-    uint8_t* words = p.scales + tile * atoms * kFp4Atom + 16 * (lane_row & 31) + 4 * (lane_row >> 5) + tid / kWord * kFp4Atom;
-    const int place = 8 * (tid / (kWord / 4) % 4);
-    const bool first = tid % kWord == 0;
-    auto write = [&](int c0, const Vec16& w) {  // units c0 + tid (whole warps)
-      uint32_t peak = peak16(w);
-      if (FMT == W4A16_FP4_MX) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
-      uint32_t byte;
-      const uint2 code = block16<FMT>(w, peak, e, byte);
-      if (tid < units - c0) codes[c0] = code;
-      uint32_t word = byte << place;
-      word |= __shfl_xor_sync(0xffffffffu, word, kWord / 4);
-      word |= __shfl_xor_sync(0xffffffffu, word, kWord / 2);
-      if (first && tid < all - c0) *reinterpret_cast<uint32_t*>(words + c0 / kWord * kFp4Atom) = word;
+  // a word of an atom is four blocks' bytes, kWord threads' units; the CTA's threads are a multiple of that
+  const int shift = 8 * (tid / (kWord / 4) % 4);
+  const bool first = tid % kWord == 0;
+  auto write = [&](int c0, const Vec16& w) {  // units c0 + tid (whole warps)
+    uint32_t peak = peak16(w);
+    if (FMT == W4A16_FP4_MX) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+    uint32_t byte;
+    const uint2 code = block16<FMT>(w, peak, e, byte);
+    uint32_t word = byte << shift;
+    word |= __shfl_xor_sync(0xffffffffu, word, kWord / 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, kWord / 2);
+    auto put = [&](int64_t at, int64_t tile, int lane_row) {
+      if (tid < units - c0) reinterpret_cast<uint2*>(p.codes + at * (p.K / 2))[c0 + tid] = code;
+      if (first && tid < all - c0)
+        *reinterpret_cast<uint32_t*>(p.scales + (tile * atoms + (c0 + tid) / kWord) * kFp4Atom + 16 * (lane_row & 31) + 4 * (lane_row >> 5)) = word;
     };
+    if (ROUTE == kNone) {
+      put(r, (int64_t)blockIdx.y * fp4_row_tiles(p.group) + n / kFp4Rows, n % kFp4Rows);
+    } else {
+      for (int j = 0; j < route.top; ++j)
+        if (const int at = s_route[j]; at >= 0) put(at, at / kFp4Rows, at % kFp4Rows);
+    }
+  };
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (i * threads < all) write(i * threads, v[i]);
+  for (int i = 0; i < C; ++i)
+    if (i * threads < all) write(i * threads, v[i]);
 #pragma unroll 1
-    for (int c0 = C * threads; c0 < all; c0 += threads) write(c0, c0 + tid < units ? load16(x + 16 * (c0 + tid)) : zero16());
+  for (int c0 = C * threads; c0 < all; c0 += threads) write(c0, c0 + tid < units ? load16(x + 16 * (c0 + tid)) : zero16());
+  if constexpr (ROUTE == kNone) {
+    if (FMT == W4A16_FP4_NV && tid == 0) p.row_scale[r] = exp2n(e);
+  } else {
+    for (int j = 0; j < route.top; ++j) {
+      const int at = s_route[j];
+      if (at >= 0) {
+        if (FMT == W4A16_FP4_NV && tid == 0) p.row_scale[at] = exp2n(e);
+      } else {  // no such expert: a row of zeros
+        uint16_t* y = route.y + (r * route.top + j) * route.y_row;
+        for (int64_t i = tid; i < route.y_row; i += threads) y[i] = 0;
+      }
+    }
   }
 }
 
@@ -174,82 +296,36 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_dequant_kernel(w4a16_fp4 w,
   }
 }
 
-// ---- routed rows ------------------------------------------------------------------------
-
-constexpr int kRouteThreads = 1024;
-
-// One CTA: rows counted by expert, the experts' tiles numbered, every row given a place in its expert's tiles.  A tile
-// starts at a place that is a multiple of 128, as its scales do.  Which of an expert's rows takes which place is left
-// to the order of the atomics: no output depends on it.
-__global__ void __launch_bounds__(kRouteThreads) fp4_route_kernel(Fp4RouteArgs p) {
-  extern __shared__ int s_count[];  // [E] rows, then the expert's first tile
-  int* s_next = s_count + p.E;      // [E] rows placed
-  __shared__ int s_warp[kRouteThreads / 32], s_base;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int e = tid; e < p.E; e += kRouteThreads) s_count[e] = s_next[e] = 0;
-  if (tid == 0) s_base = 0;
-  __syncthreads();
-  bool bad = false;
-  for (int r = tid; r < p.rows; r += kRouteThreads) {
-    const int e = p.ids[r];
-    if (e >= 0 && e < p.E) atomicAdd(&s_count[e], 1);
-    else bad = true;
-  }
-  if (bad) atomicOr(p.flags, W4A16_DEVICE_BAD_ID);
-  __syncthreads();
-  for (int e0 = 0; e0 < p.E; e0 += kRouteThreads) {
-    const int e = e0 + tid, n = e < p.E ? s_count[e] : 0;
-    const int tiles = (n + p.nt - 1) / p.nt;
-    int sum = tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int up = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += up;
-    }
-    if (lane == 31) s_warp[warp] = sum;
-    __syncthreads();
-    int first = s_base + sum - tiles;
-    for (int w = 0; w < warp; ++w) first += s_warp[w];
-    for (int t = 0; t < tiles; ++t)
-      p.tiles[first + t] = Fp4Tile{e, (first + t) * kFp4Rows, min(p.nt, n - t * p.nt), 0};
-    if (e < p.E) s_count[e] = first;
-    __syncthreads();
-    if (tid == kRouteThreads - 1) s_base = first + tiles;
-    __syncthreads();
-  }
-  if (tid == 0) *p.count = s_base;
-  for (int r = tid; r < p.rows; r += kRouteThreads) {
-    const int e = p.ids[r];
-    int place = -1;
-    if (e >= 0 && e < p.E) {
-      const int i = atomicAdd(&s_next[e], 1);
-      place = (s_count[e] + i / p.nt) * kFp4Rows + i % p.nt;
-      p.row[place] = r;
-    }
-    p.place[r] = place;
-  }
-}
-
 }  // namespace
 
 namespace {
 
 template <int FMT>
 cudaError_t quant_f(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
-  void* args[] = {const_cast<Fp4QuantArgs*>(&a)};
+  Fp4RouteArgs none = {};
+  void* args[] = {const_cast<Fp4QuantArgs*>(&a), &none};
   // Few rows: a thread a unit, for the latency (1 x 2560 1.4 us; 333 x 2304 1.6 us so and with four units a thread).
   // Many: four, whose loads are in flight together; us with one / two / four, nv: 4096 x 2560 6.9 / 6.2 / 6.2, 4001 x
   // 10240 47 / 22.5 / 20.1, 8192 x 16384 119 / 71 / 55 (HBM's 51).
   const int all = fp4_atoms(a.K, FMT) * 4 * fp4_block(FMT) / 16;
-  const bool one = !a.place && a.rows <= 152 && all <= kQuantMost;
+  const bool one = a.rows <= 152 && all <= kQuantMost;
   int threads = ((one ? all : (all + 3) / 4) + 31) / 32 * 32;
   threads = threads > kQuantMost ? kQuantMost : threads;
-  const void* fn = a.place ? (const void*)fp4_quant_kernel<FMT, 4, true>
-                   : one   ? (const void*)fp4_quant_kernel<FMT, 1, false>
-                           : (const void*)fp4_quant_kernel<FMT, 4, false>;
-  return launch(fn, dim3((unsigned)a.group, (unsigned)(a.rows / a.group)), threads, args, pdl, s);
+  const void* fn = one ? (const void*)fp4_quant_kernel<FMT, 1, kNone> : (const void*)fp4_quant_kernel<FMT, 4, kNone>;
+  return launch(fn, dim3((unsigned)a.group, (unsigned)(a.rows / a.group)), threads, 0, args, pdl, s);
+}
+
+template <int FMT>
+cudaError_t route_quant_f(const Fp4RouteArgs& r, const Fp4QuantArgs& q, bool found, int pdl, cudaStream_t s) {
+  void* args[] = {const_cast<Fp4QuantArgs*>(&q), const_cast<Fp4RouteArgs*>(&r)};
+  const int all = fp4_atoms(q.K, FMT) * 4 * fp4_block(FMT) / 16;
+  // two units a thread, and at least 256 to count the ids
+  int threads = ((all + 1) / 2 + 31) / 32 * 32;
+  if (found && threads < 256) threads = 256;
+  threads = threads > kQuantMost ? kQuantMost : threads;
+  const size_t smem = 4 * ((size_t)r.top + (found ? 2 * (size_t)r.E : 0));
+  const void* fn = found ? (const void*)fp4_quant_kernel<FMT, 2, kFound> : (const void*)fp4_quant_kernel<FMT, 2, kGiven>;
+  return launch(fn, dim3((unsigned)q.rows), threads, smem, args, pdl, s);
 }
 
 }  // namespace
@@ -258,25 +334,22 @@ cudaError_t launch_fp4_quant(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
   return a.format == W4A16_FP4_MX ? quant_f<W4A16_FP4_MX>(a, pdl, s) : quant_f<W4A16_FP4_NV>(a, pdl, s);
 }
 
+cudaError_t launch_fp4_route_quant(const Fp4RouteArgs& r, const Fp4QuantArgs& q, int pdl, cudaStream_t s) {
+  // Every token's CTA reads all ids, which grows with their number times the tokens'.  The call in us so / with a launch
+  // for the places: 8 tokens x 1 9.5 / 11.0, 64 x 8 21.3 / 23.3, 500 x 4 31.9 / 32.9, 2000 x 2 50 / 40, 4000 x 1 63 / 43.
+  const bool found = (int64_t)q.rows * r.rows <= kFoundMost;
+  if (!found) {
+    void* args[] = {const_cast<Fp4RouteArgs*>(&r)};
+    if (cudaError_t e = launch((const void*)fp4_route_kernel, dim3(1), kRouteThreads, (size_t)r.E * 8, args, pdl, s)) return e;
+  }
+  return q.format == W4A16_FP4_MX ? route_quant_f<W4A16_FP4_MX>(r, q, found, pdl, s) : route_quant_f<W4A16_FP4_NV>(r, q, found, pdl, s);
+}
+
 cudaError_t launch_fp4_dequant(const w4a16_fp4& w, uint16_t* y, int pdl, cudaStream_t s) {
   const int64_t parts = (w.K / 16 + kBack * kQuantThreads - 1) / (kBack * kQuantThreads);
   void* args[] = {const_cast<w4a16_fp4*>(&w), &y};
   if (parts > 65535) return cudaErrorInvalidConfiguration;
-  return launch((const void*)fp4_dequant_kernel, dim3((unsigned)w.rows, (unsigned)w.experts, (unsigned)parts), kQuantThreads, args, pdl, s);
-}
-
-cudaError_t launch_fp4_route(const Fp4RouteArgs& a, int pdl, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kRouteThreads);
-  cfg.dynamicSmemBytes = (size_t)a.E * 8;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, fp4_route_kernel, a);
+  return launch((const void*)fp4_dequant_kernel, dim3((unsigned)w.rows, (unsigned)w.experts, (unsigned)parts), kQuantThreads, 0, args, pdl, s);
 }
 
 }  // namespace w4a16

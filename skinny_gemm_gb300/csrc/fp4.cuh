@@ -33,11 +33,6 @@ struct Fp4QuantArgs {
   int rows, K;     // rows of x
   int group;       // rows of one expert: their scale tiles start anew
   int format;
-  // routed: row r of x goes to the places place[r * top + j]; a place of -1 (bad id) zeroes y's row instead
-  const int32_t* place;
-  int top;
-  uint16_t* y;
-  int64_t y_row;
 };
 cudaError_t launch_fp4_quant(const Fp4QuantArgs& a, int pdl, cudaStream_t s);
 cudaError_t launch_fp4_dequant(const w4a16_fp4& w, uint16_t* y, int pdl, cudaStream_t s);
@@ -47,15 +42,19 @@ struct Fp4Tile {
   int expert, place, count, unused;
 };
 struct Fp4RouteArgs {
-  const int32_t* ids;  // [rows]
-  int rows, E, nt;     // nt: most rows of a tile
+  const int32_t* ids;  // [rows]: the `top` choices of token after token
+  int rows, top, E, nt;  // nt: most rows of a tile
+  int span;            // places of a tile: nt up to a multiple of 128
   int32_t* place;      // [rows]: where the row's codes go, -1 for a bad id
   int32_t* row;        // [places]: the row of a place
   Fp4Tile* tiles;
   int32_t* count;      // [1]: tiles
+  uint16_t* y;         // rows of bad ids are zeroed: y_row values each
+  int64_t y_row;
   int* flags;
 };
-cudaError_t launch_fp4_route(const Fp4RouteArgs& a, int pdl, cudaStream_t s);
+// The rows' places, and the tokens x (q.rows of them) quantised into those.
+cudaError_t launch_fp4_route_quant(const Fp4RouteArgs& a, const Fp4QuantArgs& q, int pdl, cudaStream_t s);
 
 struct Fp4MmArgs {
   const uint16_t* x;  // bf16 rows that the product quantises itself (fp4_mm_fuses), or nullptr and:
