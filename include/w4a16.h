@@ -491,7 +491,10 @@ int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream);
 /* y[m][n] = bf16( x'[m] . W[n] ), x' = x quantised row by row as above, in w's
  * format; products of codes and scales are exact, their sums fp32.  x bf16, row
  * m at x + m * x_stride (a multiple of 8; 16-byte aligned), y bf16 [M][w->rows] (or
- * [M][w->rows / 2] for an act), 2-byte aligned.  workspace: device memory of
+ * [M][w->rows / 2] for an act), 2-byte aligned, not over x.  Up to 128 rows a
+ * row's result is the one-row call's, bit for bit; more rows are summed in
+ * another order (one piece of K instead of the splits that few rows of W take).
+ * workspace: device memory of
  * w4a16_fp4_mm_workspace_bytes(M, K, format) bytes, 256-byte aligned, no initial
  * contents needed; calls that share one must not overlap on the GPU.  M >= 0;
  * M == 0 is a no-op. */
@@ -560,8 +563,9 @@ const char* w4a16_last_error(void);
  * expects 16 bytes more than its copies deliver, so that warp's bounded wait
  * gives up, raises W4A16_DEVICE_TIMEOUT and leaves its rows unwritten; every
  * copy still lands, so nothing is in flight when the kernel exits; in every
- * w4a16_kv_attention launch the first slot of keys of one CTA waits for an
- * arrival that never comes, to the same end) and
+ * w4a16_kv_attention launch the first slot of keys, and in every product of
+ * w4a16_fp4_* the first stage, of one CTA waits for an arrival that never
+ * comes, to the same end) and
  * W4A16_FORCE_KERNEL (simt | tc | vanilla).  They are read once, at the
  * first call, otherwise. */
 void w4a16_debug_reload_env(void);

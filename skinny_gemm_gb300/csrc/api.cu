@@ -720,6 +720,13 @@ int check_fp4_rows(const void* x, int64_t x_stride, int64_t rows, int K) {
   return W4A16_OK;
 }
 
+// CTAs write y while others read x.
+int check_fp4_apart(const void* x, int64_t x_stride, int64_t x_rows, int K, const void* y, int64_t y_values) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  const uintptr_t n = 2 * (uintptr_t)((x_rows > 1 ? (x_rows - 1) * x_stride : 0) + K), m = 2 * (uintptr_t)y_values;
+  return a < b + m && b < a + n ? fail(W4A16_ERR_SHAPE, "y overlaps x") : W4A16_OK;
+}
+
 int check_fp4_act(const w4a16_fp4* w, int act) {
   if (act != W4A16_FP4_LINEAR && act != W4A16_FP4_SILU && act != W4A16_FP4_GELU)
     return fail(W4A16_ERR_KERNEL, "unknown activation %d", act);
@@ -819,6 +826,7 @@ int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a1
   if (int rc = check_fp4_rows(x, x_stride, M, w->K)) return rc;
   if (!y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "y must be 2-byte aligned");
+  if (int rc = check_fp4_apart(x, x_stride, M, w->K, y, (int64_t)M * (act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2))) return rc;
   const Fp4Space sp = fp4_space(M, M, 0, w->K, w->format);
   if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total)) return rc;
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
@@ -895,6 +903,8 @@ int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, c
   if (int rc = check_fp4_rows(x, x_stride, T, w->K)) return rc;
   if (!ids || !y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(ids, 4) || misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "ids must be 4-byte and y 2-byte aligned");
+  if (int rc = check_fp4_apart(x, x_stride, T, w->K, y, (int64_t)T * top * (act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2)))
+    return rc;
   const int64_t rows = (int64_t)T * top, tiles = fp4_id_tiles(rows, w->experts), places = tiles * fp4_id_span(rows, w->experts);
   if (places > INT32_MAX) return fail(W4A16_ERR_EXPERTS, "T * top = %lld rows are too many for one call", (long long)rows);
   const Fp4Space sp = fp4_space(places, rows, tiles, w->K, w->format);

@@ -1005,14 +1005,15 @@ def fp4_quant(x: torch.Tensor, format: str = "nv", out: FP4Matrix | None = None,
         raise ValueError(f"K = {K} must be a positive multiple of 32")
     M, stride = _fp4_x(x, K, None)
     E = x.shape[0] if x.dim() == 3 else 1
+    dev = x.get_device()
+    raw = _stream_on(stream, dev)
     if out is None:
         out = FP4Matrix.empty(M // max(E, 1), K, max(E, 1), format, x.device)
     elif (out.N * out.E, out.K, out.format) != (M, K, format):
         raise ValueError(f"out must have {M} rows of {K} codes, format {format}")
-    dev = x.get_device()
-    if out._dev != dev:
+    elif out._dev != dev:
         raise ValueError(f"out is on cuda:{out._dev}, x on cuda:{dev}")
-    rc = lib().w4a16_fp4_quant(x.data_ptr(), stride, out._ptr, _stream_on(stream, dev))
+    rc = lib().w4a16_fp4_quant(x.data_ptr(), stride, out._ptr, raw)
     if rc:
         _raise(rc)
     return out

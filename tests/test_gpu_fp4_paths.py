@@ -1,0 +1,245 @@
+"""Microscaled 4-bit products as programs run them: captured, on several streams, in a chain, with waits that run out, and past 2^31."""
+import time
+import zlib
+
+import numpy as np
+import pytest
+import torch
+
+import fp4_cases as fc
+from skinny_gemm_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(*seed):
+    return torch.Generator().manual_seed(zlib.crc32(repr(seed).encode()))
+
+
+def made(fmt, M, N, K, E=1):
+    g = gen(fmt, M, N, K, E)
+    codes, byte, factor, _ = fc.weights(g, E, N, K, fmt)
+    return fc.activations(g, M, K).cuda(), fc.matrix(ops, codes, byte, factor, E, fmt)
+
+
+# one of each kernel: rows quantised in the product, split over a cluster, several tiles a CTA, 64 and 128 rows, pairs
+CASES = [("nv", 1, 500, 2560), ("mx", 5, 300, 4096), ("nv", 9, 640, 2048), ("nv", 3, 50000, 256), ("mx", 60, 300, 512), ("nv", 100, 1000, 1024), ("nv", 400, 1500, 800)]
+
+
+@pytest.mark.parametrize("fmt,M,N,K", CASES)
+def test_captured_and_replayed(fmt, M, N, K):
+    """The first call of all is captured; replays take the inputs that are there then, and graphs of one stream do not share memory."""
+    x, w = made(fmt, M, N, K)
+    other = x.flip(0).contiguous() * 0.5
+    y, z = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    a, b = x.clone(), other.clone()
+    g, h = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        ops.fp4_mm(a, w, out=y)
+    with torch.cuda.graph(h):
+        ops.fp4_mm(b, w, out=z)
+    want, want2 = ops.fp4_mm(x, w), ops.fp4_mm(other, w)
+    for _ in range(3):
+        g.replay()
+        h.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, want2)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):  # both at once
+        with torch.cuda.stream(s):
+            g.replay()
+        with torch.cuda.stream(t):
+            h.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, want2)
+    a.copy_(other)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want2) and ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt,M,N,K", CASES)
+def test_streams(fmt, M, N, K):
+    """Calls on several streams at once, with the stream's own workspaces and with given ones."""
+    x, w = made(fmt, M, N, K)
+    want = ops.fp4_mm(x, w)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [torch.empty_like(want) for _ in range(6)]
+    n = ops.lib().w4a16_fp4_mm_workspace_bytes(M, K, ops.FP4_FORMATS[fmt])
+    own = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            ops.fp4_mm(x, w, out=outs[i], stream=s)
+            with torch.cuda.stream(s):
+                ops.fp4_mm(x, w, out=outs[3 + i], workspace=own[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and ops.device_status() == 0
+
+
+def test_routed_captured_and_streams():
+    x, w = made("nv", 40, 130, 320, E=6)
+    ids = torch.randint(0, 6, (40, 2), generator=gen(1), dtype=torch.int32).cuda()
+    want = ops.fp4_mm_id(x, w, ids)
+    y = torch.empty_like(want)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        ops.fp4_mm_id(x, w, ids, out=y)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [torch.empty_like(want) for _ in range(3)]
+    for _ in range(3):
+        g.replay()
+        for o, s in zip(outs, streams):
+            ops.fp4_mm_id(x, w, ids, out=o, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and all(torch.equal(o, want) for o in outs)
+    ids.fill_(3)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, ops.fp4_mm_id(x, w, ids)) and ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("M", [1, 5, 40, 300])
+def test_weights_written_just_before(fmt, M):
+    """Weights quantised, and written again, on the same stream right before the product that reads them."""
+    g = gen(fmt, M)
+    x = fc.activations(g, M, 512).cuda()
+    a, b = (torch.randn(2000, 512, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    wa, wb = ops.fp4_quant(a, fmt), ops.fp4_quant(b, fmt)
+    torch.cuda.synchronize()
+    ya, yb = ops.fp4_mm(x, wa), ops.fp4_mm(x, wb)
+    w = ops.FP4Matrix.empty(2000, 512, format=fmt)
+    torch.cuda.synchronize()
+    got = []
+    for i in range(20):
+        ops.fp4_quant(b if i % 2 else a, fmt, out=w)
+        got.append(ops.fp4_mm(x, w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, yb if i % 2 else ya) for i, y in enumerate(got))
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_block_of_a_decoder_layer(fmt):
+    """A gated feed-forward block, a routed one and the shared quantisation of q, k and v in a row, captured as a step is, against
+    float64 of the same chain of roundings."""
+    g = gen(fmt, "layer")
+    H, F, T, E = 320, 448, 6, 4
+    x = fc.activations(g, T, H)
+    wg, wu = (torch.randn(F, H, generator=g).div(H ** 0.5).to(torch.bfloat16) for _ in range(2))
+    wd = torch.randn(H, F, generator=g).div(F ** 0.5).to(torch.bfloat16)
+    we = torch.randn(E, 2 * F, H, generator=g).div(H ** 0.5).to(torch.bfloat16)
+    qw = [torch.randn(n, H, generator=g).div(H ** 0.5).to(torch.bfloat16) for n in (256, 64, 64)]
+    ids = torch.randint(0, E, (T, 2), generator=g, dtype=torch.int32).cuda()
+    up, down = ops.FP4Matrix.gated(wg.cuda(), wu.cuda(), fmt), ops.fp4_quant(wd.cuda(), fmt)
+    experts = ops.fp4_quant(we.cuda(), fmt)
+    qkv = [ops.fp4_quant(w.cuda(), fmt) for w in qw]
+    xd = x.cuda()
+
+    def step():
+        q = ops.fp4_quant(xd, fmt)
+        heads = [ops.fp4_mm(q, w) for w in qkv]
+        h = ops.fp4_gated(xd, up, act="gelu")
+        return heads, h, ops.fp4_mm(h, down), ops.fp4_mm_id(xd, experts, ids, act="silu")
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        heads, h, y, routed = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert ops.device_status() == 0
+
+    def held(t):
+        return fc.values(*fc.quant(t.cpu(), fmt), fmt)
+
+    def inside(got, want, bound):
+        err = np.abs(got.double().cpu().numpy() - want)
+        assert (err <= bound).all(), (err / bound).max()
+
+    xv = held(x)
+    for got, w in zip(heads, qw):
+        inside(got, xv @ held(w).T, fc.product_bound(xv @ held(w).T, xv, held(w)))
+    gate, u = xv @ held(wg).T, xv @ held(wu).T
+    inside(h, fc.act64(gate, "gelu") * u, fc.gated_bound(gate, u, xv, held(wg), held(wu), "gelu"))
+    hv = held(h)  # the chain goes on from the rounded h
+    inside(y, hv @ held(wd).T, fc.product_bound(hv @ held(wd).T, hv, held(wd)))
+    for t in range(T):
+        for j in range(2):
+            w = held(we[int(ids[t, j])])
+            gate, u = xv[t:t + 1] @ w[0::2].T, xv[t:t + 1] @ w[1::2].T
+            inside(routed[t, j][None], fc.act64(gate, "silu") * u, fc.gated_bound(gate, u, xv[t:t + 1], w[0::2], w[1::2], "silu"))
+
+
+@pytest.mark.parametrize("E", [1, 4096])
+def test_many_experts_and_tokens(E):
+    """More routed rows than every CTA counts for itself (a launch of its own finds the places), and the most experts."""
+    T, top, N, K = (3000, 2, 66, 64) if E == 1 else (1200, 3, 18, 32)
+    x, w = made("mx", T, N, K, E)
+    ids = torch.randint(0, E, (T, top), generator=gen(E), dtype=torch.int32).cuda()
+    ids[5, 0], ids[T - 1, top - 1] = -7, E
+    y = ops.fp4_mm_id(x, w, ids)
+    assert ops.device_status() == ops.DEVICE_BAD_ID
+    xv = fc.values(*fc.quant(x.cpu(), "mx"), "mx")
+    wv = ops.fp4_dequant(w).double().cpu().numpy().reshape(E, N, K)
+    i = ids.cpu().numpy()
+    bad = (i < 0) | (i >= E)
+    want = np.einsum("tjnk,tk->tjn", wv[np.where(bad, 0, i)], xv) if E > 1 else np.repeat((xv @ wv[0].T)[:, None], top, 1)
+    mass = np.abs(xv).sum(1)[:, None, None] * np.abs(wv).max()
+    err = np.abs(y.double().cpu().numpy() - np.where(bad[..., None], 0, want))
+    assert (err <= np.abs(want) * 2.0 ** -8 + mass * (1.1 * K * 2.0 ** -23 + 2.0 ** -22) * 1.01 + 2.0 ** -133).all()
+    assert not y[torch.from_numpy(bad).cuda()].any()
+
+
+def test_past_2_31():
+    """Outputs and codes whose offsets do not fit 32 bits."""
+    M, N, K = 8400, 262144, 32  # 2.2e9 values of y
+    x, w = made("mx", M, N, K)
+    y = ops.fp4_mm(x, w)
+    xv, rows = fc.values(*fc.quant(x.cpu()[-300:], "mx"), "mx"), slice(N - 400, N)
+    wv = ops.fp4_dequant(w)[rows].double().cpu().numpy()
+    want = xv @ wv.T
+    err = np.abs(y[-300:, rows].double().cpu().numpy() - want)
+    assert (err <= fc.product_bound(want, xv, wv)).all() and ops.device_status() == 0
+    del x, w, y
+    torch.cuda.empty_cache()
+    N, K = 140000, 32768  # 2.3e9 bytes of codes, a factor of 1
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((ops.fp4_scale_bytes(N, K, "nv"),), 0x30, dtype=torch.uint8, device="cuda")
+    w = ops.FP4Matrix(codes, scales, None, N, K)
+    x = fc.activations(gen(2), 3, K).cuda()
+    y = ops.fp4_mm(x, w)
+    xv = fc.values(*fc.quant(x.cpu(), "nv"), "nv")
+    c = codes[-200:].cpu().numpy()
+    c = np.stack([c & 15, c >> 4], -1).reshape(200, K)
+    wv = fc.values(c, np.full((200, K // 16), 0x30, np.uint8), None, "nv")
+    want = xv @ wv.T
+    err = np.abs(y[:, -200:].double().cpu().numpy() - want)
+    assert (err <= fc.product_bound(want, xv, wv)).all() and ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt,M,N,K", CASES)
+def test_waits_run_out_and_the_context_survives(fmt, M, N, K, monkeypatch):
+    """The first stage of one CTA waits for an arrival that never comes (every copy still lands): all roles give up, the flag is
+    raised, and the next call is right."""
+    x, w = made(fmt, M, N, K)
+    want = ops.fp4_mm(x, w)
+    assert ops.device_status() == 0
+    monkeypatch.setenv("W4A16_FAULT", "wait")
+    ops.lib().w4a16_debug_reload_env()
+    try:
+        t0 = time.perf_counter()
+        ops.fp4_mm(x, w)
+        flags = ops.device_status()
+        elapsed = time.perf_counter() - t0
+    finally:
+        monkeypatch.delenv("W4A16_FAULT")
+        ops.lib().w4a16_debug_reload_env()
+    assert flags == ops.DEVICE_TIMEOUT and elapsed < 20
+    for _ in range(3):
+        assert torch.equal(ops.fp4_mm(x, w), want)
+    assert ops.device_status() == 0
