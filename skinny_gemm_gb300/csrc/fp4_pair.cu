@@ -54,7 +54,7 @@ struct Cols {
   static constexpr int kShared = 8 - kAccStep / 32;  // 32s of columns that both accumulators have
   static_assert(kSetsAt + kSets * kSet <= 512 && kShared <= 6, "the SM's tensor memory");
 };
-constexpr int kBars = 3 * S + 6;
+constexpr int kBars = 2 * S + 6;
 constexpr int kSmem = S * kStage + kEpi * 384 + kBars * 8 + 16 + 1024;
 static_assert(kSmem <= 227 * 1024, "a CTA's shared memory");
 
@@ -111,20 +111,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   auto W_of = [&](int s) { return X_of(s) + kXTile; };
   auto SX_of = [&](int s) { return W_of(s) + kWTile; };
   auto SW_of = [&](int s) { return SX_of(s) + kXScale; };
-  auto full = [&](int s) { return bars + 8u * s; };            // this CTA's copies landed
-  auto empty = [&](int s) { return bars + 8u * (S + s); };     // the MMAs are done with it (both CTAs)
-  auto peer = [&](int s) { return bars + 8u * (2 * S + s); };  // leader: the other CTA's copies landed
-  auto acc_full = [&](int b) { return bars + 8u * (3 * S + b); };
-  auto acc_free = [&](int b) { return bars + 8u * (3 * S + 2 + b); };   // leader: all of it read, by both CTAs
-  auto part_free = [&](int b) { return bars + 8u * (3 * S + 4 + b); };  // leader: the shared columns read
+  auto full = [&](int s) { return bars + 8u * s; };         // this CTA's copies landed; leader: the other CTA's too
+  auto empty = [&](int s) { return bars + 8u * (S + s); };  // the MMAs are done with it (both CTAs)
+  auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };
+  auto acc_free = [&](int b) { return bars + 8u * (2 * S + 2 + b); };   // leader: all of it read, by both CTAs
+  auto part_free = [&](int b) { return bars + 8u * (2 * S + 4 + b); };  // leader: the shared columns read
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (bars - sb) + 8 * kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 1 + (p.fault_wait && blockIdx.x == 0 && s == 0));  // (debug: an arrival that never comes)
+      // (debug: an arrival that never comes)
+      mbar_init(full(s), (rank == 0 ? 2 : 1) + (p.fault_wait && blockIdx.x == 0 && s == 0));
       mbar_init(empty(s), 1);
-      mbar_init(peer(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
@@ -212,8 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       const uint32_t w_col = (uint32_t)(nt * tn % 128 / 32);
       bool ok = true;
       for (int k = 0; k < ns; ++k, ++it) {
-        ok = mbar_wait_warp(full(s), parity, limit) && mbar_wait_warp(peer(s), parity, limit) &&
-             (it < (uint32_t)kSets || mbar_wait_warp(empty(old), old_parity, limit));
+        ok = mbar_wait_warp(full(s), parity, limit) &&
+             (kSets >= S || it < (uint32_t)kSets || mbar_wait_warp(empty(old), old_parity, limit));
         if (!ok) {
           if (lane == 0) timeout();
           break;
@@ -266,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       for (int k = 0; k < ns; ++k, ++it) {
         const int s = (int)(it % S);
         if (!(ok = mbar_wait_warp(full(s), (it / S) & 1, limit))) break;
-        if (lane == 0) mbar_arrive_cluster(peer(s) + to);
+        if (lane == 0) mbar_arrive_cluster(full(s) + to);
       }
       if (!ok) {
         if (lane == 0) timeout();

@@ -908,42 +908,44 @@ class FP4Matrix:
             _on_device(row_scale, "row_scale", dev)
         self.N, self.K, self.E, self.format = N, K, E, format
         self._codes, self._scales, self._row_scale, self._flat = codes, scales, row_scale, None
-        self._bind(codes.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(), codes.device, dev)
-
-    def _bind(self, codes, scales, row_scale, device, dev) -> None:
-        self._c = Fp4Struct(codes, scales, row_scale, self.N, self.K, self.E, FP4_FORMATS[self.format])
-        self._ptr, self._device, self._dev = ctypes.addressof(self._c), device, dev
+        self._device, self._dev = codes.device, dev
+        self._c = Fp4Struct(codes.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(), N, K, E,
+                            FP4_FORMATS[format])
+        self._ptr = ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, N: int, K: int, E: int = 1, format: str = "nv", device="cuda") -> "FP4Matrix":
-        n = fp4_scale_bytes(N, K, format)
+        n = E * fp4_scale_bytes(N, K, format)
         if K <= 0 or K % 32 or N < 0 or E < 1:
             raise ValueError(f"N = {N}, K = {K} (a positive multiple of 32), E = {E}")
-        self = cls.__new__(cls)
+        # one block of memory: scales (a multiple of 512 bytes), codes (of 16), factors; their tensors are made when asked for
+        m, nv = E * N * (K // 2), format == "nv"
+        flat = torch.empty((n + m) // 4 + (E * N if nv else 0), dtype=torch.float32, device=device)
+        self, at = cls.__new__(cls), flat.data_ptr()
         self.N, self.K, self.E, self.format = N, K, E, format
-        # scales (a multiple of 512 bytes) and codes in one block of memory; their tensors are made when asked for
-        flat = torch.empty(E * n + E * N * (K // 2), dtype=torch.uint8, device=device)
-        f = torch.empty(E * N, dtype=torch.float32, device=device) if format == "nv" else None
-        self._flat, self._codes, self._scales, self._row_scale = flat, None, None, f
-        at = flat.data_ptr()
-        self._bind(at + E * n, at, None if f is None else f.data_ptr(), flat.device, flat.get_device())
+        self._flat, self._codes, self._scales, self._row_scale = flat, None, None, None
+        self._device, self._dev = flat.device, flat.get_device()
+        self._c = Fp4Struct(at + n, at, at + n + m if nv else None, N, K, E, FP4_FORMATS[format])
+        self._ptr = ctypes.addressof(self._c)
         return self
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            self._scales = self._flat[:self.E * fp4_scale_bytes(self.N, self.K, self.format)]
+            self._scales = self._flat.view(torch.uint8)[:self.E * fp4_scale_bytes(self.N, self.K, self.format)]
         return self._scales
 
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
             n = self.E * fp4_scale_bytes(self.N, self.K, self.format)
-            self._codes = self._flat[n:].view(self.E * self.N, self.K // 2)
+            self._codes = self._flat.view(torch.uint8)[n:n + self.E * self.N * (self.K // 2)].view(self.E * self.N, self.K // 2)
         return self._codes
 
     @property
     def row_scale(self) -> torch.Tensor | None:
+        if self._row_scale is None and self._flat is not None and self.format == "nv":
+            self._row_scale = self._flat.narrow(0, self._flat.shape[0] - self.E * self.N, self.E * self.N)
         return self._row_scale
 
     @classmethod
@@ -984,15 +986,16 @@ def _fp4_x(x: torch.Tensor, K: int, dev: int | None):
     """(rows, row stride) of bf16 activations [.., K]: dense rows, which may be apart where x is [M, K]."""
     if not (isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16 and x.is_cuda):
         _dev_tensor(x, torch.bfloat16, "x")
-    if x.dim() < 1 or x.shape[-1] != K:
-        raise ValueError(f"x must be [.., {K}] (got {tuple(x.shape)})")
+    shape = x.shape
+    if not shape or shape[-1] != K:
+        raise ValueError(f"x must be [.., {K}] (got {tuple(shape)})")
     if dev is not None and x.get_device() != dev:
         _on_device(x, "x", dev)
     if x.is_contiguous():
-        return x.numel() // K, K
-    if x.dim() != 2 or x.stride(1) != 1:
+        return shape[0] if len(shape) == 2 else x.numel() // K, K
+    if len(shape) != 2 or x.stride(1) != 1:
         raise ValueError("x must be contiguous, or [M, K] with contiguous rows")
-    return x.shape[0], x.stride(0) if x.shape[0] > 1 else K
+    return shape[0], x.stride(0) if shape[0] > 1 else K
 
 
 def fp4_quant(x: torch.Tensor, format: str = "nv", out: FP4Matrix | None = None, stream=None) -> FP4Matrix:
@@ -1004,16 +1007,16 @@ def fp4_quant(x: torch.Tensor, format: str = "nv", out: FP4Matrix | None = None,
     if K <= 0 or K % 32:
         raise ValueError(f"K = {K} must be a positive multiple of 32")
     M, stride = _fp4_x(x, K, None)
-    E = x.shape[0] if x.dim() == 3 else 1
     dev = x.get_device()
     raw = _stream_on(stream, dev)
     if out is None:
-        out = FP4Matrix.empty(M // max(E, 1), K, max(E, 1), format, x.device)
+        E = max(x.shape[0], 1) if x.dim() == 3 else 1
+        out = FP4Matrix.empty(M // E, K, E, format, x.device)
     elif (out.N * out.E, out.K, out.format) != (M, K, format):
         raise ValueError(f"out must have {M} rows of {K} codes, format {format}")
     elif out._dev != dev:
         raise ValueError(f"out is on cuda:{out._dev}, x on cuda:{dev}")
-    rc = lib().w4a16_fp4_quant(x.data_ptr(), stride, out._ptr, raw)
+    rc = (_lib or lib()).w4a16_fp4_quant(x.data_ptr(), stride, out._ptr, raw)
     if rc:
         _raise(rc)
     return out
@@ -1027,7 +1030,7 @@ def fp4_dequant(w: FP4Matrix, out: torch.Tensor | None = None, stream=None) -> t
         out = torch.empty(shape, dtype=torch.bfloat16, device=w._device)
     else:
         _fp4_out(out, shape, w._dev)
-    rc = lib().w4a16_fp4_dequant(w._ptr, out.data_ptr(), raw)
+    rc = (_lib or lib()).w4a16_fp4_dequant(w._ptr, out.data_ptr(), raw)
     if rc:
         _raise(rc)
     return out
@@ -1042,18 +1045,20 @@ def _fp4_out(out: torch.Tensor, shape, dev: int) -> None:
 
 @functools.lru_cache(maxsize=1024)
 def _fp4_mm_bytes(M: int, K: int, format: int) -> int:
-    return int(lib().w4a16_fp4_mm_workspace_bytes(M, K, format))
+    return int((_lib or lib()).w4a16_fp4_mm_workspace_bytes(M, K, format))
 
 
 @functools.lru_cache(maxsize=1024)
 def _fp4_mm_id_bytes(*sizes: int) -> int:
-    return int(lib().w4a16_fp4_mm_id_workspace_bytes(*sizes))
+    return int((_lib or lib()).w4a16_fp4_mm_id_workspace_bytes(*sizes))
 
 
 def _fp4_act(w: FP4Matrix, act) -> int:
+    if act is None:
+        return 0
     if act not in FP4_ACTS:
         raise ValueError(f"unknown activation {act!r}; one of {list(FP4_ACTS)}")
-    if act is not None and w.N % 2:
+    if w.N % 2:
         raise ValueError(f"N = {w.N}: gate and up rows come in pairs")
     return FP4_ACTS[act]
 
@@ -1074,25 +1079,28 @@ def _fp4_product(x, w: FP4Matrix, act, out, stream, workspace):
         raise ValueError("stacked experts: use fp4_mm_id")
     a = _fp4_act(w, act)
     cols = w.N if a == 0 else w.N // 2
-    raw = _stream_on(stream, w._dev)
-    if isinstance(x, FP4Matrix):
-        M, lead = x.N, (x.N,)
+    dev = w._dev
+    raw = _stream_on(stream, dev)
+    quantised = isinstance(x, FP4Matrix)
+    if quantised:
+        M = x.N
+        lead = (M,)
         if x.K != w.K or x.format != w.format or x.E != 1:
             raise ValueError(f"x has K={x.K}, format {x.format}, E={x.E}; weights have K={w.K}, format {w.format}")
-        if x._dev != w._dev:
-            raise ValueError(f"x is on cuda:{x._dev}, w on cuda:{w._dev}")
+        if x._dev != dev:
+            raise ValueError(f"x is on cuda:{x._dev}, w on cuda:{dev}")
     else:
-        M, stride = _fp4_x(x, w.K, w._dev)
+        M, stride = _fp4_x(x, w.K, dev)
         lead = x.shape[:-1]
     if out is None:
         out = torch.empty((*lead, cols), dtype=torch.bfloat16, device=w._device)
     else:
-        _fp4_out(out, (M, cols), w._dev)
-    if isinstance(x, FP4Matrix):
-        rc = lib().w4a16_fp4_mm_q(x._ptr, w._ptr, out.data_ptr(), a, raw)
+        _fp4_out(out, (M, cols), dev)
+    if quantised:
+        rc = (_lib or lib()).w4a16_fp4_mm_q(x._ptr, w._ptr, out.data_ptr(), a, raw)
     else:
-        keep, ws, wn = _fp4_space(_fp4_mm_bytes(M, w.K, w._c.format), workspace, raw, stream, w)
-        rc = lib().w4a16_fp4_mm(x.data_ptr(), stride, w._ptr, out.data_ptr(), M, a, ws, wn, raw)
+        keep, ws, wn = _fp4_space(_fp4_mm_bytes(M, w.K, FP4_FORMATS[w.format]), workspace, raw, stream, w)
+        rc = (_lib or lib()).w4a16_fp4_mm(x.data_ptr(), stride, w._ptr, out.data_ptr(), M, a, ws, wn, raw)
     if rc:
         _raise(rc)
     return out
@@ -1134,8 +1142,8 @@ def fp4_mm_id(x: torch.Tensor, w: FP4Matrix, ids: torch.Tensor, act: str | None 
         out = torch.empty(shape, dtype=torch.bfloat16, device=w._device)
     else:
         _fp4_out(out, shape, w._dev)
-    keep, ws, wn = _fp4_space(_fp4_mm_id_bytes(T, top, w.K, w.E, w._c.format), workspace, raw, stream, w)
-    rc = lib().w4a16_fp4_mm_id(x.data_ptr(), stride, w._ptr, ip, out.data_ptr(), T, top, a, ws, wn, raw)
+    keep, ws, wn = _fp4_space(_fp4_mm_id_bytes(T, top, w.K, w.E, FP4_FORMATS[w.format]), workspace, raw, stream, w)
+    rc = (_lib or lib()).w4a16_fp4_mm_id(x.data_ptr(), stride, w._ptr, ip, out.data_ptr(), T, top, a, ws, wn, raw)
     if rc:
         _raise(rc)
     return out
