@@ -58,18 +58,24 @@ constexpr int kSetCols = 32;          // 16 columns of W's scales, 16 of x's
 constexpr int kThreads = 192;
 constexpr int kMaxSplit = 8;
 constexpr int kCtaSmem = 113 * 1024;  // of which two fit an SM
+// A ring leaves room for a CTA of the next call's quantiser beside two of its own, which else starts only when they are
+// gone (5 rows x 10240 x 2560: 6.8 us, with rings of all 113 KB 7.8).
+constexpr int kRing = 108 * 1024 + 512;
+constexpr int kOwnAtom = 256;  // an atom's first 16 rows (the MMA's others are whatever follows)
 
 template <int NT>
 struct Geo {
   static constexpr int kX = NT * 128;
-  static constexpr int kStage = kWTile + kX + 2 * kScaleTile;
-  static constexpr int kStages = (kCtaSmem - 1280) / kStage;
+  static constexpr int kXAtom = NT == 16 ? kOwnAtom : kFp4Atom;  // bytes of an atom of x's scales that are fetched
+  static constexpr int kStage = kWTile + kScaleTile + kX + 4 * kXAtom;
+  static constexpr int kPast = kFp4Atom - kXAtom;  // bytes that the last atom's copy reads past the ring
+  static constexpr int kStages = (kRing - kPast) / kStage;
   static constexpr int kAcc = NT == 128 ? 1 : 2;
   static constexpr uint32_t kTmemCols = 256;
   static constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
-  static constexpr int kSmem = kStages * kStage + kBars * 8 + 16 + 1024;
+  static constexpr int kSmem = kStages * kStage + kPast + kBars * 8 + 16;
   static_assert(kSmem <= kCtaSmem && kAcc * NT + kStages * kSetCols <= (int)kTmemCols, "half an SM's shared and tensor memory");
-  static_assert(NT * kWRows * 4 <= kStages * kStage, "the partial sums of a split tile take the stages' place");
+  static_assert(NT * kWRows * 4 <= kStages * kStage, "the partial sums of a split tile, which else take the stages' place");
 };
 
 struct Maps {
@@ -79,10 +85,12 @@ struct Maps {
   CUtensorMap xs;
 };
 
-// Activation rows that a CTA quantises: codes of its stages as the tiles that TMA would have brought, their scales 16
-// rows at a time (an atom's other rows are what follows).
-constexpr int kOwnRows = 16, kOwnStage = kOwnRows * 128, kOwnAtom = 256, kOwnThreads = 128;
+// Activation rows that a CTA quantises: codes of its stages as the tiles that TMA would have brought, and their scales.
+constexpr int kOwnRows = 16, kOwnStage = kOwnRows * 128, kOwnThreads = 128;
 constexpr int kOwnUnits = 512;  // of sixteen values: most of a CTA
+// Room of its own for a split tile's partial sums from the other CTAs (16 columns in 2, 4 or 8 parts, all but one): a CTA
+// need not wait for the others' MMAs before it sends its own (5 x 2560 x 10240: 5.9 us, else 6.2).
+constexpr int kOwnParts = kOwnRows * kWRows * 4 / kMaxSplit * (kMaxSplit - 1);
 
 struct OwnRows {
   uint32_t peak[kOwnRows], finite[kOwnRows];  // largest |x| of a row, and of its finite values where that is not
@@ -196,8 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   const int S = OWN ? p.slots : G::kStages;
   constexpr int kStage = OWN ? kWTile + kScaleTile : G::kStage;
   constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;  // of a stage and 128 rows
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t base[];  // (the tiles' swizzle counts from multiples of 1024)
   const uint32_t sb = smem_u32(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
@@ -205,7 +212,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   const int k0 = p.stages * rank / split, k1 = p.stages * (rank + 1) / split;
   const int own_stages = OWN ? (p.stages + split - 1) / split : 0;
   const uint32_t own_codes = sb + (uint32_t)(S * kStage), own_scales = own_codes + (uint32_t)(own_stages * kOwnStage);
-  const uint32_t bars = OWN ? own_scales + (uint32_t)(own_stages * kAtoms * kOwnAtom + kOwnAtom) : own_codes;
+  const uint32_t behind = OWN ? own_scales + (uint32_t)(own_stages * kAtoms * kOwnAtom + kOwnAtom) : own_codes;
+  constexpr int kParts = OWN ? kOwnParts : 0;
+  const uint32_t parts = kParts ? behind : sb, bars = behind + (OWN ? kParts : G::kPast);
   auto W_of = [&](int s) { return sb + (uint32_t)(s * kStage); };
   auto SW_of = [&](int s) { return W_of(s) + kWTile; };
   auto X_of = [&](int s) { return SW_of(s) + kScaleTile; };
@@ -241,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *s_tmem;
+  if (kParts && split > 1) cluster_arrive();  // (this CTA is there to be written to)
   pdl_launch_dependents();
   const int64_t first = blockIdx.x / (unsigned)split, step = gridDim.x / (unsigned)split;
   const uint32_t limit = p.fault_wait ? 4096u : 1u << 18;  // tries of a wait: about a second
@@ -259,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
     if (lane == 0) {
       const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
       auto load_w = [&](int s, int k, int wrow, int ws) {
-        mbar_expect_tx(full(s), OWN ? kWTile + kAtoms * kFp4Atom : kWTile + G::kX + 2 * kAtoms * kFp4Atom);
+        mbar_expect_tx(full(s), kWTile + kAtoms * kFp4Atom + (OWN ? 0 : G::kX + kAtoms * G::kXAtom));
         tma_load_2d(W_of(s), &maps.w, k * 128, wrow, full(s), stream);
         tma_load_3d(SW_of(s), &maps.ws, 0, k * kAtoms, ws, full(s), stream);
       };
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
         const int atoms = p.atoms - k * kAtoms, steps = (p.K - k * kFp4StageK + 63) / 64;
         auto copy = [&](int a) {
           tmem_copy_scales(cw + 4 * a, sw + (uint64_t)(a * (kFp4Atom >> 4)));
-          tmem_copy_scales(cx + 4 * a, sx + (uint64_t)(a * ((OWN ? kOwnAtom : kFp4Atom) >> 4)));
+          tmem_copy_scales(cx + 4 * a, sx + (uint64_t)(a * (G::kXAtom >> 4)));
         };
         auto mma = [&](int j) {
           const bool add = k > k0 || j > 0;
@@ -412,17 +422,19 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   __syncthreads();
   if (split > 1) {
     // ---- a split tile: partial sums to the CTAs that add them up ----
-    // Rank g adds the columns [g per, (g + 1) per).  The sums take the stages' place when no MMA of the cluster reads
-    // those any more; a CTA that gave up takes part in the barriers all the same.
+    // Rank g adds the columns [g per, (g + 1) per).  Where the sums take the stages' place, no MMA of the cluster may
+    // read those any more; a CTA that gave up takes part in the barriers all the same.
     const int q = warp & 3, xt = (int)(first / p.row_tiles), wt = (int)(first % p.row_tiles);
     const bool live = first < units && !*s_abort;
     const int count = min(NT, p.M - xt * NT), per = (count + split - 1) / split;
-    cluster_arrive();
+    if (!kParts) cluster_arrive();
     cluster_wait();
     if (live && warp >= 2) {
       tc_fence_after_sync();
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
       int g = 0, col = 0;  // column c is the col-th of rank g's
+      // a part's place at its rank; this CTA's own part lies in its stages, which are its own again
+      auto part_of = [&](int to) { return to == rank || !kParts ? sb + (uint32_t)(rank * per * kWRows * 4) : parts + (uint32_t)((rank - (rank > to)) * per * kWRows * 4); };
 #pragma unroll 1
       for (int c = 0; c < count; c += 16) {
         float v[16];
@@ -431,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (c + i >= count) break;
-          st_cluster_f32(cluster_map(sb + (uint32_t)(((rank * per + col) * kWRows + 32 * q + lane) * 4), (uint32_t)g), v[i]);
+          st_cluster_f32(cluster_map(part_of(g) + (uint32_t)((col * kWRows + 32 * q + lane) * 4), (uint32_t)g), v[i]);
           if (++col == per) col = 0, ++g;
         }
       }
@@ -448,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
         const float fx = OWN ? (FMT == W4A16_FP4_NV ? own->factor[rank * per + c] : 1.0f) : p.xf ? p.xf[place + c] : 1.0f;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         for (int g = 0; g < split; ++g) {
-          const float4 f = lds128f(sb + (uint32_t)(((g * per + c) * kWRows + 4 * lane) * 4));
+          const uint32_t from = g == rank || !kParts ? sb + (uint32_t)(g * per * kWRows * 4) : parts + (uint32_t)((g - (g > rank)) * per * kWRows * 4);
+          const float4 f = lds128f(from + (uint32_t)((c * kWRows + 4 * lane) * 4));
           v[0] += f.x;
           v[1] += f.y;
           v[2] += f.z;
@@ -487,7 +500,7 @@ int split_of(int row_tiles, int stages) {
 
 // Where the kernel quantises: shared memory of a ring of `slots` beside a CTA's `stages` of x, and how many slots fit.
 constexpr int own_smem(int slots, int stages) {
-  return slots * (kWTile + kScaleTile) + stages * (kOwnStage + 4 * kOwnAtom) + kOwnAtom + (2 * slots + 5) * 8 + 8 + (int)sizeof(OwnRows) + 1024;
+  return slots * (kWTile + kScaleTile) + stages * (kOwnStage + 4 * kOwnAtom) + kOwnAtom + kOwnParts + (2 * slots + 5) * 8 + 8 + (int)sizeof(OwnRows);
 }
 int own_slots(int stages) {
   int slots = 5;
@@ -531,7 +544,7 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
     return e;
   if (cudaError_t e = fp4_scale_map(&maps.ws, a.w.scales, (int64_t)p.row_tiles * a.w.experts, a.w.K, FMT, 1)) return e;
   if (!OWN)
-    if (cudaError_t e = fp4_scale_map(&maps.xs, a.xs, (a.x_rows + 127) / 128, a.w.K, FMT, 1)) return e;
+    if (cudaError_t e = fp4_scale_map(&maps.xs, a.xs, (a.x_rows + 127) / 128, a.w.K, FMT, 1, G::kXAtom / 4)) return e;
   const int64_t units = (int64_t)p.row_tiles * (a.tiles ? a.max_tiles : p.x_tiles);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.split > 1 ? units * p.split : units < 2 * sms ? units : 2 * sms));

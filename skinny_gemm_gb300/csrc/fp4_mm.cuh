@@ -74,10 +74,11 @@ inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
 
 // The scales' map: [row tiles][atoms along K][128 words], boxes of `tiles` x a stage's atoms (what lies past the end
 // is read as zeros).  Tiled copies: as untiled ones of 2 KB, three a stage, they took 330 cycles of the copy engine.
-inline cudaError_t fp4_scale_map(CUtensorMap* map, const void* scales, int64_t row_tiles, int K, int format, int tiles) {
+// words: of an atom's 128, 64 for its first 16 rows.
+inline cudaError_t fp4_scale_map(CUtensorMap* map, const void* scales, int64_t row_tiles, int K, int format, int tiles, int words = 128) {
   const int atoms = fp4_atoms(K, format);
   const int64_t dims[3] = {kFp4Atom / 4, atoms, row_tiles}, strides[2] = {kFp4Atom, (int64_t)atoms * kFp4Atom};
-  const int box[3] = {kFp4Atom / 4, format == W4A16_FP4_MX ? 2 : 4, tiles};
+  const int box[3] = {words, format == W4A16_FP4_MX ? 2 : 4, tiles};
   return encode_map_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
