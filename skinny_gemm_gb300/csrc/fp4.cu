@@ -35,7 +35,7 @@ cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** a
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-constexpr int kQuantThreads = 256;  // of the way back
+constexpr int kBackThreads = 256;   // most threads of the way back
 constexpr int kQuantMost = 768;     // threads of a row: 80 registers each
 constexpr int kFoundMost = 1 << 20; // tokens x routed rows, up to which every token's CTA finds its places itself
 
@@ -248,10 +248,8 @@ __global__ void __launch_bounds__(kQuantMost, 1) fp4_quant_kernel(Fp4QuantArgs p
 }
 
 // Units of sixteen values: value = bf16(code * scale * factor), exact unless it leaves bf16's range.  code * scale is
-// exact in fp16 for nv (6 significant bits, 2^-10 to 2688).
-constexpr int kBack = 1;  // units a thread
-
-__global__ void __launch_bounds__(kQuantThreads) fp4_dequant_kernel(w4a16_fp4 w, uint16_t* y) {
+// exact in fp16 for nv (6 significant bits, 2^-10 to 2688).  A thread has one unit.
+__global__ void __launch_bounds__(kBackThreads) fp4_dequant_kernel(w4a16_fp4 w, uint16_t* y) {
   pdl_wait();
   pdl_launch_dependents();
   const int n = blockIdx.x, part = blockIdx.z;  // row of expert blockIdx.y
@@ -261,39 +259,26 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_dequant_kernel(w4a16_fp4 w,
   const int64_t tile = (int64_t)blockIdx.y * fp4_row_tiles(w.rows) + n / kFp4Rows;
   const uint8_t* scales = w.scales + tile * atoms * kFp4Atom + 16 * (n & 31) + 4 * (n % kFp4Rows >> 5);
   const float factor = w.row_scale ? w.row_scale[r] : 1.0f;
-  uint2 code[kBack];
-  uint32_t byte[kBack];
+  const int c = part * blockDim.x + threadIdx.x, b = mx ? c / 2 : c;
+  if (c >= units) return;
+  const uint2 code = *reinterpret_cast<const uint2*>(w.codes + r * (w.K / 2) + 8 * (int64_t)c);
+  const uint32_t byte = scales[(int64_t)(b / 4) * kFp4Atom + b % 4];
+  float s = 1.0f, f = factor;
+  if (mx) f = __fmul_rn(byte == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte - 127), factor);
+  else s = (byte & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte & 0x7Fu) << 20 | (byte & 0x80u) << 24), exp2n(120));
+  const __half2 sh = __float2half2_rn(s);
+  uint32_t out[8];
 #pragma unroll
-  for (int i = 0; i < kBack; ++i) {
-    const int c = (part * kBack + i) * kQuantThreads + threadIdx.x, b = mx ? c / 2 : c;
-    code[i] = make_uint2(0, 0);
-    byte[i] = 0;
-    if (c < units) {
-      code[i] = *reinterpret_cast<const uint2*>(w.codes + r * (w.K / 2) + 8 * (int64_t)c);
-      byte[i] = scales[(int64_t)(b / 4) * kFp4Atom + b % 4];
-    }
+  for (int k = 0; k < 8; ++k) {
+    uint32_t pair;
+    asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(pair) : "r"((k < 4 ? code.x : code.y) >> (8 * (k % 4))));
+    const float2 h = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&pair), sh));
+    const __nv_bfloat162 o = __floats2bfloat162_rn(__fmul_rn(h.x, f), __fmul_rn(h.y, f));
+    out[k] = *reinterpret_cast<const uint32_t*>(&o);
   }
-#pragma unroll
-  for (int i = 0; i < kBack; ++i) {
-    const int c = (part * kBack + i) * kQuantThreads + threadIdx.x;
-    if (c >= units) break;
-    float s = 1.0f, f = factor;
-    if (mx) f = __fmul_rn(byte[i] == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte[i] - 127), factor);
-    else s = (byte[i] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte[i] & 0x7Fu) << 20 | (byte[i] & 0x80u) << 24), exp2n(120));
-    const __half2 sh = __float2half2_rn(s);
-    uint32_t out[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t pair;
-      asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(pair) : "r"((k < 4 ? code[i].x : code[i].y) >> (8 * (k % 4))));
-      const float2 h = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&pair), sh));
-      const __nv_bfloat162 o = __floats2bfloat162_rn(__fmul_rn(h.x, f), __fmul_rn(h.y, f));
-      out[k] = *reinterpret_cast<const uint32_t*>(&o);
-    }
-    uint4* to = reinterpret_cast<uint4*>(y + r * w.K + 16 * (int64_t)c);
-    to[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    to[1] = make_uint4(out[4], out[5], out[6], out[7]);
-  }
+  uint4* to = reinterpret_cast<uint4*>(y + r * w.K + 16 * (int64_t)c);
+  to[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  to[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 }  // namespace
@@ -305,13 +290,17 @@ cudaError_t quant_f(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
   Fp4RouteArgs none = {};
   void* args[] = {const_cast<Fp4QuantArgs*>(&a), &none};
   // Few rows: a thread a unit, for the latency (1 x 2560 1.4 us; 333 x 2304 1.6 us so and with four units a thread).
-  // Many: four, whose loads are in flight together; us with one / two / four, nv: 4096 x 2560 6.9 / 6.2 / 6.2, 4001 x
-  // 10240 47 / 22.5 / 20.1, 8192 x 16384 119 / 71 / 55 (HBM's 51).
+  // Many: four or five, whose loads are in flight together, whichever leaves fewer threads without; us with one / two /
+  // four / five, nv: 4096 x 2560 6.9 / 6.2 / 6.4 / 5.5, 4001 x 10240 47 / 22.5 / 21.0 / 19.0 (HBM's 15.6), 8192 x 16384
+  // 119 / 71 / 56.3 / 59.3 (HBM's 51).
   const int all = fp4_atoms(a.K, FMT) * 4 * fp4_block(FMT) / 16;
   const bool one = a.rows <= 152 && all <= kQuantMost;
-  int threads = ((one ? all : (all + 3) / 4) + 31) / 32 * 32;
-  threads = threads > kQuantMost ? kQuantMost : threads;
-  const void* fn = one ? (const void*)fp4_quant_kernel<FMT, 1, kNone> : (const void*)fp4_quant_kernel<FMT, 4, kNone>;
+  auto threads_of = [&](int units) { return ((all + units - 1) / units + 31) / 32 * 32; };
+  const int each = one ? 1 : 5 * threads_of(5) <= 4 * threads_of(4) ? 5 : 4;
+  const int threads = threads_of(each) > kQuantMost ? kQuantMost : threads_of(each);
+  const void* fn = each == 1   ? (const void*)fp4_quant_kernel<FMT, 1, kNone>
+                   : each == 4 ? (const void*)fp4_quant_kernel<FMT, 4, kNone>
+                               : (const void*)fp4_quant_kernel<FMT, 5, kNone>;
   return launch(fn, dim3((unsigned)a.group, (unsigned)(a.rows / a.group)), threads, 0, args, pdl, s);
 }
 
@@ -346,10 +335,12 @@ cudaError_t launch_fp4_route_quant(const Fp4RouteArgs& r, const Fp4QuantArgs& q,
 }
 
 cudaError_t launch_fp4_dequant(const w4a16_fp4& w, uint16_t* y, int pdl, cudaStream_t s) {
-  const int64_t parts = (w.K / 16 + kBack * kQuantThreads - 1) / (kBack * kQuantThreads);
+  // equal parts of a row, of whole warps
+  const int units = w.K / 16, parts = (units + kBackThreads - 1) / kBackThreads;
+  const int threads = ((units + parts - 1) / parts + 31) / 32 * 32;
   void* args[] = {const_cast<w4a16_fp4*>(&w), &y};
   if (parts > 65535) return cudaErrorInvalidConfiguration;
-  return launch((const void*)fp4_dequant_kernel, dim3((unsigned)w.rows, (unsigned)w.experts, (unsigned)parts), kQuantThreads, 0, args, pdl, s);
+  return launch((const void*)fp4_dequant_kernel, dim3((unsigned)w.rows, (unsigned)w.experts, (unsigned)parts), threads, 0, args, pdl, s);
 }
 
 }  // namespace w4a16
