@@ -491,7 +491,7 @@ int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream);
 /* y[m][n] = bf16( x'[m] . W[n] ), x' = x quantised row by row as above, in w's
  * format; products of codes and scales are exact, their sums fp32.  x bf16, row
  * m at x + m * x_stride (a multiple of 8; 16-byte aligned), y bf16 [M][w->rows] (or
- * [M][w->rows / 2] for an act), 2-byte aligned, not over x.  Up to 128 rows a
+ * [M][w->rows / 2] for an act), 2-byte aligned, not over x.  Up to 64 rows a
  * row's result is the one-row call's, bit for bit; more rows are summed in
  * another order (one piece of K instead of the splits that few rows of W take).
  * workspace: device memory of

@@ -13,15 +13,14 @@
 //   warp 0      TMA producer
 //   warp 1      scales from shared to tensor memory, MMAs, commits
 //   warps 2-5   epilogue: accumulator -> registers, factors, activation, bf16
-//               stores; two accumulators (one for NT = 128), so that the next
-//               tile's MMAs run
+//               stores; two accumulators, so that the next tile's MMAs run
 // Two CTAs an SM: what a stage costs beside its bytes is the issue of eight
 // copies of scales and four MMAs, and two warps issue side by side.
 //
 // K split over a cluster.  Where W has few row tiles, `split` CTAs take a
 // tile's stages between them; every CTA then sends each other one its columns
 // through distributed shared memory, and the sums are added in the order of K.
-// The split depends on W's shape alone: up to 128 rows of x a row's result is
+// The split depends on W's shape alone: up to 64 rows of x a row's result is
 // the same, bit for bit, whatever the other rows of the call.
 //
 // A few activation rows (decode, verify) are quantised in the kernel, by the
@@ -70,7 +69,7 @@ struct Geo {
   static constexpr int kStage = kWTile + kScaleTile + kX + 4 * kXAtom;
   static constexpr int kPast = kFp4Atom - kXAtom;  // bytes that the last atom's copy reads past the ring
   static constexpr int kStages = (kRing - kPast) / kStage;
-  static constexpr int kAcc = NT == 128 ? 1 : 2;
+  static constexpr int kAcc = 2;
   static constexpr uint32_t kTmemCols = 256;
   static constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
   static constexpr int kSmem = kStages * kStage + kPast + kBars * 8 + 16;
@@ -510,7 +509,7 @@ int own_slots(int stages) {
 
 struct Device {
   int sms = 0;
-  bool attr[10] = {};
+  bool attr[8] = {};
 };
 Device g_dev[64];
 
@@ -518,7 +517,7 @@ template <int NT, int FMT, bool OWN = false>
 cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStream_t s) {
   using G = Geo<NT>;
   auto* fn = fp4_mm_kernel<NT, FMT, OWN>;
-  constexpr int kIndex = (OWN ? 4 : NT == 16 ? 0 : NT == 32 ? 1 : NT == 64 ? 2 : 3) * 2 + (FMT == W4A16_FP4_MX);
+  constexpr int kIndex = (OWN ? 3 : NT == 16 ? 0 : NT == 32 ? 1 : 2) * 2 + (FMT == W4A16_FP4_MX);
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -580,7 +579,10 @@ bool fp4_mm_fuses(const w4a16_fp4& w, int M) {
   return w.format == W4A16_FP4_MX || (int64_t)M * w.K <= (M == 1 ? 16384 : 8192);
 }
 
-int fp4_mm_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+// The smallest tile that takes all rows, and from 65 rows on the pair kernel's.  Us with a tile of 64 or 128 here / there:
+// 64 rows to 10240 x 2560 10.2 / 9.4, to 2560 x 10240 10.5 / 15.8; 128 rows 13.2 / 9.6 and 14.7 / 16.6; 100 rows to 262144 x
+// 2560 100 / 82.
+int fp4_mm_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 256; }
 
 cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   const int nt = a.tiles ? a.nt : fp4_mm_tile(a.M);
@@ -598,8 +600,7 @@ cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   switch (nt) {
     case 16: return mx ? launch_t<16, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<16, W4A16_FP4_NV>(a, p, pdl, s);
     case 32: return mx ? launch_t<32, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<32, W4A16_FP4_NV>(a, p, pdl, s);
-    case 64: return mx ? launch_t<64, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<64, W4A16_FP4_NV>(a, p, pdl, s);
-    default: return mx ? launch_t<128, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<128, W4A16_FP4_NV>(a, p, pdl, s);
+    default: return mx ? launch_t<64, W4A16_FP4_MX>(a, p, pdl, s) : launch_t<64, W4A16_FP4_NV>(a, p, pdl, s);
   }
 }
 

@@ -224,14 +224,14 @@ def test_gated_many_rows(fmt, act):
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
 @pytest.mark.parametrize("N,K", [(300, 2560), (2560, 1024), (10240, 512), (40000, 96), (100, 256)])
 def test_rows_do_not_depend_on_the_batch(fmt, N, K):
-    """Up to 128 rows a row's result is the one-row call's, bit for bit."""
+    """Up to 64 rows a row's result is the one-row call's, bit for bit."""
     from skinny_gemm_gb300 import ops
 
-    x, w, _, _ = product(ops, fmt, 128, N, K)
-    one = torch.cat([ops.fp4_mm(x[i:i + 1], w) for i in (0, 3, 31, 100, 127)])
-    for M in (4, 16, 17, 32, 40, 64, 65, 101, 128):
+    x, w, _, _ = product(ops, fmt, 64, N, K)
+    one = torch.cat([ops.fp4_mm(x[i:i + 1], w) for i in (0, 3, 15, 31, 50, 63)])
+    for M in (4, 5, 16, 17, 32, 33, 55, 64):
         y = ops.fp4_mm(x[:M], w)
-        for j, i in enumerate((0, 3, 31, 100, 127)):
+        for j, i in enumerate((0, 3, 15, 31, 50, 63)):
             if i < M:
                 assert torch.equal(y[i], one[j]), (M, i)
 
