@@ -71,7 +71,7 @@ struct Geo {
   static constexpr int kStages = (kRing - kPast) / kStage;
   static constexpr int kAcc = 2;
   static constexpr uint32_t kTmemCols = 256;
-  static constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kAcc + 2;
   static constexpr int kSmem = kStages * kStage + kPast + kBars * 8 + 16;
   static_assert(kSmem <= kCtaSmem && kAcc * NT + kStages * kSetCols <= (int)kTmemCols, "half an SM's shared and tensor memory");
   static_assert(NT * kWRows * 4 <= kStages * kStage, "the partial sums of a split tile, which else take the stages' place");
@@ -92,60 +92,64 @@ constexpr int kOwnUnits = 512;  // of sixteen values: most of a CTA
 constexpr int kOwnParts = kOwnRows * kWRows * 4 / kMaxSplit * (kMaxSplit - 1);
 
 struct OwnRows {
-  uint32_t peak[kOwnRows], finite[kOwnRows];  // largest |x| of a row, and of its finite values where that is not
+  uint32_t peak[kOwnRows], finite[kOwnRows];  // largest |x| of a row's part, and of its finite values where that is not
+  uint32_t whole[kOwnRows];                   // ... of the row: the largest of the cluster's parts
   float factor[kOwnRows];
 };
 
+// nv needs a row's peak before its first code.  Each CTA finds its part's, and sends it to all of the cluster
+// (`told`: a barrier of M * split arrivals); a row or so (two units a thread) is read whole instead.  Us so / by the other
+// way in every case: 1 x 2560 to 10240 5.9 / 6.7, 5 x 2304 gated to 9216 9.6 / 11.0, 5 x 10240 to 2560 8.9 / 17.
 template <int FMT>
-__device__ __forceinline__ void quantise_own(const Fp4MmParams& p, OwnRows* own, uint32_t codes, uint32_t scales, int t, int k0, int k1) {
-  constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;
+__device__ __forceinline__ bool quantise_own(const Fp4MmParams& p, OwnRows* own, uint32_t told, uint32_t codes, uint32_t scales, int t, int k0, int k1,
+                                             uint32_t limit) {
+  constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4, kEach = kOwnUnits / kOwnThreads;
   const int units = p.K / 16, lane = t & 31;
   const int per = 16 * (k1 - k0), all = p.M * per;  // units of a row's part, whole stages (what lies past K is zero)
-  auto load = [&](int i) {  // the i-th unit of this CTA's part
-    const int m = i / per, c = 16 * k0 + i - m * per;
-    return i < all && c < units ? fp4::load16(p.x + m * p.x_stride + 16 * c) : fp4::zero16();
-  };
-  auto write = [&](int i, const fp4::Vec16& v) {  // (whole warps)
-    const int m = min(i / per, p.M - 1), u = i - i / per * per;
-    uint32_t peak = fp4::peak16(v);
-    if (FMT == W4A16_FP4_MX) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
-    int e = 0;
-    if (FMT == W4A16_FP4_NV) e = (int)(__float_as_uint(own->factor[m]) >> 23) - 127;
-    uint32_t byte;
-    const uint2 code = fp4::block16<FMT>(v, peak, e, byte);
-    const int stage = u / 16, unit = u % 16, b = FMT == W4A16_FP4_MX ? unit / 2 : unit;
-    if (i < all) {
-      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(codes + (uint32_t)(stage * kOwnStage + m * 128 + (((unit >> 1) ^ (m & 7)) << 4) + (unit & 1) * 8)),
-                   "r"(code.x), "r"(code.y)
-                   : "memory");
-      if (FMT == W4A16_FP4_NV || !(unit & 1))
-        asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + (uint32_t)((stage * kAtoms + b / 4) * kOwnAtom + m * 16 + b % 4)), "r"(byte) : "memory");
-    }
-  };
-  constexpr int kBatch = 4;
-  fp4::Vec16 mine[kOwnUnits / kOwnThreads];  // (requested before the peaks are known)
+  fp4::Vec16 mine[kEach];
+  int row[kEach];
 #pragma unroll
-  for (int j = 0; j < kOwnUnits / kOwnThreads; ++j) mine[j] = load(t + j * kOwnThreads);
+  for (int j = 0; j < kEach; ++j) {
+    const int i = t + j * kOwnThreads, m = i / per, c = 16 * k0 + i - m * per;
+    row[j] = min(m, p.M - 1);
+    mine[j] = i < all && c < units ? fp4::load16(p.x + m * p.x_stride + 16 * c) : fp4::zero16();
+  }
+  constexpr int kWhole = 2;
+  const bool whole = FMT == W4A16_FP4_NV && p.split > 1 && p.M * units <= kWhole * kOwnThreads;
+  fp4::Vec16 rows[kWhole];
+  int rows_of[kWhole];
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < kWhole; ++j) {
+      const int i = t + j * kOwnThreads, m = i / units;
+      rows_of[j] = min(m, p.M - 1);
+      rows[j] = m < p.M ? fp4::load16(p.x + m * p.x_stride + 16 * (i - m * units)) : fp4::zero16();
+    }
+  }
+  bool ok = true;
   if (FMT == W4A16_FP4_NV) {
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kOwnThreads) : "memory"); };
-    // 128, 64, 32, 16 or 8 threads a row, each of which keeps its own peak until the end
-    int each = kOwnThreads;
-    while (each * p.M > kOwnThreads) each /= 2;
-    const int m = t / each, at = t % each;
+    auto fold = [&](uint32_t peak, int m, uint32_t* to) {
+      const int m0 = __shfl_sync(0xffffffffu, m, 0), m1 = __shfl_sync(0xffffffffu, m, 31);
+      if (m1 - m0 <= 1) {  // the warp's units lie in one row or two
+        const uint32_t a = __reduce_max_sync(0xffffffffu, m == m0 ? peak : 0u), b = __reduce_max_sync(0xffffffffu, m == m0 ? 0u : peak);
+        if (lane == 0) atomicMax(to + m0, a);
+        if (lane == 31 && m1 > m0) atomicMax(to + m1, b);
+      } else {
+        atomicMax(to + m, peak);
+      }
+    };
     auto peaks = [&](auto&& of, uint32_t* to) {
-      uint32_t peak = 0;
-      if (m < p.M)
-        for (int c0 = at; c0 < units; c0 += kBatch * each) {
-          fp4::Vec16 v[kBatch];
+      if (whole) {
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j)
-            v[j] = c0 + j * each < units ? fp4::load16(p.x + m * p.x_stride + 16 * (c0 + j * each)) : fp4::zero16();
+        for (int j = 0; j < kWhole; ++j) fold(of(rows[j]), rows_of[j], to);
+      } else {
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) peak = max(peak, of(v[j]));
+        for (int j = 0; j < kEach; ++j) {
+          if (j * kOwnThreads >= all) break;
+          fold(of(mine[j]), row[j], to);
         }
-      __syncwarp();
-      for (int d = 1; d < each && d < 32; d *= 2) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, d));
-      if (m < p.M && at % 32 == 0) atomicMax(to + m, peak);
+      }
     };
     peaks([](const fp4::Vec16& v) { return fp4::peak16(v); }, own->peak);
     sync();
@@ -154,13 +158,42 @@ __device__ __forceinline__ void quantise_own(const Fp4MmParams& p, OwnRows* own,
       peaks([](const fp4::Vec16& v) { return fp4::finite_peak16(v); }, own->finite);
       sync();
     }
-    if (t < p.M) own->factor[t] = fp4::exp2n(fp4::factor_exp(odd >> t & 1 ? own->finite[t] : own->peak[t]));
+    auto part = [&](int m) { return odd >> m & 1 ? own->finite[m] : own->peak[m]; };
+    if (p.split > 1) cluster_wait();  // (the others are there)
+    if (p.split == 1 || whole) {
+      if (t < p.M) own->whole[t] = part(t);
+    } else {
+      if (t < p.M * p.split) {
+        const int m = t % p.M, g = t / p.M;
+        red_max_cluster(cluster_map(smem_u32(own->whole + m), (uint32_t)g), part(m));
+        mbar_arrive_release_cluster(cluster_map(told, (uint32_t)g));
+      }
+      __syncwarp();
+      ok = mbar_wait_acquire_cluster(told, 0, limit);
+    }
+    if (t < p.M) own->factor[t] = fp4::exp2n(fp4::factor_exp(own->whole[t]));
     sync();
   }
 #pragma unroll
-  for (int j = 0; j < kOwnUnits / kOwnThreads; ++j)
-    if (j * kOwnThreads < all) write(t + j * kOwnThreads, mine[j]);
+  for (int j = 0; j < kEach; ++j) {  // (whole warps)
+    if (j * kOwnThreads >= all) break;
+    const int i = t + j * kOwnThreads, m = row[j], u = i % per;
+    uint32_t peak = fp4::peak16(mine[j]);
+    if (FMT == W4A16_FP4_MX) peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+    const int e = FMT == W4A16_FP4_NV ? (int)(__float_as_uint(own->factor[m]) >> 23) - 127 : 0;
+    uint32_t byte;
+    const uint2 code = fp4::block16<FMT>(mine[j], peak, e, byte);
+    const int stage = u / 16, unit = u % 16, b = FMT == W4A16_FP4_MX ? unit / 2 : unit;
+    if (i < all) {
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(codes + (uint32_t)(stage * kOwnStage + m * 128 + (((unit >> 1) ^ (m & 7)) << 4) + (unit & 1) * 8)),
+                   "r"(code.x), "r"(code.y)
+                   : "memory");
+      if (FMT == W4A16_FP4_NV || !(unit & 1))
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + (uint32_t)((stage * kAtoms + b / 4) * kOwnAtom + m * 16 + b % 4)), "r"(byte) : "memory");
+    }
+  }
   fence_proxy_async();
+  return ok;
 }
 
 // One sum of row `row` of W and place `at` of x, whole warps (gate and up rows are neighbours).
@@ -222,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   auto empty = [&](int s) { return bars + 8u * (S + s); };
   auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };
   auto acc_free = [&](int b) { return bars + 8u * (2 * S + NB + b); };
-  const uint32_t own_full = bars + 8u * (2 * S + 2 * NB);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (own_full + 8 - sb));
+  const uint32_t own_full = bars + 8u * (2 * S + 2 * NB), told = own_full + 8;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (told + 8 - sb));
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   OwnRows* own = reinterpret_cast<OwnRows*>(s_tmem + 2);
 
@@ -237,10 +270,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
       mbar_init(acc_free(b), 4);
     }
     mbar_init(own_full, kOwnThreads);
+    if (OWN) mbar_init(told, (uint32_t)(p.M * split));
     *s_abort = 0;
     fence_barrier_init();
   }
-  if (OWN && threadIdx.x >= 32 && threadIdx.x < 32 + kOwnRows) own->peak[threadIdx.x - 32] = own->finite[threadIdx.x - 32] = 0;
+  if (OWN && threadIdx.x >= 32 && threadIdx.x < 32 + kOwnRows) own->peak[threadIdx.x - 32] = own->finite[threadIdx.x - 32] = own->whole[threadIdx.x - 32] = 0;
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), G::kTmemCols);
     tmem_relinquish();
@@ -374,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
     // ---- epilogue ----
     const int q = warp & 3, r = 32 * q + lane;
     if (OWN) {
-      quantise_own<FMT>(p, own, own_codes, own_scales, threadIdx.x - 64, k0, k1);
+      if (!quantise_own<FMT>(p, own, told, own_codes, own_scales, threadIdx.x - 64, k0, k1, limit) && lane == 0) timeout();
       mbar_arrive(own_full);
     }
     const float* xf = OWN ? (FMT == W4A16_FP4_NV ? own->factor : nullptr) : p.xf;
@@ -427,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
     const bool live = first < units && !*s_abort;
     const int count = min(NT, p.M - xt * NT), per = (count + split - 1) / split;
     if (!kParts) cluster_arrive();
-    cluster_wait();
+    if (!(OWN && FMT == W4A16_FP4_NV && warp >= 2)) cluster_wait();  // (those have waited)
     if (live && warp >= 2) {
       tc_fence_after_sync();
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
@@ -499,7 +533,7 @@ int split_of(int row_tiles, int stages) {
 
 // Where the kernel quantises: shared memory of a ring of `slots` beside a CTA's `stages` of x, and how many slots fit.
 constexpr int own_smem(int slots, int stages) {
-  return slots * (kWTile + kScaleTile) + stages * (kOwnStage + 4 * kOwnAtom) + kOwnAtom + kOwnParts + (2 * slots + 5) * 8 + 8 + (int)sizeof(OwnRows);
+  return slots * (kWTile + kScaleTile) + stages * (kOwnStage + 4 * kOwnAtom) + kOwnAtom + kOwnParts + (2 * slots + 6) * 8 + 8 + (int)sizeof(OwnRows);
 }
 int own_slots(int stages) {
   int slots = 5;
@@ -569,14 +603,13 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
 
 }  // namespace
 
+// The GPU's us so / with the quantiser's launch before it: nv 1 row x 2560 to 10240 5.7 / 6.7, 5 rows 8.2 / 7.6, 1 x 2560 to
+// 262144 56.6 / 58.3, 5 x 2304 gated to 9216 9.7 / 9.1; mx 5 x 10240 to 2560 5.8 / 7.0.  A call from the host takes 10.5 to
+// 11.5 / 13.5 to 15 in all of these.  Past kOwnUnits the CTAs' part grows: 16 x 2560 (mx) 9.4 / 7.7.
 bool fp4_mm_fuses(const w4a16_fp4& w, int M) {
   const int stages = (w.K + kFp4StageK - 1) / kFp4StageK, split = split_of((int)fp4_row_tiles(w.rows), stages);
   const int part = (stages + split - 1) / split;
-  if (M > kOwnRows || M * 16 * part > kOwnUnits || own_slots(part) < 3) return false;
-  // nv needs the peaks of whole rows, which all CTAs read: worth a launch for a row or so.  Us so / with the quantiser's
-  // launch: one row x 2560 to 10240 rows 6.4 / 6.7, 5 rows 9.9 / 7.4, 5 x 10240 17 / 7.7.  mx: 5 x 10240 to 2560 6.2 / 7.0;
-  // 16 x 2560 (past kOwnUnits) 9.4 / 7.7.  The host's part of a call is 2 to 3 us less in every case.
-  return w.format == W4A16_FP4_MX || (int64_t)M * w.K <= (M == 1 ? 16384 : 8192);
+  return M <= kOwnRows && M * 16 * part <= kOwnUnits && own_slots(part) >= 3;
 }
 
 // The smallest tile that takes all rows, and from 65 rows on the pair kernel's.  Us with a tile of 64 or 128 here / there:
