@@ -758,13 +758,14 @@ Fp4Space fp4_space(int64_t places, int64_t rows, int64_t tiles, int K, int forma
   return s;
 }
 
-// Routed: rows of an activation tile, and the most tiles that there can be.  Twice an expert's mean share, so that most
-// experts have one tile; from some 25 rows on the pair kernel's, however empty: K = 2048, N = 1536, us with the smaller
-// tiles / with it: 64 tokens x 8 of 64 experts (8 rows each) 21 / 30, 500 x 4 of 64 (32) 31.9 / 31.3, 1000 x 1 of 16 (63)
-// 24.8 / 20.1, 1600 x 1 of 16 24.8 / 21.6, 2000 x 2 of 16 40 / 26, 1500 x 6 of 90 84 / 55.
+// Routed: rows of an activation tile, and the most tiles that there can be.  Twice an expert's mean share up to 16 rows;
+// then 32 rows, of which the large experts take two tiles (their weights come from L2 the second time), as a tile of 64
+// has fewer slots in its ring; and from some 40 rows on the pair kernel's tile, however empty.  K = 2048, N = 1536, 64
+// experts, mean rows: us with 32 / 64 / 256: 20 24.1 / 28.0 / 27.9; 31 27.8 / 31.9 / 30.9; 40 33.0 / 34.8 / 34.5; 50 37.3 /
+// 39.0 / 35.9; 63 (16 experts) 19.5 / 20.9 / 20.0; 250 (16) - / 40 (of 128) / 26.
 int fp4_id_tile(int64_t rows, int experts) {
   const int64_t mean = (rows + experts - 1) / experts;
-  return mean > 24 ? 256 : fp4_mm_tile(2 * (int)mean);
+  return mean > 40 ? 256 : mean > 8 ? 32 : 16;
 }
 int fp4_id_span(int64_t rows, int experts) { return fp4_id_tile(rows, experts) > 128 ? 256 : 128; }
 int64_t fp4_id_tiles(int64_t rows, int experts) {
