@@ -918,34 +918,32 @@ class FP4Matrix:
         n = E * fp4_scale_bytes(N, K, format)
         if K <= 0 or K % 32 or N < 0 or E < 1:
             raise ValueError(f"N = {N}, K = {K} (a positive multiple of 32), E = {E}")
-        # one block of memory: scales (a multiple of 512 bytes), codes (of 16), factors; their tensors are made when asked for
-        m, nv = E * N * (K // 2), format == "nv"
-        flat = torch.empty((n + m) // 4 + (E * N if nv else 0), dtype=torch.float32, device=device)
+        # scales (a multiple of 512 bytes) and codes in one block of memory; their tensors are made when asked for
+        flat = torch.empty(n + E * N * (K // 2), dtype=torch.uint8, device=device)
+        f = torch.empty(E * N, dtype=torch.float32, device=device) if format == "nv" else None
         self, at = cls.__new__(cls), flat.data_ptr()
         self.N, self.K, self.E, self.format = N, K, E, format
-        self._flat, self._codes, self._scales, self._row_scale = flat, None, None, None
+        self._flat, self._codes, self._scales, self._row_scale = flat, None, None, f
         self._device, self._dev = flat.device, flat.get_device()
-        self._c = Fp4Struct(at + n, at, at + n + m if nv else None, N, K, E, FP4_FORMATS[format])
+        self._c = Fp4Struct(at + n, at, None if f is None else f.data_ptr(), N, K, E, FP4_FORMATS[format])
         self._ptr = ctypes.addressof(self._c)
         return self
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            self._scales = self._flat.view(torch.uint8)[:self.E * fp4_scale_bytes(self.N, self.K, self.format)]
+            self._scales = self._flat[:self.E * fp4_scale_bytes(self.N, self.K, self.format)]
         return self._scales
 
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
             n = self.E * fp4_scale_bytes(self.N, self.K, self.format)
-            self._codes = self._flat.view(torch.uint8)[n:n + self.E * self.N * (self.K // 2)].view(self.E * self.N, self.K // 2)
+            self._codes = self._flat[n:].view(self.E * self.N, self.K // 2)
         return self._codes
 
     @property
     def row_scale(self) -> torch.Tensor | None:
-        if self._row_scale is None and self._flat is not None and self.format == "nv":
-            self._row_scale = self._flat.narrow(0, self._flat.shape[0] - self.E * self.N, self.E * self.N)
         return self._row_scale
 
     @classmethod
