@@ -243,3 +243,113 @@ def test_waits_run_out_and_the_context_survives(fmt, M, N, K, monkeypatch):
     for _ in range(3):
         assert torch.equal(ops.fp4_mm(x, w), want)
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("M,N,K", [(3, 512, 2048), (30, 512, 320), (9, 40000, 96), (300, 512, 320), (300, 520, 64)])
+def test_outputs_at_any_address(M, N, K, act):
+    """Outputs that begin at any even address are written whole, and nothing beside them."""
+    x, w = made("nv", M, N, K)
+    call = (lambda **kw: ops.fp4_mm(x, w, **kw)) if act is None else (lambda **kw: ops.fp4_gated(x, w, act, **kw))
+    want = call()
+    n = want.numel()
+    for shift in (0, 1, 2, 4, 8, 13, 16):
+        buf = torch.full((n + 64,), 5.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[16 + shift:16 + shift + n].view(want.shape)
+        call(out=out)
+        assert torch.equal(out, want) and (buf[:16 + shift] == 5).all() and (buf[16 + shift + n:] == 5).all(), shift
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("setting", ["0", "1"])
+def test_launch_settings(setting, monkeypatch):
+    """Plain launches, and overlapped ones without early fetches, give the same bits."""
+    cases = [made(*c) for c in CASES]
+    xe, we = made("nv", 50, 200, 96, E=5)
+    ids = torch.randint(0, 5, (50, 3), generator=gen(9), dtype=torch.int32).cuda()
+    want = [ops.fp4_mm(x, w) for x, w in cases] + [ops.fp4_mm_id(xe, we, ids)]
+    monkeypatch.setenv("W4A16_PDL", setting)
+    ops.lib().w4a16_debug_reload_env()
+    try:
+        got = [ops.fp4_mm(x, w) for x, w in cases] + [ops.fp4_mm_id(xe, we, ids)]
+        torch.cuda.synchronize()
+    finally:
+        monkeypatch.delenv("W4A16_PDL")
+        ops.lib().w4a16_debug_reload_env()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and ops.device_status() == 0
+
+
+def test_between_the_library_s_other_calls():
+    """Attention over the paged cache, affine 4-bit products and microscaled ones back to back on one stream, as launches that
+    overlap; captured and not: the bits of the calls one by one."""
+    from skinny_gemm_gb300 import synth
+
+    H, hq, hkv, dim, T, E = 512, 8, 2, 64, 6, 3
+    g = gen("mixed")
+    wq = ops.W4Matrix.from_host(synth.make_weights(1, hq * dim, H))
+    rand = lambda *s: torch.randn(*s, generator=g).div(s[-1] ** 0.5).to(torch.bfloat16).cuda()  # noqa: E731
+    wkv, wo, w13, w2 = ops.fp4_quant(rand(2 * hkv * dim, H)), ops.fp4_quant(rand(H, hq * dim), "mx"), ops.FP4Matrix.gated(rand(1536, H), rand(1536, H)), ops.fp4_quant(rand(H, 1536))
+    we = ops.fp4_quant(rand(E, 256, H), "mx")
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    big = torch.randn(200, H, generator=g).to(torch.bfloat16).cuda()
+    ids = torch.randint(0, E, (T, 2), generator=g, dtype=torch.int32).cuda()
+    cached = torch.tensor([700, 30], dtype=torch.int32, device="cuda")
+    new = torch.tensor([4, 2], dtype=torch.int32, device="cuda")
+    cache = ops.KVCache.empty(64, hkv, 16, dim)
+    free = torch.arange(64, dtype=torch.int32, device="cuda")
+    table = torch.full((2, 48), -1, dtype=torch.int32, device="cuda")
+    first = ops.kv_plan(torch.zeros_like(cached), cached, table, free, 730, 16)
+    ops.kv_append(*(torch.randn(730, hkv, dim, generator=g).to(torch.bfloat16).cuda() for _ in range(2)), cache, first.slots)
+    plan = ops.kv_plan(cached, new, table, free, T, 16, head=first.head)
+    torch.cuda.synchronize()
+
+    def layer(sync=lambda: None):
+        q = ops.mm(x, wq)
+        sync()
+        kv = ops.fp4_mm(x, wkv).view(T, 2 * hkv, dim)
+        sync()
+        ops.kv_append(kv[:, :hkv], kv[:, hkv:], cache, plan.slots)
+        sync()
+        o = ops.kv_attention(q.view(T, hq, dim), cache, table, plan.cu, plan.lens, 4, 768)
+        sync()
+        y = ops.fp4_mm(o.view(T, -1), wo)
+        sync()
+        h = ops.fp4_gated(y, w13)
+        sync()
+        z = ops.fp4_mm(h, w2)
+        sync()
+        r = ops.fp4_mm_id(z, we, ids)
+        sync()
+        p = ops.fp4_gated(big, w13)
+        sync()
+        return q, kv, o, y, h, z, r, p
+
+    want = [t.clone() for t in layer(torch.cuda.synchronize)]
+    for _ in range(20):
+        got = layer()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer()
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and ops.device_status() == 0
+
+
+@pytest.mark.parametrize("T,top,E", [(6, 1, 4), (300, 4, 9)])
+def test_routed_waits_run_out(T, top, E, monkeypatch):
+    x, w = made("nv", T, 200, 320, E)
+    ids = torch.randint(0, E, (T, top), generator=gen(T), dtype=torch.int32).cuda()
+    want = ops.fp4_mm_id(x, w, ids)
+    monkeypatch.setenv("W4A16_FAULT", "wait")
+    ops.lib().w4a16_debug_reload_env()
+    try:
+        ops.fp4_mm_id(x, w, ids)
+        flags = ops.device_status()
+    finally:
+        monkeypatch.delenv("W4A16_FAULT")
+        ops.lib().w4a16_debug_reload_env()
+    assert flags == ops.DEVICE_TIMEOUT
+    assert torch.equal(ops.fp4_mm_id(x, w, ids), want) and ops.device_status() == 0
