@@ -474,12 +474,12 @@ size_t w4a16_fp4_scale_bytes(int rows, int K, int format);
  *   code = e2m1(x / scale [/ f]), to nearest, ties to the even code, at most 6;
  *          a code of 0 may have either sign
  * A block with a NaN or an infinity gets a NaN scale and codes 0; q is over a
- * row's finite values.  Zero rows is a no-op. */
+ * row's finite values.  out must not overlap x.  Zero rows is a no-op. */
 int w4a16_fp4_quant(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* out, void* stream);
 
 /* y[r][k] = bf16(code * scale * row_scale), bf16 [experts * rows][K], 16-byte
- * aligned.  Exact for what w4a16_fp4_quant writes, but for values past bf16's
- * range; a NaN scale makes its block NaN. */
+ * aligned, not over w.  Exact for what w4a16_fp4_quant writes, but for values
+ * past bf16's range; a NaN scale makes its block NaN. */
 int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream);
 
 /* What a product gives per row: W's rows n as they are, or pairs of them,
@@ -491,7 +491,7 @@ int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream);
 /* y[m][n] = bf16( x'[m] . W[n] ), x' = x quantised row by row as above, in w's
  * format; products of codes and scales are exact, their sums fp32.  x bf16, row
  * m at x + m * x_stride (a multiple of 8; 16-byte aligned), y bf16 [M][w->rows] (or
- * [M][w->rows / 2] for an act), 2-byte aligned, not over x.  Up to 64 rows a
+ * [M][w->rows / 2] for an act), 2-byte aligned, not over x or w.  Up to 64 rows a
  * row's result is the one-row call's, bit for bit; more rows are summed in
  * another order (one piece of K instead of the splits that few rows of W take).
  * workspace: device memory of

@@ -720,11 +720,21 @@ int check_fp4_rows(const void* x, int64_t x_stride, int64_t rows, int K) {
   return W4A16_OK;
 }
 
-// CTAs write y while others read x.
-int check_fp4_apart(const void* x, int64_t x_stride, int64_t x_rows, int K, const void* y, int64_t y_values) {
+// CTAs write the one while others read the other.
+bool fp4_overlap(const void* x, int64_t x_bytes, const void* y, int64_t y_bytes) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-  const uintptr_t n = 2 * (uintptr_t)((x_rows > 1 ? (x_rows - 1) * x_stride : 0) + K), m = 2 * (uintptr_t)y_values;
-  return a < b + m && b < a + n ? fail(W4A16_ERR_SHAPE, "y overlaps x") : W4A16_OK;
+  return a < b + (uintptr_t)y_bytes && b < a + (uintptr_t)x_bytes;
+}
+bool fp4_overlaps(const w4a16_fp4& m, const void* y, int64_t y_bytes) {
+  return fp4_overlap(m.codes, (int64_t)m.experts * m.rows * (m.K / 2), y, y_bytes) ||
+         fp4_overlap(m.scales, m.experts * fp4_scale_bytes(m.rows, m.K, m.format), y, y_bytes) ||
+         (m.row_scale && fp4_overlap(m.row_scale, 4LL * m.experts * m.rows, y, y_bytes));
+}
+int64_t fp4_x_bytes(int64_t x_stride, int64_t rows, int K) { return 2 * ((rows > 1 ? (rows - 1) * x_stride : 0) + K); }
+int64_t fp4_y_bytes(const w4a16_fp4* w, int64_t rows, int act) { return 2 * rows * (act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2); }
+int check_fp4_apart(const void* x, int64_t x_bytes, const w4a16_fp4* w, const void* y, int64_t y_bytes) {
+  if (fp4_overlap(x, x_bytes, y, y_bytes)) return fail(W4A16_ERR_SHAPE, "y overlaps x");
+  return fp4_overlaps(*w, y, y_bytes) ? fail(W4A16_ERR_SHAPE, "y overlaps w") : W4A16_OK;
 }
 
 int check_fp4_act(const w4a16_fp4* w, int act) {
@@ -794,6 +804,7 @@ int w4a16_fp4_quant(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* out,
   if (out->format == W4A16_FP4_NV && !out->row_scale) return fail(W4A16_ERR_NULL, "out: nv needs row_scale");
   const int rows = out->rows * out->experts;
   if (int rc = check_fp4_rows(x, x_stride, rows, out->K)) return rc;
+  if (fp4_overlaps(*out, x, fp4_x_bytes(x_stride, rows, out->K))) return fail(W4A16_ERR_SHAPE, "out overlaps x");
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
   Fp4QuantArgs a{x, x_stride, out->codes, out->scales, out->row_scale, rows, out->K, out->rows, out->format};
   cudaError_t e = launch_fp4_quant(a, env().pdl, static_cast<cudaStream_t>(stream));
@@ -806,6 +817,7 @@ int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream) {
   if (w->rows == 0) return W4A16_OK;
   if (!y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(y, 16)) return fail(W4A16_ERR_ALIGN, "y must be 16-byte aligned");
+  if (fp4_overlaps(*w, y, 2LL * w->experts * w->rows * w->K)) return fail(W4A16_ERR_SHAPE, "y overlaps w");
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
   cudaError_t e = launch_fp4_dequant(*w, y, env().pdl, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_dequant launch");
@@ -827,7 +839,7 @@ int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a1
   if (int rc = check_fp4_rows(x, x_stride, M, w->K)) return rc;
   if (!y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "y must be 2-byte aligned");
-  if (int rc = check_fp4_apart(x, x_stride, M, w->K, y, (int64_t)M * (act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2))) return rc;
+  if (int rc = check_fp4_apart(x, fp4_x_bytes(x_stride, M, w->K), w, y, fp4_y_bytes(w, M, act))) return rc;
   const Fp4Space sp = fp4_space(M, M, 0, w->K, w->format);
   if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total)) return rc;
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
@@ -871,6 +883,8 @@ int w4a16_fp4_mm_q(const w4a16_fp4* x, const w4a16_fp4* w, w4a16_bf16* y, int ac
   if (x->rows == 0) return W4A16_OK;
   if (!y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "y must be 2-byte aligned");
+  const int64_t y_bytes = fp4_y_bytes(w, x->rows, act);
+  if (fp4_overlaps(*x, y, y_bytes) || fp4_overlaps(*w, y, y_bytes)) return fail(W4A16_ERR_SHAPE, "y overlaps x or w");
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
   Fp4MmArgs a = {};
   a.xc = x->codes;
@@ -904,8 +918,7 @@ int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, c
   if (int rc = check_fp4_rows(x, x_stride, T, w->K)) return rc;
   if (!ids || !y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(ids, 4) || misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "ids must be 4-byte and y 2-byte aligned");
-  if (int rc = check_fp4_apart(x, x_stride, T, w->K, y, (int64_t)T * top * (act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2)))
-    return rc;
+  if (int rc = check_fp4_apart(x, fp4_x_bytes(x_stride, T, w->K), w, y, fp4_y_bytes(w, (int64_t)T * top, act))) return rc;
   const int64_t rows = (int64_t)T * top, tiles = fp4_id_tiles(rows, w->experts), places = tiles * fp4_id_span(rows, w->experts);
   if (places > INT32_MAX) return fail(W4A16_ERR_EXPERTS, "T * top = %lld rows are too many for one call", (long long)rows);
   const Fp4Space sp = fp4_space(places, rows, tiles, w->K, w->format);

@@ -36,6 +36,7 @@ cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** a
 }
 
 constexpr int kBackThreads = 256;   // most threads of the way back
+constexpr int kGridZ = 65535;       // most CTAs of a grid's third axis
 constexpr int kQuantMost = 768;     // threads of a row: 80 registers each
 constexpr int kFoundMost = 1 << 20; // tokens x routed rows, up to which every token's CTA finds its places itself
 
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kQuantMost, 1) fp4_quant_kernel(Fp4QuantArgs p
 }
 
 // Units of sixteen values: value = bf16(code * scale * factor), exact unless it leaves bf16's range.  code * scale is
-// exact in fp16 for nv (6 significant bits, 2^-10 to 2688).  A thread has one unit.
+// exact in fp16 for nv (6 significant bits, 2^-10 to 2688).  A thread has one unit (of rows past 2^28 values, more).
 __global__ void __launch_bounds__(kBackThreads) fp4_dequant_kernel(w4a16_fp4 w, uint16_t* y) {
   pdl_wait();
   pdl_launch_dependents();
@@ -259,26 +260,27 @@ __global__ void __launch_bounds__(kBackThreads) fp4_dequant_kernel(w4a16_fp4 w, 
   const int64_t tile = (int64_t)blockIdx.y * fp4_row_tiles(w.rows) + n / kFp4Rows;
   const uint8_t* scales = w.scales + tile * atoms * kFp4Atom + 16 * (n & 31) + 4 * (n % kFp4Rows >> 5);
   const float factor = w.row_scale ? w.row_scale[r] : 1.0f;
-  const int c = part * blockDim.x + threadIdx.x, b = mx ? c / 2 : c;
-  if (c >= units) return;
-  const uint2 code = *reinterpret_cast<const uint2*>(w.codes + r * (w.K / 2) + 8 * (int64_t)c);
-  const uint32_t byte = scales[(int64_t)(b / 4) * kFp4Atom + b % 4];
-  float s = 1.0f, f = factor;
-  if (mx) f = __fmul_rn(byte == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte - 127), factor);
-  else s = (byte & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte & 0x7Fu) << 20 | (byte & 0x80u) << 24), exp2n(120));
-  const __half2 sh = __float2half2_rn(s);
-  uint32_t out[8];
+  for (int c = part * blockDim.x + threadIdx.x; c < units; c += gridDim.z * blockDim.x) {
+    const int b = mx ? c / 2 : c;
+    const uint2 code = *reinterpret_cast<const uint2*>(w.codes + r * (w.K / 2) + 8 * (int64_t)c);
+    const uint32_t byte = scales[(int64_t)(b / 4) * kFp4Atom + b % 4];
+    float s = 1.0f, f = factor;
+    if (mx) f = __fmul_rn(byte == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte - 127), factor);
+    else s = (byte & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte & 0x7Fu) << 20 | (byte & 0x80u) << 24), exp2n(120));
+    const __half2 sh = __float2half2_rn(s);
+    uint32_t out[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    uint32_t pair;
-    asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(pair) : "r"((k < 4 ? code.x : code.y) >> (8 * (k % 4))));
-    const float2 h = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&pair), sh));
-    const __nv_bfloat162 o = __floats2bfloat162_rn(__fmul_rn(h.x, f), __fmul_rn(h.y, f));
-    out[k] = *reinterpret_cast<const uint32_t*>(&o);
+    for (int k = 0; k < 8; ++k) {
+      uint32_t pair;
+      asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(pair) : "r"((k < 4 ? code.x : code.y) >> (8 * (k % 4))));
+      const float2 h = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&pair), sh));
+      const __nv_bfloat162 o = __floats2bfloat162_rn(__fmul_rn(h.x, f), __fmul_rn(h.y, f));
+      out[k] = *reinterpret_cast<const uint32_t*>(&o);
+    }
+    uint4* to = reinterpret_cast<uint4*>(y + r * w.K + 16 * (int64_t)c);
+    to[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    to[1] = make_uint4(out[4], out[5], out[6], out[7]);
   }
-  uint4* to = reinterpret_cast<uint4*>(y + r * w.K + 16 * (int64_t)c);
-  to[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  to[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 }  // namespace
@@ -336,10 +338,9 @@ cudaError_t launch_fp4_route_quant(const Fp4RouteArgs& r, const Fp4QuantArgs& q,
 
 cudaError_t launch_fp4_dequant(const w4a16_fp4& w, uint16_t* y, int pdl, cudaStream_t s) {
   // equal parts of a row, of whole warps
-  const int units = w.K / 16, parts = (units + kBackThreads - 1) / kBackThreads;
-  const int threads = ((units + parts - 1) / parts + 31) / 32 * 32;
+  const int units = w.K / 16, all = (units + kBackThreads - 1) / kBackThreads, parts = all < kGridZ ? all : kGridZ;
+  const int threads = parts < kGridZ ? ((units + parts - 1) / parts + 31) / 32 * 32 : kBackThreads;
   void* args[] = {const_cast<w4a16_fp4*>(&w), &y};
-  if (parts > 65535) return cudaErrorInvalidConfiguration;
   return launch((const void*)fp4_dequant_kernel, dim3((unsigned)w.rows, (unsigned)w.experts, (unsigned)parts), threads, 0, args, pdl, s);
 }
 

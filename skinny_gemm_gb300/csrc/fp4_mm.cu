@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
       const int row = wt * kWRows + r;
       const bool mine = row < p.N;
       const float fw = p.wf && mine ? p.wf[expert * p.N + row] : 1.0f;
-      if (!mbar_wait_warp(acc_full(b), (n / NB) & 1, limit)) {
+      if (!mbar_wait_warp(acc_full(b), (n / NB) & 1, limit + (uint32_t)p.stages)) {  // (a tile of a long K: a try is longer than a stage)
         if (lane == 0) timeout();
         break;
       }

@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
         }
         __syncwarp();
       }
-      if (!mbar_wait_warp(acc_full(b), (n >> 1) & 1, limit)) {
+      if (!mbar_wait_warp(acc_full(b), (n >> 1) & 1, limit + (uint32_t)p.stages)) {
         if (lane == 0) timeout();
         break;
       }

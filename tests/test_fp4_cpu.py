@@ -63,6 +63,7 @@ def test_matrix_refusals(L):
     assert L.w4a16_fp4_dequant(ref(matrix()), None, None) == ops.ERR_NULL
     assert L.w4a16_fp4_dequant(ref(matrix()), Q + 8, None) == ops.ERR_ALIGN
     assert call(rows=0, codes=None, scales=None) == ops.OK
+    assert call(codes=Q + 128 * 512 - 16) == call(scales=Q) == call(row_scale=Q + 64) == ops.ERR_SHAPE and "overlaps" in err(L)
 
 
 def test_quant_refusals(L):
@@ -73,6 +74,8 @@ def test_quant_refusals(L):
     assert call(row_scale=None) == ops.ERR_NULL and "row_scale" in err(L)
     assert call(stride=248) == ops.ERR_SHAPE and call(stride=260) == ops.ERR_ALIGN and call(x=Q + 8) == ops.ERR_ALIGN
     assert call(rows=0, x=None) == ops.OK
+    for kw in ({"codes": Q + 2 * 127 * 256}, {"scales": Q + 512}, {"row_scale": Q - 4}, {"codes": Q - 128 * 128 + 16}):
+        assert call(**kw) == ops.ERR_SHAPE and "overlaps" in err(L)
 
 
 def test_mm_refusals(L):
@@ -90,7 +93,7 @@ def test_mm_refusals(L):
     assert call(rows=127, act=1) == ops.ERR_SHAPE and "pairs" in err(L)
     assert call(rows=0) == ops.ERR_SHAPE
     assert call(experts=2) == ops.ERR_EXPERTS and "fp4_mm_id" in err(L)
-    assert call(y=Q + 2 * 256) == call(y=Q - 2 * 3 * 128 + 2) == ops.ERR_SHAPE and "overlaps" in err(L)
+    assert call(y=Q + 2 * 256) == call(y=Q - 2 * 3 * 128 + 2) == call(codes=R) == ops.ERR_SHAPE and "overlaps" in err(L)
 
 
 def test_mm_q_refusals(L):
@@ -101,6 +104,7 @@ def test_mm_q_refusals(L):
     assert call(x=matrix(rows=5, experts=2)) == call(experts=2) == ops.ERR_EXPERTS
     assert call(y=None) == ops.ERR_NULL and call(y=R + 1) == ops.ERR_ALIGN and call(act=9) == ops.ERR_KERNEL
     assert call(x=matrix(rows=0), y=None) == ops.OK
+    assert call(x=matrix(rows=5, codes=R)) == call(x=matrix(rows=5, row_scale=R + 4)) == call(scales=R + 16) == ops.ERR_SHAPE and "overlaps" in err(L)
 
 
 def test_mm_id_refusals(L):

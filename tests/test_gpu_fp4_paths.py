@@ -353,3 +353,19 @@ def test_routed_waits_run_out(T, top, E, monkeypatch):
         ops.lib().w4a16_debug_reload_env()
     assert flags == ops.DEVICE_TIMEOUT
     assert torch.equal(ops.fp4_mm_id(x, w, ids), want) and ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_longest_row(fmt):
+    """K = 2^30.  Values that the codes hold exactly come back as they were; a product with few that are not zero is exact."""
+    K = 1 << 30
+    grid = torch.tensor([0.5, -1.5, 2, 0, -4, 1, -3, 6] * 4, dtype=torch.bfloat16, device="cuda")
+    x = grid.repeat(K // 32).view(1, K)
+    x[0, -32:] = grid.flip(0)
+    w = ops.fp4_quant(x, fmt)
+    assert torch.equal(ops.fp4_dequant(w), x)
+    x.zero_()
+    x[0, 6], x[0, K // 2 + 3], x[0, K - 3] = -3.0, 6.0, 4.0  # beside -3, 0 and 2
+    # nv takes the 4 alone in its block for 4.125: its scale is e4m3(4 / 6) = 0.6875 (of a power of two; 2/3 lies between 0.625 and
+    # that, nearer to it), its code e2m1(4 / 0.6875) = 6.  The -3 has scale 1/2 and comes back whole, and mx's scales are 1.
+    assert ops.fp4_mm(x, w).item() == -3.0 * -3 + (4.125 if fmt == "nv" else 4.0) * 2 and ops.device_status() == 0
