@@ -124,7 +124,8 @@ __device__ __forceinline__ uint2 block16(const Vec16& v, uint32_t peak, int e, u
       s = __fmul_rn(s, exp2n(e));
     }
     const float r = byte ? rcp(s) : 0.0f;
-    const float2 rr = make_float2(r, r), up = make_float2(3072.0f, 3072.0f), down = make_float2(-3072.0f, -3072.0f);
+    constexpr float kRound = 1.5f * 2048.0f;
+    const float2 rr = make_float2(r, r), up = make_float2(kRound, kRound), down = make_float2(-kRound, -kRound);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       const float2 q = add2(fma2(make_float2(y[i], y[i + 1]), rr, up), down);
