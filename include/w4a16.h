@@ -493,7 +493,7 @@ int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream);
  * m at x + m * x_stride (a multiple of 8; 16-byte aligned), y bf16 [M][w->rows] (or
  * [M][w->rows / 2] for an act), 2-byte aligned, not over x or w.  Up to 64 rows a
  * row's result is the one-row call's, bit for bit; more rows are summed in
- * another order (one piece of K instead of the splits that few rows of W take).
+ * another order, which M, W's shape and (routed) the sizes of the call decide.
  * workspace: device memory of
  * w4a16_fp4_mm_workspace_bytes(M, K, format) bytes, 256-byte aligned, no initial
  * contents needed; calls that share one must not overlap on the GPU.  M >= 0;

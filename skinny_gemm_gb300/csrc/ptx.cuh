@@ -192,6 +192,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 // Whole warps only (.aligned): arrive with release, wait with acquire.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// ... that does not wait for this thread's stores.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address of shared-memory location `addr` in the CTA of cluster rank `rank`.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
@@ -222,6 +224,12 @@ __device__ __forceinline__ bool mbar_wait_acquire_cluster(uint32_t bar, uint32_t
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+// Bytes of this CTA's shared memory to another CTA's, counted on a barrier there (cluster_map addresses; 16-byte multiples).
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "r"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
 
 // ---- shared memory and register shuffles ------------------------------------------------
 
@@ -237,6 +245,9 @@ __device__ __forceinline__ uint16_t lds16(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void sts128f(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
 __device__ __forceinline__ float4 lds128f(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
@@ -443,11 +454,11 @@ __device__ __forceinline__ void umma2_mxf4(uint32_t d_tmem, uint64_t adesc, uint
 __device__ __forceinline__ void tmem_copy_scales2(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
-// One arrival on the barrier at this offset of both CTAs.
-__device__ __forceinline__ void umma_commit2_if(uint32_t go, uint32_t bar) {
+// One arrival on the barrier at this offset of the cluster's CTAs in `mask`.
+__device__ __forceinline__ void umma_commit2_if(uint32_t go, uint32_t bar, uint16_t mask) {
   asm volatile(
-      "{ .reg .pred q; .reg .b16 m; setp.ne.b32 q, %1, 0; mov.b16 m, 3;\n"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m; }" ::"r"(bar), "r"(go)
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2; }" ::"r"(bar), "r"(go), "h"(mask)
       : "memory");
 }
 // An arrival on a barrier of another CTA of the cluster (a cluster_map address).

@@ -209,11 +209,48 @@ def test_mm_many_rows(fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("M,N,K", [(70, 64, 2048), (130, 200, 8192), (300, 1111, 2080), (129, 2570, 4128), (300, 2500, 9024), (500, 1281, 10272)])
+def test_mm_split_over_pairs(fmt, M, N, K):
+    """Few tiles and a long K: two and four pairs share a tile, whole and ragged ones."""
+    from skinny_gemm_gb300 import ops
+
+    x, w, xv, wv = product(ops, fmt, M, N, K)
+    y = ops.fp4_mm(x, w)
+    assert ops.device_status() == 0
+    want = xv @ wv.T
+    check(y, want, fc.product_bound(want, xv, wv))
+    for _ in range(5):
+        assert torch.equal(ops.fp4_mm(x, w), y)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("T,top,E,N,K", [(100, 1, 2, 300, 4096), (90, 2, 3, 514, 2336), (60, 1, 1, 1000, 8192)])
+def test_mm_id_split_over_pairs(fmt, T, top, E, N, K):
+    from skinny_gemm_gb300 import ops
+
+    g = gen(fmt, T, top, E, N, K)
+    codes, byte, factor, wv = fc.weights(g, E, N, K, fmt)
+    w = fc.matrix(ops, codes, byte, factor, E, fmt)
+    x = fc.activations(g, T, K)
+    ids = torch.randint(0, E, (T, top), generator=g, dtype=torch.int32)
+    y, z = ops.fp4_mm_id(x.cuda(), w, ids.cuda()), ops.fp4_mm_id(x.cuda(), w, ids.cuda(), act="gelu")
+    assert ops.device_status() == 0
+    xv, wv = fc.values(*fc.quant(x, fmt), fmt), wv.reshape(E, N, K)
+    for e in range(E):
+        t, j = np.nonzero(ids.numpy() == e)
+        at = torch.from_numpy(t), torch.from_numpy(j)
+        want = xv[t] @ wv[e].T
+        check(y[at], want, fc.product_bound(want, xv[t], wv[e]))
+        gate, up = want[:, 0::2], want[:, 1::2]
+        check(z[at], fc.act64(gate, "gelu") * up, fc.gated_bound(gate, up, xv[t], wv[e, 0::2], wv[e, 1::2], "gelu"))
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_gated_many_rows(fmt, act):
     from skinny_gemm_gb300 import ops
 
-    for M, F, K in ((300, 200, 288), (700, 1111, 96)):
+    for M, F, K in ((300, 200, 288), (700, 1111, 96), (150, 333, 4096), (260, 1200, 5152)):
         x, w, xv, wv = product(ops, fmt, M, 2 * F, K, act)
         y = ops.fp4_gated(x, w, act)
         assert ops.device_status() == 0

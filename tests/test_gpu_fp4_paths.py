@@ -22,8 +22,9 @@ def made(fmt, M, N, K, E=1):
     return fc.activations(g, M, K).cuda(), fc.matrix(ops, codes, byte, factor, E, fmt)
 
 
-# one of each kernel: rows quantised in the product, split over a cluster, several tiles a CTA, 64 and 128 rows, pairs
-CASES = [("nv", 1, 500, 2560), ("mx", 5, 300, 4096), ("nv", 9, 640, 2048), ("nv", 3, 50000, 256), ("mx", 60, 300, 512), ("nv", 100, 1000, 1024), ("nv", 400, 1500, 800)]
+# one of each kernel: rows quantised in the product, split over a cluster, several tiles a CTA, 64 rows, pairs, four and two pairs a tile
+CASES = [("nv", 1, 500, 2560), ("mx", 5, 300, 4096), ("nv", 9, 640, 2048), ("nv", 3, 50000, 256), ("mx", 60, 300, 512), ("nv", 100, 1000, 1024), ("nv", 400, 1500, 800),
+         ("mx", 70, 300, 4096), ("nv", 300, 2500, 9024)]
 
 
 @pytest.mark.parametrize("fmt,M,N,K", CASES)
