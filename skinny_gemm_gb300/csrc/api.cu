@@ -947,6 +947,8 @@ int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, c
   a.tiles = r.tiles;
   a.tile_count = r.count;
   a.row = r.row;
+  a.ids = ids;
+  a.early = true;
   a.max_tiles = (int)tiles;
   a.nt = r.nt;
   a.flags = flags;

@@ -71,7 +71,8 @@ struct Fp4MmArgs {
   const int32_t* tile_count;
   const int32_t* row;
   int max_tiles, nt;
-  bool early;         // the weights are complete before the kernel before this one lets it start
+  const int32_t* ids; // routed: [M], the experts of the rows
+  bool early;         // the weights (and ids) are complete before the kernel before this one lets it start
   int* flags;
   int fault_wait;     // debug (W4A16_FAULT=wait): the first CTA's first stage waits for bytes that never come
 };

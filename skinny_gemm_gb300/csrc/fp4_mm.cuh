@@ -22,12 +22,14 @@ struct Fp4MmParams {
   const Fp4Tile* tiles;  // routed, or nullptr
   const int32_t* tile_count;
   const int32_t* row;
+  const int32_t* ids;  // routed, to find the first unit's expert before the tiles are there (fp4_mm.cu), or nullptr
   int* flags;
   int N, K, M, act;
   int row_tiles, x_tiles;  // 128-row tiles of an expert's W; activation tiles (not routed)
   int atoms, stages;       // scale atoms along K; stages along K
   int vec;                 // y's rows take 8-byte stores (fp4_pair.cu: of how many bytes, 32, 16 or 0)
   int split, early;        // CTAs that share a tile's K; W may be fetched before the wait for the kernel before
+  int E, nt;               // ids: experts, rows of a tile
   int slots;               // of the ring, where the kernel quantises
   int fault_wait;
 };
@@ -55,6 +57,7 @@ inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
   p.tiles = a.tiles;
   p.tile_count = a.tile_count;
   p.row = a.row;
+  p.ids = nullptr;
   p.flags = a.flags;
   p.N = a.w.rows;
   p.K = a.w.K;
@@ -67,6 +70,8 @@ inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
   p.vec = 0;
   p.split = 1;
   p.early = 0;
+  p.E = a.w.experts;
+  p.nt = x_tile;
   p.slots = 0;
   p.fault_wait = a.fault_wait;
   return p;

@@ -123,6 +123,38 @@ def test_weights_written_just_before(fmt, M):
     assert all(torch.equal(y, yb if i % 2 else ya) for i, y in enumerate(got))
 
 
+@pytest.mark.parametrize("T,top,E", [(8, 1, 8), (30, 3, 20), (256, 4, 1024), (256, 4, 1025), (205, 5, 1024)])
+def test_routes_and_experts_written_just_before(T, top, E):
+    """Ids, activations and experts written on the same stream right before the call that reads them; rows without an expert among
+    them."""
+    g = gen(T, top, E)
+    made_ids = [torch.randint(-1, E, (T, top), generator=g, dtype=torch.int32).cuda() for _ in range(2)]
+    made_x = [fc.activations(g, T, 256).cuda() for _ in range(2)]
+    made_w = [torch.randn(E, 40, 256, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    want = []
+    for i, x, w in zip(made_ids, made_x, made_w):
+        want.append(ops.fp4_mm_id(x, ops.fp4_quant(w), i))
+        torch.cuda.synchronize()
+    each = ops.fp4_dequant(ops.fp4_quant(made_w[1]))[made_ids[1].long().clamp(min=0)].double()
+    plain = torch.einsum("tjnk,tk->tjn", each, ops.fp4_dequant(ops.fp4_quant(made_x[1])).double()) * (made_ids[1] >= 0)[..., None]
+    assert (want[1].double() - plain).norm() <= 2.0 ** -8 * plain.norm()
+    ids, x, w = torch.zeros_like(made_ids[0]), torch.zeros_like(made_x[0]), ops.FP4Matrix.empty(40, 256, E)
+    torch.cuda.synchronize()
+    for i in range(12):
+        ops.fp4_quant(made_w[i % 2], out=w)
+        x.copy_(made_x[i % 2])
+        ids.copy_(made_ids[i % 2])
+        assert torch.equal(ops.fp4_mm_id(x, w, ids), want[i % 2]), i
+    got = []
+    for i in range(12):
+        ids.copy_(made_ids[i % 2])
+        x.copy_(made_x[i % 2])
+        ops.fp4_quant(made_w[i % 2], out=w)
+        got.append(ops.fp4_mm_id(x, w, ids))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got)) and ops.device_status() == ops.DEVICE_BAD_ID
+
+
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
 def test_block_of_a_decoder_layer(fmt):
     """A gated feed-forward block, a routed one and the shared quantisation of q, k and v in a row, captured as a step is, against
