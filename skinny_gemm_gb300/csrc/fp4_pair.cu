@@ -38,26 +38,29 @@ using namespace ptx;
 
 constexpr int kXTile = 128 * 128;  // 16 KB: this CTA's 128 rows of x
 constexpr int kWTile = 128 * 128;  // its half of W's rows (up to 128)
-constexpr int kXScale = 2048, kWScale = 4096;
-constexpr int kStage = kXTile + kWTile + kXScale + kWScale;
-constexpr int S = 5;
 constexpr int kEpi = 12;  // epilogue warps, three for each 32 lanes
 constexpr int kThreads = 32 * (2 + kEpi);
 // Tensor memory's columns: two accumulators of 256, the second from kAccStep on, then the scale sets (a stage's atoms of
 // x's scales, 4 columns each, and of W's, 8).
 template <int FMT>
-struct Cols {
+struct Geo {
   static constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;  // of a stage
+  static constexpr int kXScale = kAtoms * kFp4Atom, kWScale = 2 * kXScale;
+  static constexpr int kStage = kXTile + kWTile + kXScale + kWScale;
+  static constexpr int kStages = 5;
+  static constexpr int kBars = 2 * kStages + 7;
+  static constexpr int kSmem = kStages * kStage + kEpi * 384 + kBars * 8 + 16;
   static constexpr int kSet = 12 * kAtoms;
   static constexpr int kSets = FMT == W4A16_FP4_MX ? 5 : 3;
   static constexpr int kAccStep = FMT == W4A16_FP4_MX ? 128 : 96;
   static constexpr int kSetsAt = kAccStep + 256;
   static constexpr int kShared = 8 - kAccStep / 32;  // 32s of columns that both accumulators have
   static_assert(kSetsAt + kSets * kSet <= 512 && kShared <= 6, "the SM's tensor memory");
+  // Of an SM's 256 KB the L1 gets what shared memory's 196 or 228 KB leave, and the next call's quantiser needs it (4096 x
+  // 10240 x 2560, nv: 49.7 us, with 1 KB more 51.6; mx with six stages 46.3, with five 45.1, though 8192 x 16384 x 16384 takes
+  // 583 and with six 575).
+  static_assert(kSmem + 1024 <= 196 * 1024, "a CTA's shared memory, with the system's 1 KB");
 };
-constexpr int kBars = 2 * S + 7;
-constexpr int kSmem = S * kStage + kEpi * 384 + kBars * 8 + 16 + 1024;
-static_assert(kSmem <= 227 * 1024, "a CTA's shared memory");
 
 struct Maps {
   CUtensorMap w;  // u8 [experts * N][K / 2], box 128 bytes x TN / 2 rows, 128-byte swizzle
@@ -172,11 +175,10 @@ __device__ __forceinline__ void put32(const Fp4MmParams& p, const Rows& row, con
 // the order of K.
 template <int FMT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_constant__ Maps maps, PairParams pp) {
-  using T = Cols<FMT>;
-  constexpr int kAtoms = T::kAtoms, kSets = T::kSets;
+  using T = Geo<FMT>;
+  constexpr int kAtoms = T::kAtoms, kSets = T::kSets, S = T::kStages, kStage = T::kStage;
   const Fp4MmParams& p = pp.p;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t base[];  // (the tiles' swizzle counts from multiples of 1024)
   const uint32_t sb = smem_u32(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = SPLIT ? p.split : 1;
@@ -187,14 +189,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   auto X_of = [&](int s) { return sb + (uint32_t)(s * kStage); };
   auto W_of = [&](int s) { return X_of(s) + kXTile; };
   auto SX_of = [&](int s) { return W_of(s) + kWTile; };
-  auto SW_of = [&](int s) { return SX_of(s) + kXScale; };
+  auto SW_of = [&](int s) { return SX_of(s) + T::kXScale; };
   auto full = [&](int s) { return bars + 8u * s; };         // this CTA's copies landed; leader: the other CTA's too
   auto empty = [&](int s) { return bars + 8u * (S + s); };  // the MMAs are done with it (both CTAs)
   auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };
   auto acc_free = [&](int b) { return bars + 8u * (2 * S + 2 + b); };   // leader: all of it read, by both CTAs
   auto part_free = [&](int b) { return bars + 8u * (2 * S + 4 + b); };  // leader: the shared columns read
   const uint32_t sums = bars + 8u * (2 * S + 6);  // SPLIT: the other parts' sums of this pair's columns landed
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (bars - sb) + 8 * kBars);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (bars - sb) + 8 * T::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
   const int64_t first = blockIdx.x / (2u * split), step = gridDim.x / (2u * split);
@@ -526,9 +528,9 @@ constexpr int kPairs = 76;  // of SMs
 constexpr int kMaxSplit = 4;
 // Whether the partial sums that come and go have room in the stages: at most `most` 32s of columns from each other pair come,
 // at most all but one of the smallest share go.
-bool split_fits(int split, int tn) {
+bool split_fits(int split, int tn, int stage_bytes) {
   const int chunks = tn / 32, most = (chunks + split - 1) / split;
-  return ((split - 1) * most + chunks - chunks / split) * 16384 <= S * kStage;
+  return ((split - 1) * most + chunks - chunks / split) * 16384 <= stage_bytes;
 }
 // What the exchange of a split tile's sums costs, where a stage costs tn + 64 (0.36 us at 256): 2 us.  nv, us with 1 / 2 / 4
 // pairs a tile: K = 10240, N = 2560: 130 rows 14.3 / 11.1 / 11.0, 300 rows 14.7 / 12.4 / -, 512 rows 14.9 / 12.9 / -; K = 2560,
@@ -552,7 +554,7 @@ cudaError_t launch_t(const Fp4MmArgs& a, const PairParams& p, int64_t units, int
       if (cudaError_t e = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev)) return e;
     bool& done = g_attr[dev][2 * SPLIT + (FMT == W4A16_FP4_MX)];
     if (!done) {
-      if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
+      if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<FMT>::kSmem)) return e;
       done = true;
     }
     sms = g_sms[dev];
@@ -570,7 +572,7 @@ cudaError_t launch_t(const Fp4MmArgs& a, const PairParams& p, int64_t units, int
   const int split = SPLIT ? p.p.split : 1;
   cfg.gridDim = dim3((unsigned)(2 * split * (SPLIT || units < sms / 2 ? units : sms / 2)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)kSmem;
+  cfg.dynamicSmemBytes = (size_t)Geo<FMT>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -590,11 +592,13 @@ cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   p.p = fp4_params(a, 256);
   p.tn = 256;
   const int x_tiles = a.tiles ? a.max_tiles : p.p.x_tiles;
+  const bool mx = a.w.format == W4A16_FP4_MX;
+  const int ring = mx ? Geo<W4A16_FP4_MX>::kStages * Geo<W4A16_FP4_MX>::kStage : Geo<W4A16_FP4_NV>::kStages * Geo<W4A16_FP4_NV>::kStage;
   int64_t best = INT64_MAX;
   for (int split = 1; split <= kMaxSplit; split *= 2)
     for (int tn = 256; tn >= 128; tn -= 64) {
       const int64_t tiles = (int64_t)((a.w.rows + tn - 1) / tn) * x_tiles;
-      if (split > 1 && (tiles * split > kPairs || p.p.stages < 2 * split || !split_fits(split, tn))) continue;
+      if (split > 1 && (tiles * split > kPairs || p.p.stages < 2 * split || !split_fits(split, tn, ring))) continue;
       const int64_t rounds = (tiles + kPairs - 1) / kPairs;
       const int64_t cost = rounds * ((p.p.stages + split - 1) / split) * (tn + 64) + (split > 1 ? kExchange : 0);
       if (cost < best) best = cost, p.tn = tn, p.p.split = split;
@@ -604,7 +608,6 @@ cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.y);
   p.p.vec = cols % 16 == 0 && at % 32 == 0 ? 32 : cols % 8 == 0 && at % 16 == 0 ? 16 : 0;
   const int64_t units = (int64_t)p.n_tiles * x_tiles;
-  const bool mx = a.w.format == W4A16_FP4_MX;
   if (p.p.split > 1) return mx ? launch_t<W4A16_FP4_MX, true>(a, p, units, pdl, s) : launch_t<W4A16_FP4_NV, true>(a, p, units, pdl, s);
   return mx ? launch_t<W4A16_FP4_MX, false>(a, p, units, pdl, s) : launch_t<W4A16_FP4_NV, false>(a, p, units, pdl, s);
 }
