@@ -291,12 +291,14 @@ template <int FMT>
 cudaError_t quant_f(const Fp4QuantArgs& a, int pdl, cudaStream_t s) {
   Fp4RouteArgs none = {};
   void* args[] = {const_cast<Fp4QuantArgs*>(&a), &none};
-  // Few rows: a thread a unit, for the latency (1 x 2560 1.4 us; 333 x 2304 1.6 us so and with four units a thread).
-  // Many: four or five, whose loads are in flight together, whichever leaves fewer threads without; us with one / two /
+  // Up to some 1600 units an SM: a thread a unit, for the latency.  A product's call in us so / with four or five units a
+  // thread: 256 rows x 2560 9.7 / 10.2, 512 x 2560 14.4 / 16.4, 800 x 2304 15.3 / 16.9, 1500 x 2560 (gated, mx) 35.4 / 37.0,
+  // 300 x 10240 16.4 / 17.0; but 512 x 10240 19.8 / 17.6, 777 x 10240 26.7 / 22.1.
+  // More: four or five, whose loads are in flight together, whichever leaves fewer threads without; us with one / two /
   // four / five, nv: 4096 x 2560 6.9 / 6.2 / 6.4 / 5.5, 4001 x 10240 47 / 22.5 / 21.0 / 19.0 (HBM's 15.6), 8192 x 16384
   // 119 / 71 / 56.3 / 59.3 (HBM's 51).
   const int all = fp4_atoms(a.K, FMT) * 4 * fp4_block(FMT) / 16;
-  const bool one = a.rows <= 152 && all <= kQuantMost;
+  const bool one = (int64_t)a.rows * all <= 152 * 1600 && all <= kQuantMost;
   auto threads_of = [&](int units) { return ((all + units - 1) / units + 31) / 32 * 32; };
   const int each = one ? 1 : 5 * threads_of(5) <= 4 * threads_of(4) ? 5 : 4;
   const int threads = threads_of(each) > kQuantMost ? kQuantMost : threads_of(each);
