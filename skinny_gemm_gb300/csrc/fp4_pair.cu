@@ -14,7 +14,7 @@
 //              and commits; the other CTA: passes "stage landed" on
 //   warps 2-13 epilogue: 32 lanes x a third of the columns each
 // Few tiles and a long K: clusters of two or four pairs share a tile (SPLIT).
-// Tensor memory: two accumulators, which at 256 columns share 160 (mx: 128), beside
+// Tensor memory: two accumulators of 256 columns that share 160 (mx: 128), beside
 // three sets of scales of 48 columns (mx: five of 24).  A set is written again
 // when the MMAs that read it are done; with two sets the MMAs waited for the
 // copies.  The epilogue takes the shared columns into registers first, and lets
@@ -40,8 +40,8 @@ constexpr int kXTile = 128 * 128;  // 16 KB: this CTA's 128 rows of x
 constexpr int kWTile = 128 * 128;  // its half of W's rows (up to 128)
 constexpr int kEpi = 12;  // epilogue warps, three for each 32 lanes
 constexpr int kThreads = 32 * (2 + kEpi);
-// Tensor memory's columns: two accumulators of tn, the second from acc_step(tn) on, and at the end the scale sets (a
-// stage's atoms of x's scales, 4 columns each, and of W's, 8).
+// Tensor memory's columns: two accumulators of 256, the second from kAccStep on, then the scale sets (a stage's atoms of
+// x's scales, 4 columns each, and of W's, 8).
 template <int FMT>
 struct Geo {
   static constexpr int kAtoms = FMT == W4A16_FP4_MX ? 2 : 4;  // of a stage
@@ -52,9 +52,10 @@ struct Geo {
   static constexpr int kSmem = kStages * kStage + kEpi * 384 + kBars * 8 + 16;
   static constexpr int kSet = 12 * kAtoms;
   static constexpr int kSets = FMT == W4A16_FP4_MX ? 5 : 3;
-  static constexpr int kSetsAt = 512 - kSets * kSet;
-  static __host__ __device__ constexpr int acc_step(int tn) { return 2 * tn <= kSetsAt ? tn : (kSetsAt - tn) / 32 * 32; }
-  static_assert(acc_step(256) >= 64, "at most six 32s of columns that both accumulators have");
+  static constexpr int kAccStep = FMT == W4A16_FP4_MX ? 128 : 96;
+  static constexpr int kSetsAt = kAccStep + 256;
+  static constexpr int kShared = 8 - kAccStep / 32;  // 32s of columns that both accumulators have
+  static_assert(kSetsAt + kSets * kSet <= 512 && kShared <= 6, "the SM's tensor memory");
   // Of an SM's 256 KB the L1 gets what shared memory's 196 or 228 KB leave, and the next call's quantiser needs it (4096 x
   // 10240 x 2560, nv: 49.7 us, with 1 KB more 51.6; mx with six stages 46.3, with five 45.1, though 8192 x 16384 x 16384 takes
   // 583 and with six 575).
@@ -90,11 +91,12 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
 
 // Which tile a pair's unit is: sixteen activation tiles by all of W's, then the next sixteen, so that the pairs at work at
 // a time share what they read (8192 x 16384 x 16384 with 4 / 8 / 16: 641 / 596 / 586 us).
-__device__ __forceinline__ void unit_tile(uint32_t u, int x_tiles, int n_tiles, int& xt, int& nt) {
-  const uint32_t per = 16u * n_tiles, g = u / per, r = u - g * per;
-  const uint32_t wide = min(16, x_tiles - 16 * (int)g);
-  nt = (int)(wide == 16 ? r >> 4 : r / wide);
-  xt = (int)(16 * g + (r - nt * wide));
+__device__ __forceinline__ void unit_tile(int64_t u, int x_tiles, int n_tiles, int& xt, int& nt) {
+  const int64_t per = 16LL * n_tiles;
+  const int g = (int)(u / per), r = (int)(u % per);
+  const int wide = min(16, x_tiles - 16 * g);
+  xt = 16 * g + r % wide;
+  nt = r / wide;
 }
 
 // A thread's row of a tile.
@@ -104,7 +106,7 @@ struct Rows {
   int n0;  // the tile's first row of W
   bool mine, factors;
   Rows() = default;
-  __device__ __forceinline__ Rows(const Fp4MmParams& p, const PairParams& pp, uint32_t u, int x_tiles, int r) {
+  __device__ __forceinline__ Rows(const Fp4MmParams& p, const PairParams& pp, int64_t u, int x_tiles, int r) {
     int xt, nt;
     unit_tile(u, x_tiles, pp.n_tiles, xt, nt);
     n0 = nt * pp.tn;
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (bars - sb) + 8 * T::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
-  const uint32_t first = blockIdx.x / (2u * split), step = gridDim.x / (2u * split);
+  const int64_t first = blockIdx.x / (2u * split), step = gridDim.x / (2u * split);
   const int k0 = SPLIT ? p.stages * part / split : 0, k1 = SPLIT ? p.stages * (part + 1) / split : p.stages, tn = pp.tn;
   const uint32_t limit = p.fault_wait ? 4096u : 1u << 18;  // tries of a wait: about a second
   auto timeout = [&]() {
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   };
   // what a unit's stages are loaded from
   int x_row = 0, xs_tile = 0, w_row = 0, ws_tile = 0;
-  auto locate = [&](uint32_t u, int x_tiles) {
+  auto locate = [&](int64_t u, int x_tiles) {
     int xt, nt;
     unit_tile(u, x_tiles, pp.n_tiles, xt, nt);
     int64_t expert = 0;
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     // 7.5 us, else 8.0; between this thread's barriers and the others' start, 8.7.)
     pdl_wait();
     const int x_tiles = p.tiles ? *p.tile_count : p.x_tiles;
-    if (first < (uint32_t)x_tiles * pp.n_tiles) {
+    if (first < (int64_t)x_tiles * pp.n_tiles) {
       locate(first, x_tiles);
       for (; it < S && k0 + (int)it < k1; ++it) load((int)it, k0 + (int)it);
     }
@@ -270,16 +272,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   pdl_launch_dependents();
   pdl_wait();
   const int x_tiles = p.tiles ? *p.tile_count : p.x_tiles;
-  const uint32_t units = (uint32_t)x_tiles * pp.n_tiles;  // (fewer than 2^31, checked by the host)
+  const int64_t units = (int64_t)x_tiles * pp.n_tiles;
 
-  const int acc_step = T::acc_step(tn);
   Rows split_row{};
 
   if (warp == 0) {
     // ---- TMA producer ----
     if (lane == 0) {
       int k = k0 + (int)it;  // (those of the first unit that are on their way)
-      for (uint32_t u = first; u < units && !*s_abort; u += step, k = k0) {
+      for (int64_t u = first; u < units && !*s_abort; u += step, k = k0) {
         locate(u, x_tiles);
         for (; k < k1; ++k, ++it) {
           const int s = (int)(it % S);
@@ -304,22 +305,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     uint32_t n = 0;                     // tiles
     int s = 0, set = 0, old = S - kSets;  // slot, scale set, and the slot of kSets stages before
     uint32_t parity = 0, old_parity = 1;
-    for (uint32_t u = first; u < units && !*s_abort; u += step, ++n) {
+    for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
+      int xt, nt;
+      unit_tile(u, x_tiles, pp.n_tiles, xt, nt);
       const int b = (int)(n & 1);
       // this accumulator's last tile is read, and the columns it shares with the other's
       if ((n >= 2 && !mbar_wait_warp(acc_free(b), ((n >> 1) - 1) & 1, limit)) ||
-          (n >= 1 && acc_step < tn && !mbar_wait_warp(part_free(b ^ 1), ((n - 1) >> 1) & 1, limit))) {
+          (n >= 1 && !mbar_wait_warp(part_free(b ^ 1), ((n - 1) >> 1) & 1, limit))) {
         if (lane == 0) timeout();
         break;
       }
       tc_fence_after_sync();
-      const uint32_t acc = (uint32_t)(b * acc_step);
-      uint32_t w_col = 0;  // the tile's first row of W within its tile of scales, in columns
-      if (tn == 192) {
-        int xt, nt;
-        unit_tile(u, x_tiles, pp.n_tiles, xt, nt);
-        w_col = 2 * (nt & 1);
-      }
+      const uint32_t acc = (uint32_t)(b * T::kAccStep);
+      const uint32_t w_col = (uint32_t)(nt * tn % 128 / 32);
       bool ok = true;
       for (int k = k0; k < k1; ++k, ++it) {
         ok = mbar_wait_warp(full(s), parity, limit) &&
@@ -371,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   } else if (warp == 1) {
     // ---- the other CTA: its stages landed ----
     const uint32_t to = cluster_map(bars, lead) - bars;
-    for (uint32_t u = first; u < units && !*s_abort; u += step) {
+    for (int64_t u = first; u < units && !*s_abort; u += step) {
       bool ok = true;
       for (int k = k0; k < k1; ++k, ++it) {
         const int s = (int)(it % S);
@@ -387,10 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     // ---- epilogue ----
     const int q = warp & 3, third = (warp - 2) >> 2;
     const uint32_t to = cluster_map(bars, lead) - bars;
-    const int chunks = tn / 32, own = acc_step / 32;  // 32s of columns; of them not shared by the accumulators
     uint32_t n = 0;
     if (SPLIT && first < units) split_row = Rows(p, pp, first, x_tiles, 128 * (int)rank + 32 * q + lane);
-    for (uint32_t u = first; u < units && !*s_abort; u += step, ++n) {
+    for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
       const int b = (int)(n & 1);
       if (SPLIT) {  // (the rest below)
         for (int c = part + split * third, i = 0; c < tn / 32; c += 3 * split, ++i)
@@ -402,10 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       float* wf = s_wf + 96 * (warp - 2);
       // The i-th 32 columns to be read, those that both accumulators have first: the second's first and the first's last
       // ones.  Each of the three warps of 32 lanes takes every third.
-      auto column = [&](int i) {
-        const int c = i + (b ? 0 : own);
-        return 32 * (c < chunks ? c : c - chunks);
-      };
+      auto column = [&](int i) { return 32 * (b ? i : (i + T::kAccStep / 32) % 8); };
       if (o.factors) {
         __syncwarp();
 #pragma unroll
@@ -417,25 +411,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
         break;
       }
       tc_fence_after_sync();
-      const uint32_t acc = (uint32_t)(b * acc_step) + ((uint32_t)(32 * q) << 16);
-      auto exists = [&](int i) { return i < chunks && o.n0 + column(i) < p.N; };
+      const uint32_t acc = (uint32_t)(b * T::kAccStep) + ((uint32_t)(32 * q) << 16);
+      auto exists = [&](int i) { return i < 8 && column(i) < tn && o.n0 + column(i) < p.N; };
       auto put = [&](int i, float (&v)[32]) {
         if (exists(i)) put32(p, o, wf + 32 * (i / 3), o.n0 + column(i), v);
       };
       // (only where a tile comes that waits for it: no arrival is on its way to a CTA that may be gone)
-      auto arrive = [&](uint32_t bar, uint32_t next) {
+      auto arrive = [&](uint32_t bar, int64_t next) {
         tc_fence_before_sync();
         __syncwarp();
         if (next < units && lane == 0) mbar_arrive_cluster(bar + to);
       };
-      // this warp's 32s: third, third + 3, third + 6; the first two may be shared
+      // this warp's 32s: third, third + 3, third + 6; the first is always shared, the second may be
       float v[32], w[32];
-      const bool two = third + 3 < chunks - own;
-      if (own < chunks && third >= chunks - own) arrive(part_free(b), u + step);
+      const bool two = third + 3 < T::kShared;
       if (exists(third)) tmem_ld32(acc + column(third), v);
       if (two && exists(third + 3)) tmem_ld32(acc + column(third + 3), w);
       tmem_wait_ld();
-      if (third < chunks - own) arrive(part_free(b), u + step);
+      arrive(part_free(b), u + step);
       put(third, v);
       if (!two && exists(third + 3)) tmem_ld32(acc + column(third + 3), w);
       if (exists(third + 6)) tmem_ld32(acc + column(third + 6), v);
@@ -615,7 +608,6 @@ cudaError_t launch_fp4_pair(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.y);
   p.p.vec = cols % 16 == 0 && at % 32 == 0 ? 32 : cols % 8 == 0 && at % 16 == 0 ? 16 : 0;
   const int64_t units = (int64_t)p.n_tiles * x_tiles;
-  if (units > INT32_MAX - 1024) return cudaErrorInvalidConfiguration;  // (a y of more than 2^46 bytes)
   if (p.p.split > 1) return mx ? launch_t<W4A16_FP4_MX, true>(a, p, units, pdl, s) : launch_t<W4A16_FP4_NV, true>(a, p, units, pdl, s);
   return mx ? launch_t<W4A16_FP4_MX, false>(a, p, units, pdl, s) : launch_t<W4A16_FP4_NV, false>(a, p, units, pdl, s);
 }
