@@ -402,3 +402,23 @@ def test_longest_row(fmt):
     # nv takes the 4 alone in its block for 4.125: its scale is e4m3(4 / 6) = 0.6875 (of a power of two; 2/3 lies between 0.625 and
     # that, nearer to it), its code e2m1(4 / 0.6875) = 6.  The -3 has scale 1/2 and comes back whole, and mx's scales are 1.
     assert ops.fp4_mm(x, w).item() == -3.0 * -3 + (4.125 if fmt == "nv" else 4.0) * 2 and ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_rows_and_values_at_any_sixteen_bytes(fmt):
+    """Rows to quantise, and values that come back, at addresses and strides of 16 bytes."""
+    x = torch.randn(70, 96, generator=gen(fmt)).to(torch.bfloat16).cuda()
+    want = ops.fp4_quant(x, fmt)
+    back = ops.fp4_dequant(want)
+    for shift in (0, 8, 16, 24):
+        wide = torch.full((70 * 104 + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        rows = wide[shift:shift + 70 * 104].view(70, 104)[:, :96]
+        rows.copy_(x)
+        w = ops.fp4_quant(rows, fmt)
+        assert torch.equal(w.codes, want.codes) and torch.equal(ops.fp4_dequant(w), back), shift
+        for M in (3, 70):
+            assert torch.equal(ops.fp4_mm(rows[:M], want), ops.fp4_mm(x[:M], want)), (shift, M)
+        buf = torch.full((70 * 96 + 64,), 5.0, dtype=torch.bfloat16, device="cuda")
+        ops.fp4_dequant(want, out=buf[shift:shift + 70 * 96].view(70, 96))
+        assert torch.equal(buf[shift:shift + 70 * 96].view(70, 96), back) and (buf[:shift] == 5).all() and (buf[shift + 70 * 96:] == 5).all()
+    assert ops.device_status() == 0
