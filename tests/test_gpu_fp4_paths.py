@@ -422,3 +422,47 @@ def test_rows_and_values_at_any_sixteen_bytes(fmt):
         ops.fp4_dequant(want, out=buf[shift:shift + 70 * 96].view(70, 96))
         assert torch.equal(buf[shift:shift + 70 * 96].view(70, 96), back) and (buf[:shift] == 5).all() and (buf[shift + 70 * 96:] == 5).all()
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("T,top,E,N,K", [(5, 2, 6, 130, 320), (100, 1, 3, 300, 4096), (300, 2, 3, 500, 320), (1500, 1, 20, 130, 96)])
+def test_one_expert_or_none(fmt, T, top, E, N, K):
+    """All rows of one expert, so that tiles which there might be are not there; and no row with an expert at all."""
+    x, w = made(fmt, T, N, K, E=E)
+    xv, wv = ops.fp4_dequant(ops.fp4_quant(x, fmt)).double(), ops.fp4_dequant(w).double()
+    for e in (0, E - 1):
+        y = ops.fp4_mm_id(x, w, torch.full((T, top), e, dtype=torch.int32, device="cuda"))
+        want = xv @ wv[e].T
+        assert ((y.double() - want[:, None]).norm() <= 2.0 ** -8 * want.norm() * top ** 0.5) and ops.device_status() == 0
+        assert all(torch.equal(y[:, 0], y[:, j]) for j in range(top))
+    out = torch.full((T, top, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    for e in (-1, E, 2 ** 31 - 1, -2 ** 31):
+        out.fill_(3.0)
+        ops.fp4_mm_id(x, w, torch.full((T, top), e, dtype=torch.int32, device="cuda"), out=out)
+        assert ops.device_status() == ops.DEVICE_BAD_ID and not out.any()
+    one = torch.full((T, top), -1, dtype=torch.int32, device="cuda")
+    one[T // 2, 0] = 1
+    y = ops.fp4_mm_id(x, w, one)
+    assert ops.device_status() == ops.DEVICE_BAD_ID and y[T // 2, 0].any() and not y[:T // 2].any() and not y[T // 2 + 1:].any() and not y[:, 1:].any()
+
+
+@pytest.mark.parametrize("fmt,M,N,K", [("nv", 300, 2500, 9024), ("mx", 130, 640, 4096), ("nv", 2000, 2600, 512)])
+def test_many_rows_on_two_streams_at_once(fmt, M, N, K):
+    """Calls that fill the GPU, some as clusters of four pairs, at once on several streams and in replayed graphs."""
+    x, w = made(fmt, M, N, K)
+    want = ops.fp4_mm(x, w)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graphs, outs = [], [torch.empty_like(want) for _ in range(6)]
+    torch.cuda.synchronize()
+    for o in outs[3:]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ops.fp4_mm(x, w, out=o)
+        graphs.append(g)
+    for _ in range(8):
+        for s, o, g in zip(streams, outs, graphs):
+            ops.fp4_mm(x, w, out=o, stream=s)
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and ops.device_status() == 0
