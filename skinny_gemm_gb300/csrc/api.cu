@@ -933,9 +933,23 @@ int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, c
   Fp4RouteArgs r{ids, (int)rows, top, w->experts, fp4_id_tile(rows, w->experts), fp4_id_span(rows, w->experts), place, reinterpret_cast<int32_t*>(ws + sp.row),
                  reinterpret_cast<Fp4Tile*>(ws + sp.tiles), reinterpret_cast<int32_t*>(ws + sp.count), y,
                  act == W4A16_FP4_LINEAR ? w->rows : w->rows / 2, flags};
+  Fp4MmArgs a = {};
+  if (fp4_mm_id_fuses(*w, T, top)) {
+    a.x = x;
+    a.x_stride = x_stride;
+    a.w = *w;
+    a.y = y;
+    a.M = T;
+    a.act = act;
+    a.ids = ids;
+    a.top = top;
+    a.flags = flags;
+    a.fault_wait = env().fault == kFaultWait;
+    cudaError_t e = launch_fp4_mm(a, env().pdl, s);
+    return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_mm_id launch");
+  }
   Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, T, w->K, T, w->format};
   if (cudaError_t e = launch_fp4_route_quant(r, q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm_id launch");
-  Fp4MmArgs a = {};
   a.xc = ws;
   a.xs = ws + sp.scales;
   a.xf = factor;

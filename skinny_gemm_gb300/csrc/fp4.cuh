@@ -71,13 +71,15 @@ struct Fp4MmArgs {
   const int32_t* tile_count;
   const int32_t* row;
   int max_tiles, nt;
-  const int32_t* ids; // routed: [M], the experts of the rows
+  const int32_t* ids; // routed: the experts of the rows; with x (fp4_mm_id_fuses), [M][top]
+  int top;
   bool early;         // the weights (and ids) are complete before the kernel before this one lets it start
   int* flags;
   int fault_wait;     // debug (W4A16_FAULT=wait): the first CTA's first stage waits for bytes that never come
 };
 cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s);
 bool fp4_mm_fuses(const w4a16_fp4& w, int M);  // whether a product of M rows quantises them itself
+bool fp4_mm_id_fuses(const w4a16_fp4& w, int T, int top);  // ... a routed one its tokens
 int fp4_mm_tile(int M);  // rows of the activation tile that a call of M rows takes
 
 }  // namespace w4a16

@@ -26,7 +26,9 @@
 // A few activation rows (decode, verify) are quantised in the kernel, by the
 // epilogue's warps while W's first stages come: each CTA takes its own part of K
 // (and every row's peak, for nv's factor), as fp4.cu would have it, bit for bit.
-// That saves the quantiser's launch.
+// That saves the quantiser's launch.  A routed call of a few tokens (IDS) takes them
+// all as the activation tile of each expert that was chosen, and stores of its
+// columns those that chose it: no places, no launch before.
 //
 // Scales in tensor memory have a set for each slot of the ring: a stage that
 // landed in a slot says that the MMAs which read the slot before are done.
@@ -87,6 +89,7 @@ struct Maps {
 // Activation rows that a CTA quantises: codes of its stages as the tiles that TMA would have brought, and their scales.
 constexpr int kOwnRows = 16, kOwnStage = kOwnRows * 128, kOwnThreads = 128;
 constexpr int kOwnUnits = 512;  // of sixteen values: most of a CTA
+constexpr int kOwnIds = 32;     // most choices of a routed call that quantises its tokens: a lane each
 // Room of its own for a split tile's partial sums from the other CTAs (16 columns in 2, 4 or 8 parts, all but one): a CTA
 // need not wait for the others' MMAs before it sends its own (5 x 2560 x 10240: 5.9 us, else 6.2).
 constexpr int kOwnParts = kOwnRows * kWRows * 4 / kMaxSplit * (kMaxSplit - 1);
@@ -96,6 +99,36 @@ struct OwnRows {
   uint32_t whole[kOwnRows];                   // ... of the row: the largest of the cluster's parts
   float factor[kOwnRows];
 };
+
+// A routed call of a few tokens: all of them are the activation tile of every expert that one of them chose, and a choice's
+// row is stored from its expert's tile alone.
+struct OwnIds {
+  int expert[kOwnIds];  // the experts, `count` of them
+  int id[kOwnIds];      // of the choices (-1: no expert)
+  int count;
+};
+
+// All threads; what was chosen, and zeros for the rows of choices that are no expert.
+__device__ __forceinline__ void own_ids(const Fp4MmParams& p, OwnIds* s) {
+  const int n = p.M * p.top, cols = p.act == W4A16_FP4_LINEAR ? p.N : p.N / 2;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int id = lane < n ? p.ids[lane] : -1;
+    const bool bad = id < 0 || id >= p.E;
+    if (bad && lane < n && blockIdx.x == 0) atomicOr(p.flags, W4A16_DEVICE_BAD_ID);
+    if (bad) id = -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    const bool first = !bad && __ffs(same) - 1 == lane;
+    const uint32_t all = __ballot_sync(0xffffffffu, first);
+    s->id[lane] = id;
+    if (first) s->expert[__popc(all & ((1u << lane) - 1))] = id;
+    if (lane == 0) s->count = __popc(all);
+  }
+  __syncthreads();
+  for (int r = blockIdx.x; r < n; r += gridDim.x)
+    if (s->id[r] < 0)
+      for (int i = threadIdx.x; i < cols; i += kThreads) p.y[(int64_t)r * cols + i] = 0;
+}
 
 // nv needs a row's peak before its first code.  Each CTA finds its part's, and sends it to all of the cluster
 // (`told`: a barrier of M * split arrivals); a row or so (two units a thread) is read whole instead.  Us so / by the other
@@ -196,9 +229,8 @@ __device__ __forceinline__ bool quantise_own(const Fp4MmParams& p, OwnRows* own,
   return ok;
 }
 
-// One sum of row `row` of W and place `at` of x, whole warps (gate and up rows are neighbours).
-__device__ __forceinline__ void store(const Fp4MmParams& p, float v, float fw, const float* xf, int at, int row, bool mine) {
-  const int64_t m = p.row ? p.row[at] : at;
+// One sum of row `row` of W and place `at` of x, row m of y, whole warps (gate and up rows are neighbours).
+__device__ __forceinline__ void store(const Fp4MmParams& p, float v, float fw, const float* xf, int at, int64_t m, int row, bool mine) {
   float t = v * fw;
   if (xf) t *= xf[at];
   if (p.act == W4A16_FP4_LINEAR) {
@@ -262,7 +294,7 @@ __device__ __forceinline__ int expert_of(const Fp4MmParams& p, int tile, int* co
   return __reduce_max_sync(0xffffffffu, found);
 }
 
-template <int NT, int FMT, bool OWN>
+template <int NT, int FMT, bool OWN, bool IDS>
 __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_constant__ Maps maps, Fp4MmParams p) {
   using G = Geo<NT>;
   constexpr int NB = G::kAcc;
@@ -292,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(base + (told + 8 - sb));
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   OwnRows* own = reinterpret_cast<OwnRows*>(s_tmem + 2);
+  OwnIds* ids = reinterpret_cast<OwnIds*>(own + 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -324,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
   int early_expert = 0;
   if (!OWN && p.ids) early_expert = expert_of(p, (int)(first / p.row_tiles), reinterpret_cast<int*>(base));
   if (!(p.early && warp == 0)) pdl_wait();
-  auto units_now = [&]() { return (int64_t)(p.tiles ? *p.tile_count : p.x_tiles) * p.row_tiles; };
+  if (IDS) own_ids(p, ids);
+  auto units_now = [&]() { return (int64_t)(IDS ? ids->count : p.tiles ? *p.tile_count : p.x_tiles) * p.row_tiles; };
   int64_t units = p.early && warp == 0 && p.tiles ? 0 : units_now();  // (the early producer: when it has waited)
   auto timeout = [&]() {
     atomicOr(p.flags, W4A16_DEVICE_TIMEOUT);
@@ -357,7 +391,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
         const int xt = (int)(u / p.row_tiles), wt = (int)(u % p.row_tiles);
         int64_t expert = 0;
         int place = xt * NT;
-        if (p.tiles) {
+        if (IDS) {
+          expert = ids->expert[xt];
+        } else if (p.tiles) {
           expert = p.tiles[xt].expert;
           place = p.tiles[xt].place;
         }
@@ -454,7 +490,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
       const int xt = (int)(u / p.row_tiles), wt = (int)(u % p.row_tiles);
       int64_t expert = 0;
       int place = xt * NT, count = min(NT, p.M - place);
-      if (p.tiles) {
+      if (IDS) {
+        expert = ids->expert[xt];
+        place = 0;
+        count = p.M;
+      } else if (p.tiles) {
         expert = p.tiles[xt].expert;
         place = p.tiles[xt].place;
         count = p.tiles[xt].count;
@@ -479,7 +519,12 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
         for (int i = 0; i < 16; ++i) {
           if (c + i >= count) break;
           const int at = place + c + i;
-          store(p, v[i], fw, xf, at, row, mine);
+          if (IDS) {
+            for (int m = at * p.top; m < (at + 1) * p.top; ++m)
+              if (ids->id[m] == expert) store(p, v[i], fw, xf, at, m, row, mine);
+          } else {
+            store(p, v[i], fw, xf, at, p.row ? p.row[at] : at, row, mine);
+          }
         }
       }
       tc_fence_before_sync();
@@ -568,26 +613,26 @@ int split_of(int row_tiles, int stages) {
 }
 
 // Where the kernel quantises: shared memory of a ring of `slots` beside a CTA's `stages` of x, and how many slots fit.
-constexpr int own_smem(int slots, int stages) {
-  return slots * (kWTile + kScaleTile) + stages * (kOwnStage + 4 * kOwnAtom) + kOwnAtom + kOwnParts + (2 * slots + 6) * 8 + 8 + (int)sizeof(OwnRows);
+constexpr int own_smem(int slots, int stages, bool ids) {
+  return slots * (kWTile + kScaleTile) + stages * (kOwnStage + 4 * kOwnAtom) + kOwnAtom + kOwnParts + (2 * slots + 6) * 8 + 8 + (int)sizeof(OwnRows) + (ids ? (int)sizeof(OwnIds) : 0);
 }
-int own_slots(int stages) {
+int own_slots(int stages, bool ids) {
   int slots = 5;
-  while (slots > 0 && own_smem(slots, stages) > kCtaSmem) --slots;
+  while (slots > 0 && own_smem(slots, stages, ids) > kCtaSmem) --slots;
   return slots;
 }
 
 struct Device {
   int sms = 0;
-  bool attr[8] = {};
+  bool attr[10] = {};
 };
 Device g_dev[64];
 
-template <int NT, int FMT, bool OWN = false>
+template <int NT, int FMT, bool OWN = false, bool IDS = false>
 cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStream_t s) {
   using G = Geo<NT>;
-  auto* fn = fp4_mm_kernel<NT, FMT, OWN>;
-  constexpr int kIndex = (OWN ? 3 : NT == 16 ? 0 : NT == 32 ? 1 : 2) * 2 + (FMT == W4A16_FP4_MX);
+  auto* fn = fp4_mm_kernel<NT, FMT, OWN, IDS>;
+  constexpr int kIndex = (IDS ? 4 : OWN ? 3 : NT == 16 ? 0 : NT == 32 ? 1 : 2) * 2 + (FMT == W4A16_FP4_MX);
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -618,7 +663,7 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.split > 1 ? units * p.split : units < 2 * sms ? units : 2 * sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)(OWN ? own_smem(p.slots, (p.stages + p.split - 1) / p.split) : G::kSmem);
+  cfg.dynamicSmemBytes = (size_t)(OWN ? own_smem(p.slots, (p.stages + p.split - 1) / p.split, IDS) : G::kSmem);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
@@ -645,7 +690,15 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
 bool fp4_mm_fuses(const w4a16_fp4& w, int M) {
   const int stages = (w.K + kFp4StageK - 1) / kFp4StageK, split = split_of((int)fp4_row_tiles(w.rows), stages);
   const int part = (stages + split - 1) / split;
-  return M <= kOwnRows && M * 16 * part <= kOwnUnits && own_slots(part) >= 3;
+  return M <= kOwnRows && M * 16 * part <= kOwnUnits && own_slots(part, false) >= 3;
+}
+
+// The same for routed calls; us so / with the quantiser's launch, K = 2048: 1 token x 4 of 64 experts, N = 1536
+// 5.7 / 8.9, 4 x 8 10.6 / 11.9, 1 x 2 of 8 (K = 4096, N = 14336) 13.3 / 15.7, 8 x 2 of 16 (K = 1024, N = 2048) 7.5 / 7.3; with
+// twice the units 8 x 1 of 8 (N = 6144) 11.2 / 9.5.  A call from the host takes 12 to 13 / 18.
+bool fp4_mm_id_fuses(const w4a16_fp4& w, int T, int top) {
+  const int64_t stages = (w.K + kFp4StageK - 1) / kFp4StageK;
+  return T <= kOwnRows && (int64_t)T * top <= kOwnIds && T * 16 * stages <= kOwnUnits && own_slots((int)stages, true) >= 3;
 }
 
 // The smallest tile that takes all rows, and from 65 rows on the pair kernel's.  Us with a tile of 64 or 128 here / there:
@@ -663,8 +716,15 @@ cudaError_t launch_fp4_mm(const Fp4MmArgs& a, int pdl, cudaStream_t s) {
   if (!a.tiles) p.split = split_of(p.row_tiles, p.stages);
   const bool mx = a.w.format == W4A16_FP4_MX;
   if (a.x) {
-    p.slots = own_slots((p.stages + p.split - 1) / p.split);
     p.early = 0;
+    if (a.ids) {
+      p.ids = a.ids;
+      p.split = 1;
+      p.x_tiles = (int64_t)a.M * a.top < a.w.experts ? a.M * a.top : a.w.experts;  // most
+      p.slots = own_slots(p.stages, true);
+      return mx ? launch_t<16, W4A16_FP4_MX, true, true>(a, p, pdl, s) : launch_t<16, W4A16_FP4_NV, true, true>(a, p, pdl, s);
+    }
+    p.slots = own_slots((p.stages + p.split - 1) / p.split, false);
     return mx ? launch_t<16, W4A16_FP4_MX, true>(a, p, pdl, s) : launch_t<16, W4A16_FP4_NV, true>(a, p, pdl, s);
   }
   switch (nt) {

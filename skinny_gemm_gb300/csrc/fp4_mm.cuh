@@ -30,6 +30,7 @@ struct Fp4MmParams {
   int vec;                 // y's rows take 8-byte stores (fp4_pair.cu: of how many bytes, 32, 16 or 0)
   int split, early;        // CTAs that share a tile's K; W may be fetched before the wait for the kernel before
   int E, nt;               // ids: experts, rows of a tile
+  int top;                 // choices of a token, where the kernel quantises these
   int slots;               // of the ring, where the kernel quantises
   int fault_wait;
 };
@@ -72,6 +73,7 @@ inline Fp4MmParams fp4_params(const Fp4MmArgs& a, int x_tile) {
   p.early = 0;
   p.E = a.w.experts;
   p.nt = x_tile;
+  p.top = a.top;
   p.slots = 0;
   p.fault_wait = a.fault_wait;
   return p;

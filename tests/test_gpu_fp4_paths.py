@@ -466,3 +466,50 @@ def test_many_rows_on_two_streams_at_once(fmt, M, N, K):
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs) and ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("top,E,N,K,act", [(2, 9, 130, 2048, None), (4, 64, 96, 1024, "silu"), (8, 20, 200, 320, None), (1, 3, 514, 4096, "gelu"), (3, 5, 40, 96, None)])
+def test_routed_rows_do_not_depend_on_the_batch(fmt, top, E, N, K, act):
+    """A few tokens (quantised in the product), more, and tokens 80 bytes further apart: the rows of the one call of them all."""
+    x, w = made(fmt, 40, N, K, E=E)
+    g = gen(top, E, N)
+    ids = torch.randint(0, E, (40, top), generator=g, dtype=torch.int32).cuda()
+    want = ops.fp4_mm_id(x, w, ids, act=act)
+    wide = torch.full((40, K + 40), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, :K] = x
+    for T in (1, 2, 3, 4, 5, 8, 10, 11, 16, 17, 32, 33):
+        for a in (0, 40 - T):
+            y = ops.fp4_mm_id(x[a:a + T], w, ids[a:a + T].contiguous(), act=act)
+            assert torch.equal(y, want[a:a + T]), (T, a)
+            assert torch.equal(ops.fp4_mm_id(wide[a:a + T, :K], w, ids[a:a + T].contiguous(), act=act), y)
+    x2 = x.clone()
+    x2[1, 5], x2[2, 7] = float("nan"), float("inf")
+    y = ops.fp4_mm_id(x2[:4], w, ids[:4].contiguous(), act=act)
+    assert y[1:3].isnan().all() and torch.equal(y[0], want[0]) and torch.equal(y[3], want[3])
+    assert ops.device_status() == 0
+
+
+def test_few_tokens_captured_and_on_streams():
+    """One launch a call: replayed while the same runs on other streams, with ids that change between replays."""
+    x, w = made("nv", 4, 1536, 2048, E=64)
+    ids = torch.randint(0, 64, (4, 8), generator=gen(4), dtype=torch.int32).cuda()
+    other = torch.randint(-1, 64, (4, 8), generator=gen(5), dtype=torch.int32).cuda()
+    want, want2 = ops.fp4_mm_id(x, w, ids), ops.fp4_mm_id(x, w, other)
+    assert (want2[other < 0] == 0).all() and ops.device_status() == ops.DEVICE_BAD_ID
+    now, y = ids.clone(), torch.full_like(want, 7.0)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        ops.fp4_mm_id(x, w, now, out=y)
+        ops.fp4_mm_id(x, w, now, out=y)
+    streams, outs = [torch.cuda.Stream() for _ in range(3)], [torch.empty_like(want) for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(6):
+        now.copy_(other if i % 2 else ids)
+        for s, o in zip(streams, outs):
+            ops.fp4_mm_id(x, w, ids, out=o, stream=s)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want2 if i % 2 else want) and all(torch.equal(o, want) for o in outs)
+    ops.device_status()
