@@ -952,7 +952,12 @@ class FP4Matrix:
         2 F rows that ``fp4_gated`` takes: row 2 i is gate's row i, row 2 i + 1 up's."""
         if gate.shape != up.shape or gate.dim() not in (2, 3):
             raise ValueError("gate and up must both be [F, K] or [E, F, K]")
-        return fp4_quant(torch.stack((gate, up), -2).flatten(-3, -2), format, stream=stream)
+        if stream is None:
+            return fp4_quant(torch.stack((gate, up), -2).flatten(-3, -2), format)
+        _stream_on(stream, gate.get_device())
+        with torch.cuda.stream(stream):  # the interleaved rows are the call's own: made, read and given back in its order
+            both = torch.stack((gate, up), -2).flatten(-3, -2)
+        return fp4_quant(both, format, stream=stream)
 
     @classmethod
     def from_rows(cls, codes: torch.Tensor, scales: torch.Tensor, row_scale: torch.Tensor | None = None,

@@ -1,0 +1,53 @@
+"""Microscaled 4-bit calls with stream=: all that a call does of its own runs on that stream, whatever the current one is busy with."""
+import zlib
+
+import pytest
+import torch
+
+import fp4_cases as fc
+from skinny_gemm_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+BUSY = 200_000_000  # clocks, some 0.1 s
+
+
+def gen(*seed):
+    return torch.Generator().manual_seed(zlib.crc32(repr(seed).encode()))
+
+
+def rows(seed, *shape):
+    return fc.activations(gen(seed), shape[0] if len(shape) == 2 else shape[0] * shape[1], shape[-1]).view(shape).cuda()
+
+
+def same(a, b):
+    return torch.equal(a.codes, b.codes) and torch.equal(ops.fp4_dequant(a), ops.fp4_dequant(b))
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("shape", [(512, 320), (3, 130, 96)])
+def test_gated_on_a_stream(fmt, shape):
+    """The interleaved rows are made on the stream that quantises them: the current one is busy, and then uses the memory."""
+    gate, up = rows(1, *shape), rows(2, *shape)
+    both = torch.stack((gate, up), -2).flatten(-3, -2)
+    want = ops.fp4_quant(both, fmt)
+    s = torch.cuda.Stream()
+    poison = torch.full_like(both, float("nan"))  # what memory of that size holds on the current stream
+    torch.cuda.synchronize()
+    del poison
+    torch.cuda._sleep(BUSY)
+    w = ops.FP4Matrix.gated(gate, up, fmt, stream=s)
+    poison = torch.full_like(both, float("nan"))
+    torch.cuda.synchronize()
+    assert same(w, want) and same(ops.FP4Matrix.gated(gate, up, fmt), want)
+    # and the other way round: the stream is busy while the current one goes on
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+    w = ops.FP4Matrix.gated(gate, up, fmt, stream=s)
+    again = [torch.full_like(both, float("nan")) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert same(w, want) and len(again) == 3
+    if len(shape) == 3:
+        assert (w.E, w.N) == (shape[0], 2 * shape[1])
+        values = ops.fp4_dequant(w).view(shape[0], shape[1], 2, shape[2])
+        assert torch.equal(values[:, :, 0], ops.fp4_dequant(ops.fp4_quant(gate, fmt)))
+        assert torch.equal(values[:, :, 1], ops.fp4_dequant(ops.fp4_quant(up, fmt)))
