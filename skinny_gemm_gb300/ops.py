@@ -879,6 +879,19 @@ def fp4_scale_bytes(N: int, K: int, format: str) -> int:
     return -(-N // 128) * -(-K // b) * 512
 
 
+def _fp4_empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """What a call on ``stream`` (None: the current one) writes and returns: memory of that stream, as the current one may
+    still be busy with its own, and not given back before the current one is done with it either."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    now = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if now != stream:
+        t.record_stream(now)
+    return t
+
+
 class FP4Matrix:
     """A matrix of e2m1 codes with block scales on the GPU: ``codes`` uint8 [E * N, K / 2],
     two a byte, low nibble first; ``scales`` uint8 [E * fp4_scale_bytes(N, K, format)], in
@@ -914,13 +927,14 @@ class FP4Matrix:
         self._ptr = ctypes.addressof(self._c)
 
     @classmethod
-    def empty(cls, N: int, K: int, E: int = 1, format: str = "nv", device="cuda") -> "FP4Matrix":
+    def empty(cls, N: int, K: int, E: int = 1, format: str = "nv", device="cuda", stream=None) -> "FP4Matrix":
+        """Unset; for a call on ``stream`` (None: the current one)."""
         n = E * fp4_scale_bytes(N, K, format)
         if K <= 0 or K % 32 or N < 0 or E < 1:
             raise ValueError(f"N = {N}, K = {K} (a positive multiple of 32), E = {E}")
         # scales (a multiple of 512 bytes) and codes in one block of memory; their tensors are made when asked for
-        flat = torch.empty(n + E * N * (K // 2), dtype=torch.uint8, device=device)
-        f = torch.empty(E * N, dtype=torch.float32, device=device) if format == "nv" else None
+        flat = _fp4_empty((n + E * N * (K // 2),), torch.uint8, device, stream)
+        f = _fp4_empty((E * N,), torch.float32, device, stream) if format == "nv" else None
         self, at = cls.__new__(cls), flat.data_ptr()
         self.N, self.K, self.E, self.format = N, K, E, format
         self._flat, self._codes, self._scales, self._row_scale = flat, None, None, f
@@ -1014,7 +1028,7 @@ def fp4_quant(x: torch.Tensor, format: str = "nv", out: FP4Matrix | None = None,
     raw = _stream_on(stream, dev)
     if out is None:
         E = max(x.shape[0], 1) if x.dim() == 3 else 1
-        out = FP4Matrix.empty(M // E, K, E, format, x.device)
+        out = FP4Matrix.empty(M // E, K, E, format, x.device, stream)
     elif (out.N * out.E, out.K, out.format) != (M, K, format):
         raise ValueError(f"out must have {M} rows of {K} codes, format {format}")
     elif out._dev != dev:
@@ -1030,7 +1044,7 @@ def fp4_dequant(w: FP4Matrix, out: torch.Tensor | None = None, stream=None) -> t
     shape = (w.N, w.K) if w.E == 1 else (w.E, w.N, w.K)
     raw = _stream_on(stream, w._dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=w._device)
+        out = _fp4_empty(shape, torch.bfloat16, w._device, stream)
     else:
         _fp4_out(out, shape, w._dev)
     rc = (_lib or lib()).w4a16_fp4_dequant(w._ptr, out.data_ptr(), raw)
@@ -1096,7 +1110,7 @@ def _fp4_product(x, w: FP4Matrix, act, out, stream, workspace):
         M, stride = _fp4_x(x, w.K, dev)
         lead = x.shape[:-1]
     if out is None:
-        out = torch.empty((*lead, cols), dtype=torch.bfloat16, device=w._device)
+        out = _fp4_empty((*lead, cols), torch.bfloat16, w._device, stream)
     else:
         _fp4_out(out, (M, cols), dev)
     if quantised:
@@ -1142,7 +1156,7 @@ def fp4_mm_id(x: torch.Tensor, w: FP4Matrix, ids: torch.Tensor, act: str | None 
     shape = (*ids.shape, w.N if a == 0 else w.N // 2)
     raw = _stream_on(stream, w._dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=w._device)
+        out = _fp4_empty(shape, torch.bfloat16, w._device, stream)
     else:
         _fp4_out(out, shape, w._dev)
     keep, ws, wn = _fp4_space(_fp4_mm_id_bytes(T, top, w.K, w.E, FP4_FORMATS[w.format]), workspace, raw, stream, w)

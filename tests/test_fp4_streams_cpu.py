@@ -35,3 +35,22 @@ def test_gated_rows_are_made_on_the_stream(streams, monkeypatch, shape):
     with pytest.raises(ValueError):
         ops.FP4Matrix.gated(gate, up, stream=Stream(1))
     assert len(made) == 2
+
+
+def test_results_are_made_on_the_stream(streams, monkeypatch):
+    """... and the stream that was current keeps them from being given back while it reads; a call without stream= does neither."""
+    made, kept, here = [], [], Stream(0)
+
+    class Made(torch.Tensor):
+        def record_stream(self, s):
+            kept.append(s)
+
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: made.append(list(streams)) or torch.zeros(shape, dtype=dtype).as_subclass(Made))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: here)
+    s = Stream(0)
+    m = ops.FP4Matrix.empty(3, 64, stream=s)
+    assert made == [[s], [s]] and kept == [here, here] and (m.N, m.K) == (3, 64)
+    ops.FP4Matrix.empty(3, 64, format="mx", stream=here)
+    assert made[2:] == [[here]] and len(kept) == 2  # (the current one: nothing to tell)
+    ops.FP4Matrix.empty(3, 64)
+    assert made[3:] == [[], []] and len(kept) == 2

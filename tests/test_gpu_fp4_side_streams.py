@@ -51,3 +51,43 @@ def test_gated_on_a_stream(fmt, shape):
         values = ops.fp4_dequant(w).view(shape[0], shape[1], 2, shape[2])
         assert torch.equal(values[:, :, 0], ops.fp4_dequant(ops.fp4_quant(gate, fmt)))
         assert torch.equal(values[:, :, 1], ops.fp4_dequant(ops.fp4_quant(up, fmt)))
+
+
+def calls(fmt):
+    """Calls that allocate what they return, and a tensor of that."""
+    x, w = rows(3, 128, 320), ops.fp4_quant(rows(4, 256, 320), fmt)
+    experts, ids = ops.fp4_quant(rows(5, 4, 256, 320), fmt), torch.randint(0, 4, (128, 2), generator=gen(6), dtype=torch.int32).cuda()
+    return [lambda s: ops.fp4_mm(x, w, stream=s), lambda s: ops.fp4_mm(x[:3], w, stream=s), lambda s: ops.fp4_mm(x[:40], w, stream=s), lambda s: ops.fp4_mm(ops.fp4_quant(x, fmt, stream=s), w, stream=s),
+               lambda s: ops.fp4_gated(x, w, "silu", stream=s), lambda s: ops.fp4_mm_id(x, experts, ids, stream=s), lambda s: ops.fp4_dequant(w, stream=s),
+               lambda s: ops.fp4_quant(x, fmt, stream=s)._flat] + ([lambda s: ops.fp4_quant(x, fmt, stream=s).row_scale] if fmt == "nv" else [])
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("which", range(9))
+def test_results_made_on_a_stream(fmt, which):
+    """A result's memory is not what the current stream still writes, and is not given away while the current stream still reads."""
+    all_calls = calls(fmt)
+    if which >= len(all_calls):
+        return
+    call, s = all_calls[which], torch.cuda.Stream()
+    want = call(None).clone()
+    call(s)  # (the stream's workspace is there)
+    torch.cuda.synchronize()
+    old = torch.empty_like(want)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    old.zero_().fill_(7)  # (later, to memory that the allocator has back)
+    del old
+    got = call(s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    del got
+    first = call(s)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    copy = first.clone()  # (later)
+    del first
+    with torch.cuda.stream(s):
+        other = [torch.full_like(want, 9) for _ in range(3)]  # (now, to memory that the stream has to give)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and len(other) == 3
