@@ -2062,28 +2062,39 @@ cudaError_t get_encoder() {
   return g_encode_status;
 }
 
-cudaError_t make_param_map(CUtensorMap* map, const uint16_t* P, int64_t rows, int K, int box_rows) {
+// The driver encodes tensor maps under the thread's current context, which the runtime makes current with the first of its
+// calls that needs one; here the encoding may come before that.
+template <typename... Args>
+cudaError_t encode(Args... args) {
   if (cudaError_t e = get_encoder()) return e;
+  CUresult r = g_encode(args...);
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (cudaError_t e = cudaSetDevice(dev)) return e;
+    r = g_encode(args...);
+  }
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_param_map(CUtensorMap* map, const uint16_t* P, int64_t rows, int K, int box_rows) {
   cuuint64_t dims[2] = {(cuuint64_t)(K / kGroup), (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)(K / kGroup) * 2};
   cuuint32_t box[2] = {8, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(P), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(P), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 cudaError_t make_code_map(CUtensorMap* map, const uint32_t* Wq, int64_t rows, int K, int box_rows) {
-  if (cudaError_t e = get_encoder()) return e;
   cuuint64_t dims[2] = {(cuuint64_t)(K / 8), (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)K / 2};
   cuuint32_t box[2] = {(cuuint32_t)kBoxWords, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t*>(Wq), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t*>(Wq), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Tensor maps of one weight set with boxes of box_rows rows (32 for the
@@ -2519,25 +2530,21 @@ size_t tc_workspace_bytes() { return kWsBytes; }
 
 cudaError_t encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t inner,
                           int64_t outer, int64_t row_bytes, int box_inner, int box_outer, CUtensorMapSwizzle swizzle) {
-  if (cudaError_t e = get_encoder()) return e;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
   cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 cudaError_t encode_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, const int64_t (&dims)[3],
                           const int64_t (&strides)[2], const int (&box)[3], CUtensorMapSwizzle swizzle) {
-  if (cudaError_t e = get_encoder()) return e;
   cuuint64_t d[3], st[2] = {(cuuint64_t)strides[0], (cuuint64_t)strides[1]};
   cuuint32_t b[3], estr[3] = {1, 1, 1};
   for (int i = 0; i < 3; ++i) d[i] = (cuuint64_t)dims[i], b[i] = (cuuint32_t)box[i];
-  CUresult r = g_encode(map, type, 3, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode(map, type, 3, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // K % 512 != 0: the persistent kernel's per-unit parameter slots fit next to
