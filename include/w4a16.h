@@ -412,7 +412,8 @@ int w4a16_kv_append(const w4a16_bf16* k, int64_t k_stride, const w4a16_bf16* v, 
  *
  * workspace: w4a16_kv_attention_workspace_bytes(...) bytes of device memory,
  * 256-byte aligned, no initial contents needed; calls that share one must
- * not overlap on the GPU.  With G groups of 1024 tokens in max_len (or in a
+ * not overlap on the GPU (host threads may call on one stream: a call's
+ * launches follow one another on it).  With G groups of 1024 tokens in max_len (or in a
  * window and max_new), G * T * q_heads * (4 dim + 8) bytes hold partial
  * results where G > 1, and some tens of MB at most the rest.  Above 2^32 the
  * rows are taken in several launches that share that much (more only where 32
@@ -496,7 +497,8 @@ int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream);
  * another order, which M, W's shape and (routed) the sizes of the call decide.
  * workspace: device memory of
  * w4a16_fp4_mm_workspace_bytes(M, K, format) bytes, 256-byte aligned, no initial
- * contents needed; calls that share one must not overlap on the GPU.  M >= 0;
+ * contents needed; calls that share one must not overlap on the GPU (host threads
+ * may call on one stream: a call's launches follow one another on it).  M >= 0;
  * M == 0 is a no-op. */
 size_t w4a16_fp4_mm_workspace_bytes(int M, int K, int format);
 int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a16_bf16* y, int M, int act,

@@ -101,6 +101,22 @@ int flag_pointer(int** out) {
   return W4A16_OK;
 }
 
+// ---- host threads on one stream --------------------------------------------------
+//
+// A call of several launches hands its workspace from one to the next.  Threads
+// that launch such calls on one stream take turns, so that nothing that shares
+// the workspace comes between (a stream has a workspace, and PyTorch's threads
+// have one current stream).  Some streams share a turn.
+
+constexpr int kTurns = 64;
+std::mutex g_turns[kTurns];
+
+std::mutex& turn_of(const void* stream) {
+  const uint64_t h = reinterpret_cast<uintptr_t>(stream) * 0x9E3779B97F4A7C15ull;
+  return g_turns[h >> 58];
+}
+static_assert(kTurns == 1 << (64 - 58), "the hash's bits");
+
 // ---- validation ------------------------------------------------------------------
 
 constexpr int kMaxDim = 1 << 30;
@@ -681,6 +697,7 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
   KvAttentionArgs a{q, q_stride, *cache, table, cu, lens, out, B, T, q_heads, max_blocks, max_new, max_len, window,
                     scale, workspace, counters, nullptr, env().fault == kFaultWait};
   if (int rc = flag_pointer(&a.flags)) return rc;
+  std::lock_guard<std::mutex> turn(turn_of(stream));
   cudaError_t e = launch_kv_attention(a, env().pdl, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_kv_attention launch");
 }
@@ -849,10 +866,12 @@ int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a1
   float* factor = w->format == W4A16_FP4_NV ? reinterpret_cast<float*>(ws + sp.factor) : nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   Fp4MmArgs a = {};
+  std::unique_lock<std::mutex> turn(turn_of(stream), std::defer_lock);
   if (fp4_mm_fuses(*w, M)) {
     a.x = x;
     a.x_stride = x_stride;
   } else {
+    turn.lock();
     Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, M, w->K, M, w->format};
     if (cudaError_t e = launch_fp4_quant(q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm launch");
   }
@@ -949,6 +968,7 @@ int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, c
     return e == cudaSuccess ? W4A16_OK : cuda_fail(e, "w4a16_fp4_mm_id launch");
   }
   Fp4QuantArgs q{x, x_stride, ws, ws + sp.scales, factor, T, w->K, T, w->format};
+  std::lock_guard<std::mutex> turn(turn_of(stream));
   if (cudaError_t e = launch_fp4_route_quant(r, q, env().pdl, s)) return cuda_fail(e, "w4a16_fp4_mm_id launch");
   a.xc = ws;
   a.xs = ws + sp.scales;
