@@ -231,8 +231,7 @@ __device__ __forceinline__ bool quantise_own(const Fp4MmParams& p, OwnRows* own,
 
 // One sum of row `row` of W and place `at` of x, row m of y, whole warps (gate and up rows are neighbours).
 __device__ __forceinline__ void store(const Fp4MmParams& p, float v, float fw, const float* xf, int at, int64_t m, int row, bool mine) {
-  float t = v * fw;
-  if (xf) t *= xf[at];
+  const float t = xf ? fp4_scaled(v, fw, xf[at]) : v * fw;
   if (p.act == W4A16_FP4_LINEAR) {
     if (mine) p.y[m * p.N + row] = f32_to_bf16_bits(t);
   } else {
@@ -564,14 +563,15 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
     }
     cluster_arrive();
     cluster_wait();
-    if (live) {  // a warp a column, a lane four rows
-      const int row = wt * kWRows + 4 * lane, place = xt * NT + rank * per;
-      float fw[4];
+    if (live) {  // a warp a column, a lane four rows (and column lane's factor: there are at most half of 64)
+      const int row = wt * kWRows + 4 * lane, place = xt * NT + rank * per, cols = min(per, count - rank * per);
+      float fw[4], xf = 1.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) fw[i] = p.wf && row + i < p.N ? p.wf[row + i] : 1.0f;
+      if (lane < cols) xf = OWN ? (FMT == W4A16_FP4_NV ? own->factor[rank * per + lane] : 1.0f) : p.xf ? p.xf[place + lane] : 1.0f;
 #pragma unroll 2
-      for (int c = warp; c < min(per, count - rank * per); c += kThreads / 32) {
-        const float fx = OWN ? (FMT == W4A16_FP4_NV ? own->factor[rank * per + c] : 1.0f) : p.xf ? p.xf[place + c] : 1.0f;
+      for (int c = warp; c < cols; c += kThreads / 32) {
+        const float fx = __shfl_sync(0xffffffffu, xf, c);
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         for (int g = 0; g < split; ++g) {
           const uint32_t from = g == rank || !kParts ? sb + (uint32_t)(g * per * kWRows * 4) : parts + (uint32_t)((g - (g > rank)) * per * kWRows * 4);
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
           v[3] += f.w;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = v[i] * fw[i] * fx;
+        for (int i = 0; i < 4; ++i) v[i] = fp4_scaled(v[i], fw[i], fx);
         store4(p, v, place + c, row);
       }
     }

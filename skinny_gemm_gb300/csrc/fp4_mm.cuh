@@ -43,6 +43,15 @@ __device__ __forceinline__ float fp4_activate(float g, int act) {
   return __fdividef(g, 1.0f + __expf(-t));
 }
 
+// v times the row factors of W and x, each anywhere in fp32's range.  Where their product is a normal number, as for one
+// above 1 and one below, it comes first.  Else both are above 1 or both below, and v is multiplied by one after the other: what
+// is in between lies between v and the result.  (Either order alone gives 0 or infinity for some results that are neither.)
+__device__ __forceinline__ bool fp4_normal(float f) { return ((__float_as_uint(f) + 0x00800000u) & 0x7FFFFFFFu) >= 0x01000000u; }
+__device__ __forceinline__ float fp4_scaled(float v, float fw, float fx) {
+  const float f = fw * fx;
+  return fp4_normal(f) ? v * f : v * fw * fx;
+}
+
 __device__ __forceinline__ uint32_t fp4_bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);

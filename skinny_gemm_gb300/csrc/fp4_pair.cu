@@ -99,6 +99,7 @@ struct Rows {
   float fx;
   int n0;  // the tile's first row of W
   bool mine, factors;
+  bool plain;  // all factors of x and W that an epilogue warp has of the tile have products that are normal numbers
   Rows() = default;
   __device__ __forceinline__ Rows(const Fp4MmParams& p, const PairParams& pp, int64_t u, int x_tiles, int r) {
     int xt, nt;
@@ -116,8 +117,16 @@ struct Rows {
     fx = mine && p.xf ? p.xf[place + r] : 1.0f;
     cols = p.act == W4A16_FP4_LINEAR ? p.N : p.N / 2;
     factors = p.wf || p.xf;
+    plain = true;
   }
-  __device__ __forceinline__ float wf(const Fp4MmParams& p, int n) const { return !p.wf ? 1.0f : n < p.N ? p.wf[expert * p.N + n] : 0.f; }
+  __device__ __forceinline__ float wf(const Fp4MmParams& p, int n) const { return !p.wf ? 1.0f : n < p.N ? p.wf[expert * p.N + n] : 1.0f; }
+  // lo, hi: the least and the largest of those factors' magnitudes, as bits, that this lane holds.  Whole warps, and one answer
+  // for them: what follows has instructions that a warp executes together.
+  __device__ __forceinline__ void span(uint32_t lo, uint32_t hi) {
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    plain = __all_sync(0xffffffffu, fp4_normal(__uint_as_float(lo) * fx) && fp4_normal(__uint_as_float(hi) * fx));
+  }
 };
 
 // 32 sums of a thread's row, from row n0 of W on, to y; wf: W's factors for them.  A lane stores 32 bytes of its row at a
@@ -125,11 +134,22 @@ struct Rows {
 // bytes a row.)
 __device__ __forceinline__ void put32(const Fp4MmParams& p, const Rows& row, const float* wf, int n0, float (&v)[32]) {
   if (row.factors) {
+    if (__builtin_expect(row.plain, 1)) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(wf + j);
-      mul2(v[j], v[j + 1], f.x, f.y, row.fx);
-      mul2(v[j + 2], v[j + 3], f.z, f.w, row.fx);
+      for (int j = 0; j < 32; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(wf + j);
+        mul2(v[j], v[j + 1], f.x, f.y, row.fx);
+        mul2(v[j + 2], v[j + 3], f.z, f.w, row.fx);
+      }
+    } else {
+      // (a loop over a copy: unrolled three times, its instructions cost all other calls 0.1 to 0.4 us)
+      float u[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) u[j] = v[j];
+#pragma unroll 1
+      for (int j = 0; j < 32; ++j) u[j] = fp4_scaled(u[j], wf[j], row.fx);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = u[j];
     }
   }
   const bool linear = p.act == W4A16_FP4_LINEAR;
@@ -385,21 +405,34 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     for (int64_t u = first; u < units && !*s_abort; u += step, ++n) {
       const int b = (int)(n & 1);
       if (SPLIT) {  // (the rest below)
-        for (int c = part + split * third, i = 0; c < tn / 32; c += 3 * split, ++i)
-          s_wf[96 * (warp - 2) + 32 * i + lane] = split_row.wf(p, split_row.n0 + 32 * c + lane);
+        uint32_t lo = 0x3F800000u, hi = lo;
+        for (int c = part + split * third, i = 0; c < tn / 32; c += 3 * split, ++i) {
+          const float f = split_row.wf(p, split_row.n0 + 32 * c + lane);
+          s_wf[96 * (warp - 2) + 32 * i + lane] = f;
+          lo = min(lo, __float_as_uint(fabsf(f)));
+          hi = max(hi, __float_as_uint(fabsf(f)));
+        }
+        split_row.span(lo, hi);
         if (!mbar_wait_warp(acc_full(0), 0, limit + (uint32_t)p.stages) && lane == 0) timeout();
         break;
       }
-      const Rows o(p, pp, u, x_tiles, 128 * (int)rank + 32 * q + lane);
+      Rows o(p, pp, u, x_tiles, 128 * (int)rank + 32 * q + lane);
       float* wf = s_wf + 96 * (warp - 2);
       // The i-th 32 columns to be read, those that both accumulators have first: the second's first and the first's last
       // ones.  Each of the three warps of 32 lanes takes every third.
       auto column = [&](int i) { return 32 * (b ? i : (i + T::kAccStep / 32) % 8); };
       if (o.factors) {
+        uint32_t lo = 0x3F800000u, hi = lo;
         __syncwarp();
 #pragma unroll
-        for (int g = 0; g < 3; ++g) wf[32 * g + lane] = o.wf(p, o.n0 + column(third + 3 * g) + lane);
+        for (int g = 0; g < 3; ++g) {
+          const float f = o.wf(p, o.n0 + column(third + 3 * g) + lane);
+          wf[32 * g + lane] = f;
+          lo = min(lo, __float_as_uint(fabsf(f)));
+          hi = max(hi, __float_as_uint(fabsf(f)));
+        }
         __syncwarp();
+        o.span(lo, hi);
       }
       if (!mbar_wait_warp(acc_full(b), (n >> 1) & 1, limit + (uint32_t)p.stages)) {
         if (lane == 0) timeout();
@@ -410,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       auto exists = [&](int i) { return i < 8 && column(i) < tn && o.n0 + column(i) < p.N; };
       auto put = [&](int i, float (&v)[32]) {
         if (exists(i)) put32(p, o, wf + 32 * (i / 3), o.n0 + column(i), v);
+        __syncwarp();  // (rows that are not stored are back for the next load)
       };
       // (only where a tile comes that waits for it: no arrival is on its way to a CTA that may be gone)
       auto arrive = [&](uint32_t bar, int64_t next) {
@@ -492,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
             }
           }
           put32(p, split_row, s_wf + 96 * (warp - 2) + 32 * i, n0 + 32 * c, v);
+          __syncwarp();
         }
       }
     }
