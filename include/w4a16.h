@@ -441,9 +441,9 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
  * Matrices of e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; bit
  * 3 the sign) with one scale per block of a row, as weights and, quantised by
  * the call, as activations: both operands go to the tensor cores as they lie.
- *   W4A16_FP4_MX  blocks of 32, e8m0 scales: value = code * 2^(byte - 127)
- *   W4A16_FP4_NV  blocks of 16, e4m3 scales, a factor per row:
- *                 value = code * scale * row_scale
+ *   W4A16_FP4_MX  blocks of 32, e8m0 scales: value = code * 2^(byte - 127) [* row_scale]
+ *   W4A16_FP4_NV  blocks of 16, e4m3 scales (without a sign: bit 7 clear), a factor
+ *                 per row: value = code * scale * row_scale
  * Code k of a row lies in bits 4 (k % 2) of byte k / 2.  Scales lie in atoms
  * of 512 bytes, 128 rows by 4 blocks: block b of row r is byte
  *   (r / 128 * ceil(blocks / 4) + b / 4) * 512 + 16 (r % 32) + 4 (r % 128 / 32) + b % 4
@@ -456,7 +456,7 @@ int w4a16_kv_attention(const w4a16_bf16* q, int64_t q_stride, const w4a16_kv_cac
 typedef struct {
   uint8_t* codes;   /* [experts * rows][K / 2], 16-byte aligned */
   uint8_t* scales;  /* experts times w4a16_fp4_scale_bytes(rows, K, format), 16-byte aligned */
-  float* row_scale; /* [experts * rows]; NULL: 1 (mx has none) */
+  float* row_scale; /* [experts * rows]; NULL: 1 (mx needs none) */
   int rows;         /* rows of one expert (N of a weight matrix, M of activations) */
   int K;            /* a multiple of 32 */
   int experts;      /* 1 for a plain matrix */
@@ -468,8 +468,8 @@ size_t w4a16_fp4_scale_bytes(int rows, int K, int format);
 
 /* Quantise out->experts * out->rows rows of bf16, row r at x + r * x_stride
  * (elements, a multiple of 8; x 16-byte aligned), into out's codes, scales and
- * (nv) row_scale.  With p = max |x| of a block, q = max |x| of a row:
- *   mx  scale = 2^e, e = max(floor(log2 p) - 2, -127)
+ * row_scale.  With p = max |x| of a block, q = max |x| of a row:
+ *   mx  scale = 2^e, e = max(floor(log2 p) - 2, -127); row_scale = 1, where there is one
  *   nv  row_scale = f, the smallest power of two >= 2^-126 with q <= 6 * 448 f;
  *       scale = e4m3(p / f / 6), to nearest even; a block of scale 0 has codes +0
  *   code = e2m1(x / scale [/ f]), to nearest, ties to the even code, at most 6;

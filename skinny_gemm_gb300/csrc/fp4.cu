@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kQuantMost, 1) fp4_quant_kernel(Fp4QuantArgs p
 #pragma unroll 1
   for (int c0 = C * threads; c0 < all; c0 += threads) write(c0, c0 + tid < units ? load16(x + 16 * (c0 + tid)) : zero16());
   if constexpr (ROUTE == kNone) {
-    if (FMT == W4A16_FP4_NV && tid == 0) p.row_scale[r] = exp2n(e);
+    if (tid == 0 && (FMT == W4A16_FP4_NV || p.row_scale)) p.row_scale[r] = FMT == W4A16_FP4_NV ? exp2n(e) : 1.0f;
   } else {
     for (int j = 0; j < route.top; ++j) {
       const int at = s_route[j];

@@ -1,0 +1,35 @@
+"""Microscaled 4-bit matrices made and made again: row factors that a caller brings."""
+import zlib
+
+import pytest
+import torch
+
+import fp4_cases as fc
+from skinny_gemm_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(*seed):
+    return torch.Generator().manual_seed(zlib.crc32(repr(seed).encode()))
+
+
+@pytest.mark.parametrize("E,N,K", [(1, 1, 32), (1, 300, 320), (3, 130, 2304)])
+def test_mx_rows_quantised_over_factors(E, N, K):
+    """An mx matrix may have row factors; rows quantised into it have factors of 1, whatever was there."""
+    x = fc.activations(gen(E, N, K), E * N, K).cuda()
+    x = x if E == 1 else x.view(E, N, K)
+    want = ops.fp4_quant(x, "mx")
+    old = torch.rand(E * N, generator=gen(1)).cuda() * 100 - 3
+    old[0] = float("nan")
+    w = ops.FP4Matrix(torch.zeros_like(want.codes), torch.zeros_like(want.scales), old, N, K, E, "mx")
+    assert ops.fp4_quant(x, "mx", out=w) is w
+    assert torch.equal(ops.fp4_dequant(w), ops.fp4_dequant(want))
+    rows = fc.activations(gen(2), 5, K).cuda()
+    if E == 1:
+        assert torch.equal(ops.fp4_mm(rows, w), ops.fp4_mm(rows, want))
+        assert torch.equal(ops.fp4_mm(w, ops.fp4_quant(rows, "mx")), ops.fp4_mm(want, ops.fp4_quant(rows, "mx")))
+    else:
+        ids = torch.tensor([0, 1, 2, 1, 0], dtype=torch.int32, device="cuda")
+        assert torch.equal(ops.fp4_mm_id(rows, w, ids), ops.fp4_mm_id(rows, want, ids))
+    assert ops.device_status() == 0
