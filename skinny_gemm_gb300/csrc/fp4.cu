@@ -265,8 +265,12 @@ __global__ void __launch_bounds__(kBackThreads) fp4_dequant_kernel(w4a16_fp4 w, 
     const uint2 code = *reinterpret_cast<const uint2*>(w.codes + r * (w.K / 2) + 8 * (int64_t)c);
     const uint32_t byte = scales[(int64_t)(b / 4) * kFp4Atom + b % 4];
     float s = 1.0f, f = factor;
-    if (mx) f = __fmul_rn(byte == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte - 127), factor);
-    else s = (byte & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte & 0x7Fu) << 20 | (byte & 0x80u) << 24), exp2n(120));
+    if (mx) {
+      const float e = byte == 255 ? __uint_as_float(0x7FC00000u) : exp2i((int)byte - 127);
+      f = __fmul_rn(e, factor);
+      // past fp32's range, 2^8 of it go to the codes (exact in fp16), and what is still past it makes all of them infinite but 0
+      if (isinf(f)) s = 256.0f, f = fmaxf(fminf(__fmul_rn(__fmul_rn(e, 1.0f / 256), factor), 3.4028235e38f), -3.4028235e38f);
+    } else s = (byte & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float((byte & 0x7Fu) << 20 | (byte & 0x80u) << 24), exp2n(120));
     const __half2 sh = __float2half2_rn(s);
     uint32_t out[8];
 #pragma unroll

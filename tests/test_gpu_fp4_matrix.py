@@ -33,3 +33,14 @@ def test_mx_rows_quantised_over_factors(E, N, K):
         ids = torch.tensor([0, 1, 2, 1, 0], dtype=torch.int32, device="cuda")
         assert torch.equal(ops.fp4_mm_id(rows, w, ids), ops.fp4_mm_id(rows, want, ids))
     assert ops.device_status() == 0
+
+
+def test_mx_scales_and_factors_at_their_ends():
+    """Values of mx matrices whose scales and row factors are large, small or one of each: zeros stay zeros."""
+    N, K = 40, 64
+    codes = (torch.arange(N * K).view(N, K) % 16).numpy().astype("uint8")
+    byte = torch.tensor([[254, 1], [250, 130], [0, 254], [3, 0], [127, 254]] * 8, dtype=torch.uint8).numpy()
+    factor = torch.tensor([2.0 ** 20, 1.375 * 2.0 ** 100, 1.25 * 2.0 ** -90, 1.5 * 2.0 ** 126, 2.0 ** -126, 1.0, 0.75, -1.5] * 5).numpy()
+    w = fc.matrix(ops, codes, byte, factor, 1, "mx")
+    want = fc.values(codes, byte, None, "mx") * factor.astype("float64")[:, None]  # (exact: 2 + 4 significant bits)
+    assert torch.equal(ops.fp4_dequant(w).double(), torch.from_numpy(want).to(torch.bfloat16).double().cuda())
