@@ -974,10 +974,10 @@ class FP4Matrix:
         return fp4_quant(both, format, stream=stream)
 
     @classmethod
-    def from_rows(cls, codes: torch.Tensor, scales: torch.Tensor, row_scale: torch.Tensor | None = None,
+    def from_rows(cls, codes: torch.Tensor, scales: torch.Tensor, row_scale: torch.Tensor | float | None = None,
                   format: str = "nv") -> "FP4Matrix":
         """From codes uint8 [N, K / 2] or [E, N, K / 2] and scale bytes uint8 [.., N, K / block]
-        in row order; row_scale float32 [.., N], or one number for all rows."""
+        in row order; row_scale [.., N], or one number (of Python, or a tensor of one) for all rows."""
         E, N, K = (1 if codes.dim() == 2 else codes.shape[0]), codes.shape[-2], 2 * codes.shape[-1]
         fp4_scale_bytes(N, K, format)
         nb = K // FP4_BLOCK[format]
@@ -988,7 +988,7 @@ class FP4Matrix:
         full[:, :N, :nb] = scales.view(E, N, nb)
         tiled = full.view(E, rows // 128, 4, 32, cols // 4, 4).permute(0, 1, 4, 3, 2, 5).reshape(-1).contiguous()
         if row_scale is not None:
-            row_scale = row_scale.to(torch.float32).expand(codes.shape[:-1]).reshape(-1).contiguous()
+            row_scale = torch.as_tensor(row_scale, dtype=torch.float32, device=codes.device).expand(codes.shape[:-1]).reshape(-1).contiguous()
         return cls(codes.reshape(E * N, K // 2), tiled, row_scale, N, K, E, format)
 
     @property

@@ -44,3 +44,19 @@ def test_mx_scales_and_factors_at_their_ends():
     w = fc.matrix(ops, codes, byte, factor, 1, "mx")
     want = fc.values(codes, byte, None, "mx") * factor.astype("float64")[:, None]  # (exact: 2 + 4 significant bits)
     assert torch.equal(ops.fp4_dequant(w).double(), torch.from_numpy(want).to(torch.bfloat16).double().cuda())
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("E", [1, 3])
+def test_one_factor_for_all_rows(fmt, E):
+    """A checkpoint's one factor of a matrix: a number, a tensor of one on either side, or one each row."""
+    g = gen(fmt, E)
+    N, K, f = 70, 96, 0.375
+    codes, byte, _, _ = fc.weights(g, E, N, K, fmt)
+    lead = (N,) if E == 1 else (E, N)
+    c, s = (torch.from_numpy(a).view(*lead, -1).cuda() for a in (fc.pack(codes), byte))
+    want = torch.from_numpy(fc.values(codes, byte, None, fmt) * f).to(torch.bfloat16).cuda().view(*lead, K)
+    for factor in (f, torch.tensor(f), torch.tensor([f], device="cuda"), torch.tensor(f, dtype=torch.float64, device="cuda"), torch.full(lead, f, device="cuda"), torch.full(lead, f)):
+        w = ops.FP4Matrix.from_rows(c, s, factor, fmt)
+        assert torch.equal(ops.fp4_dequant(w), want)
+    assert torch.equal(ops.fp4_dequant(ops.FP4Matrix.from_rows(c, s, 2, fmt)).float(), want.float() / f * 2)
