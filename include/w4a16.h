@@ -496,8 +496,8 @@ int w4a16_fp4_dequant(const w4a16_fp4* w, w4a16_bf16* y, void* stream);
  * row's result is the one-row call's, bit for bit; more rows are summed in
  * another order, which M, W's shape and (routed) the sizes of the call decide.
  * workspace: device memory of
- * w4a16_fp4_mm_workspace_bytes(M, K, format) bytes, 256-byte aligned, no initial
- * contents needed; calls that share one must not overlap on the GPU (host threads
+ * w4a16_fp4_mm_workspace_bytes(M, K, format) bytes, 256-byte aligned, apart from the
+ * call's operands, no initial contents needed; calls that share one must not overlap on the GPU (host threads
  * may call on one stream: a call's launches follow one another on it).  M >= 0;
  * M == 0 is a no-op. */
 size_t w4a16_fp4_mm_workspace_bytes(int M, int K, int format);
@@ -510,7 +510,7 @@ int w4a16_fp4_mm_q(const w4a16_fp4* x, const w4a16_fp4* w, w4a16_bf16* y, int ac
 
 /* Routed experts: y[t][j] = W[ids[t * top + j]] x'[t] for T tokens of `top`
  * choices each (an expert may occur twice); ids int32 [T][top] on the device, y
- * bf16 [T][top][rows or rows / 2].  An id outside 0..experts-1 gives a row of
+ * bf16 [T][top][rows or rows / 2], not over x, w or ids.  An id outside 0..experts-1 gives a row of
  * zeros and raises W4A16_DEVICE_BAD_ID.  experts <= 4096, T >= 0, top 1..1024. */
 size_t w4a16_fp4_mm_id_workspace_bytes(int T, int top, int K, int experts, int format);
 int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, const int32_t* ids, w4a16_bf16* y,

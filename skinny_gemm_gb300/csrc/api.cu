@@ -800,11 +800,13 @@ int64_t fp4_id_tiles(int64_t rows, int experts) {
   return (rows < experts ? rows : experts) + rows / fp4_id_tile(rows, experts);
 }
 
-int check_fp4_space(const void* ws, size_t bytes, size_t need) {
+// The workspace holds what the call's launches hand on (for routed calls, places of rows too).
+int check_fp4_space(const void* ws, size_t bytes, size_t need, const void* x, int64_t x_bytes, const void* y, int64_t y_bytes) {
   if (!ws) return fail(W4A16_ERR_NULL, "the call needs a workspace of %zu bytes", need);
   if (misaligned(ws, 256)) return fail(W4A16_ERR_ALIGN, "the workspace must be 256-byte aligned");
   if (bytes < need) return fail(W4A16_ERR_SHAPE, "a workspace of %zu bytes is too small (%zu)", bytes, need);
-  return W4A16_OK;
+  if (fp4_overlap(ws, (int64_t)need, x, x_bytes)) return fail(W4A16_ERR_SHAPE, "x overlaps the workspace");
+  return fp4_overlap(ws, (int64_t)need, y, y_bytes) ? fail(W4A16_ERR_SHAPE, "y overlaps the workspace") : W4A16_OK;
 }
 
 }  // namespace
@@ -856,9 +858,10 @@ int w4a16_fp4_mm(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, w4a1
   if (int rc = check_fp4_rows(x, x_stride, M, w->K)) return rc;
   if (!y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "y must be 2-byte aligned");
-  if (int rc = check_fp4_apart(x, fp4_x_bytes(x_stride, M, w->K), w, y, fp4_y_bytes(w, M, act))) return rc;
+  const int64_t x_bytes = fp4_x_bytes(x_stride, M, w->K), y_bytes = fp4_y_bytes(w, M, act);
+  if (int rc = check_fp4_apart(x, x_bytes, w, y, y_bytes)) return rc;
   const Fp4Space sp = fp4_space(M, M, 0, w->K, w->format);
-  if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total)) return rc;
+  if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total, x, x_bytes, y, y_bytes)) return rc;
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
   int* flags = nullptr;
   if (int rc = flag_pointer(&flags)) return rc;
@@ -937,11 +940,13 @@ int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, c
   if (int rc = check_fp4_rows(x, x_stride, T, w->K)) return rc;
   if (!ids || !y) return fail(W4A16_ERR_NULL, "null tensor pointer");
   if (misaligned(ids, 4) || misaligned(y, 2)) return fail(W4A16_ERR_ALIGN, "ids must be 4-byte and y 2-byte aligned");
-  if (int rc = check_fp4_apart(x, fp4_x_bytes(x_stride, T, w->K), w, y, fp4_y_bytes(w, (int64_t)T * top, act))) return rc;
+  const int64_t x_bytes = fp4_x_bytes(x_stride, T, w->K), y_bytes = fp4_y_bytes(w, (int64_t)T * top, act);
+  if (int rc = check_fp4_apart(x, x_bytes, w, y, y_bytes)) return rc;
+  if (fp4_overlap(ids, 4LL * T * top, y, y_bytes)) return fail(W4A16_ERR_SHAPE, "y overlaps ids");
   const int64_t rows = (int64_t)T * top, tiles = fp4_id_tiles(rows, w->experts), places = tiles * fp4_id_span(rows, w->experts);
   if (places > INT32_MAX) return fail(W4A16_ERR_EXPERTS, "T * top = %lld rows are too many for one call", (long long)rows);
   const Fp4Space sp = fp4_space(places, rows, tiles, w->K, w->format);
-  if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total)) return rc;
+  if (int rc = check_fp4_space(workspace, workspace_bytes, sp.total, x, x_bytes, y, y_bytes)) return rc;
   if (env().fault == kFaultLaunch) return fail(W4A16_ERR_CUDA, "injected launch fault (W4A16_FAULT)");
   int* flags = nullptr;
   if (int rc = flag_pointer(&flags)) return rc;
