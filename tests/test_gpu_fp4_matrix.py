@@ -60,3 +60,15 @@ def test_one_factor_for_all_rows(fmt, E):
         w = ops.FP4Matrix.from_rows(c, s, factor, fmt)
         assert torch.equal(ops.fp4_dequant(w), want)
     assert torch.equal(ops.fp4_dequant(ops.FP4Matrix.from_rows(c, s, 2, fmt)).float(), want.float() / f * 2)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [1, 5, 16, 40, 64, 70, 300])
+def test_gated_of_quantised_rows(fmt, act, M):
+    """One quantisation for both a gated and a plain product: the bits of the calls that quantise themselves."""
+    x = fc.activations(gen(3, M), M, 320).cuda()
+    w = ops.FP4Matrix.gated(fc.activations(gen(4), 140, 320).cuda(), fc.activations(gen(5), 140, 320).cuda(), fmt)
+    q = ops.fp4_quant(x, fmt)
+    assert torch.equal(ops.fp4_gated(q, w, act), ops.fp4_gated(x, w, act)) and torch.equal(ops.fp4_mm(q, w), ops.fp4_mm(x, w))
+    assert ops.device_status() == 0

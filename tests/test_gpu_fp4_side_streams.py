@@ -91,3 +91,26 @@ def test_results_made_on_a_stream(fmt, which):
         other = [torch.full_like(want, 9) for _ in range(3)]  # (now, to memory that the stream has to give)
     torch.cuda.synchronize()
     assert torch.equal(copy, want) and len(other) == 3
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_captured_beside_the_capturing_stream(fmt):
+    """Calls on a stream that a capture has forked, whose results and temporaries are made and given back in it."""
+    x, w = rows(7, 70, 320), ops.fp4_quant(rows(8, 256, 320), fmt)
+    want = [ops.fp4_mm(x, w), ops.fp4_gated(x[:3], w), ops.fp4_mm(ops.fp4_quant(x, fmt), w)]
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = [ops.fp4_mm(x, w, stream=s), ops.fp4_gated(x[:3], w, stream=s)]
+        for _ in range(3):
+            last = ops.fp4_mm(ops.fp4_quant(x, fmt, stream=s), w, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        total = got[0] + last
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip([*got, last], want)) and torch.equal(total, want[0] + want[2])
+    again = [ops.fp4_mm(x, w, stream=s) for _ in range(20)]  # (the allocator goes on after the capture)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[0]) for y in again) and ops.device_status() == 0
