@@ -175,6 +175,20 @@ def _stream_ptr(stream) -> int:
     return int(s.cuda_stream)
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """What a call on ``stream`` (None: the current one) writes and returns: memory of
+    that stream, as the current one may still be busy with its own, and not given back
+    before the current one is done with it either."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    now = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if now != stream:
+        t.record_stream(now)
+    return t
+
+
 def _dev_tensor(t: torch.Tensor, dtype: torch.dtype, name: str) -> torch.Tensor:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -302,7 +316,7 @@ class W4Matrix:
             raise ValueError(f"scales and biases must hold N * K / group = {N * (K // group)} values")
         out = []
         for t in (scales, biases):
-            d = torch.empty(N, K // GROUP, dtype=torch.bfloat16, device=t.device)
+            d = _empty((N, K // GROUP), torch.bfloat16, t.device, stream)
             _raise(lib().w4a16_expand_groups(t.data_ptr(), d.data_ptr(), N, K, group, _stream_ptr(stream)))
             out.append(d)
         (stream if stream is not None else torch.cuda.current_stream()).synchronize()
@@ -328,7 +342,7 @@ def mm(x: torch.Tensor, w: W4Matrix, out: torch.Tensor | None = None, kernel=Non
         raise ValueError("group-128 tables run on their own kernel; no kernel selection")
     M = x.numel() // w.K
     if out is None:
-        out = torch.empty(*x.shape[:-1], w.N, dtype=torch.bfloat16, device=x.device)
+        out = _empty((*x.shape[:-1], w.N), torch.bfloat16, x.device, stream)
     _dev_tensor(out, torch.bfloat16, "out")
     if out.numel() != M * w.N:
         raise ValueError("out has the wrong number of elements")
@@ -367,12 +381,12 @@ def mm_argmax(x: torch.Tensor, w: W4Matrix, idx: torch.Tensor | None = None, val
         raise ValueError(f"x has K={x.shape[-1]}, weights have K={w.K}")
     M = x.numel() // w.K
     if idx is None:
-        idx = torch.empty(x.shape[:-1], dtype=torch.int32, device=x.device)
+        idx = _empty(x.shape[:-1], torch.int32, x.device, stream)
     _dev_tensor(idx, torch.int32, "idx")
     if idx.numel() != M:
         raise ValueError("idx must have one element per row")
     if val is None:
-        val = torch.empty(x.shape[:-1], dtype=torch.bfloat16, device=x.device)
+        val = _empty(x.shape[:-1], torch.bfloat16, x.device, stream)
     if val is not False:
         _dev_tensor(val, torch.bfloat16, "val")
         if val.numel() != M:
@@ -397,7 +411,7 @@ def embed(ids: torch.Tensor, w: W4Matrix, out: torch.Tensor | None = None, strea
     _dev_tensor(ids, torch.int32, "ids")
     T = ids.numel()
     if out is None:
-        out = torch.empty(*ids.shape, w.K, dtype=torch.bfloat16, device=ids.device)
+        out = _empty((*ids.shape, w.K), torch.bfloat16, ids.device, stream)
     _dev_tensor(out, torch.bfloat16, "out")
     if out.numel() != T * w.K:
         raise ValueError("out has the wrong number of elements")
@@ -418,7 +432,7 @@ def mm_group(xs, ws, outs=None, stream=None) -> list:
     K = ws[0].K
     M = xs[0].numel() // K if K else 0
     if outs is None:
-        outs = [torch.empty(*x.shape[:-1], w.N, dtype=torch.bfloat16, device=x.device) for x, w in zip(xs, ws)]
+        outs = [_empty((*x.shape[:-1], w.N), torch.bfloat16, x.device, stream) for x, w in zip(xs, ws)]
     items = (Item * len(xs))()
     for i, (x, w, y) in enumerate(zip(xs, ws, outs)):
         if w.E != 1:
@@ -447,7 +461,7 @@ def mm_id(x: torch.Tensor, w: W4Matrix, ids: torch.Tensor, out: torch.Tensor | N
     if ids.numel() != T:
         raise ValueError("ids must hold one expert id per token")
     if out is None:
-        out = torch.empty(T, w.N, dtype=torch.bfloat16, device=x.device)
+        out = _empty((T, w.N), torch.bfloat16, x.device, stream)
     _dev_tensor(out, torch.bfloat16, "out")
     L = lib()
     rc = L.w4a16_mm_id_kernel(x.data_ptr(), w.Wq.data_ptr(), w.scales.data_ptr(), w.biases.data_ptr(),
@@ -459,7 +473,7 @@ def mm_id(x: torch.Tensor, w: W4Matrix, ids: torch.Tensor, out: torch.Tensor | N
 
 def unpack(w: W4Matrix, stream=None) -> torch.Tensor:
     """Codes q[N][K] as uint8 through ``w4a16_unpack`` (bit-exact debug path)."""
-    q = torch.empty(w.N, w.K, dtype=torch.uint8, device=w.Wq.device)
+    q = _empty((w.N, w.K), torch.uint8, w.Wq.device, stream)
     _raise(lib().w4a16_unpack(w.Wq.data_ptr(), q.data_ptr(), w.N, w.K, _stream_ptr(stream)))
     return q
 
@@ -467,7 +481,7 @@ def unpack(w: W4Matrix, stream=None) -> torch.Tensor:
 def dequant(w: W4Matrix, stream=None) -> torch.Tensor:
     """fp32 weights fma(q, s, b) [N][K] through ``w4a16_dequant``."""
     _g64(w, "dequant")
-    out = torch.empty(w.N, w.K, dtype=torch.float32, device=w.Wq.device)
+    out = _empty((w.N, w.K), torch.float32, w.Wq.device, stream)
     _raise(lib().w4a16_dequant(w.Wq.data_ptr(), w.scales.data_ptr(), w.biases.data_ptr(), out.data_ptr(),
                                w.N, w.K, _stream_ptr(stream)))
     return out
@@ -511,7 +525,7 @@ class STQ1Matrix:
             raise ValueError(f"STQ1_0 needs N >= 1 and K a multiple of 256 in 256..32768 (N={N}, K={K})")
         if blocks.numel() != E * N * (K // STQ1_BLOCK_WEIGHTS) * STQ1_BLOCK_BYTES:
             raise ValueError("blocks must hold E * N * K/256 blocks of 42 bytes")
-        packed = torch.empty(E * per, dtype=torch.uint8, device=blocks.device)
+        packed = _empty((E * per,), torch.uint8, blocks.device, stream)
         src = blocks.reshape(E, -1)
         for e in range(E):
             _raise(lib().stq1_pack(src[e].data_ptr(), packed.data_ptr() + e * per, N, K, _stream_ptr(stream)))
@@ -541,7 +555,7 @@ def stq1_mm(x: torch.Tensor, w: STQ1Matrix, out: torch.Tensor | None = None, str
         raise ValueError(f"x has K={x.shape[-1]}, weights have K={w.K}")
     M = x.numel() // w.K
     if out is None:
-        out = torch.empty(*x.shape[:-1], w.N, dtype=torch.float32, device=x.device)
+        out = _empty((*x.shape[:-1], w.N), torch.float32, x.device, stream)
     _dev_tensor(out, torch.float32, "out")
     if out.numel() != M * w.N:
         raise ValueError("out has the wrong number of elements")
@@ -560,7 +574,7 @@ def stq1_mm_id(x: torch.Tensor, w: STQ1Matrix, ids: torch.Tensor, out: torch.Ten
     if ids.numel() != T:
         raise ValueError("ids must hold one expert id per token")
     if out is None:
-        out = torch.empty(T, w.N, dtype=torch.float32, device=x.device)
+        out = _empty((T, w.N), torch.float32, x.device, stream)
     _dev_tensor(out, torch.float32, "out")
     _raise(lib().stq1_mm_id(x.data_ptr(), w.packed.data_ptr(), ids.data_ptr(), out.data_ptr(), T, w.N, w.K, w.E,
                             _stream_ptr(stream)))
@@ -574,7 +588,7 @@ def stq1_get_rows(ids: torch.Tensor, w: STQ1Matrix, out: torch.Tensor | None = N
     _dev_tensor(ids, torch.int32, "ids")
     T = ids.numel()
     if out is None:
-        out = torch.empty(*ids.shape, w.K, dtype=torch.float32, device=ids.device)
+        out = _empty((*ids.shape, w.K), torch.float32, ids.device, stream)
     _dev_tensor(out, torch.float32, "out")
     if out.numel() != T * w.K:
         raise ValueError("out has the wrong number of elements")
@@ -651,8 +665,9 @@ class KVPlan:
     head: torch.Tensor
 
     @classmethod
-    def empty(cls, B: int, T: int, device="cuda") -> "KVPlan":
-        flat = torch.empty(2 * B + 2 * T + 2, dtype=torch.int32, device=device)
+    def empty(cls, B: int, T: int, device="cuda", stream=None) -> "KVPlan":
+        """Unset; for a call on ``stream`` (None: the current one)."""
+        flat = _empty((2 * B + 2 * T + 2,), torch.int32, device, stream)
         return cls(*torch.unsafe_split_with_sizes(flat, (B + 1, B, T, T, 1)))  # (whole numbers: nothing to differentiate)
 
 
@@ -716,7 +731,7 @@ def kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: 
     if out is None:
         if T < 0:
             raise ValueError("T must not be negative")
-        out = KVPlan.empty(B, T, table.device)
+        out = KVPlan.empty(B, T, table.device, stream)
         cu = out.cu.data_ptr()  # the arrays lie one after another
         lens = cu + 4 * (B + 1)
         slots = lens + 4 * B
@@ -842,7 +857,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
     cup, lp = _i32(cu, "cu", B + 1, di), _i32(lens, "lens", B, di)
     raw = _stream_on(stream, di)
     if out is None:
-        out = torch.empty((T, hq, dim), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, hq, dim), torch.bfloat16, dev, stream)
     else:
         _dev_tensor(out, torch.bfloat16, "out")
         _on_device(out, "out", di)
@@ -877,19 +892,6 @@ def fp4_scale_bytes(N: int, K: int, format: str) -> int:
         raise ValueError(f"unknown format {format!r}; one of {sorted(FP4_FORMATS)}")
     b = 4 * FP4_BLOCK[format]
     return -(-N // 128) * -(-K // b) * 512
-
-
-def _fp4_empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
-    """What a call on ``stream`` (None: the current one) writes and returns: memory of that stream, as the current one may
-    still be busy with its own, and not given back before the current one is done with it either."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    now = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if now != stream:
-        t.record_stream(now)
-    return t
 
 
 class FP4Matrix:
@@ -933,8 +935,8 @@ class FP4Matrix:
         if K <= 0 or K % 32 or N < 0 or E < 1:
             raise ValueError(f"N = {N}, K = {K} (a positive multiple of 32), E = {E}")
         # scales (a multiple of 512 bytes) and codes in one block of memory; their tensors are made when asked for
-        flat = _fp4_empty((n + E * N * (K // 2),), torch.uint8, device, stream)
-        f = _fp4_empty((E * N,), torch.float32, device, stream) if format == "nv" else None
+        flat = _empty((n + E * N * (K // 2),), torch.uint8, device, stream)
+        f = _empty((E * N,), torch.float32, device, stream) if format == "nv" else None
         self, at = cls.__new__(cls), flat.data_ptr()
         self.N, self.K, self.E, self.format = N, K, E, format
         self._flat, self._codes, self._scales, self._row_scale = flat, None, None, f
@@ -1044,7 +1046,7 @@ def fp4_dequant(w: FP4Matrix, out: torch.Tensor | None = None, stream=None) -> t
     shape = (w.N, w.K) if w.E == 1 else (w.E, w.N, w.K)
     raw = _stream_on(stream, w._dev)
     if out is None:
-        out = _fp4_empty(shape, torch.bfloat16, w._device, stream)
+        out = _empty(shape, torch.bfloat16, w._device, stream)
     else:
         _fp4_out(out, shape, w._dev)
     rc = (_lib or lib()).w4a16_fp4_dequant(w._ptr, out.data_ptr(), raw)
@@ -1110,7 +1112,7 @@ def _fp4_product(x, w: FP4Matrix, act, out, stream, workspace):
         M, stride = _fp4_x(x, w.K, dev)
         lead = x.shape[:-1]
     if out is None:
-        out = _fp4_empty((*lead, cols), torch.bfloat16, w._device, stream)
+        out = _empty((*lead, cols), torch.bfloat16, w._device, stream)
     else:
         _fp4_out(out, (M, cols), dev)
     if quantised:
@@ -1156,7 +1158,7 @@ def fp4_mm_id(x: torch.Tensor, w: FP4Matrix, ids: torch.Tensor, act: str | None 
     shape = (*ids.shape, w.N if a == 0 else w.N // 2)
     raw = _stream_on(stream, w._dev)
     if out is None:
-        out = _fp4_empty(shape, torch.bfloat16, w._device, stream)
+        out = _empty(shape, torch.bfloat16, w._device, stream)
     else:
         _fp4_out(out, shape, w._dev)
     keep, ws, wn = _fp4_space(_fp4_mm_id_bytes(T, top, w.K, w.E, FP4_FORMATS[w.format]), workspace, raw, stream, w)
