@@ -510,7 +510,10 @@ int w4a16_fp4_mm_q(const w4a16_fp4* x, const w4a16_fp4* w, w4a16_bf16* y, int ac
 
 /* Routed experts: y[t][j] = W[ids[t * top + j]] x'[t] for T tokens of `top`
  * choices each (an expert may occur twice); ids int32 [T][top] on the device, y
- * bf16 [T][top][rows or rows / 2], not over x, w or ids.  An id outside 0..experts-1 gives a row of
+ * bf16 [T][top][rows or rows / 2], not over x, w or ids.  The workspace has whole tiles of
+ * 128 places (256 from some 40 rows an expert on) for each expert that may have a
+ * row, so that many experts of few rows make it large: K / 2 + K / 16 bytes a place
+ * (nv), 157 MiB for 125 tokens x 8 of 256 experts and K = 7168.  An id outside 0..experts-1 gives a row of
  * zeros and raises W4A16_DEVICE_BAD_ID.  experts <= 4096, T >= 0, top 1..1024. */
 size_t w4a16_fp4_mm_id_workspace_bytes(int T, int top, int K, int experts, int format);
 int w4a16_fp4_mm_id(const w4a16_bf16* x, int64_t x_stride, const w4a16_fp4* w, const int32_t* ids, w4a16_bf16* y,

@@ -684,9 +684,10 @@ cudaError_t launch_t(const Fp4MmArgs& a, const Fp4MmParams& p, int pdl, cudaStre
 
 }  // namespace
 
-// The GPU's us so / with the quantiser's launch before it: nv 1 row x 2560 to 10240 5.7 / 6.7, 5 rows 8.2 / 7.6, 1 x 2560 to
-// 262144 56.6 / 58.3, 5 x 2304 gated to 9216 9.7 / 9.1; mx 5 x 10240 to 2560 5.8 / 7.0.  A call from the host takes 10.5 to
-// 11.5 / 13.5 to 15 in all of these.  Past kOwnUnits the CTAs' part grows: 16 x 2560 (mx) 9.4 / 7.7.
+// The GPU's us so / with the quantiser's launch before it: nv 1 row x 2560 to 10240 5.8 / 7.1, 5 rows 7.6 to 8.5 / 7.6 to 7.9, 1 x 2560 to
+// 262144 56.8 / 59.0, 5 x 2304 gated to 9216 9.6 / 9.2, 5 x 10240 to 2560 8.9 / 8.3; mx 6.0 / 7.3.  A call from the host takes
+// 10.4 to 12 / 13 to 14 in all of these: five nv rows give up to 7% of the GPU's time in a captured step for that.  Past
+// kOwnUnits the CTAs' part grows: 16 x 2560 (mx) 9.4 / 7.7.
 bool fp4_mm_fuses(const w4a16_fp4& w, int M) {
   const int stages = (w.K + kFp4StageK - 1) / kFp4StageK, split = split_of((int)fp4_row_tiles(w.rows), stages);
   const int part = (stages + split - 1) / split;
@@ -694,8 +695,9 @@ bool fp4_mm_fuses(const w4a16_fp4& w, int M) {
 }
 
 // The same for routed calls; us so / with the quantiser's launch, K = 2048: 1 token x 4 of 64 experts, N = 1536
-// 5.7 / 8.9, 4 x 8 10.6 / 11.9, 1 x 2 of 8 (K = 4096, N = 14336) 13.3 / 15.7, 8 x 2 of 16 (K = 1024, N = 2048) 7.5 / 7.3; with
-// twice the units 8 x 1 of 8 (N = 6144) 11.2 / 9.5.  A call from the host takes 12 to 13 / 18.
+// 5.8 / 8.9, 4 x 8 10.6 / 11.5, 1 x 2 of 8 (K = 4096, N = 14336) 13.2 / 15.6, 4 x 1 of 8 (N = 6144) 7.7 / 8.4, 8 x 2 of 16
+// (K = 1024, N = 2048) 7.6 / 7.1; with twice the units 8 x 1 of 8 (N = 6144) 11.2 / 9.5.  A call from the host takes 11.5 to 14 /
+// 14.5 to 18.
 bool fp4_mm_id_fuses(const w4a16_fp4& w, int T, int top) {
   const int64_t stages = (w.K + kFp4StageK - 1) / kFp4StageK;
   return T <= kOwnRows && (int64_t)T * top <= kOwnIds && T * 16 * stages <= kOwnUnits && own_slots((int)stages, true) >= 3;

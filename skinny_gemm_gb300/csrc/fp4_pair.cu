@@ -142,7 +142,7 @@ __device__ __forceinline__ void put32(const Fp4MmParams& p, const Rows& row, con
         mul2(v[j + 2], v[j + 3], f.z, f.w, row.fx);
       }
     } else {
-      // (a loop over a copy: unrolled three times, its instructions cost all other calls 0.1 to 0.4 us)
+      // (a loop over a copy: unrolled three times, its instructions cost all other calls 0.1 to 0.3 us)
       float u[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) u[j] = v[j];
