@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_mm_kernel(const __grid_consta
 #pragma unroll 1
       for (int c = 0; c < NT; c += 16) {
         if (c >= count) break;
+        __syncwarp();  // (rows that are not stored are back)
         float v[16];
         tmem_ld16(acc + c, v);
         tmem_wait_ld();
